@@ -63,6 +63,7 @@ typedef struct precond_ctx* precond_t;
 /* gradient storage types */
 #define PRECOND_F32   0
 #define PRECOND_BF16  1
+#define PRECOND_E4M3  2  /* 8-bit form (precond_quantize8's input only) */
 
 /* option keys for precond_set_option */
 #define PRECOND_OPT_TOL            1  /* stop when ||M - I||_F <= tol*sqrt(d); default 1e-4 */
@@ -285,6 +286,128 @@ int precond_inv_root_noalloc(const float* A, int64_t d, float eps, float power, 
  */
 int precond_step_schedule(int p, double l0, double fold, int degree, int max_steps, double* alpha, double* beta,
                           double* gamma, double* lo, int* nsteps);
+
+/* =========================================================================
+ * Operators of a training step around the preconditioner: what makes the
+ * gradient that precond_step takes, for weights that are multiplied in 8 bits.
+ *
+ *   precond_rms_norm        h = x + r, its RMS norm, and the norm's 8-bit form
+ *   precond_quantize8       a matrix (a weight, an output gradient) to 8-bit form
+ *   precond_gemm8           C = A B^T: forward  y  = xq wq^T,
+ *                           input gradient      dx = dyq wtq^T,
+ *                           weight gradient     G  = dytq xtq^T   (precond_step's grads[i])
+ *   precond_distill         the loss against a teacher's top logits, and dlogits
+ *   precond_rms_norm_grad   the norm's gradients
+ *
+ * Conventions in addition to those at the top:
+ *  - Matrices are row-major with a row pitch (ld*, in elements, at least the
+ *    number of columns); other tensors are dense.  Sides are 0 .. 2^30; a
+ *    matrix without elements needs neither pointer nor pitch.
+ *  - Work is enqueued on `stream` and uses no memory but the caller's: calls on
+ *    several streams need no ordering among themselves, and every call may be
+ *    captured into a CUDA graph, once one call of this group has run on the
+ *    handle (it sets kernel attributes).
+ *  - Outputs may not overlap inputs or each other unless the call says so (EINVAL).
+ *  - Results do not depend on timing: no sum's order changes between calls.
+ *
+ * 8-bit form of a rows x cols matrix: `q`, e4m3 bytes, 16-byte aligned, pitch a
+ * multiple of 16; and `scale`, ceil(cols / 512) * ceil(rows / 128) * 512 bytes,
+ * 16-byte aligned.  The value of q[r][c] is e4m3(q[r][c]) * 2^(b - 127), b the
+ * scale byte of row r and block k = c / 128, which lies at
+ *   ((k / 4) * ceil(rows / 128) + r / 128) * 512 + (r % 32) * 16 + (r % 128 / 32) * 4 + k % 4.
+ * Writers give rows and blocks past the matrix's end the byte 127.  A block's
+ * scale is the least power of two (at least 2^-127) with every finite magnitude
+ * at most 448 times it, and 1 for a block of zeros; values that are not finite
+ * become NaN.
+ */
+#define PRECOND_BLOCK_ROW  0  /* a scale for each row and 128 columns */
+#define PRECOND_BLOCK_TILE 1  /* one for each 128 x 128 block: q and qt then hold the same values */
+
+/*
+ * h = x + residual (rounded to dtype; h = x without a residual),
+ * rstd = 1 / sqrt(mean over columns of h^2 + eps), y = h rstd weight.
+ *   x, residual  : rows x cols, PRECOND_F32 or PRECOND_BF16 (`dtype`); residual may be NULL
+ *   weight       : cols, PRECOND_F32 or PRECOND_BF16 (`weight_dtype`)
+ *   eps          : > 0
+ *   total        : h, given exactly when residual is; may be x or residual themselves
+ *   y            : the norm in dtype, or NULL
+ *   q, scale     : its 8-bit form (rounded once, from fp32), or both NULL
+ *   rstd         : rows floats for precond_rms_norm_grad, or NULL
+ */
+int precond_rms_norm(precond_t h, const void* x, const void* residual, const void* weight, int dtype,
+                     int weight_dtype, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr, float eps, void* total,
+                     int64_t ldt, void* y, int64_t ldy, void* q, int64_t ldq, uint8_t* scale, float* rstd,
+                     void* stream);
+
+/*
+ * Gradients of precond_rms_norm (the rounding to 8 bits counts as the
+ * identity), with n = x rstd:
+ *   dx = dresidual + rstd (dy weight - n mean over columns of (dy weight n)),
+ *   dw = sum over rows of dy n.
+ *   x          : the forward pass's h;  rstd: as it left them
+ *   dresidual  : the gradient that reaches h past the norm, or NULL (zero)
+ *   dx         : in dtype; may be dy, dresidual or x themselves where cols <= 8192
+ *   dw         : cols floats
+ *   workspace  : precond_rms_norm_grad_workspace(rows, cols) bytes, 16-byte
+ *                aligned, in use until the call's work has completed
+ */
+int precond_rms_norm_grad(precond_t h, const void* dy, const void* x, const void* weight, const float* rstd,
+                          const void* dresidual, int dtype, int weight_dtype, int64_t rows, int64_t cols, int64_t lddy,
+                          int64_t ldx, int64_t lddr, void* dx, int64_t lddx, float* dw, void* workspace,
+                          int64_t workspace_bytes, void* stream);
+int64_t precond_rms_norm_grad_workspace(int64_t rows, int64_t cols);   /* -1: bad sizes */
+
+/*
+ * The 8-bit form of x (rows x cols): q by rows, and qt, that of the transposed
+ * matrix (cols x rows), in one pass over x.  Either may be NULL (with its
+ * scales), not both.
+ *   x       : PRECOND_F32, PRECOND_BF16, or PRECOND_E4M3 (itself in 8-bit form,
+ *             with x_scale: an activation kept in 8 bits is put in blocks of
+ *             tokens this way; NULL otherwise).  Powers of two as scales make
+ *             that exact but for values below a block's smallest e4m3 number.
+ *   block   : PRECOND_BLOCK_ROW or PRECOND_BLOCK_TILE
+ */
+int precond_quantize8(precond_t h, const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                      const uint8_t* x_scale, int block, void* q, int64_t ldq, uint8_t* scale, void* qt, int64_t ldqt,
+                      uint8_t* scale_t, void* stream);
+
+/*
+ * C = A B^T, or C += A B^T (accumulate, PRECOND_F32 only): A is M x K and B is
+ * N x K in 8-bit form, C is M x N in PRECOND_F32 or PRECOND_BF16 (`c_dtype`).
+ * Products are exact; sums are fp32, for an fp32 C in stretches of 512 columns
+ * that are added to each other in round-to-nearest.
+ */
+int precond_gemm8(precond_t h, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const uint8_t* scale_a,
+                  const void* B, int64_t ldb, const uint8_t* scale_b, void* C, int64_t ldc, int c_dtype,
+                  int accumulate, void* stream);
+
+/*
+ * Synchronises `stream`; PRECOND_ECUDA if a wait inside a precond_gemm8 kernel
+ * of this handle ran out since the last call (its result is then not valid).
+ */
+int precond_gemm8_status(precond_t h, void* stream);
+
+/*
+ * Distillation loss of every row and, with `dlogits`, its gradient:
+ *   p = softmax(teacher / temperature) over the row's candidates,
+ *   q = softmax(logits / temperature) over the vocabulary,
+ *   loss = weight temperature^2 sum_j p_j (log p_j - log q[ids_j]),
+ *   dlogits_v = weight temperature (q_v - sum of p_j over ids_j = v).
+ *   logits      : rows x vocab, PRECOND_F32 or PRECOND_BF16; dlogits likewise, and may be logits itself
+ *   ids         : rows x top, int32 or int64 (`id_bits` 32 or 64), 1 <= top <= 1024; an entry outside
+ *                 0 .. vocab - 1 is no candidate.  An id may occur more than once.
+ *   teacher     : the candidates' logits, rows x top, PRECOND_F32 or PRECOND_BF16; -infinity gives p = 0
+ *   weight      : rows floats (the upstream gradient and the row's mask), NULL for 1.  A row of weight 0
+ *                 is not read: its loss and gradient are 0 whatever its logits hold.
+ *   loss        : rows floats
+ * A row without a candidate (or with teacher logits of -infinity only) has loss and gradient 0.  A
+ * candidate that the student gives no probability makes the loss infinite (its gradient stays finite);
+ * a row of logits that are all -infinity has none to give, and NaN for both.
+ */
+int precond_distill(precond_t h, const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ldz,
+                    const void* ids, int id_bits, int64_t ldi, const void* teacher, int teacher_dtype, int64_t ldt,
+                    int top, const float* weight, float temperature, float* loss, void* dlogits, int64_t lddz,
+                    void* stream);
 
 /* Static text for a status code. */
 const char* precond_error_string(int code);

@@ -267,3 +267,18 @@ class Preconditioner:
             self.close()
         except Exception:
             pass
+
+
+_OPERATORS = ("BLOCK_ROW", "BLOCK_TILE", "E4M3", "dequantize8", "empty8", "precond_distill", "precond_gemm8",
+              "precond_gemm8_status", "precond_quantize8", "precond_rms_norm", "precond_rms_norm_grad",
+              "precond_rms_norm_grad_workspace", "scale_shape", "scales8")
+
+
+def __getattr__(name):
+    """The training-step operators (operators.py); that module needs torch, which the rest imports only where used."""
+    if name in _OPERATORS:
+        from . import operators
+        for n in _OPERATORS:
+            globals()[n] = getattr(operators, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,14 +1,15 @@
-"""Build libprecond.so in-tree with nvcc for sm_103a (no cmake, one translation unit)."""
+"""Build libprecond.so in-tree with nvcc for sm_103a (no cmake; the translation units compile in parallel)."""
 import os
 import shutil
 import subprocess
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libprecond.so")
-SOURCES = ["precond.cu"]
+SOURCES = ["precond.cu", "operators.cu"]
 FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
-         "-Xcompiler", "-fPIC", "-shared"]
+         "-Xcompiler", "-fPIC"]
 
 
 def nvcc():
@@ -31,10 +32,19 @@ def build(force=False, verbose=False):
     if not force and not sources_newer_than(OUT):
         return OUT
     tmp = OUT + ".tmp"
-    cmd = [nvcc()] + FLAGS + ["-o", tmp] + [os.path.join(CSRC, s) for s in SOURCES]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True, cwd=CSRC)
+    with tempfile.TemporaryDirectory(prefix="precond_build_") as d:
+        objs = [os.path.join(d, os.path.splitext(s)[0] + ".o") for s in SOURCES]
+        cmds = [[nvcc()] + FLAGS + ["-c", "-o", o, os.path.join(CSRC, s)] for s, o in zip(SOURCES, objs)]
+        link = [nvcc()] + FLAGS + ["-shared", "-o", tmp] + objs
+        if verbose:
+            for c in cmds + [link]:
+                print(" ".join(c))
+        procs = [subprocess.Popen(c, cwd=CSRC) for c in cmds]
+        codes = [p.wait() for p in procs]
+        for c, rc in zip(cmds, codes):
+            if rc:
+                raise subprocess.CalledProcessError(rc, c)
+        subprocess.run(link, check=True, cwd=CSRC)
     os.replace(tmp, OUT)
     return OUT
 

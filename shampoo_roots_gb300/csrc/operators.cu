@@ -1,0 +1,428 @@
+// Host side of the training-step operators of include/precond.h: RMS norm and
+// its gradients, the 8-bit form, the product of two 8-bit matrices and the
+// distillation loss.  Arguments are checked here, before anything is enqueued;
+// kernels go to the caller's stream and use no memory but the caller's.
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdio>
+#include <cstring>
+
+#include "distill.cuh"
+#include "gemm8.cuh"
+#include "handle.h"
+#include "quantize8.cuh"
+#include "rms_norm.cuh"
+
+using namespace precond;
+
+namespace {
+
+constexpr int64_t MAX_SIDE = (int64_t)1 << 30;     // rows, columns: kernels index a side with 32 bits
+constexpr int PLAN_SMS = 152;                       // a GB300's: sizes the dw workspace without a device
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+size_t size_of(int dtype) { return dtype == PRECOND_F32 ? 4 : dtype == PRECOND_BF16 ? 2 : 1; }
+bool float_type(int d) { return d == PRECOND_F32 || d == PRECOND_BF16; }
+bool side(int64_t n) { return n >= 0 && n <= MAX_SIDE; }
+// A matrix of `rows` x `cols` elements with rows `ld` apart; a matrix without elements needs neither pointer nor pitch.
+bool matrix(const void* p, int64_t rows, int64_t cols, int64_t ld, int dtype) {
+  if (rows == 0 || cols == 0) return true;
+  return ld >= cols && ld <= MAX_SIDE && p && aligned(p, size_of(dtype));
+}
+// An 8-bit matrix: 16-byte aligned rows, scales on 16 bytes.
+bool matrix8(const void* q, int64_t ld, const uint8_t* s, int64_t rows, int64_t cols) {
+  if (rows == 0 || cols == 0) return true;
+  return ld >= cols && ld % 16 == 0 && ld <= MAX_SIDE && q && s && aligned(q, 16) && aligned(s, 16);
+}
+// Rows that 16-byte loads can take whole.
+bool vectors(const void* p, int64_t cols, int64_t ld, int dtype) {
+  const int64_t per = 16 / (int64_t)size_of(dtype);
+  return !p || (aligned(p, 16) && cols % 8 == 0 && ld % per == 0);
+}
+struct Range { const char* lo; const char* hi; };
+Range range(const void* p, int64_t rows, int64_t ld, int64_t cols, size_t size) {
+  const char* b = reinterpret_cast<const char*>(p);
+  if (!p || rows <= 0 || cols <= 0) return {nullptr, nullptr};
+  return {b, b + ((rows - 1) * ld + cols) * (int64_t)size};
+}
+bool overlap(Range a, Range b) { return a.lo && b.lo && a.lo < b.hi && b.lo < a.hi; }
+Range scale_range(const uint8_t* s, int64_t rows, int64_t cols) {
+  return range(s, 1, 0, (int64_t)q8_groups(cols) * q8_row_blocks(rows) * 512, 1);
+}
+
+int cuda_error(const char* what, cudaError_t e) {
+  fprintf(stderr, "libprecond: %s: %s\n", what, cudaGetErrorString(e));
+  return PRECOND_ECUDA;
+}
+#define OP_CK(call)                                              \
+  do {                                                           \
+    const cudaError_t e_ = (call);                               \
+    if (e_ != cudaSuccess) return cuda_error(#call, e_);         \
+  } while (0)
+
+// The device current and the kernels' attributes set.
+template <int BN>
+cudaError_t gemm8_attributes() {
+  cudaError_t e = cudaFuncSetAttribute(gemm8_kernel<BN, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Gemm8Smem<BN>::BYTES);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(gemm8_kernel<BN, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Gemm8Smem<BN>::BYTES);
+  return e;
+}
+int prepare(Handle* h) {
+  int now = -1;
+  OP_CK(cudaGetDevice(&now));
+  if (now != h->device) OP_CK(cudaSetDevice(h->device));
+  if (!h->op_ready) {
+    OP_CK(gemm8_attributes<16>());
+    OP_CK(gemm8_attributes<32>());
+    OP_CK(gemm8_attributes<64>());
+    OP_CK(gemm8_attributes<128>());
+    OP_CK(cudaMalloc(&h->op_err, sizeof(unsigned int)));
+    OP_CK(cudaMemset(h->op_err, 0, sizeof(unsigned int)));
+    OP_CK(cudaDeviceSynchronize());
+    h->op_ready = true;
+  }
+  return PRECOND_OK;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, int cluster, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+// ------------------------------------------------------------------------- norm
+// Threads of a row and rows of a block.  A row is 8 columns a thread up to 512
+// threads, then 16 (and 32 forward); longer rows take the kernels that read a
+// row twice.  Blocks of short rows hold several, to have 256 threads.
+struct RowShape { int threads, rows, nv; };
+RowShape row_shape(int64_t cols, int max_nv) {
+  const int64_t vec = (cols + 7) / 8;
+  RowShape s = {0, 1, 0};
+  for (int nv = 1; nv <= max_nv; nv *= 2)
+    if (vec <= 512 * nv) {
+      s.nv = nv;
+      break;
+    }
+  if (!s.nv) {
+    s.threads = 1024;
+    return s;
+  }
+  s.threads = (int)std::max<int64_t>(32, ((vec + s.nv - 1) / s.nv + 31) / 32 * 32);
+  s.rows = std::min(8, std::max(1, 256 / s.threads));
+  return s;
+}
+constexpr int NORM_NV = 4, GRAD_NV = 2;
+
+int64_t row_blocks_of(const RowShape& s, int64_t rows, int sms) {
+  const int64_t resident = std::max(1, (s.nv ? 1024 : 2048) / (s.threads * s.rows));
+  return std::max<int64_t>(1, std::min((rows + s.rows - 1) / s.rows, resident * sms));
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_norm(const RmsNormArgs& a, const RowShape& s, unsigned grid, cudaStream_t st) {
+  const dim3 block(s.threads, s.rows);
+  switch (s.nv) {
+    case 1: return launch(rms_norm_kernel<T, 1, VEC>, dim3(grid), block, 0, st, 1, a);
+    case 2: return launch(rms_norm_kernel<T, 2, VEC>, dim3(grid), block, 0, st, 1, a);
+    case 4: return launch(rms_norm_kernel<T, 4, VEC>, dim3(grid), block, 0, st, 1, a);
+    default: return launch(rms_norm_long_kernel<T, VEC>, dim3(grid), block, 0, st, 1, a);
+  }
+}
+template <typename T, bool VEC>
+cudaError_t launch_grad(const RmsGradArgs& a, const RowShape& s, unsigned grid, cudaStream_t st) {
+  const dim3 block(s.threads, s.rows);
+  switch (s.nv) {
+    case 1: return launch(rms_grad_kernel<T, 1, VEC>, dim3(grid), block, 0, st, 1, a);
+    case 2: return launch(rms_grad_kernel<T, 2, VEC>, dim3(grid), block, 0, st, 1, a);
+    default: return launch(rms_grad_long_kernel<T, VEC>, dim3(grid), block, 0, st, 1, a);
+  }
+}
+
+// ------------------------------------------------------------------------- product
+int encode8(Handle* h, CUtensorMap* map, const void* q, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld};
+  cuuint32_t box[2] = {(cuuint32_t)G8_BK, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = h->encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), dims, strides, box, estr,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    fprintf(stderr, "libprecond: cuTensorMapEncodeTiled failed (%d)\n", (int)r);
+    return PRECOND_ECUDA;
+  }
+  return PRECOND_OK;
+}
+
+template <int BN>
+cudaError_t launch_gemm8(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm8Args& g, int64_t tiles, int parts, int sms,
+                         cudaStream_t st) {
+  const unsigned grid = parts > 1 ? (unsigned)(tiles * parts) : (unsigned)std::min<int64_t>(tiles, sms);
+  auto k = g.c_bf16 ? gemm8_kernel<BN, false> : gemm8_kernel<BN, true>;
+  return launch(k, dim3(grid), dim3(G8_THREADS), Gemm8Smem<BN>::BYTES, st, parts, ma, mb, g);
+}
+
+}  // namespace
+
+extern "C" {
+
+int precond_rms_norm(precond_t ph, const void* x, const void* residual, const void* weight, int dtype, int weight_dtype,
+                     int64_t rows, int64_t cols, int64_t ldx, int64_t ldr, float eps, void* total, int64_t ldt, void* y,
+                     int64_t ldy, void* q, int64_t ldq, uint8_t* scale, float* rstd, void* stream) {
+  Handle* h = as_handle(ph);
+  if (!h || !float_type(dtype) || !float_type(weight_dtype) || !side(rows) || !side(cols) || !(eps > 0.f)) return PRECOND_EINVAL;
+  const size_t sz = size_of(dtype);
+  if (!matrix(x, rows, cols, ldx, dtype) || !matrix(weight, 1, cols, cols, weight_dtype) || !aligned(rstd, 4)) return PRECOND_EINVAL;
+  if ((residual != nullptr) != (total != nullptr)) return PRECOND_EINVAL;
+  if (residual && (!matrix(residual, rows, cols, ldr, dtype) || !matrix(total, rows, cols, ldt, dtype))) return PRECOND_EINVAL;
+  if (y && !matrix(y, rows, cols, ldy, dtype)) return PRECOND_EINVAL;
+  if ((q != nullptr) != (scale != nullptr) || (q && !matrix8(q, ldq, scale, rows, cols))) return PRECOND_EINVAL;
+  if (rows && cols && !total && !y && !q && !rstd) return PRECOND_EINVAL;
+  // outputs may not overlap anything, but for `total` over x or residual, element for element
+  const Range in[3] = {range(x, rows, ldx, cols, sz), range(residual, rows, ldr, cols, sz),
+                       range(weight, 1, 0, cols, size_of(weight_dtype))};
+  const Range out[5] = {range(total, rows, ldt, cols, sz), range(y, rows, ldy, cols, sz), range(q, rows, ldq, cols, 1),
+                        q ? scale_range(scale, rows, cols) : Range{nullptr, nullptr}, range(rstd, 1, 0, rows, 4)};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 3; ++j) {
+      const bool same = i == 0 && ((j == 0 && total == x && ldt == ldx) || (j == 1 && total == residual && ldt == ldr));
+      if (!same && overlap(out[i], in[j])) return PRECOND_EINVAL;
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return PRECOND_EINVAL;
+  }
+  if (h->device < 0) return PRECOND_ENODEV;
+  if (rows == 0 || cols == 0) return PRECOND_OK;
+  int rc = prepare(h);
+  if (rc) return rc;
+  RmsNormArgs a = {x, residual, weight, total, y, (uint8_t*)q, scale, rstd, rows, cols, ldx, ldr, ldt, ldy, ldq, eps,
+                   weight_dtype == PRECOND_BF16};
+  const RowShape s = row_shape(cols, NORM_NV);
+  const unsigned grid = (unsigned)row_blocks_of(s, q ? q8_row_blocks(rows) * 128 : rows, h->num_sms);
+  const bool vec = vectors(x, cols, ldx, dtype) && vectors(residual, cols, ldr, dtype) && vectors(total, cols, ldt, dtype) &&
+                   vectors(y, cols, ldy, dtype);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == PRECOND_BF16)
+    OP_CK((vec ? launch_norm<__nv_bfloat16, true>(a, s, grid, st) : launch_norm<__nv_bfloat16, false>(a, s, grid, st)));
+  else
+    OP_CK((vec ? launch_norm<float, true>(a, s, grid, st) : launch_norm<float, false>(a, s, grid, st)));
+  ++h->launches;
+  return PRECOND_OK;
+}
+
+int64_t precond_rms_norm_grad_workspace(int64_t rows, int64_t cols) {
+  if (!side(rows) || !side(cols)) return -1;
+  if (rows == 0 || cols == 0) return 0;
+  const RowShape s = row_shape(cols, GRAD_NV);
+  return row_blocks_of(s, rows, PLAN_SMS) * s.rows * cols * 4;
+}
+
+int precond_rms_norm_grad(precond_t ph, const void* dy, const void* x, const void* weight, const float* rstd,
+                          const void* dresidual, int dtype, int weight_dtype, int64_t rows, int64_t cols, int64_t lddy,
+                          int64_t ldx, int64_t lddr, void* dx, int64_t lddx, float* dw, void* workspace,
+                          int64_t workspace_bytes, void* stream) {
+  Handle* h = as_handle(ph);
+  if (!h || !float_type(dtype) || !float_type(weight_dtype) || !side(rows) || !side(cols)) return PRECOND_EINVAL;
+  const size_t sz = size_of(dtype);
+  if (!matrix(dy, rows, cols, lddy, dtype) || !matrix(x, rows, cols, ldx, dtype) || !matrix(dx, rows, cols, lddx, dtype) ||
+      !matrix(weight, 1, cols, cols, weight_dtype) || !matrix(rstd, 1, rows, rows, PRECOND_F32) ||
+      !matrix(dw, 1, cols, cols, PRECOND_F32) || (dresidual && !matrix(dresidual, rows, cols, lddr, dtype)))
+    return PRECOND_EINVAL;
+  const int64_t need = precond_rms_norm_grad_workspace(rows, cols);
+  if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return PRECOND_EINVAL;
+  const Range in[5] = {range(dy, rows, lddy, cols, sz), range(dresidual, rows, lddr, cols, sz), range(x, rows, ldx, cols, sz),
+                       range(weight, 1, 0, cols, size_of(weight_dtype)), range(rstd, 1, 0, rows, 4)};
+  const Range out[3] = {range(dx, rows, lddx, cols, sz), range(dw, 1, 0, cols, 4), range(workspace, 1, 0, need, 1)};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 5; ++j) {
+      // dx may lie over dy, dresidual or x, element for element, where a row is read once
+      const bool same = i == 0 && row_shape(cols, GRAD_NV).nv &&
+                        ((j == 0 && dx == dy && lddx == lddy) || (j == 1 && dx == dresidual && lddx == lddr) ||
+                         (j == 2 && dx == x && lddx == ldx));
+      if (!same && overlap(out[i], in[j])) return PRECOND_EINVAL;
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return PRECOND_EINVAL;
+  }
+  if (h->device < 0) return PRECOND_ENODEV;
+  if (cols == 0) return PRECOND_OK;
+  int rc = prepare(h);
+  if (rc) return rc;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (rows == 0) {
+    OP_CK(cudaMemsetAsync(dw, 0, cols * 4, st));
+    return PRECOND_OK;
+  }
+  RmsGradArgs a = {dy, x, dresidual, weight, rstd, dx, (float*)workspace, rows, cols, lddy, ldx, lddr, lddx,
+                   weight_dtype == PRECOND_BF16};
+  const RowShape s = row_shape(cols, GRAD_NV);
+  const unsigned grid = (unsigned)row_blocks_of(s, rows, std::min(h->num_sms, PLAN_SMS));
+  const bool vec = vectors(dy, cols, lddy, dtype) && vectors(x, cols, ldx, dtype) && vectors(dresidual, cols, lddr, dtype) &&
+                   vectors(dx, cols, lddx, dtype);
+  if (dtype == PRECOND_BF16)
+    OP_CK((vec ? launch_grad<__nv_bfloat16, true>(a, s, grid, st) : launch_grad<__nv_bfloat16, false>(a, s, grid, st)));
+  else
+    OP_CK((vec ? launch_grad<float, true>(a, s, grid, st) : launch_grad<float, false>(a, s, grid, st)));
+  OP_CK(launch(rms_dw_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(32, 32), 0, st, 1, (const float*)workspace,
+               (int)grid * s.rows, cols, dw));
+  h->launches += 2;
+  return PRECOND_OK;
+}
+
+int precond_quantize8(precond_t ph, const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx, const uint8_t* x_scale,
+                      int block, void* q, int64_t ldq, uint8_t* scale, void* qt, int64_t ldqt, uint8_t* scale_t, void* stream) {
+  Handle* h = as_handle(ph);
+  if (!h || !side(rows) || !side(cols) || (block != PRECOND_BLOCK_ROW && block != PRECOND_BLOCK_TILE)) return PRECOND_EINVAL;
+  if (dtype == PRECOND_E4M3) {
+    if (!matrix8(x, ldx, x_scale, rows, cols)) return PRECOND_EINVAL;
+  } else if (!float_type(dtype) || x_scale || !matrix(x, rows, cols, ldx, dtype)) {
+    return PRECOND_EINVAL;
+  }
+  if ((q != nullptr) != (scale != nullptr) || (qt != nullptr) != (scale_t != nullptr) || (rows && cols && !q && !qt)) return PRECOND_EINVAL;
+  if ((q && !matrix8(q, ldq, scale, rows, cols)) || (qt && !matrix8(qt, ldqt, scale_t, cols, rows))) return PRECOND_EINVAL;
+  const Range in[2] = {range(x, rows, ldx, cols, size_of(dtype)),
+                       x_scale ? scale_range(x_scale, rows, cols) : Range{nullptr, nullptr}};
+  const Range out[4] = {range(q, rows, ldq, cols, 1), q ? scale_range(scale, rows, cols) : Range{nullptr, nullptr},
+                        range(qt, cols, ldqt, rows, 1), qt ? scale_range(scale_t, cols, rows) : Range{nullptr, nullptr}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 2; ++j)
+      if (overlap(out[i], in[j])) return PRECOND_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return PRECOND_EINVAL;
+  }
+  const int64_t tiles = q8_row_blocks(rows) * q8_row_blocks(cols);
+  if (tiles > INT32_MAX) return PRECOND_EINVAL;
+  if (h->device < 0) return PRECOND_ENODEV;
+  if (rows == 0 || cols == 0) return PRECOND_OK;
+  int rc = prepare(h);
+  if (rc) return rc;
+  Quant8Args a = {x, ldx, x_scale, rows, cols, block == PRECOND_BLOCK_TILE, (uint8_t*)q, ldq, scale, (uint8_t*)qt, ldqt, scale_t};
+  const bool vec = dtype == PRECOND_E4M3 || vectors(x, cols, ldx, dtype);
+  auto k = dtype == PRECOND_E4M3 ? quantize8_kernel<QIN_E4M3, true>
+           : dtype == PRECOND_BF16 ? (vec ? quantize8_kernel<QIN_BF16, true> : quantize8_kernel<QIN_BF16, false>)
+                                   : (vec ? quantize8_kernel<QIN_F32, true> : quantize8_kernel<QIN_F32, false>);
+  OP_CK(launch(k, dim3((unsigned)tiles), dim3(256), 0, (cudaStream_t)stream, 1, a));
+  ++h->launches;
+  return PRECOND_OK;
+}
+
+int precond_gemm8(precond_t ph, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const uint8_t* scale_a,
+                  const void* B, int64_t ldb, const uint8_t* scale_b, void* C, int64_t ldc, int c_dtype, int accumulate,
+                  void* stream) {
+  Handle* h = as_handle(ph);
+  if (!h || !side(M) || !side(N) || !side(K) || !float_type(c_dtype)) return PRECOND_EINVAL;
+  if (accumulate && c_dtype != PRECOND_F32) return PRECOND_EINVAL;
+  if (!matrix8(A, lda, scale_a, M, K) || !matrix8(B, ldb, scale_b, N, K) || !matrix(C, M, N, ldc, c_dtype)) return PRECOND_EINVAL;
+  const Range in[4] = {range(A, M, lda, K, 1), range(B, N, ldb, K, 1),
+                       M && K ? scale_range(scale_a, M, K) : Range{nullptr, nullptr},
+                       N && K ? scale_range(scale_b, N, K) : Range{nullptr, nullptr}};
+  const Range out = range(C, M, ldc, N, size_of(c_dtype));
+  for (const Range& r : in)
+    if (overlap(out, r)) return PRECOND_EINVAL;
+  if (h->device < 0) return PRECOND_ENODEV;
+  if (M == 0 || N == 0) return PRECOND_OK;
+  int rc = prepare(h);
+  if (rc) return rc;
+  cudaStream_t st = (cudaStream_t)stream;
+
+  // The MMA's rows are always 128 a tile, its columns 16 to 128.  A side of at most 64
+  // goes to the columns (a few tokens against a weight: the weight's rows fill the tile
+  // and its bytes, which bound the call, are read once).
+  const bool swap = M <= 64 && M < N;
+  Gemm8Args g = {swap ? N : M, swap ? M : N, K, scale_a, q8_row_blocks(M), scale_b, q8_row_blocks(N), C, ldc,
+                 c_dtype == PRECOND_BF16, accumulate, swap, h->op_err};
+  if (swap) {
+    std::swap(A, B);
+    std::swap(lda, ldb);
+    std::swap(g.sa, g.sb);
+    std::swap(g.sa_rb, g.sb_rb);
+  }
+  const int bn = g.N <= 16 ? 16 : g.N <= 32 ? 32 : g.N <= 64 ? 64 : 128;
+  const int64_t tiles = ((g.M + G8_BM - 1) / G8_BM) * ((g.N + bn - 1) / bn);
+  if (tiles > INT32_MAX) return PRECOND_EINVAL;
+  // Few tiles: a cluster of up to 8 CTAs shares each, a stretch of whole scale groups of K each.
+  const int groups = q8_groups(K);
+  int parts = 1;
+  while (parts < 8 && tiles * parts * 2 <= h->num_sms && parts * 2 <= groups) parts *= 2;
+  CUtensorMap ma, mb;
+  memset(&ma, 0, sizeof(ma));
+  memset(&mb, 0, sizeof(mb));
+  if (K > 0 && ((rc = encode8(h, &ma, A, g.M, K, lda, G8_BM)) || (rc = encode8(h, &mb, B, g.N, K, ldb, bn)))) return rc;
+  cudaError_t e = cudaSuccess;
+  switch (bn) {
+    case 16: e = launch_gemm8<16>(ma, mb, g, tiles, parts, h->num_sms, st); break;
+    case 32: e = launch_gemm8<32>(ma, mb, g, tiles, parts, h->num_sms, st); break;
+    case 64: e = launch_gemm8<64>(ma, mb, g, tiles, parts, h->num_sms, st); break;
+    default: e = launch_gemm8<128>(ma, mb, g, tiles, parts, h->num_sms, st); break;
+  }
+  OP_CK(e);
+  ++h->launches;
+  return PRECOND_OK;
+}
+
+int precond_gemm8_status(precond_t ph, void* stream) {
+  Handle* h = as_handle(ph);
+  if (!h) return PRECOND_EINVAL;
+  if (h->device < 0) return PRECOND_ENODEV;
+  int rc = prepare(h);
+  if (rc) return rc;
+  unsigned int word = 0;
+  cudaStream_t st = (cudaStream_t)stream;
+  OP_CK(cudaMemcpyAsync(&word, h->op_err, sizeof(word), cudaMemcpyDeviceToHost, st));
+  OP_CK(cudaMemsetAsync(h->op_err, 0, sizeof(word), st));
+  OP_CK(cudaStreamSynchronize(st));
+  return word ? PRECOND_ECUDA : PRECOND_OK;
+}
+
+int precond_distill(precond_t ph, const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ldz, const void* ids,
+                    int id_bits, int64_t ldi, const void* teacher, int teacher_dtype, int64_t ldt, int top,
+                    const float* weight, float temperature, float* loss, void* dlogits, int64_t lddz, void* stream) {
+  Handle* h = as_handle(ph);
+  if (!h || !float_type(dtype) || !float_type(teacher_dtype) || !side(rows) || !side(vocab) || vocab < 1) return PRECOND_EINVAL;
+  if ((id_bits != 32 && id_bits != 64) || top < 1 || top > DISTILL_MAX_TOP || !(temperature > 0.f) || temperature > 3e38f)
+    return PRECOND_EINVAL;
+  const size_t sz = size_of(dtype);
+  if (!matrix(logits, rows, vocab, ldz, dtype) || !matrix(teacher, rows, top, ldt, teacher_dtype) ||
+      !matrix(loss, 1, rows, rows, PRECOND_F32) || (dlogits && !matrix(dlogits, rows, vocab, lddz, dtype)) ||
+      (weight && !aligned(weight, 4)) || ldi < top || ldi > MAX_SIDE || (rows && (!ids || !aligned(ids, id_bits / 8))))
+    return PRECOND_EINVAL;
+  const Range in[4] = {range(logits, rows, ldz, vocab, sz), range(ids, rows, ldi, top, id_bits / 8),
+                       range(teacher, rows, ldt, top, size_of(teacher_dtype)), range(weight, 1, 0, rows, 4)};
+  const Range out[2] = {range(dlogits, rows, lddz, vocab, sz), range(loss, 1, 0, rows, 4)};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 4; ++j) {
+      const bool same = i == 0 && j == 0 && dlogits == logits && lddz == ldz;
+      if (!same && overlap(out[i], in[j])) return PRECOND_EINVAL;
+    }
+  if (overlap(out[0], out[1])) return PRECOND_EINVAL;
+  if (rows > (int64_t)INT32_MAX / 8) return PRECOND_EINVAL;
+  if (h->device < 0) return PRECOND_ENODEV;
+  if (rows == 0) return PRECOND_OK;
+  int rc = prepare(h);
+  if (rc) return rc;
+  DistillArgs a = {logits, ldz, ids, ldi, id_bits == 64, teacher, ldt, teacher_dtype == PRECOND_BF16, weight, loss, dlogits, lddz,
+                   rows, vocab, top, temperature};
+  // Blocks of a row: as many as keep the GPU full where rows are few, each with at least 8192 logits.
+  int parts = 1;
+  while (parts < 8 && rows * parts < 2 * h->num_sms && vocab / (parts * 2) >= 8192) parts *= 2;
+  auto k = dtype == PRECOND_BF16 ? distill_kernel<__nv_bfloat16> : distill_kernel<float>;
+  OP_CK(launch(k, dim3((unsigned)(rows * parts)), dim3(DISTILL_THREADS), 0, (cudaStream_t)stream, parts, a));
+  ++h->launches;
+  return PRECOND_OK;
+}
+
+}  // extern "C"

@@ -30,15 +30,12 @@
 #include "engine.cuh"
 #include "gemm_f64.cuh"
 #include "gemm_tc.cuh"
+#include "handle.h"
 #include "stages.cuh"
 
 using namespace precond;
 
 namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 constexpr size_t ALIGN = 1024;
 inline size_t align_up(size_t x, size_t a = ALIGN) { return (x + a - 1) / a * a; }
@@ -97,8 +94,7 @@ struct Plan {
 
 }  // namespace
 
-struct precond_ctx {
-  int device = -1;
+struct precond_ctx : precond::Handle {
   double tol = 1e-4;
   int max_iter = 0, min_iter = 4, engine = 0, small_dim = 64, timing = 0, use_graph = 1;
   int classical = 0;                   // 1: classical Newton step polynomial at every iteration
@@ -124,14 +120,11 @@ struct precond_ctx {
   std::vector<int> last_root_d;       // per root: d
   std::vector<int> last_root_class, last_root_slot;
   Plan last_plan;
-  int64_t launches = 0;
   int64_t ns_launches = 0;
   bool in_ns = false;                  // timing: inside the iteration stage
   std::vector<cudaEvent_t> gemm_ev;    // timing: start/stop pairs around iteration-stage GEMMs
   size_t gemm_ev_used = 0;
-  EncodeTiledFn encode = nullptr;
   bool tc_attr_set = false;
-  int num_sms = 152;                   // a GB300's; a device handle reads its device's count
   // CUDA graph of the last plan (replayed on an internal stream joined to the caller's by events)
   struct Graph {                       // one captured plan
     std::string key;
@@ -1269,6 +1262,10 @@ int run_planned(precond_ctx* h, const Plan& P, float beta, float eps, cudaStream
 
 }  // namespace
 
+namespace precond {
+Handle* as_handle(precond_t h) { return h; }
+}  // namespace precond
+
 // =========================================================================== C ABI
 extern "C" {
 
@@ -1313,6 +1310,7 @@ int precond_destroy(precond_t h) {
     cudaSetDevice(h->device);
     cudaDeviceSynchronize();
     if (h->ws) cudaFree(h->ws);
+    if (h->op_err) cudaFree(h->op_err);
     if (h->pinned) cudaFreeHost(h->pinned);
     if (h->upload_done) cudaEventDestroy(h->upload_done);
     if (h->events)
