@@ -28,6 +28,8 @@
 #include <cooperative_groups.h>
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "form8.cuh"
 #include "ptx.cuh"
 
@@ -36,8 +38,11 @@ namespace precond {
 constexpr int G8_BM = 128;             // rows of A a CTA takes (the MMA's M)
 constexpr int G8_BK = 128;             // one scale block, one swizzled row
 constexpr int G8_SEGMENT = 4;          // blocks between promotions (512 columns: one scale group)
+constexpr int G8_PAIR_SEGMENT = 8;     // the same, for pairs of CTAs
 constexpr int G8_EPI_WARPS = 8;
+constexpr int G8_XS_LD = 33;            // a drain warp's scratch: 32 x 32 results, rows an odd number of words apart
 constexpr int G8_THREADS = 64 + 32 * G8_EPI_WARPS;
+constexpr int G8_PAIR_THREADS = 128 + 32 * G8_EPI_WARPS;   // a warpgroup that loads and issues, two that drain
 
 struct Gemm8Args {
   int64_t M, N, K;                     // of the MMA's view: M rows of its A operand
@@ -45,6 +50,7 @@ struct Gemm8Args {
   const uint8_t* sb; int64_t sb_rb;
   void* c; int64_t ldc;
   int c_bf16, accumulate;
+  int sectors;                         // C's rows begin at multiples of 32 bytes
   int swap;                            // 1: C is N x M (the operands were exchanged)
   unsigned int* err;
 };
@@ -53,16 +59,17 @@ template <int BN>
 struct Gemm8Smem {
   static constexpr int A_BYTES = G8_BM * G8_BK;
   static constexpr int B_BYTES = BN * G8_BK;
-  static constexpr int SFB_ATOMS = (BN + 127) / 128;
-  static constexpr int SF_BYTES = 512 * (1 + SFB_ATOMS);
-  static constexpr int STAGES = BN >= 128 ? 6 : 8;
+  static constexpr int SF_BYTES = 1024;                 // 128 rows of A and of B
+  static constexpr int STAGES = BN == 128 ? 5 : BN == 64 ? 7 : 8;
   static constexpr int OFF_SF = STAGES * (A_BYTES + B_BYTES);
-  static constexpr int OFF_BAR = OFF_SF + STAGES * SF_BYTES;
+  static constexpr int OFF_XS = OFF_SF + STAGES * SF_BYTES;                 // a scratch of each drain warp
+  static constexpr int OFF_BAR = OFF_XS + G8_EPI_WARPS * 32 * G8_XS_LD * 4;
+  static constexpr int PART_LD = BN + 1;                                    // a stretch's sums, over the ring
   static constexpr int BYTES = 1024 + OFF_BAR + 256;
   // tensor memory: two sum buffers, then two scale buffers
   static constexpr int ACC_COLS = BN < 32 ? 32 : BN;
   static constexpr int SF_COL = 2 * ACC_COLS;
-  static constexpr int SF_COLS = 4 * (1 + SFB_ATOMS);
+  static constexpr int SF_COLS = 8;
   static constexpr int TMEM_COLS = 2 * ACC_COLS + 2 * SF_COLS <= 128 ? 128 : 2 * ACC_COLS + 2 * SF_COLS <= 256 ? 256 : 512;
 };
 
@@ -112,52 +119,96 @@ __device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// One element of the result.
-__device__ __forceinline__ void g8_store(const Gemm8Args& g, int64_t o, float v) {
-  if (g.c_bf16) {
-    reinterpret_cast<__nv_bfloat16*>(g.c)[o] = __float2bfloat16_rn(v);
-  } else {
-    float* p = reinterpret_cast<float*>(g.c) + o;
-    *p = g.accumulate ? *p + v : v;
-  }
+// One element of the result, its old value added.
+__device__ __forceinline__ void g8_put(const Gemm8Args& g, int64_t o, float v) {
+  if (g.c_bf16) reinterpret_cast<__nv_bfloat16*>(g.c)[o] = __float2bfloat16_rn(v);
+  else reinterpret_cast<float*>(g.c)[o] = v;
 }
 
-// 16 consecutive columns n .. of MMA row m.
-__device__ __forceinline__ void g8_store16(const Gemm8Args& g, int64_t m, int64_t n, const float (&v)[16]) {
-  if (m >= g.M) return;
+// 32 bytes, one sector.
+__device__ __forceinline__ void st_sector(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+// Columns n .. n + 31 of the warp's 32 MMA rows m0 .. (one a lane).  Where C's rows are whole sectors a lane
+// stores its row's (16 lanes of a bf16 C at 2 B a lane and row took 39 us for 2500 x 1300 x 256, against 17 us
+// through the scratch); otherwise the rows pass through the warp's scratch and leave 32 columns at a time.
+// Accumulating, the loads of several rows go before their stores: one memory latency, not one each.
+__device__ __forceinline__ void g8_store32(const Gemm8Args& g, float* xs, int64_t m0, int64_t n, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  if (m0 >= g.M || n >= g.N) return;
+  const int64_t m = m0 + lane;
   if (g.swap) {                         // lanes hold consecutive elements of a row of C
+    if (m >= g.M) return;
+    const int64_t o = n * g.ldc + m;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (n + i < g.N) g8_store(g, (n + i) * g.ldc + m, v[i]);
+    for (int h = 0; h < 32; h += 16) {
+      float old[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        old[i] = g.accumulate && n + h + i < g.N ? reinterpret_cast<const float*>(g.c)[o + (h + i) * g.ldc] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (n + h + i < g.N) g8_put(g, o + (h + i) * g.ldc, old[i] + v[h + i]);
+    }
     return;
   }
-  const int64_t o = m * g.ldc + n;
-  const int size = g.c_bf16 ? 2 : 4;
-  char* p = reinterpret_cast<char*>(g.c) + o * size;
-  if (n + 16 <= g.N && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+  if (g.sectors && n + 32 <= g.N) {
+    if (m >= g.M) return;
+    char* p = reinterpret_cast<char*>(g.c) + (m * g.ldc + n) * (g.c_bf16 ? 2 : 4);
     if (g.c_bf16) {
-      uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = bf16x2_bits(v[2 * i], v[2 * i + 1]);
-      reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else {
+      for (int j = 0; j < 2; ++j) {
+        uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float4* q = reinterpret_cast<float4*>(p) + i;
-        float4 x = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        if (g.accumulate) {
-          const float4 y = *q;
-          x = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+        for (int i = 0; i < 8; ++i) w[i] = bf16x2_bits(v[16 * j + 2 * i], v[16 * j + 2 * i + 1]);
+        st_sector(p + 32 * j, w);
+      }
+      return;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {       // 16 columns at a time: a pair's drain has few registers left
+      float4 old[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        old[i] = g.accumulate ? reinterpret_cast<const float4*>(p)[4 * h + i] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4& x = old[2 * j + (i >> 2)];
+          w[i] = __float_as_uint((&x.x)[i & 3] + v[16 * h + 8 * j + i]);
         }
-        *q = x;
+        st_sector(p + 64 * h + 32 * j, w);
       }
     }
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (n + i < g.N) g8_store(g, o + i, v[i]);
+  for (int i = 0; i < 32; ++i) xs[lane * G8_XS_LD + i] = v[i];
+  __syncwarp();
+  const int rows = (int)min((int64_t)32, g.M - m0);
+  if (n + lane < g.N) {
+    const int64_t o = m0 * g.ldc + n + lane;
+    for (int h = 0; h < rows; h += 8) {
+      float old[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        old[i] = g.accumulate && h + i < rows ? reinterpret_cast<const float*>(g.c)[o + (h + i) * g.ldc] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (h + i < rows) g8_put(g, o + (h + i) * g.ldc, old[i] + xs[(h + i) * G8_XS_LD + lane]);
+    }
+  }
+  __syncwarp();
+}
+
+// One lane of the warp; what it issues keeps its operands in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p != 0;
 }
 
 constexpr int G8_RASTER = 8;           // tile rows that run side by side, so that their panels stay in L2
@@ -233,99 +284,96 @@ gemm8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
 
   if (warp == 0) {
     // ------------------------------------------------ loads
-    if (lane == 0) {
-      uint32_t q = 0;
-      bool ok = true;
-      for (int64_t t = first_tile; t < tiles && ok; t += tile_step) {
-        int64_t ti, tj;
-        g8_tile(t, tiles_m, tiles_n, ti, tj);
-        const int64_t rb_b = tj * BN / 128;              // first 128-row block of B's scales
-        const uint32_t sfb_bytes = 512u * (uint32_t)min((int64_t)SM::SFB_ATOMS, g.sb_rb - rb_b);
-        for (int kb = kb0; kb < kb1; ++kb, ++q) {
-          const uint32_t s = q % SM::STAGES, round = q / SM::STAGES;
-          if (round > 0 && !mbar_wait(empty_bar(s), (round - 1) & 1, g.err, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const bool head = (kb & 3) == 0;
-          const uint32_t st = base + s * (SM::A_BYTES + SM::B_BYTES);
-          mbar_expect_tx(full_bar(s), SM::A_BYTES + SM::B_BYTES + (head ? 512u + sfb_bytes : 0u));
+    uint32_t q = 0;
+    bool ok = true;
+    for (int64_t t = first_tile; t < tiles && ok; t += tile_step) {
+      int64_t ti, tj;
+      g8_tile(t, tiles_m, tiles_n, ti, tj);
+      const int64_t rb_b = tj * BN / 128;              // first 128-row block of B's scales
+      for (int kb = kb0; kb < kb1; ++kb, ++q) {
+        const uint32_t s = q % SM::STAGES, round = q / SM::STAGES;
+        if (round > 0 && !mbar_wait(empty_bar(s), (round - 1) & 1, g.err, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const bool head = (kb & 3) == 0;
+        const uint32_t st = base + s * (SM::A_BYTES + SM::B_BYTES);
+        if (elect_one()) {
+          mbar_expect_tx(full_bar(s), SM::A_BYTES + SM::B_BYTES + (head ? 1024u : 0u));
           tma_load_2d(st, &map_a, full_bar(s), kb * G8_BK, (int)(ti * G8_BM));
           tma_load_2d(st + SM::A_BYTES, &map_b, full_bar(s), kb * G8_BK, (int)(tj * BN));
           if (head) {
             const uint32_t sf = base + SM::OFF_SF + s * SM::SF_BYTES;
             bulk_load(sf, g.sa + ((int64_t)(kb >> 2) * g.sa_rb + ti) * 512, 512u, full_bar(s));
-            bulk_load(sf + 512, g.sb + ((int64_t)(kb >> 2) * g.sb_rb + rb_b) * 512, sfb_bytes, full_bar(s));
+            bulk_load(sf + 512, g.sb + ((int64_t)(kb >> 2) * g.sb_rb + rb_b) * 512, 512u, full_bar(s));
           }
         }
+        __syncwarp();
       }
-      // every copy issued has landed before the CTA may exit
-      for (uint32_t i = (q > (uint32_t)SM::STAGES ? q - SM::STAGES : 0u); i < q; ++i)
-        mbar_wait_own(full_bar(i % SM::STAGES), (i / SM::STAGES) & 1, g.err);
     }
+    // every copy issued has landed before the CTA may exit
+    for (uint32_t i = (q > (uint32_t)SM::STAGES ? q - SM::STAGES : 0u); i < q; ++i)
+      mbar_wait_own(full_bar(i % SM::STAGES), (i / SM::STAGES) & 1, g.err);
   } else if (warp == 1) {
     // ------------------------------------------------ MMAs
-    if (lane == 0) {
-      uint32_t q = 0, seg = 0, grp = 0;
-      bool ok = true;
-      for (int64_t t = first_tile; t < tiles && ok; t += tile_step) {
-        for (int kb = kb0; kb < kb1; ++kb, ++q) {
-          const bool first = PROMOTE ? ((kb - kb0) % G8_SEGMENT == 0) : kb == kb0;
-          const uint32_t buf = seg & 1;
-          if (first) {
-            if (seg >= 2 && !mbar_wait(acc_empty(buf), ((seg >> 1) - 1) & 1, g.err, abort_flag)) {
-              ok = false;
-              break;
-            }
+    // The warp runs the loop together and one elected lane issues: descriptors then stay in uniform
+    // registers (a loop of lane 0 alone took 0.39 us a block of a pair's tile, not 0.26).
+    uint32_t q = 0, seg = 0, grp = 0;
+    bool ok = true;
+    for (int64_t t = first_tile; t < tiles && ok; t += tile_step) {
+      for (int kb = kb0; kb < kb1; ++kb, ++q) {
+        const bool first = PROMOTE ? ((kb - kb0) % G8_SEGMENT == 0) : kb == kb0;
+        const bool last = kb == kb1 - 1 || (PROMOTE && (kb - kb0) % G8_SEGMENT == G8_SEGMENT - 1);
+        const uint32_t buf = seg & 1, s = q % SM::STAGES;
+        if ((first && seg >= 2 && !mbar_wait(acc_empty(buf), ((seg >> 1) - 1) & 1, g.err, abort_flag)) ||
+            !mbar_wait(full_bar(s), (q / SM::STAGES) & 1, g.err, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t st = base + s * (SM::A_BYTES + SM::B_BYTES);
+        const bool head = (kb & 3) == 0;
+        grp += head;
+        const uint32_t tsf = tmem + SM::SF_COL + (grp & 1) * SM::SF_COLS;
+        const uint32_t idesc = mx_idesc<BN>(kb & 3);
+        const uint64_t da = sw128_desc(st), db = sw128_desc(st + SM::A_BYTES);
+        const uint32_t d = tmem + buf * SM::ACC_COLS;
+        if (elect_one()) {
+          if (head) {
+            const uint64_t sf = scale_desc(base + SM::OFF_SF + s * SM::SF_BYTES);
+            copy_scales(tsf, sf);
+            copy_scales(tsf + 4, sf + 32);
           }
-          const uint32_t s = q % SM::STAGES;
-          if (!mbar_wait(full_bar(s), (q / SM::STAGES) & 1, g.err, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t st = base + s * (SM::A_BYTES + SM::B_BYTES);
-          if ((kb & 3) == 0) {
-            ++grp;
-            const uint32_t sf = base + SM::OFF_SF + s * SM::SF_BYTES;
-            const uint32_t tsf = tmem + SM::SF_COL + (grp & 1) * SM::SF_COLS;
-            copy_scales(tsf, scale_desc(sf));
-#pragma unroll
-            for (int b = 0; b < SM::SFB_ATOMS; ++b) copy_scales(tsf + 4 + 4 * b, scale_desc(sf + 512 + 512 * b));
-          }
-          const uint32_t tsf = tmem + SM::SF_COL + (grp & 1) * SM::SF_COLS;
-          const uint32_t idesc = mx_idesc<BN>(kb & 3);
 #pragma unroll
           for (int k = 0; k < G8_BK / 32; ++k)
-            mx_mma(tmem + buf * SM::ACC_COLS, sw128_desc(st + 32 * k), sw128_desc(st + SM::A_BYTES + 32 * k), idesc, tsf,
-                   tsf + 4, first && k == 0 ? 0u : 1u);
+            mx_mma(d, da + 2 * k, db + 2 * k, idesc, tsf, tsf + 4, first && k == 0 ? 0u : 1u);
           tc_commit(empty_bar(s));
-          if (kb == kb1 - 1 || (PROMOTE && (kb - kb0) % G8_SEGMENT == G8_SEGMENT - 1)) {
-            tc_commit(acc_full(buf));
-            ++seg;
-          }
+          if (last) tc_commit(acc_full(buf));
         }
+        __syncwarp();
+        seg += last;
       }
-      // every MMA issued has completed before tensor memory is released
-      tc_commit(final_bar);
-      mbar_wait_own(final_bar, 0, g.err);
     }
+    // every MMA issued has completed before tensor memory is released
+    if (elect_one()) tc_commit(final_bar);
+    __syncwarp();
+    mbar_wait_own(final_bar, 0, g.err);
   } else {
     // ------------------------------------------------ sums and results
-    constexpr int HALF = BN >= 32 ? BN / 2 : BN;       // columns of this warp (BN = 16: the first four warps take all)
+    constexpr int HALF = BN >= 64 ? BN / 2 : BN;       // columns of a warp (BN <= 32: the first four warps take all)
+    constexpr int STEP = HALF < 32 ? HALF : 32;
     const int qd = warp & 3, own = (warp - 2) >> 2;
-    const bool works = BN >= 32 || own == 0;
-    const int r = qd * 32 + lane;
+    const bool works = BN >= 64 || own == 0;
     const uint32_t tlane = tmem + ((uint32_t)(qd * 32) << 16) + (uint32_t)(own * HALF);
+    float* xs = reinterpret_cast<float*>(gbase + SM::OFF_XS) + (warp - 2) * (32 * G8_XS_LD);
     const int segs = kb1 <= kb0 ? 0 : PROMOTE ? (kb1 - kb0 + G8_SEGMENT - 1) / G8_SEGMENT : 1;
     uint32_t seg = 0;
     for (int64_t t = first_tile; t < tiles; t += tile_step) {
       int64_t ti, tj;
       g8_tile(t, tiles_m, tiles_n, ti, tj);
-      const int64_t m = ti * G8_BM + r, n0 = tj * BN + own * HALF;
-      float acc[HALF];
+      float sum[HALF];
 #pragma unroll
-      for (int j = 0; j < HALF; ++j) acc[j] = 0.f;
+      for (int j = 0; j < HALF; ++j) sum[j] = 0.f;
       bool ok = true;
       for (int i = 0; i < segs; ++i, ++seg) {
         const uint32_t buf = seg & 1;
@@ -336,12 +384,13 @@ gemm8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         tc_fence_after();
         if (works) {
 #pragma unroll
-          for (int j = 0; j < HALF; j += 16) {
-            uint32_t v[16];
-            tmem_ld16_nowait(tlane + buf * SM::ACC_COLS + j, v);
+          for (int j = 0; j < HALF; j += STEP) {
+            uint32_t v[STEP];
+#pragma unroll
+            for (int k = 0; k < STEP; k += 16) tmem_ld16_nowait(tlane + buf * SM::ACC_COLS + j + k, v + k);
             tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) acc[j + k] += __uint_as_float(v[k]);
+            for (int k = 0; k < STEP; ++k) sum[j + k] += __uint_as_float(v[k]);
           }
         }
         tc_fence_before();
@@ -349,22 +398,20 @@ gemm8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         if (lane == 0) mbar_arrive(acc_empty(buf));
       }
       if (!ok) break;
+      if (!works) continue;
       if (parts == 1) {
-        if (works) {
 #pragma unroll
-          for (int j = 0; j < HALF; j += 16) {
-            float v[16];
+        for (int j = 0; j < HALF; j += STEP) {
+          float v[32];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = acc[j + k];
-            g8_store16(g, m, n0 + j, v);
-          }
+          for (int k = 0; k < 32; ++k) v[k] = k < STEP ? sum[j + k] : 0.f;
+          g8_store32(g, xs, ti * G8_BM + qd * 32, tj * BN + own * HALF + j, v);
         }
-      } else if (works) {
-        // this CTA's sums to its own shared memory (the ring is idle: its last MMA has completed),
-        // columns outermost, for the cluster to read
-        float* mine = reinterpret_cast<float*>(gbase);
+      } else {
+        // to this CTA's own shared memory (the ring is idle: its last MMA has completed), for the cluster
+        float* mine = reinterpret_cast<float*>(gbase) + (qd * 32 + lane) * SM::PART_LD + own * HALF;
 #pragma unroll
-        for (int j = 0; j < HALF; ++j) mine[(own * HALF + j) * G8_BM + r] = acc[j];
+        for (int j = 0; j < HALF; ++j) mine[j] = sum[j];
       }
     }
   }
@@ -372,19 +419,36 @@ gemm8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
   if (parts > 1) {
     __syncwarp();
     cluster.sync();
-    // column c of the tile belongs to CTA c % parts; 128 threads a column
+    // Every CTA adds 1 / parts of the tile's elements, the stretches in their order: lanes along C's rows.
+    // All loads of a round go before their sums.
     int64_t ti, tj;
     g8_tile(first_tile, tiles_m, tiles_n, ti, tj);
-    if (threadIdx.x < 256) {
-      const int r = threadIdx.x & 127;
-      const int64_t m = ti * G8_BM + r;
-      for (int c = part + parts * (threadIdx.x >> 7); c < BN; c += 2 * parts) {
-        float v = 0.f;
-        for (int k = 0; k < parts; ++k)
-          v += cluster.map_shared_rank(reinterpret_cast<float*>(gbase), k)[c * G8_BM + r];
-        const int64_t n = tj * BN + c;
-        if (m < g.M && n < g.N) g8_store(g, g.swap ? n * g.ldc + m : m * g.ldc + n, v);
+    constexpr int ROUND = 4;
+    const int share = (G8_BM * BN + parts - 1) / parts, threads = blockDim.x;
+    for (int e0 = threadIdx.x; e0 < share; e0 += ROUND * threads) {
+      float v[ROUND], old[ROUND];
+      int64_t o[ROUND];
+#pragma unroll
+      for (int u = 0; u < ROUND; ++u) {
+        const int e = part * share + e0 + u * threads;
+        const int r = g.swap ? e % G8_BM : e / BN, c = g.swap ? e / G8_BM : e % BN;
+        const int64_t m = ti * G8_BM + r, n = tj * BN + c;
+        const bool in = e0 + u * threads < share && e < G8_BM * BN && m < g.M && n < g.N;
+        o[u] = in ? (g.swap ? n * g.ldc + m : m * g.ldc + n) : -1;
+        old[u] = in && g.accumulate ? reinterpret_cast<const float*>(g.c)[o[u]] : 0.f;
+        v[u] = 0.f;
+        if (in) {
+          float w[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            w[k] = k < parts ? cluster.map_shared_rank(reinterpret_cast<float*>(gbase), k)[r * SM::PART_LD + c] : 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[u] += w[k];
+        }
       }
+#pragma unroll
+      for (int u = 0; u < ROUND; ++u)
+        if (o[u] >= 0) g8_put(g, o[u], old[u] + v[u]);
     }
     cluster.sync();
   }
@@ -394,6 +458,282 @@ gemm8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;"
                  ::"r"(tmem), "r"((uint32_t)SM::TMEM_COLS) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ pairs of CTAs
+// Larger products: the two SMs of a CTA pair share one tcgen05.mma of M = N = 256
+// (cta_group::2).  Each CTA holds 128 rows of A and 128 of B, so that a block of
+// 128 columns costs it 32 KB of loads and 512 cycles of MMA: half the loads and
+// shared-memory reads of a 128 x 128 tile at the same rate.
+//
+// The even CTA (the leader) issues the MMAs and the scale copies for both.
+// Both CTAs' loads complete on the leader's barriers; commits go to both CTAs;
+// "drained" comes back to the leader from both.
+//
+// Tensor memory holds two sum buffers and two of scales.  Two buffers of 256
+// columns do not fit beside the scales: they share 32 columns (0..255 and
+// 224..479), which the drain reads first; the next tile's MMAs wait for those,
+// and for the rest of the tile before it.
+struct PairSmem {
+  static constexpr int BN = 256;
+  static constexpr int A_BYTES = 128 * G8_BK;
+  static constexpr int B_BYTES = BN / 2 * G8_BK;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int SF_BYTES = 512 * 3;                             // own rows of A, all of B
+  static constexpr int STAGES = 5;
+  static constexpr int OFF_SF = STAGES * STAGE_BYTES;
+  static constexpr int OFF_XS = OFF_SF + STAGES * SF_BYTES;            // a scratch of each drain warp
+  static constexpr int OFF_BAR = OFF_XS + G8_EPI_WARPS * 32 * G8_XS_LD * 4;
+  static constexpr int BYTES = 1024 + OFF_BAR + 256;
+  static constexpr int ACC1 = 224;                                     // second buffer's first column
+  static constexpr int SF_COL = ACC1 + BN, SF_COLS = 12;
+  static_assert(SF_COL + 2 * SF_COLS <= 512, "tensor memory");
+  static_assert(BYTES <= 232448, "shared memory");
+};
+
+struct PairMaps {
+  CUtensorMap a, b, sa, sb;
+};
+
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void copy_scales_pair(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void mx_mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                            uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc));
+}
+// Arrives on the barrier of both CTAs once the MMAs and copies issued so far have completed.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               ::"r"(bar), "h"((uint16_t)3) : "memory");
+}
+// On a barrier of another CTA of the cluster.  Relaxed: it tells that tensor memory has been read
+// (tcgen05.wait::ld has returned), and no memory is handed over; a release waited for everything this
+// thread had in flight, 0.8 us of every segment (4096 x 1024 x 8192 to fp32: 43.0 us, 36.9 us relaxed).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+template <bool PROMOTE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_PAIR_THREADS, 1)
+gemm8_pair_kernel(const __grid_constant__ PairMaps maps, Gemm8Args g) {
+  using SM = PairSmem;
+  constexpr int BN = SM::BN;
+  namespace cg = cooperative_groups;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* tail = smem_raw + (base - raw) + SM::OFF_BAR;
+  const uint32_t bars = smem_u32(tail);
+  auto full_bar = [&](uint32_t s) { return bars + 8u * s; };
+  auto empty_bar = [&](uint32_t s) { return bars + 8u * (SM::STAGES + s); };
+  auto acc_full = [&](uint32_t b) { return bars + 8u * (2 * SM::STAGES + b); };
+  auto acc_empty = [&](uint32_t b) { return bars + 8u * (2 * SM::STAGES + 2 + b); };
+  const uint32_t shared_empty = bars + 8u * (2 * SM::STAGES + 4);
+  const uint32_t final_bar = bars + 8u * (2 * SM::STAGES + 5);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + 8 * (2 * SM::STAGES + 6));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  cg::cluster_group cluster = cg::this_cluster();
+  const uint32_t rank = cluster.block_rank();
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    const CUtensorMap* all[4] = {&maps.a, &maps.b, &maps.sa, &maps.sb};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(all[i])) : "memory");
+    for (int s = 0; s < SM::STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), 1);
+      mbar_init(acc_empty(b), 2 * G8_EPI_WARPS);
+    }
+    mbar_init(shared_empty, G8_EPI_WARPS);          // four warps of each CTA
+    mbar_init(final_bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_u32(tmem_slot)), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster.sync();                                    // the peer's barriers are ready
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  uint32_t to_leader;                                // from a barrier to the leader's
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to_leader) : "r"(bars));
+  to_leader -= bars;
+
+  const int64_t tiles_m = (g.M + 255) / 256, tiles_n = (g.N + BN - 1) / BN;
+  const int64_t tiles = tiles_m * tiles_n;
+  const int64_t first_tile = blockIdx.x / 2, tile_step = gridDim.x / 2;
+  const int nkb = (int)((g.K + G8_BK - 1) / G8_BK);
+
+  // registers: 384 x 168 at launch; 128 x 80 + 256 x 208 = 63488 now
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  if (warp == 0) {
+    // ------------------------------------------------ loads of this CTA's halves
+    uint32_t q = 0;
+    bool ok = true;
+    for (int64_t t = first_tile; t < tiles && ok; t += tile_step) {
+      int64_t ti, tj;
+      g8_tile(t, tiles_m, tiles_n, ti, tj);
+      const int ra = (int)(2 * ti + rank), rb = (int)(tj * BN / 128);   // (first) blocks of 128 rows
+      for (int kb = 0; kb < nkb; ++kb, ++q) {
+        const uint32_t s = q % SM::STAGES, round = q / SM::STAGES;
+        if (round > 0 && !mbar_wait(empty_bar(s), (round - 1) & 1, g.err, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const bool head = (kb & 3) == 0;
+        const uint32_t st = base + s * SM::STAGE_BYTES, bar = full_bar(s) + to_leader;
+        if (elect_one()) {
+          if (leader) mbar_expect_tx(full_bar(s), 2 * (SM::STAGE_BYTES + (head ? SM::SF_BYTES : 0)));
+          tma_load_2d_pair(st, &maps.a, bar, kb * G8_BK, ra * 128);
+          tma_load_2d_pair(st + SM::A_BYTES, &maps.b, bar, kb * G8_BK, (int)(tj * BN) + (int)rank * (BN / 2));
+          if (head) {
+            const uint32_t sf = base + SM::OFF_SF + s * SM::SF_BYTES;
+            tma_load_2d_pair(sf, &maps.sa, bar, 0, (kb >> 2) * (int)g.sa_rb + ra);
+            tma_load_2d_pair(sf + 512, &maps.sb, bar, 0, (kb >> 2) * (int)g.sb_rb + rb);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // the leader sees every copy of both CTAs land before either may exit
+    if (leader)
+      for (uint32_t i = (q > (uint32_t)SM::STAGES ? q - SM::STAGES : 0u); i < q; ++i)
+        mbar_wait_own(full_bar(i % SM::STAGES), (i / SM::STAGES) & 1, g.err);
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMAs (leader)
+    // The warp runs the loop together and one elected lane issues: descriptors then stay in uniform registers.
+    if (leader) {
+      uint32_t q = 0, seg = 0, grp = 0;
+      bool ok = true;
+      for (int64_t t = first_tile; t < tiles && ok; t += tile_step) {
+        for (int kb = 0; kb < nkb; ++kb, ++q) {
+          const bool first = PROMOTE ? kb % G8_PAIR_SEGMENT == 0 : kb == 0;
+          const bool last = kb == nkb - 1 || (PROMOTE && kb % G8_PAIR_SEGMENT == G8_PAIR_SEGMENT - 1);
+          const uint32_t buf = seg & 1;
+          if (first) {
+            if ((seg >= 1 && !mbar_wait(shared_empty, (seg - 1) & 1, g.err, abort_flag)) ||
+                (seg >= 2 && !mbar_wait(acc_empty(buf), ((seg >> 1) - 1) & 1, g.err, abort_flag))) {
+              ok = false;
+              break;
+            }
+          }
+          const uint32_t s = q % SM::STAGES;
+          if (!mbar_wait(full_bar(s), (q / SM::STAGES) & 1, g.err, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = base + s * SM::STAGE_BYTES;
+          const bool head = (kb & 3) == 0;
+          grp += head;
+          const uint32_t tsf = tmem + SM::SF_COL + (grp & 1) * SM::SF_COLS;
+          const uint32_t id = kb & 3;
+          const uint32_t idesc = id << 4 | (uint32_t)(BN >> 3) << 17 | 1u << 23 | (256u >> 4) << 24 | id << 29;
+          const uint64_t da = sw128_desc(st), db = sw128_desc(st + SM::A_BYTES);
+          const uint32_t d = tmem + buf * SM::ACC1;
+          if (elect_one()) {
+            if (head) {
+              const uint64_t sf = scale_desc(base + SM::OFF_SF + s * SM::SF_BYTES);
+#pragma unroll
+              for (int b = 0; b < 3; ++b) copy_scales_pair(tsf + 4 * b, sf + 32 * b);
+            }
+#pragma unroll
+            for (int k = 0; k < G8_BK / 32; ++k)
+              mx_mma_pair(d, da + 2 * k, db + 2 * k, idesc, tsf, tsf + 4, first && k == 0 ? 0u : 1u);
+            tc_commit_pair(empty_bar(s));
+            if (last) tc_commit_pair(acc_full(buf));
+          }
+          __syncwarp();
+          seg += last;
+        }
+      }
+      if (elect_one()) tc_commit_pair(final_bar);
+      __syncwarp();
+      mbar_wait_own(final_bar, 0, g.err);
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ------------------------------------------------ sums and results
+    constexpr int HALF = BN / 2, STEP = 32;            // columns of a warp, and of one read
+    const int qd = warp & 3, own = (warp >> 2) - 1;   // tensor-memory lane quadrant, column half
+    const uint32_t tlane = tmem + ((uint32_t)(qd * 32) << 16) + own * HALF;
+    float* xs = reinterpret_cast<float*>(smem_raw + (base - raw) + SM::OFF_XS) + (warp - 4) * (32 * G8_XS_LD);
+    const int segs = PROMOTE ? (nkb + G8_PAIR_SEGMENT - 1) / G8_PAIR_SEGMENT : 1;
+    uint32_t seg = 0;
+    for (int64_t t = first_tile; t < tiles; t += tile_step) {
+      int64_t ti, tj;
+      g8_tile(t, tiles_m, tiles_n, ti, tj);
+      float sum[HALF];
+      bool ok = true;
+      for (int i = 0; i < segs; ++i, ++seg) {
+        const uint32_t buf = seg & 1;
+        if (!mbar_wait(acc_full(buf), (seg >> 1) & 1, g.err, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // where the buffers share columns (224..255 of the first, 0..31 of the second), the upper
+        // half's warps go downwards, so that both begin with those
+#pragma unroll
+        for (int j = 0; j < HALF; j += STEP) {
+          uint32_t v[STEP];
+          const uint32_t at = tlane + buf * SM::ACC1 + (own ? HALF - STEP - j : j);
+#pragma unroll
+          for (int k = 0; k < STEP; k += 16) tmem_ld16_nowait(at + k, v + k);
+          tmem_ld_wait();
+          if (j == 0 && own != (int)buf) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(shared_empty + to_leader);
+          }
+#pragma unroll
+          for (int k = 0; k < STEP; ++k) sum[j + k] = (PROMOTE && i > 0 ? sum[j + k] : 0.f) + __uint_as_float(v[k]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty(buf) + to_leader);
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int j = 0; j < HALF; j += STEP) {
+        float v[STEP];
+#pragma unroll
+        for (int k = 0; k < STEP; ++k) v[k] = sum[j + k];
+g8_store32(g, xs, ti * 256 + rank * 128 + qd * 32, tj * BN + own * HALF + (own ? HALF - STEP - j : j), v);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster.sync();                                    // both CTAs are done with each other's barriers and tensor memory
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
 }
 

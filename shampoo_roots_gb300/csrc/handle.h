@@ -21,6 +21,7 @@ struct Handle {
   int64_t launches = 0;                // kernels launched since creation
   EncodeTiledFn encode = nullptr;
   unsigned int* op_err = nullptr;      // operators: device word, set when a bounded wait ran out
+  int pairs = 0;                       // operators: CTA pairs that are resident at once
   bool op_ready = false;               // operators: kernel attributes set on this device
 };
 

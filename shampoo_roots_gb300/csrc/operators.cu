@@ -80,6 +80,14 @@ int prepare(Handle* h) {
     OP_CK(gemm8_attributes<32>());
     OP_CK(gemm8_attributes<64>());
     OP_CK(gemm8_attributes<128>());
+    OP_CK(cudaFuncSetAttribute(gemm8_pair_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, PairSmem::BYTES));
+    OP_CK(cudaFuncSetAttribute(gemm8_pair_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, PairSmem::BYTES));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(h->num_sms / 2 * 2);
+    cfg.blockDim = dim3(G8_PAIR_THREADS);
+    cfg.dynamicSmemBytes = PairSmem::BYTES;
+    OP_CK(cudaOccupancyMaxActiveClusters(&h->pairs, gemm8_pair_kernel<false>, &cfg));
+    if (h->pairs < 1) return PRECOND_ECUDA;
     OP_CK(cudaMalloc(&h->op_err, sizeof(unsigned int)));
     OP_CK(cudaMemset(h->op_err, 0, sizeof(unsigned int)));
     OP_CK(cudaDeviceSynchronize());
@@ -165,6 +173,36 @@ int encode8(Handle* h, CUtensorMap* map, const void* q, int64_t rows, int64_t co
     fprintf(stderr, "libprecond: cuTensorMapEncodeTiled failed (%d)\n", (int)r);
     return PRECOND_ECUDA;
   }
+  return PRECOND_OK;
+}
+
+// The scales of `blocks` x 128 rows a group as rows of 512 bytes; boxes of `box` of them.
+int encode_scales(Handle* h, CUtensorMap* map, const uint8_t* s, int64_t blocks, int groups, int box_rows) {
+  cuuint64_t dims[2] = {128, (cuuint64_t)(blocks * groups)};
+  cuuint64_t strides[1] = {512};
+  cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = h->encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(s), dims, strides, box, estr,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    fprintf(stderr, "libprecond: cuTensorMapEncodeTiled failed (%d)\n", (int)r);
+    return PRECOND_ECUDA;
+  }
+  return PRECOND_OK;
+}
+
+int launch_pair(Handle* h, const void* A, int64_t lda, const void* B, int64_t ldb, const Gemm8Args& g, cudaStream_t st) {
+  PairMaps maps;
+  const int groups = q8_groups(g.K);
+  int rc;
+  if ((rc = encode8(h, &maps.a, A, g.M, g.K, lda, 128)) || (rc = encode8(h, &maps.b, B, g.N, g.K, ldb, 128)) ||
+      (rc = encode_scales(h, &maps.sa, g.sa, g.sa_rb, groups, 1)) || (rc = encode_scales(h, &maps.sb, g.sb, g.sb_rb, groups, 2)))
+    return rc;
+  const int64_t tiles = ((g.M + 255) / 256) * ((g.N + 255) / 256);
+  const unsigned grid = 2 * (unsigned)std::min<int64_t>(tiles, h->pairs);
+  auto k = g.c_bf16 ? gemm8_pair_kernel<false> : gemm8_pair_kernel<true>;
+  OP_CK(launch(k, dim3(grid), dim3(G8_PAIR_THREADS), PairSmem::BYTES, st, 1, maps, g));
   return PRECOND_OK;
 }
 
@@ -344,7 +382,7 @@ int precond_gemm8(precond_t ph, int64_t M, int64_t N, int64_t K, const void* A, 
   // and its bytes, which bound the call, are read once).
   const bool swap = M <= 64 && M < N;
   Gemm8Args g = {swap ? N : M, swap ? M : N, K, scale_a, q8_row_blocks(M), scale_b, q8_row_blocks(N), C, ldc,
-                 c_dtype == PRECOND_BF16, accumulate, swap, h->op_err};
+                 c_dtype == PRECOND_BF16, accumulate, aligned(C, 32) && ldc * (int64_t)size_of(c_dtype) % 32 == 0, swap, h->op_err};
   if (swap) {
     std::swap(A, B);
     std::swap(lda, ldb);
@@ -355,9 +393,19 @@ int precond_gemm8(precond_t ph, int64_t M, int64_t N, int64_t K, const void* A, 
   const int64_t tiles = ((g.M + G8_BM - 1) / G8_BM) * ((g.N + bn - 1) / bn);
   if (tiles > INT32_MAX) return PRECOND_EINVAL;
   // Few tiles: a cluster of up to 8 CTAs shares each, a stretch of whole scale groups of K each.
-  const int groups = q8_groups(K);
+  const int blocks = (int)((K + G8_BK - 1) / G8_BK), groups = q8_groups(K);
   int parts = 1;
   while (parts < 8 && tiles * parts * 2 <= h->num_sms && parts * 2 <= groups) parts *= 2;
+  // Pairs of CTAs where they are expected to end first: a 256 x 256 tile's block of K takes a pair 0.30 us,
+  // a 128 x 128 tile's a CTA 0.25 us, and joining stretches 2 us.
+  const int64_t pair_tiles = ((g.M + 255) / 256) * ((g.N + 255) / 256);
+  const double pair_us = 0.30 * blocks * (double)((pair_tiles + h->pairs - 1) / h->pairs);
+  const double lone_us = 0.25 * ((groups + parts - 1) / parts * 4) * (double)((tiles * parts + h->num_sms - 1) / h->num_sms) + (parts > 1 ? 2.0 : 0.0);
+  if (bn == 128 && K > 0 && pair_us <= lone_us) {
+    if ((rc = launch_pair(h, A, lda, B, ldb, g, st))) return rc;
+    ++h->launches;
+    return PRECOND_OK;
+  }
   CUtensorMap ma, mb;
   memset(&ma, 0, sizeof(ma));
   memset(&mb, 0, sizeof(mb));
