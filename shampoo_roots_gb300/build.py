@@ -2,11 +2,13 @@
 import os
 import shutil
 import subprocess
+import sysconfig
 import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libprecond.so")
+BINDING = os.path.join(HERE, "_binding.so")      # csrc/binding.c: the operators' argument marshalling
 SOURCES = ["precond.cu", "operators.cu"]
 FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC"]
@@ -29,13 +31,15 @@ def sources_newer_than(target):
 
 
 def build(force=False, verbose=False):
-    if not force and not sources_newer_than(OUT):
+    if not force and not sources_newer_than(OUT) and not sources_newer_than(BINDING):
         return OUT
     tmp = OUT + ".tmp"
     with tempfile.TemporaryDirectory(prefix="precond_build_") as d:
         objs = [os.path.join(d, os.path.splitext(s)[0] + ".o") for s in SOURCES]
         cmds = [[nvcc()] + FLAGS + ["-c", "-o", o, os.path.join(CSRC, s)] for s, o in zip(SOURCES, objs)]
         link = [nvcc()] + FLAGS + ["-shared", "-o", tmp] + objs
+        cmds.append(["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"], "-o", BINDING + ".tmp",
+                     os.path.join(CSRC, "binding.c")])
         if verbose:
             for c in cmds + [link]:
                 print(" ".join(c))
@@ -45,6 +49,7 @@ def build(force=False, verbose=False):
             if rc:
                 raise subprocess.CalledProcessError(rc, c)
         subprocess.run(link, check=True, cwd=CSRC)
+    os.replace(BINDING + ".tmp", BINDING)
     os.replace(tmp, OUT)
     return OUT
 
