@@ -40,12 +40,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// max that keeps a NaN
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 constexpr float LOG2E = 1.4426950408889634f;
 
 // Running (maximum, sum of exp((z - max) / tau)): joins (m2, s2) to (m, s).
@@ -61,14 +55,14 @@ template <typename T> struct LogitVec;                    // one 16-byte vector 
 template <> struct LogitVec<__nv_bfloat16> {
   static constexpr int N = 8;
   static __device__ __forceinline__ void unpack(uint4 w, float (&f)[8]) {
-    Raw8<__nv_bfloat16> o;
-    o.v = w;
-    unpack8(o, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float((&w.x)[i] << 16);
+      f[2 * i + 1] = __uint_as_float((&w.x)[i] & 0xFFFF0000u);
+    }
   }
   static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-    Raw8<__nv_bfloat16> o;
-    pack8(o, f);
-    return o.v;
+    return make_uint4(bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]), bf16x2_bits(f[4], f[5]), bf16x2_bits(f[6], f[7]));
   }
 };
 template <> struct LogitVec<float> {

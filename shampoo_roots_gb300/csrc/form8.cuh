@@ -68,140 +68,200 @@ __device__ __forceinline__ unsigned finite_bits(float x) {
   return b < INF_BITS ? b : 0u;
 }
 
-// ------------------------------------------------------------- 8 consecutive elements
-// Raw loads keep a prefetched vector at its storage size.  L1 is bypassed for
-// data that a kernel reads once.
-template <typename T> struct Raw8;
-template <> struct Raw8<__nv_bfloat16> { uint4 v; };
-template <> struct Raw8<float> { uint4 v, w; };
-
-__device__ __forceinline__ uint4 ld_once(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+// ------------------------------------------------------------- 16 consecutive elements
+// A thread's vector is 16 elements: 32 bytes of bf16 (one sector, one load), so
+// that 8 lanes hold a scale block.  Arithmetic goes in fp32 pairs (add, mul and
+// fma .f32x2 round each half as the scalar instruction does), half the
+// instructions of the scalar form.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 f2_of(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ float2 f2_get(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum2(f2 v) {
+  const float2 x = f2_get(v);
+  return x.x + x.y;
+}
 
-// Elements c .. c + 7 of a row of `cols`; what lies past the row's end is zero.
-// VEC: the row is 16-byte aligned and cols % 8 == 0.
+struct F16 { f2 p[8]; };                               // 16 values
+template <typename T> struct Raw16;                    // 16 elements as stored
+template <> struct Raw16<__nv_bfloat16> { uint32_t w[8]; };
+template <> struct Raw16<float> { uint32_t w[16]; };
+
+__device__ __forceinline__ void ld_sector(uint32_t* w, const void* p) {   // 32 bytes, 32-byte aligned
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p) : "memory");
+}
+__device__ __forceinline__ void st_sector(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+
+// Elements c .. c + 15 of a row of `cols`; what lies past the row's end is zero.
+// VEC: rows are 32-byte aligned and cols is a multiple of 16.
 template <bool VEC>
-__device__ __forceinline__ void load8(Raw8<__nv_bfloat16>& o, const __nv_bfloat16* row, int64_t c, int64_t cols) {
-  o.v = make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void load16(Raw16<__nv_bfloat16>& o, const __nv_bfloat16* row, int c, int cols) {
   if (VEC) {
-    if (c < cols) o.v = ld_once(row + c);
+    if (c < cols) {
+      ld_sector(o.w, row + c);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o.w[i] = 0;
+    }
   } else {
     const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
-    uint32_t* w = &o.v.x;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < cols) w[i >> 1] |= (uint32_t)p[c + i] << (16 * (i & 1));
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t lo = c + 2 * i < cols ? p[c + 2 * i] : 0, hi = c + 2 * i + 1 < cols ? p[c + 2 * i + 1] : 0;
+      o.w[i] = lo | hi << 16;
+    }
   }
 }
 template <bool VEC>
-__device__ __forceinline__ void load8(Raw8<float>& o, const float* row, int64_t c, int64_t cols) {
-  o.v = o.w = make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void load16(Raw16<float>& o, const float* row, int c, int cols) {
   if (VEC) {
     if (c < cols) {
-      o.v = ld_once(row + c);
-      o.w = ld_once(row + c + 4);
+      ld_sector(o.w, row + c);
+      ld_sector(o.w + 8, row + c + 8);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o.w[i] = 0;
     }
   } else {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(row);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (c + i < cols) (&o.v.x)[i] = p[c + i];
-      if (c + 4 + i < cols) (&o.w.x)[i] = p[c + 4 + i];
+    for (int i = 0; i < 16; ++i) o.w[i] = c + i < cols ? p[c + i] : 0;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store16(__nv_bfloat16* row, int c, int cols, const Raw16<__nv_bfloat16>& o) {
+  if (VEC) {
+    if (c < cols) st_sector(row + c, o.w);
+  } else {
+    uint16_t* p = reinterpret_cast<uint16_t*>(row);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (c + i < cols) p[c + i] = (uint16_t)(o.w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store16(float* row, int c, int cols, const Raw16<float>& o) {
+  if (VEC) {
+    if (c < cols) {
+      st_sector(row + c, o.w);
+      st_sector(row + c + 8, o.w + 8);
     }
+  } else {
+    uint32_t* p = reinterpret_cast<uint32_t*>(row);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (c + i < cols) p[c + i] = o.w[i];
   }
 }
-__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& o, float (&f)[8]) {
-  const uint32_t* w = &o.v.x;
+__device__ __forceinline__ F16 unpack(const Raw16<__nv_bfloat16>& o) {
+  F16 f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 8; ++i) f.p[i] = f2_of(__uint_as_float(o.w[i] << 16), __uint_as_float(o.w[i] & 0xFFFF0000u));
+  return f;
 }
-__device__ __forceinline__ void unpack8(const Raw8<float>& o, float (&f)[8]) {
+__device__ __forceinline__ F16 unpack(const Raw16<float>& o) {
+  F16 f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = __uint_as_float((&o.v.x)[i]);
-    f[4 + i] = __uint_as_float((&o.w.x)[i]);
-  }
+  for (int i = 0; i < 8; ++i) f.p[i] = f2_of(__uint_as_float(o.w[2 * i]), __uint_as_float(o.w[2 * i + 1]));
+  return f;
 }
 __device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ void pack8(Raw8<__nv_bfloat16>& o, const float (&f)[8]) {
-  o.v = make_uint4(bf16x2_bits(f[0], f[1]), bf16x2_bits(f[2], f[3]), bf16x2_bits(f[4], f[5]), bf16x2_bits(f[6], f[7]));
-}
-__device__ __forceinline__ void pack8(Raw8<float>& o, const float (&f)[8]) {
+__device__ __forceinline__ void pack(Raw16<__nv_bfloat16>& o, const F16& f) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    (&o.v.x)[i] = __float_as_uint(f[i]);
-    (&o.w.x)[i] = __float_as_uint(f[4 + i]);
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = f2_get(f.p[i]);
+    o.w[i] = bf16x2_bits(x.x, x.y);
   }
 }
-template <bool VEC>
-__device__ __forceinline__ void store8(__nv_bfloat16* row, int64_t c, int64_t cols, const Raw8<__nv_bfloat16>& o) {
-  if (VEC) {
-    if (c < cols) *reinterpret_cast<uint4*>(row + c) = o.v;
-  } else {
-    uint16_t* p = reinterpret_cast<uint16_t*>(row);
-    const uint32_t* w = &o.v.x;
+__device__ __forceinline__ void pack(Raw16<float>& o, const F16& f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < cols) p[c + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = f2_get(f.p[i]);
+    o.w[2 * i] = __float_as_uint(x.x);
+    o.w[2 * i + 1] = __float_as_uint(x.y);
   }
 }
-template <bool VEC>
-__device__ __forceinline__ void store8(float* row, int64_t c, int64_t cols, const Raw8<float>& o) {
-  if (VEC) {
-    if (c < cols) {
-      *reinterpret_cast<uint4*>(row + c) = o.v;
-      *reinterpret_cast<uint4*>(row + c + 4) = o.w;
-    }
-  } else {
-    uint32_t* p = reinterpret_cast<uint32_t*>(row);
+// 16 e4m3 bytes at columns c .. c + 15 of a row (16-byte aligned, c % 16 == 0).
+__device__ __forceinline__ void store_q16(uint8_t* row, int c, int cols, uint4 b) {
+  if (c + 16 <= cols) {
+    *reinterpret_cast<uint4*>(row + c) = b;
+  } else if (c < cols) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (c + i < cols) p[c + i] = (&o.v.x)[i];
-      if (c + 4 + i < cols) p[c + 4 + i] = (&o.w.x)[i];
-    }
+    for (int i = 0; i < 16; ++i)
+      if (c + i < cols) row[c + i] = (uint8_t)((&b.x)[i >> 2] >> (8 * (i & 3)));
   }
 }
-// 8 e4m3 bytes at columns c .. c + 7 of a row (16-byte aligned, c % 8 == 0).
-__device__ __forceinline__ void store_q8(uint8_t* row, int64_t c, int64_t cols, uint2 b) {
-  if (c + 8 <= cols) {
-    *reinterpret_cast<uint2*>(row + c) = b;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < cols) row[c + i] = (uint8_t)((i < 4 ? b.x : b.y) >> (8 * (i & 3)));
-  }
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
-
-// Exponent byte of the 128-column block that a half-warp holds (8 values a
-// lane); every lane of the half-warp gets it.  All 32 lanes call it.  Values
-// that are not finite turn into NaN.
-__device__ __forceinline__ unsigned q8_block_exponent(float (&f)[8]) {
-  unsigned m = 0;
+// Exponent byte of the 128-column block that 8 lanes hold (16 values a lane);
+// each of them gets it.  All 32 lanes call it.  Values that are not finite turn
+// into NaN.
+__device__ __forceinline__ unsigned q8_block_exponent(F16& f) {
+  float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(f[i]));
+  for (int i = 0; i < 8; ++i) {
+    const float2 x = f2_get(f.p[i]);
+    m = max_nan(m, max_nan(fabsf(x.x), fabsf(x.y)));
+  }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (__any_sync(0xffffffffu, m >= INF_BITS)) {
-    m = 0;
+  for (int o = 4; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  unsigned b = abs_bits(m);
+  if (__any_sync(0xffffffffu, b >= INF_BITS)) {
+    b = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      m = max(m, finite_bits(f[i]));
-      f[i] = finite_or_nan(f[i]);
+      const float2 x = f2_get(f.p[i]);
+      b = max(b, max(finite_bits(x.x), finite_bits(x.y)));
+      f.p[i] = f2_of(finite_or_nan(x.x), finite_or_nan(x.y));
     }
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 4; o > 0; o >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
   }
-  return q8_exponent(m);
+  return q8_exponent(b);
+}
+__device__ __forceinline__ uint4 q8_pack16(const F16& f, float inv) {
+  const f2 s = f2_of(inv, inv);
+  uint4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = f2_get(mul2(f.p[2 * i], s)), b = f2_get(mul2(f.p[2 * i + 1], s));
+    (&o.x)[i] = q8_pack4(a.x, a.y, b.x, b.y);
+  }
+  return o;
 }
 
 }  // namespace precond

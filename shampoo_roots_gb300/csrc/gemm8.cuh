@@ -125,11 +125,6 @@ __device__ __forceinline__ void g8_put(const Gemm8Args& g, int64_t o, float v) {
   else reinterpret_cast<float*>(g.c)[o] = v;
 }
 
-// 32 bytes, one sector.
-__device__ __forceinline__ void st_sector(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-               ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
-}
 // Columns n .. n + 31 of the warp's 32 MMA rows m0 .. (one a lane).  Where C's rows are whole sectors a lane
 // stores its row's (16 lanes of a bf16 C at 2 B a lane and row took 39 us for 2500 x 1300 x 256, against 17 us
 // through the scratch); otherwise the rows pass through the warp's scratch and leave 32 columns at a time.

@@ -37,10 +37,9 @@ bool matrix8(const void* q, int64_t ld, const uint8_t* s, int64_t rows, int64_t 
   if (rows == 0 || cols == 0) return true;
   return ld >= cols && ld % 16 == 0 && ld <= MAX_SIDE && q && s && aligned(q, 16) && aligned(s, 16);
 }
-// Rows that 16-byte loads can take whole.
+// Rows that 32-byte loads can take whole.
 bool vectors(const void* p, int64_t cols, int64_t ld, int dtype) {
-  const int64_t per = 16 / (int64_t)size_of(dtype);
-  return !p || (aligned(p, 16) && cols % 8 == 0 && ld % per == 0);
+  return !p || (aligned(p, 32) && cols % 16 == 0 && ld * (int64_t)size_of(dtype) % 32 == 0);
 }
 struct Range { const char* lo; const char* hi; };
 Range range(const void* p, int64_t rows, int64_t ld, int64_t cols, size_t size) {
@@ -113,12 +112,13 @@ cudaError_t launch(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cuda
 }
 
 // ------------------------------------------------------------------------- norm
-// Threads of a row and rows of a block.  A row is 8 columns a thread up to 512
-// threads, then 16 (and 32 forward); longer rows take the kernels that read a
-// row twice.  Blocks of short rows hold several, to have 256 threads.
+constexpr int NORM_NV = 2, GRAD_NV = 1;             // most vectors a thread
+// Threads of a row and rows of a block.  A row is 16 columns a thread up to 512
+// threads, then 32; longer rows take the kernels that read a row twice.  Blocks
+// of short rows hold several, to have 256 threads.
 struct RowShape { int threads, rows, nv; };
 RowShape row_shape(int64_t cols, int max_nv) {
-  const int64_t vec = (cols + 7) / 8;
+  const int64_t vec = (cols + 15) / 16;
   RowShape s = {0, 1, 0};
   for (int nv = 1; nv <= max_nv; nv *= 2)
     if (vec <= 512 * nv) {
@@ -126,17 +126,16 @@ RowShape row_shape(int64_t cols, int max_nv) {
       break;
     }
   if (!s.nv) {
-    s.threads = 1024;
+    s.threads = max_nv == NORM_NV ? 1024 : 512;
     return s;
   }
   s.threads = (int)std::max<int64_t>(32, ((vec + s.nv - 1) / s.nv + 31) / 32 * 32);
   s.rows = std::min(8, std::max(1, 256 / s.threads));
   return s;
 }
-constexpr int NORM_NV = 4, GRAD_NV = 2;
 
 int64_t row_blocks_of(const RowShape& s, int64_t rows, int sms) {
-  const int64_t resident = std::max(1, (s.nv ? 1024 : 2048) / (s.threads * s.rows));
+  const int64_t resident = std::max(1, 1024 / (s.threads * s.rows));
   return std::max<int64_t>(1, std::min((rows + s.rows - 1) / s.rows, resident * sms));
 }
 
@@ -146,7 +145,6 @@ cudaError_t launch_norm(const RmsNormArgs& a, const RowShape& s, unsigned grid, 
   switch (s.nv) {
     case 1: return launch(rms_norm_kernel<T, 1, VEC>, dim3(grid), block, 0, st, 1, a);
     case 2: return launch(rms_norm_kernel<T, 2, VEC>, dim3(grid), block, 0, st, 1, a);
-    case 4: return launch(rms_norm_kernel<T, 4, VEC>, dim3(grid), block, 0, st, 1, a);
     default: return launch(rms_norm_long_kernel<T, VEC>, dim3(grid), block, 0, st, 1, a);
   }
 }
@@ -155,7 +153,6 @@ cudaError_t launch_grad(const RmsGradArgs& a, const RowShape& s, unsigned grid, 
   const dim3 block(s.threads, s.rows);
   switch (s.nv) {
     case 1: return launch(rms_grad_kernel<T, 1, VEC>, dim3(grid), block, 0, st, 1, a);
-    case 2: return launch(rms_grad_kernel<T, 2, VEC>, dim3(grid), block, 0, st, 1, a);
     default: return launch(rms_grad_long_kernel<T, VEC>, dim3(grid), block, 0, st, 1, a);
   }
 }
@@ -247,7 +244,7 @@ int precond_rms_norm(precond_t ph, const void* x, const void* residual, const vo
   if (rows == 0 || cols == 0) return PRECOND_OK;
   int rc = prepare(h);
   if (rc) return rc;
-  RmsNormArgs a = {x, residual, weight, total, y, (uint8_t*)q, scale, rstd, rows, cols, ldx, ldr, ldt, ldy, ldq, eps,
+  RmsNormArgs a = {x, residual, weight, total, y, (uint8_t*)q, scale, rstd, ldx, ldr, ldt, ldy, ldq, (int)rows, (int)cols, eps,
                    weight_dtype == PRECOND_BF16};
   const RowShape s = row_shape(cols, NORM_NV);
   const unsigned grid = (unsigned)row_blocks_of(s, q ? q8_row_blocks(rows) * 128 : rows, h->num_sms);
@@ -305,7 +302,7 @@ int precond_rms_norm_grad(precond_t ph, const void* dy, const void* x, const voi
     OP_CK(cudaMemsetAsync(dw, 0, cols * 4, st));
     return PRECOND_OK;
   }
-  RmsGradArgs a = {dy, x, dresidual, weight, rstd, dx, (float*)workspace, rows, cols, lddy, ldx, lddr, lddx,
+  RmsGradArgs a = {dy, x, dresidual, weight, rstd, dx, (float*)workspace, lddy, ldx, lddr, lddx, (int)rows, (int)cols,
                    weight_dtype == PRECOND_BF16};
   const RowShape s = row_shape(cols, GRAD_NV);
   const unsigned grid = (unsigned)row_blocks_of(s, rows, std::min(h->num_sms, PLAN_SMS));
@@ -349,11 +346,11 @@ int precond_quantize8(precond_t ph, const void* x, int dtype, int64_t rows, int6
   int rc = prepare(h);
   if (rc) return rc;
   Quant8Args a = {x, ldx, x_scale, rows, cols, block == PRECOND_BLOCK_TILE, (uint8_t*)q, ldq, scale, (uint8_t*)qt, ldqt, scale_t};
-  const bool vec = dtype == PRECOND_E4M3 || vectors(x, cols, ldx, dtype);
-  auto k = dtype == PRECOND_E4M3 ? quantize8_kernel<QIN_E4M3, true>
-           : dtype == PRECOND_BF16 ? (vec ? quantize8_kernel<QIN_BF16, true> : quantize8_kernel<QIN_BF16, false>)
-                                   : (vec ? quantize8_kernel<QIN_F32, true> : quantize8_kernel<QIN_F32, false>);
-  OP_CK(launch(k, dim3((unsigned)tiles), dim3(256), 0, (cudaStream_t)stream, 1, a));
+  // 8 columns in one load: 16 bytes of bf16, 32 of fp32
+  const int64_t step = 8 * (int64_t)size_of(dtype);
+  const int vec = aligned(x, step) && cols % 8 == 0 && ldx * (int64_t)size_of(dtype) % step == 0;
+  auto k = dtype == PRECOND_E4M3 ? quantize8_kernel<QIN_E4M3> : dtype == PRECOND_BF16 ? quantize8_kernel<QIN_BF16> : quantize8_kernel<QIN_F32>;
+  OP_CK(launch(k, dim3((unsigned)tiles), dim3(256), 0, (cudaStream_t)stream, 1, a, vec));
   ++h->launches;
   return PRECOND_OK;
 }

@@ -10,6 +10,9 @@
 // and the transposed bytes of a column are 8 consecutive ones of the output.
 // They cross through 16 KB of shared memory, 8-byte pieces at position ty XOR tx
 // of their column (no bank conflicts either way), and leave as 128-byte rows.
+// The tile stays in registers as it is stored (32 registers of bf16) and is
+// unpacked where it is used, which leaves room for four blocks on an SM; bf16
+// maxima are taken on packed pairs of magnitude bits.
 #pragma once
 
 #include "form8.cuh"
@@ -27,40 +30,103 @@ struct Quant8Args {
   uint8_t* qt; int64_t ldqt; uint8_t* st;
 };
 
-// Columns c .. c + 7 of row `row` as fp32; zero outside the matrix.
-template <int IN, bool VEC>
-__device__ __forceinline__ void quant_load(const Quant8Args& a, int64_t row, int64_t c, float (&f)[8]) {
-  if (IN == QIN_F32) {
-    Raw8<float> o;
-    load8<VEC>(o, reinterpret_cast<const float*>(a.x) + row * a.ldx, c, a.cols);
-    unpack8(o, f);
-  } else if (IN == QIN_BF16) {
-    Raw8<__nv_bfloat16> o;
-    load8<VEC>(o, reinterpret_cast<const __nv_bfloat16*>(a.x) + row * a.ldx, c, a.cols);
-    unpack8(o, f);
-  } else {
-    const uint8_t* p = reinterpret_cast<const uint8_t*>(a.x) + row * a.ldx + c;   // 16-byte aligned rows, c % 8 == 0
-    uint2 b = make_uint2(0, 0);
-    if (c + 8 <= a.cols) {
-      b = *reinterpret_cast<const uint2*>(p);
+// A thread's 8 x 8 elements as stored; get() gives one as fp32.
+template <int IN> struct QuantTile;
+template <> struct QuantTile<QIN_F32> {
+  uint32_t w[8][8];
+  __device__ __forceinline__ float get(int i, int j) const { return __uint_as_float(w[i][j]); }
+  __device__ __forceinline__ void set_nan(int i, int j) { w[i][j] = 0x7FFFFFFFu; }
+  __device__ __forceinline__ void load(const Quant8Args& a, bool vec, int i, int64_t row, int64_t c) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(a.x) + row * a.ldx + c;
+    if (vec && c < a.cols) {
+      ld_sector(w[i], p);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < a.cols) (i < 4 ? b.x : b.y) |= (uint32_t)p[i] << (8 * (i & 3));
+      for (int j = 0; j < 8; ++j) w[i][j] = c + j < a.cols ? p[j] : 0;
     }
-    const float v = c < a.cols ? q8_value(a.x_scale[q8_scale_at(row, (int)(c >> 7), q8_row_blocks(a.rows))]) : 0.f;
+  }
+};
+template <> struct QuantTile<QIN_BF16> {
+  uint32_t w[8][4];
+  __device__ __forceinline__ float get(int i, int j) const {
+    return __uint_as_float(j & 1 ? w[i][j >> 1] & 0xFFFF0000u : w[i][j >> 1] << 16);
+  }
+  __device__ __forceinline__ void set_nan(int i, int j) { w[i][j >> 1] |= j & 1 ? 0x7FFF0000u : 0x7FFFu; }
+  __device__ __forceinline__ void load(const Quant8Args& a, bool vec, int i, int64_t row, int64_t c) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(a.x) + row * a.ldx + c;
+    if (vec && c < a.cols) {
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3]) : "l"(p) : "memory");
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = i < 2 ? b.x : b.y;
-      q8_unpack2((uint16_t)(w >> (16 * (i & 1))), f[2 * i], f[2 * i + 1]);
-      f[2 * i] *= v;
-      f[2 * i + 1] *= v;
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = c + 2 * j < a.cols ? p[2 * j] : 0, hi = c + 2 * j + 1 < a.cols ? p[2 * j + 1] : 0;
+        w[i][j] = lo | hi << 16;
+      }
+    }
+  }
+};
+template <> struct QuantTile<QIN_E4M3> {
+  uint32_t w[8][2];
+  float scale[8];                    // of the rows: a tile's columns are one block
+  __device__ __forceinline__ float get(int i, int j) const {
+    float lo, hi;
+    q8_unpack2((uint16_t)(w[i][j >> 2] >> (16 * ((j >> 1) & 1))), lo, hi);
+    return (j & 1 ? hi : lo) * scale[i];
+  }
+  __device__ __forceinline__ void set_nan(int i, int j) {}          // e4m3's only non-finite value is NaN already
+  __device__ __forceinline__ void load(const Quant8Args& a, bool, int i, int64_t row, int64_t c) {
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(a.x) + row * a.ldx + c;   // 16-byte aligned rows, c % 8 == 0
+    w[i][0] = w[i][1] = 0;
+    if (c + 8 <= a.cols) {
+      const uint2 b = *reinterpret_cast<const uint2*>(p);
+      w[i][0] = b.x;
+      w[i][1] = b.y;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j < a.cols) w[i][j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+    }
+    scale[i] = c < a.cols ? q8_value(a.x_scale[q8_scale_at(row, (int)(c >> 7), q8_row_blocks(a.rows))]) : 0.f;
+  }
+};
+
+// Magnitude bits (fp32) of the 8 rows' and 8 columns' largest values in the thread's tile.
+template <int IN>
+__device__ __forceinline__ void quant_maxima(const QuantTile<IN>& v, unsigned (&rm)[8], unsigned (&cm)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) cm[j] = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    rm[i] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const unsigned b = abs_bits(v.get(i, j));
+      rm[i] = max(rm[i], b);
+      cm[j] = max(cm[j], b);
     }
   }
 }
+template <>
+__device__ __forceinline__ void quant_maxima<QIN_BF16>(const QuantTile<QIN_BF16>& v, unsigned (&rm)[8], unsigned (&cm)[8]) {
+  uint32_t c[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t b = v.w[i][j] & 0x7FFF7FFFu;
+      r = __vmaxu2(r, b);
+      c[j] = __vmaxu2(c[j], b);
+    }
+    rm[i] = max(r << 16, r & 0xFFFF0000u);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) cm[j] = j & 1 ? c[j >> 1] & 0xFFFF0000u : c[j >> 1] << 16;
+}
 
-template <int IN, bool VEC>
-__global__ void __launch_bounds__(256) quantize8_kernel(Quant8Args a) {
+template <int IN>
+__global__ void __launch_bounds__(256, IN == QIN_F32 ? 2 : IN == QIN_BF16 ? 4 : 3) quantize8_kernel(Quant8Args a, int vec) {
   __shared__ __align__(16) uint8_t tr[128 * 128];
   __shared__ unsigned cmax[8][128];
   __shared__ unsigned char cexp[128];
@@ -70,41 +136,38 @@ __global__ void __launch_bounds__(256) quantize8_kernel(Quant8Args a) {
   const int64_t tj = blockIdx.x % col_tiles, ti = blockIdx.x / col_tiles;
   const int64_t r0 = ti * 128 + 8 * ty, c0 = tj * 128 + 8 * tx;
 
-  float v[8][8];
+  QuantTile<IN> v;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (r0 + i < a.rows) {
-      quant_load<IN, VEC>(a, r0 + i, c0, v[i]);
+      v.load(a, vec, i, r0 + i, c0);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+      for (auto& x : v.w[i]) x = 0;
+      if constexpr (IN == QIN_E4M3) v.scale[i] = 0.f;
     }
   }
-  unsigned any = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) any = max(any, abs_bits(v[i][j]));
-  if (any >= INF_BITS) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = finite_or_nan(v[i][j]);
-  }
-  // row maxima (a half-warp holds a row) and column maxima (over the block); a NaN counts as nothing
+  // row maxima (a half-warp holds a row) and column maxima (over the block)
   unsigned rexp[8], cm[8];
+  quant_maxima<IN>(v, rexp, cm);
+  unsigned most = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) cm[j] = 0;
+  for (int i = 0; i < 8; ++i) most = max(most, rexp[i]);
+  if (__syncthreads_or(most >= INF_BITS)) {
+    // somewhere in the tile a value is not finite: it becomes NaN and counts for no maximum
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    unsigned m = 0;
+    for (int j = 0; j < 8; ++j) cm[j] = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const unsigned b = any >= INF_BITS ? finite_bits(v[i][j]) : abs_bits(v[i][j]);
-      m = max(m, b);
-      cm[j] = max(cm[j], b);
+    for (int i = 0; i < 8; ++i) {
+      rexp[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const unsigned b = finite_bits(v.get(i, j));
+        if (abs_bits(v.get(i, j)) >= INF_BITS) v.set_nan(i, j);
+        rexp[i] = max(rexp[i], b);
+        cm[j] = max(cm[j], b);
+      }
     }
-    rexp[i] = m;
   }
   if (a.tile || a.qt) {
 #pragma unroll
@@ -142,10 +205,18 @@ __global__ void __launch_bounds__(256) quantize8_kernel(Quant8Args a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float inv = q8_inverse(rexp[i]);
-      if (r0 + i < a.rows)
-        store_q8(a.q + (r0 + i) * a.ldq, c0, a.cols,
-                 make_uint2(q8_pack4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv),
-                            q8_pack4(v[i][4] * inv, v[i][5] * inv, v[i][6] * inv, v[i][7] * inv)));
+      const uint2 b = make_uint2(q8_pack4(v.get(i, 0) * inv, v.get(i, 1) * inv, v.get(i, 2) * inv, v.get(i, 3) * inv),
+                                 q8_pack4(v.get(i, 4) * inv, v.get(i, 5) * inv, v.get(i, 6) * inv, v.get(i, 7) * inv));
+      if (r0 + i < a.rows) {
+        uint8_t* p = a.q + (r0 + i) * a.ldq + c0;
+        if (c0 + 8 <= a.cols) {
+          *reinterpret_cast<uint2*>(p) = b;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (c0 + j < a.cols) p[j] = (uint8_t)((j < 4 ? b.x : b.y) >> (8 * (j & 3)));
+        }
+      }
       if (tx == 0) a.s[q8_scale_at(r0 + i, (int)tj, row_tiles)] = (uint8_t)(r0 + i < a.rows ? rexp[i] : Q8_ONE);
     }
     // the blocks of the last group past the end
@@ -159,8 +230,8 @@ __global__ void __launch_bounds__(256) quantize8_kernel(Quant8Args a) {
       const unsigned b = a.tile ? rexp[0] : cexp[8 * tx + j];
       const float inv = q8_inverse(b);
       *reinterpret_cast<uint2*>(tr + (8 * tx + j) * 128 + ((ty ^ tx) << 3)) =
-          make_uint2(q8_pack4(v[0][j] * inv, v[1][j] * inv, v[2][j] * inv, v[3][j] * inv),
-                     q8_pack4(v[4][j] * inv, v[5][j] * inv, v[6][j] * inv, v[7][j] * inv));
+          make_uint2(q8_pack4(v.get(0, j) * inv, v.get(1, j) * inv, v.get(2, j) * inv, v.get(3, j) * inv),
+                     q8_pack4(v.get(4, j) * inv, v.get(5, j) * inv, v.get(6, j) * inv, v.get(7, j) * inv));
       if (ty == 0) a.st[q8_scale_at(c0 + j, (int)ti, col_tiles)] = (uint8_t)(c0 + j < a.cols ? b : Q8_ONE);
     }
     if (ti == row_tiles - 1 && threadIdx.x < 128)

@@ -7,10 +7,10 @@
 //
 // Both are bound by memory: 7 B an element forward (bf16 x, r, h and e4m3 q),
 // 8 B backward (dy, h, dr, dx).  A row stays in the registers of `blockDim.x`
-// threads, 8 consecutive columns a vector, so that a 128-column scale block is
-// a half-warp and the row is read once; the block keeps its columns of w (and
-// of the dw sum) for all of its rows, and loads the next row before it works
-// on the present one.  Rows are joined by one barrier of the row's threads.
+// threads, 16 consecutive columns a vector, so that the row is read once; the
+// block keeps its columns of w (and of the dw sum) for all of its rows, and
+// loads the next row before it works on the present one.  The threads of a row
+// meet at one barrier a row.
 #pragma once
 
 #include "form8.cuh"
@@ -20,7 +20,8 @@ namespace precond {
 struct RmsNormArgs {
   const void* x; const void* r; const void* w; void* h; void* y;
   uint8_t* q; uint8_t* scale; float* rstd;
-  int64_t rows, cols, ldx, ldr, ldh, ldy, ldq;
+  int64_t ldx, ldr, ldh, ldy, ldq;
+  int rows, cols;
   float eps;
   int w_bf16;
 };
@@ -28,17 +29,30 @@ struct RmsNormArgs {
 struct RmsGradArgs {
   const void* dy; const void* x; const void* dr; const void* w; const float* rstd;
   void* dx; float* partial;           // partial: [gridDim.x * blockDim.y][cols]
-  int64_t rows, cols, lddy, ldx, lddr, lddx;
+  int64_t lddy, ldx, lddr, lddx;
+  int rows, cols;
   int w_bf16;
 };
 
-__device__ __forceinline__ float load_w(const void* w, int bf16, int64_t c) {
+__device__ __forceinline__ float load_w(const void* w, int bf16, int c) {
   return bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(w)[c]) : reinterpret_cast<const float*>(w)[c];
+}
+__device__ __forceinline__ F16 load_w16(const void* w, int bf16, int c, int cols) {
+  F16 f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    f.p[i] = f2_of(c + 2 * i < cols ? load_w(w, bf16, c + 2 * i) : 0.f, c + 2 * i + 1 < cols ? load_w(w, bf16, c + 2 * i + 1) : 0.f);
+  return f;
+}
+__device__ __forceinline__ f2 squares(const F16& v, f2 s) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = fma2(v.p[i], v.p[i], s);
+  return s;
 }
 
 // Sum over the blockDim.x threads of one row (blockDim.x a multiple of 32), the
-// same value in each.  `red` has room for 2 x blockDim.y x 32; calls alternate
-// between its halves, so that one barrier a call is enough.
+// same value in each.  `red` has room for 2 x blockDim.y x 32, zeroed; calls
+// alternate between its halves, so that one barrier a call is enough.
 __device__ __forceinline__ float row_sum(float v, float* red, int half) {
   v = warp_sum(v);
   const int nw = blockDim.x >> 5;
@@ -46,279 +60,306 @@ __device__ __forceinline__ float row_sum(float v, float* red, int half) {
   float* mine = red + (half * blockDim.y + threadIdx.y) * 32;
   if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = v;
   asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.y), "r"((int)blockDim.x) : "memory");
-  float s = 0.f;
-  for (int i = 0; i < nw; ++i) s += mine[i];
-  return s;
+  float4 s = *reinterpret_cast<const float4*>(mine);
+  for (int i = 4; i < nw; i += 4) {
+    const float4 t = *reinterpret_cast<const float4*>(mine + i);
+    s = make_float4(s.x + t.x, s.y + t.y, s.z + t.z, s.w + t.w);
+  }
+  return (s.x + s.y) + (s.z + s.w);
+}
+__device__ __forceinline__ void zero_red(float* red, int n) {
+  for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < n; i += blockDim.x * blockDim.y) red[i] = 0.f;
+  __syncthreads();
 }
 
-// One vector's 8-bit form, scale byte and plain output.
+// h = x + r, rounded to the stream's type.  The bf16 addition rounds the exact
+// sum once; the fp32 sum rounded to bf16 is the same (where fp32 drops bits of
+// the sum, the smaller term lies below 2^-16 of the larger and cannot reach a tie).
+__device__ __forceinline__ void add_stream(Raw16<__nv_bfloat16>& x, const Raw16<__nv_bfloat16>& r) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(x.w[i]) : "r"(r.w[i]));
+}
+__device__ __forceinline__ void add_stream(Raw16<float>& x, const Raw16<float>& r) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x.w[i] = __float_as_uint(__uint_as_float(x.w[i]) + __uint_as_float(r.w[i]));
+}
+
+// One vector's outputs; `at` is its scale byte's place.
 template <typename T, bool VEC>
-__device__ __forceinline__ void norm_write(const RmsNormArgs& a, int64_t row, int64_t c, float (&y)[8], int64_t rblocks) {
+__device__ __forceinline__ void norm_write(const RmsNormArgs& a, int64_t row, int c, F16& y, size_t at) {
   if (a.y) {
-    Raw8<T> o;
-    pack8(o, y);
-    store8<VEC>(reinterpret_cast<T*>(a.y) + row * a.ldy, c, a.cols, o);
+    Raw16<T> o;
+    pack(o, y);
+    store16<VEC>(reinterpret_cast<T*>(a.y) + row * a.ldy, c, a.cols, o);
   }
   if (a.q) {
     const unsigned b = q8_block_exponent(y);
-    const float inv = q8_inverse(b);
-    store_q8(a.q + row * a.ldq, c, a.cols,
-             make_uint2(q8_pack4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                        q8_pack4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv)));
-    if ((threadIdx.x & 15) == 0 && c < a.cols) a.scale[q8_scale_at(row, (int)(c >> 7), rblocks)] = (uint8_t)b;
+    store_q16(a.q + row * a.ldq, c, a.cols, q8_pack16(y, q8_inverse(b)));
+    if ((threadIdx.x & 7) == 0 && c < a.cols) a.scale[at] = (uint8_t)b;
   }
 }
-
 // The scale bytes past the matrix's end: a row's trailing blocks, or a whole row of padding.
 __device__ __forceinline__ void norm_pad(const RmsNormArgs& a, int64_t row, int64_t rblocks) {
-  const int nkb = row < a.rows ? (int)((a.cols + 127) >> 7) : 0;
+  const int nkb = row < a.rows ? (a.cols + 127) >> 7 : 0;
   for (int kb = nkb + threadIdx.x; kb < 4 * q8_groups(a.cols); kb += blockDim.x)
     a.scale[q8_scale_at(row, kb, rblocks)] = (uint8_t)Q8_ONE;
 }
 
-// NV vectors of 8 columns a thread.
+// NV vectors of 16 columns a thread.
 template <typename T, int NV, bool VEC>
-__global__ void __launch_bounds__(512) rms_norm_kernel(RmsNormArgs a) {
-  __shared__ float red[2 * 8 * 32];
-  const T* x = reinterpret_cast<const T*>(a.x);
-  const T* r = reinterpret_cast<const T*>(a.r);
-  T* h = reinterpret_cast<T*>(a.h);
+__global__ void __launch_bounds__(512, NV == 1 && sizeof(T) == 2 ? 2 : 1) rms_norm_kernel(RmsNormArgs a) {
+  __shared__ __align__(16) float red[2 * 8 * 32];
+  zero_red(red, 2 * 8 * 32);
   const int64_t rblocks = q8_row_blocks(a.rows);
-  const int64_t last = a.q ? rblocks * 128 : a.rows;
-  const int64_t step = (int64_t)gridDim.x * blockDim.y;
-  int64_t c[NV];
-  float w[NV][8];
+  const int step = gridDim.x * blockDim.y;
+  int row = blockIdx.x * blockDim.y + threadIdx.y;
+  const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
+  const T* r = reinterpret_cast<const T*>(a.r) + row * a.ldr;
+  F16 w[NV];
+  int c[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    c[j] = ((int64_t)j * blockDim.x + threadIdx.x) * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[j][i] = c[j] + i < a.cols ? load_w(a.w, a.w_bf16, c[j] + i) : 0.f;
+    c[j] = (j * blockDim.x + threadIdx.x) * 16;
+    w[j] = load_w16(a.w, a.w_bf16, c[j], a.cols);
   }
-  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  Raw8<T> nx[NV], nr[NV];
+  Raw16<T> nx[NV], nr[NV];
   if (row < a.rows) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      load8<VEC>(nx[j], x + row * a.ldx, c[j], a.cols);
-      if (r) load8<VEC>(nr[j], r + row * a.ldr, c[j], a.cols);
+      load16<VEC>(nx[j], x, c[j], a.cols);
+      if (a.r) load16<VEC>(nr[j], r, c[j], a.cols);
     }
   }
-  for (int half = 0; row < last; row += step, half ^= 1) {
-    if (a.q) norm_pad(a, row, rblocks);
-    if (row >= a.rows) continue;
-    float v[NV][8];
-    float ss = 0.f;
+  for (int half = 0; row < a.rows; row += step, half ^= 1) {
+    F16 v[NV];
+    f2 ss = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      unpack8(nx[j], v[j]);
-      if (r) {
-        float f[8];
-        unpack8(nr[j], f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] += f[i];
-        Raw8<T> o;
-        pack8(o, v[j]);
-        store8<VEC>(h + row * a.ldh, c[j], a.cols, o);
-        unpack8(o, v[j]);                 // the norm is that of the stream as it is kept
+      if (a.r) {
+        add_stream(nx[j], nr[j]);
+        store16<VEC>(reinterpret_cast<T*>(a.h) + row * a.ldh, c[j], a.cols, nx[j]);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
+      v[j] = unpack(nx[j]);
+      ss = squares(v[j], ss);
     }
-    const int64_t next = row + step;
-    if (next < a.rows) {
+    x += step * a.ldx;
+    r += step * a.ldr;
+    if (row + step < a.rows) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        load8<VEC>(nx[j], x + next * a.ldx, c[j], a.cols);
-        if (r) load8<VEC>(nr[j], r + next * a.ldr, c[j], a.cols);
+        load16<VEC>(nx[j], x, c[j], a.cols);
+        if (a.r) load16<VEC>(nr[j], r, c[j], a.cols);
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum(ss, red, half) / (float)a.cols + a.eps);
+    const float rstd = 1.0f / sqrtf(row_sum(sum2(ss), red, half) / (float)a.cols + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
-    if (a.q || a.y) {
+    if (!a.q && !a.y) continue;
+    const f2 rs = f2_of(rstd, rstd);
+    const size_t at_row = q8_scale_at(row, 0, rblocks);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
+    for (int j = 0; j < NV; ++j) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = (v[j][i] * rstd) * w[j][i];
-        norm_write<T, VEC>(a, row, c[j], v[j], rblocks);
-      }
+      for (int i = 0; i < 8; ++i) v[j].p[i] = mul2(mul2(v[j].p[i], rs), w[j].p[i]);
+      const int kb = c[j] >> 7;
+      norm_write<T, VEC>(a, row, c[j], v[j], (size_t)(kb >> 2) * rblocks * 512 + (kb & 3) + at_row);
     }
+    if (a.q && (a.cols & 511)) norm_pad(a, row, rblocks);
   }
+  if (a.q)
+    for (; row < rblocks * 128; row += step) norm_pad(a, row, rblocks);
 }
 
 // Rows too long for registers: one block a row, which is read again (from L2) after its norm is known.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(1024) rms_norm_long_kernel(RmsNormArgs a) {
-  __shared__ float red[2 * 32];
+__global__ void __launch_bounds__(1024, 1) rms_norm_long_kernel(RmsNormArgs a) {
+  __shared__ __align__(16) float red[2 * 32];
+  zero_red(red, 2 * 32);
   const int64_t rblocks = q8_row_blocks(a.rows);
   const int64_t last = a.q ? rblocks * 128 : a.rows;
-  const int64_t span = (a.cols + 8 * 1024 - 1) / (8 * 1024) * (8 * 1024);   // every lane takes part in the block maxima
-  for (int64_t row = blockIdx.x, half = 0; row < last; row += gridDim.x, half ^= 1) {
+  const int64_t span = ((int64_t)a.cols + 16 * 1024 - 1) / (16 * 1024) * (16 * 1024);   // every lane takes part in the block maxima
+  int half = 0;
+  for (int64_t row = blockIdx.x; row < last; row += gridDim.x, half ^= 1) {
     if (a.q) norm_pad(a, row, rblocks);
     if (row >= a.rows) continue;
     const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
     const T* r = reinterpret_cast<const T*>(a.r) + row * a.ldr;
     T* h = reinterpret_cast<T*>(a.h) + row * a.ldh;
-    float ss = 0.f;
-    for (int64_t c = (int64_t)threadIdx.x * 8; c < span; c += 8 * 1024) {
-      Raw8<T> o;
-      float v[8];
-      load8<VEC>(o, x, c, a.cols);
-      unpack8(o, v);
+    f2 ss = 0;
+    for (int64_t c = threadIdx.x * 16; c < span; c += 16 * 1024) {
+      Raw16<T> o, p;
+      load16<VEC>(o, x, (int)c, a.cols);
       if (a.r) {
-        float f[8];
-        load8<VEC>(o, r, c, a.cols);
-        unpack8(o, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += f[i];
-        pack8(o, v);
-        store8<VEC>(h, c, a.cols, o);
-        unpack8(o, v);
+        load16<VEC>(p, r, (int)c, a.cols);
+        add_stream(o, p);
+        store16<VEC>(h, (int)c, a.cols, o);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+      ss = squares(unpack(o), ss);
     }
-    const float rstd = 1.0f / sqrtf(row_sum(ss, red, (int)half) / (float)a.cols + a.eps);
+    const float rstd = 1.0f / sqrtf(row_sum(sum2(ss), red, half) / (float)a.cols + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     if (!a.q && !a.y) continue;
-    for (int64_t c = (int64_t)threadIdx.x * 8; c < span; c += 8 * 1024) {
-      Raw8<T> o;
-      float v[8];
-      load8<VEC>(o, a.r ? h : x, c, a.cols);       // h: this thread's own stores
-      unpack8(o, v);
+    const f2 rs = f2_of(rstd, rstd);
+    for (int64_t c = threadIdx.x * 16; c < span; c += 16 * 1024) {
+      Raw16<T> o;
+      load16<VEC>(o, a.r ? h : x, (int)c, a.cols);       // h: this thread's own stores
+      F16 v = unpack(o);
+      const F16 w = load_w16(a.w, a.w_bf16, (int)c, a.cols);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = c + i < a.cols ? (v[i] * rstd) * load_w(a.w, a.w_bf16, c + i) : 0.f;
-      norm_write<T, VEC>(a, row, c, v, rblocks);
+      for (int i = 0; i < 8; ++i) v.p[i] = mul2(mul2(v.p[i], rs), w.p[i]);
+      const int kb = (int)(c >> 7);
+      norm_write<T, VEC>(a, row, (int)c, v, q8_scale_at(row, kb, rblocks));
     }
   }
 }
 
 // ------------------------------------------------------------- gradients
+// One vector: g = dy w, n = x rstd; adds to dw and to the row's g n.
+__device__ __forceinline__ f2 grad_terms(F16& g, F16& n, const F16& w, F16& dw, f2 rs, f2 dot) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    n.p[i] = mul2(n.p[i], rs);
+    dw.p[i] = fma2(g.p[i], n.p[i], dw.p[i]);
+    g.p[i] = mul2(g.p[i], w.p[i]);
+    dot = fma2(g.p[i], n.p[i], dot);
+  }
+  return dot;
+}
+// dx = rstd (g - n mean) (+ dr)
+template <typename T>
+__device__ __forceinline__ void grad_out(Raw16<T>& o, const F16& g, const F16& n, f2 rs, f2 minus_mean, const Raw16<T>* dr) {
+  F16 d;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) d.p[i] = mul2(rs, fma2(n.p[i], minus_mean, g.p[i]));
+  if (dr) {
+    const F16 f = unpack(*dr);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d.p[i] = add2(d.p[i], f.p[i]);
+  }
+  pack(o, d);
+}
+
 template <typename T, int NV, bool VEC>
-__global__ void __launch_bounds__(512) rms_grad_kernel(RmsGradArgs a) {
-  __shared__ float red[2 * 8 * 32];
-  const T* dy = reinterpret_cast<const T*>(a.dy);
-  const T* x = reinterpret_cast<const T*>(a.x);
-  const T* dr = reinterpret_cast<const T*>(a.dr);
-  T* dx = reinterpret_cast<T*>(a.dx);
-  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+__global__ void __launch_bounds__(512, 1) rms_grad_kernel(RmsGradArgs a) {
+  __shared__ __align__(16) float red[2 * 8 * 32];
+  zero_red(red, 2 * 8 * 32);
+  const int step = gridDim.x * blockDim.y;
+  int row = blockIdx.x * blockDim.y + threadIdx.y;
+  const T* dy = reinterpret_cast<const T*>(a.dy) + row * a.lddy;
+  const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
+  const T* dr = reinterpret_cast<const T*>(a.dr) + row * a.lddr;
+  T* dx = reinterpret_cast<T*>(a.dx) + row * a.lddx;
   const float inv_cols = 1.0f / (float)a.cols;
-  int64_t c[NV];
-  float w[NV][8], dw[NV][8];
+  int c[NV];
+  F16 w[NV], dw[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    c[j] = ((int64_t)j * blockDim.x + threadIdx.x) * 8;
+    c[j] = (j * blockDim.x + threadIdx.x) * 16;
+    w[j] = load_w16(a.w, a.w_bf16, c[j], a.cols);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[j][i] = c[j] + i < a.cols ? load_w(a.w, a.w_bf16, c[j] + i) : 0.f;
-      dw[j][i] = 0.f;
-    }
+    for (int i = 0; i < 8; ++i) dw[j].p[i] = 0;
   }
-  int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  Raw8<T> ny[NV], nx[NV], nr[NV];
+  Raw16<T> ny[NV], nx[NV], nr[NV];
   float nrstd = 0.f;
-  auto fetch = [&](int64_t k) {
+  auto fetch = [&](int k) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      load8<VEC>(ny[j], dy + k * a.lddy, c[j], a.cols);
-      load8<VEC>(nx[j], x + k * a.ldx, c[j], a.cols);
-      if (dr) load8<VEC>(nr[j], dr + k * a.lddr, c[j], a.cols);
+      load16<VEC>(ny[j], dy, c[j], a.cols);
+      load16<VEC>(nx[j], x, c[j], a.cols);
+      if (a.dr) load16<VEC>(nr[j], dr, c[j], a.cols);
     }
     nrstd = a.rstd[k];
+    dy += step * a.lddy;
+    x += step * a.ldx;
+    dr += step * a.lddr;
   };
   if (row < a.rows) fetch(row);
   for (int half = 0; row < a.rows; row += step, half ^= 1) {
-    const float rstd = nrstd;
-    float g[NV][8], n[NV][8];
-    Raw8<T> res[NV];
-    float dot = 0.f;
+    const f2 rs = f2_of(nrstd, nrstd);
+    F16 g[NV], n[NV];
+    Raw16<T> res[NV];
+    f2 dot = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      unpack8(ny[j], g[j]);
-      unpack8(nx[j], n[j]);
-      if (dr) res[j] = nr[j];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        n[j][i] *= rstd;
-        dw[j][i] = fmaf(g[j][i], n[j][i], dw[j][i]);
-        g[j][i] *= w[j][i];
-        dot = fmaf(g[j][i], n[j][i], dot);
-      }
+      g[j] = unpack(ny[j]);
+      n[j] = unpack(nx[j]);
+      if (a.dr) res[j] = nr[j];
+      dot = grad_terms(g[j], n[j], w[j], dw[j], rs, dot);
     }
     if (row + step < a.rows) fetch(row + step);
-    const float mean = row_sum(dot, red, half) * inv_cols;
+    const float mean = -row_sum(sum2(dot), red, half) * inv_cols;
+    const f2 mm = f2_of(mean, mean);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      float f[8];
-      if (dr) unpack8(res[j], f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float d = rstd * (g[j][i] - n[j][i] * mean);
-        g[j][i] = dr ? d + f[i] : d;
-      }
-      Raw8<T> o;
-      pack8(o, g[j]);
-      store8<VEC>(dx + row * a.lddx, c[j], a.cols, o);
+      Raw16<T> o;
+      grad_out(o, g[j], n[j], rs, mm, a.dr ? &res[j] : nullptr);
+      store16<VEC>(dx, c[j], a.cols, o);
     }
+    dx += step * a.lddx;
   }
   float* out = a.partial + ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * a.cols;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c[j] + i < a.cols) out[c[j] + i] = dw[j][i];
+    for (int i = 0; i < 8; ++i) {
+      const float2 d = f2_get(dw[j].p[i]);
+      if (c[j] + 2 * i < a.cols) out[c[j] + 2 * i] = d.x;
+      if (c[j] + 2 * i + 1 < a.cols) out[c[j] + 2 * i + 1] = d.y;
+    }
 }
 
 // Rows too long for registers: the block's dw sums live in its row of `partial`
 // (each thread adds to its own columns).
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(1024) rms_grad_long_kernel(RmsGradArgs a) {
-  __shared__ float red[2 * 32];
+__global__ void __launch_bounds__(512, 1) rms_grad_long_kernel(RmsGradArgs a) {
+  __shared__ __align__(16) float red[2 * 32];
+  zero_red(red, 2 * 32);
   float* out = a.partial + (int64_t)blockIdx.x * a.cols;
   const float inv_cols = 1.0f / (float)a.cols;
+  const int stride = 16 * blockDim.x;
   bool first = true;
-  for (int64_t row = blockIdx.x, half = 0; row < a.rows; row += gridDim.x, half ^= 1) {
+  int half = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, half ^= 1) {
     const T* dy = reinterpret_cast<const T*>(a.dy) + row * a.lddy;
     const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
     const T* dr = reinterpret_cast<const T*>(a.dr) + row * a.lddr;
     T* dx = reinterpret_cast<T*>(a.dx) + row * a.lddx;
-    const float rstd = a.rstd[row];
-    float dot = 0.f;
-    for (int64_t c = (int64_t)threadIdx.x * 8; c < a.cols; c += 8 * 1024) {
-      Raw8<T> o;
-      float g[8], n[8];
-      load8<VEC>(o, dy, c, a.cols);
-      unpack8(o, g);
-      load8<VEC>(o, x, c, a.cols);
-      unpack8(o, n);
+    const f2 rs = f2_of(a.rstd[row], a.rstd[row]);
+    f2 dot = 0;
+    for (int64_t c = threadIdx.x * 16; c < a.cols; c += stride) {
+      Raw16<T> o;
+      load16<VEC>(o, dy, (int)c, a.cols);
+      F16 g = unpack(o);
+      load16<VEC>(o, x, (int)c, a.cols);
+      F16 n = unpack(o), dw;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (c + i < a.cols) {
-          n[i] *= rstd;
-          out[c + i] = first ? g[i] * n[i] : fmaf(g[i], n[i], out[c + i]);
-          dot = fmaf(g[i] * load_w(a.w, a.w_bf16, c + i), n[i], dot);
-        }
-    }
-    first = false;
-    const float mean = row_sum(dot, red, (int)half) * inv_cols;
-    for (int64_t c = (int64_t)threadIdx.x * 8; c < a.cols; c += 8 * 1024) {
-      Raw8<T> o;
-      float g[8], n[8], f[8];
-      load8<VEC>(o, dy, c, a.cols);
-      unpack8(o, g);
-      load8<VEC>(o, x, c, a.cols);
-      unpack8(o, n);
-      if (a.dr) {
-        load8<VEC>(o, dr, c, a.cols);
-        unpack8(o, f);
-      }
+        dw.p[i] = f2_of(first || c + 2 * i >= a.cols ? 0.f : out[c + 2 * i], first || c + 2 * i + 1 >= a.cols ? 0.f : out[c + 2 * i + 1]);
+      dot = grad_terms(g, n, load_w16(a.w, a.w_bf16, (int)c, a.cols), dw, rs, dot);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float w = c + i < a.cols ? load_w(a.w, a.w_bf16, c + i) : 0.f;
-        const float d = rstd * (g[i] * w - (n[i] * rstd) * mean);
-        g[i] = a.dr ? d + f[i] : d;
+        const float2 d = f2_get(dw.p[i]);
+        if (c + 2 * i < a.cols) out[c + 2 * i] = d.x;
+        if (c + 2 * i + 1 < a.cols) out[c + 2 * i + 1] = d.y;
       }
-      pack8(o, g);
-      store8<VEC>(dx, c, a.cols, o);
+    }
+    first = false;
+    const float mean = -row_sum(sum2(dot), red, half) * inv_cols;
+    const f2 mm = f2_of(mean, mean);
+    for (int64_t c = threadIdx.x * 16; c < a.cols; c += stride) {
+      Raw16<T> o, res;
+      load16<VEC>(o, dy, (int)c, a.cols);
+      F16 g = unpack(o);
+      load16<VEC>(o, x, (int)c, a.cols);
+      F16 n = unpack(o);
+      const F16 w = load_w16(a.w, a.w_bf16, (int)c, a.cols);
+      if (a.dr) load16<VEC>(res, dr, (int)c, a.cols);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        n.p[i] = mul2(n.p[i], rs);
+        g.p[i] = mul2(g.p[i], w.p[i]);
+      }
+      grad_out(o, g, n, rs, mm, a.dr ? &res : nullptr);
+      store16<VEC>(dx, (int)c, a.cols, o);
     }
   }
 }
@@ -329,8 +370,10 @@ __global__ void __launch_bounds__(1024) rms_dw_kernel(const float* partial, int 
   __shared__ float s[32][33];
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
-  if (c < cols)
+  if (c < cols) {
+#pragma unroll 4
     for (int p = threadIdx.y; p < parts; p += 32) v += partial[(int64_t)p * cols + c];
+  }
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   v = warp_sum(s[threadIdx.x][threadIdx.y]);
