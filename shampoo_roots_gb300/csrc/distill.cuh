@@ -4,14 +4,26 @@
 //   loss = weight tau^2 sum_j p_j (log p_j - log q_{id_j}),   dz_v = weight tau (q_v - sum_{j: id_j = v} p_j)
 //
 // (tau^2 keeps the gradient's size when tau changes.)  Bound by memory: the
-// logits are read once for the running maximum and sum, and the gradient is
-// written once.  A row belongs to a cluster of 1 to 8 blocks (more where there
-// are few rows), which join their (maximum, sum) through distributed shared
-// memory in the blocks' order; the gradient's pass reads the row's slice again,
-// from L2, where it still is (a row is at most some hundred KB, and the rows in
-// flight stay below the 129 MB).  The candidates' logits are read before
-// anything is written, so that dz may be z itself, and their gradients are
-// written last, the candidates of one id added in their order.
+// logits are read once and the gradient is written once.  A row belongs to a
+// cluster of 1 to 8 blocks, whose threads keep its logits in registers as they
+// are stored (up to 64 KB a block): a thread takes the maximum and the sum of its
+// own part, the blocks join theirs through distributed shared memory in their
+// order, and the gradient is formed from the registers.  (Reading the row again
+// from L2 cost DRAM 3.6 GB for 1.9 GB of logits at 8192 x 131072: the rows in
+// flight do not fit beside the gradients.  967 us.)  Rows beyond 8 blocks'
+// registers take the kernel that reads them twice.
+//
+// With c = log2(e) / tau and m = max(z), q_v = 2^(z_v c - k) / S, S = sum 2^(z_v
+// c - k), k = m c: the exponent is one fma, and the rounding of k cancels.  Where
+// m c is so large that its rounding would move the exponent (beyond 10^6: a row
+// that is masked with the type's lowest value throughout) it is (z_v - m) c
+// instead; both are (z_v - b) c - k.
+//
+// The candidates are the work of a warp of their own, beside those that stream
+// the logits (one of these doing both held the others up: 1200 us, 830 without
+// candidates).  Their logits are read before anything is written, so that dz may
+// be z itself, and their gradients are written last, those of one id added in
+// the candidates' order.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -20,7 +32,7 @@
 
 namespace precond {
 
-constexpr int DISTILL_THREADS = 512;
+constexpr int DISTILL_THREADS = 512;                 // most that stream a block's part; 32 more for the candidates
 constexpr int DISTILL_MAX_TOP = 1024;
 
 struct DistillArgs {
@@ -35,18 +47,34 @@ struct DistillArgs {
   float tau;
 };
 
+// 2^x; and with results below 2^-126 flushed to 0, one instruction instead of four.
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-constexpr float LOG2E = 1.4426950408889634f;
+__device__ __forceinline__ float ex2_flush(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
-// Running (maximum, sum of exp((z - max) / tau)): joins (m2, s2) to (m, s).
+struct Shift {
+  float b, k;
+  __device__ __forceinline__ Shift(float m, float c) {
+    const bool far = !(fabsf(m) * c <= 1e6f);
+    b = far ? m : 0.f;
+    k = far ? 0.f : m * c;
+  }
+  __device__ __forceinline__ float operator()(float z, float c) const { return fmaf(z - b, c, -k); }
+};
+// Running (maximum m, sum S of 2^(z c - m c)): joins (m2, s2) to (m, s).  Equal maxima (-inf among them) need no factor.
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float c) {
   const float M = max_nan(m, m2);
-  const float a = m == M ? s : s * ex2((m - M) * c);     // equal maxima (-inf among them): no factor
-  const float b = m2 == M ? s2 : s2 * ex2((m2 - M) * c);
+  const Shift sh(M, c);
+  const float a = m == M ? s : s * ex2(sh(m, c));
+  const float b = m2 == M ? s2 : s2 * ex2(sh(m2, c));
   m = M;
   s = a + b;
 }
@@ -85,13 +113,343 @@ __device__ __forceinline__ void set_float(__nv_bfloat16* p, float x) { *p = __fl
 struct DistillShared {
   float p[DISTILL_MAX_TOP], logp[DISTILL_MAX_TOP], z[DISTILL_MAX_TOP];
   int id[DISTILL_MAX_TOP];          // -1: no candidate
-  float wm[DISTILL_THREADS / 32], ws[DISTILL_THREADS / 32];
-  float cm[8], cs[8];               // the cluster's blocks
-  int live;
+  float m[8][DISTILL_THREADS / 32], s[8][DISTILL_THREADS / 32];   // of the streaming warps of the cluster's blocks
+  float most;                       // the teacher's largest logit
+  // ids already seen: open addressing, each slot an id and the first candidate that has it
+  int key[2 * DISTILL_MAX_TOP], first[2 * DISTILL_MAX_TOP];
 };
 
+// A block's part of a row: elements [lo, hi), 16-byte vectors from `body` on, single ones before and after.
+struct Slice {
+  int lo, hi, body, nvec, tail;
+  template <typename T>
+  __device__ __forceinline__ Slice(const T* z, int vocab, int parts, int part) {
+    const int per = (((vocab + parts - 1) / parts) + 63) / 64 * 64;
+    lo = min(vocab, part * per);
+    hi = min(vocab, lo + per);
+    const int head = (int)(((16 - (reinterpret_cast<uintptr_t>(z + lo) & 15)) & 15) / sizeof(T));
+    body = lo + min(hi - lo, head);
+    nvec = (hi - body) / LogitVec<T>::N;
+    tail = body + nvec * LogitVec<T>::N;
+  }
+  // the single element of thread `tid` (there are fewer than 2 x 8), or -1
+  __device__ __forceinline__ int single(int tid) const {
+    if (tid < body - lo) return lo + tid;
+    tid -= body - lo;
+    return tid < hi - tail ? tail + tid : -1;
+  }
+};
+
+// The candidates' ids, the teacher's and the student's logits, log p and p, by one warp.  (Of the student's logits a
+// block needs those of its part, and the first block all of them, for the loss.)
 template <typename T>
-__global__ void __launch_bounds__(DISTILL_THREADS) distill_kernel(DistillArgs a) {
+__device__ __forceinline__ void distill_candidates(const DistillArgs& a, DistillShared& sh, int64_t row, const T* z,
+                                                   const Slice& sl, bool all) {
+  const int lane = threadIdx.x & 31;
+  float most = -INFINITY;
+  for (int j = lane; j < a.top; j += 32) {
+    const int64_t id = a.ids64 ? reinterpret_cast<const int64_t*>(a.ids)[row * a.ldi + j]
+                               : (int64_t) reinterpret_cast<const int32_t*>(a.ids)[row * a.ldi + j];
+    const bool ok = id >= 0 && id < a.vocab;
+    const float t = !ok ? -INFINITY : (a.t_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.t)[row * a.ldt + j])
+                                                : reinterpret_cast<const float*>(a.t)[row * a.ldt + j]);
+    sh.id[j] = ok ? (int)id : -1;
+    sh.logp[j] = t;
+    sh.z[j] = ok && (all || (id >= sl.lo && id < sl.hi)) ? as_float(z[id]) : 0.f;
+    most = max_nan(most, t);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if (lane == 0) sh.most = most;         // -inf: no candidate
+  float st = 0.f;
+  for (int j = lane; j < a.top; j += 32) {
+    const float d = (sh.logp[j] - most) / a.tau;
+    sh.logp[j] = d;
+    st += expf(d);
+  }
+  const float ls = logf(warp_sum(st));
+  for (int j = lane; j < a.top; j += 32) {
+    sh.logp[j] -= ls;
+    sh.p[j] = expf(sh.logp[j]);
+  }
+  __syncwarp();
+}
+
+// Makes p[j] the sum over all candidates of id[j] in this block's part, for the first of them; the ids of the others,
+// and of candidates elsewhere, become -1.  By one warp, after the loss (which takes each p by itself).
+__device__ __forceinline__ void distill_unite(const DistillArgs& a, DistillShared& sh, const Slice& sl) {
+  const int lane = threadIdx.x & 31;
+  int size = 64;
+  while (size < 2 * a.top) size *= 2;
+  for (int i = lane; i < size; i += 32) {
+    sh.key[i] = -1;
+    sh.first[i] = DISTILL_MAX_TOP;
+  }
+  __syncwarp();
+  auto find = [&](int id) {              // the slot of an id, taken if it is new; at most half of them are taken
+    int h = (int)((unsigned)id * 2654435761u >> 16) & (size - 1);
+    for (int tries = 0; tries < size; ++tries, h = (h + 1) & (size - 1)) {
+      const int k = atomicCAS(&sh.key[h], -1, id);
+      if (k == -1 || k == id) break;
+    }
+    return h;
+  };
+  bool again = false;
+  for (int j = lane; j < a.top; j += 32) {
+    const int id = sh.id[j];
+    if (id >= sl.lo && id < sl.hi) atomicMin(&sh.first[find(id)], j);
+  }
+  __syncwarp();
+  for (int j = lane; j < a.top; j += 32) {
+    const int id = sh.id[j];
+    if (id >= sl.lo && id < sl.hi) again |= sh.first[find(id)] != j;
+  }
+  if (__any_sync(0xffffffffu, again)) {  // an id more than once: add in order
+    for (int j = lane; j < a.top; j += 32) {
+      const int id = sh.id[j];
+      if (id < sl.lo || id >= sl.hi || sh.first[find(id)] != j) continue;
+      float p = 0.f;
+      for (int i = j; i < a.top; ++i)
+        if (sh.id[i] == id) p += sh.p[i];
+      sh.logp[j] = p;                    // the loss is done with log p
+    }
+    __syncwarp();
+    for (int j = lane; j < a.top; j += 32) {
+      const int id = sh.id[j];
+      if (id < sl.lo || id >= sl.hi) continue;
+      sh.p[j] = sh.first[find(id)] == j ? sh.logp[j] : -1.f;   // -1 marks the others: ids are still being compared
+    }
+    __syncwarp();
+    for (int j = lane; j < a.top; j += 32)
+      if (sh.p[j] == -1.f) sh.id[j] = -1;
+  }
+  __syncwarp();
+}
+
+// (maximum, sum) over the cluster; every thread gets it.  Each streaming warp gives its own to every block, and after
+// one barrier each warp joins them all, in the order of blocks and warps.  `use` is uniform over the cluster.
+__device__ __forceinline__ void distill_join(DistillShared& sh, cooperative_groups::cluster_group& cluster, float& m, float& s,
+                                             float c, bool use, int streaming) {
+  const int parts = (int)cluster.num_blocks(), part = (int)cluster.block_rank();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (use && warp < streaming) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+      join(m, s, m2, s2, c);
+    }
+    if (lane < parts) {
+      *cluster.map_shared_rank(&sh.m[part][warp], lane) = m;
+      *cluster.map_shared_rank(&sh.s[part][warp], lane) = s;
+    }
+  }
+  if (parts > 1) cluster.sync();
+  else __syncthreads();
+  if (use) {
+    m = -INFINITY;
+    s = 0.f;
+    for (int i = lane; i < parts * streaming; i += 32) join(m, s, sh.m[i / streaming][i % streaming], sh.s[i / streaming][i % streaming], c);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+      join(m, s, m2, s2, c);
+    }
+  }
+}
+
+// The row's loss, by one warp: log q = ln 2 (z c - k) - ln S.
+__device__ __forceinline__ void distill_loss(const DistillArgs& a, const DistillShared& sh, int64_t row, float weight, float c,
+                                             const Shift& at, float s, bool teaches) {
+  const int lane = threadIdx.x & 31;
+  float l = 0.f;
+  if (teaches) {
+    const float ls = logf(s);
+    for (int j = lane; j < a.top; j += 32)
+      if (sh.p[j] != 0.0f) l += sh.p[j] * (sh.logp[j] - fmaf(at(sh.z[j], c), LN2, -ls));
+    l = warp_sum(l);
+  }
+  if (lane == 0) a.loss[row] = teaches ? weight * (a.tau * a.tau) * l : 0.0f;
+}
+
+// The candidates' gradients, over the dense ones: scale (q - p), by the warp that united them.
+template <typename T>
+__device__ __forceinline__ void distill_patch(const DistillArgs& a, const DistillShared& sh, const Slice& sl, T* dz, float scale,
+                                              float c, const Shift& at, float s) {
+  for (int j = threadIdx.x & 31; j < a.top; j += 32) {
+    const int id = sh.id[j];
+    if (id >= sl.lo && id < sl.hi) set_float(dz + id, scale * (ex2(at(sh.z[j], c)) / s - sh.p[j]));
+  }
+}
+
+// The candidates' gradients come after the streaming warps' stores: one barrier of the whole block, in both roles.
+__device__ __forceinline__ void dense_done() { asm volatile("bar.sync 1, %0;" ::"r"((int)blockDim.x) : "memory"); }
+
+// One logit into a thread's running (maximum, sum).
+__device__ __forceinline__ void distill_take(float& m, float& s, float v, float c) {
+  const float M = max_nan(m, v);
+  const Shift at(M, c);
+  if (M != m) {
+    s *= ex2(at(m, c));                 // 0 at the first finite value; NaN stays
+    m = M;
+  }
+  if (m != -INFINITY) s += ex2(at(v, c));
+}
+// 2^(z c - k) of a vector, in pairs.  A sum flushes what lies 2^-126 below its largest term; a gradient (which a
+// large weight may scale up) takes the slower form for a vector that has such a value.
+template <int N, bool KEEP>
+__device__ __forceinline__ void distill_powers(float (&f)[N], const Shift& at, float c) {
+  const f2 b = f2_of(-at.b, -at.b), c2 = f2_of(c, c), k = f2_of(-at.k, -at.k);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 x = f2_get(fma2(add2(f2_of(f[i], f[i + 1]), b), c2, k));
+    f[i] = x.x;
+    f[i + 1] = x.y;
+  }
+  bool low = false;
+  if (KEEP) {
+    float least = f[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) least = fminf(least, f[i]);
+    low = least < -126.f;
+  }
+  if (low) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = ex2(f[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = ex2_flush(f[i]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void distill_take(float& m, float& s, float (&f)[LogitVec<T>::N], float c) {
+  constexpr int N = LogitVec<T>::N;
+  float M = max3_nan(m, f[0], f[1]);
+#pragma unroll
+  for (int i = 2; i < N; i += 2) M = max3_nan(M, f[i], f[i + 1]);
+  const Shift at(M, c);
+  if (M != m) {
+    s *= ex2(at(m, c));
+    m = M;
+  }
+  if (m != -INFINITY) {
+    distill_powers<N, false>(f, at, c);
+    f2 e = f2_of(f[0], f[1]);
+#pragma unroll
+    for (int i = 2; i < N; i += 2) e = add2(e, f2_of(f[i], f[i + 1]));
+    s += sum2(e);
+  }
+}
+// scale 2^(z c - k) of a vector.
+template <typename T>
+__device__ __forceinline__ void distill_dense(float (&f)[LogitVec<T>::N], const Shift& at, float c, float g) {
+  constexpr int N = LogitVec<T>::N;
+  distill_powers<N, true>(f, at, c);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 x = f2_get(mul2(f2_of(f[i], f[i + 1]), f2_of(g, g)));
+    f[i] = x.x;
+    f[i + 1] = x.y;
+  }
+}
+
+// ------------------------------------------------------------- rows in registers: NV vectors a thread
+template <typename T, int NV>
+__global__ void __launch_bounds__(DISTILL_THREADS + 32, 2) distill_kernel(DistillArgs a) {
+  namespace cg = cooperative_groups;
+  using V = LogitVec<T>;
+  __shared__ DistillShared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int parts = (int)cluster.num_blocks(), part = (int)cluster.block_rank();
+  const int64_t row = blockIdx.x / parts;
+  const int tid = threadIdx.x, threads = blockDim.x - 32;      // the last warp: candidates
+  const bool streams = tid < threads;
+  const T* z = reinterpret_cast<const T*>(a.z) + row * a.ldz;
+  T* dz = reinterpret_cast<T*>(a.dz) + row * a.lddz;
+  const float weight = a.weight ? a.weight[row] : 1.0f;
+  const float c = LOG2E / a.tau;
+  const Slice sl(z, (int)a.vocab, parts, part);
+  const bool reads = weight != 0.0f;
+
+  // what lies past the part's end counts as -infinity
+  uint4 w[NV];
+  constexpr uint32_t NONE = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
+  float one = -INFINITY;
+  const int at = streams ? sl.single(tid) : -1;
+  if (reads && streams) {
+    const uint4* zv = reinterpret_cast<const uint4*>(z + sl.body);
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      w[u] = make_uint4(NONE, NONE, NONE, NONE);
+      if (tid + u * threads < sl.nvec) w[u] = zv[tid + u * threads];
+    }
+    if (at >= 0) one = as_float(z[at]);
+  }
+  if (reads && !streams) distill_candidates(a, sh, row, z, sl, part == 0);
+  float m = one, s = 0.f;
+  if (reads && streams) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      float f[V::N];
+      V::unpack(w[u], f);
+#pragma unroll
+      for (int e = 0; e < V::N; e += 2) m = max3_nan(m, f[e], f[e + 1]);
+    }
+    if (m != -INFINITY) {
+      const Shift mine(m, c);
+      f2 e2 = f2_of(ex2(mine(one, c)), 0.f);
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        float f[V::N];
+        V::unpack(w[u], f);
+        distill_powers<V::N, false>(f, mine, c);
+#pragma unroll
+        for (int e = 0; e < V::N; e += 2) e2 = add2(e2, f2_of(f[e], f[e + 1]));
+      }
+      s = sum2(e2);
+    }
+  }
+  distill_join(sh, cluster, m, s, c, reads, threads >> 5);
+  const Shift shift(m, c);
+  const bool teaches = reads && sh.most != -INFINITY;
+  if (!streams) {
+    if (part == 0) distill_loss(a, sh, row, weight, c, shift, s, teaches);
+    if (!a.dz) return;
+    if (teaches) distill_unite(a, sh, sl);
+    dense_done();
+    if (teaches) distill_patch(a, sh, sl, reinterpret_cast<T*>(a.dz) + row * a.lddz, weight * a.tau, c, shift, s);
+    return;
+  }
+  if (!a.dz) return;
+
+  const float scale = weight * a.tau;
+  const float g = teaches ? scale / s : 0.f;
+  if (at >= 0) set_float(dz + at, teaches ? g * ex2(shift(one, c)) : 0.f);
+  const bool aligned = (reinterpret_cast<uintptr_t>(dz + sl.body) & 15) == 0;
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int i = tid + u * threads;
+    if (i >= sl.nvec) break;
+    float f[V::N];
+    if (teaches) {
+      V::unpack(w[u], f);
+      distill_dense<T>(f, shift, c, g);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) f[e] = 0.f;
+    }
+    if (aligned) {
+      reinterpret_cast<uint4*>(dz + sl.body)[i] = V::pack(f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V::N; ++e) set_float(dz + sl.body + i * V::N + e, f[e]);
+    }
+  }
+  dense_done();
+}
+
+// ------------------------------------------------------------- longer rows, read twice
+template <typename T>
+__global__ void __launch_bounds__(DISTILL_THREADS + 32) distill_long_kernel(DistillArgs a) {
   namespace cg = cooperative_groups;
   using V = LogitVec<T>;
   constexpr int U = 4;              // vectors in flight a thread
@@ -99,194 +457,80 @@ __global__ void __launch_bounds__(DISTILL_THREADS) distill_kernel(DistillArgs a)
   cg::cluster_group cluster = cg::this_cluster();
   const int parts = (int)cluster.num_blocks(), part = (int)cluster.block_rank();
   const int64_t row = blockIdx.x / parts;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, threads = blockDim.x - 32;      // the last warp: candidates
+  const bool streams = tid < threads;
   const T* z = reinterpret_cast<const T*>(a.z) + row * a.ldz;
   T* dz = reinterpret_cast<T*>(a.dz) + row * a.lddz;
   const float weight = a.weight ? a.weight[row] : 1.0f;
   const float c = LOG2E / a.tau;
-  const int V64 = (int)a.vocab;
+  const Slice sl(z, (int)a.vocab, parts, part);
+  const bool reads = weight != 0.0f;
+  const uint4* zv = reinterpret_cast<const uint4*>(z + sl.body);
+  const int at = streams ? sl.single(tid) : -1;
 
-  // this block's slice of the row: [lo, hi), with 16-byte aligned vectors from `body` on
-  const int per = (((V64 + parts - 1) / parts) + 63) / 64 * 64;
-  const int lo = min(V64, part * per), hi = min(V64, lo + per);
-  const int head = min(hi - lo, (int)(((16 - (reinterpret_cast<uintptr_t>(z + lo) & 15)) & 15) / sizeof(T)));
-  const int body = lo + head;
-  const int nvec = (hi - body) / V::N;
-  const int tail = body + nvec * V::N;
-
-  // ---- the candidates (warp 0 of each block, while the others begin with the logits)
-  if (warp == 0) {
-    float mt = -INFINITY;
-    for (int j = lane; j < a.top; j += 32) {
-      const int64_t id = a.ids64 ? reinterpret_cast<const int64_t*>(a.ids)[row * a.ldi + j]
-                                 : (int64_t) reinterpret_cast<const int32_t*>(a.ids)[row * a.ldi + j];
-      const bool ok = id >= 0 && id < a.vocab;
-      const float t = !ok ? -INFINITY : (a.t_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.t)[row * a.ldt + j])
-                                                  : reinterpret_cast<const float*>(a.t)[row * a.ldt + j]);
-      sh.id[j] = ok ? (int)id : -1;
-      sh.logp[j] = t;
-      sh.z[j] = ok ? as_float(z[id]) : 0.f;
-      mt = max_nan(mt, t);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mt = max_nan(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-    const bool live = mt != -INFINITY;
-    float st = 0.f;
-    for (int j = lane; j < a.top; j += 32) {
-      const float d = live ? (sh.logp[j] - mt) / a.tau : -INFINITY;
-      sh.logp[j] = d;
-      st += expf(d);
-    }
-    st = warp_sum(st);
-    const float ls = logf(st);
-    for (int j = lane; j < a.top; j += 32) {
-      sh.logp[j] = sh.logp[j] - ls;
-      sh.p[j] = live ? expf(sh.logp[j]) : 0.f;
-    }
-    if (lane == 0) sh.live = live;
-  }
-  bool teaches = weight != 0.0f;
-
-  // ---- running maximum and sum of this block's slice
+  if (reads && !streams) distill_candidates(a, sh, row, z, sl, part == 0);
   float m = -INFINITY, s = 0.f;
-  if (teaches) {
-    auto take = [&](float v) {
-      const float M = max_nan(m, v);
-      if (M != m) {
-        s *= ex2((m - M) * c);            // 0 at the first finite value; NaN stays
-        m = M;
-      }
-      if (m != -INFINITY) s += ex2((v - m) * c);
-    };
-    for (int i = tid; i < head; i += DISTILL_THREADS) take(as_float(z[lo + i]));
-    for (int i = tail + tid; i < hi; i += DISTILL_THREADS) take(as_float(z[i]));
-    const uint4* zv = reinterpret_cast<const uint4*>(z + body);
-    for (int i0 = tid; i0 < nvec; i0 += U * DISTILL_THREADS) {
+  if (reads && streams) {
+    if (at >= 0) distill_take(m, s, as_float(z[at]), c);
+    for (int i0 = tid; i0 < sl.nvec; i0 += U * threads) {
       uint4 w[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * DISTILL_THREADS;
-        w[u] = zv[i < nvec ? i : i0];
-      }
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * threads < sl.nvec) w[u] = zv[i0 + u * threads];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (i0 + u * DISTILL_THREADS < nvec) {
+        if (i0 + u * threads < sl.nvec) {
           float f[V::N];
           V::unpack(w[u], f);
-          float M = m;
-#pragma unroll
-          for (int k = 0; k < V::N; ++k) M = max_nan(M, f[k]);
-          if (M != m) {
-            s *= ex2((m - M) * c);
-            m = M;
-          }
-          if (m != -INFINITY) {
-            float e = 0.f;
-#pragma unroll
-            for (int k = 0; k < V::N; ++k) e += ex2((f[k] - m) * c);
-            s += e;
-          }
+          distill_take<T>(m, s, f, c);
         }
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-      join(m, s, m2, s2, c);
-    }
-    if (lane == 0) {
-      sh.wm[warp] = m;
-      sh.ws[warp] = s;
-    }
   }
-  __syncthreads();
-  teaches = teaches && sh.live;
-  if (weight != 0.0f) {
-    if (warp == 0) {
-      m = lane < DISTILL_THREADS / 32 ? sh.wm[lane] : -INFINITY;
-      s = lane < DISTILL_THREADS / 32 ? sh.ws[lane] : 0.f;
-#pragma unroll
-      for (int o = DISTILL_THREADS / 64; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-        join(m, s, m2, s2, c);
-      }
-      if (lane < parts) {               // to every block of the cluster
-        *cluster.map_shared_rank(&sh.cm[part], lane) = m;
-        *cluster.map_shared_rank(&sh.cs[part], lane) = s;
-      }
-    }
-  }
-  cluster.sync();
-  if (weight != 0.0f) {
-    m = sh.cm[0];
-    s = sh.cs[0];
-    for (int k = 1; k < parts; ++k) join(m, s, sh.cm[k], sh.cs[k], c);
-  }
-
-  // ---- the loss (block 0, warp 0)
-  if (part == 0 && warp == 0) {
-    float l = 0.f;
-    if (teaches) {
-      const float ls = logf(s), it = 1.0f / a.tau;
-      for (int j = lane; j < a.top; j += 32)
-        if (sh.p[j] != 0.0f) l += sh.p[j] * (sh.logp[j] - ((sh.z[j] - m) * it - ls));
-      l = warp_sum(l);
-    }
-    if (lane == 0) a.loss[row] = teaches ? weight * (a.tau * a.tau) * l : 0.0f;
+  distill_join(sh, cluster, m, s, c, reads, threads >> 5);
+  const Shift shift(m, c);
+  const bool teaches = reads && sh.most != -INFINITY;
+  if (!streams) {
+    if (part == 0) distill_loss(a, sh, row, weight, c, shift, s, teaches);
+    if (!a.dz) return;
+    if (teaches) distill_unite(a, sh, sl);
+    dense_done();
+    if (teaches) distill_patch(a, sh, sl, reinterpret_cast<T*>(a.dz) + row * a.lddz, weight * a.tau, c, shift, s);
+    return;
   }
   if (!a.dz) return;
 
-  // ---- the gradient of this block's slice
   const float scale = weight * a.tau;
-  const float f = teaches ? scale / s : 0.f;
-  for (int i = tid; i < head; i += DISTILL_THREADS) set_float(dz + lo + i, teaches ? f * ex2((as_float(z[lo + i]) - m) * c) : 0.f);
-  for (int i = tail + tid; i < hi; i += DISTILL_THREADS) set_float(dz + i, teaches ? f * ex2((as_float(z[i]) - m) * c) : 0.f);
-  const uint4* zv = reinterpret_cast<const uint4*>(z + body);
-  const bool aligned = (reinterpret_cast<uintptr_t>(dz + body) & 15) == 0;
-  for (int i0 = tid; i0 < nvec; i0 += U * DISTILL_THREADS) {
+  const float g = teaches ? scale / s : 0.f;
+  if (at >= 0) set_float(dz + at, teaches ? g * ex2(shift(as_float(z[at]), c)) : 0.f);
+  const bool aligned = (reinterpret_cast<uintptr_t>(dz + sl.body) & 15) == 0;
+  for (int i0 = tid; i0 < sl.nvec; i0 += U * threads) {
     uint4 w[U];
     if (teaches) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * DISTILL_THREADS;
-        w[u] = zv[i < nvec ? i : i0];
-      }
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * threads < sl.nvec) w[u] = zv[i0 + u * threads];
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * DISTILL_THREADS;
-      if (i >= nvec) break;
-      float g[V::N];
+      const int i = i0 + u * threads;
+      if (i >= sl.nvec) break;
+      float f[V::N];
 #pragma unroll
-      for (int k = 0; k < V::N; ++k) g[k] = 0.f;
+      for (int e = 0; e < V::N; ++e) f[e] = 0.f;
       if (teaches) {
-        V::unpack(w[u], g);
-#pragma unroll
-        for (int k = 0; k < V::N; ++k) g[k] = f * ex2((g[k] - m) * c);
+        V::unpack(w[u], f);
+        distill_dense<T>(f, shift, c, g);
       }
       if (aligned) {
-        reinterpret_cast<uint4*>(dz + body)[i] = V::pack(g);
+        reinterpret_cast<uint4*>(dz + sl.body)[i] = V::pack(f);
       } else {
 #pragma unroll
-        for (int k = 0; k < V::N; ++k) set_float(dz + body + i * V::N + k, g[k]);
+        for (int e = 0; e < V::N; ++e) set_float(dz + sl.body + i * V::N + e, f[e]);
       }
     }
   }
-  if (!teaches) return;
-  __syncthreads();
-  for (int j = tid; j < a.top; j += DISTILL_THREADS) {
-    const int id = sh.id[j];
-    if (id < lo || id >= hi) continue;
-    bool first = true;
-    float p = 0.f;
-    for (int k = 0; k < a.top; ++k) {
-      if (sh.id[k] == id) {
-        if (k < j) first = false;
-        p += sh.p[k];
-      }
-    }
-    if (first) set_float(dz + id, scale * (ex2((sh.z[j] - m) * c) / s - p));
-  }
+  dense_done();
 }
 
 }  // namespace precond

@@ -106,8 +106,8 @@ __device__ __forceinline__ float sum2(f2 v) {
 
 struct F16 { f2 p[8]; };                               // 16 values
 template <typename T> struct Raw16;                    // 16 elements as stored
-template <> struct Raw16<__nv_bfloat16> { uint32_t w[8]; };
-template <> struct Raw16<float> { uint32_t w[16]; };
+template <> struct Raw16<__nv_bfloat16> { alignas(16) uint32_t w[8]; };
+template <> struct Raw16<float> { alignas(16) uint32_t w[16]; };
 
 __device__ __forceinline__ void ld_sector(uint32_t* w, const void* p) {   // 32 bytes, 32-byte aligned
   asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -120,65 +120,101 @@ __device__ __forceinline__ void st_sector(void* p, const uint32_t* w) {
 }
 
 // Elements c .. c + 15 of a row of `cols`; what lies past the row's end is zero.
-// VEC: rows are 32-byte aligned and cols is a multiple of 16.
-template <bool VEC>
-__device__ __forceinline__ void load16(Raw16<__nv_bfloat16>& o, const __nv_bfloat16* row, int c, int cols) {
-  if (VEC) {
-    if (c < cols) {
-      ld_sector(o.w, row + c);
+// VEC: rows begin at multiples of 32 bytes, and a thread takes whole sectors.
+// Otherwise the warp takes its 512 elements in stripes (lane l elements l, l +
+// 32, ...), which are consecutive in memory whatever the row's alignment (2 B a
+// lane at a stride of 32 B costs 16 times the L1 work), and settle() exchanges
+// them through the warp's scratch of 512 elements.  All lanes of a warp call
+// these together, with consecutive c.
+template <typename T> __device__ __forceinline__ uint32_t element_bits(const T* p);
+template <> __device__ __forceinline__ uint32_t element_bits(const __nv_bfloat16* p) { return *reinterpret_cast<const uint16_t*>(p); }
+template <> __device__ __forceinline__ uint32_t element_bits(const float* p) { return *reinterpret_cast<const uint32_t*>(p); }
+template <typename T> struct Storage;
+template <> struct Storage<__nv_bfloat16> { typedef uint16_t type; };
+template <> struct Storage<float> { typedef uint32_t type; };
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void load16(Raw16<T>& o, const T* row, int c, int cols) {
+  constexpr int E = 4 / sizeof(T);                       // elements a word
+#pragma unroll
+  for (int h = 0; h < 16 / E; h += 8) {                  // a sector: 8 words
+    if (VEC) {
+      const int at = c + h * E;
+      if (at + 8 * E <= cols) {
+        ld_sector(o.w + h, row + at);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          o.w[h + i] = 0;
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (at + i * E + e < cols) o.w[h + i] |= element_bits(row + at + i * E + e) << (16 * e);
+        }
+      }
     } else {
+      const int lane = threadIdx.x & 31, at = c - 15 * lane;   // the warp's first element, + lane
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o.w[i] = 0;
-    }
-  } else {
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+      for (int i = 0; i < 8; ++i) {
+        o.w[h + i] = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t lo = c + 2 * i < cols ? p[c + 2 * i] : 0, hi = c + 2 * i + 1 < cols ? p[c + 2 * i + 1] : 0;
-      o.w[i] = lo | hi << 16;
+        for (int e = 0; e < E; ++e) {
+          const int k = at + 32 * ((h + i) * E + e);
+          if (k < cols) o.w[h + i] |= element_bits(row + k) << (16 * e);
+        }
+      }
     }
   }
 }
-template <bool VEC>
-__device__ __forceinline__ void load16(Raw16<float>& o, const float* row, int c, int cols) {
-  if (VEC) {
-    if (c < cols) {
-      ld_sector(o.w, row + c);
-      ld_sector(o.w + 8, row + c + 8);
-    } else {
+// From stripes to 16 consecutive elements a lane, and back.
+template <typename T>
+__device__ __forceinline__ void to_stripes(const Raw16<T>& o, typename Storage<T>::type* xs) {
+  constexpr int E = 4 / sizeof(T);
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o.w[i] = 0;
-    }
-  } else {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(row);
+  for (int i = 0; i < 16 / E; ++i)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o.w[i] = c + i < cols ? p[c + i] : 0;
-  }
+    for (int e = 0; e < E; ++e) xs[32 * (i * E + e) + lane] = (typename Storage<T>::type)(o.w[i] >> (16 * e));
 }
-template <bool VEC>
-__device__ __forceinline__ void store16(__nv_bfloat16* row, int c, int cols, const Raw16<__nv_bfloat16>& o) {
-  if (VEC) {
-    if (c < cols) st_sector(row + c, o.w);
-  } else {
-    uint16_t* p = reinterpret_cast<uint16_t*>(row);
+template <bool VEC, typename T>
+__device__ __forceinline__ void settle(Raw16<T>& o, void* scratch) {
+  if (VEC) return;
+  typename Storage<T>::type* xs = reinterpret_cast<typename Storage<T>::type*>(scratch);
+  to_stripes(o, xs);
+  __syncwarp();
+  const uint4* p = reinterpret_cast<const uint4*>(xs + 16 * (threadIdx.x & 31));
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (c + i < cols) p[c + i] = (uint16_t)(o.w[i >> 1] >> (16 * (i & 1)));
-  }
+  for (int i = 0; i < (int)sizeof(o.w) / 16; ++i) *reinterpret_cast<uint4*>(o.w + 4 * i) = p[i];
+  __syncwarp();
 }
-template <bool VEC>
-__device__ __forceinline__ void store16(float* row, int c, int cols, const Raw16<float>& o) {
+template <bool VEC, typename T>
+__device__ __forceinline__ void store16(T* row, int c, int cols, const Raw16<T>& o, void* scratch) {
+  constexpr int E = 4 / sizeof(T);
+  typedef typename Storage<T>::type S;
+  S* p = reinterpret_cast<S*>(row);
   if (VEC) {
-    if (c < cols) {
-      st_sector(row + c, o.w);
-      st_sector(row + c + 8, o.w + 8);
-    }
-  } else {
-    uint32_t* p = reinterpret_cast<uint32_t*>(row);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (c + i < cols) p[c + i] = o.w[i];
+    for (int h = 0; h < 16 / E; h += 8) {
+      const int at = c + h * E;
+      if (at + 8 * E <= cols) {
+        st_sector(row + at, o.w + h);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8 * E; ++i)
+          if (at + i < cols) p[at + i] = (S)(o.w[h + i / E] >> (16 * (i % E)));
+      }
+    }
+    return;
   }
+  S* xs = reinterpret_cast<S*>(scratch);
+  const int lane = threadIdx.x & 31, at = c - 15 * lane;
+  uint4* q = reinterpret_cast<uint4*>(xs + 16 * lane);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(o.w) / 16; ++i) q[i] = *reinterpret_cast<const uint4*>(o.w + 4 * i);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (at + 32 * i < cols) p[at + 32 * i] = xs[32 * i + lane];
+  __syncwarp();
 }
 __device__ __forceinline__ F16 unpack(const Raw16<__nv_bfloat16>& o) {
   F16 f;
@@ -221,10 +257,20 @@ __device__ __forceinline__ void store_q16(uint8_t* row, int c, int cols, uint4 b
       if (c + i < cols) row[c + i] = (uint8_t)((&b.x)[i >> 2] >> (8 * (i & 3)));
   }
 }
-// max that keeps a NaN
+// Maxima that keep a NaN: of two values, and of a value and two magnitudes.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 // Exponent byte of the 128-column block that 8 lanes hold (16 values a lane);
@@ -235,7 +281,7 @@ __device__ __forceinline__ unsigned q8_block_exponent(F16& f) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float2 x = f2_get(f.p[i]);
-    m = max_nan(m, max_nan(fabsf(x.x), fabsf(x.y)));
+    m = max3_abs(m, x.x, x.y);
   }
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));

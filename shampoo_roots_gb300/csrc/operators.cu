@@ -37,9 +37,9 @@ bool matrix8(const void* q, int64_t ld, const uint8_t* s, int64_t rows, int64_t 
   if (rows == 0 || cols == 0) return true;
   return ld >= cols && ld % 16 == 0 && ld <= MAX_SIDE && q && s && aligned(q, 16) && aligned(s, 16);
 }
-// Rows that 32-byte loads can take whole.
-bool vectors(const void* p, int64_t cols, int64_t ld, int dtype) {
-  return !p || (aligned(p, 32) && cols % 16 == 0 && ld * (int64_t)size_of(dtype) % 32 == 0);
+// Rows that begin at multiples of 32 bytes.
+bool sector_rows(const void* p, int64_t ld, int dtype) {
+  return !p || (aligned(p, 32) && ld * (int64_t)size_of(dtype) % 32 == 0);
 }
 struct Range { const char* lo; const char* hi; };
 Range range(const void* p, int64_t rows, int64_t ld, int64_t cols, size_t size) {
@@ -112,26 +112,17 @@ cudaError_t launch(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cuda
 }
 
 // ------------------------------------------------------------------------- norm
-constexpr int NORM_NV = 2, GRAD_NV = 1;             // most vectors a thread
-// Threads of a row and rows of a block.  A row is 16 columns a thread up to 512
-// threads, then 32; longer rows take the kernels that read a row twice.  Blocks
-// of short rows hold several, to have 256 threads.
+// Threads of a row and rows of a block: 16 columns a thread up to `one` threads
+// (a norm's 384 leave two blocks on an SM), then 32 up to 512 threads where the
+// kernel has that form; longer rows take the kernels that read a row twice.
+// Blocks of short rows hold several, to have 256 threads.
 struct RowShape { int threads, rows, nv; };
-RowShape row_shape(int64_t cols, int max_nv) {
-  const int64_t vec = (cols + 15) / 16;
-  RowShape s = {0, 1, 0};
-  for (int nv = 1; nv <= max_nv; nv *= 2)
-    if (vec <= 512 * nv) {
-      s.nv = nv;
-      break;
-    }
-  if (!s.nv) {
-    s.threads = max_nv == NORM_NV ? 1024 : 512;
-    return s;
-  }
-  s.threads = (int)std::max<int64_t>(32, ((vec + s.nv - 1) / s.nv + 31) / 32 * 32);
-  s.rows = std::min(8, std::max(1, 256 / s.threads));
-  return s;
+RowShape row_shape(int64_t cols, bool norm) {
+  const int64_t vec = (cols + 15) / 16, one = norm ? 384 : 512, two = norm ? 1024 : 0;
+  if (vec > std::max(one, two)) return {512, 1, 0};
+  const int nv = vec <= one ? 1 : 2;
+  const int threads = (int)std::max<int64_t>(32, ((vec + nv - 1) / nv + 31) / 32 * 32);
+  return {threads, std::min(8, std::max(1, 256 / threads)), nv};
 }
 
 int64_t row_blocks_of(const RowShape& s, int64_t rows, int sms) {
@@ -142,18 +133,20 @@ int64_t row_blocks_of(const RowShape& s, int64_t rows, int sms) {
 template <typename T, bool VEC>
 cudaError_t launch_norm(const RmsNormArgs& a, const RowShape& s, unsigned grid, cudaStream_t st) {
   const dim3 block(s.threads, s.rows);
+  const size_t smem = VEC ? 0 : (size_t)s.threads * s.rows * 16 * sizeof(T);    // the warps' exchange buffers
   switch (s.nv) {
-    case 1: return launch(rms_norm_kernel<T, 1, VEC>, dim3(grid), block, 0, st, 1, a);
-    case 2: return launch(rms_norm_kernel<T, 2, VEC>, dim3(grid), block, 0, st, 1, a);
-    default: return launch(rms_norm_long_kernel<T, VEC>, dim3(grid), block, 0, st, 1, a);
+    case 1: return launch(rms_norm_kernel<T, 1, VEC>, dim3(grid), block, smem, st, 1, a);
+    case 2: return launch(rms_norm_kernel<T, 2, VEC>, dim3(grid), block, smem, st, 1, a);
+    default: return launch(rms_norm_long_kernel<T, VEC>, dim3(grid), block, smem, st, 1, a);
   }
 }
 template <typename T, bool VEC>
 cudaError_t launch_grad(const RmsGradArgs& a, const RowShape& s, unsigned grid, cudaStream_t st) {
   const dim3 block(s.threads, s.rows);
+  const size_t smem = VEC ? 0 : (size_t)s.threads * s.rows * 16 * sizeof(T);    // the warps' exchange buffers
   switch (s.nv) {
-    case 1: return launch(rms_grad_kernel<T, 1, VEC>, dim3(grid), block, 0, st, 1, a);
-    default: return launch(rms_grad_long_kernel<T, VEC>, dim3(grid), block, 0, st, 1, a);
+    case 1: return launch(rms_grad_kernel<T, 1, VEC>, dim3(grid), block, smem, st, 1, a);
+    default: return launch(rms_grad_long_kernel<T, VEC>, dim3(grid), block, smem, st, 1, a);
   }
 }
 
@@ -246,10 +239,10 @@ int precond_rms_norm(precond_t ph, const void* x, const void* residual, const vo
   if (rc) return rc;
   RmsNormArgs a = {x, residual, weight, total, y, (uint8_t*)q, scale, rstd, ldx, ldr, ldt, ldy, ldq, (int)rows, (int)cols, eps,
                    weight_dtype == PRECOND_BF16};
-  const RowShape s = row_shape(cols, NORM_NV);
+  const RowShape s = row_shape(cols, true);
   const unsigned grid = (unsigned)row_blocks_of(s, q ? q8_row_blocks(rows) * 128 : rows, h->num_sms);
-  const bool vec = vectors(x, cols, ldx, dtype) && vectors(residual, cols, ldr, dtype) && vectors(total, cols, ldt, dtype) &&
-                   vectors(y, cols, ldy, dtype);
+  const bool vec = sector_rows(x, ldx, dtype) && sector_rows(residual, ldr, dtype) && sector_rows(total, ldt, dtype) &&
+                   sector_rows(y, ldy, dtype);
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == PRECOND_BF16)
     OP_CK((vec ? launch_norm<__nv_bfloat16, true>(a, s, grid, st) : launch_norm<__nv_bfloat16, false>(a, s, grid, st)));
@@ -262,7 +255,7 @@ int precond_rms_norm(precond_t ph, const void* x, const void* residual, const vo
 int64_t precond_rms_norm_grad_workspace(int64_t rows, int64_t cols) {
   if (!side(rows) || !side(cols)) return -1;
   if (rows == 0 || cols == 0) return 0;
-  const RowShape s = row_shape(cols, GRAD_NV);
+  const RowShape s = row_shape(cols, false);
   return row_blocks_of(s, rows, PLAN_SMS) * s.rows * cols * 4;
 }
 
@@ -285,7 +278,7 @@ int precond_rms_norm_grad(precond_t ph, const void* dy, const void* x, const voi
   for (int i = 0; i < 3; ++i) {
     for (int j = 0; j < 5; ++j) {
       // dx may lie over dy, dresidual or x, element for element, where a row is read once
-      const bool same = i == 0 && row_shape(cols, GRAD_NV).nv &&
+      const bool same = i == 0 && row_shape(cols, false).nv &&
                         ((j == 0 && dx == dy && lddx == lddy) || (j == 1 && dx == dresidual && lddx == lddr) ||
                          (j == 2 && dx == x && lddx == ldx));
       if (!same && overlap(out[i], in[j])) return PRECOND_EINVAL;
@@ -304,10 +297,10 @@ int precond_rms_norm_grad(precond_t ph, const void* dy, const void* x, const voi
   }
   RmsGradArgs a = {dy, x, dresidual, weight, rstd, dx, (float*)workspace, lddy, ldx, lddr, lddx, (int)rows, (int)cols,
                    weight_dtype == PRECOND_BF16};
-  const RowShape s = row_shape(cols, GRAD_NV);
+  const RowShape s = row_shape(cols, false);
   const unsigned grid = (unsigned)row_blocks_of(s, rows, std::min(h->num_sms, PLAN_SMS));
-  const bool vec = vectors(dy, cols, lddy, dtype) && vectors(x, cols, ldx, dtype) && vectors(dresidual, cols, lddr, dtype) &&
-                   vectors(dx, cols, lddx, dtype);
+  const bool vec = sector_rows(dy, lddy, dtype) && sector_rows(x, ldx, dtype) && sector_rows(dresidual, lddr, dtype) &&
+                   sector_rows(dx, lddx, dtype);
   if (dtype == PRECOND_BF16)
     OP_CK((vec ? launch_grad<__nv_bfloat16, true>(a, s, grid, st) : launch_grad<__nv_bfloat16, false>(a, s, grid, st)));
   else
@@ -348,7 +341,7 @@ int precond_quantize8(precond_t ph, const void* x, int dtype, int64_t rows, int6
   Quant8Args a = {x, ldx, x_scale, rows, cols, block == PRECOND_BLOCK_TILE, (uint8_t*)q, ldq, scale, (uint8_t*)qt, ldqt, scale_t};
   // 8 columns in one load: 16 bytes of bf16, 32 of fp32
   const int64_t step = 8 * (int64_t)size_of(dtype);
-  const int vec = aligned(x, step) && cols % 8 == 0 && ldx * (int64_t)size_of(dtype) % step == 0;
+  const int vec = aligned(x, step) && ldx * (int64_t)size_of(dtype) % step == 0;
   auto k = dtype == PRECOND_E4M3 ? quantize8_kernel<QIN_E4M3> : dtype == PRECOND_BF16 ? quantize8_kernel<QIN_BF16> : quantize8_kernel<QIN_F32>;
   OP_CK(launch(k, dim3((unsigned)tiles), dim3(256), 0, (cudaStream_t)stream, 1, a, vec));
   ++h->launches;
@@ -461,11 +454,21 @@ int precond_distill(precond_t ph, const void* logits, int dtype, int64_t rows, i
   if (rc) return rc;
   DistillArgs a = {logits, ldz, ids, ldi, id_bits == 64, teacher, ldt, teacher_dtype == PRECOND_BF16, weight, loss, dlogits, lddz,
                    rows, vocab, top, temperature};
-  // Blocks of a row: as many as keep the GPU full where rows are few, each with at least 8192 logits.
+  // Blocks of a row: as many as hold it in registers, and more where rows are few, each with at least 8192 logits.
+  const int64_t per_vec = 16 / (int64_t)sz, capacity = 8 * DISTILL_THREADS * per_vec;
   int parts = 1;
-  while (parts < 8 && rows * parts < 2 * h->num_sms && vocab / (parts * 2) >= 8192) parts *= 2;
-  auto k = dtype == PRECOND_BF16 ? distill_kernel<__nv_bfloat16> : distill_kernel<float>;
-  OP_CK(launch(k, dim3((unsigned)(rows * parts)), dim3(DISTILL_THREADS), 0, (cudaStream_t)stream, parts, a));
+  while (parts < 8 && (((vocab + parts - 1) / parts + 63) / 64 * 64 > capacity || (rows * parts < 2 * h->num_sms && vocab / (parts * 2) >= 8192)))
+    parts *= 2;
+  const int64_t vecs = ((vocab + parts - 1) / parts + 63) / 64 * 64 / per_vec;
+  const int nv = vecs <= DISTILL_THREADS ? 1 : vecs <= 2 * DISTILL_THREADS ? 2 : vecs <= 4 * DISTILL_THREADS ? 4 : vecs <= 8 * DISTILL_THREADS ? 8 : 0;
+  const int threads = nv == 0 ? DISTILL_THREADS : (int)std::max<int64_t>(64, ((vecs + nv - 1) / nv + 31) / 32 * 32);
+  const bool bf16 = dtype == PRECOND_BF16;
+  auto k = nv == 1 ? (bf16 ? distill_kernel<__nv_bfloat16, 1> : distill_kernel<float, 1>)
+           : nv == 2 ? (bf16 ? distill_kernel<__nv_bfloat16, 2> : distill_kernel<float, 2>)
+           : nv == 4 ? (bf16 ? distill_kernel<__nv_bfloat16, 4> : distill_kernel<float, 4>)
+           : nv == 8 ? (bf16 ? distill_kernel<__nv_bfloat16, 8> : distill_kernel<float, 8>)
+                     : (bf16 ? distill_long_kernel<__nv_bfloat16> : distill_long_kernel<float>);
+  OP_CK(launch(k, dim3((unsigned)(rows * parts)), dim3(threads + 32), 0, (cudaStream_t)stream, parts, a));
   ++h->launches;
   return PRECOND_OK;
 }

@@ -12,7 +12,7 @@
 // of their column (no bank conflicts either way), and leave as 128-byte rows.
 // The tile stays in registers as it is stored (32 registers of bf16) and is
 // unpacked where it is used, which leaves room for four blocks on an SM; bf16
-// maxima are taken on packed pairs of magnitude bits.
+// maxima are taken on packed pairs.
 #pragma once
 
 #include "form8.cuh"
@@ -36,14 +36,24 @@ template <> struct QuantTile<QIN_F32> {
   uint32_t w[8][8];
   __device__ __forceinline__ float get(int i, int j) const { return __uint_as_float(w[i][j]); }
   __device__ __forceinline__ void set_nan(int i, int j) { w[i][j] = 0x7FFFFFFFu; }
-  __device__ __forceinline__ void load(const Quant8Args& a, bool vec, int i, int64_t row, int64_t c) {
+  static constexpr int WORDS = 8;
+  __device__ __forceinline__ void load(const Quant8Args& a, int i, int64_t row, int64_t c) {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(a.x) + row * a.ldx + c;
-    if (vec && c < a.cols) {
+    if (c + 8 <= a.cols) {
       ld_sector(w[i], p);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[i][j] = c + j < a.cols ? p[j] : 0;
     }
+  }
+  __device__ __forceinline__ void load_stripes(const Quant8Args& a, int i, int64_t row, int64_t c0, int tx) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(a.x) + row * a.ldx;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[i][j] = c0 + 16 * j + tx < a.cols ? p[c0 + 16 * j + tx] : 0;
+  }
+  __device__ __forceinline__ void put_stripes(int i, void* xs, int tx) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) reinterpret_cast<uint32_t*>(xs)[16 * j + tx] = w[i][j];
   }
 };
 template <> struct QuantTile<QIN_BF16> {
@@ -52,9 +62,26 @@ template <> struct QuantTile<QIN_BF16> {
     return __uint_as_float(j & 1 ? w[i][j >> 1] & 0xFFFF0000u : w[i][j >> 1] << 16);
   }
   __device__ __forceinline__ void set_nan(int i, int j) { w[i][j >> 1] |= j & 1 ? 0x7FFF0000u : 0x7FFFu; }
-  __device__ __forceinline__ void load(const Quant8Args& a, bool vec, int i, int64_t row, int64_t c) {
+  static constexpr int WORDS = 4;
+  __device__ __forceinline__ void load_stripes(const Quant8Args& a, int i, int64_t row, int64_t c0, int tx) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(a.x) + row * a.ldx;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t k = c0 + 32 * j + tx;
+      const uint32_t lo = k < a.cols ? p[k] : 0, hi = k + 16 < a.cols ? p[k + 16] : 0;
+      w[i][j] = lo | hi << 16;
+    }
+  }
+  __device__ __forceinline__ void put_stripes(int i, void* xs, int tx) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      reinterpret_cast<uint16_t*>(xs)[32 * j + tx] = (uint16_t)w[i][j];
+      reinterpret_cast<uint16_t*>(xs)[32 * j + 16 + tx] = (uint16_t)(w[i][j] >> 16);
+    }
+  }
+  __device__ __forceinline__ void load(const Quant8Args& a, int i, int64_t row, int64_t c) {
     const uint16_t* p = reinterpret_cast<const uint16_t*>(a.x) + row * a.ldx + c;
-    if (vec && c < a.cols) {
+    if (c + 8 <= a.cols) {
       asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                    : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3]) : "l"(p) : "memory");
     } else {
@@ -75,7 +102,10 @@ template <> struct QuantTile<QIN_E4M3> {
     return (j & 1 ? hi : lo) * scale[i];
   }
   __device__ __forceinline__ void set_nan(int i, int j) {}          // e4m3's only non-finite value is NaN already
-  __device__ __forceinline__ void load(const Quant8Args& a, bool, int i, int64_t row, int64_t c) {
+  static constexpr int WORDS = 2;
+  __device__ __forceinline__ void load_stripes(const Quant8Args&, int, int64_t, int64_t, int) {}    // its rows are aligned
+  __device__ __forceinline__ void put_stripes(int, void*, int) const {}
+  __device__ __forceinline__ void load(const Quant8Args& a, int i, int64_t row, int64_t c) {
     const uint8_t* p = reinterpret_cast<const uint8_t*>(a.x) + row * a.ldx + c;   // 16-byte aligned rows, c % 8 == 0
     w[i][0] = w[i][1] = 0;
     if (c + 8 <= a.cols) {
@@ -91,9 +121,16 @@ template <> struct QuantTile<QIN_E4M3> {
   }
 };
 
-// Magnitude bits (fp32) of the 8 rows' and 8 columns' largest values in the thread's tile.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {   // keeps a NaN
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Magnitude bits (fp32) of the 8 rows' largest values over the half-warp's 128 columns, and of the thread's 8
+// columns over its 8 rows; the return value is at least INF_BITS where one of the thread's values is not finite.
 template <int IN>
-__device__ __forceinline__ void quant_maxima(const QuantTile<IN>& v, unsigned (&rm)[8], unsigned (&cm)[8]) {
+__device__ __forceinline__ unsigned quant_maxima(const QuantTile<IN>& v, unsigned (&rm)[8], unsigned (&cm)[8], bool finite) {
+  unsigned most = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) cm[j] = 0;
 #pragma unroll
@@ -101,28 +138,44 @@ __device__ __forceinline__ void quant_maxima(const QuantTile<IN>& v, unsigned (&
     rm[i] = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const unsigned b = abs_bits(v.get(i, j));
+      const unsigned b = finite ? finite_bits(v.get(i, j)) : abs_bits(v.get(i, j));
       rm[i] = max(rm[i], b);
       cm[j] = max(cm[j], b);
     }
+    most = max(most, rm[i]);
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) rm[i] = max(rm[i], __shfl_xor_sync(0xffffffffu, rm[i], o));
+  return most;
 }
-template <>
-__device__ __forceinline__ void quant_maxima<QIN_BF16>(const QuantTile<QIN_BF16>& v, unsigned (&rm)[8], unsigned (&cm)[8]) {
-  uint32_t c[4] = {0, 0, 0, 0};
+// bf16: on packed pairs, of columns and then of rows.
+__device__ __forceinline__ unsigned quant_maxima_bf16(const QuantTile<QIN_BF16>& v, unsigned (&rm)[8], unsigned (&cm)[8]) {
+  uint32_t c[4], most = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t r = 0;
+  for (int i = 0; i < 8; i += 2) {
+    uint32_t r[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t b = v.w[i][j] & 0x7FFF7FFFu;
-      r = __vmaxu2(r, b);
-      c[j] = __vmaxu2(c[j], b);
+    for (int k = 0; k < 2; ++k) {
+      uint32_t b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        b[j] = v.w[i + k][j] & 0x7FFF7FFFu;
+        c[j] = i + k == 0 ? b[j] : max_bf16x2(c[j], b[j]);
+      }
+      r[k] = max_bf16x2(max_bf16x2(b[0], b[1]), max_bf16x2(b[2], b[3]));
     }
-    rm[i] = max(r << 16, r & 0xFFFF0000u);
+    uint32_t m = max_bf16x2(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[0], r[1], 0x7632));   // rows i, i + 1
+    most = i == 0 ? m : max_bf16x2(most, m);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    rm[i] = m << 16;
+    rm[i + 1] = m & 0xFFFF0000u;
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) cm[j] = j & 1 ? c[j >> 1] & 0xFFFF0000u : c[j >> 1] << 16;
+  return max(most << 16, most & 0xFFFF0000u);
 }
 
 template <int IN>
@@ -140,34 +193,38 @@ __global__ void __launch_bounds__(256, IN == QIN_F32 ? 2 : IN == QIN_BF16 ? 4 : 
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (r0 + i < a.rows) {
-      v.load(a, vec, i, r0 + i, c0);
+      if (vec) v.load(a, i, r0 + i, c0);
+      else v.load_stripes(a, i, r0 + i, tj * 128, tx);
     } else {
 #pragma unroll
       for (auto& x : v.w[i]) x = 0;
       if constexpr (IN == QIN_E4M3) v.scale[i] = 0.f;
     }
   }
-  // row maxima (a half-warp holds a row) and column maxima (over the block)
-  unsigned rexp[8], cm[8];
-  quant_maxima<IN>(v, rexp, cm);
-  unsigned most = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) most = max(most, rexp[i]);
-  if (__syncthreads_or(most >= INF_BITS)) {
-    // somewhere in the tile a value is not finite: it becomes NaN and counts for no maximum
-#pragma unroll
-    for (int j = 0; j < 8; ++j) cm[j] = 0;
+  if (!vec) {
+    // rows that are not aligned came in stripes (lane tx columns tx, tx + 16, ...: consecutive in memory);
+    // each half-warp exchanges its rows through shared memory, 512 bytes
+    uint8_t* xs = tr + (threadIdx.x >> 4) * 512;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      rexp[i] = 0;
+      v.put_stripes(i, xs, tx);
+      __syncwarp();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const unsigned b = finite_bits(v.get(i, j));
-        if (abs_bits(v.get(i, j)) >= INF_BITS) v.set_nan(i, j);
-        rexp[i] = max(rexp[i], b);
-        cm[j] = max(cm[j], b);
-      }
+      for (int k = 0; k < QuantTile<IN>::WORDS; ++k) v.w[i][k] = reinterpret_cast<const uint32_t*>(xs)[QuantTile<IN>::WORDS * tx + k];
+      __syncwarp();
     }
+  }
+  unsigned rexp[8], cm[8], most;
+  if constexpr (IN == QIN_BF16) most = quant_maxima_bf16(v, rexp, cm);
+  else most = quant_maxima<IN>(v, rexp, cm, false);
+  if (__syncthreads_or(most >= INF_BITS)) {
+    // somewhere in the tile a value is not finite: it becomes NaN and counts for no maximum
+    quant_maxima<IN>(v, rexp, cm, true);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (abs_bits(v.get(i, j)) >= INF_BITS) v.set_nan(i, j);
   }
   if (a.tile || a.qt) {
 #pragma unroll
@@ -193,31 +250,33 @@ __global__ void __launch_bounds__(256, IN == QIN_F32 ? 2 : IN == QIN_BF16 ? 4 : 
     const unsigned b = q8_exponent(max(max(tmax[0], tmax[1]), max(tmax[2], tmax[3])));
 #pragma unroll
     for (int i = 0; i < 8; ++i) rexp[i] = b;
-  } else if (a.q) {
+  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) rexp[i] = max(rexp[i], __shfl_xor_sync(0xffffffffu, rexp[i], o));
-      rexp[i] = q8_exponent(rexp[i]);
-    }
+    for (int i = 0; i < 8; ++i) rexp[i] = q8_exponent(rexp[i]);
   }
+  const bool whole = ti * 128 + 128 <= a.rows && tj * 128 + 128 <= a.cols;
   if (a.q) {
+    uint8_t* p = a.q + r0 * a.ldq + c0;
+    uint8_t* sp = a.s + q8_scale_at(r0, (int)tj, row_tiles);          // 8 rows: 16 bytes apart
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; ++i, p += a.ldq) {
       const float inv = q8_inverse(rexp[i]);
-      const uint2 b = make_uint2(q8_pack4(v.get(i, 0) * inv, v.get(i, 1) * inv, v.get(i, 2) * inv, v.get(i, 3) * inv),
-                                 q8_pack4(v.get(i, 4) * inv, v.get(i, 5) * inv, v.get(i, 6) * inv, v.get(i, 7) * inv));
-      if (r0 + i < a.rows) {
-        uint8_t* p = a.q + (r0 + i) * a.ldq + c0;
-        if (c0 + 8 <= a.cols) {
-          *reinterpret_cast<uint2*>(p) = b;
-        } else {
+      const f2 s2 = f2_of(inv, inv);
+      uint32_t b[2];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (c0 + j < a.cols) p[j] = (uint8_t)((j < 4 ? b.x : b.y) >> (8 * (j & 3)));
-        }
+      for (int h = 0; h < 2; ++h) {
+        const float2 x = f2_get(mul2(f2_of(v.get(i, 4 * h), v.get(i, 4 * h + 1)), s2));
+        const float2 y = f2_get(mul2(f2_of(v.get(i, 4 * h + 2), v.get(i, 4 * h + 3)), s2));
+        b[h] = q8_pack4(x.x, x.y, y.x, y.y);
       }
-      if (tx == 0) a.s[q8_scale_at(r0 + i, (int)tj, row_tiles)] = (uint8_t)(r0 + i < a.rows ? rexp[i] : Q8_ONE);
+      if (whole || (r0 + i < a.rows && c0 + 8 <= a.cols)) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[1]);
+      } else if (r0 + i < a.rows) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c0 + j < a.cols) p[j] = (uint8_t)(b[j >> 2] >> (8 * (j & 3)));
+      }
+      if (tx == 0) sp[16 * i] = (uint8_t)(r0 + i < a.rows ? rexp[i] : Q8_ONE);
     }
     // the blocks of the last group past the end
     if (tj == col_tiles - 1 && threadIdx.x < 128)
@@ -225,14 +284,21 @@ __global__ void __launch_bounds__(256, IN == QIN_F32 ? 2 : IN == QIN_BF16 ? 4 : 
         a.s[q8_scale_at(ti * 128 + threadIdx.x, (int)kb, row_tiles)] = (uint8_t)Q8_ONE;
   }
   if (a.qt) {
+    uint8_t* sp = a.st + q8_scale_at(c0, (int)ti, col_tiles);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const unsigned b = a.tile ? rexp[0] : cexp[8 * tx + j];
       const float inv = q8_inverse(b);
-      *reinterpret_cast<uint2*>(tr + (8 * tx + j) * 128 + ((ty ^ tx) << 3)) =
-          make_uint2(q8_pack4(v.get(0, j) * inv, v.get(1, j) * inv, v.get(2, j) * inv, v.get(3, j) * inv),
-                     q8_pack4(v.get(4, j) * inv, v.get(5, j) * inv, v.get(6, j) * inv, v.get(7, j) * inv));
-      if (ty == 0) a.st[q8_scale_at(c0 + j, (int)ti, col_tiles)] = (uint8_t)(c0 + j < a.cols ? b : Q8_ONE);
+      const f2 s2 = f2_of(inv, inv);
+      uint32_t o[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float2 x = f2_get(mul2(f2_of(v.get(4 * h, j), v.get(4 * h + 1, j)), s2));
+        const float2 y = f2_get(mul2(f2_of(v.get(4 * h + 2, j), v.get(4 * h + 3, j)), s2));
+        o[h] = q8_pack4(x.x, x.y, y.x, y.y);
+      }
+      *reinterpret_cast<uint2*>(tr + (8 * tx + j) * 128 + ((ty ^ tx) << 3)) = make_uint2(o[0], o[1]);
+      if (ty == 0) sp[16 * j] = (uint8_t)(c0 + j < a.cols ? b : Q8_ONE);
     }
     if (ti == row_tiles - 1 && threadIdx.x < 128)
       for (int64_t kb = row_tiles; kb < 4 * (int64_t)q8_groups(a.rows); ++kb)
@@ -246,9 +312,9 @@ __global__ void __launch_bounds__(256, IN == QIN_F32 ? 2 : IN == QIN_BF16 ? 4 : 
       uint4 b = *reinterpret_cast<const uint4*>(tr + c * 128 + (((2 * p) ^ x) >> 1) * 16);
       if (x & 1) b = make_uint4(b.z, b.w, b.x, b.y);
       const int64_t oc = ti * 128 + 16 * p, orow = tj * 128 + c;
-      if (orow < a.cols && oc < a.rows) {
+      if (whole || (orow < a.cols && oc < a.rows)) {
         uint8_t* dst = a.qt + orow * a.ldqt + oc;
-        if (oc + 16 <= a.rows) {
+        if (whole || oc + 16 <= a.rows) {
           *reinterpret_cast<uint4*>(dst) = b;
         } else {
 #pragma unroll

@@ -84,13 +84,20 @@ __device__ __forceinline__ void add_stream(Raw16<float>& x, const Raw16<float>& 
   for (int i = 0; i < 16; ++i) x.w[i] = __float_as_uint(__uint_as_float(x.w[i]) + __uint_as_float(r.w[i]));
 }
 
+// A warp's exchange buffer where rows are not aligned (form8.cuh), in dynamic shared memory.
+template <typename T, bool VEC>
+__device__ __forceinline__ void* warp_scratch() {
+  extern __shared__ __align__(16) uint8_t row_scratch[];
+  return VEC ? nullptr : row_scratch + ((threadIdx.y * blockDim.x + threadIdx.x) >> 5) * (512 * sizeof(T));
+}
+
 // One vector's outputs; `at` is its scale byte's place.
 template <typename T, bool VEC>
-__device__ __forceinline__ void norm_write(const RmsNormArgs& a, int64_t row, int c, F16& y, size_t at) {
+__device__ __forceinline__ void norm_write(const RmsNormArgs& a, int64_t row, int c, F16& y, size_t at, void* xs) {
   if (a.y) {
     Raw16<T> o;
     pack(o, y);
-    store16<VEC>(reinterpret_cast<T*>(a.y) + row * a.ldy, c, a.cols, o);
+    store16<VEC>(reinterpret_cast<T*>(a.y) + row * a.ldy, c, a.cols, o, xs);
   }
   if (a.q) {
     const unsigned b = q8_block_exponent(y);
@@ -105,16 +112,27 @@ __device__ __forceinline__ void norm_pad(const RmsNormArgs& a, int64_t row, int6
     a.scale[q8_scale_at(row, kb, rblocks)] = (uint8_t)Q8_ONE;
 }
 
+// 1 / sqrt(mean + eps): the hardware's estimate and one Newton step, y (3 - x y^2) / 2.  (Every thread of a row
+// computes it; a division and a correctly rounded root cost 40 instructions of the 390 a vector took.)
+__device__ __forceinline__ float rstd_of(float sum, float inv_cols, float eps) {
+  const float x = fmaf(sum, inv_cols, eps);
+  const float y = rsqrtf(x);
+  const float z = y * fmaf(-0.5f * x * y, y, 1.5f);
+  return x < 1e30f ? z : y;            // x y y may overflow only where x does
+}
+
 // NV vectors of 16 columns a thread.
 template <typename T, int NV, bool VEC>
-__global__ void __launch_bounds__(512, NV == 1 && sizeof(T) == 2 ? 2 : 1) rms_norm_kernel(RmsNormArgs a) {
+__global__ void __launch_bounds__(NV == 1 ? 384 : 512, NV == 1 ? 2 : 1) rms_norm_kernel(RmsNormArgs a) {
   __shared__ __align__(16) float red[2 * 8 * 32];
   zero_red(red, 2 * 8 * 32);
+  void* xs = warp_scratch<T, VEC>();
   const int64_t rblocks = q8_row_blocks(a.rows);
   const int step = gridDim.x * blockDim.y;
   int row = blockIdx.x * blockDim.y + threadIdx.y;
   const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
   const T* r = reinterpret_cast<const T*>(a.r) + row * a.ldr;
+  const float inv_cols = 1.0f / (float)a.cols;
   F16 w[NV];
   int c[NV];
 #pragma unroll
@@ -135,9 +153,11 @@ __global__ void __launch_bounds__(512, NV == 1 && sizeof(T) == 2 ? 2 : 1) rms_no
     f2 ss = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      settle<VEC>(nx[j], xs);
       if (a.r) {
+        settle<VEC>(nr[j], xs);
         add_stream(nx[j], nr[j]);
-        store16<VEC>(reinterpret_cast<T*>(a.h) + row * a.ldh, c[j], a.cols, nx[j]);
+        store16<VEC>(reinterpret_cast<T*>(a.h) + row * a.ldh, c[j], a.cols, nx[j], xs);
       }
       v[j] = unpack(nx[j]);
       ss = squares(v[j], ss);
@@ -151,7 +171,7 @@ __global__ void __launch_bounds__(512, NV == 1 && sizeof(T) == 2 ? 2 : 1) rms_no
         if (a.r) load16<VEC>(nr[j], r, c[j], a.cols);
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum(sum2(ss), red, half) / (float)a.cols + a.eps);
+    const float rstd = rstd_of(row_sum(sum2(ss), red, half), inv_cols, a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     if (!a.q && !a.y) continue;
     const f2 rs = f2_of(rstd, rstd);
@@ -161,7 +181,7 @@ __global__ void __launch_bounds__(512, NV == 1 && sizeof(T) == 2 ? 2 : 1) rms_no
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[j].p[i] = mul2(mul2(v[j].p[i], rs), w[j].p[i]);
       const int kb = c[j] >> 7;
-      norm_write<T, VEC>(a, row, c[j], v[j], (size_t)(kb >> 2) * rblocks * 512 + (kb & 3) + at_row);
+      norm_write<T, VEC>(a, row, c[j], v[j], (size_t)(kb >> 2) * rblocks * 512 + (kb & 3) + at_row, xs);
     }
     if (a.q && (a.cols & 511)) norm_pad(a, row, rblocks);
   }
@@ -171,12 +191,14 @@ __global__ void __launch_bounds__(512, NV == 1 && sizeof(T) == 2 ? 2 : 1) rms_no
 
 // Rows too long for registers: one block a row, which is read again (from L2) after its norm is known.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(1024, 1) rms_norm_long_kernel(RmsNormArgs a) {
+__global__ void __launch_bounds__(512, 2) rms_norm_long_kernel(RmsNormArgs a) {
   __shared__ __align__(16) float red[2 * 32];
   zero_red(red, 2 * 32);
+  void* xs = warp_scratch<T, VEC>();
   const int64_t rblocks = q8_row_blocks(a.rows);
   const int64_t last = a.q ? rblocks * 128 : a.rows;
-  const int64_t span = ((int64_t)a.cols + 16 * 1024 - 1) / (16 * 1024) * (16 * 1024);   // every lane takes part in the block maxima
+  const int64_t stride = 16 * blockDim.x, span = (a.cols + stride - 1) / stride * stride;   // whole warps
+  const float inv_cols = 1.0f / (float)a.cols;
   int half = 0;
   for (int64_t row = blockIdx.x; row < last; row += gridDim.x, half ^= 1) {
     if (a.q) norm_pad(a, row, rblocks);
@@ -185,29 +207,32 @@ __global__ void __launch_bounds__(1024, 1) rms_norm_long_kernel(RmsNormArgs a) {
     const T* r = reinterpret_cast<const T*>(a.r) + row * a.ldr;
     T* h = reinterpret_cast<T*>(a.h) + row * a.ldh;
     f2 ss = 0;
-    for (int64_t c = threadIdx.x * 16; c < span; c += 16 * 1024) {
+    for (int64_t c = threadIdx.x * 16; c < span; c += stride) {
       Raw16<T> o, p;
       load16<VEC>(o, x, (int)c, a.cols);
+      settle<VEC>(o, xs);
       if (a.r) {
         load16<VEC>(p, r, (int)c, a.cols);
+        settle<VEC>(p, xs);
         add_stream(o, p);
-        store16<VEC>(h, (int)c, a.cols, o);
+        store16<VEC>(h, (int)c, a.cols, o, xs);
       }
       ss = squares(unpack(o), ss);
     }
-    const float rstd = 1.0f / sqrtf(row_sum(sum2(ss), red, half) / (float)a.cols + a.eps);
+    const float rstd = rstd_of(row_sum(sum2(ss), red, half), inv_cols, a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     if (!a.q && !a.y) continue;
     const f2 rs = f2_of(rstd, rstd);
-    for (int64_t c = threadIdx.x * 16; c < span; c += 16 * 1024) {
+    for (int64_t c = threadIdx.x * 16; c < span; c += stride) {
       Raw16<T> o;
-      load16<VEC>(o, a.r ? h : x, (int)c, a.cols);       // h: this thread's own stores
+      load16<VEC>(o, a.r ? h : x, (int)c, a.cols);       // h: this warp's own stores
+      settle<VEC>(o, xs);
       F16 v = unpack(o);
       const F16 w = load_w16(a.w, a.w_bf16, (int)c, a.cols);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v.p[i] = mul2(mul2(v.p[i], rs), w.p[i]);
       const int kb = (int)(c >> 7);
-      norm_write<T, VEC>(a, row, (int)c, v, q8_scale_at(row, kb, rblocks));
+      norm_write<T, VEC>(a, row, (int)c, v, q8_scale_at(row, kb, rblocks), xs);
     }
   }
 }
@@ -242,6 +267,7 @@ template <typename T, int NV, bool VEC>
 __global__ void __launch_bounds__(512, 1) rms_grad_kernel(RmsGradArgs a) {
   __shared__ __align__(16) float red[2 * 8 * 32];
   zero_red(red, 2 * 8 * 32);
+  void* xs = warp_scratch<T, VEC>();
   const int step = gridDim.x * blockDim.y;
   int row = blockIdx.x * blockDim.y + threadIdx.y;
   const T* dy = reinterpret_cast<const T*>(a.dy) + row * a.lddy;
@@ -280,9 +306,14 @@ __global__ void __launch_bounds__(512, 1) rms_grad_kernel(RmsGradArgs a) {
     f2 dot = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      settle<VEC>(ny[j], xs);
+      settle<VEC>(nx[j], xs);
       g[j] = unpack(ny[j]);
       n[j] = unpack(nx[j]);
-      if (a.dr) res[j] = nr[j];
+      if (a.dr) {
+        settle<VEC>(nr[j], xs);
+        res[j] = nr[j];
+      }
       dot = grad_terms(g[j], n[j], w[j], dw[j], rs, dot);
     }
     if (row + step < a.rows) fetch(row + step);
@@ -292,7 +323,7 @@ __global__ void __launch_bounds__(512, 1) rms_grad_kernel(RmsGradArgs a) {
     for (int j = 0; j < NV; ++j) {
       Raw16<T> o;
       grad_out(o, g[j], n[j], rs, mm, a.dr ? &res[j] : nullptr);
-      store16<VEC>(dx, c[j], a.cols, o);
+      store16<VEC>(dx, c[j], a.cols, o, xs);
     }
     dx += step * a.lddx;
   }
@@ -313,9 +344,10 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(512, 1) rms_grad_long_kernel(RmsGradArgs a) {
   __shared__ __align__(16) float red[2 * 32];
   zero_red(red, 2 * 32);
+  void* xs = warp_scratch<T, VEC>();
   float* out = a.partial + (int64_t)blockIdx.x * a.cols;
   const float inv_cols = 1.0f / (float)a.cols;
-  const int stride = 16 * blockDim.x;
+  const int64_t stride = 16 * blockDim.x, span = (a.cols + stride - 1) / stride * stride;   // whole warps
   bool first = true;
   int half = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, half ^= 1) {
@@ -325,11 +357,13 @@ __global__ void __launch_bounds__(512, 1) rms_grad_long_kernel(RmsGradArgs a) {
     T* dx = reinterpret_cast<T*>(a.dx) + row * a.lddx;
     const f2 rs = f2_of(a.rstd[row], a.rstd[row]);
     f2 dot = 0;
-    for (int64_t c = threadIdx.x * 16; c < a.cols; c += stride) {
+    for (int64_t c = threadIdx.x * 16; c < span; c += stride) {
       Raw16<T> o;
       load16<VEC>(o, dy, (int)c, a.cols);
+      settle<VEC>(o, xs);
       F16 g = unpack(o);
       load16<VEC>(o, x, (int)c, a.cols);
+      settle<VEC>(o, xs);
       F16 n = unpack(o), dw;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -345,21 +379,26 @@ __global__ void __launch_bounds__(512, 1) rms_grad_long_kernel(RmsGradArgs a) {
     first = false;
     const float mean = -row_sum(sum2(dot), red, half) * inv_cols;
     const f2 mm = f2_of(mean, mean);
-    for (int64_t c = threadIdx.x * 16; c < a.cols; c += stride) {
+    for (int64_t c = threadIdx.x * 16; c < span; c += stride) {
       Raw16<T> o, res;
       load16<VEC>(o, dy, (int)c, a.cols);
+      settle<VEC>(o, xs);
       F16 g = unpack(o);
       load16<VEC>(o, x, (int)c, a.cols);
+      settle<VEC>(o, xs);
       F16 n = unpack(o);
       const F16 w = load_w16(a.w, a.w_bf16, (int)c, a.cols);
-      if (a.dr) load16<VEC>(res, dr, (int)c, a.cols);
+      if (a.dr) {
+        load16<VEC>(res, dr, (int)c, a.cols);
+        settle<VEC>(res, xs);
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         n.p[i] = mul2(n.p[i], rs);
         g.p[i] = mul2(g.p[i], w.p[i]);
       }
       grad_out(o, g, n, rs, mm, a.dr ? &res : nullptr);
-      store16<VEC>(dx, (int)c, a.cols, o);
+      store16<VEC>(dx, (int)c, a.cols, o, xs);
     }
   }
 }
