@@ -400,6 +400,8 @@ int precond_gemm8_status(precond_t h, void* stream);
  *   weight      : rows floats (the upstream gradient and the row's mask), NULL for 1.  A row of weight 0
  *                 is not read: its loss and gradient are 0 whatever its logits hold.
  *   loss        : rows floats
+ *   workspace   : precond_distill_workspace bytes, 16-byte aligned, in use until the call's work has
+ *                 completed; may be NULL where that is 0
  * A row without a candidate (or with teacher logits of -infinity only) has loss and gradient 0.  A
  * candidate that the student gives no probability makes the loss infinite (its gradient stays finite);
  * a row of logits that are all -infinity has none to give, and NaN for both.
@@ -407,7 +409,9 @@ int precond_gemm8_status(precond_t h, void* stream);
 int precond_distill(precond_t h, const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ldz,
                     const void* ids, int id_bits, int64_t ldi, const void* teacher, int teacher_dtype, int64_t ldt,
                     int top, const float* weight, float temperature, float* loss, void* dlogits, int64_t lddz,
-                    void* stream);
+                    void* workspace, int64_t workspace_bytes, void* stream);
+/* Bytes; 0 where the call needs none (few rows).  in_place: dlogits is logits.  -1: bad arguments. */
+int64_t precond_distill_workspace(int64_t rows, int64_t vocab, int top, int dtype, int in_place);
 
 /* Static text for a status code. */
 const char* precond_error_string(int code);

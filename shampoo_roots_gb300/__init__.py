@@ -269,7 +269,7 @@ class Preconditioner:
             pass
 
 
-_OPERATORS = ("BLOCK_ROW", "BLOCK_TILE", "E4M3", "dequantize8", "empty8", "precond_distill", "precond_gemm8",
+_OPERATORS = ("BLOCK_ROW", "BLOCK_TILE", "E4M3", "dequantize8", "empty8", "precond_distill", "precond_distill_workspace", "precond_gemm8",
               "precond_gemm8_status", "precond_quantize8", "precond_rms_norm", "precond_rms_norm_grad",
               "precond_rms_norm_grad_workspace", "scale_shape", "scales8")
 

@@ -17,7 +17,7 @@ typedef struct {
 enum { T_F32, T_BF16, T_E4M3, T_E8M0, T_U8, T_I32, T_I64, T_COUNT };
 static PyObject* dtypes[T_COUNT];
 static PyObject *s_shape, *s_stride, *s_data_ptr, *s_dtype, *s_get_device, *raw_stream;
-enum { E_NORM, E_GRAD, E_QUANTIZE, E_GEMM, E_DISTILL, E_COUNT };
+enum { E_NORM, E_GRAD, E_QUANTIZE, E_GEMM, E_DISTILL, E_DISTILL_WS, E_COUNT };
 static void* entry[E_COUNT];
 
 static int bad(PyObject* type, const char* what, const char* why) {
@@ -273,13 +273,15 @@ static PyObject* gemm8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(((fn)entry[E_GEMM])(h, A.rows, B.rows, A.cols, A.p, A.ld, sa.p, B.p, B.ld, sb.p, c.p, c.ld, ct, acc, st));
 }
 
-/* (h, logits, ids, teacher, loss, weight, temperature, dlogits, stream) */
+/* (h, logits, ids, teacher, loss, weight, temperature, dlogits, workspace, stream); bytes of workspace where that is
+ * None and some is needed, as a negative number below every status. */
 static PyObject* distill(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   typedef int (*fn)(void*, const void*, int, int64_t, int64_t, int64_t, const void*, int, int64_t, const void*, int, int64_t, int,
-                    const float*, float, float*, void*, int64_t, void*);
-  Tensor z, ids, t, loss, w, dz;
+                    const float*, float, float*, void*, int64_t, void*, int64_t, void*);
+  typedef int64_t (*need_fn)(int64_t, int64_t, int, int, int);
+  Tensor z, ids, t, loss, w, dz, ws;
   void *h, *st;
-  if (count(n, 9) || handle(a[0], &h) || matrix(a[1], "logits", &z)) return NULL;
+  if (count(n, 10) || handle(a[0], &h) || matrix(a[1], "logits", &z)) return NULL;
   const int dt = float_type(&z, "logits");
   if (dt < 0 || matrix(a[2], "ids", &ids)) return NULL;
   if (ids.dtype != dtypes[T_I32] && ids.dtype != dtypes[T_I64]) {
@@ -290,11 +292,23 @@ static PyObject* distill(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   const int tt = float_type(&t, "teacher");
   const double tau = PyFloat_AsDouble(a[6]);
   if (tt < 0 || PyErr_Occurred() || vector(a[4], "loss", &loss, z.rows, 1) || maybe_vector(a[5], "weight", &w, z.rows) ||
-      maybe(a[7], "dlogits", &dz, z.rows, z.cols, z.dtype) || stream_of(a[8], a[1], &st))
+      maybe(a[7], "dlogits", &dz, z.rows, z.cols, z.dtype) || stream_of(a[9], a[1], &st))
     return NULL;
+  const int top = (int)(ids.cols > 1 << 30 ? 1 << 30 : ids.cols);
+  ws.p = NULL;
+  ws.rows = 0;
+  if (a[8] != Py_None) {
+    if (get(a[8], "workspace", &ws)) return NULL;
+    if (ws.dim != 1 || !ws.contiguous || ws.dtype != dtypes[T_U8]) {
+      PyErr_SetString(PyExc_ValueError, "workspace must be a contiguous vector of uint8");
+      return NULL;
+    }
+  } else {
+    const int64_t need = ((need_fn)entry[E_DISTILL_WS])(z.rows, z.cols, top, dt, dz.p == z.p);
+    if (need > 0) return PyLong_FromLongLong(-1000 - need);
+  }
   return PyLong_FromLong(((fn)entry[E_DISTILL])(h, z.p, dt, z.rows, z.cols, z.ld, ids.p, ids.dtype == dtypes[T_I32] ? 32 : 64, ids.ld,
-                                                t.p, tt, t.ld, (int)(ids.cols > 1 << 30 ? 1 << 30 : ids.cols), w.p, (float)tau,
-                                                loss.p, dz.p, dz.ld, st));
+                                                t.p, tt, t.ld, top, w.p, (float)tau, loss.p, dz.p, dz.ld, ws.p, ws.rows, st));
 }
 
 /* set_up(dtypes, raw_stream, entries): what the calls need, once. */

@@ -7,11 +7,19 @@
 // logits are read once and the gradient is written once.  A row belongs to a
 // cluster of 1 to 8 blocks, whose threads keep its logits in registers as they
 // are stored (up to 64 KB a block): a thread takes the maximum and the sum of its
-// own part, the blocks join theirs through distributed shared memory in their
+// own part, the blocks join theirs through distributed shared memory in a fixed
 // order, and the gradient is formed from the registers.  (Reading the row again
 // from L2 cost DRAM 3.6 GB for 1.9 GB of logits at 8192 x 131072: the rows in
 // flight do not fit beside the gradients.  967 us.)  Rows beyond 8 blocks'
-// registers take the kernel that reads them twice.
+// registers are read twice.
+//
+// The candidates take one warp some microseconds of latency: two dependent loads,
+// a softmax, a table that unites equal ids.  Where the rows fit the GPU at once
+// that warp is part of the row's block, beside those that stream the logits.
+// Many rows leave the candidates to a second kernel with a warp a row, which
+// finds the (m, S) of the rows in a workspace: as a part of each block that warp
+// kept it on the SM longer than the logits did (8192 x 131072: 904 us, without
+// candidates 713).  A call in place gathers the candidates' logits first.
 //
 // With c = log2(e) / tau and m = max(z), q_v = 2^(z_v c - k) / S, S = sum 2^(z_v
 // c - k), k = m c: the exponent is one fma, and the rounding of k cancels.  Where
@@ -19,11 +27,9 @@
 // that is masked with the type's lowest value throughout) it is (z_v - m) c
 // instead; both are (z_v - b) c - k.
 //
-// The candidates are the work of a warp of their own, beside those that stream
-// the logits (one of these doing both held the others up: 1200 us, 830 without
-// candidates).  Their logits are read before anything is written, so that dz may
-// be z itself, and their gradients are written last, those of one id added in
-// the candidates' order.
+// The candidates' logits are read before anything is written, so that dz may be
+// z itself, and their gradients are written last, those of one id added in the
+// candidates' order.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -45,6 +51,8 @@ struct DistillArgs {
   int64_t rows, vocab;
   int top;
   float tau;
+  float2* stats;                  // many rows: (m, S) of each
+  float* kept;                    // many rows in place: the candidates' logits, rows x top
 };
 
 // 2^x; and with results below 2^-126 flushed to 0, one instruction instead of four.
@@ -69,19 +77,29 @@ struct Shift {
   }
   __device__ __forceinline__ float operator()(float z, float c) const { return fmaf(z - b, c, -k); }
 };
-// Running (maximum m, sum S of 2^(z c - m c)): joins (m2, s2) to (m, s).  Equal maxima (-inf among them) need no factor.
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float c) {
-  const float M = max_nan(m, m2);
-  const Shift sh(M, c);
-  const float a = m == M ? s : s * ex2(sh(m, c));
-  const float b = m2 == M ? s2 : s2 * ex2(sh(m2, c));
+// (maximum m, sum S of 2^(z c - m c)) of the lanes, joined over the warp: the common maximum first, then one factor
+// a lane.  (A butterfly that joins pairs takes two factors and a shift at each of its five steps.)
+__device__ __forceinline__ void join_warp(float& m, float& s, float c) {
+  float M = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
+  s = warp_sum(m == M ? s : s * ex2(Shift(M, c)(m, c)));   // equal maxima (-inf among them) need no factor
   m = M;
-  s = a + b;
 }
 
 template <typename T> struct LogitVec;                    // one 16-byte vector of logits
 template <> struct LogitVec<__nv_bfloat16> {
   static constexpr int N = 8;
+  // the largest of NV vectors; a NaN stays
+  template <int NV>
+  static __device__ __forceinline__ float largest(const uint4 (&w)[NV]) {
+    uint32_t m = w[0].x;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"((&w[u].x)[i]));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+  }
   static __device__ __forceinline__ void unpack(uint4 w, float (&f)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -95,6 +113,16 @@ template <> struct LogitVec<__nv_bfloat16> {
 };
 template <> struct LogitVec<float> {
   static constexpr int N = 4;
+  template <int NV>
+  static __device__ __forceinline__ float largest(const uint4 (&w)[NV]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      m = max3_nan(m, __uint_as_float(w[u].x), __uint_as_float(w[u].y));
+      m = max3_nan(m, __uint_as_float(w[u].z), __uint_as_float(w[u].w));
+    }
+    return m;
+  }
   static __device__ __forceinline__ void unpack(uint4 w, float (&f)[4]) {
     f[0] = __uint_as_float(w.x);
     f[1] = __uint_as_float(w.y);
@@ -110,13 +138,30 @@ __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ void set_float(float* p, float x) { *p = x; }
 __device__ __forceinline__ void set_float(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// A row's shared memory, as large as its candidates need.
 struct DistillShared {
-  float p[DISTILL_MAX_TOP], logp[DISTILL_MAX_TOP], z[DISTILL_MAX_TOP];
-  int id[DISTILL_MAX_TOP];          // -1: no candidate
-  float m[8][DISTILL_THREADS / 32], s[8][DISTILL_THREADS / 32];   // of the streaming warps of the cluster's blocks
-  float most;                       // the teacher's largest logit
-  // ids already seen: open addressing, each slot an id and the first candidate that has it
-  int key[2 * DISTILL_MAX_TOP], first[2 * DISTILL_MAX_TOP];
+  float2* sums;                     // (maximum, sum) of the streaming warps of the cluster's blocks
+  float* p; float* logp; float* z; int* id;      // candidates; id -1: none
+  int* key; int* first;             // ids already seen: open addressing, an id and the first candidate that has it
+  float* most;                      // the teacher's largest logit
+  int slots;
+  static __host__ __device__ int slots_for(int top) {
+    int n = 64;
+    while (n < 2 * top) n *= 2;
+    return n;
+  }
+  static __host__ __device__ int bytes(int top, int sums) { return (sums * 8 + 16 * top + 8 * slots_for(top) + 4 + 15) / 16 * 16; }
+  __device__ __forceinline__ DistillShared(uint8_t* base, int top, int nsums) {
+    sums = reinterpret_cast<float2*>(base);
+    p = reinterpret_cast<float*>(sums + nsums);
+    logp = p + top;
+    z = logp + top;
+    id = reinterpret_cast<int*>(z + top);
+    slots = slots_for(top);
+    key = id + top;
+    first = key + slots;
+    most = reinterpret_cast<float*>(first + slots);
+  }
 };
 
 // A block's part of a row: elements [lo, hi), 16-byte vectors from `body` on, single ones before and after.
@@ -140,11 +185,11 @@ struct Slice {
   }
 };
 
-// The candidates' ids, the teacher's and the student's logits, log p and p, by one warp.  (Of the student's logits a
-// block needs those of its part, and the first block all of them, for the loss.)
+// The candidates' ids, the teacher's and the student's logits, by one warp.  (Of the student's logits a block needs
+// those of its part, and the first block all of them, for the loss.)
 template <typename T>
-__device__ __forceinline__ void distill_candidates(const DistillArgs& a, DistillShared& sh, int64_t row, const T* z,
-                                                   const Slice& sl, bool all) {
+__device__ __forceinline__ void distill_gather(const DistillArgs& a, const DistillShared& sh, int64_t row, const T* z,
+                                               const Slice& sl, bool all) {
   const int lane = threadIdx.x & 31;
   float most = -INFINITY;
   for (int j = lane; j < a.top; j += 32) {
@@ -155,12 +200,18 @@ __device__ __forceinline__ void distill_candidates(const DistillArgs& a, Distill
                                                 : reinterpret_cast<const float*>(a.t)[row * a.ldt + j]);
     sh.id[j] = ok ? (int)id : -1;
     sh.logp[j] = t;
-    sh.z[j] = ok && (all || (id >= sl.lo && id < sl.hi)) ? as_float(z[id]) : 0.f;
+    sh.z[j] = !ok ? 0.f : a.kept ? a.kept[row * a.top + j] : all || (id >= sl.lo && id < sl.hi) ? as_float(z[id]) : 0.f;
     most = max_nan(most, t);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if (lane == 0) sh.most = most;         // -inf: no candidate
+  if (lane == 0) *sh.most = most;        // -inf: no candidate
+  __syncwarp();
+}
+// log p and p, by the same warp.
+__device__ __forceinline__ void distill_teacher(const DistillArgs& a, const DistillShared& sh) {
+  const int lane = threadIdx.x & 31;
+  const float most = *sh.most;
   float st = 0.f;
   for (int j = lane; j < a.top; j += 32) {
     const float d = (sh.logp[j] - most) / a.tau;
@@ -177,10 +228,8 @@ __device__ __forceinline__ void distill_candidates(const DistillArgs& a, Distill
 
 // Makes p[j] the sum over all candidates of id[j] in this block's part, for the first of them; the ids of the others,
 // and of candidates elsewhere, become -1.  By one warp, after the loss (which takes each p by itself).
-__device__ __forceinline__ void distill_unite(const DistillArgs& a, DistillShared& sh, const Slice& sl) {
-  const int lane = threadIdx.x & 31;
-  int size = 64;
-  while (size < 2 * a.top) size *= 2;
+__device__ __forceinline__ void distill_unite(const DistillArgs& a, const DistillShared& sh, const Slice& sl) {
+  const int lane = threadIdx.x & 31, size = sh.slots;
   for (int i = lane; i < size; i += 32) {
     sh.key[i] = -1;
     sh.first[i] = DISTILL_MAX_TOP;
@@ -226,35 +275,36 @@ __device__ __forceinline__ void distill_unite(const DistillArgs& a, DistillShare
   __syncwarp();
 }
 
-// (maximum, sum) over the cluster; every thread gets it.  Each streaming warp gives its own to every block, and after
-// one barrier each warp joins them all, in the order of blocks and warps.  `use` is uniform over the cluster.
-__device__ __forceinline__ void distill_join(DistillShared& sh, cooperative_groups::cluster_group& cluster, float& m, float& s,
-                                             float c, bool use, int streaming) {
-  const int parts = (int)cluster.num_blocks(), part = (int)cluster.block_rank();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (use && warp < streaming) {
+// The barrier of a row, in two halves: the streaming warps' sums are there and the candidates' logits have been read.
+// Without a cluster it is two named barriers of the block: the streaming warps wait for the candidates' warp at one,
+// it for them at the other, after its work in between.
+__device__ __forceinline__ void row_arrive(int parts, bool streams) {
+  __syncwarp();
+  if (parts > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  else asm volatile("bar.arrive %0, %1;" ::"r"(streams ? 2 : 3), "r"((int)blockDim.x) : "memory");
+}
+__device__ __forceinline__ void row_wait(int parts, bool streams) {
+  __syncwarp();
+  if (parts > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else asm volatile("bar.sync %0, %1;" ::"r"(streams ? 3 : 2), "r"((int)blockDim.x) : "memory");
+}
+// All warps' sums (up to 128: four a lane), joined in a fixed order; every thread gets them.
+__device__ __forceinline__ void join_sums(const DistillShared& sh, int n, float& m, float& s, float c) {
+  const int lane = threadIdx.x & 31;
+  float2 x[4];
+  m = -INFINITY;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-      join(m, s, m2, s2, c);
-    }
-    if (lane < parts) {
-      *cluster.map_shared_rank(&sh.m[part][warp], lane) = m;
-      *cluster.map_shared_rank(&sh.s[part][warp], lane) = s;
-    }
+  for (int i = 0; i < 4; ++i) {
+    x[i] = lane + 32 * i < n ? sh.sums[lane + 32 * i] : make_float2(-INFINITY, 0.f);
+    m = max_nan(m, x[i].x);
   }
-  if (parts > 1) cluster.sync();
-  else __syncthreads();
-  if (use) {
-    m = -INFINITY;
-    s = 0.f;
-    for (int i = lane; i < parts * streaming; i += 32) join(m, s, sh.m[i / streaming][i % streaming], sh.s[i / streaming][i % streaming], c);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-      join(m, s, m2, s2, c);
-    }
-  }
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const Shift at(m, c);
+  s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s += x[i].x == m ? x[i].y : x[i].y * ex2(at(x[i].x, c));
+  s = warp_sum(s);
 }
 
 // The row's loss, by one warp: log q = ln 2 (z c - k) - ln S.
@@ -281,9 +331,6 @@ __device__ __forceinline__ void distill_patch(const DistillArgs& a, const Distil
   }
 }
 
-// The candidates' gradients come after the streaming warps' stores: one barrier of the whole block, in both roles.
-__device__ __forceinline__ void dense_done() { asm volatile("bar.sync 1, %0;" ::"r"((int)blockDim.x) : "memory"); }
-
 // One logit into a thread's running (maximum, sum).
 __device__ __forceinline__ void distill_take(float& m, float& s, float v, float c) {
   const float M = max_nan(m, v);
@@ -294,31 +341,26 @@ __device__ __forceinline__ void distill_take(float& m, float& s, float v, float 
   }
   if (m != -INFINITY) s += ex2(at(v, c));
 }
-// 2^(z c - k) of a vector, in pairs.  A sum flushes what lies 2^-126 below its largest term; a gradient (which a
-// large weight may scale up) takes the slower form for a vector that has such a value.
-template <int N, bool KEEP>
+// 2^(z c - k) of a vector, in pairs; FAR and KEEP are the rare forms (Shift, ex2).
+template <int N, bool FAR, bool KEEP>
 __device__ __forceinline__ void distill_powers(float (&f)[N], const Shift& at, float c) {
   const f2 b = f2_of(-at.b, -at.b), c2 = f2_of(c, c), k = f2_of(-at.k, -at.k);
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
-    const float2 x = f2_get(fma2(add2(f2_of(f[i], f[i + 1]), b), c2, k));
-    f[i] = x.x;
-    f[i + 1] = x.y;
+    f2 z = f2_of(f[i], f[i + 1]);
+    if (FAR) z = add2(z, b);
+    const float2 x = f2_get(fma2(z, c2, k));
+    f[i] = KEEP ? ex2(x.x) : ex2_flush(x.x);
+    f[i + 1] = KEEP ? ex2(x.y) : ex2_flush(x.y);
   }
-  bool low = false;
-  if (KEEP) {
-    float least = f[0];
+}
+template <int N>
+__device__ __forceinline__ f2 distill_sum(f2 e, float (&f)[N], const Shift& at, float c) {
+  if (at.b != 0.f) distill_powers<N, true, false>(f, at, c);
+  else distill_powers<N, false, false>(f, at, c);
 #pragma unroll
-    for (int i = 1; i < N; ++i) least = fminf(least, f[i]);
-    low = least < -126.f;
-  }
-  if (low) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = ex2(f[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = ex2_flush(f[i]);
-  }
+  for (int i = 0; i < N; i += 2) e = add2(e, f2_of(f[i], f[i + 1]));
+  return e;
 }
 template <typename T>
 __device__ __forceinline__ void distill_take(float& m, float& s, float (&f)[LogitVec<T>::N], float c) {
@@ -331,19 +373,15 @@ __device__ __forceinline__ void distill_take(float& m, float& s, float (&f)[Logi
     s *= ex2(at(m, c));
     m = M;
   }
-  if (m != -INFINITY) {
-    distill_powers<N, false>(f, at, c);
-    f2 e = f2_of(f[0], f[1]);
-#pragma unroll
-    for (int i = 2; i < N; i += 2) e = add2(e, f2_of(f[i], f[i + 1]));
-    s += sum2(e);
-  }
+  if (m != -INFINITY) s += sum2(distill_sum<N>(0, f, at, c));
 }
-// scale 2^(z c - k) of a vector.
+// g 2^(z c - k) of a vector.  A power below 2^-126 is flushed, unless a large factor might bring it back (`rare`: or
+// the shift is of the other form).
 template <typename T>
-__device__ __forceinline__ void distill_dense(float (&f)[LogitVec<T>::N], const Shift& at, float c, float g) {
+__device__ __forceinline__ void distill_dense(float (&f)[LogitVec<T>::N], const Shift& at, float c, float g, bool rare) {
   constexpr int N = LogitVec<T>::N;
-  distill_powers<N, true>(f, at, c);
+  if (rare) distill_powers<N, true, true>(f, at, c);
+  else distill_powers<N, false, false>(f, at, c);
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
     const float2 x = f2_get(mul2(f2_of(f[i], f[i + 1]), f2_of(g, g)));
@@ -351,176 +389,74 @@ __device__ __forceinline__ void distill_dense(float (&f)[LogitVec<T>::N], const 
     f[i + 1] = x.y;
   }
 }
-
-// ------------------------------------------------------------- rows in registers: NV vectors a thread
+// The streaming warps' logits of a row's part: NV vectors a thread in registers, or (NV = 0, longer rows) read twice.
 template <typename T, int NV>
-__global__ void __launch_bounds__(DISTILL_THREADS + 32, 2) distill_kernel(DistillArgs a) {
-  namespace cg = cooperative_groups;
+struct Part {
+  uint4 w[NV > 0 ? NV : 1];
+  float one;                            // the thread's single element
+  int at;
   using V = LogitVec<T>;
-  __shared__ DistillShared sh;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int parts = (int)cluster.num_blocks(), part = (int)cluster.block_rank();
-  const int64_t row = blockIdx.x / parts;
-  const int tid = threadIdx.x, threads = blockDim.x - 32;      // the last warp: candidates
-  const bool streams = tid < threads;
-  const T* z = reinterpret_cast<const T*>(a.z) + row * a.ldz;
-  T* dz = reinterpret_cast<T*>(a.dz) + row * a.lddz;
-  const float weight = a.weight ? a.weight[row] : 1.0f;
-  const float c = LOG2E / a.tau;
-  const Slice sl(z, (int)a.vocab, parts, part);
-  const bool reads = weight != 0.0f;
-
+  static constexpr int U = 4;           // NV = 0: vectors in flight
   // what lies past the part's end counts as -infinity
-  uint4 w[NV];
-  constexpr uint32_t NONE = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
-  float one = -INFINITY;
-  const int at = streams ? sl.single(tid) : -1;
-  if (reads && streams) {
+  __device__ __forceinline__ void load(const T* z, const Slice& sl, int tid, int threads) {
+    constexpr uint32_t NONE = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
     const uint4* zv = reinterpret_cast<const uint4*>(z + sl.body);
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       w[u] = make_uint4(NONE, NONE, NONE, NONE);
       if (tid + u * threads < sl.nvec) w[u] = zv[tid + u * threads];
     }
-    if (at >= 0) one = as_float(z[at]);
+    one = at >= 0 ? as_float(z[at]) : -INFINITY;
   }
-  if (reads && !streams) distill_candidates(a, sh, row, z, sl, part == 0);
-  float m = one, s = 0.f;
-  if (reads && streams) {
+  __device__ __forceinline__ void sums(const T* z, const Slice& sl, int tid, int threads, float c, float& m, float& s) {
+    m = one;
+    s = 0.f;
+    if constexpr (NV > 0) {
+      m = max_nan(m, V::template largest<NV>(w));
+      if (m != -INFINITY) {
+        const Shift mine(m, c);
+        f2 e2 = f2_of(ex2(mine(one, c)), 0.f);
 #pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      float f[V::N];
-      V::unpack(w[u], f);
-#pragma unroll
-      for (int e = 0; e < V::N; e += 2) m = max3_nan(m, f[e], f[e + 1]);
-    }
-    if (m != -INFINITY) {
-      const Shift mine(m, c);
-      f2 e2 = f2_of(ex2(mine(one, c)), 0.f);
-#pragma unroll
-      for (int u = 0; u < NV; ++u) {
-        float f[V::N];
-        V::unpack(w[u], f);
-        distill_powers<V::N, false>(f, mine, c);
-#pragma unroll
-        for (int e = 0; e < V::N; e += 2) e2 = add2(e2, f2_of(f[e], f[e + 1]));
-      }
-      s = sum2(e2);
-    }
-  }
-  distill_join(sh, cluster, m, s, c, reads, threads >> 5);
-  const Shift shift(m, c);
-  const bool teaches = reads && sh.most != -INFINITY;
-  if (!streams) {
-    if (part == 0) distill_loss(a, sh, row, weight, c, shift, s, teaches);
-    if (!a.dz) return;
-    if (teaches) distill_unite(a, sh, sl);
-    dense_done();
-    if (teaches) distill_patch(a, sh, sl, reinterpret_cast<T*>(a.dz) + row * a.lddz, weight * a.tau, c, shift, s);
-    return;
-  }
-  if (!a.dz) return;
-
-  const float scale = weight * a.tau;
-  const float g = teaches ? scale / s : 0.f;
-  if (at >= 0) set_float(dz + at, teaches ? g * ex2(shift(one, c)) : 0.f);
-  const bool aligned = (reinterpret_cast<uintptr_t>(dz + sl.body) & 15) == 0;
-#pragma unroll
-  for (int u = 0; u < NV; ++u) {
-    const int i = tid + u * threads;
-    if (i >= sl.nvec) break;
-    float f[V::N];
-    if (teaches) {
-      V::unpack(w[u], f);
-      distill_dense<T>(f, shift, c, g);
-    } else {
-#pragma unroll
-      for (int e = 0; e < V::N; ++e) f[e] = 0.f;
-    }
-    if (aligned) {
-      reinterpret_cast<uint4*>(dz + sl.body)[i] = V::pack(f);
-    } else {
-#pragma unroll
-      for (int e = 0; e < V::N; ++e) set_float(dz + sl.body + i * V::N + e, f[e]);
-    }
-  }
-  dense_done();
-}
-
-// ------------------------------------------------------------- longer rows, read twice
-template <typename T>
-__global__ void __launch_bounds__(DISTILL_THREADS + 32) distill_long_kernel(DistillArgs a) {
-  namespace cg = cooperative_groups;
-  using V = LogitVec<T>;
-  constexpr int U = 4;              // vectors in flight a thread
-  __shared__ DistillShared sh;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int parts = (int)cluster.num_blocks(), part = (int)cluster.block_rank();
-  const int64_t row = blockIdx.x / parts;
-  const int tid = threadIdx.x, threads = blockDim.x - 32;      // the last warp: candidates
-  const bool streams = tid < threads;
-  const T* z = reinterpret_cast<const T*>(a.z) + row * a.ldz;
-  T* dz = reinterpret_cast<T*>(a.dz) + row * a.lddz;
-  const float weight = a.weight ? a.weight[row] : 1.0f;
-  const float c = LOG2E / a.tau;
-  const Slice sl(z, (int)a.vocab, parts, part);
-  const bool reads = weight != 0.0f;
-  const uint4* zv = reinterpret_cast<const uint4*>(z + sl.body);
-  const int at = streams ? sl.single(tid) : -1;
-
-  if (reads && !streams) distill_candidates(a, sh, row, z, sl, part == 0);
-  float m = -INFINITY, s = 0.f;
-  if (reads && streams) {
-    if (at >= 0) distill_take(m, s, as_float(z[at]), c);
-    for (int i0 = tid; i0 < sl.nvec; i0 += U * threads) {
-      uint4 w[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i0 + u * threads < sl.nvec) w[u] = zv[i0 + u * threads];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (i0 + u * threads < sl.nvec) {
+        for (int u = 0; u < NV; ++u) {
           float f[V::N];
           V::unpack(w[u], f);
-          distill_take<T>(m, s, f, c);
+          e2 = distill_sum<V::N>(e2, f, mine, c);
+        }
+        s = sum2(e2);
+      }
+    } else {
+      if (m != -INFINITY) s = 1.f;
+      const uint4* zv = reinterpret_cast<const uint4*>(z + sl.body);
+      for (int i0 = tid; i0 < sl.nvec; i0 += U * threads) {
+        uint4 x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i0 + u * threads < sl.nvec) x[u] = zv[i0 + u * threads];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (i0 + u * threads < sl.nvec) {
+            float f[V::N];
+            V::unpack(x[u], f);
+            distill_take<T>(m, s, f, c);
+          }
         }
       }
     }
   }
-  distill_join(sh, cluster, m, s, c, reads, threads >> 5);
-  const Shift shift(m, c);
-  const bool teaches = reads && sh.most != -INFINITY;
-  if (!streams) {
-    if (part == 0) distill_loss(a, sh, row, weight, c, shift, s, teaches);
-    if (!a.dz) return;
-    if (teaches) distill_unite(a, sh, sl);
-    dense_done();
-    if (teaches) distill_patch(a, sh, sl, reinterpret_cast<T*>(a.dz) + row * a.lddz, weight * a.tau, c, shift, s);
-    return;
-  }
-  if (!a.dz) return;
-
-  const float scale = weight * a.tau;
-  const float g = teaches ? scale / s : 0.f;
-  if (at >= 0) set_float(dz + at, teaches ? g * ex2(shift(as_float(z[at]), c)) : 0.f);
-  const bool aligned = (reinterpret_cast<uintptr_t>(dz + sl.body) & 15) == 0;
-  for (int i0 = tid; i0 < sl.nvec; i0 += U * threads) {
-    uint4 w[U];
-    if (teaches) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (i0 + u * threads < sl.nvec) w[u] = zv[i0 + u * threads];
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * threads;
-      if (i >= sl.nvec) break;
+  // the gradient of the part, or zeros (`g` 0 and nothing read)
+  __device__ __forceinline__ void store(const T* z, T* dz, const Slice& sl, int tid, int threads, bool teaches, const Shift& shift,
+                                        float c, float g) {
+    const bool rare = shift.b != 0.f || fabsf(g) > 1e6f;
+    const bool aligned = (reinterpret_cast<uintptr_t>(dz + sl.body) & 15) == 0;
+    if (at >= 0) set_float(dz + at, teaches ? g * ex2(shift(one, c)) : 0.f);
+    auto vec = [&](int i, const uint4& x) {
       float f[V::N];
-#pragma unroll
-      for (int e = 0; e < V::N; ++e) f[e] = 0.f;
       if (teaches) {
-        V::unpack(w[u], f);
-        distill_dense<T>(f, shift, c, g);
+        V::unpack(x, f);
+        distill_dense<T>(f, shift, c, g, rare);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V::N; ++e) f[e] = 0.f;
       }
       if (aligned) {
         reinterpret_cast<uint4*>(dz + sl.body)[i] = V::pack(f);
@@ -528,9 +464,137 @@ __global__ void __launch_bounds__(DISTILL_THREADS + 32) distill_long_kernel(Dist
 #pragma unroll
         for (int e = 0; e < V::N; ++e) set_float(dz + sl.body + i * V::N + e, f[e]);
       }
+    };
+    if constexpr (NV > 0) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u)
+        if (tid + u * threads < sl.nvec) vec(tid + u * threads, w[u]);
+    } else {
+      const uint4* zv = reinterpret_cast<const uint4*>(z + sl.body);
+      for (int i0 = tid; i0 < sl.nvec; i0 += U * threads) {
+        uint4 x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (teaches && i0 + u * threads < sl.nvec) x[u] = zv[i0 + u * threads];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i0 + u * threads < sl.nvec) vec(i0 + u * threads, x[u]);
+      }
     }
   }
-  dense_done();
+};
+
+// A cluster takes a row.  FUSED: the block's last warp does the candidates; otherwise every warp streams, and (m, S)
+// goes to the workspace.
+template <typename T, int NV, bool FUSED>
+__global__ void __launch_bounds__(DISTILL_THREADS + (FUSED ? 32 : 0), 2) distill_kernel(DistillArgs a) {
+  namespace cg = cooperative_groups;
+  extern __shared__ __align__(16) uint8_t distill_smem[];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int parts = (int)cluster.num_blocks(), part = (int)cluster.block_rank();
+  const int tid = threadIdx.x, threads = FUSED ? blockDim.x - 32 : blockDim.x, streaming = threads >> 5;
+  const int warp = tid >> 5, lane = tid & 31;
+  const int64_t row = blockIdx.x / parts;
+  const DistillShared sh(distill_smem, a.top, parts * streaming);
+  const float c = LOG2E / a.tau;
+  const float weight = a.weight ? a.weight[row] : 1.0f;
+  const bool reads = weight != 0.0f;    // uniform over the cluster
+  const T* z = reinterpret_cast<const T*>(a.z) + row * a.ldz;
+  T* dz = reinterpret_cast<T*>(a.dz) + row * a.lddz;
+  const Slice sl(z, (int)a.vocab, parts, part);
+  float m, s;
+
+  if (!FUSED || tid < threads) {
+    // ------------------------------------------------ logits
+    Part<T, NV> x;
+    x.at = sl.single(tid);
+    Shift shift(0.f, c);
+    bool teaches = false;
+    if (reads) {
+      x.load(z, sl, tid, threads);
+      x.sums(z, sl, tid, threads, c, m, s);
+      join_warp(m, s, c);
+      if (lane < parts) *cluster.map_shared_rank(&sh.sums[part * streaming + warp], lane) = make_float2(m, s);
+      if (FUSED || parts > 1) {
+        row_arrive(parts, true);
+        row_wait(parts, true);
+      } else {
+        __syncthreads();
+      }
+      join_sums(sh, parts * streaming, m, s, c);
+      shift = Shift(m, c);
+      teaches = !FUSED || *sh.most != -INFINITY;
+      if (!FUSED && part == 0 && tid == 0) a.stats[row] = make_float2(m, s);
+    }
+    if (a.dz) {
+      x.store(z, dz, sl, tid, threads, teaches, shift, c, teaches ? weight * a.tau / s : 0.f);
+      if (FUSED && reads) {
+        __syncwarp();
+        asm volatile("bar.arrive 1, %0;" ::"r"((int)blockDim.x) : "memory");   // the candidates' gradients come after these
+      }
+    }
+  } else if (reads) {
+    // ------------------------------------------------ candidates
+    distill_gather(a, sh, row, z, sl, part == 0);
+    row_arrive(parts, false);
+    distill_teacher(a, sh);
+    const bool teaches = *sh.most != -INFINITY;
+    row_wait(parts, false);
+    join_sums(sh, parts * streaming, m, s, c);
+    const Shift shift(m, c);
+    if (part == 0) distill_loss(a, sh, row, weight, c, shift, s, teaches);
+    if (a.dz) {
+      if (teaches) distill_unite(a, sh, sl);
+      __syncwarp();
+      asm volatile("bar.sync 1, %0;" ::"r"((int)blockDim.x) : "memory");
+      if (teaches) distill_patch(a, sh, sl, dz, weight * a.tau, c, shift, s);
+    }
+  } else if (part == 0 && lane == 0) {
+    a.loss[row] = 0.0f;
+  }
+}
+
+// Many rows in place: the candidates' logits, before they are overwritten.
+template <typename T>
+__global__ void __launch_bounds__(256) distill_keep_kernel(DistillArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.rows * a.top) return;
+  const int64_t row = i / a.top, j = i % a.top;
+  const int64_t id = a.ids64 ? reinterpret_cast<const int64_t*>(a.ids)[row * a.ldi + j]
+                             : (int64_t) reinterpret_cast<const int32_t*>(a.ids)[row * a.ldi + j];
+  a.kept[i] = id >= 0 && id < a.vocab ? as_float((reinterpret_cast<const T*>(a.z) + row * a.ldz)[id]) : 0.f;
+}
+
+// Many rows: a warp does the loss and the candidates' gradients of a row, after distill_kernel.
+template <typename T>
+__global__ void distill_candidates_kernel(DistillArgs a) {
+  extern __shared__ __align__(16) uint8_t distill_smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
+  if (row >= a.rows) return;
+  const DistillShared sh(distill_smem + warp * DistillShared::bytes(a.top, 0), a.top, 0);
+  const float weight = a.weight ? a.weight[row] : 1.0f;
+  if (weight == 0.0f) {
+    if (lane == 0) a.loss[row] = 0.0f;
+    return;
+  }
+  const T* z = reinterpret_cast<const T*>(a.z) + row * a.ldz;
+  T* dz = reinterpret_cast<T*>(a.dz) + row * a.lddz;
+  const Slice all(z, (int)a.vocab, 1, 0);
+  const float c = LOG2E / a.tau;
+  const float2 st = a.stats[row];
+  distill_gather(a, sh, row, z, all, true);
+  distill_teacher(a, sh);
+  const bool teaches = *sh.most != -INFINITY;
+  const Shift shift(st.x, c);
+  distill_loss(a, sh, row, weight, c, shift, st.y, teaches);
+  if (!a.dz) return;
+  if (teaches) {
+    distill_unite(a, sh, all);
+    distill_patch(a, sh, all, dz, weight * a.tau, c, shift, st.y);
+  } else {                              // nothing is taught: the gradient of the softmax alone is taken back
+    for (int64_t i = lane; i < a.vocab; i += 32) set_float(dz + i, 0.f);
+  }
 }
 
 }  // namespace precond

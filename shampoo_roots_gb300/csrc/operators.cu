@@ -150,6 +150,30 @@ cudaError_t launch_grad(const RmsGradArgs& a, const RowShape& s, unsigned grid, 
   }
 }
 
+// ------------------------------------------------------------------------- distillation
+// Blocks of a row: as many as hold it in registers, and more where rows are few, each with at least 8192 logits.
+int distill_parts(int64_t rows, int64_t vocab, int dtype) {
+  const int64_t sz = (int64_t)size_of(dtype), capacity = 8 * DISTILL_THREADS * 16 / sz;
+  int parts = 1;
+  while (parts < 8 && (((vocab + parts - 1) / parts + 63) / 64 * 64 > capacity ||
+                       (rows * parts < 2 * PLAN_SMS && vocab / (parts * 2) >= 8192)))
+    parts *= 2;
+  return parts;
+}
+// Whether the candidates have a kernel of their own: from four blocks' work a SM on, the blocks stay for them.
+bool distill_split(int64_t rows, int64_t vocab, int dtype) { return rows * distill_parts(rows, vocab, dtype) >= 4 * PLAN_SMS; }
+typedef void (*DistillKernel)(DistillArgs);
+const DistillKernel distill_fused_kernels[2][5] = {
+    {distill_kernel<float, 0, true>, distill_kernel<float, 1, true>, distill_kernel<float, 2, true>, distill_kernel<float, 4, true>,
+     distill_kernel<float, 8, true>},
+    {distill_kernel<__nv_bfloat16, 0, true>, distill_kernel<__nv_bfloat16, 1, true>, distill_kernel<__nv_bfloat16, 2, true>,
+     distill_kernel<__nv_bfloat16, 4, true>, distill_kernel<__nv_bfloat16, 8, true>}};
+const DistillKernel distill_split_kernels[2][5] = {
+    {distill_kernel<float, 0, false>, distill_kernel<float, 1, false>, distill_kernel<float, 2, false>,
+     distill_kernel<float, 4, false>, distill_kernel<float, 8, false>},
+    {distill_kernel<__nv_bfloat16, 0, false>, distill_kernel<__nv_bfloat16, 1, false>, distill_kernel<__nv_bfloat16, 2, false>,
+     distill_kernel<__nv_bfloat16, 4, false>, distill_kernel<__nv_bfloat16, 8, false>}};
+
 // ------------------------------------------------------------------------- product
 int encode8(Handle* h, CUtensorMap* map, const void* q, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
@@ -426,9 +450,16 @@ int precond_gemm8_status(precond_t ph, void* stream) {
   return word ? PRECOND_ECUDA : PRECOND_OK;
 }
 
+int64_t precond_distill_workspace(int64_t rows, int64_t vocab, int top, int dtype, int in_place) {
+  if (!side(rows) || !side(vocab) || vocab < 1 || top < 1 || top > DISTILL_MAX_TOP || !float_type(dtype)) return -1;
+  if (!distill_split(rows, vocab, dtype)) return 0;
+  return rows * 8 + (in_place ? rows * top * 4 : 0);
+}
+
 int precond_distill(precond_t ph, const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ldz, const void* ids,
                     int id_bits, int64_t ldi, const void* teacher, int teacher_dtype, int64_t ldt, int top,
-                    const float* weight, float temperature, float* loss, void* dlogits, int64_t lddz, void* stream) {
+                    const float* weight, float temperature, float* loss, void* dlogits, int64_t lddz, void* workspace,
+                    int64_t workspace_bytes, void* stream) {
   Handle* h = as_handle(ph);
   if (!h || !float_type(dtype) || !float_type(teacher_dtype) || !side(rows) || !side(vocab) || vocab < 1) return PRECOND_EINVAL;
   if ((id_bits != 32 && id_bits != 64) || top < 1 || top > DISTILL_MAX_TOP || !(temperature > 0.f) || temperature > 3e38f)
@@ -438,38 +469,50 @@ int precond_distill(precond_t ph, const void* logits, int dtype, int64_t rows, i
       !matrix(loss, 1, rows, rows, PRECOND_F32) || (dlogits && !matrix(dlogits, rows, vocab, lddz, dtype)) ||
       (weight && !aligned(weight, 4)) || ldi < top || ldi > MAX_SIDE || (rows && (!ids || !aligned(ids, id_bits / 8))))
     return PRECOND_EINVAL;
+  const int64_t need = precond_distill_workspace(rows, vocab, top, dtype, dlogits == logits);
+  if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return PRECOND_EINVAL;
   const Range in[4] = {range(logits, rows, ldz, vocab, sz), range(ids, rows, ldi, top, id_bits / 8),
                        range(teacher, rows, ldt, top, size_of(teacher_dtype)), range(weight, 1, 0, rows, 4)};
-  const Range out[2] = {range(dlogits, rows, lddz, vocab, sz), range(loss, 1, 0, rows, 4)};
-  for (int i = 0; i < 2; ++i)
+  const Range out[3] = {range(dlogits, rows, lddz, vocab, sz), range(loss, 1, 0, rows, 4), range(workspace, 1, 0, need, 1)};
+  for (int i = 0; i < 3; ++i) {
     for (int j = 0; j < 4; ++j) {
       const bool same = i == 0 && j == 0 && dlogits == logits && lddz == ldz;
       if (!same && overlap(out[i], in[j])) return PRECOND_EINVAL;
     }
-  if (overlap(out[0], out[1])) return PRECOND_EINVAL;
-  if (rows > (int64_t)INT32_MAX / 8) return PRECOND_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return PRECOND_EINVAL;
+  }
+  if (rows > (int64_t)INT32_MAX / 8 || rows * top / 256 > INT32_MAX) return PRECOND_EINVAL;
   if (h->device < 0) return PRECOND_ENODEV;
   if (rows == 0) return PRECOND_OK;
   int rc = prepare(h);
   if (rc) return rc;
+  const bool bf16 = dtype == PRECOND_BF16, split = distill_split(rows, vocab, dtype);
+  cudaStream_t st = (cudaStream_t)stream;
   DistillArgs a = {logits, ldz, ids, ldi, id_bits == 64, teacher, ldt, teacher_dtype == PRECOND_BF16, weight, loss, dlogits, lddz,
-                   rows, vocab, top, temperature};
-  // Blocks of a row: as many as hold it in registers, and more where rows are few, each with at least 8192 logits.
-  const int64_t per_vec = 16 / (int64_t)sz, capacity = 8 * DISTILL_THREADS * per_vec;
-  int parts = 1;
-  while (parts < 8 && (((vocab + parts - 1) / parts + 63) / 64 * 64 > capacity || (rows * parts < 2 * h->num_sms && vocab / (parts * 2) >= 8192)))
-    parts *= 2;
-  const int64_t vecs = ((vocab + parts - 1) / parts + 63) / 64 * 64 / per_vec;
-  const int nv = vecs <= DISTILL_THREADS ? 1 : vecs <= 2 * DISTILL_THREADS ? 2 : vecs <= 4 * DISTILL_THREADS ? 4 : vecs <= 8 * DISTILL_THREADS ? 8 : 0;
+                   rows, vocab, top, temperature, (float2*)workspace, nullptr};
+  const int parts = distill_parts(rows, vocab, dtype);
+  const int64_t vecs = ((vocab + parts - 1) / parts + 63) / 64 * 64 * (int64_t)sz / 16;
+  const int i = vecs <= DISTILL_THREADS ? 1 : vecs <= 2 * DISTILL_THREADS ? 2 : vecs <= 4 * DISTILL_THREADS ? 3 : vecs <= 8 * DISTILL_THREADS ? 4 : 0;
+  const int nv = i ? 1 << (i - 1) : 0;
   const int threads = nv == 0 ? DISTILL_THREADS : (int)std::max<int64_t>(64, ((vecs + nv - 1) / nv + 31) / 32 * 32);
-  const bool bf16 = dtype == PRECOND_BF16;
-  auto k = nv == 1 ? (bf16 ? distill_kernel<__nv_bfloat16, 1> : distill_kernel<float, 1>)
-           : nv == 2 ? (bf16 ? distill_kernel<__nv_bfloat16, 2> : distill_kernel<float, 2>)
-           : nv == 4 ? (bf16 ? distill_kernel<__nv_bfloat16, 4> : distill_kernel<float, 4>)
-           : nv == 8 ? (bf16 ? distill_kernel<__nv_bfloat16, 8> : distill_kernel<float, 8>)
-                     : (bf16 ? distill_long_kernel<__nv_bfloat16> : distill_long_kernel<float>);
-  OP_CK(launch(k, dim3((unsigned)(rows * parts)), dim3(threads + 32), 0, (cudaStream_t)stream, parts, a));
+  if (split && dlogits == logits) {
+    a.kept = (float*)((char*)workspace + rows * 8);
+    OP_CK(launch(bf16 ? distill_keep_kernel<__nv_bfloat16> : distill_keep_kernel<float>, dim3((unsigned)((rows * top + 255) / 256)),
+                 dim3(256), 0, st, 1, a));
+    ++h->launches;
+  }
+  const int sums = parts * threads / 32;
+  OP_CK(launch((split ? distill_split_kernels : distill_fused_kernels)[bf16][i], dim3((unsigned)(rows * parts)),
+               dim3(threads + (split ? 0 : 32)), split ? sums * 8 : DistillShared::bytes(top, sums), st, parts, a));
   ++h->launches;
+  if (split) {
+    // a warp a row, eight to a block where their candidates fit
+    const int each = DistillShared::bytes(top, 0), warps = std::max(1, std::min(8, (48 << 10) / each));
+    OP_CK(launch(bf16 ? distill_candidates_kernel<__nv_bfloat16> : distill_candidates_kernel<float>,
+                 dim3((unsigned)((rows + warps - 1) / warps)), dim3(32 * warps), (size_t)each * warps, st, 1, a));
+    ++h->launches;
+  }
   return PRECOND_OK;
 }
 

@@ -19,7 +19,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import HERE, OK, _check, _stream, load
+from . import BF16, F32, HERE, OK, _check, _stream, load
 
 BLOCK_ROW, BLOCK_TILE = 0, 1
 E4M3 = 2
@@ -41,7 +41,7 @@ def _load_binding():
     m.set_up((torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.uint8, torch.int32, torch.int64),
              torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else _current_stream,
              tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (
-                 L.precond_rms_norm, L.precond_rms_norm_grad, L.precond_quantize8, L.precond_gemm8, L.precond_distill)))
+                 L.precond_rms_norm, L.precond_rms_norm_grad, L.precond_quantize8, L.precond_gemm8, L.precond_distill, L.precond_distill_workspace)))
     return m
 
 
@@ -122,9 +122,23 @@ def precond_gemm8_status(h, stream=None, raw: bool = False) -> int:
     return code if raw or code == OK else _check(code, "precond_gemm8_status")
 
 
-def precond_distill(h, logits, ids, teacher, loss, weight=None, temperature: float = 1.0, dlogits=None, stream=None,
-                    raw: bool = False) -> int:
+def precond_distill_workspace(rows: int, vocab: int, top: int, dtype: torch.dtype, in_place: bool = False) -> int:
+    """Bytes of workspace of precond_distill."""
+    L = load()
+    L.precond_distill_workspace.restype = ctypes.c_int64
+    L.precond_distill_workspace.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int]
+    return L.precond_distill_workspace(rows, vocab, top, F32 if dtype == torch.float32 else BF16, int(in_place))
+
+
+def precond_distill(h, logits, ids, teacher, loss, weight=None, temperature: float = 1.0, dlogits=None, workspace=None,
+                    stream=None, raw: bool = False) -> int:
     """loss of every row against the teacher's top logits (``teacher`` at the vocabulary places ``ids``) and,
-    with ``dlogits``, its gradient (in place if it is ``logits``)."""
-    code = _b.distill(h, logits, ids, teacher, loss, weight, temperature, dlogits, stream)
+    with ``dlogits``, its gradient (in place if it is ``logits``).  Without a workspace one comes from torch's
+    allocator where the call needs it (on the current stream; give one together with another ``stream``)."""
+    code = _b.distill(h, logits, ids, teacher, loss, weight, temperature, dlogits, workspace, stream)
+    if code < -1000:
+        if stream is not None and _stream(stream) != _stream(None):
+            raise ValueError("give a workspace with a stream other than torch's current one")
+        workspace = torch.empty(-1000 - code, dtype=torch.uint8, device=logits.device)
+        code = _b.distill(h, logits, ids, teacher, loss, weight, temperature, dlogits, workspace, stream)
     return code if raw or code == OK else _check(code, "precond_distill")

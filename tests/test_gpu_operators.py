@@ -398,7 +398,8 @@ def check_distill(pc, z, ids, t, w, tau, grad=True, place=None, in_place=False):
     tol = (wt * tau)[:, None] * 3 * unit[:, None] * (want.abs() / (wt * tau)[:, None].clamp(min=1e-30) + 0) + 1e-30
     cand = torch.zeros(rows, vocab, dtype=torch.float64)
     ok = (ids >= 0) & (ids < vocab)
-    cand.scatter_(1, ids.clamp(0, vocab - 1).long(), ok.double())
+    cand.scatter_add_(1, ids.clamp(0, vocab - 1).long(), ok.double())
+    cand = cand.clamp(max=1)
     tol = tol + cand * (wt * tau)[:, None] * 3 * unit[:, None]          # q - p of a candidate may cancel
     if z.dtype == torch.bfloat16:
         tol = tol + E16 * want.abs()
@@ -414,6 +415,22 @@ def test_distill(pc, rows, vocab, top, dtype):
     z, ids, t, w = distill_inputs(rows, vocab, top, dtype)
     check_distill(pc, z, ids, t, w, 2.0)
     check_distill(pc, z, ids, t, None, 0.7, grad=False)
+
+
+@pytest.mark.parametrize("rows,vocab,top", [(700, 7, 3), (650, 333, 40), (1300, 1001, 5), (80, 70001, 300), (640, 2048, 1024)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_distill_many_rows(pc, rows, vocab, top, dtype):
+    """Rows whose candidates have a kernel of their own; some without candidates, some with one id throughout, in place."""
+    top = min(top, vocab)
+    z, ids, t, w = distill_inputs(rows, vocab, top, dtype)
+    ids[5::9] = -1
+    ids[7::11] = ids[7::11, :1]
+    t[3::13] = -math.inf
+    a = check_distill(pc, z, ids, t, w, 1.5)
+    b = check_distill(pc, z, ids, t, w, 1.5, in_place=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    c = check_distill(pc, z, ids, t, w, 1.5, grad=False)
+    assert torch.equal(a[0], c[0])
 
 
 def test_distill_types_and_places(pc):
@@ -462,6 +479,27 @@ def test_distill_masks(pc, vocab):
     w[14], w[15] = 1e-20, 1e20
     check_distill(pc, z, ids, t, w, 1.0)
     check_distill(pc, z, ids, t, w, 0.25)
+
+
+def test_distill_masks_many_rows(pc):
+    """The same kinds of rows, a hundred times each."""
+    low = torch.finfo(torch.float32).min
+    z, ids, t, w = distill_inputs(1100, 120, 12, "f32", masked=False)
+    ids[0::11] = -1
+    t[1::11] = -math.inf
+    ids[2::11] = ids[2::11, :1]
+    ids[3::11, 0], ids[3::11, 1] = 120, 2 ** 31 - 1
+    z[4::11, 60:] = -math.inf
+    ids[4::11] = torch.arange(12, dtype=torch.int32)
+    z[5::11] = low
+    z[6::11] = math.nan
+    w[6::11] = 0
+    z[7::11] = 1e30
+    z[8::11, 1:] = low
+    ids[8::11] = torch.arange(12, dtype=torch.int32)
+    t[8::11, 1:] = -math.inf
+    check_distill(pc, z, ids, t, w, 1.0)
+    check_distill(pc, z, ids, t, w, 0.25, in_place=True)
 
 
 def test_distill_unlikely_candidate(pc):
