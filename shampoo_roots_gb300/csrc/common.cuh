@@ -82,6 +82,12 @@ __device__ T block_sum(T v) {
   return r;
 }
 
+// Programmatic launches (the operators): a kernel may be scheduled while its predecessor in the stream still runs,
+// once every block of that one has called let_next_start(), and reads or writes no global memory before
+// wait_for_previous(), which returns when the predecessor has completed.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ float load_grad(const void* g, int dtype, long long idx) {
   if (dtype == PRECOND_BF16)
     return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(g)[idx]);

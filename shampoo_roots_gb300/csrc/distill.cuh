@@ -497,6 +497,8 @@ __global__ void __launch_bounds__(DISTILL_THREADS + (FUSED ? 32 : 0), 2) distill
   const int64_t row = blockIdx.x / parts;
   const DistillShared sh(distill_smem, a.top, parts * streaming);
   const float c = LOG2E / a.tau;
+  wait_for_previous();
+  let_next_start();
   const float weight = a.weight ? a.weight[row] : 1.0f;
   const bool reads = weight != 0.0f;    // uniform over the cluster
   const T* z = reinterpret_cast<const T*>(a.z) + row * a.ldz;
@@ -557,6 +559,8 @@ __global__ void __launch_bounds__(DISTILL_THREADS + (FUSED ? 32 : 0), 2) distill
 // Many rows in place: the candidates' logits, before they are overwritten.
 template <typename T>
 __global__ void __launch_bounds__(256) distill_keep_kernel(DistillArgs a) {
+  wait_for_previous();
+  let_next_start();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= a.rows * a.top) return;
   const int64_t row = i / a.top, j = i % a.top;
@@ -571,6 +575,8 @@ __global__ void distill_candidates_kernel(DistillArgs a) {
   extern __shared__ __align__(16) uint8_t distill_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
+  wait_for_previous();
+  let_next_start();
   if (row >= a.rows) return;
   const DistillShared sh(distill_smem + warp * DistillShared::bytes(a.top, 0), a.top, 0);
   const float weight = a.weight ? a.weight[row] : 1.0f;

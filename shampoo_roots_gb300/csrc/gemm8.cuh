@@ -268,6 +268,8 @@ gemm8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_for_previous();
+  let_next_start();
 
   const int64_t tiles_m = (g.M + G8_BM - 1) / G8_BM, tiles_n = (g.N + BN - 1) / BN;
   const int64_t tiles = tiles_m * tiles_n;
@@ -572,6 +574,8 @@ gemm8_pair_kernel(const __grid_constant__ PairMaps maps, Gemm8Args g) {
   cluster.sync();                                    // the peer's barriers are ready
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  wait_for_previous();
+  let_next_start();
   uint32_t to_leader;                                // from a barrier to the leader's
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to_leader) : "r"(bars));
   to_leader -= bars;

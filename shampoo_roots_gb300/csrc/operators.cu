@@ -102,12 +102,14 @@ cudaError_t launch(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cuda
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;     // common.cuh, wait_for_previous
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
 
@@ -125,8 +127,9 @@ RowShape row_shape(int64_t cols, bool norm) {
   return {threads, std::min(8, std::max(1, 256 / threads)), nv};
 }
 
-int64_t row_blocks_of(const RowShape& s, int64_t rows, int sms) {
-  const int64_t resident = std::max(1, 1024 / (s.threads * s.rows));
+// Blocks of a persistent grid: 1024 threads an SM (norm: 80 registers a thread), 512 (gradient: 128).
+int64_t row_blocks_of(const RowShape& s, int64_t rows, int sms, bool norm) {
+  const int64_t resident = std::max(1, (norm ? 1024 : 512) / (s.threads * s.rows));
   return std::max<int64_t>(1, std::min((rows + s.rows - 1) / s.rows, resident * sms));
 }
 
@@ -143,7 +146,8 @@ cudaError_t launch_norm(const RmsNormArgs& a, const RowShape& s, unsigned grid, 
 template <typename T, bool VEC>
 cudaError_t launch_grad(const RmsGradArgs& a, const RowShape& s, unsigned grid, cudaStream_t st) {
   const dim3 block(s.threads, s.rows);
-  const size_t smem = VEC ? 0 : (size_t)s.threads * s.rows * 16 * sizeof(T);    // the warps' exchange buffers
+  // the warps' exchange buffers, and then the dw sums of the rows side by side
+  const size_t smem = std::max<size_t>(VEC ? 0 : (size_t)s.threads * s.rows * 16 * sizeof(T), s.rows > 1 ? (size_t)s.threads * s.rows * 64 : 0);
   switch (s.nv) {
     case 1: return launch(rms_grad_kernel<T, 1, VEC>, dim3(grid), block, smem, st, 1, a);
     default: return launch(rms_grad_long_kernel<T, VEC>, dim3(grid), block, smem, st, 1, a);
@@ -264,7 +268,7 @@ int precond_rms_norm(precond_t ph, const void* x, const void* residual, const vo
   RmsNormArgs a = {x, residual, weight, total, y, (uint8_t*)q, scale, rstd, ldx, ldr, ldt, ldy, ldq, (int)rows, (int)cols, eps,
                    weight_dtype == PRECOND_BF16};
   const RowShape s = row_shape(cols, true);
-  const unsigned grid = (unsigned)row_blocks_of(s, q ? q8_row_blocks(rows) * 128 : rows, h->num_sms);
+  const unsigned grid = (unsigned)row_blocks_of(s, q ? q8_row_blocks(rows) * 128 : rows, h->num_sms, true);
   const bool vec = sector_rows(x, ldx, dtype) && sector_rows(residual, ldr, dtype) && sector_rows(total, ldt, dtype) &&
                    sector_rows(y, ldy, dtype);
   cudaStream_t st = (cudaStream_t)stream;
@@ -280,7 +284,7 @@ int64_t precond_rms_norm_grad_workspace(int64_t rows, int64_t cols) {
   if (!side(rows) || !side(cols)) return -1;
   if (rows == 0 || cols == 0) return 0;
   const RowShape s = row_shape(cols, false);
-  return row_blocks_of(s, rows, PLAN_SMS) * s.rows * cols * 4;
+  return row_blocks_of(s, rows, PLAN_SMS, false) * cols * 4;
 }
 
 int precond_rms_norm_grad(precond_t ph, const void* dy, const void* x, const void* weight, const float* rstd,
@@ -322,7 +326,7 @@ int precond_rms_norm_grad(precond_t ph, const void* dy, const void* x, const voi
   RmsGradArgs a = {dy, x, dresidual, weight, rstd, dx, (float*)workspace, lddy, ldx, lddr, lddx, (int)rows, (int)cols,
                    weight_dtype == PRECOND_BF16};
   const RowShape s = row_shape(cols, false);
-  const unsigned grid = (unsigned)row_blocks_of(s, rows, std::min(h->num_sms, PLAN_SMS));
+  const unsigned grid = (unsigned)row_blocks_of(s, rows, std::min(h->num_sms, PLAN_SMS), false);
   const bool vec = sector_rows(dy, lddy, dtype) && sector_rows(x, ldx, dtype) && sector_rows(dresidual, lddr, dtype) &&
                    sector_rows(dx, lddx, dtype);
   if (dtype == PRECOND_BF16)
@@ -330,7 +334,7 @@ int precond_rms_norm_grad(precond_t ph, const void* dy, const void* x, const voi
   else
     OP_CK((vec ? launch_grad<float, true>(a, s, grid, st) : launch_grad<float, false>(a, s, grid, st)));
   OP_CK(launch(rms_dw_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(32, 32), 0, st, 1, (const float*)workspace,
-               (int)grid * s.rows, cols, dw));
+               (int)grid, cols, dw));
   h->launches += 2;
   return PRECOND_OK;
 }
@@ -362,7 +366,7 @@ int precond_quantize8(precond_t ph, const void* x, int dtype, int64_t rows, int6
   if (rows == 0 || cols == 0) return PRECOND_OK;
   int rc = prepare(h);
   if (rc) return rc;
-  Quant8Args a = {x, ldx, x_scale, rows, cols, block == PRECOND_BLOCK_TILE, (uint8_t*)q, ldq, scale, (uint8_t*)qt, ldqt, scale_t};
+  Quant8Args a = {x, ldx, x_scale, (int)rows, (int)cols, block == PRECOND_BLOCK_TILE, (uint8_t*)q, ldq, scale, (uint8_t*)qt, ldqt, scale_t};
   // 8 columns in one load: 16 bytes of bf16, 32 of fp32
   const int64_t step = 8 * (int64_t)size_of(dtype);
   const int vec = aligned(x, step) && ldx * (int64_t)size_of(dtype) % step == 0;

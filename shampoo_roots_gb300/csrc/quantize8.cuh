@@ -24,7 +24,7 @@ enum { QIN_F32 = PRECOND_F32, QIN_BF16 = PRECOND_BF16, QIN_E4M3 = PRECOND_E4M3 }
 struct Quant8Args {
   const void* x; int64_t ldx;
   const uint8_t* x_scale;            // 8-bit input: its scales
-  int64_t rows, cols;
+  int rows, cols;
   int tile;                          // 1: one scale per 128 x 128 block
   uint8_t* q; int64_t ldq; uint8_t* s;
   uint8_t* qt; int64_t ldqt; uint8_t* st;
@@ -37,7 +37,7 @@ template <> struct QuantTile<QIN_F32> {
   __device__ __forceinline__ float get(int i, int j) const { return __uint_as_float(w[i][j]); }
   __device__ __forceinline__ void set_nan(int i, int j) { w[i][j] = 0x7FFFFFFFu; }
   static constexpr int WORDS = 8;
-  __device__ __forceinline__ void load(const Quant8Args& a, int i, int64_t row, int64_t c) {
+  __device__ __forceinline__ void load(const Quant8Args& a, int i, int64_t row, int c) {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(a.x) + row * a.ldx + c;
     if (c + 8 <= a.cols) {
       ld_sector(w[i], p);
@@ -46,7 +46,7 @@ template <> struct QuantTile<QIN_F32> {
       for (int j = 0; j < 8; ++j) w[i][j] = c + j < a.cols ? p[j] : 0;
     }
   }
-  __device__ __forceinline__ void load_stripes(const Quant8Args& a, int i, int64_t row, int64_t c0, int tx) {
+  __device__ __forceinline__ void load_stripes(const Quant8Args& a, int i, int64_t row, int c0, int tx) {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(a.x) + row * a.ldx;
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[i][j] = c0 + 16 * j + tx < a.cols ? p[c0 + 16 * j + tx] : 0;
@@ -63,11 +63,11 @@ template <> struct QuantTile<QIN_BF16> {
   }
   __device__ __forceinline__ void set_nan(int i, int j) { w[i][j >> 1] |= j & 1 ? 0x7FFF0000u : 0x7FFFu; }
   static constexpr int WORDS = 4;
-  __device__ __forceinline__ void load_stripes(const Quant8Args& a, int i, int64_t row, int64_t c0, int tx) {
+  __device__ __forceinline__ void load_stripes(const Quant8Args& a, int i, int64_t row, int c0, int tx) {
     const uint16_t* p = reinterpret_cast<const uint16_t*>(a.x) + row * a.ldx;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int64_t k = c0 + 32 * j + tx;
+      const int k = c0 + 32 * j + tx;
       const uint32_t lo = k < a.cols ? p[k] : 0, hi = k + 16 < a.cols ? p[k + 16] : 0;
       w[i][j] = lo | hi << 16;
     }
@@ -79,7 +79,7 @@ template <> struct QuantTile<QIN_BF16> {
       reinterpret_cast<uint16_t*>(xs)[32 * j + 16 + tx] = (uint16_t)(w[i][j] >> 16);
     }
   }
-  __device__ __forceinline__ void load(const Quant8Args& a, int i, int64_t row, int64_t c) {
+  __device__ __forceinline__ void load(const Quant8Args& a, int i, int64_t row, int c) {
     const uint16_t* p = reinterpret_cast<const uint16_t*>(a.x) + row * a.ldx + c;
     if (c + 8 <= a.cols) {
       asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -103,9 +103,9 @@ template <> struct QuantTile<QIN_E4M3> {
   }
   __device__ __forceinline__ void set_nan(int i, int j) {}          // e4m3's only non-finite value is NaN already
   static constexpr int WORDS = 2;
-  __device__ __forceinline__ void load_stripes(const Quant8Args&, int, int64_t, int64_t, int) {}    // its rows are aligned
+  __device__ __forceinline__ void load_stripes(const Quant8Args&, int, int64_t, int, int) {}    // its rows are aligned
   __device__ __forceinline__ void put_stripes(int, void*, int) const {}
-  __device__ __forceinline__ void load(const Quant8Args& a, int i, int64_t row, int64_t c) {
+  __device__ __forceinline__ void load(const Quant8Args& a, int i, int64_t row, int c) {
     const uint8_t* p = reinterpret_cast<const uint8_t*>(a.x) + row * a.ldx + c;   // 16-byte aligned rows, c % 8 == 0
     w[i][0] = w[i][1] = 0;
     if (c + 8 <= a.cols) {
@@ -185,9 +185,12 @@ __global__ void __launch_bounds__(256, IN == QIN_F32 ? 2 : IN == QIN_BF16 ? 4 : 
   __shared__ unsigned char cexp[128];
   __shared__ unsigned tmax[4];
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, warp = threadIdx.x >> 5;
-  const int64_t col_tiles = (a.cols + 127) >> 7, row_tiles = (a.rows + 127) >> 7;
-  const int64_t tj = blockIdx.x % col_tiles, ti = blockIdx.x / col_tiles;
-  const int64_t r0 = ti * 128 + 8 * ty, c0 = tj * 128 + 8 * tx;
+  const unsigned col_tiles = (unsigned)(a.cols + 127) >> 7, row_tiles = (unsigned)(a.rows + 127) >> 7;
+  const int ti = (int)(blockIdx.x / col_tiles), tj = (int)(blockIdx.x - ti * col_tiles);
+  const int r0 = ti * 128 + 8 * ty, c0 = tj * 128 + 8 * tx;
+  const bool whole = ti * 128 + 128 <= a.rows && tj * 128 + 128 <= a.cols;
+  wait_for_previous();
+  let_next_start();
 
   QuantTile<IN> v;
 #pragma unroll
@@ -254,9 +257,8 @@ __global__ void __launch_bounds__(256, IN == QIN_F32 ? 2 : IN == QIN_BF16 ? 4 : 
 #pragma unroll
     for (int i = 0; i < 8; ++i) rexp[i] = q8_exponent(rexp[i]);
   }
-  const bool whole = ti * 128 + 128 <= a.rows && tj * 128 + 128 <= a.cols;
   if (a.q) {
-    uint8_t* p = a.q + r0 * a.ldq + c0;
+    uint8_t* p = a.q + (int64_t)r0 * a.ldq + c0;
     uint8_t* sp = a.s + q8_scale_at(r0, (int)tj, row_tiles);          // 8 rows: 16 bytes apart
 #pragma unroll
     for (int i = 0; i < 8; ++i, p += a.ldq) {
@@ -279,9 +281,9 @@ __global__ void __launch_bounds__(256, IN == QIN_F32 ? 2 : IN == QIN_BF16 ? 4 : 
       if (tx == 0) sp[16 * i] = (uint8_t)(r0 + i < a.rows ? rexp[i] : Q8_ONE);
     }
     // the blocks of the last group past the end
-    if (tj == col_tiles - 1 && threadIdx.x < 128)
-      for (int64_t kb = col_tiles; kb < 4 * (int64_t)q8_groups(a.cols); ++kb)
-        a.s[q8_scale_at(ti * 128 + threadIdx.x, (int)kb, row_tiles)] = (uint8_t)Q8_ONE;
+    if (tj == (int)col_tiles - 1 && threadIdx.x < 128)
+      for (int kb = col_tiles; kb < 4 * q8_groups(a.cols); ++kb)
+        a.s[q8_scale_at(ti * 128 + threadIdx.x, kb, row_tiles)] = (uint8_t)Q8_ONE;
   }
   if (a.qt) {
     uint8_t* sp = a.st + q8_scale_at(c0, (int)ti, col_tiles);
@@ -300,9 +302,9 @@ __global__ void __launch_bounds__(256, IN == QIN_F32 ? 2 : IN == QIN_BF16 ? 4 : 
       *reinterpret_cast<uint2*>(tr + (8 * tx + j) * 128 + ((ty ^ tx) << 3)) = make_uint2(o[0], o[1]);
       if (ty == 0) sp[16 * j] = (uint8_t)(c0 + j < a.cols ? b : Q8_ONE);
     }
-    if (ti == row_tiles - 1 && threadIdx.x < 128)
-      for (int64_t kb = row_tiles; kb < 4 * (int64_t)q8_groups(a.rows); ++kb)
-        a.st[q8_scale_at(tj * 128 + threadIdx.x, (int)kb, col_tiles)] = (uint8_t)Q8_ONE;
+    if (ti == (int)row_tiles - 1 && threadIdx.x < 128)
+      for (int kb = row_tiles; kb < 4 * q8_groups(a.rows); ++kb)
+        a.st[q8_scale_at(tj * 128 + threadIdx.x, kb, col_tiles)] = (uint8_t)Q8_ONE;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -311,9 +313,9 @@ __global__ void __launch_bounds__(256, IN == QIN_F32 ? 2 : IN == QIN_BF16 ? 4 : 
       const int x = c >> 3;
       uint4 b = *reinterpret_cast<const uint4*>(tr + c * 128 + (((2 * p) ^ x) >> 1) * 16);
       if (x & 1) b = make_uint4(b.z, b.w, b.x, b.y);
-      const int64_t oc = ti * 128 + 16 * p, orow = tj * 128 + c;
+      const int oc = ti * 128 + 16 * p, orow = tj * 128 + c;
       if (whole || (orow < a.cols && oc < a.rows)) {
-        uint8_t* dst = a.qt + orow * a.ldqt + oc;
+        uint8_t* dst = a.qt + (int64_t)orow * a.ldqt + oc;
         if (whole || oc + 16 <= a.rows) {
           *reinterpret_cast<uint4*>(dst) = b;
         } else {

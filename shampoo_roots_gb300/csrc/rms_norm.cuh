@@ -28,7 +28,7 @@ struct RmsNormArgs {
 
 struct RmsGradArgs {
   const void* dy; const void* x; const void* dr; const void* w; const float* rstd;
-  void* dx; float* partial;           // partial: [gridDim.x * blockDim.y][cols]
+  void* dx; float* partial;           // partial: [gridDim.x][cols]
   int64_t lddy, ldx, lddr, lddx;
   int rows, cols;
   int w_bf16;
@@ -126,6 +126,8 @@ template <typename T, int NV, bool VEC>
 __global__ void __launch_bounds__(NV == 1 ? 384 : 512, NV == 1 ? 2 : 1) rms_norm_kernel(RmsNormArgs a) {
   __shared__ __align__(16) float red[2 * 8 * 32];
   zero_red(red, 2 * 8 * 32);
+  wait_for_previous();
+  let_next_start();
   void* xs = warp_scratch<T, VEC>();
   const int64_t rblocks = q8_row_blocks(a.rows);
   const int step = gridDim.x * blockDim.y;
@@ -194,6 +196,8 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(512, 2) rms_norm_long_kernel(RmsNormArgs a) {
   __shared__ __align__(16) float red[2 * 32];
   zero_red(red, 2 * 32);
+  wait_for_previous();
+  let_next_start();
   void* xs = warp_scratch<T, VEC>();
   const int64_t rblocks = q8_row_blocks(a.rows);
   const int64_t last = a.q ? rblocks * 128 : a.rows;
@@ -267,6 +271,8 @@ template <typename T, int NV, bool VEC>
 __global__ void __launch_bounds__(512, 1) rms_grad_kernel(RmsGradArgs a) {
   __shared__ __align__(16) float red[2 * 8 * 32];
   zero_red(red, 2 * 8 * 32);
+  wait_for_previous();
+  let_next_start();
   void* xs = warp_scratch<T, VEC>();
   const int step = gridDim.x * blockDim.y;
   int row = blockIdx.x * blockDim.y + threadIdx.y;
@@ -327,7 +333,18 @@ __global__ void __launch_bounds__(512, 1) rms_grad_kernel(RmsGradArgs a) {
     }
     dx += step * a.lddx;
   }
-  float* out = a.partial + ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * a.cols;
+  if (blockDim.y > 1) {                  // the block's rows side by side (NV is 1): in their order, through shared memory
+    extern __shared__ __align__(16) uint8_t row_scratch[];
+    F16* side = reinterpret_cast<F16*>(row_scratch);
+    __syncthreads();                     // the exchange buffers lie there too
+    side[threadIdx.y * blockDim.x + threadIdx.x] = dw[0];
+    __syncthreads();
+    if (threadIdx.y > 0) return;
+    for (int y = 1; y < blockDim.y; ++y)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dw[0].p[i] = add2(dw[0].p[i], side[y * blockDim.x + threadIdx.x].p[i]);
+  }
+  float* out = a.partial + (int64_t)blockIdx.x * a.cols;
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -344,6 +361,8 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(512, 1) rms_grad_long_kernel(RmsGradArgs a) {
   __shared__ __align__(16) float red[2 * 32];
   zero_red(red, 2 * 32);
+  wait_for_previous();
+  let_next_start();
   void* xs = warp_scratch<T, VEC>();
   float* out = a.partial + (int64_t)blockIdx.x * a.cols;
   const float inv_cols = 1.0f / (float)a.cols;
@@ -407,10 +426,12 @@ __global__ void __launch_bounds__(512, 1) rms_grad_long_kernel(RmsGradArgs a) {
 // column take every 32nd sum, then their results are added in order).
 __global__ void __launch_bounds__(1024) rms_dw_kernel(const float* partial, int parts, int64_t cols, float* dw) {
   __shared__ float s[32][33];
+  wait_for_previous();
+  let_next_start();
   const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
   if (c < cols) {
-#pragma unroll 4
+#pragma unroll 8
     for (int p = threadIdx.y; p < parts; p += 32) v += partial[(int64_t)p * cols + c];
   }
   s[threadIdx.y][threadIdx.x] = v;
