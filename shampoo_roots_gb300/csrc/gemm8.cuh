@@ -60,12 +60,15 @@ struct Gemm8Smem {
   static constexpr int A_BYTES = G8_BM * G8_BK;
   static constexpr int B_BYTES = BN * G8_BK;
   static constexpr int SF_BYTES = 1024;                 // 128 rows of A and of B
-  static constexpr int STAGES = BN == 128 ? 5 : BN == 64 ? 7 : 8;
+  static constexpr int CTAS = BN <= 32 ? 2 : 1;         // on an SM: few tokens need all SMs' loads, not wide tiles
+  static constexpr int STAGES = BN == 128 ? 5 : BN == 64 ? 7 : BN == 32 ? 4 : 5;
+  static constexpr int DRAIN_WARPS = BN >= 64 ? G8_EPI_WARPS : 4;      // that have columns of their own
   static constexpr int OFF_SF = STAGES * (A_BYTES + B_BYTES);
   static constexpr int OFF_XS = OFF_SF + STAGES * SF_BYTES;                 // a scratch of each drain warp
-  static constexpr int OFF_BAR = OFF_XS + G8_EPI_WARPS * 32 * G8_XS_LD * 4;
+  static constexpr int OFF_BAR = OFF_XS + DRAIN_WARPS * 32 * G8_XS_LD * 4;
   static constexpr int PART_LD = BN + 1;                                    // a stretch's sums, over the ring
   static constexpr int BYTES = 1024 + OFF_BAR + 256;
+  static_assert(CTAS * (BYTES + 1024) <= 228 * 1024, "shared memory of an SM");
   // tensor memory: two sum buffers, then two scale buffers
   static constexpr int ACC_COLS = BN < 32 ? 32 : BN;
   static constexpr int SF_COL = 2 * ACC_COLS;
@@ -119,63 +122,47 @@ __device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// One element of the result, its old value added.
+// One element of the result.  Accumulating, the addition is the memory's: each element gets one a call, so its place
+// in time changes nothing, and nobody waits for the old value (loads of 8 rows before their stores kept 8 KB an SM in
+// flight: 4085 x 2834 x 768 took 80 us).  It flushes subnormal sums to zero.
 __device__ __forceinline__ void g8_put(const Gemm8Args& g, int64_t o, float v) {
   if (g.c_bf16) reinterpret_cast<__nv_bfloat16*>(g.c)[o] = __float2bfloat16_rn(v);
+  else if (g.accumulate) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(reinterpret_cast<float*>(g.c) + o), "f"(v) : "memory");
   else reinterpret_cast<float*>(g.c)[o] = v;
 }
 
 // Columns n .. n + 31 of the warp's 32 MMA rows m0 .. (one a lane).  Where C's rows are whole sectors a lane
 // stores its row's (16 lanes of a bf16 C at 2 B a lane and row took 39 us for 2500 x 1300 x 256, against 17 us
-// through the scratch); otherwise the rows pass through the warp's scratch and leave 32 columns at a time.
-// Accumulating, the loads of several rows go before their stores: one memory latency, not one each.
+// through the scratch); otherwise, and when accumulating, the rows pass through the warp's scratch and leave 32
+// columns at a time.
 __device__ __forceinline__ void g8_store32(const Gemm8Args& g, float* xs, int64_t m0, int64_t n, const float (&v)[32]) {
   const int lane = threadIdx.x & 31;
   if (m0 >= g.M || n >= g.N) return;
   const int64_t m = m0 + lane;
   if (g.swap) {                         // lanes hold consecutive elements of a row of C
     if (m >= g.M) return;
-    const int64_t o = n * g.ldc + m;
 #pragma unroll
-    for (int h = 0; h < 32; h += 16) {
-      float old[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        old[i] = g.accumulate && n + h + i < g.N ? reinterpret_cast<const float*>(g.c)[o + (h + i) * g.ldc] : 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (n + h + i < g.N) g8_put(g, o + (h + i) * g.ldc, old[i] + v[h + i]);
-    }
+    for (int i = 0; i < 32; ++i)
+      if (n + i < g.N) g8_put(g, (n + i) * g.ldc + m, v[i]);
     return;
   }
-  if (g.sectors && n + 32 <= g.N) {
+  if (g.sectors && !g.accumulate && n + 32 <= g.N) {
     if (m >= g.M) return;
     char* p = reinterpret_cast<char*>(g.c) + (m * g.ldc + n) * (g.c_bf16 ? 2 : 4);
+    uint32_t w[8];
     if (g.c_bf16) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        uint32_t w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = bf16x2_bits(v[16 * j + 2 * i], v[16 * j + 2 * i + 1]);
         st_sector(p + 32 * j, w);
       }
-      return;
-    }
+    } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {       // 16 columns at a time: a pair's drain has few registers left
-      float4 old[4];
+      for (int j = 0; j < 4; ++j) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        old[i] = g.accumulate ? reinterpret_cast<const float4*>(p)[4 * h + i] : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4& x = old[2 * j + (i >> 2)];
-          w[i] = __float_as_uint((&x.x)[i & 3] + v[16 * h + 8 * j + i]);
-        }
-        st_sector(p + 64 * h + 32 * j, w);
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * j + i]);
+        st_sector(p + 32 * j, w);
       }
     }
     return;
@@ -186,14 +173,11 @@ __device__ __forceinline__ void g8_store32(const Gemm8Args& g, float* xs, int64_
   const int rows = (int)min((int64_t)32, g.M - m0);
   if (n + lane < g.N) {
     const int64_t o = m0 * g.ldc + n + lane;
-    for (int h = 0; h < rows; h += 8) {
-      float old[8];
+    if (rows == 32) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        old[i] = g.accumulate && h + i < rows ? reinterpret_cast<const float*>(g.c)[o + (h + i) * g.ldc] : 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (h + i < rows) g8_put(g, o + (h + i) * g.ldc, old[i] + xs[(h + i) * G8_XS_LD + lane]);
+      for (int i = 0; i < 32; ++i) g8_put(g, o + i * g.ldc, xs[i * G8_XS_LD + lane]);
+    } else {
+      for (int i = 0; i < rows; ++i) g8_put(g, o + i * g.ldc, xs[i * G8_XS_LD + lane]);
     }
   }
   __syncwarp();
@@ -219,7 +203,7 @@ __device__ __forceinline__ void g8_tile(int64_t t, int64_t tiles_m, int64_t tile
 // tiles) shares one tile, each CTA a stretch of K, and every CTA adds and
 // writes its share of the columns, in the order of the stretches.
 template <int BN, bool PROMOTE>
-__global__ void __launch_bounds__(G8_THREADS, 1)
+__global__ void __launch_bounds__(G8_THREADS, Gemm8Smem<BN>::CTAS)
 gemm8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, Gemm8Args g) {
   using SM = Gemm8Smem<BN>;
   namespace cg = cooperative_groups;
@@ -423,7 +407,7 @@ gemm8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     constexpr int ROUND = 4;
     const int share = (G8_BM * BN + parts - 1) / parts, threads = blockDim.x;
     for (int e0 = threadIdx.x; e0 < share; e0 += ROUND * threads) {
-      float v[ROUND], old[ROUND];
+      float v[ROUND];
       int64_t o[ROUND];
 #pragma unroll
       for (int u = 0; u < ROUND; ++u) {
@@ -432,7 +416,6 @@ gemm8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         const int64_t m = ti * G8_BM + r, n = tj * BN + c;
         const bool in = e0 + u * threads < share && e < G8_BM * BN && m < g.M && n < g.N;
         o[u] = in ? (g.swap ? n * g.ldc + m : m * g.ldc + n) : -1;
-        old[u] = in && g.accumulate ? reinterpret_cast<const float*>(g.c)[o[u]] : 0.f;
         v[u] = 0.f;
         if (in) {
           float w[8];
@@ -445,7 +428,7 @@ gemm8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
       }
 #pragma unroll
       for (int u = 0; u < ROUND; ++u)
-        if (o[u] >= 0) g8_put(g, o[u], old[u] + v[u]);
+        if (o[u] >= 0) g8_put(g, o[u], v[u]);
     }
     cluster.sync();
   }

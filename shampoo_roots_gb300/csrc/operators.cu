@@ -227,7 +227,7 @@ int launch_pair(Handle* h, const void* A, int64_t lda, const void* B, int64_t ld
 template <int BN>
 cudaError_t launch_gemm8(const CUtensorMap& ma, const CUtensorMap& mb, const Gemm8Args& g, int64_t tiles, int parts, int sms,
                          cudaStream_t st) {
-  const unsigned grid = parts > 1 ? (unsigned)(tiles * parts) : (unsigned)std::min<int64_t>(tiles, sms);
+  const unsigned grid = parts > 1 ? (unsigned)(tiles * parts) : (unsigned)std::min<int64_t>(tiles, sms * Gemm8Smem<BN>::CTAS);
   auto k = g.c_bf16 ? gemm8_kernel<BN, false> : gemm8_kernel<BN, true>;
   return launch(k, dim3(grid), dim3(G8_THREADS), Gemm8Smem<BN>::BYTES, st, parts, ma, mb, g);
 }
@@ -413,7 +413,8 @@ int precond_gemm8(precond_t ph, int64_t M, int64_t N, int64_t K, const void* A, 
   // Few tiles: a cluster of up to 8 CTAs shares each, a stretch of whole scale groups of K each.
   const int blocks = (int)((K + G8_BK - 1) / G8_BK), groups = q8_groups(K);
   int parts = 1;
-  while (parts < 8 && tiles * parts * 2 <= h->num_sms && parts * 2 <= groups) parts *= 2;
+  const int places = h->num_sms * (bn <= 32 ? 2 : 1);
+  while (parts < 8 && tiles * parts * 2 <= places && parts * 2 <= groups) parts *= 2;
   // Pairs of CTAs where they are expected to end first: a 256 x 256 tile's block of K takes a pair 0.30 us,
   // a 128 x 128 tile's a CTA 0.25 us, and joining stretches 2 us.
   const int64_t pair_tiles = ((g.M + 255) / 256) * ((g.N + 255) / 256);
