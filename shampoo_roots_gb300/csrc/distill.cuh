@@ -142,25 +142,27 @@ __device__ __forceinline__ void set_float(__nv_bfloat16* p, float x) { *p = __fl
 struct DistillShared {
   float2* sums;                     // (maximum, sum) of the streaming warps of the cluster's blocks
   float* p; float* logp; float* z; int* id;      // candidates; id -1: none
-  int* key; int* first;             // ids already seen: open addressing, an id and the first candidate that has it
+  int* key;                         // a table to find equal ids
   float* most;                      // the teacher's largest logit
   int slots;
   static __host__ __device__ int slots_for(int top) {
     int n = 64;
-    while (n < 2 * top) n *= 2;
+    while (n < 4 * top) n *= 2;
     return n;
   }
-  static __host__ __device__ int bytes(int top, int sums) { return (sums * 8 + 16 * top + 8 * slots_for(top) + 4 + 15) / 16 * 16; }
+  static __host__ __device__ int bytes(int top, int sums) {
+    return ((sums + 1) / 2 * 2) * 8 + 16 * ((top + 3) / 4 * 4) + 4 * slots_for(top) + 16;
+  }
   __device__ __forceinline__ DistillShared(uint8_t* base, int top, int nsums) {
+    const int n = (top + 3) / 4 * 4;
     sums = reinterpret_cast<float2*>(base);
-    p = reinterpret_cast<float*>(sums + nsums);
-    logp = p + top;
-    z = logp + top;
-    id = reinterpret_cast<int*>(z + top);
+    p = reinterpret_cast<float*>(sums + (nsums + 1) / 2 * 2);
+    logp = p + n;
+    z = logp + n;
+    id = reinterpret_cast<int*>(z + n);
     slots = slots_for(top);
-    key = id + top;
-    first = key + slots;
-    most = reinterpret_cast<float*>(first + slots);
+    key = id + n;
+    most = reinterpret_cast<float*>(key + slots);
   }
 };
 
@@ -185,94 +187,201 @@ struct Slice {
   }
 };
 
-// The candidates' ids, the teacher's and the student's logits, by one warp.  (Of the student's logits a block needs
-// those of its part, and the first block all of them, for the loss.)
+// The candidates of a row, the work of one warp, in its steps: gather (ids, the teacher's and the student's logits;
+// of these a block needs those of its part, and the first block all, for the loss), teach (log p and p), loss, unite
+// (p of the first candidate of an id becomes the sum over all of that id; the others, and those outside the block's
+// part, drop out) and patch (their gradients).  `most` is the teacher's largest logit, -inf where there is no
+// candidate.
 template <typename T>
-__device__ __forceinline__ void distill_gather(const DistillArgs& a, const DistillShared& sh, int64_t row, const T* z,
-                                               const Slice& sl, bool all) {
-  const int lane = threadIdx.x & 31;
-  float most = -INFINITY;
-  for (int j = lane; j < a.top; j += 32) {
-    const int64_t id = a.ids64 ? reinterpret_cast<const int64_t*>(a.ids)[row * a.ldi + j]
-                               : (int64_t) reinterpret_cast<const int32_t*>(a.ids)[row * a.ldi + j];
-    const bool ok = id >= 0 && id < a.vocab;
-    const float t = !ok ? -INFINITY : (a.t_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.t)[row * a.ldt + j])
-                                                : reinterpret_cast<const float*>(a.t)[row * a.ldt + j]);
-    sh.id[j] = ok ? (int)id : -1;
-    sh.logp[j] = t;
-    sh.z[j] = !ok ? 0.f : a.kept ? a.kept[row * a.top + j] : all || (id >= sl.lo && id < sl.hi) ? as_float(z[id]) : 0.f;
-    most = max_nan(most, t);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if (lane == 0) *sh.most = most;        // -inf: no candidate
-  __syncwarp();
+__device__ __forceinline__ void candidate(const DistillArgs& a, int64_t row, int j, int& id, float& t) {
+  const int64_t i = a.ids64 ? reinterpret_cast<const int64_t*>(a.ids)[row * a.ldi + j]
+                            : (int64_t) reinterpret_cast<const int32_t*>(a.ids)[row * a.ldi + j];
+  t = a.t_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.t)[row * a.ldt + j])
+               : reinterpret_cast<const float*>(a.t)[row * a.ldt + j];
+  id = i >= 0 && i < a.vocab ? (int)i : -1;
+  if (id < 0) t = -INFINITY;
 }
-// log p and p, by the same warp.
-__device__ __forceinline__ void distill_teacher(const DistillArgs& a, const DistillShared& sh) {
-  const int lane = threadIdx.x & 31;
-  const float most = *sh.most;
-  float st = 0.f;
-  for (int j = lane; j < a.top; j += 32) {
-    const float d = (sh.logp[j] - most) / a.tau;
-    sh.logp[j] = d;
-    st += expf(d);
+template <typename T>
+__device__ __forceinline__ float candidate_logit(const DistillArgs& a, int64_t row, int j, int id, const T* z, const Slice& sl, bool all) {
+  if (id < 0) return 0.f;
+  if (a.kept) return a.kept[row * a.top + j];
+  return all || (id >= sl.lo && id < sl.hi) ? as_float(z[id]) : 0.f;
+}
+__device__ __forceinline__ float warp_max_nan(float m) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+// Whether an id occurs twice among those >= 0 of sh.id (j = lane, lane + 32, ...; -1 elsewhere).  Each id writes its
+// index to a place of the table that its hash and the round give, and reads it back: an index of the same id there is
+// a second occurrence, one of another id a collision, which the next round tells apart.  Two equal ids meet in the
+// round in which one of them is read back, at the latest, since they always have the same place.
+__device__ __forceinline__ bool repeated_ids(const DistillShared& sh, int top) {
+  const int lane = threadIdx.x & 31, mask = sh.slots - 1;
+  unsigned open = 0;                     // candidates that have not been read back
+  for (int q = 0; lane + 32 * q < top; ++q) open |= sh.id[lane + 32 * q] >= 0 ? 1u << q : 0;
+  bool twice = false;
+  for (unsigned round = 1; __any_sync(0xffffffffu, open != 0); round += 2) {
+    auto place = [&](int id) { return (int)(((unsigned)id * 2654435761u * round) >> 15) & mask; };
+    for (unsigned m = open; m; m &= m - 1) {
+      const int j = lane + 32 * (__ffs(m) - 1);
+      sh.key[place(sh.id[j])] = j;
+    }
+    __syncwarp();
+    for (unsigned m = open; m; m &= m - 1) {
+      const int q = __ffs(m) - 1, j = lane + 32 * q, id = sh.id[j], k = sh.key[place(id)];
+      if (k == j) open &= ~(1u << q);
+      else if (sh.id[k] == id) twice = true, open &= ~(1u << q);
+    }
+    __syncwarp();
   }
-  const float ls = logf(warp_sum(st));
-  for (int j = lane; j < a.top; j += 32) {
-    sh.logp[j] -= ls;
-    sh.p[j] = expf(sh.logp[j]);
+  return __any_sync(0xffffffffu, twice);
+}
+// Then: p of the first of an id becomes the sum over that id in order, the others' ids -1 (the loss is done with logp).
+__device__ __forceinline__ void unite_ids(const DistillShared& sh, int top) {
+  const int lane = threadIdx.x & 31;
+  for (int j = lane; j < top; j += 32) {
+    float p = 0.f;
+    bool again = false;
+    for (int i = 0; i < top; ++i)
+      if (sh.id[i] == sh.id[j]) {
+        p += sh.p[i];
+        again |= i < j;
+      }
+    sh.logp[j] = again ? -1.f : p;       // -1: not the first
+  }
+  __syncwarp();
+  for (int j = lane; j < top; j += 32) {
+    if (sh.logp[j] == -1.f) sh.id[j] = -1;
+    sh.p[j] = sh.logp[j];
   }
   __syncwarp();
 }
 
-// Makes p[j] the sum over all candidates of id[j] in this block's part, for the first of them; the ids of the others,
-// and of candidates elsewhere, become -1.  By one warp, after the loss (which takes each p by itself).
-__device__ __forceinline__ void distill_unite(const DistillArgs& a, const DistillShared& sh, const Slice& sl) {
-  const int lane = threadIdx.x & 31, size = sh.slots;
-  for (int i = lane; i < size; i += 32) {
-    sh.key[i] = -1;
-    sh.first[i] = DISTILL_MAX_TOP;
-  }
-  __syncwarp();
-  auto find = [&](int id) {              // the slot of an id, taken if it is new; at most half of them are taken
-    int h = (int)((unsigned)id * 2654435761u >> 16) & (size - 1);
-    for (int tries = 0; tries < size; ++tries, h = (h + 1) & (size - 1)) {
-      const int k = atomicCAS(&sh.key[h], -1, id);
-      if (k == -1 || k == id) break;
+// Up to 128: four a lane, in registers.
+struct FewCandidates {
+  static constexpr int Q = 4;
+  int id[Q];
+  float logp[Q], z[Q], p[Q], most;
+  template <typename T>
+  __device__ __forceinline__ void gather(const DistillArgs& a, const DistillShared&, int64_t row, const T* z_, const Slice& sl, bool all) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      id[q] = -1;
+      logp[q] = -INFINITY;
+      if (lane + 32 * q < a.top) candidate<T>(a, row, lane + 32 * q, id[q], logp[q]);
     }
-    return h;
-  };
-  bool again = false;
-  for (int j = lane; j < a.top; j += 32) {
-    const int id = sh.id[j];
-    if (id >= sl.lo && id < sl.hi) atomicMin(&sh.first[find(id)], j);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) z[q] = candidate_logit(a, row, lane + 32 * q, id[q], z_, sl, all);
+    most = warp_max_nan(max_nan(max_nan(logp[0], logp[1]), max_nan(logp[2], logp[3])));
   }
-  __syncwarp();
-  for (int j = lane; j < a.top; j += 32) {
-    const int id = sh.id[j];
-    if (id >= sl.lo && id < sl.hi) again |= sh.first[find(id)] != j;
+  __device__ __forceinline__ void teach(const DistillArgs& a, const DistillShared&) {
+    float st = 0.f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      logp[q] = (logp[q] - most) / a.tau;
+      st += expf(logp[q]);               // 0 for what is no candidate
+    }
+    const float ls = logf(warp_sum(st));
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      logp[q] -= ls;
+      p[q] = id[q] >= 0 ? expf(logp[q]) : 0.f;
+    }
   }
-  if (__any_sync(0xffffffffu, again)) {  // an id more than once: add in order
-    for (int j = lane; j < a.top; j += 32) {
-      const int id = sh.id[j];
-      if (id < sl.lo || id >= sl.hi || sh.first[find(id)] != j) continue;
-      float p = 0.f;
-      for (int i = j; i < a.top; ++i)
-        if (sh.id[i] == id) p += sh.p[i];
-      sh.logp[j] = p;                    // the loss is done with log p
+  __device__ __forceinline__ float divergence(const DistillArgs&, const DistillShared&, float c, const Shift& at, float ls) const {
+    float l = 0.f;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (p[q] != 0.0f) l += p[q] * (logp[q] - fmaf(at(z[q], c), LN2, -ls));
+    return l;
+  }
+  __device__ __forceinline__ void unite(const DistillArgs& a, const DistillShared& sh, const Slice& sl) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      if (id[q] < sl.lo || id[q] >= sl.hi) id[q] = -1;
+      if (lane + 32 * q < a.top) sh.id[lane + 32 * q] = id[q];
     }
     __syncwarp();
+    if (!repeated_ids(sh, a.top)) return;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (lane + 32 * q < a.top) sh.p[lane + 32 * q] = p[q];
+    __syncwarp();
+    unite_ids(sh, a.top);
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (lane + 32 * q < a.top) {
+        id[q] = sh.id[lane + 32 * q];
+        p[q] = sh.p[lane + 32 * q];
+      }
+  }
+  template <typename T>
+  __device__ __forceinline__ void patch(const DistillArgs&, const DistillShared&, T* dz, float scale, float c, const Shift& at, float s) const {
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (id[q] >= 0) set_float(dz + id[q], scale * (ex2(at(z[q], c)) / s - p[q]));
+  }
+};
+
+// More: in shared memory.
+struct ManyCandidates {
+  float most;
+  template <typename T>
+  __device__ __forceinline__ void gather(const DistillArgs& a, const DistillShared& sh, int64_t row, const T* z, const Slice& sl, bool all) {
+    const int lane = threadIdx.x & 31;
+    most = -INFINITY;
     for (int j = lane; j < a.top; j += 32) {
-      const int id = sh.id[j];
-      if (id < sl.lo || id >= sl.hi) continue;
-      sh.p[j] = sh.first[find(id)] == j ? sh.logp[j] : -1.f;   // -1 marks the others: ids are still being compared
+      candidate<T>(a, row, j, sh.id[j], sh.logp[j]);
+      sh.z[j] = candidate_logit(a, row, j, sh.id[j], z, sl, all);
+      most = max_nan(most, sh.logp[j]);
+    }
+    most = warp_max_nan(most);
+    __syncwarp();
+  }
+  __device__ __forceinline__ void teach(const DistillArgs& a, const DistillShared& sh) {
+    const int lane = threadIdx.x & 31;
+    float st = 0.f;
+    for (int j = lane; j < a.top; j += 32) {
+      const float d = (sh.logp[j] - most) / a.tau;
+      sh.logp[j] = d;
+      st += expf(d);
+    }
+    const float ls = logf(warp_sum(st));
+    for (int j = lane; j < a.top; j += 32) {
+      sh.logp[j] -= ls;
+      sh.p[j] = sh.id[j] >= 0 ? expf(sh.logp[j]) : 0.f;
     }
     __syncwarp();
-    for (int j = lane; j < a.top; j += 32)
-      if (sh.p[j] == -1.f) sh.id[j] = -1;
   }
-  __syncwarp();
+  __device__ __forceinline__ float divergence(const DistillArgs& a, const DistillShared& sh, float c, const Shift& at, float ls) const {
+    float l = 0.f;
+    for (int j = threadIdx.x & 31; j < a.top; j += 32)
+      if (sh.p[j] != 0.0f) l += sh.p[j] * (sh.logp[j] - fmaf(at(sh.z[j], c), LN2, -ls));
+    return l;
+  }
+  __device__ __forceinline__ void unite(const DistillArgs& a, const DistillShared& sh, const Slice& sl) {
+    for (int j = threadIdx.x & 31; j < a.top; j += 32)
+      if (sh.id[j] < sl.lo || sh.id[j] >= sl.hi) sh.id[j] = -1;
+    __syncwarp();
+    if (repeated_ids(sh, a.top)) unite_ids(sh, a.top);
+  }
+  template <typename T>
+  __device__ __forceinline__ void patch(const DistillArgs& a, const DistillShared& sh, T* dz, float scale, float c, const Shift& at, float s) const {
+    for (int j = threadIdx.x & 31; j < a.top; j += 32)
+      if (sh.id[j] >= 0) set_float(dz + sh.id[j], scale * (ex2(at(sh.z[j], c)) / s - sh.p[j]));
+  }
+};
+
+// The row's loss: log q = ln 2 (z c - k) - ln S.
+template <typename C>
+__device__ __forceinline__ void distill_loss(const DistillArgs& a, const DistillShared& sh, const C& cand, int64_t row, float weight,
+                                             float c, const Shift& at, float s, bool teaches) {
+  const float l = teaches ? warp_sum(cand.divergence(a, sh, c, at, logf(s))) : 0.f;
+  if ((threadIdx.x & 31) == 0) a.loss[row] = teaches ? weight * (a.tau * a.tau) * l : 0.0f;
 }
 
 // The barrier of a row, in two halves: the streaming warps' sums are there and the candidates' logits have been read.
@@ -305,30 +414,6 @@ __device__ __forceinline__ void join_sums(const DistillShared& sh, int n, float&
 #pragma unroll
   for (int i = 0; i < 4; ++i) s += x[i].x == m ? x[i].y : x[i].y * ex2(at(x[i].x, c));
   s = warp_sum(s);
-}
-
-// The row's loss, by one warp: log q = ln 2 (z c - k) - ln S.
-__device__ __forceinline__ void distill_loss(const DistillArgs& a, const DistillShared& sh, int64_t row, float weight, float c,
-                                             const Shift& at, float s, bool teaches) {
-  const int lane = threadIdx.x & 31;
-  float l = 0.f;
-  if (teaches) {
-    const float ls = logf(s);
-    for (int j = lane; j < a.top; j += 32)
-      if (sh.p[j] != 0.0f) l += sh.p[j] * (sh.logp[j] - fmaf(at(sh.z[j], c), LN2, -ls));
-    l = warp_sum(l);
-  }
-  if (lane == 0) a.loss[row] = teaches ? weight * (a.tau * a.tau) * l : 0.0f;
-}
-
-// The candidates' gradients, over the dense ones: scale (q - p), by the warp that united them.
-template <typename T>
-__device__ __forceinline__ void distill_patch(const DistillArgs& a, const DistillShared& sh, const Slice& sl, T* dz, float scale,
-                                              float c, const Shift& at, float s) {
-  for (int j = threadIdx.x & 31; j < a.top; j += 32) {
-    const int id = sh.id[j];
-    if (id >= sl.lo && id < sl.hi) set_float(dz + id, scale * (ex2(at(sh.z[j], c)) / s - sh.p[j]));
-  }
 }
 
 // One logit into a thread's running (maximum, sum).
@@ -537,20 +622,25 @@ __global__ void __launch_bounds__(DISTILL_THREADS + (FUSED ? 32 : 0), 2) distill
     }
   } else if (reads) {
     // ------------------------------------------------ candidates
-    distill_gather(a, sh, row, z, sl, part == 0);
-    row_arrive(parts, false);
-    distill_teacher(a, sh);
-    const bool teaches = *sh.most != -INFINITY;
-    row_wait(parts, false);
-    join_sums(sh, parts * streaming, m, s, c);
-    const Shift shift(m, c);
-    if (part == 0) distill_loss(a, sh, row, weight, c, shift, s, teaches);
-    if (a.dz) {
-      if (teaches) distill_unite(a, sh, sl);
-      __syncwarp();
-      asm volatile("bar.sync 1, %0;" ::"r"((int)blockDim.x) : "memory");
-      if (teaches) distill_patch(a, sh, sl, dz, weight * a.tau, c, shift, s);
-    }
+    auto work = [&](auto cand) {
+      cand.gather(a, sh, row, z, sl, part == 0);
+      if (lane == 0) *sh.most = cand.most;
+      row_arrive(parts, false);
+      cand.teach(a, sh);
+      const bool teaches = cand.most != -INFINITY;
+      row_wait(parts, false);
+      join_sums(sh, parts * streaming, m, s, c);
+      const Shift shift(m, c);
+      if (part == 0) distill_loss(a, sh, cand, row, weight, c, shift, s, teaches);
+      if (a.dz) {
+        if (teaches) cand.unite(a, sh, sl);
+        __syncwarp();
+        asm volatile("bar.sync 1, %0;" ::"r"((int)blockDim.x) : "memory");
+        if (teaches) cand.patch(a, sh, dz, weight * a.tau, c, shift, s);
+      }
+    };
+    if (a.top <= 32 * FewCandidates::Q) work(FewCandidates());
+    else work(ManyCandidates());
   } else if (part == 0 && lane == 0) {
     a.loss[row] = 0.0f;
   }
@@ -569,9 +659,11 @@ __global__ void __launch_bounds__(256) distill_keep_kernel(DistillArgs a) {
   a.kept[i] = id >= 0 && id < a.vocab ? as_float((reinterpret_cast<const T*>(a.z) + row * a.ldz)[id]) : 0.f;
 }
 
-// Many rows: a warp does the loss and the candidates' gradients of a row, after distill_kernel.
-template <typename T>
-__global__ void distill_candidates_kernel(DistillArgs a) {
+// Many rows: a warp does the loss and the candidates' gradients of a row, after distill_kernel.  Four blocks an SM:
+// with six (40 registers) this kernel takes 60 us, not 47, at 8192 x 128 candidates, and the next call's first kernel,
+// which starts beside it, loses another 100.
+template <typename T, typename C>
+__global__ void __launch_bounds__(256, 4) distill_candidates_kernel(DistillArgs a) {
   extern __shared__ __align__(16) uint8_t distill_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
@@ -579,25 +671,26 @@ __global__ void distill_candidates_kernel(DistillArgs a) {
   let_next_start();
   if (row >= a.rows) return;
   const DistillShared sh(distill_smem + warp * DistillShared::bytes(a.top, 0), a.top, 0);
+  const T* z = reinterpret_cast<const T*>(a.z) + row * a.ldz;
+  T* dz = reinterpret_cast<T*>(a.dz) + row * a.lddz;
+  const Slice whole(z, (int)a.vocab, 1, 0);
+  const float c = LOG2E / a.tau;
   const float weight = a.weight ? a.weight[row] : 1.0f;
   if (weight == 0.0f) {
     if (lane == 0) a.loss[row] = 0.0f;
     return;
   }
-  const T* z = reinterpret_cast<const T*>(a.z) + row * a.ldz;
-  T* dz = reinterpret_cast<T*>(a.dz) + row * a.lddz;
-  const Slice all(z, (int)a.vocab, 1, 0);
-  const float c = LOG2E / a.tau;
   const float2 st = a.stats[row];
-  distill_gather(a, sh, row, z, all, true);
-  distill_teacher(a, sh);
-  const bool teaches = *sh.most != -INFINITY;
+  C cand;
+  cand.gather(a, sh, row, z, whole, true);
+  cand.teach(a, sh);
+  const bool teaches = cand.most != -INFINITY;
   const Shift shift(st.x, c);
-  distill_loss(a, sh, row, weight, c, shift, st.y, teaches);
+  distill_loss(a, sh, cand, row, weight, c, shift, st.y, teaches);
   if (!a.dz) return;
   if (teaches) {
-    distill_unite(a, sh, all);
-    distill_patch(a, sh, all, dz, weight * a.tau, c, shift, st.y);
+    cand.unite(a, sh, whole);
+    cand.patch(a, sh, dz, weight * a.tau, c, shift, st.y);
   } else {                              // nothing is taught: the gradient of the softmax alone is taken back
     for (int64_t i = lane; i < a.vocab; i += 32) set_float(dz + i, 0.f);
   }
