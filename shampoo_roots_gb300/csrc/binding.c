@@ -16,8 +16,8 @@ typedef struct {
 
 enum { T_F32, T_BF16, T_E4M3, T_E8M0, T_U8, T_I32, T_I64, T_COUNT };
 static PyObject* dtypes[T_COUNT];
-static PyObject *s_shape, *s_stride, *s_data_ptr, *s_dtype, *s_get_device, *raw_stream;
-enum { E_NORM, E_GRAD, E_QUANTIZE, E_GEMM, E_DISTILL, E_DISTILL_WS, E_COUNT };
+static PyObject *s_shape, *s_stride, *s_data_ptr, *s_dtype, *s_get_device, *s_new_empty, *raw_stream;
+enum { E_NORM, E_GRAD, E_GRAD_WS, E_QUANTIZE, E_GEMM, E_DISTILL, E_DISTILL_WS, E_COUNT };
 static void* entry[E_COUNT];
 
 static int bad(PyObject* type, const char* what, const char* why) {
@@ -175,6 +175,41 @@ static int stream_of(PyObject* stream, PyObject* t, void** out) {
   Py_DECREF(s);
   return PyErr_Occurred() ? -1 : 0;
 }
+/* The workspace argument: None is memory of torch's allocator, a float32 vector like `like` (*own, to be released
+ * after the call).  That belongs to the current stream, so another one needs a workspace of the caller's. */
+static int workspace_of(PyObject* given, PyObject* like, int64_t need, PyObject* stream, void* st, Tensor* o, PyObject** own) {
+  *own = NULL;
+  o->p = NULL;
+  o->rows = 0;
+  if (given != Py_None) {
+    if (get(given, "workspace", o)) return -1;
+    if (o->dim != 1 || !o->contiguous || (o->dtype != dtypes[T_U8] && o->dtype != dtypes[T_F32])) {
+      PyErr_SetString(PyExc_ValueError, "workspace must be a contiguous vector of uint8 or float32");
+      return -1;
+    }
+    if (o->dtype == dtypes[T_F32]) o->rows *= 4;
+    return 0;
+  }
+  if (need <= 0) return 0;
+  if (stream != Py_None) {
+    void* current;
+    if (stream_of(Py_None, like, &current)) return -1;
+    if (current != st) return bad(PyExc_ValueError, "give a workspace", "with a stream other than torch's current one");
+  }
+  PyObject* n = PyLong_FromLongLong((need + 3) / 4);
+  if (!n) return -1;
+  *own = PyObject_CallMethodOneArg(like, s_new_empty, n);
+  Py_DECREF(n);
+  PyObject* p = *own ? PyObject_CallMethodNoArgs(*own, s_data_ptr) : NULL;
+  if (p) {
+    o->p = PyLong_AsVoidPtr(p);
+    o->rows = need;
+    Py_DECREF(p);
+  }
+  if (!PyErr_Occurred()) return 0;
+  Py_CLEAR(*own);
+  return -1;
+}
 static int handle(PyObject* h, void** out) {
   *out = h == Py_None ? NULL : PyLong_AsVoidPtr(h);
   return PyErr_Occurred() ? -1 : 0;
@@ -208,6 +243,8 @@ static PyObject* rms_norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 static PyObject* rms_norm_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   typedef int (*fn)(void*, const void*, const void*, const void*, const float*, const void*, int, int, int64_t, int64_t,
                     int64_t, int64_t, int64_t, void*, int64_t, float*, void*, int64_t, void*);
+  typedef int64_t (*need_fn)(int64_t, int64_t);
+  PyObject* own;
   Tensor dy, x, w, rs, dx, dw, dr, ws;
   void *h, *st;
   if (count(n, 10) || handle(a[0], &h) || matrix(a[1], "dy", &dy)) return NULL;
@@ -216,14 +253,13 @@ static PyObject* rms_norm_grad(PyObject* self, PyObject* const* a, Py_ssize_t n)
   const int wt = float_type(&w, "weight");
   if (wt < 0 || vector(a[4], "rstd", &rs, dy.rows, 1) || matrix_like(a[5], "dx", &dx, dy.rows, dy.cols, dy.dtype) ||
       vector(a[6], "dw", &dw, dy.cols, 1) || maybe(a[7], "dresidual", &dr, dy.rows, dy.cols, dy.dtype) ||
-      get(a[8], "workspace", &ws) || stream_of(a[9], a[1], &st))
+      stream_of(a[9], a[1], &st) ||
+      workspace_of(a[8], a[6], a[8] == Py_None ? ((need_fn)entry[E_GRAD_WS])(dy.rows, dy.cols) : 0, a[9], st, &ws, &own))
     return NULL;
-  if (ws.dim != 1 || !ws.contiguous || (ws.dtype != dtypes[T_U8] && ws.dtype != dtypes[T_F32])) {
-    PyErr_SetString(PyExc_ValueError, "workspace must be a contiguous vector of uint8 or float32");
-    return NULL;
-  }
-  return PyLong_FromLong(((fn)entry[E_GRAD])(h, dy.p, x.p, w.p, rs.p, dr.p, dt, wt, dy.rows, dy.cols, dy.ld, x.ld, dr.ld, dx.p,
-                                             dx.ld, dw.p, ws.p, ws.rows * (ws.dtype == dtypes[T_U8] ? 1 : 4), st));
+  const int code = ((fn)entry[E_GRAD])(h, dy.p, x.p, w.p, rs.p, dr.p, dt, wt, dy.rows, dy.cols, dy.ld, x.ld, dr.ld, dx.p, dx.ld,
+                                       dw.p, ws.p, ws.rows, st);
+  Py_XDECREF(own);
+  return PyLong_FromLong(code);
 }
 
 /* (h, x, q, scale, qt, scale_t, block, x_scale, stream) */
@@ -273,12 +309,12 @@ static PyObject* gemm8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(((fn)entry[E_GEMM])(h, A.rows, B.rows, A.cols, A.p, A.ld, sa.p, B.p, B.ld, sb.p, c.p, c.ld, ct, acc, st));
 }
 
-/* (h, logits, ids, teacher, loss, weight, temperature, dlogits, workspace, stream); bytes of workspace where that is
- * None and some is needed, as a negative number below every status. */
+/* (h, logits, ids, teacher, loss, weight, temperature, dlogits, workspace, stream) */
 static PyObject* distill(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   typedef int (*fn)(void*, const void*, int, int64_t, int64_t, int64_t, const void*, int, int64_t, const void*, int, int64_t, int,
                     const float*, float, float*, void*, int64_t, void*, int64_t, void*);
   typedef int64_t (*need_fn)(int64_t, int64_t, int, int, int);
+  PyObject* own;
   Tensor z, ids, t, loss, w, dz, ws;
   void *h, *st;
   if (count(n, 10) || handle(a[0], &h) || matrix(a[1], "logits", &z)) return NULL;
@@ -295,20 +331,13 @@ static PyObject* distill(PyObject* self, PyObject* const* a, Py_ssize_t n) {
       maybe(a[7], "dlogits", &dz, z.rows, z.cols, z.dtype) || stream_of(a[9], a[1], &st))
     return NULL;
   const int top = (int)(ids.cols > 1 << 30 ? 1 << 30 : ids.cols);
-  ws.p = NULL;
-  ws.rows = 0;
-  if (a[8] != Py_None) {
-    if (get(a[8], "workspace", &ws)) return NULL;
-    if (ws.dim != 1 || !ws.contiguous || ws.dtype != dtypes[T_U8]) {
-      PyErr_SetString(PyExc_ValueError, "workspace must be a contiguous vector of uint8");
-      return NULL;
-    }
-  } else {
-    const int64_t need = ((need_fn)entry[E_DISTILL_WS])(z.rows, z.cols, top, dt, dz.p == z.p);
-    if (need > 0) return PyLong_FromLongLong(-1000 - need);
-  }
-  return PyLong_FromLong(((fn)entry[E_DISTILL])(h, z.p, dt, z.rows, z.cols, z.ld, ids.p, ids.dtype == dtypes[T_I32] ? 32 : 64, ids.ld,
-                                                t.p, tt, t.ld, top, w.p, (float)tau, loss.p, dz.p, dz.ld, ws.p, ws.rows, st));
+  if (workspace_of(a[8], a[4], a[8] == Py_None ? ((need_fn)entry[E_DISTILL_WS])(z.rows, z.cols, top, dt, dz.p == z.p) : 0, a[9], st,
+                   &ws, &own))
+    return NULL;
+  const int code = ((fn)entry[E_DISTILL])(h, z.p, dt, z.rows, z.cols, z.ld, ids.p, ids.dtype == dtypes[T_I32] ? 32 : 64, ids.ld, t.p,
+                                          tt, t.ld, top, w.p, (float)tau, loss.p, dz.p, dz.ld, ws.p, ws.rows, st);
+  Py_XDECREF(own);
+  return PyLong_FromLong(code);
 }
 
 /* set_up(dtypes, raw_stream, entries): what the calls need, once. */
@@ -343,7 +372,7 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1,
 PyMODINIT_FUNC PyInit__binding(void) {
   if (!(s_shape = PyUnicode_InternFromString("shape")) || !(s_stride = PyUnicode_InternFromString("stride")) ||
       !(s_data_ptr = PyUnicode_InternFromString("data_ptr")) || !(s_dtype = PyUnicode_InternFromString("dtype")) ||
-      !(s_get_device = PyUnicode_InternFromString("get_device")))
+      !(s_get_device = PyUnicode_InternFromString("get_device")) || !(s_new_empty = PyUnicode_InternFromString("new_empty")))
     return NULL;
   return PyModule_Create(&module);
 }

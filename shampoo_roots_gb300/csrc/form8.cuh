@@ -105,9 +105,9 @@ __device__ __forceinline__ float sum2(f2 v) {
 }
 
 struct F16 { f2 p[8]; };                               // 16 values
-template <typename T> struct Raw16;                    // 16 elements as stored
-template <> struct Raw16<__nv_bfloat16> { alignas(16) uint32_t w[8]; };
-template <> struct Raw16<float> { alignas(16) uint32_t w[16]; };
+template <typename T> struct Raw16;                    // 16 elements as stored; the last two: unaligned rows (load16)
+template <> struct Raw16<__nv_bfloat16> { alignas(16) uint32_t w[8]; uint32_t edge; int place; };
+template <> struct Raw16<float> { alignas(16) uint32_t w[16]; uint32_t edge; int place; };
 
 __device__ __forceinline__ void ld_sector(uint32_t* w, const void* p) {   // 32 bytes, 32-byte aligned
   asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -121,11 +121,15 @@ __device__ __forceinline__ void st_sector(void* p, const uint32_t* w) {
 
 // Elements c .. c + 15 of a row of `cols`; what lies past the row's end is zero.
 // VEC: rows begin at multiples of 32 bytes, and a thread takes whole sectors.
-// Otherwise the warp takes its 512 elements in stripes (lane l elements l, l +
-// 32, ...), which are consecutive in memory whatever the row's alignment (2 B a
-// lane at a stride of 32 B costs 16 times the L1 work), and settle() exchanges
-// them through the warp's scratch of 512 elements.  All lanes of a warp call
-// these together, with consecutive c.
+// Otherwise the warp's 512 elements are taken as the aligned granules of 16
+// bytes that lie inside them (lane l granules l, l + 32, ...: consecutive in
+// memory) and the elements before and after those, one a lane.  Registers wait
+// for no load before settle(), which brings them into order through the warp's
+// scratch: granules as they are, then 16 consecutive elements a lane out of
+// three or five granules, shifted by the row's offset.  Nothing outside the row
+// is read or written.  All lanes of a warp call these together, with
+// consecutive c.  (Element loads at a stride of 32, their halves joined at once,
+// took 122 us where this takes NORMU, for the norm of 20244 x 1213 bf16.)
 template <typename T> __device__ __forceinline__ uint32_t element_bits(const T* p);
 template <> __device__ __forceinline__ uint32_t element_bits(const __nv_bfloat16* p) { return *reinterpret_cast<const uint16_t*>(p); }
 template <> __device__ __forceinline__ uint32_t element_bits(const float* p) { return *reinterpret_cast<const uint32_t*>(p); }
@@ -133,12 +137,35 @@ template <typename T> struct Storage;
 template <> struct Storage<__nv_bfloat16> { typedef uint16_t type; };
 template <> struct Storage<float> { typedef uint32_t type; };
 
+// A warp's scratch: granules of 16 bytes, in an order in which lanes that read every second or fourth meet no bank twice.
+template <typename T> struct Scratch {
+  static constexpr int G = 16 / sizeof(T);             // elements of a granule
+  static constexpr int PER_LANE = 16 / G;              // granules a lane
+  static constexpr int BYTES = 512 * sizeof(T) + 128;  // one granule more, rounded up
+  static __device__ __forceinline__ int slot(int g) { return g ^ ((g >> 3) & 7); }
+  static __device__ __forceinline__ int element(int e) { return slot(e / G) * G + e % G; }
+};
+// An unaligned segment of up to 512 elements: `head` (1 .. G) elements, whole granules up to `tail`, the rest.
+template <typename T>
+struct Segment {
+  static constexpr int G = Scratch<T>::G;
+  int shift, head, len, tail, edge;                    // edge: this lane's single element, or -1
+  __device__ __forceinline__ Segment(const T* row, int c, int cols) {
+    const int lane = threadIdx.x & 31;
+    shift = (int)(reinterpret_cast<uintptr_t>(row) / sizeof(T)) & (G - 1);
+    head = G - shift;
+    len = min(cols - (c - 16 * lane), 512);
+    tail = head + max(len - head, 0) / G * G;
+    edge = lane < G ? (lane < head && lane < len ? lane : -1) : lane < 2 * G && tail + lane - G < len ? tail + lane - G : -1;
+  }
+};
+
 template <bool VEC, typename T>
 __device__ __forceinline__ void load16(Raw16<T>& o, const T* row, int c, int cols) {
   constexpr int E = 4 / sizeof(T);                       // elements a word
+  if (VEC) {
 #pragma unroll
-  for (int h = 0; h < 16 / E; h += 8) {                  // a sector: 8 words
-    if (VEC) {
+    for (int h = 0; h < 16 / E; h += 8) {                // a sector: 8 words
       const int at = c + h * E;
       if (at + 8 * E <= cols) {
         ld_sector(o.w + h, row + at);
@@ -151,47 +178,69 @@ __device__ __forceinline__ void load16(Raw16<T>& o, const T* row, int c, int col
             if (at + i * E + e < cols) o.w[h + i] |= element_bits(row + at + i * E + e) << (16 * e);
         }
       }
-    } else {
-      const int lane = threadIdx.x & 31, at = c - 15 * lane;   // the warp's first element, + lane
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        o.w[h + i] = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int k = at + 32 * ((h + i) * E + e);
-          if (k < cols) o.w[h + i] |= element_bits(row + k) << (16 * e);
-        }
-      }
     }
+    return;
   }
-}
-// From stripes to 16 consecutive elements a lane, and back.
-template <typename T>
-__device__ __forceinline__ void to_stripes(const Raw16<T>& o, typename Storage<T>::type* xs) {
-  constexpr int E = 4 / sizeof(T);
+  constexpr int G = Scratch<T>::G;
+  const Segment<T> s(row, c, cols);
   const int lane = threadIdx.x & 31;
+  const T* p = row + (c - 16 * lane);
 #pragma unroll
-  for (int i = 0; i < 16 / E; ++i)
+  for (int i = 0; i < Scratch<T>::PER_LANE; ++i) {
+    const int e = s.head + (lane + 32 * i) * G;
+    uint32_t* w = o.w + 4 * i;
+    w[0] = w[1] = w[2] = w[3] = 0;
+    if (e + G <= s.len)
+      asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p + e) : "memory");
+  }
+  o.edge = 0;
+  if (s.edge >= 0) o.edge = element_bits(p + s.edge);
+  // its element in the scratch (a head's past the row's end: zero), and the shift
+  const int at = s.edge >= 0 ? s.edge : lane < s.head ? lane : -1;
+  o.place = (at < 0 ? 0xFFF : Scratch<T>::element(at + s.shift)) | (s.shift << 12);
+}
+// n words of t from word (or, for the lowest bit of bf16, half word) `shift` on.
+template <int N, typename T>
+__device__ __forceinline__ void shift_words(uint32_t* t, uint32_t* out, int n, int shift) {
+  constexpr int E = 4 / sizeof(T);
 #pragma unroll
-    for (int e = 0; e < E; ++e) xs[32 * (i * E + e) + lane] = (typename Storage<T>::type)(o.w[i] >> (16 * e));
+  for (int k = 4; k > 0; k >>= 1) {
+    const bool on = shift & (k * E);
+#pragma unroll
+    for (int i = 0; i + k < N; ++i) t[i] = on ? t[i + k] : t[i];
+  }
+#pragma unroll
+  for (int i = 0; i < n; ++i) out[i] = E == 1 ? t[i] : __funnelshift_r(t[i], t[i + 1 < N ? i + 1 : i], (shift & 1) * 16);
 }
 template <bool VEC, typename T>
 __device__ __forceinline__ void settle(Raw16<T>& o, void* scratch) {
   if (VEC) return;
-  typename Storage<T>::type* xs = reinterpret_cast<typename Storage<T>::type*>(scratch);
-  to_stripes(o, xs);
-  __syncwarp();
-  const uint4* p = reinterpret_cast<const uint4*>(xs + 16 * (threadIdx.x & 31));
+  constexpr int P = Scratch<T>::PER_LANE;
+  uint4* xs = reinterpret_cast<uint4*>(scratch);
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(o.w) / 16; ++i) *reinterpret_cast<uint4*>(o.w + 4 * i) = p[i];
+  for (int i = 0; i < P; ++i)
+    xs[Scratch<T>::slot(lane + 32 * i + 1)] = make_uint4(o.w[4 * i], o.w[4 * i + 1], o.w[4 * i + 2], o.w[4 * i + 3]);
+  __syncwarp();
+  const int at = o.place & 0xFFF;
+  if (at != 0xFFF) reinterpret_cast<typename Storage<T>::type*>(scratch)[at] = (typename Storage<T>::type)o.edge;
+  __syncwarp();
+  uint32_t t[4 * P + 4];
+#pragma unroll
+  for (int i = 0; i <= P; ++i) {
+    const uint4 g = xs[Scratch<T>::slot(P * lane + i)];
+    t[4 * i] = g.x; t[4 * i + 1] = g.y; t[4 * i + 2] = g.z; t[4 * i + 3] = g.w;
+  }
+  shift_words<4 * P + 4, T>(t, o.w, 4 * P, o.place >> 12);
   __syncwarp();
 }
 template <bool VEC, typename T>
 __device__ __forceinline__ void store16(T* row, int c, int cols, const Raw16<T>& o, void* scratch) {
   constexpr int E = 4 / sizeof(T);
   typedef typename Storage<T>::type S;
-  S* p = reinterpret_cast<S*>(row);
   if (VEC) {
+    S* p = reinterpret_cast<S*>(row);
 #pragma unroll
     for (int h = 0; h < 16 / E; h += 8) {
       const int at = c + h * E;
@@ -205,15 +254,26 @@ __device__ __forceinline__ void store16(T* row, int c, int cols, const Raw16<T>&
     }
     return;
   }
-  S* xs = reinterpret_cast<S*>(scratch);
-  const int lane = threadIdx.x & 31, at = c - 15 * lane;
-  uint4* q = reinterpret_cast<uint4*>(xs + 16 * lane);
+  constexpr int G = Scratch<T>::G, P = Scratch<T>::PER_LANE;
+  const Segment<T> s(row, c, cols);
+  const int lane = threadIdx.x & 31;
+  S* p = reinterpret_cast<S*>(row) + (c - 16 * lane);
+  uint4* xs = reinterpret_cast<uint4*>(scratch);
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(o.w) / 16; ++i) q[i] = *reinterpret_cast<const uint4*>(o.w + 4 * i);
+  for (int i = 0; i < P; ++i)
+    xs[Scratch<T>::slot(P * lane + i)] = make_uint4(o.w[4 * i], o.w[4 * i + 1], o.w[4 * i + 2], o.w[4 * i + 3]);
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (at + 32 * i < cols) p[at + 32 * i] = xs[32 * i + lane];
+  for (int i = 0; i < P; ++i) {
+    const int k = lane + 32 * i, e = s.head + k * G;
+    if (e + G <= s.len) {                                // then k + 1 is a granule of the segment
+      const uint4 a = xs[Scratch<T>::slot(k)], b = xs[Scratch<T>::slot(k + 1)];
+      uint32_t t[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, v[4];
+      shift_words<8, T>(t, v, 4, s.head);
+      *reinterpret_cast<uint4*>(p + e) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  if (s.edge >= 0) p[s.edge] = reinterpret_cast<const S*>(scratch)[Scratch<T>::element(s.edge)];
   __syncwarp();
 }
 __device__ __forceinline__ F16 unpack(const Raw16<__nv_bfloat16>& o) {

@@ -21,6 +21,7 @@ using namespace precond;
 namespace {
 
 constexpr int64_t MAX_SIDE = (int64_t)1 << 30;     // rows, columns: kernels index a side with 32 bits
+constexpr int GRAD_IN_PLACE = 8192;                 // columns up to which a gradient may be written over its inputs
 constexpr int PLAN_SMS = 152;                       // a GB300's: sizes the dw workspace without a device
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -114,29 +115,42 @@ cudaError_t launch(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cuda
 }
 
 // ------------------------------------------------------------------------- norm
-// Threads of a row and rows of a block: 16 columns a thread up to `one` threads
-// (a norm's 384 leave two blocks on an SM), then 32 up to 512 threads where the
-// kernel has that form; longer rows take the kernels that read a row twice.
-// Blocks of short rows hold several, to have 256 threads.
-struct RowShape { int threads, rows, nv; };
-RowShape row_shape(int64_t cols, bool norm) {
-  const int64_t vec = (cols + 15) / 16, one = norm ? 384 : 512, two = norm ? 1024 : 0;
-  if (vec > std::max(one, two)) return {512, 1, 0};
-  const int nv = vec <= one ? 1 : 2;
-  const int threads = (int)std::max<int64_t>(32, ((vec + nv - 1) / nv + 31) / 32 * 32);
-  return {threads, std::min(8, std::max(1, 256 / threads)), nv};
+// Threads of a row and rows of a block.  A norm has 16 columns a thread up to
+// 384 threads (which leave two blocks of bf16 on an SM), then 32 up to 512
+// threads; a gradient 16 up to 512 threads (fp32: 384), then shares the row
+// among a cluster of 2 to 8 blocks.  Longer rows take the kernels that read a
+// row twice.  Blocks of short rows hold several; up to 256 columns, where rows
+// begin at sectors, a warp does.
+struct RowShape { int threads, rows, nv, parts; };
+RowShape row_shape(int64_t cols, int nv, int parts, int dtype, bool vec) {
+  const int64_t n = (cols + 15) / 16, mine = (n + nv * parts - 1) / (nv * parts);
+  const int threads = vec && n <= 16 ? (n <= 8 ? 8 : 16) : (int)std::max<int64_t>(32, (mine + 31) / 32 * 32);
+  return {threads, std::max(1, (dtype == PRECOND_BF16 ? 256 : 128) / threads), nv, parts};
+}
+RowShape norm_shape(int64_t cols, int dtype, bool vec) {
+  if (cols > 16 * 1024) return {512, 1, 0, 1};
+  return row_shape(cols, cols <= 16 * 384 ? 1 : 2, 1, dtype, vec);
+}
+RowShape grad_shape(int64_t cols, int dtype, bool vec) {
+  const int64_t one = 16 * (dtype == PRECOND_BF16 ? 512 : 384);
+  if (cols > 8 * one) return {512, 1, 0, 1};
+  return row_shape(cols, 1, (int)std::max<int64_t>(1, (cols + one - 1) / one), dtype, vec);
 }
 
-// Blocks of a persistent grid: 1024 threads an SM (norm: 80 registers a thread), 512 (gradient: 128).
-int64_t row_blocks_of(const RowShape& s, int64_t rows, int sms, bool norm) {
-  const int64_t resident = std::max(1, (norm ? 1024 : 512) / (s.threads * s.rows));
-  return std::max<int64_t>(1, std::min((rows + s.rows - 1) / s.rows, resident * sms));
+// Blocks (or clusters) of a persistent grid: what the registers let an SM hold (norm, bf16: 80 a thread; gradient,
+// bf16: 128; fp32: 168).
+int64_t row_blocks_of(const RowShape& s, int64_t rows, int sms, int sm_threads) {
+  const int64_t resident = std::max(1, sm_threads / (s.threads * s.rows));
+  return std::max<int64_t>(1, std::min((rows + s.rows - 1) / s.rows, resident * sms / s.parts));
+}
+int64_t grad_blocks(int64_t rows, int64_t cols, int dtype, bool vec, int sms) {
+  return row_blocks_of(grad_shape(cols, dtype, vec), rows, sms, dtype == PRECOND_BF16 ? 512 : 384);
 }
 
 template <typename T, bool VEC>
 cudaError_t launch_norm(const RmsNormArgs& a, const RowShape& s, unsigned grid, cudaStream_t st) {
   const dim3 block(s.threads, s.rows);
-  const size_t smem = VEC ? 0 : (size_t)s.threads * s.rows * 16 * sizeof(T);    // the warps' exchange buffers
+  const size_t smem = VEC ? 0 : (size_t)s.threads * s.rows / 32 * Scratch<T>::BYTES;    // the warps' exchange buffers
   switch (s.nv) {
     case 1: return launch(rms_norm_kernel<T, 1, VEC>, dim3(grid), block, smem, st, 1, a);
     case 2: return launch(rms_norm_kernel<T, 2, VEC>, dim3(grid), block, smem, st, 1, a);
@@ -147,11 +161,10 @@ template <typename T, bool VEC>
 cudaError_t launch_grad(const RmsGradArgs& a, const RowShape& s, unsigned grid, cudaStream_t st) {
   const dim3 block(s.threads, s.rows);
   // the warps' exchange buffers, and then the dw sums of the rows side by side
-  const size_t smem = std::max<size_t>(VEC ? 0 : (size_t)s.threads * s.rows * 16 * sizeof(T), s.rows > 1 ? (size_t)s.threads * s.rows * 64 : 0);
-  switch (s.nv) {
-    case 1: return launch(rms_grad_kernel<T, 1, VEC>, dim3(grid), block, smem, st, 1, a);
-    default: return launch(rms_grad_long_kernel<T, VEC>, dim3(grid), block, smem, st, 1, a);
-  }
+  const size_t smem = std::max<size_t>(VEC ? 0 : (size_t)s.threads * s.rows / 32 * Scratch<T>::BYTES, s.rows > 1 ? (size_t)s.threads * s.rows * 64 : 0);
+  if (s.nv == 0) return launch(rms_grad_long_kernel<T, VEC>, dim3(grid), block, smem, st, 1, a);
+  if (s.parts > 1) return launch(rms_grad_kernel<T, VEC, true>, dim3(grid * s.parts), block, smem, st, s.parts, a);
+  return launch(rms_grad_kernel<T, VEC, false>, dim3(grid), block, smem, st, 1, a);
 }
 
 // ------------------------------------------------------------------------- distillation
@@ -267,10 +280,10 @@ int precond_rms_norm(precond_t ph, const void* x, const void* residual, const vo
   if (rc) return rc;
   RmsNormArgs a = {x, residual, weight, total, y, (uint8_t*)q, scale, rstd, ldx, ldr, ldt, ldy, ldq, (int)rows, (int)cols, eps,
                    weight_dtype == PRECOND_BF16};
-  const RowShape s = row_shape(cols, true);
-  const unsigned grid = (unsigned)row_blocks_of(s, q ? q8_row_blocks(rows) * 128 : rows, h->num_sms, true);
   const bool vec = sector_rows(x, ldx, dtype) && sector_rows(residual, ldr, dtype) && sector_rows(total, ldt, dtype) &&
                    sector_rows(y, ldy, dtype);
+  const RowShape s = norm_shape(cols, dtype, vec);
+  const unsigned grid = (unsigned)row_blocks_of(s, q ? q8_row_blocks(rows) * 128 : rows, h->num_sms, dtype == PRECOND_BF16 ? 768 : 384);
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == PRECOND_BF16)
     OP_CK((vec ? launch_norm<__nv_bfloat16, true>(a, s, grid, st) : launch_norm<__nv_bfloat16, false>(a, s, grid, st)));
@@ -283,8 +296,9 @@ int precond_rms_norm(precond_t ph, const void* x, const void* residual, const vo
 int64_t precond_rms_norm_grad_workspace(int64_t rows, int64_t cols) {
   if (!side(rows) || !side(cols)) return -1;
   if (rows == 0 || cols == 0) return 0;
-  const RowShape s = row_shape(cols, false);
-  return row_blocks_of(s, rows, PLAN_SMS, false) * cols * 4;
+  // of either type; rows in parts of a warp take fewer blocks
+  return std::max(grad_blocks(rows, cols, PRECOND_BF16, false, PLAN_SMS), grad_blocks(rows, cols, PRECOND_F32, false, PLAN_SMS)) *
+         cols * 4;
 }
 
 int precond_rms_norm_grad(precond_t ph, const void* dy, const void* x, const void* weight, const float* rstd,
@@ -305,8 +319,8 @@ int precond_rms_norm_grad(precond_t ph, const void* dy, const void* x, const voi
   const Range out[3] = {range(dx, rows, lddx, cols, sz), range(dw, 1, 0, cols, 4), range(workspace, 1, 0, need, 1)};
   for (int i = 0; i < 3; ++i) {
     for (int j = 0; j < 5; ++j) {
-      // dx may lie over dy, dresidual or x, element for element, where a row is read once
-      const bool same = i == 0 && row_shape(cols, false).nv &&
+      // dx may lie over dy, dresidual or x, element for element, where a row is surely read once
+      const bool same = i == 0 && cols <= GRAD_IN_PLACE &&
                         ((j == 0 && dx == dy && lddx == lddy) || (j == 1 && dx == dresidual && lddx == lddr) ||
                          (j == 2 && dx == x && lddx == ldx));
       if (!same && overlap(out[i], in[j])) return PRECOND_EINVAL;
@@ -325,10 +339,10 @@ int precond_rms_norm_grad(precond_t ph, const void* dy, const void* x, const voi
   }
   RmsGradArgs a = {dy, x, dresidual, weight, rstd, dx, (float*)workspace, lddy, ldx, lddr, lddx, (int)rows, (int)cols,
                    weight_dtype == PRECOND_BF16};
-  const RowShape s = row_shape(cols, false);
-  const unsigned grid = (unsigned)row_blocks_of(s, rows, std::min(h->num_sms, PLAN_SMS), false);
   const bool vec = sector_rows(dy, lddy, dtype) && sector_rows(x, ldx, dtype) && sector_rows(dresidual, lddr, dtype) &&
                    sector_rows(dx, lddx, dtype);
+  const RowShape s = grad_shape(cols, dtype, vec);
+  const unsigned grid = (unsigned)grad_blocks(rows, cols, dtype, vec, std::min(h->num_sms, PLAN_SMS));
   if (dtype == PRECOND_BF16)
     OP_CK((vec ? launch_grad<__nv_bfloat16, true>(a, s, grid, st) : launch_grad<__nv_bfloat16, false>(a, s, grid, st)));
   else

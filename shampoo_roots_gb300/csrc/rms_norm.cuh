@@ -13,9 +13,13 @@
 // meet at one barrier a row.
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include "form8.cuh"
 
 namespace precond {
+
+namespace cg = cooperative_groups;
 
 struct RmsNormArgs {
   const void* x; const void* r; const void* w; void* h; void* y;
@@ -28,7 +32,7 @@ struct RmsNormArgs {
 
 struct RmsGradArgs {
   const void* dy; const void* x; const void* dr; const void* w; const float* rstd;
-  void* dx; float* partial;           // partial: [gridDim.x][cols]
+  void* dx; float* partial;           // partial: [blocks, or clusters][cols]
   int64_t lddy, ldx, lddr, lddx;
   int rows, cols;
   int w_bf16;
@@ -50,12 +54,16 @@ __device__ __forceinline__ f2 squares(const F16& v, f2 s) {
   return s;
 }
 
-// Sum over the blockDim.x threads of one row (blockDim.x a multiple of 32), the
+// Sum over the blockDim.x threads of one row (8, 16 or a multiple of 32), the
 // same value in each.  `red` has room for 2 x blockDim.y x 32, zeroed; calls
 // alternate between its halves, so that one barrier a call is enough.
 __device__ __forceinline__ float row_sum(float v, float* red, int half) {
-  v = warp_sum(v);
   const int nw = blockDim.x >> 5;
+  if (nw == 0) {
+    for (int o = blockDim.x >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+  v = warp_sum(v);
   if (nw == 1) return v;
   float* mine = red + (half * blockDim.y + threadIdx.y) * 32;
   if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = v;
@@ -66,6 +74,48 @@ __device__ __forceinline__ float row_sum(float v, float* red, int half) {
     s = make_float4(s.x + t.x, s.y + t.y, s.z + t.z, s.w + t.w);
   }
   return (s.x + s.y) + (s.z + s.w);
+}
+// The same over the blocks of a cluster (blockDim.y is 1, at most 16 warps a
+// block).  Every warp leaves its sum with each block, as a word that also holds
+// the number of the call, and every warp polls its own block's words: the join
+// waits for these sums alone.  (A cluster barrier, or any release, also waits
+// for the previous row's dx to reach L2: 110 us where this takes GRADC, for the
+// gradient of 3000 x 16384 bf16.)  Calls alternate between the halves of
+// `slots` (2 x 8 x 16, zeroed in every block): a warp writes for call n + 2 when
+// it has seen call n + 1 from every warp, so that all of them have read call n.
+// The blocks of a cluster are resident together; a wait that runs out all the
+// same gives NaN, for this row and the block's later ones.
+__device__ __forceinline__ float cluster_row_sum(float v, unsigned long long* slots, unsigned call, bool& lost) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int parts = (int)cluster.num_blocks(), lane = threadIdx.x & 31;
+  v = warp_sum(v);
+  unsigned long long* mine = slots + (call & 1) * 128;
+  if (lane < parts) {
+    uint32_t to;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+        : "=r"(to) : "r"((uint32_t)__cvta_generic_to_shared(mine + cluster.block_rank() * 16 + (threadIdx.x >> 5))), "r"(lane));
+    asm volatile("st.relaxed.cluster.shared::cluster.u64 [%0], %1;"
+                 ::"r"(to), "l"((unsigned long long)call << 32 | __float_as_uint(v)) : "memory");
+  }
+  const int nw = blockDim.x >> 5;
+  float s = 0.f;
+#pragma unroll 1
+  for (int i = lane; i < 16 * parts; i += 32) {
+    if ((i & 15) >= nw) continue;
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(mine + i);
+    unsigned long long got = 0;
+    for (int spin = 0; !lost; ++spin) {
+      asm volatile("ld.relaxed.cluster.shared::cta.u64 %0, [%1];" : "=l"(got) : "r"(at) : "memory");
+      if ((unsigned)(got >> 32) == call) break;
+      if (spin > 20000000) lost = true;
+    }
+    s += __uint_as_float((unsigned)got);
+  }
+  if (__any_sync(0xffffffffu, lost)) {
+    lost = true;
+    s = __uint_as_float(0x7FFFFFFFu);
+  }
+  return warp_sum(s);
 }
 __device__ __forceinline__ void zero_red(float* red, int n) {
   for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < n; i += blockDim.x * blockDim.y) red[i] = 0.f;
@@ -88,21 +138,21 @@ __device__ __forceinline__ void add_stream(Raw16<float>& x, const Raw16<float>& 
 template <typename T, bool VEC>
 __device__ __forceinline__ void* warp_scratch() {
   extern __shared__ __align__(16) uint8_t row_scratch[];
-  return VEC ? nullptr : row_scratch + ((threadIdx.y * blockDim.x + threadIdx.x) >> 5) * (512 * sizeof(T));
+  return VEC ? nullptr : row_scratch + ((threadIdx.y * blockDim.x + threadIdx.x) >> 5) * Scratch<T>::BYTES;
 }
 
 // One vector's outputs; `at` is its scale byte's place.
 template <typename T, bool VEC>
-__device__ __forceinline__ void norm_write(const RmsNormArgs& a, int64_t row, int c, F16& y, size_t at, void* xs) {
+__device__ __forceinline__ void norm_write(const RmsNormArgs& a, int64_t row, int c, int cols, F16& y, size_t at, void* xs) {
   if (a.y) {
     Raw16<T> o;
     pack(o, y);
-    store16<VEC>(reinterpret_cast<T*>(a.y) + row * a.ldy, c, a.cols, o, xs);
+    store16<VEC>(reinterpret_cast<T*>(a.y) + row * a.ldy, c, cols, o, xs);
   }
   if (a.q) {
     const unsigned b = q8_block_exponent(y);
-    store_q16(a.q + row * a.ldq, c, a.cols, q8_pack16(y, q8_inverse(b)));
-    if ((threadIdx.x & 7) == 0 && c < a.cols) a.scale[at] = (uint8_t)b;
+    store_q16(a.q + row * a.ldq, c, cols, q8_pack16(y, q8_inverse(b)));
+    if ((threadIdx.x & 7) == 0 && c < cols) a.scale[at] = (uint8_t)b;
   }
 }
 // The scale bytes past the matrix's end: a row's trailing blocks, or a whole row of padding.
@@ -121,9 +171,11 @@ __device__ __forceinline__ float rstd_of(float sum, float inv_cols, float eps) {
   return x < 1e30f ? z : y;            // x y y may overflow only where x does
 }
 
-// NV vectors of 16 columns a thread.
+// NV vectors of 16 columns a thread.  Rows of up to 256 columns share a warp
+// (blockDim.x 8 or 16): its lanes stay together, and rows past the last count as
+// rows of no columns.
 template <typename T, int NV, bool VEC>
-__global__ void __launch_bounds__(NV == 1 ? 384 : 512, NV == 1 ? 2 : 1) rms_norm_kernel(RmsNormArgs a) {
+__global__ void __launch_bounds__(NV == 1 ? 384 : 512, NV == 1 && sizeof(T) == 2 ? 2 : 1) rms_norm_kernel(RmsNormArgs a) {
   __shared__ __align__(16) float red[2 * 8 * 32];
   zero_red(red, 2 * 8 * 32);
   wait_for_previous();
@@ -132,6 +184,8 @@ __global__ void __launch_bounds__(NV == 1 ? 384 : 512, NV == 1 ? 2 : 1) rms_norm
   const int64_t rblocks = q8_row_blocks(a.rows);
   const int step = gridDim.x * blockDim.y;
   int row = blockIdx.x * blockDim.y + threadIdx.y;
+  const int below = blockDim.x < 32 ? (threadIdx.x + threadIdx.y * blockDim.x) % 32 / blockDim.x : 0;   // rows below it in its warp
+  int cols = row < a.rows ? a.cols : 0;
   const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
   const T* r = reinterpret_cast<const T*>(a.r) + row * a.ldr;
   const float inv_cols = 1.0f / (float)a.cols;
@@ -143,14 +197,14 @@ __global__ void __launch_bounds__(NV == 1 ? 384 : 512, NV == 1 ? 2 : 1) rms_norm
     w[j] = load_w16(a.w, a.w_bf16, c[j], a.cols);
   }
   Raw16<T> nx[NV], nr[NV];
-  if (row < a.rows) {
+  if (row - below < a.rows) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      load16<VEC>(nx[j], x, c[j], a.cols);
-      if (a.r) load16<VEC>(nr[j], r, c[j], a.cols);
+      load16<VEC>(nx[j], x, c[j], cols);
+      if (a.r) load16<VEC>(nr[j], r, c[j], cols);
     }
   }
-  for (int half = 0; row < a.rows; row += step, half ^= 1) {
+  for (int half = 0; row - below < a.rows; row += step, half ^= 1) {
     F16 v[NV];
     f2 ss = 0;
 #pragma unroll
@@ -159,33 +213,36 @@ __global__ void __launch_bounds__(NV == 1 ? 384 : 512, NV == 1 ? 2 : 1) rms_norm
       if (a.r) {
         settle<VEC>(nr[j], xs);
         add_stream(nx[j], nr[j]);
-        store16<VEC>(reinterpret_cast<T*>(a.h) + row * a.ldh, c[j], a.cols, nx[j], xs);
+        store16<VEC>(reinterpret_cast<T*>(a.h) + row * a.ldh, c[j], cols, nx[j], xs);
       }
       v[j] = unpack(nx[j]);
       ss = squares(v[j], ss);
     }
     x += step * a.ldx;
     r += step * a.ldr;
-    if (row + step < a.rows) {
+    const int next = row + step < a.rows ? a.cols : 0;
+    if (row + step - below < a.rows) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        load16<VEC>(nx[j], x, c[j], a.cols);
-        if (a.r) load16<VEC>(nr[j], r, c[j], a.cols);
+        load16<VEC>(nx[j], x, c[j], next);
+        if (a.r) load16<VEC>(nr[j], r, c[j], next);
       }
     }
     const float rstd = rstd_of(row_sum(sum2(ss), red, half), inv_cols, a.eps);
-    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
-    if (!a.q && !a.y) continue;
-    const f2 rs = f2_of(rstd, rstd);
-    const size_t at_row = q8_scale_at(row, 0, rblocks);
+    if (a.rstd && threadIdx.x == 0 && cols) a.rstd[row] = rstd;
+    if (a.q || a.y) {
+      const f2 rs = f2_of(rstd, rstd);
+      const size_t at_row = q8_scale_at(row, 0, rblocks);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
+      for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j].p[i] = mul2(mul2(v[j].p[i], rs), w[j].p[i]);
-      const int kb = c[j] >> 7;
-      norm_write<T, VEC>(a, row, c[j], v[j], (size_t)(kb >> 2) * rblocks * 512 + (kb & 3) + at_row, xs);
+        for (int i = 0; i < 8; ++i) v[j].p[i] = mul2(mul2(v[j].p[i], rs), w[j].p[i]);
+        const int kb = c[j] >> 7;
+        norm_write<T, VEC>(a, row, c[j], cols, v[j], (size_t)(kb >> 2) * rblocks * 512 + (kb & 3) + at_row, xs);
+      }
+      if (a.q && (a.cols & 511) && row < rblocks * 128) norm_pad(a, row, rblocks);
     }
-    if (a.q && (a.cols & 511)) norm_pad(a, row, rblocks);
+    cols = next;
   }
   if (a.q)
     for (; row < rblocks * 128; row += step) norm_pad(a, row, rblocks);
@@ -236,7 +293,7 @@ __global__ void __launch_bounds__(512, 2) rms_norm_long_kernel(RmsNormArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v.p[i] = mul2(mul2(v.p[i], rs), w.p[i]);
       const int kb = (int)(c >> 7);
-      norm_write<T, VEC>(a, row, (int)c, v, q8_scale_at(row, kb, rblocks), xs);
+      norm_write<T, VEC>(a, row, (int)c, a.cols, v, q8_scale_at(row, kb, rblocks), xs);
     }
   }
 }
@@ -267,92 +324,88 @@ __device__ __forceinline__ void grad_out(Raw16<T>& o, const F16& g, const F16& n
   pack(o, d);
 }
 
-template <typename T, int NV, bool VEC>
-__global__ void __launch_bounds__(512, 1) rms_grad_kernel(RmsGradArgs a) {
-  __shared__ __align__(16) float red[2 * 8 * 32];
+// fp32 takes 168 registers a thread: with 128 the vectors in flight do not fit.
+template <typename T, bool VEC, bool CLUSTER>
+__global__ void __launch_bounds__(sizeof(T) == 4 ? 384 : 512, 1) rms_grad_kernel(RmsGradArgs a) {
+  __shared__ __align__(16) float red[2 * 8 * 32];      // of a cluster: its 2 x 8 x 16 words
   zero_red(red, 2 * 8 * 32);
+  constexpr bool EARLY = sizeof(T) == 2 && VEC;        // dr with the row's other vectors (else there is no room for it)
+  if (CLUSTER) cg::this_cluster().sync();
   wait_for_previous();
   let_next_start();
   void* xs = warp_scratch<T, VEC>();
-  const int step = gridDim.x * blockDim.y;
-  int row = blockIdx.x * blockDim.y + threadIdx.y;
+  const int parts = CLUSTER ? (int)cg::this_cluster().num_blocks() : 1;
+  const int group = CLUSTER ? blockIdx.x / parts : blockIdx.x;          // of blocks that share rows
+  const int step = (CLUSTER ? gridDim.x / parts : gridDim.x) * blockDim.y;
+  int row = group * blockDim.y + threadIdx.y;
+  const int below = blockDim.x < 32 ? (threadIdx.x + threadIdx.y * blockDim.x) % 32 / blockDim.x : 0;   // as in the norm
+  int cols = row < a.rows ? a.cols : 0;
   const T* dy = reinterpret_cast<const T*>(a.dy) + row * a.lddy;
   const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
   const T* dr = reinterpret_cast<const T*>(a.dr) + row * a.lddr;
   T* dx = reinterpret_cast<T*>(a.dx) + row * a.lddx;
   const float inv_cols = 1.0f / (float)a.cols;
-  int c[NV];
-  F16 w[NV], dw[NV];
+  const int c = ((CLUSTER ? (int)cg::this_cluster().block_rank() * (int)blockDim.x : 0) + threadIdx.x) * 16;
+  const F16 w = load_w16(a.w, a.w_bf16, c, a.cols);
+  F16 dw;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    c[j] = (j * blockDim.x + threadIdx.x) * 16;
-    w[j] = load_w16(a.w, a.w_bf16, c[j], a.cols);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dw[j].p[i] = 0;
-  }
-  Raw16<T> ny[NV], nx[NV], nr[NV];
+  for (int i = 0; i < 8; ++i) dw.p[i] = 0;
+  Raw16<T> ny, nx, nr;
   float nrstd = 0.f;
-  auto fetch = [&](int k) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      load16<VEC>(ny[j], dy, c[j], a.cols);
-      load16<VEC>(nx[j], x, c[j], a.cols);
-      if (a.dr) load16<VEC>(nr[j], dr, c[j], a.cols);
-    }
-    nrstd = a.rstd[k];
+  bool lost = false;
+  if (row - below < a.rows) {
+    load16<VEC>(ny, dy, c, cols);
+    load16<VEC>(nx, x, c, cols);
+    if (a.dr) load16<VEC>(nr, dr, c, cols);
+    if (cols) nrstd = a.rstd[row];
+  }
+  for (unsigned call = 1; row - below < a.rows; row += step, ++call) {
+    const f2 rs = f2_of(nrstd, nrstd);
+    const bool more = row + step - below < a.rows;
+    const int next = row + step < a.rows ? a.cols : 0;
+    Raw16<T> res = nr;
+    settle<VEC>(ny, xs);
+    settle<VEC>(nx, xs);
+    F16 g = unpack(ny), n = unpack(nx);
+    const f2 dot = grad_terms(g, n, w, dw, rs, 0);
     dy += step * a.lddy;
     x += step * a.ldx;
     dr += step * a.lddr;
-  };
-  if (row < a.rows) fetch(row);
-  for (int half = 0; row < a.rows; row += step, half ^= 1) {
-    const f2 rs = f2_of(nrstd, nrstd);
-    F16 g[NV], n[NV];
-    Raw16<T> res[NV];
-    f2 dot = 0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      settle<VEC>(ny[j], xs);
-      settle<VEC>(nx[j], xs);
-      g[j] = unpack(ny[j]);
-      n[j] = unpack(nx[j]);
-      if (a.dr) {
-        settle<VEC>(nr[j], xs);
-        res[j] = nr[j];
-      }
-      dot = grad_terms(g[j], n[j], w[j], dw[j], rs, dot);
+    if (more) {
+      load16<VEC>(ny, dy, c, next);
+      load16<VEC>(nx, x, c, next);
+      if (EARLY && a.dr) load16<VEC>(nr, dr, c, next);
+      if (next) nrstd = a.rstd[row + step];
     }
-    if (row + step < a.rows) fetch(row + step);
-    const float mean = -row_sum(sum2(dot), red, half) * inv_cols;
-    const f2 mm = f2_of(mean, mean);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      Raw16<T> o;
-      grad_out(o, g[j], n[j], rs, mm, a.dr ? &res[j] : nullptr);
-      store16<VEC>(dx, c[j], a.cols, o, xs);
-    }
+    const float sum = CLUSTER ? cluster_row_sum(sum2(dot), reinterpret_cast<unsigned long long*>(red), call, lost)
+                              : row_sum(sum2(dot), red, call & 1);
+    const float mean = -sum * inv_cols;
+    Raw16<T> o;
+    if (a.dr) settle<VEC>(res, xs);
+    grad_out(o, g, n, rs, f2_of(mean, mean), a.dr ? &res : nullptr);
+    if (!EARLY && more && a.dr) load16<VEC>(nr, dr, c, next);    // used after the next row's join
+    store16<VEC>(dx, c, cols, o, xs);
     dx += step * a.lddx;
+    cols = next;
   }
-  if (blockDim.y > 1) {                  // the block's rows side by side (NV is 1): in their order, through shared memory
+  if (blockDim.y > 1) {                  // the block's rows side by side: in their order, through shared memory
     extern __shared__ __align__(16) uint8_t row_scratch[];
     F16* side = reinterpret_cast<F16*>(row_scratch);
     __syncthreads();                     // the exchange buffers lie there too
-    side[threadIdx.y * blockDim.x + threadIdx.x] = dw[0];
+    side[threadIdx.y * blockDim.x + threadIdx.x] = dw;
     __syncthreads();
     if (threadIdx.y > 0) return;
     for (int y = 1; y < blockDim.y; ++y)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dw[0].p[i] = add2(dw[0].p[i], side[y * blockDim.x + threadIdx.x].p[i]);
+      for (int i = 0; i < 8; ++i) dw.p[i] = add2(dw.p[i], side[y * blockDim.x + threadIdx.x].p[i]);
   }
-  float* out = a.partial + (int64_t)blockIdx.x * a.cols;
+  float* out = a.partial + (int64_t)group * a.cols;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 d = f2_get(dw[j].p[i]);
-      if (c[j] + 2 * i < a.cols) out[c[j] + 2 * i] = d.x;
-      if (c[j] + 2 * i + 1 < a.cols) out[c[j] + 2 * i + 1] = d.y;
-    }
+  for (int i = 0; i < 8; ++i) {
+    const float2 d = f2_get(dw.p[i]);
+    if (c + 2 * i < a.cols) out[c + 2 * i] = d.x;
+    if (c + 2 * i + 1 < a.cols) out[c + 2 * i + 1] = d.y;
+  }
 }
 
 // Rows too long for registers: the block's dw sums live in its row of `partial`

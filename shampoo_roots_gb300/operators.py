@@ -41,7 +41,8 @@ def _load_binding():
     m.set_up((torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.uint8, torch.int32, torch.int64),
              torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else _current_stream,
              tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (
-                 L.precond_rms_norm, L.precond_rms_norm_grad, L.precond_quantize8, L.precond_gemm8, L.precond_distill, L.precond_distill_workspace)))
+                 L.precond_rms_norm, L.precond_rms_norm_grad, L.precond_rms_norm_grad_workspace, L.precond_quantize8, L.precond_gemm8,
+                 L.precond_distill, L.precond_distill_workspace)))
     return m
 
 
@@ -94,10 +95,6 @@ def precond_rms_norm_grad(h, dy, x, weight, rstd, dx, dw, dresidual=None, worksp
                           raw: bool = False) -> int:
     """dx and dw of precond_rms_norm; x is the forward pass's total.  Without a workspace one comes from torch's
     allocator (on the current stream; give one together with another ``stream``)."""
-    if workspace is None:
-        if stream is not None and _stream(stream) != _stream(None):
-            raise ValueError("give a workspace with a stream other than torch's current one")
-        workspace = torch.empty(load().precond_rms_norm_grad_workspace(*dy.shape), dtype=torch.uint8, device=dy.device)
     code = _b.rms_norm_grad(h, dy, x, weight, rstd, dx, dw, dresidual, workspace, stream)
     return code if raw or code == OK else _check(code, "precond_rms_norm_grad")
 
@@ -136,9 +133,4 @@ def precond_distill(h, logits, ids, teacher, loss, weight=None, temperature: flo
     with ``dlogits``, its gradient (in place if it is ``logits``).  Without a workspace one comes from torch's
     allocator where the call needs it (on the current stream; give one together with another ``stream``)."""
     code = _b.distill(h, logits, ids, teacher, loss, weight, temperature, dlogits, workspace, stream)
-    if code < -1000:
-        if stream is not None and _stream(stream) != _stream(None):
-            raise ValueError("give a workspace with a stream other than torch's current one")
-        workspace = torch.empty(-1000 - code, dtype=torch.uint8, device=logits.device)
-        code = _b.distill(h, logits, ids, teacher, loss, weight, temperature, dlogits, workspace, stream)
     return code if raw or code == OK else _check(code, "precond_distill")
