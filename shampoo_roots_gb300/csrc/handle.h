@@ -22,6 +22,7 @@ struct Handle {
   EncodeTiledFn encode = nullptr;
   unsigned int* op_err = nullptr;      // operators: device word, set when a bounded wait ran out
   int pairs = 0;                       // operators: CTA pairs that are resident at once
+  int clusters[9] = {};                // operators: clusters of n blocks that are resident at once, one block on an SM
   bool op_ready = false;               // operators: kernel attributes set on this device
 };
 

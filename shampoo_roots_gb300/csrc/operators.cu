@@ -23,6 +23,7 @@ namespace {
 constexpr int64_t MAX_SIDE = (int64_t)1 << 30;     // rows, columns: kernels index a side with 32 bits
 constexpr int GRAD_IN_PLACE = 8192;                 // columns up to which a gradient may be written over its inputs
 constexpr int PLAN_SMS = 152;                       // a GB300's: sizes the dw workspace without a device
+constexpr int PLAN_CLUSTERS[9] = {0, 152, 76, 0, 38, 0, 0, 0, 19};
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 size_t size_of(int dtype) { return dtype == PRECOND_F32 ? 4 : dtype == PRECOND_BF16 ? 2 : 1; }
@@ -88,6 +89,20 @@ int prepare(Handle* h) {
     cfg.dynamicSmemBytes = PairSmem::BYTES;
     OP_CK(cudaOccupancyMaxActiveClusters(&h->pairs, gemm8_pair_kernel<false>, &cfg));
     if (h->pairs < 1) return PRECOND_ECUDA;
+    for (int n = 2; n <= 8; n *= 2) {
+      cudaLaunchAttribute size = {};
+      size.id = cudaLaunchAttributeClusterDimension;
+      size.val.clusterDim.x = n;
+      size.val.clusterDim.y = size.val.clusterDim.z = 1;
+      cfg.gridDim = dim3(n * PLAN_CLUSTERS[n]);
+      cfg.blockDim = dim3(512);
+      cfg.dynamicSmemBytes = 0;
+      cfg.attrs = &size;
+      cfg.numAttrs = 1;
+      OP_CK(cudaOccupancyMaxActiveClusters(&h->clusters[n], rms_grad_kernel<__nv_bfloat16, true, ROW_CLUSTER>, &cfg));
+      h->clusters[n] = std::min(h->clusters[n], PLAN_CLUSTERS[n]);
+      if (h->clusters[n] < 1) return PRECOND_ECUDA;
+    }
     OP_CK(cudaMalloc(&h->op_err, sizeof(unsigned int)));
     OP_CK(cudaMemset(h->op_err, 0, sizeof(unsigned int)));
     OP_CK(cudaDeviceSynchronize());
@@ -115,56 +130,60 @@ cudaError_t launch(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cuda
 }
 
 // ------------------------------------------------------------------------- norm
-// Threads of a row and rows of a block.  A norm has 16 columns a thread up to
-// 384 threads (which leave two blocks of bf16 on an SM), then 32 up to 512
-// threads; a gradient 16 up to 512 threads (fp32: 384), then shares the row
-// among a cluster of 2 to 8 blocks.  Longer rows take the kernels that read a
-// row twice.  Blocks of short rows hold several; up to 256 columns, where rows
-// begin at sectors, a warp does.
-struct RowShape { int threads, rows, nv, parts; };
-RowShape row_shape(int64_t cols, int nv, int parts, int dtype, bool vec) {
-  const int64_t n = (cols + 15) / 16, mine = (n + nv * parts - 1) / (nv * parts);
+// Threads of a row, rows of a block and blocks of a row.  16 columns a thread, up
+// to 384 threads (a bf16 gradient: 512); then a norm of aligned rows has 32 up
+// to 512 threads, and what is still longer a cluster of 2, 4 or 8 blocks (3 took
+// 1.9 times as long as 4 for a norm of 16384 columns; 32 columns a thread 63 us
+// where a cluster of 4 took 74).  Longer rows (parts 0) take the kernels that
+// read a row twice.  Blocks of short rows hold several; up to 256 columns, where
+// rows begin at sectors, a warp does.
+struct RowShape { int threads, rows, vectors, parts; };
+RowShape row_shape(int64_t cols, int dtype, bool grad, bool vec) {
+  const int64_t one = grad && dtype == PRECOND_BF16 ? 512 : 384, n = (cols + 15) / 16;
+  if (!grad && vec && n > one && n <= 1024) return {(int)((n + 63) / 64 * 32), 1, 2, 1};
+  int parts = 1;
+  while (parts < 8 && n > parts * one) parts *= 2;
+  if (n > parts * one) return {512, 1, 0, 0};
+  const int64_t mine = (n + parts - 1) / parts;
   const int threads = vec && n <= 16 ? (n <= 8 ? 8 : 16) : (int)std::max<int64_t>(32, (mine + 31) / 32 * 32);
-  return {threads, std::max(1, (dtype == PRECOND_BF16 ? 256 : 128) / threads), nv, parts};
-}
-RowShape norm_shape(int64_t cols, int dtype, bool vec) {
-  if (cols > 16 * 1024) return {512, 1, 0, 1};
-  return row_shape(cols, cols <= 16 * 384 ? 1 : 2, 1, dtype, vec);
-}
-RowShape grad_shape(int64_t cols, int dtype, bool vec) {
-  const int64_t one = 16 * (dtype == PRECOND_BF16 ? 512 : 384);
-  if (cols > 8 * one) return {512, 1, 0, 1};
-  return row_shape(cols, 1, (int)std::max<int64_t>(1, (cols + one - 1) / one), dtype, vec);
+  return {threads, parts > 1 ? 1 : std::max(1, (dtype == PRECOND_BF16 ? 256 : 128) / threads), 1, parts};
 }
 
-// Blocks (or clusters) of a persistent grid: what the registers let an SM hold (norm, bf16: 80 a thread; gradient,
-// bf16: 128; fp32: 168).
-int64_t row_blocks_of(const RowShape& s, int64_t rows, int sms, int sm_threads) {
+// Blocks (or clusters) of a persistent grid: what the registers let an SM hold
+// (norm of aligned bf16 rows, 16 columns a thread: 80 registers; other bf16:
+// 128; fp32: 168).  Fewer clusters fit than SMs would hold, as each lies within
+// a part of the chip; `clusters` of them with one block on an SM.
+int64_t row_blocks_of(const RowShape& s, int64_t rows, int sm_threads, int sms, const int* clusters) {
   const int64_t resident = std::max(1, sm_threads / (s.threads * s.rows));
-  return std::max<int64_t>(1, std::min((rows + s.rows - 1) / s.rows, resident * sms / s.parts));
+  const int64_t most = resident * (s.parts > 1 ? clusters[s.parts] : sms);
+  return std::max<int64_t>(1, std::min((rows + s.rows - 1) / s.rows, most));
 }
-int64_t grad_blocks(int64_t rows, int64_t cols, int dtype, bool vec, int sms) {
-  return row_blocks_of(grad_shape(cols, dtype, vec), rows, sms, dtype == PRECOND_BF16 ? 512 : 384);
+int64_t norm_blocks(const RowShape& s, int64_t rows, int dtype, bool vec, int sms, const int* clusters) {
+  return row_blocks_of(s, rows, s.vectors == 2 ? 512 : dtype == PRECOND_F32 ? 384 : vec ? 768 : 512, sms, clusters);
+}
+int64_t grad_blocks(const RowShape& s, int64_t rows, int dtype, int sms, const int* clusters) {
+  return row_blocks_of(s, rows, dtype == PRECOND_F32 ? 384 : 512, sms, clusters);
 }
 
 template <typename T, bool VEC>
 cudaError_t launch_norm(const RmsNormArgs& a, const RowShape& s, unsigned grid, cudaStream_t st) {
   const dim3 block(s.threads, s.rows);
   const size_t smem = VEC ? 0 : (size_t)s.threads * s.rows / 32 * Scratch<T>::BYTES;    // the warps' exchange buffers
-  switch (s.nv) {
-    case 1: return launch(rms_norm_kernel<T, 1, VEC>, dim3(grid), block, smem, st, 1, a);
-    case 2: return launch(rms_norm_kernel<T, 2, VEC>, dim3(grid), block, smem, st, 1, a);
-    default: return launch(rms_norm_long_kernel<T, VEC>, dim3(grid), block, smem, st, 1, a);
-  }
+  if (s.parts == 0) return launch(rms_norm_long_kernel<T, VEC>, dim3(grid), block, smem, st, 1, a);
+  if (s.parts > 1) return launch(rms_norm_kernel<T, 1, VEC, ROW_CLUSTER>, dim3(grid * s.parts), block, smem, st, s.parts, a);
+  if (s.vectors == 2) return launch(rms_norm_kernel<T, 2, true, ROW_BLOCK>, dim3(grid), block, smem, st, 1, a);
+  if (s.threads < 32) return launch(rms_norm_kernel<T, 1, true, ROW_PART>, dim3(grid), block, smem, st, 1, a);
+  return launch(rms_norm_kernel<T, 1, VEC, ROW_BLOCK>, dim3(grid), block, smem, st, 1, a);
 }
 template <typename T, bool VEC>
 cudaError_t launch_grad(const RmsGradArgs& a, const RowShape& s, unsigned grid, cudaStream_t st) {
   const dim3 block(s.threads, s.rows);
   // the warps' exchange buffers, and then the dw sums of the rows side by side
   const size_t smem = std::max<size_t>(VEC ? 0 : (size_t)s.threads * s.rows / 32 * Scratch<T>::BYTES, s.rows > 1 ? (size_t)s.threads * s.rows * 64 : 0);
-  if (s.nv == 0) return launch(rms_grad_long_kernel<T, VEC>, dim3(grid), block, smem, st, 1, a);
-  if (s.parts > 1) return launch(rms_grad_kernel<T, VEC, true>, dim3(grid * s.parts), block, smem, st, s.parts, a);
-  return launch(rms_grad_kernel<T, VEC, false>, dim3(grid), block, smem, st, 1, a);
+  if (s.parts == 0) return launch(rms_grad_long_kernel<T, VEC>, dim3(grid), block, smem, st, 1, a);
+  if (s.parts > 1) return launch(rms_grad_kernel<T, VEC, ROW_CLUSTER>, dim3(grid * s.parts), block, smem, st, s.parts, a);
+  if (s.threads < 32) return launch(rms_grad_kernel<T, true, ROW_PART>, dim3(grid), block, smem, st, 1, a);
+  return launch(rms_grad_kernel<T, VEC, ROW_BLOCK>, dim3(grid), block, smem, st, 1, a);
 }
 
 // ------------------------------------------------------------------------- distillation
@@ -282,8 +301,8 @@ int precond_rms_norm(precond_t ph, const void* x, const void* residual, const vo
                    weight_dtype == PRECOND_BF16};
   const bool vec = sector_rows(x, ldx, dtype) && sector_rows(residual, ldr, dtype) && sector_rows(total, ldt, dtype) &&
                    sector_rows(y, ldy, dtype);
-  const RowShape s = norm_shape(cols, dtype, vec);
-  const unsigned grid = (unsigned)row_blocks_of(s, q ? q8_row_blocks(rows) * 128 : rows, h->num_sms, dtype == PRECOND_BF16 ? 768 : 384);
+  const RowShape s = row_shape(cols, dtype, false, vec);
+  const unsigned grid = (unsigned)norm_blocks(s, q ? q8_row_blocks(rows) * 128 : rows, dtype, vec, h->num_sms, h->clusters);
   cudaStream_t st = (cudaStream_t)stream;
   if (dtype == PRECOND_BF16)
     OP_CK((vec ? launch_norm<__nv_bfloat16, true>(a, s, grid, st) : launch_norm<__nv_bfloat16, false>(a, s, grid, st)));
@@ -296,9 +315,11 @@ int precond_rms_norm(precond_t ph, const void* x, const void* residual, const vo
 int64_t precond_rms_norm_grad_workspace(int64_t rows, int64_t cols) {
   if (!side(rows) || !side(cols)) return -1;
   if (rows == 0 || cols == 0) return 0;
-  // of either type; rows in parts of a warp take fewer blocks
-  return std::max(grad_blocks(rows, cols, PRECOND_BF16, false, PLAN_SMS), grad_blocks(rows, cols, PRECOND_F32, false, PLAN_SMS)) *
-         cols * 4;
+  // of either type; rows in parts of a warp, and clusters that do not fit, only make fewer
+  int64_t blocks = 0;
+  for (const int dtype : {PRECOND_BF16, PRECOND_F32})
+    blocks = std::max(blocks, grad_blocks(row_shape(cols, dtype, true, false), rows, dtype, PLAN_SMS, PLAN_CLUSTERS));
+  return blocks * cols * 4;
 }
 
 int precond_rms_norm_grad(precond_t ph, const void* dy, const void* x, const void* weight, const float* rstd,
@@ -341,8 +362,8 @@ int precond_rms_norm_grad(precond_t ph, const void* dy, const void* x, const voi
                    weight_dtype == PRECOND_BF16};
   const bool vec = sector_rows(dy, lddy, dtype) && sector_rows(x, ldx, dtype) && sector_rows(dresidual, lddr, dtype) &&
                    sector_rows(dx, lddx, dtype);
-  const RowShape s = grad_shape(cols, dtype, vec);
-  const unsigned grid = (unsigned)grad_blocks(rows, cols, dtype, vec, std::min(h->num_sms, PLAN_SMS));
+  const RowShape s = row_shape(cols, dtype, true, vec);
+  const unsigned grid = (unsigned)grad_blocks(s, rows, dtype, std::min(h->num_sms, PLAN_SMS), h->clusters);
   if (dtype == PRECOND_BF16)
     OP_CK((vec ? launch_grad<__nv_bfloat16, true>(a, s, grid, st) : launch_grad<__nv_bfloat16, false>(a, s, grid, st)));
   else

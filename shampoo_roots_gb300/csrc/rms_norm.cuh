@@ -38,6 +38,9 @@ struct RmsGradArgs {
   int w_bf16;
 };
 
+// How a row lies on threads: whole warps of a block, those of a cluster's blocks, part of a warp.
+enum { ROW_BLOCK, ROW_CLUSTER, ROW_PART };
+
 __device__ __forceinline__ float load_w(const void* w, int bf16, int c) {
   return bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(w)[c]) : reinterpret_cast<const float*>(w)[c];
 }
@@ -54,12 +57,14 @@ __device__ __forceinline__ f2 squares(const F16& v, f2 s) {
   return s;
 }
 
-// Sum over the blockDim.x threads of one row (8, 16 or a multiple of 32), the
-// same value in each.  `red` has room for 2 x blockDim.y x 32, zeroed; calls
+// Sum over the blockDim.x threads of one row (a multiple of 32; PART: 8 or 16),
+// the same value in each.  `red` has room for 2 x blockDim.y x 32, zeroed; calls
 // alternate between its halves, so that one barrier a call is enough.
+template <bool PART>
 __device__ __forceinline__ float row_sum(float v, float* red, int half) {
   const int nw = blockDim.x >> 5;
-  if (nw == 0) {
+  if (PART) {
+#pragma unroll 1
     for (int o = blockDim.x >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   }
@@ -171,40 +176,46 @@ __device__ __forceinline__ float rstd_of(float sum, float inv_cols, float eps) {
   return x < 1e30f ? z : y;            // x y y may overflow only where x does
 }
 
-// NV vectors of 16 columns a thread.  Rows of up to 256 columns share a warp
-// (blockDim.x 8 or 16): its lanes stay together, and rows past the last count as
-// rows of no columns.
-template <typename T, int NV, bool VEC>
-__global__ void __launch_bounds__(NV == 1 ? 384 : 512, NV == 1 && sizeof(T) == 2 ? 2 : 1) rms_norm_kernel(RmsNormArgs a) {
-  __shared__ __align__(16) float red[2 * 8 * 32];
+// NV vectors of 16 columns a thread (NV 2: whole blocks, aligned rows).  Rows of
+// up to 256 columns share a warp (ROW_PART, blockDim.x 8 or 16): its lanes stay
+// together, and rows past the last count as rows of no columns.
+template <typename T, int NV, bool VEC, int ROWS>
+__global__ void __launch_bounds__(NV == 2 || (sizeof(T) == 2 && !VEC) ? 512 : 384, NV == 1 && sizeof(T) == 2 && VEC ? 2 : 1)
+    rms_norm_kernel(RmsNormArgs a) {
+  constexpr bool CLUSTER = ROWS == ROW_CLUSTER, PART = ROWS == ROW_PART;
+  __shared__ __align__(16) float red[2 * 8 * 32];      // of a cluster: its 2 x 8 x 16 words
   zero_red(red, 2 * 8 * 32);
+  if (CLUSTER) cg::this_cluster().sync();
   wait_for_previous();
   let_next_start();
   void* xs = warp_scratch<T, VEC>();
   const int64_t rblocks = q8_row_blocks(a.rows);
-  const int step = gridDim.x * blockDim.y;
-  int row = blockIdx.x * blockDim.y + threadIdx.y;
-  const int below = blockDim.x < 32 ? (threadIdx.x + threadIdx.y * blockDim.x) % 32 / blockDim.x : 0;   // rows below it in its warp
-  int cols = row < a.rows ? a.cols : 0;
-  const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
-  const T* r = reinterpret_cast<const T*>(a.r) + row * a.ldr;
+  const int parts = CLUSTER ? (int)cg::this_cluster().num_blocks() : 1, rank = CLUSTER ? (int)cg::this_cluster().block_rank() : 0;
+  const int step = gridDim.x / parts * blockDim.y;
+  int row = blockIdx.x / parts * blockDim.y + threadIdx.y;
+  const int below = PART ? (threadIdx.x + threadIdx.y * blockDim.x) % 32 / blockDim.x : 0;   // rows below it in its warp
+  int cols = !PART || row < a.rows ? a.cols : 0;
+  // rows' addresses are formed anew: pointers kept from row to row cost registers that the vectors need
+  auto x = [&](int64_t k) { return reinterpret_cast<const T*>(a.x) + k * a.ldx; };
+  auto r = [&](int64_t k) { return reinterpret_cast<const T*>(a.r) + k * a.ldr; };
   const float inv_cols = 1.0f / (float)a.cols;
   F16 w[NV];
   int c[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    c[j] = (j * blockDim.x + threadIdx.x) * 16;
+    c[j] = ((j + rank) * (int)blockDim.x + threadIdx.x) * 16;        // one of j and rank is 0
     w[j] = load_w16(a.w, a.w_bf16, c[j], a.cols);
   }
   Raw16<T> nx[NV], nr[NV];
+  bool lost = false;
   if (row - below < a.rows) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      load16<VEC>(nx[j], x, c[j], cols);
-      if (a.r) load16<VEC>(nr[j], r, c[j], cols);
+      load16<VEC>(nx[j], x(row), c[j], cols);
+      if (a.r) load16<VEC>(nr[j], r(row), c[j], cols);
     }
   }
-  for (int half = 0; row - below < a.rows; row += step, half ^= 1) {
+  for (unsigned call = 1; row - below < a.rows; row += step, ++call) {
     F16 v[NV];
     f2 ss = 0;
 #pragma unroll
@@ -218,33 +229,31 @@ __global__ void __launch_bounds__(NV == 1 ? 384 : 512, NV == 1 && sizeof(T) == 2
       v[j] = unpack(nx[j]);
       ss = squares(v[j], ss);
     }
-    x += step * a.ldx;
-    r += step * a.ldr;
-    const int next = row + step < a.rows ? a.cols : 0;
+    const int next = !PART || row + step < a.rows ? a.cols : 0;
     if (row + step - below < a.rows) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        load16<VEC>(nx[j], x, c[j], next);
-        if (a.r) load16<VEC>(nr[j], r, c[j], next);
+        load16<VEC>(nx[j], x(row + step), c[j], next);
+        if (a.r) load16<VEC>(nr[j], r(row + step), c[j], next);
       }
     }
-    const float rstd = rstd_of(row_sum(sum2(ss), red, half), inv_cols, a.eps);
-    if (a.rstd && threadIdx.x == 0 && cols) a.rstd[row] = rstd;
+    const float sum = CLUSTER ? cluster_row_sum(sum2(ss), reinterpret_cast<unsigned long long*>(red), call, lost)
+                              : row_sum<PART>(sum2(ss), red, call & 1);
+    const float rstd = rstd_of(sum, inv_cols, a.eps);
+    if (a.rstd && threadIdx.x == 0 && rank == 0 && cols) a.rstd[row] = rstd;
     if (a.q || a.y) {
       const f2 rs = f2_of(rstd, rstd);
-      const size_t at_row = q8_scale_at(row, 0, rblocks);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[j].p[i] = mul2(mul2(v[j].p[i], rs), w[j].p[i]);
-        const int kb = c[j] >> 7;
-        norm_write<T, VEC>(a, row, c[j], cols, v[j], (size_t)(kb >> 2) * rblocks * 512 + (kb & 3) + at_row, xs);
+        norm_write<T, VEC>(a, row, c[j], cols, v[j], q8_scale_at(row, c[j] >> 7, rblocks), xs);
       }
-      if (a.q && (a.cols & 511) && row < rblocks * 128) norm_pad(a, row, rblocks);
+      if (a.q && (a.cols & 511) && rank == 0 && row < rblocks * 128) norm_pad(a, row, rblocks);
     }
     cols = next;
   }
-  if (a.q)
+  if (a.q && rank == 0)
     for (; row < rblocks * 128; row += step) norm_pad(a, row, rblocks);
 }
 
@@ -280,7 +289,7 @@ __global__ void __launch_bounds__(512, 2) rms_norm_long_kernel(RmsNormArgs a) {
       }
       ss = squares(unpack(o), ss);
     }
-    const float rstd = rstd_of(row_sum(sum2(ss), red, half), inv_cols, a.eps);
+    const float rstd = rstd_of(row_sum<false>(sum2(ss), red, half), inv_cols, a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     if (!a.q && !a.y) continue;
     const f2 rs = f2_of(rstd, rstd);
@@ -325,10 +334,11 @@ __device__ __forceinline__ void grad_out(Raw16<T>& o, const F16& g, const F16& n
 }
 
 // fp32 takes 168 registers a thread: with 128 the vectors in flight do not fit.
-template <typename T, bool VEC, bool CLUSTER>
+template <typename T, bool VEC, int ROWS>
 __global__ void __launch_bounds__(sizeof(T) == 4 ? 384 : 512, 1) rms_grad_kernel(RmsGradArgs a) {
   __shared__ __align__(16) float red[2 * 8 * 32];      // of a cluster: its 2 x 8 x 16 words
   zero_red(red, 2 * 8 * 32);
+  constexpr bool CLUSTER = ROWS == ROW_CLUSTER, PART = ROWS == ROW_PART;
   constexpr bool EARLY = sizeof(T) == 2 && VEC;        // dr with the row's other vectors (else there is no room for it)
   if (CLUSTER) cg::this_cluster().sync();
   wait_for_previous();
@@ -338,12 +348,12 @@ __global__ void __launch_bounds__(sizeof(T) == 4 ? 384 : 512, 1) rms_grad_kernel
   const int group = CLUSTER ? blockIdx.x / parts : blockIdx.x;          // of blocks that share rows
   const int step = (CLUSTER ? gridDim.x / parts : gridDim.x) * blockDim.y;
   int row = group * blockDim.y + threadIdx.y;
-  const int below = blockDim.x < 32 ? (threadIdx.x + threadIdx.y * blockDim.x) % 32 / blockDim.x : 0;   // as in the norm
-  int cols = row < a.rows ? a.cols : 0;
-  const T* dy = reinterpret_cast<const T*>(a.dy) + row * a.lddy;
-  const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
-  const T* dr = reinterpret_cast<const T*>(a.dr) + row * a.lddr;
-  T* dx = reinterpret_cast<T*>(a.dx) + row * a.lddx;
+  const int below = PART ? (threadIdx.x + threadIdx.y * blockDim.x) % 32 / blockDim.x : 0;   // as in the norm
+  int cols = !PART || row < a.rows ? a.cols : 0;
+  // addresses formed anew, as in the norm
+  auto dy = [&](int64_t k) { return reinterpret_cast<const T*>(a.dy) + k * a.lddy; };
+  auto x = [&](int64_t k) { return reinterpret_cast<const T*>(a.x) + k * a.ldx; };
+  auto dr = [&](int64_t k) { return reinterpret_cast<const T*>(a.dr) + k * a.lddr; };
   const float inv_cols = 1.0f / (float)a.cols;
   const int c = ((CLUSTER ? (int)cg::this_cluster().block_rank() * (int)blockDim.x : 0) + threadIdx.x) * 16;
   const F16 w = load_w16(a.w, a.w_bf16, c, a.cols);
@@ -354,38 +364,34 @@ __global__ void __launch_bounds__(sizeof(T) == 4 ? 384 : 512, 1) rms_grad_kernel
   float nrstd = 0.f;
   bool lost = false;
   if (row - below < a.rows) {
-    load16<VEC>(ny, dy, c, cols);
-    load16<VEC>(nx, x, c, cols);
-    if (a.dr) load16<VEC>(nr, dr, c, cols);
+    load16<VEC>(ny, dy(row), c, cols);
+    load16<VEC>(nx, x(row), c, cols);
+    if (a.dr) load16<VEC>(nr, dr(row), c, cols);
     if (cols) nrstd = a.rstd[row];
   }
   for (unsigned call = 1; row - below < a.rows; row += step, ++call) {
     const f2 rs = f2_of(nrstd, nrstd);
     const bool more = row + step - below < a.rows;
-    const int next = row + step < a.rows ? a.cols : 0;
+    const int next = !PART || row + step < a.rows ? a.cols : 0;
     Raw16<T> res = nr;
     settle<VEC>(ny, xs);
     settle<VEC>(nx, xs);
     F16 g = unpack(ny), n = unpack(nx);
     const f2 dot = grad_terms(g, n, w, dw, rs, 0);
-    dy += step * a.lddy;
-    x += step * a.ldx;
-    dr += step * a.lddr;
     if (more) {
-      load16<VEC>(ny, dy, c, next);
-      load16<VEC>(nx, x, c, next);
-      if (EARLY && a.dr) load16<VEC>(nr, dr, c, next);
+      load16<VEC>(ny, dy(row + step), c, next);
+      load16<VEC>(nx, x(row + step), c, next);
+      if (EARLY && a.dr) load16<VEC>(nr, dr(row + step), c, next);
       if (next) nrstd = a.rstd[row + step];
     }
     const float sum = CLUSTER ? cluster_row_sum(sum2(dot), reinterpret_cast<unsigned long long*>(red), call, lost)
-                              : row_sum(sum2(dot), red, call & 1);
+                              : row_sum<PART>(sum2(dot), red, call & 1);
     const float mean = -sum * inv_cols;
     Raw16<T> o;
     if (a.dr) settle<VEC>(res, xs);
     grad_out(o, g, n, rs, f2_of(mean, mean), a.dr ? &res : nullptr);
-    if (!EARLY && more && a.dr) load16<VEC>(nr, dr, c, next);    // used after the next row's join
-    store16<VEC>(dx, c, cols, o, xs);
-    dx += step * a.lddx;
+    if (!EARLY && more && a.dr) load16<VEC>(nr, dr(row + step), c, next);    // used after the next row's join
+    store16<VEC>(reinterpret_cast<T*>(a.dx) + row * a.lddx, c, cols, o, xs);
     cols = next;
   }
   if (blockDim.y > 1) {                  // the block's rows side by side: in their order, through shared memory
@@ -449,7 +455,7 @@ __global__ void __launch_bounds__(512, 1) rms_grad_long_kernel(RmsGradArgs a) {
       }
     }
     first = false;
-    const float mean = -row_sum(sum2(dot), red, half) * inv_cols;
+    const float mean = -row_sum<false>(sum2(dot), red, half) * inv_cols;
     const f2 mm = f2_of(mean, mean);
     for (int64_t c = threadIdx.x * 16; c < span; c += stride) {
       Raw16<T> o, res;
