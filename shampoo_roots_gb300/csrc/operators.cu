@@ -132,11 +132,10 @@ cudaError_t launch(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cuda
 // ------------------------------------------------------------------------- norm
 // Threads of a row, rows of a block and blocks of a row.  16 columns a thread, up
 // to 384 threads (a bf16 gradient: 512); then a norm of aligned rows has 32 up
-// to 512 threads, and what is still longer a cluster of 2, 4 or 8 blocks (3 took
-// 1.9 times as long as 4 for a norm of 16384 columns; 32 columns a thread 63 us
-// where a cluster of 4 took 74).  Longer rows (parts 0) take the kernels that
-// read a row twice.  Blocks of short rows hold several; up to 256 columns, where
-// rows begin at sectors, a warp does.
+// to 512 threads (16384 columns: 58 us where a cluster of 4 took 74), and what
+// is still longer a cluster of 2, 4 or 8 blocks.  Longer rows (parts 0) take the
+// kernels that read a row twice.  Blocks of short rows hold several; up to 256
+// columns, where rows begin at sectors, a warp does.
 struct RowShape { int threads, rows, vectors, parts; };
 RowShape row_shape(int64_t cols, int dtype, bool grad, bool vec) {
   const int64_t one = grad && dtype == PRECOND_BF16 ? 512 : 384, n = (cols + 15) / 16;
