@@ -134,7 +134,8 @@ cudaError_t launch(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cuda
 // to 384 threads (a bf16 gradient: 512); then a norm of aligned rows has 32 up
 // to 512 threads (16384 columns: 58 us where a cluster of 4 took 74), and what
 // is still longer a cluster of 2, 4 or 8 blocks.  Longer rows (parts 0) take the
-// kernels that read a row twice.  Blocks of short rows hold several; up to 256
+// kernels that read a row twice.  Blocks of short rows hold several, for warps on each of
+// the SM's four parts (20244 x 1213: 4 rows of 3 warps 59 us, one row 84); up to 256
 // columns, where rows begin at sectors, a warp does.
 struct RowShape { int threads, rows, vectors, parts; };
 RowShape row_shape(int64_t cols, int dtype, bool grad, bool vec) {
@@ -145,7 +146,9 @@ RowShape row_shape(int64_t cols, int dtype, bool grad, bool vec) {
   if (n > parts * one) return {512, 1, 0, 0};
   const int64_t mine = (n + parts - 1) / parts;
   const int threads = vec && n <= 16 ? (n <= 8 ? 8 : 16) : (int)std::max<int64_t>(32, (mine + 31) / 32 * 32);
-  return {threads, parts > 1 ? 1 : std::max(1, (dtype == PRECOND_BF16 ? 256 : 128) / threads), 1, parts};
+  int rows = 1;
+  while (parts == 1 && threads * rows % 128 && threads * (rows + 1) <= 384) ++rows;
+  return {threads, rows, 1, parts};
 }
 
 // Blocks (or clusters) of a persistent grid: what the registers let an SM hold

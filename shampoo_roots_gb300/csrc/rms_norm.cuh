@@ -324,12 +324,12 @@ __device__ __forceinline__ f2 grad_terms(F16& g, F16& n, const F16& w, F16& dw, 
 }
 // dx = rstd (g - n mean) (+ dr)
 template <typename T>
-__device__ __forceinline__ void grad_out(Raw16<T>& o, const F16& g, const F16& n, f2 rs, f2 minus_mean, const Raw16<T>* dr) {
+__device__ __forceinline__ void grad_out(Raw16<T>& o, const F16& g, const F16& n, f2 rs, f2 minus_mean, bool add, const Raw16<T>& dr) {
   F16 d;
 #pragma unroll
   for (int i = 0; i < 8; ++i) d.p[i] = mul2(rs, fma2(n.p[i], minus_mean, g.p[i]));
-  if (dr) {
-    const F16 f = unpack(*dr);
+  if (add) {
+    const F16 f = unpack(dr);
 #pragma unroll
     for (int i = 0; i < 8; ++i) d.p[i] = add2(d.p[i], f.p[i]);
   }
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(sizeof(T) == 4 ? 384 : 512, 1) rms_grad_kernel
     const float mean = -sum * inv_cols;
     Raw16<T> o;
     if (a.dr) settle<VEC>(res, xs);
-    grad_out(o, g, n, rs, f2_of(mean, mean), a.dr ? &res : nullptr);
+    grad_out(o, g, n, rs, f2_of(mean, mean), a.dr != nullptr, res);
     if (!EARLY && more && a.dr) load16<VEC>(nr, dr(row + step), c, next);    // used after the next row's join
     store16<VEC>(reinterpret_cast<T*>(a.dx) + row * a.lddx, c, cols, o, xs);
     cols = next;
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(512, 1) rms_grad_long_kernel(RmsGradArgs a) {
         n.p[i] = mul2(n.p[i], rs);
         g.p[i] = mul2(g.p[i], w.p[i]);
       }
-      grad_out(o, g, n, rs, mm, a.dr ? &res : nullptr);
+      grad_out(o, g, n, rs, mm, a.dr != nullptr, res);
       store16<VEC>(dx, (int)c, a.cols, o, xs);
     }
   }
