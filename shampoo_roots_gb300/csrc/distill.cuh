@@ -259,9 +259,9 @@ __device__ __forceinline__ void unite_ids(const DistillShared& sh, int top) {
   __syncwarp();
 }
 
-// Up to 128: four a lane, in registers.
+// Up to 128 or 256: Q a lane, in registers.
+template <int Q>
 struct FewCandidates {
-  static constexpr int Q = 4;
   int id[Q];
   float logp[Q], z[Q], p[Q], most;
   template <typename T>
@@ -275,7 +275,10 @@ struct FewCandidates {
     }
 #pragma unroll
     for (int q = 0; q < Q; ++q) z[q] = candidate_logit(a, row, lane + 32 * q, id[q], z_, sl, all);
-    most = warp_max_nan(max_nan(max_nan(logp[0], logp[1]), max_nan(logp[2], logp[3])));
+    most = logp[0];
+#pragma unroll
+    for (int q = 1; q < Q; ++q) most = max_nan(most, logp[q]);
+    most = warp_max_nan(most);
   }
   __device__ __forceinline__ void teach(const DistillArgs& a, const DistillShared&) {
     float st = 0.f;
@@ -639,7 +642,8 @@ __global__ void __launch_bounds__(DISTILL_THREADS + (FUSED ? 32 : 0), 2) distill
         if (teaches) cand.patch(a, sh, dz, weight * a.tau, c, shift, s);
       }
     };
-    if (a.top <= 32 * FewCandidates::Q) work(FewCandidates());
+    if (a.top <= 128) work(FewCandidates<4>());
+    else if (a.top <= 256) work(FewCandidates<8>());
     else work(ManyCandidates());
   } else if (part == 0 && lane == 0) {
     a.loss[row] = 0.0f;

@@ -66,7 +66,9 @@ struct Gemm8Smem {
   static constexpr int OFF_SF = STAGES * (A_BYTES + B_BYTES);
   static constexpr int OFF_XS = OFF_SF + STAGES * SF_BYTES;                 // a scratch of each drain warp
   static constexpr int OFF_BAR = OFF_XS + DRAIN_WARPS * 32 * G8_XS_LD * 4;
-  static constexpr int PART_LD = BN + 1;                                    // a stretch's sums, over the ring
+  // a stretch's sums, over the ring, along C's rows: [128][BN], transposed [BN][128], 4 floats apart modulo 32
+  static constexpr int PART_LD = BN + 4, PART_LDT = G8_BM + 4;
+  static_assert(G8_BM * PART_LD * 4 <= OFF_SF && BN * PART_LDT * 4 <= OFF_SF, "the sums fit into the ring");
   static constexpr int BYTES = 1024 + OFF_BAR + 256;
   static_assert(CTAS * (BYTES + 1024) <= 228 * 1024, "shared memory of an SM");
   // tensor memory: two sum buffers, then two scale buffers
@@ -197,6 +199,82 @@ __device__ __forceinline__ void g8_tile(int64_t t, int64_t tiles_m, int64_t tile
   const int64_t rows = min(tiles_m - first, (int64_t)G8_RASTER), loc = t % per;
   ti = first + loc % rows;
   tj = loc / rows;
+}
+
+// A cluster's stretches: every CTA adds 1 / P of the tile's elements, the
+// stretches in their order, lanes along C's rows, 4 elements at a time where C's
+// rows allow it.  8 loads of 16 bytes from the others' shared memory are in
+// flight (61 x 448 x 2560 fp32: 7.0 us; single elements,
+// 4 in flight, 15.5).
+template <int BN, int P>
+__device__ __forceinline__ void g8_join(const Gemm8Args& g, float* sums, int64_t m0, int64_t n0, int part) {
+  using SM = Gemm8Smem<BN>;
+  cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+  const float* from[P];
+#pragma unroll
+  for (int k = 0; k < P; ++k) from[k] = cluster.map_shared_rank(sums, k);
+  constexpr int LOG = BN == 16 ? 4 : BN == 32 ? 5 : BN == 64 ? 6 : 7;
+  const int log = g.swap ? 7 : LOG, mask = (1 << log) - 1, ld = g.swap ? SM::PART_LDT : SM::PART_LD;       // C's rows in the tile
+  const int64_t row0 = g.swap ? n0 : m0, col0 = g.swap ? m0 : n0, rows = g.swap ? g.N : g.M, cols = g.swap ? g.M : g.N;
+  constexpr int SHARE = G8_BM * BN / P;
+  if (g.sectors) {
+    constexpr int U = 8 / P;
+    for (int u0 = threadIdx.x; u0 < SHARE / 4; u0 += U * G8_THREADS) {
+      float4 w[U][P];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int e = part * SHARE + 4 * (u0 + u * G8_THREADS);
+#pragma unroll
+        for (int k = 0; k < P; ++k)
+          if (u0 + u * G8_THREADS < SHARE / 4) w[u][k] = *reinterpret_cast<const float4*>(from[k] + (e >> log) * ld + (e & mask));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int e = part * SHARE + 4 * (u0 + u * G8_THREADS);
+        const int64_t row = row0 + (e >> log), col = col0 + (e & mask);
+        if (u0 + u * G8_THREADS >= SHARE / 4 || row >= rows || col >= cols) continue;
+        float4 v = w[u][0];
+#pragma unroll
+        for (int k = 1; k < P; ++k) v = make_float4(v.x + w[u][k].x, v.y + w[u][k].y, v.z + w[u][k].z, v.w + w[u][k].w);
+        const int64_t o = row * g.ldc + col;
+        if (col + 4 <= cols) {
+          if (g.c_bf16)
+            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(g.c) + o) = make_uint2(bf16x2_bits(v.x, v.y), bf16x2_bits(v.z, v.w));
+          else if (g.accumulate)
+            asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};"
+                         ::"l"(reinterpret_cast<float*>(g.c) + o), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+          else
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(g.c) + o) = v;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (col + i < cols) g8_put(g, o + i, (&v.x)[i]);
+        }
+      }
+    }
+    return;
+  }
+  constexpr int U = 32 / P;
+  for (int e0 = threadIdx.x; e0 < SHARE; e0 += U * G8_THREADS) {
+    float w[U][P];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int e = part * SHARE + e0 + u * G8_THREADS;
+#pragma unroll
+      for (int k = 0; k < P; ++k)
+        if (e0 + u * G8_THREADS < SHARE) w[u][k] = from[k][(e >> log) * ld + (e & mask)];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int e = part * SHARE + e0 + u * G8_THREADS;
+      const int64_t row = row0 + (e >> log), col = col0 + (e & mask);
+      if (e0 + u * G8_THREADS >= SHARE || row >= rows || col >= cols) continue;
+      float v = w[u][0];
+#pragma unroll
+      for (int k = 1; k < P; ++k) v += w[u][k];
+      g8_put(g, row * g.ldc + col, v);
+    }
+  }
 }
 
 // A persistent CTA takes tiles blockIdx.x, + gridDim.x, ...; a cluster (few
@@ -390,9 +468,16 @@ gemm8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         }
       } else {
         // to this CTA's own shared memory (the ring is idle: its last MMA has completed), for the cluster
-        float* mine = reinterpret_cast<float*>(gbase) + (qd * 32 + lane) * SM::PART_LD + own * HALF;
+        float* mine = reinterpret_cast<float*>(gbase);
+        const int r = qd * 32 + lane;
+        if (g.swap) {
 #pragma unroll
-        for (int j = 0; j < HALF; ++j) mine[j] = sum[j];
+          for (int j = 0; j < HALF; ++j) mine[(own * HALF + j) * SM::PART_LDT + r] = sum[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < HALF; j += 4)
+            *reinterpret_cast<float4*>(mine + r * SM::PART_LD + own * HALF + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
+        }
       }
     }
   }
@@ -400,37 +485,13 @@ gemm8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
   if (parts > 1) {
     __syncwarp();
     cluster.sync();
-    // Every CTA adds 1 / parts of the tile's elements, the stretches in their order: lanes along C's rows.
-    // All loads of a round go before their sums.
     int64_t ti, tj;
     g8_tile(first_tile, tiles_m, tiles_n, ti, tj);
-    constexpr int ROUND = 4;
-    const int share = (G8_BM * BN + parts - 1) / parts, threads = blockDim.x;
-    for (int e0 = threadIdx.x; e0 < share; e0 += ROUND * threads) {
-      float v[ROUND];
-      int64_t o[ROUND];
-#pragma unroll
-      for (int u = 0; u < ROUND; ++u) {
-        const int e = part * share + e0 + u * threads;
-        const int r = g.swap ? e % G8_BM : e / BN, c = g.swap ? e / G8_BM : e % BN;
-        const int64_t m = ti * G8_BM + r, n = tj * BN + c;
-        const bool in = e0 + u * threads < share && e < G8_BM * BN && m < g.M && n < g.N;
-        o[u] = in ? (g.swap ? n * g.ldc + m : m * g.ldc + n) : -1;
-        v[u] = 0.f;
-        if (in) {
-          float w[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            w[k] = k < parts ? cluster.map_shared_rank(reinterpret_cast<float*>(gbase), k)[r * SM::PART_LD + c] : 0.f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[u] += w[k];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < ROUND; ++u)
-        if (o[u] >= 0) g8_put(g, o[u], v[u]);
-    }
-    cluster.sync();
+    if (parts == 2) g8_join<BN, 2>(g, reinterpret_cast<float*>(gbase), ti * G8_BM, tj * BN, part);
+    else if (parts == 4) g8_join<BN, 4>(g, reinterpret_cast<float*>(gbase), ti * G8_BM, tj * BN, part);
+    else g8_join<BN, 8>(g, reinterpret_cast<float*>(gbase), ti * G8_BM, tj * BN, part);
+    // the others have read this CTA's sums (nothing else is ordered: its results need not have reached memory)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();

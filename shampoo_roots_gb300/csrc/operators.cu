@@ -551,9 +551,13 @@ int precond_distill(precond_t ph, const void* logits, int dtype, int64_t rows, i
   if (split) {
     // a warp a row, eight to a block where their candidates fit
     const int each = DistillShared::bytes(top, 0), warps = std::max(1, std::min(8, (48 << 10) / each));
-    const bool few = top <= 32 * FewCandidates::Q;
-    auto k = bf16 ? (few ? distill_candidates_kernel<__nv_bfloat16, FewCandidates> : distill_candidates_kernel<__nv_bfloat16, ManyCandidates>)
-                  : (few ? distill_candidates_kernel<float, FewCandidates> : distill_candidates_kernel<float, ManyCandidates>);
+    const int in = top <= 128 ? 0 : top <= 256 ? 1 : 2;          // registers of 4 or 8 a lane, shared memory
+    static const DistillKernel kernels[2][3] = {
+        {distill_candidates_kernel<float, FewCandidates<4>>, distill_candidates_kernel<float, FewCandidates<8>>,
+         distill_candidates_kernel<float, ManyCandidates>},
+        {distill_candidates_kernel<__nv_bfloat16, FewCandidates<4>>, distill_candidates_kernel<__nv_bfloat16, FewCandidates<8>>,
+         distill_candidates_kernel<__nv_bfloat16, ManyCandidates>}};
+    auto k = kernels[bf16][in];
     OP_CK(launch(k,
                  dim3((unsigned)((rows + warps - 1) / warps)), dim3(32 * warps), (size_t)each * warps, st, 1, a));
     ++h->launches;

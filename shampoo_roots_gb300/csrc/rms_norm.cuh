@@ -84,7 +84,7 @@ __device__ __forceinline__ float row_sum(float v, float* red, int half) {
 // block).  Every warp leaves its sum with each block, as a word that also holds
 // the number of the call, and every warp polls its own block's words: the join
 // waits for these sums alone.  (A cluster barrier, or any release, also waits
-// for the previous row's dx to reach L2: 110 us where this takes GRADC, for the
+// for the previous row's dx to reach L2: 110 us where this took 88, for the
 // gradient of 3000 x 16384 bf16.)  Calls alternate between the halves of
 // `slots` (2 x 8 x 16, zeroed in every block): a warp writes for call n + 2 when
 // it has seen call n + 1 from every warp, so that all of them have read call n.

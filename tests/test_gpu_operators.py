@@ -175,6 +175,15 @@ def test_rms_norm_pitch(pc, cols):
     check_norm(pc, 19, cols, "f32", "f32", True, pitch=8)
 
 
+@pytest.mark.parametrize("rows,cols,dtype,pitch", [(500, 48, "bf16", 0), (77, 130, "bf16", 14), (301, 256, "f32", 0), (40, 7001, "bf16", 0),
+                                                   (90, 6146, "f32", 6), (77, 13001, "bf16", 1), (50, 24577, "f32", 0), (45, 49153, "bf16", 0),
+                                                   (700, 1213, "bf16", 0), (330, 2009, "f32", 0), (200, 530, "bf16", 1)])
+def test_rms_norm_layouts(pc, rows, cols, dtype, pitch):
+    """Several rows in a warp, rows at every alignment, rows shared by 2, 4 and 8 blocks and longer ones; more rows than run at once."""
+    check_norm(pc, rows, cols, dtype, "f32", True, pitch=pitch)
+    check_norm(pc, rows, cols, dtype, "bf16", False, pitch=pitch)
+
+
 def test_rms_norm_values(pc):
     """Rows of zeros, of tiny and of large numbers, a NaN row; its neighbours keep their values."""
     check_norm(pc, 64, 640, "f32", "f32", False, scale=1e-12)
@@ -245,6 +254,14 @@ def test_rms_norm_grad_pitch(pc):
     check_grad(pc, 19, 1001, "bf16", True, pitch=3)
     check_grad(pc, 19, 1000, "f32", True, pitch=8)
     check_grad(pc, 5, 9001, "bf16", True, pitch=3)
+
+
+@pytest.mark.parametrize("rows,cols,dtype,pitch", [(3000, 48, "bf16", 0), (77, 130, "bf16", 14), (1001, 256, "f32", 0), (200, 9001, "bf16", 0),
+                                                   (190, 6146, "f32", 6), (77, 17000, "bf16", 8), (50, 24577, "f32", 0), (45, 49153, "bf16", 1),
+                                                   (2000, 1213, "bf16", 0), (600, 2009, "f32", 0), (900, 530, "bf16", 1)])
+def test_rms_norm_grad_layouts(pc, rows, cols, dtype, pitch):
+    check_grad(pc, rows, cols, dtype, True, pitch=pitch)
+    check_grad(pc, rows, cols, dtype, False, pitch=pitch)
 
 
 def test_rms_norm_grad_in_place(pc):
@@ -322,6 +339,16 @@ def test_gemm_accumulate(pc, m, n, k):
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_gemm_pitch(pc, m, n, k, ldc, out):
     check_gemm(pc, m, n, k, out, pitch=1, ldc=ldc)
+
+
+@pytest.mark.parametrize("m,n,k,ldc", [(70, 300, 1024, 304), (130, 260, 2048, 264), (128, 128, 4096, 128), (129, 250, 4000, 251),
+                                       (8, 128, 1024, 128), (20, 500, 2048, 512), (60, 300, 4096, 301), (16, 16, 3000, 16)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_gemm_stretches(pc, m, n, k, ldc, out):
+    """Tiles that 2, 4 or 8 blocks share, a stretch of K each: results of 4 elements at a time and single ones."""
+    check_gemm(pc, m, n, k, out, ldc=ldc)
+    if out == "f32":
+        check_gemm(pc, m, n, k, out, accumulate=True, ldc=ldc)
 
 
 @pytest.mark.parametrize("m,n,k", [(0, 5, 5), (5, 0, 5), (130, 70, 0), (3, 200, 0)])
@@ -431,6 +458,14 @@ def test_distill_many_rows(pc, rows, vocab, top, dtype):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     c = check_distill(pc, z, ids, t, w, 1.5, grad=False)
     assert torch.equal(a[0], c[0])
+
+
+@pytest.mark.parametrize("rows,vocab,top", [(700, 1500, 129), (650, 3001, 256), (9, 5000, 200), (640, 400, 257)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_distill_candidate_counts(pc, rows, vocab, top, dtype):
+    z, ids, t, w = distill_inputs(rows, vocab, top, dtype)
+    ids[1::3, 128:] = ids[1::3, :top - 128]                   # a second occurrence past the first 128
+    check_distill(pc, z, ids, t, w, 1.5)
 
 
 def test_distill_types_and_places(pc):
