@@ -40,7 +40,7 @@ constexpr int G8_BK = 128;             // one scale block, one swizzled row
 constexpr int G8_SEGMENT = 4;          // blocks between promotions (512 columns: one scale group)
 constexpr int G8_PAIR_SEGMENT = 8;     // the same, for pairs of CTAs
 constexpr int G8_EPI_WARPS = 8;
-constexpr int G8_XS_LD = 33;            // a drain warp's scratch: 32 x 32 results, rows an odd number of words apart
+constexpr int G8_XS = 32 * 32;         // a drain warp's scratch: 32 x 32 results
 constexpr int G8_THREADS = 64 + 32 * G8_EPI_WARPS;
 constexpr int G8_PAIR_THREADS = 128 + 32 * G8_EPI_WARPS;   // a warpgroup that loads and issues, two that drain
 
@@ -50,7 +50,7 @@ struct Gemm8Args {
   const uint8_t* sb; int64_t sb_rb;
   void* c; int64_t ldc;
   int c_bf16, accumulate;
-  int sectors;                         // C's rows begin at multiples of 32 bytes
+  int sectors, quads;                  // C's rows begin at multiples of 32 bytes, of 4 elements
   int swap;                            // 1: C is N x M (the operands were exchanged)
   unsigned int* err;
 };
@@ -65,7 +65,7 @@ struct Gemm8Smem {
   static constexpr int DRAIN_WARPS = BN >= 64 ? G8_EPI_WARPS : 4;      // that have columns of their own
   static constexpr int OFF_SF = STAGES * (A_BYTES + B_BYTES);
   static constexpr int OFF_XS = OFF_SF + STAGES * SF_BYTES;                 // a scratch of each drain warp
-  static constexpr int OFF_BAR = OFF_XS + DRAIN_WARPS * 32 * G8_XS_LD * 4;
+  static constexpr int OFF_BAR = OFF_XS + DRAIN_WARPS * G8_XS * 4;
   // a stretch's sums, over the ring, along C's rows: [128][BN], transposed [BN][128], 4 floats apart modulo 32
   static constexpr int PART_LD = BN + 4, PART_LDT = G8_BM + 4;
   static_assert(G8_BM * PART_LD * 4 <= OFF_SF && BN * PART_LDT * 4 <= OFF_SF, "the sums fit into the ring");
@@ -127,16 +127,40 @@ __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.
 // One element of the result.  Accumulating, the addition is the memory's: each element gets one a call, so its place
 // in time changes nothing, and nobody waits for the old value (loads of 8 rows before their stores kept 8 KB an SM in
 // flight: 4085 x 2834 x 768 took 80 us).  It flushes subnormal sums to zero.
+template <bool F32>
 __device__ __forceinline__ void g8_put(const Gemm8Args& g, int64_t o, float v) {
-  if (g.c_bf16) reinterpret_cast<__nv_bfloat16*>(g.c)[o] = __float2bfloat16_rn(v);
+  if (!F32) reinterpret_cast<__nv_bfloat16*>(g.c)[o] = __float2bfloat16_rn(v);
   else if (g.accumulate) asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(reinterpret_cast<float*>(g.c) + o), "f"(v) : "memory");
   else reinterpret_cast<float*>(g.c)[o] = v;
 }
 
+// Place of a result in the scratch: the groups of 4 of a row in an order of their own, so that neither rows nor
+// columns meet a bank twice.
+__device__ __forceinline__ int g8_at(int r, int c) { return r * 32 + (((c >> 2) ^ (r & 7)) << 2) + (c & 3); }
+
+// Four elements of a row of C from a multiple of 4 on, of which `left` exist.
+template <bool F32>
+__device__ __forceinline__ void g8_put4(const Gemm8Args& g, int64_t o, float4 v, int64_t left) {
+  if (left >= 4) {
+    if (!F32)
+      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(g.c) + o) = make_uint2(bf16x2_bits(v.x, v.y), bf16x2_bits(v.z, v.w));
+    else if (g.accumulate)
+      asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};"
+                   ::"l"(reinterpret_cast<float*>(g.c) + o), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+    else
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(g.c) + o) = v;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < left) g8_put<F32>(g, o + i, (&v.x)[i]);
+}
+
 // Columns n .. n + 31 of the warp's 32 MMA rows m0 .. (one a lane).  Where C's rows are whole sectors a lane
-// stores its row's (16 lanes of a bf16 C at 2 B a lane and row took 39 us for 2500 x 1300 x 256, against 17 us
-// through the scratch); otherwise, and when accumulating, the rows pass through the warp's scratch and leave 32
-// columns at a time.
+// stores its row's; otherwise, and when accumulating, the rows pass through the warp's scratch and leave 32 columns
+// at a time, 4 a lane where C's rows allow it (12000 x 3000 x 250 to bf16: 35 us, one a lane 48).  The loops over rows
+// are short on purpose: unrolled to the end, their addresses spilled registers and that took 66.
+template <bool F32>
 __device__ __forceinline__ void g8_store32(const Gemm8Args& g, float* xs, int64_t m0, int64_t n, const float (&v)[32]) {
   const int lane = threadIdx.x & 31;
   if (m0 >= g.M || n >= g.N) return;
@@ -145,14 +169,14 @@ __device__ __forceinline__ void g8_store32(const Gemm8Args& g, float* xs, int64_
     if (m >= g.M) return;
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-      if (n + i < g.N) g8_put(g, (n + i) * g.ldc + m, v[i]);
+      if (n + i < g.N) g8_put<F32>(g, (n + i) * g.ldc + m, v[i]);
     return;
   }
   if (g.sectors && !g.accumulate && n + 32 <= g.N) {
     if (m >= g.M) return;
-    char* p = reinterpret_cast<char*>(g.c) + (m * g.ldc + n) * (g.c_bf16 ? 2 : 4);
+    char* p = reinterpret_cast<char*>(g.c) + (m * g.ldc + n) * (F32 ? 4 : 2);
     uint32_t w[8];
-    if (g.c_bf16) {
+    if (!F32) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
@@ -170,17 +194,22 @@ __device__ __forceinline__ void g8_store32(const Gemm8Args& g, float* xs, int64_
     return;
   }
 #pragma unroll
-  for (int i = 0; i < 32; ++i) xs[lane * G8_XS_LD + i] = v[i];
+  for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(xs + g8_at(lane, i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
   __syncwarp();
   const int rows = (int)min((int64_t)32, g.M - m0);
+  if (g.quads) {                        // 8 lanes a row
+    const int r0 = lane >> 3, c = 4 * (lane & 7);
+    const int64_t o = (m0 + r0) * g.ldc + n + c, left = g.N - n - c;
+#pragma unroll 2
+    for (int i = 0; i < 32; i += 4)
+      if (r0 + i < rows) g8_put4<F32>(g, o + i * g.ldc, *reinterpret_cast<const float4*>(xs + g8_at(r0 + i, c)), left);
+    __syncwarp();
+    return;
+  }
   if (n + lane < g.N) {
     const int64_t o = m0 * g.ldc + n + lane;
-    if (rows == 32) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) g8_put(g, o + i * g.ldc, xs[i * G8_XS_LD + lane]);
-    } else {
-      for (int i = 0; i < rows; ++i) g8_put(g, o + i * g.ldc, xs[i * G8_XS_LD + lane]);
-    }
+#pragma unroll 8
+    for (int i = 0; i < rows; ++i) g8_put<F32>(g, o + i * g.ldc, xs[g8_at(i, lane)]);
   }
   __syncwarp();
 }
@@ -206,7 +235,7 @@ __device__ __forceinline__ void g8_tile(int64_t t, int64_t tiles_m, int64_t tile
 // rows allow it.  8 loads of 16 bytes from the others' shared memory are in
 // flight (61 x 448 x 2560 fp32: 7.0 us; single elements,
 // 4 in flight, 15.5).
-template <int BN, int P>
+template <int BN, int P, bool F32>
 __device__ __forceinline__ void g8_join(const Gemm8Args& g, float* sums, int64_t m0, int64_t n0, int part) {
   using SM = Gemm8Smem<BN>;
   cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
@@ -217,7 +246,7 @@ __device__ __forceinline__ void g8_join(const Gemm8Args& g, float* sums, int64_t
   const int log = g.swap ? 7 : LOG, mask = (1 << log) - 1, ld = g.swap ? SM::PART_LDT : SM::PART_LD;       // C's rows in the tile
   const int64_t row0 = g.swap ? n0 : m0, col0 = g.swap ? m0 : n0, rows = g.swap ? g.N : g.M, cols = g.swap ? g.M : g.N;
   constexpr int SHARE = G8_BM * BN / P;
-  if (g.sectors) {
+  if (g.quads) {
     constexpr int U = 8 / P;
     for (int u0 = threadIdx.x; u0 < SHARE / 4; u0 += U * G8_THREADS) {
       float4 w[U][P];
@@ -236,20 +265,7 @@ __device__ __forceinline__ void g8_join(const Gemm8Args& g, float* sums, int64_t
         float4 v = w[u][0];
 #pragma unroll
         for (int k = 1; k < P; ++k) v = make_float4(v.x + w[u][k].x, v.y + w[u][k].y, v.z + w[u][k].z, v.w + w[u][k].w);
-        const int64_t o = row * g.ldc + col;
-        if (col + 4 <= cols) {
-          if (g.c_bf16)
-            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(g.c) + o) = make_uint2(bf16x2_bits(v.x, v.y), bf16x2_bits(v.z, v.w));
-          else if (g.accumulate)
-            asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};"
-                         ::"l"(reinterpret_cast<float*>(g.c) + o), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
-          else
-            *reinterpret_cast<float4*>(reinterpret_cast<float*>(g.c) + o) = v;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (col + i < cols) g8_put(g, o + i, (&v.x)[i]);
-        }
+        g8_put4<F32>(g, row * g.ldc + col, v, cols - col);
       }
     }
     return;
@@ -272,7 +288,7 @@ __device__ __forceinline__ void g8_join(const Gemm8Args& g, float* sums, int64_t
       float v = w[u][0];
 #pragma unroll
       for (int k = 1; k < P; ++k) v += w[u][k];
-      g8_put(g, row * g.ldc + col, v);
+      g8_put<F32>(g, row * g.ldc + col, v);
     }
   }
 }
@@ -424,7 +440,7 @@ gemm8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     const int qd = warp & 3, own = (warp - 2) >> 2;
     const bool works = BN >= 64 || own == 0;
     const uint32_t tlane = tmem + ((uint32_t)(qd * 32) << 16) + (uint32_t)(own * HALF);
-    float* xs = reinterpret_cast<float*>(gbase + SM::OFF_XS) + (warp - 2) * (32 * G8_XS_LD);
+    float* xs = reinterpret_cast<float*>(gbase + SM::OFF_XS) + (warp - 2) * G8_XS;
     const int segs = kb1 <= kb0 ? 0 : PROMOTE ? (kb1 - kb0 + G8_SEGMENT - 1) / G8_SEGMENT : 1;
     uint32_t seg = 0;
     for (int64_t t = first_tile; t < tiles; t += tile_step) {
@@ -464,7 +480,7 @@ gemm8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
           float v[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) v[k] = k < STEP ? sum[j + k] : 0.f;
-          g8_store32(g, xs, ti * G8_BM + qd * 32, tj * BN + own * HALF + j, v);
+          g8_store32<PROMOTE>(g, xs, ti * G8_BM + qd * 32, tj * BN + own * HALF + j, v);
         }
       } else {
         // to this CTA's own shared memory (the ring is idle: its last MMA has completed), for the cluster
@@ -487,9 +503,9 @@ gemm8_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     cluster.sync();
     int64_t ti, tj;
     g8_tile(first_tile, tiles_m, tiles_n, ti, tj);
-    if (parts == 2) g8_join<BN, 2>(g, reinterpret_cast<float*>(gbase), ti * G8_BM, tj * BN, part);
-    else if (parts == 4) g8_join<BN, 4>(g, reinterpret_cast<float*>(gbase), ti * G8_BM, tj * BN, part);
-    else g8_join<BN, 8>(g, reinterpret_cast<float*>(gbase), ti * G8_BM, tj * BN, part);
+    if (parts == 2) g8_join<BN, 2, PROMOTE>(g, reinterpret_cast<float*>(gbase), ti * G8_BM, tj * BN, part);
+    else if (parts == 4) g8_join<BN, 4, PROMOTE>(g, reinterpret_cast<float*>(gbase), ti * G8_BM, tj * BN, part);
+    else g8_join<BN, 8, PROMOTE>(g, reinterpret_cast<float*>(gbase), ti * G8_BM, tj * BN, part);
     // the others have read this CTA's sums (nothing else is ordered: its results need not have reached memory)
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
@@ -525,7 +541,7 @@ struct PairSmem {
   static constexpr int STAGES = 5;
   static constexpr int OFF_SF = STAGES * STAGE_BYTES;
   static constexpr int OFF_XS = OFF_SF + STAGES * SF_BYTES;            // a scratch of each drain warp
-  static constexpr int OFF_BAR = OFF_XS + G8_EPI_WARPS * 32 * G8_XS_LD * 4;
+  static constexpr int OFF_BAR = OFF_XS + G8_EPI_WARPS * G8_XS * 4;
   static constexpr int BYTES = 1024 + OFF_BAR + 256;
   static constexpr int ACC1 = 224;                                     // second buffer's first column
   static constexpr int SF_COL = ACC1 + BN, SF_COLS = 12;
@@ -724,7 +740,7 @@ gemm8_pair_kernel(const __grid_constant__ PairMaps maps, Gemm8Args g) {
     constexpr int HALF = BN / 2, STEP = 32;            // columns of a warp, and of one read
     const int qd = warp & 3, own = (warp >> 2) - 1;   // tensor-memory lane quadrant, column half
     const uint32_t tlane = tmem + ((uint32_t)(qd * 32) << 16) + own * HALF;
-    float* xs = reinterpret_cast<float*>(smem_raw + (base - raw) + SM::OFF_XS) + (warp - 4) * (32 * G8_XS_LD);
+    float* xs = reinterpret_cast<float*>(smem_raw + (base - raw) + SM::OFF_XS) + (warp - 4) * G8_XS;
     const int segs = PROMOTE ? (nkb + G8_PAIR_SEGMENT - 1) / G8_PAIR_SEGMENT : 1;
     uint32_t seg = 0;
     for (int64_t t = first_tile; t < tiles; t += tile_step) {
@@ -766,7 +782,7 @@ gemm8_pair_kernel(const __grid_constant__ PairMaps maps, Gemm8Args g) {
         float v[STEP];
 #pragma unroll
         for (int k = 0; k < STEP; ++k) v[k] = sum[j + k];
-g8_store32(g, xs, ti * 256 + rank * 128 + qd * 32, tj * BN + own * HALF + (own ? HALF - STEP - j : j), v);
+g8_store32<PROMOTE>(g, xs, ti * 256 + rank * 128 + qd * 32, tj * BN + own * HALF + (own ? HALF - STEP - j : j), v);
       }
     }
   }

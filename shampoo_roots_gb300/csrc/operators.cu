@@ -437,7 +437,8 @@ int precond_gemm8(precond_t ph, int64_t M, int64_t N, int64_t K, const void* A, 
   // and its bytes, which bound the call, are read once).
   const bool swap = M <= 64 && M < N;
   Gemm8Args g = {swap ? N : M, swap ? M : N, K, scale_a, q8_row_blocks(M), scale_b, q8_row_blocks(N), C, ldc,
-                 c_dtype == PRECOND_BF16, accumulate, aligned(C, 32) && ldc * (int64_t)size_of(c_dtype) % 32 == 0, swap, h->op_err};
+                 c_dtype == PRECOND_BF16, accumulate, aligned(C, 32) && ldc * (int64_t)size_of(c_dtype) % 32 == 0,
+                 aligned(C, 4 * size_of(c_dtype)) && ldc % 4 == 0, swap, h->op_err};
   if (swap) {
     std::swap(A, B);
     std::swap(lda, ldb);
@@ -452,11 +453,19 @@ int precond_gemm8(precond_t ph, int64_t M, int64_t N, int64_t K, const void* A, 
   int parts = 1;
   const int places = h->num_sms * (bn <= 32 ? 2 : 1);
   while (parts < 8 && tiles * parts * 2 <= places && parts * 2 <= groups) parts *= 2;
-  // Pairs of CTAs where they are expected to end first: a 256 x 256 tile's block of K takes a pair 0.30 us,
-  // a 128 x 128 tile's a CTA 0.25 us, and joining stretches 2 us.
+  // Pairs of CTAs where they are expected to end first: a 256 x 256 tile's block of K takes a pair 0.30 us, a 128 x 128
+  // tile's a CTA 0.25 us; results leave beside the next tile's products, in the times below (as g8_store32 writes
+  // them: rows of whole sectors, 4 elements at a time, single ones; bf16, fp32); joining stretches takes 1.5 us more.
+  // (Measured: 6734 x 832 x 468 accumulated 17.3 us in pairs, 11.6 alone; 2048^3 to bf16 11.1 and 14.1.)
+  static const double results_us[2][3][2] = {{{1.1, 1.3}, {2.0, 2.4}, {3.0, 4.0}}, {{2.5, 3.5}, {4.0, 6.0}, {4.5, 8.0}}};
+  const int how = g.sectors && !accumulate ? 0 : g.quads ? 1 : 2;
+  auto expected = [&](int pair, double products, int64_t waves) {
+    const double results = results_us[pair][how][!g.c_bf16];
+    return products + (double)(waves - 1) * std::max(products, results) + results;
+  };
   const int64_t pair_tiles = ((g.M + 255) / 256) * ((g.N + 255) / 256);
-  const double pair_us = 0.30 * blocks * (double)((pair_tiles + h->pairs - 1) / h->pairs);
-  const double lone_us = 0.25 * ((groups + parts - 1) / parts * 4) * (double)((tiles * parts + h->num_sms - 1) / h->num_sms) + (parts > 1 ? 2.0 : 0.0);
+  const double pair_us = expected(1, 0.30 * blocks, (pair_tiles + h->pairs - 1) / h->pairs);
+  const double lone_us = expected(0, 0.25 * ((groups + parts - 1) / parts * 4), (tiles * parts + h->num_sms - 1) / h->num_sms) + (parts > 1 ? 1.5 : 0.0);
   if (bn == 128 && K > 0 && pair_us <= lone_us) {
     if ((rc = launch_pair(h, A, lda, B, ldb, g, st))) return rc;
     ++h->launches;
@@ -535,7 +544,12 @@ int precond_distill(precond_t ph, const void* logits, int dtype, int64_t rows, i
                    rows, vocab, top, temperature, (float2*)workspace, nullptr};
   const int parts = distill_parts(rows, vocab, dtype);
   const int64_t vecs = ((vocab + parts - 1) / parts + 63) / 64 * 64 * (int64_t)sz / 16;
-  const int i = vecs <= DISTILL_THREADS ? 1 : vecs <= 2 * DISTILL_THREADS ? 2 : vecs <= 4 * DISTILL_THREADS ? 3 : vecs <= 8 * DISTILL_THREADS ? 4 : 0;
+  // Vectors a thread: one block after another on an SM hides nothing, so blocks that only stream have as few threads as
+  // hold their part, 64 at least (8192 x 8000 bf16: 53 us, with 512 threads of 2 vectors 77); a block that also waits
+  // for its candidates as many as it can.
+  int i = 0;
+  if (vecs <= 8 * DISTILL_THREADS)
+    for (i = 1; i < 4 && (split ? vecs >= 128 << (i - 1) : vecs > DISTILL_THREADS << (i - 1));) ++i;
   const int nv = i ? 1 << (i - 1) : 0;
   const int threads = nv == 0 ? DISTILL_THREADS : (int)std::max<int64_t>(64, ((vecs + nv - 1) / nv + 31) / 32 * 32);
   if (split && dlogits == logits) {
