@@ -406,9 +406,11 @@ int precond_quantize8(precond_t ph, const void* x, int dtype, int64_t rows, int6
   Quant8Args a = {x, ldx, x_scale, (int)rows, (int)cols, block == PRECOND_BLOCK_TILE, (uint8_t*)q, ldq, scale, (uint8_t*)qt, ldqt, scale_t};
   // 8 columns in one load: 16 bytes of bf16, 32 of fp32
   const int64_t step = 8 * (int64_t)size_of(dtype);
-  const int vec = aligned(x, step) && ldx * (int64_t)size_of(dtype) % step == 0;
-  auto k = dtype == PRECOND_E4M3 ? quantize8_kernel<QIN_E4M3> : dtype == PRECOND_BF16 ? quantize8_kernel<QIN_BF16> : quantize8_kernel<QIN_F32>;
-  OP_CK(launch(k, dim3((unsigned)tiles), dim3(256), 0, (cudaStream_t)stream, 1, a, vec));
+  const bool vec = aligned(x, step) && ldx * (int64_t)size_of(dtype) % step == 0;
+  auto k = dtype == PRECOND_E4M3   ? quantize8_kernel<QIN_E4M3, true>
+           : dtype == PRECOND_BF16 ? (vec ? quantize8_kernel<QIN_BF16, true> : quantize8_kernel<QIN_BF16, false>)
+                                   : (vec ? quantize8_kernel<QIN_F32, true> : quantize8_kernel<QIN_F32, false>);
+  OP_CK(launch(k, dim3((unsigned)tiles), dim3(256), 0, (cudaStream_t)stream, 1, a));
   ++h->launches;
   return PRECOND_OK;
 }

@@ -33,10 +33,10 @@ struct Quant8Args {
 // A thread's 8 x 8 elements as stored; get() gives one as fp32.
 template <int IN> struct QuantTile;
 template <> struct QuantTile<QIN_F32> {
+  typedef float Element;
   uint32_t w[8][8];
   __device__ __forceinline__ float get(int i, int j) const { return __uint_as_float(w[i][j]); }
   __device__ __forceinline__ void set_nan(int i, int j) { w[i][j] = 0x7FFFFFFFu; }
-  static constexpr int WORDS = 8;
   __device__ __forceinline__ void load(const Quant8Args& a, int i, int64_t row, int c) {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(a.x) + row * a.ldx + c;
     if (c + 8 <= a.cols) {
@@ -46,39 +46,14 @@ template <> struct QuantTile<QIN_F32> {
       for (int j = 0; j < 8; ++j) w[i][j] = c + j < a.cols ? p[j] : 0;
     }
   }
-  __device__ __forceinline__ void load_stripes(const Quant8Args& a, int i, int64_t row, int c0, int tx) {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(a.x) + row * a.ldx;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[i][j] = c0 + 16 * j + tx < a.cols ? p[c0 + 16 * j + tx] : 0;
-  }
-  __device__ __forceinline__ void put_stripes(int i, void* xs, int tx) const {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) reinterpret_cast<uint32_t*>(xs)[16 * j + tx] = w[i][j];
-  }
 };
 template <> struct QuantTile<QIN_BF16> {
+  typedef __nv_bfloat16 Element;
   uint32_t w[8][4];
   __device__ __forceinline__ float get(int i, int j) const {
     return __uint_as_float(j & 1 ? w[i][j >> 1] & 0xFFFF0000u : w[i][j >> 1] << 16);
   }
   __device__ __forceinline__ void set_nan(int i, int j) { w[i][j >> 1] |= j & 1 ? 0x7FFF0000u : 0x7FFFu; }
-  static constexpr int WORDS = 4;
-  __device__ __forceinline__ void load_stripes(const Quant8Args& a, int i, int64_t row, int c0, int tx) {
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(a.x) + row * a.ldx;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = c0 + 32 * j + tx;
-      const uint32_t lo = k < a.cols ? p[k] : 0, hi = k + 16 < a.cols ? p[k + 16] : 0;
-      w[i][j] = lo | hi << 16;
-    }
-  }
-  __device__ __forceinline__ void put_stripes(int i, void* xs, int tx) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      reinterpret_cast<uint16_t*>(xs)[32 * j + tx] = (uint16_t)w[i][j];
-      reinterpret_cast<uint16_t*>(xs)[32 * j + 16 + tx] = (uint16_t)(w[i][j] >> 16);
-    }
-  }
   __device__ __forceinline__ void load(const Quant8Args& a, int i, int64_t row, int c) {
     const uint16_t* p = reinterpret_cast<const uint16_t*>(a.x) + row * a.ldx + c;
     if (c + 8 <= a.cols) {
@@ -94,6 +69,7 @@ template <> struct QuantTile<QIN_BF16> {
   }
 };
 template <> struct QuantTile<QIN_E4M3> {
+  typedef void Element;              // its rows are aligned
   uint32_t w[8][2];
   float scale[8];                    // of the rows: a tile's columns are one block
   __device__ __forceinline__ float get(int i, int j) const {
@@ -102,9 +78,6 @@ template <> struct QuantTile<QIN_E4M3> {
     return (j & 1 ? hi : lo) * scale[i];
   }
   __device__ __forceinline__ void set_nan(int i, int j) {}          // e4m3's only non-finite value is NaN already
-  static constexpr int WORDS = 2;
-  __device__ __forceinline__ void load_stripes(const Quant8Args&, int, int64_t, int, int) {}    // its rows are aligned
-  __device__ __forceinline__ void put_stripes(int, void*, int) const {}
   __device__ __forceinline__ void load(const Quant8Args& a, int i, int64_t row, int c) {
     const uint8_t* p = reinterpret_cast<const uint8_t*>(a.x) + row * a.ldx + c;   // 16-byte aligned rows, c % 8 == 0
     w[i][0] = w[i][1] = 0;
@@ -118,6 +91,80 @@ template <> struct QuantTile<QIN_E4M3> {
         if (c + j < a.cols) w[i][j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
     }
     scale[i] = c < a.cols ? q8_value(a.x_scale[q8_scale_at(row, (int)(c >> 7), q8_row_blocks(a.rows))]) : 0.f;
+  }
+};
+
+// A row of a tile that is not aligned, taken by a half-warp as the aligned
+// granules of 16 bytes that lie inside it (lane tx granules tx, tx + 16) and the
+// elements before and after those, one a lane (form8.cuh does the same for 512
+// elements of a warp; 8000 x 7001 bf16 by rows: 46 us, in stripes 60).
+template <typename T>
+struct TileRow {
+  static constexpr int G = 16 / sizeof(T), PER_LANE = 8 / G;
+  const T* p;
+  int shift, head, len, edge;         // edge: this lane's single element, or -1
+  __device__ __forceinline__ TileRow(const Quant8Args& a, int64_t row, int c0, int tx) {
+    p = reinterpret_cast<const T*>(a.x) + row * a.ldx + c0;
+    shift = (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T)) & (G - 1);
+    head = G - shift;
+    len = min(a.cols - c0, 128);
+    const int tail = head + max(len - head, 0) / G * G;
+    edge = tx < G ? (tx < head && tx < len ? tx : -1) : tx < 2 * G && tail + tx - G < len ? tail + tx - G : -1;
+  }
+  __device__ __forceinline__ void load(uint32_t* w, uint32_t& single, int tx) const {
+#pragma unroll
+    for (int k = 0; k < PER_LANE; ++k) {
+      const int e = head + (tx + 16 * k) * G;
+      w[4 * k] = w[4 * k + 1] = w[4 * k + 2] = w[4 * k + 3] = 0;
+      if (e + G <= len)
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[4 * k]), "=r"(w[4 * k + 1]), "=r"(w[4 * k + 2]), "=r"(w[4 * k + 3]) : "l"(p + e) : "memory");
+    }
+    single = 0;
+    if (edge >= 0) single = element_bits(p + edge);
+  }
+  // into order, through the half-warp's scratch of 34 granules
+  __device__ __forceinline__ void settle(uint32_t* w, uint32_t single, int tx, uint8_t* xs) const {
+    uint4* g = reinterpret_cast<uint4*>(xs);
+#pragma unroll
+    for (int k = 0; k < PER_LANE; ++k) g[tx + 16 * k + 1] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    __syncwarp();
+    const int at = edge >= 0 ? edge : tx < head ? tx : -1;       // a head's past the row's end: zero
+    if (at >= 0) reinterpret_cast<typename Storage<T>::type*>(xs)[at + shift] = (typename Storage<T>::type)single;
+    __syncwarp();
+    uint32_t t[4 * PER_LANE + 4];
+#pragma unroll
+    for (int k = 0; k <= PER_LANE; ++k) {
+      const uint4 x = g[PER_LANE * tx + k];
+      t[4 * k] = x.x; t[4 * k + 1] = x.y; t[4 * k + 2] = x.z; t[4 * k + 3] = x.w;
+    }
+    shift_words<4 * PER_LANE + 4, T>(t, w, 4 * PER_LANE, shift);
+    __syncwarp();
+  }
+};
+// fp32: in stripes, lane tx elements tx, tx + 16, ... (8000 x 7001 by tiles, both ways: 79 us, in
+// granules 94).
+template <>
+struct TileRow<float> {
+  const uint32_t* p;
+  int len;
+  __device__ __forceinline__ TileRow(const Quant8Args& a, int64_t row, int c0, int)
+      : p(reinterpret_cast<const uint32_t*>(a.x) + row * a.ldx + c0), len(a.cols - c0) {}
+  __device__ __forceinline__ void load(uint32_t* w, uint32_t&, int tx) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (16 * j + tx < len) w[j] = p[16 * j + tx];
+  }
+  __device__ __forceinline__ void settle(uint32_t* w, uint32_t, int tx, uint8_t* xs) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) reinterpret_cast<uint32_t*>(xs)[16 * j + tx] = w[j];
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint4 x = reinterpret_cast<const uint4*>(xs)[2 * tx + k];
+      w[4 * k] = x.x; w[4 * k + 1] = x.y; w[4 * k + 2] = x.z; w[4 * k + 3] = x.w;
+    }
+    __syncwarp();
   }
 };
 
@@ -178,8 +225,8 @@ __device__ __forceinline__ unsigned quant_maxima_bf16(const QuantTile<QIN_BF16>&
   return max(most << 16, most & 0xFFFF0000u);
 }
 
-template <int IN>
-__global__ void __launch_bounds__(256, IN == QIN_F32 ? 2 : IN == QIN_BF16 ? 4 : 3) quantize8_kernel(Quant8Args a, int vec) {
+template <int IN, bool VEC>
+__global__ void __launch_bounds__(256, IN == QIN_F32 ? 2 : IN == QIN_BF16 ? (VEC ? 4 : 3) : 3) quantize8_kernel(Quant8Args a) {
   __shared__ __align__(16) uint8_t tr[128 * 128];
   __shared__ unsigned cmax[8][128];
   __shared__ unsigned char cexp[128];
@@ -193,29 +240,29 @@ __global__ void __launch_bounds__(256, IN == QIN_F32 ? 2 : IN == QIN_BF16 ? 4 : 
   let_next_start();
 
   QuantTile<IN> v;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (r0 + i < a.rows) {
-      if (vec) v.load(a, i, r0 + i, c0);
-      else v.load_stripes(a, i, r0 + i, tj * 128, tx);
-    } else {
-#pragma unroll
-      for (auto& x : v.w[i]) x = 0;
-      if constexpr (IN == QIN_E4M3) v.scale[i] = 0.f;
-    }
-  }
-  if (!vec) {
-    // rows that are not aligned came in stripes (lane tx columns tx, tx + 16, ...: consecutive in memory);
-    // each half-warp exchanges its rows through shared memory, 512 bytes
-    uint8_t* xs = tr + (threadIdx.x >> 4) * 512;
+  if constexpr (VEC) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      v.put_stripes(i, xs, tx);
-      __syncwarp();
+      if (r0 + i < a.rows) {
+        v.load(a, i, r0 + i, c0);
+      } else {
 #pragma unroll
-      for (int k = 0; k < QuantTile<IN>::WORDS; ++k) v.w[i][k] = reinterpret_cast<const uint32_t*>(xs)[QuantTile<IN>::WORDS * tx + k];
-      __syncwarp();
+        for (auto& x : v.w[i]) x = 0;
+        if constexpr (IN == QIN_E4M3) v.scale[i] = 0.f;
+      }
     }
+  } else {
+    typedef TileRow<typename QuantTile<IN>::Element> Row;
+    uint32_t single[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      single[i] = 0;
+#pragma unroll
+      for (auto& x : v.w[i]) x = 0;
+      if (r0 + i < a.rows) Row(a, r0 + i, tj * 128, tx).load(v.w[i], single[i], tx);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) Row(a, r0 + i, tj * 128, tx).settle(v.w[i], single[i], tx, tr + ty * 1024);
   }
   unsigned rexp[8], cm[8], most;
   if constexpr (IN == QIN_BF16) most = quant_maxima_bf16(v, rexp, cm);
