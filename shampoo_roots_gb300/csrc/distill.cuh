@@ -138,11 +138,14 @@ __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ void set_float(float* p, float x) { *p = x; }
 __device__ __forceinline__ void set_float(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// A row's shared memory, as large as its candidates need.
+// A row's shared memory, as large as its candidates need.  Up to DISTILL_FEW of them only their ids lie here, and p over
+// the table when it has served: the streaming kernel, which may start while the candidates' still runs, has as much L1
+// as that leaves it (with all of the SM's memory shared it took 870 us for 8192 x 131072, not 717).
+constexpr int DISTILL_FEW = 256;
 struct DistillShared {
   float2* sums;                     // (maximum, sum) of the streaming warps of the cluster's blocks
   float* p; float* logp; float* z; int* id;      // candidates; id -1: none
-  int* key;                         // a table to find equal ids
+  uint16_t* key;                    // a table to find equal ids
   float* most;                      // the teacher's largest logit
   int slots;
   static __host__ __device__ int slots_for(int top) {
@@ -151,18 +154,18 @@ struct DistillShared {
     return n;
   }
   static __host__ __device__ int bytes(int top, int sums) {
-    return ((sums + 1) / 2 * 2) * 8 + 16 * ((top + 3) / 4 * 4) + 4 * slots_for(top) + 16;
+    return (sums + 1) / 2 * 16 + (top <= DISTILL_FEW ? 4 : 16) * ((top + 3) / 4 * 4) + 2 * slots_for(top) + 16;
   }
   __device__ __forceinline__ DistillShared(uint8_t* base, int top, int nsums) {
     const int n = (top + 3) / 4 * 4;
     sums = reinterpret_cast<float2*>(base);
-    p = reinterpret_cast<float*>(sums + (nsums + 1) / 2 * 2);
+    id = reinterpret_cast<int*>(sums + (nsums + 1) / 2 * 2);
+    slots = slots_for(top);
+    key = reinterpret_cast<uint16_t*>(id + n);
+    most = reinterpret_cast<float*>(key + slots);
+    p = top <= DISTILL_FEW ? reinterpret_cast<float*>(key) : most + 4;
     logp = p + n;
     z = logp + n;
-    id = reinterpret_cast<int*>(z + n);
-    slots = slots_for(top);
-    key = id + n;
-    most = reinterpret_cast<float*>(key + slots);
   }
 };
 
@@ -213,50 +216,58 @@ __device__ __forceinline__ float warp_max_nan(float m) {
   return m;
 }
 
-// Whether an id occurs twice among those >= 0 of sh.id (j = lane, lane + 32, ...; -1 elsewhere).  Each id writes its
-// index to a place of the table that its hash and the round give, and reads it back: an index of the same id there is
-// a second occurrence, one of another id a collision, which the next round tells apart.  Two equal ids meet in the
-// round in which one of them is read back, at the latest, since they always have the same place.
-__device__ __forceinline__ bool repeated_ids(const DistillShared& sh, int top) {
+// Second occurrences among the ids >= 0 of sh.id (j = lane, lane + 32, ...; -1 elsewhere): the lane's, a bit each; of
+// equal ids all but one.  Each id writes its index to a place of the table that its hash and the round give, and reads
+// it back: an index of the same id there is another occurrence, one of another id a collision, which the next round
+// tells apart.  Equal ids always have the same place, so they are all done in the round in which one of them is read
+// back.
+__device__ __forceinline__ unsigned repeated_ids(const DistillShared& sh, int top) {
   const int lane = threadIdx.x & 31, mask = sh.slots - 1;
-  unsigned open = 0;                     // candidates that have not been read back
+  unsigned open = 0, twice = 0;          // candidates that have not been read back; second occurrences
   for (int q = 0; lane + 32 * q < top; ++q) open |= sh.id[lane + 32 * q] >= 0 ? 1u << q : 0;
-  bool twice = false;
   for (unsigned round = 1; __any_sync(0xffffffffu, open != 0); round += 2) {
     auto place = [&](int id) { return (int)(((unsigned)id * 2654435761u * round) >> 15) & mask; };
     for (unsigned m = open; m; m &= m - 1) {
       const int j = lane + 32 * (__ffs(m) - 1);
-      sh.key[place(sh.id[j])] = j;
+      sh.key[place(sh.id[j])] = (uint16_t)j;
     }
     __syncwarp();
     for (unsigned m = open; m; m &= m - 1) {
       const int q = __ffs(m) - 1, j = lane + 32 * q, id = sh.id[j], k = sh.key[place(id)];
-      if (k == j) open &= ~(1u << q);
-      else if (sh.id[k] == id) twice = true, open &= ~(1u << q);
+      if (k == j || sh.id[k] == id) open &= ~(1u << q);
+      if (k != j && sh.id[k] == id) twice |= 1u << q;
     }
     __syncwarp();
   }
-  return __any_sync(0xffffffffu, twice);
+  return twice;
 }
-// Then: p of the first of an id becomes the sum over that id in order, the others' ids -1 (the loss is done with logp).
-__device__ __forceinline__ void unite_ids(const DistillShared& sh, int top) {
+// Then, one id after another: p of its first place becomes the sum over all of them in order, the others' ids -1 (the
+// loss is done with p).
+__device__ __forceinline__ void unite_ids(const DistillShared& sh, int top, unsigned twice) {
   const int lane = threadIdx.x & 31;
-  for (int j = lane; j < top; j += 32) {
-    float p = 0.f;
-    bool again = false;
-    for (int i = 0; i < top; ++i)
-      if (sh.id[i] == sh.id[j]) {
-        p += sh.p[i];
-        again |= i < j;
+  for (unsigned any; (any = __ballot_sync(0xffffffffu, twice != 0)) != 0;) {
+    const int from = __ffs(any) - 1;
+    const int id = sh.id[from + 32 * (__shfl_sync(0xffffffffu, __ffs(twice), from) - 1)];
+    __syncwarp();
+    float sum = 0.f;
+    int first = -1;
+    for (int q = 0; 32 * q < top; ++q) {
+      const int j = lane + 32 * q;
+      const bool same = j < top && sh.id[j] == id;
+      for (unsigned m = __ballot_sync(0xffffffffu, same); m; m &= m - 1) {
+        const int k = __ffs(m) - 1 + 32 * q;
+        if (first < 0) first = k;
+        sum += sh.p[k];
       }
-    sh.logp[j] = again ? -1.f : p;       // -1: not the first
+      if (same) {
+        twice &= ~(1u << q);
+        if (j != first) sh.id[j] = -1;
+      }
+    }
+    __syncwarp();
+    if (lane == 0) sh.p[first] = sum;
+    __syncwarp();
   }
-  __syncwarp();
-  for (int j = lane; j < top; j += 32) {
-    if (sh.logp[j] == -1.f) sh.id[j] = -1;
-    sh.p[j] = sh.logp[j];
-  }
-  __syncwarp();
 }
 
 // Up to 128 or 256: Q a lane, in registers.
@@ -309,12 +320,13 @@ struct FewCandidates {
       if (lane + 32 * q < a.top) sh.id[lane + 32 * q] = id[q];
     }
     __syncwarp();
-    if (!repeated_ids(sh, a.top)) return;
+    const unsigned twice = repeated_ids(sh, a.top);
+    if (!__any_sync(0xffffffffu, twice != 0)) return;
 #pragma unroll
     for (int q = 0; q < Q; ++q)
       if (lane + 32 * q < a.top) sh.p[lane + 32 * q] = p[q];
     __syncwarp();
-    unite_ids(sh, a.top);
+    unite_ids(sh, a.top, twice);
 #pragma unroll
     for (int q = 0; q < Q; ++q)
       if (lane + 32 * q < a.top) {
@@ -370,7 +382,7 @@ struct ManyCandidates {
     for (int j = threadIdx.x & 31; j < a.top; j += 32)
       if (sh.id[j] < sl.lo || sh.id[j] >= sl.hi) sh.id[j] = -1;
     __syncwarp();
-    if (repeated_ids(sh, a.top)) unite_ids(sh, a.top);
+    unite_ids(sh, a.top, repeated_ids(sh, a.top));
   }
   template <typename T>
   __device__ __forceinline__ void patch(const DistillArgs& a, const DistillShared& sh, T* dz, float scale, float c, const Shift& at, float s) const {
@@ -643,7 +655,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS + (FUSED ? 32 : 0), 2) distill
       }
     };
     if (a.top <= 128) work(FewCandidates<4>());
-    else if (a.top <= 256) work(FewCandidates<8>());
+    else if (a.top <= DISTILL_FEW) work(FewCandidates<8>());
     else work(ManyCandidates());
   } else if (part == 0 && lane == 0) {
     a.loss[row] = 0.0f;

@@ -64,6 +64,23 @@ int cuda_error(const char* what, cudaError_t e) {
     if (e_ != cudaSuccess) return cuda_error(#call, e_);         \
   } while (0)
 
+typedef void (*DistillKernel)(DistillArgs);
+const DistillKernel distill_fused_kernels[2][5] = {
+    {distill_kernel<float, 0, true>, distill_kernel<float, 1, true>, distill_kernel<float, 2, true>, distill_kernel<float, 4, true>,
+     distill_kernel<float, 8, true>},
+    {distill_kernel<__nv_bfloat16, 0, true>, distill_kernel<__nv_bfloat16, 1, true>, distill_kernel<__nv_bfloat16, 2, true>,
+     distill_kernel<__nv_bfloat16, 4, true>, distill_kernel<__nv_bfloat16, 8, true>}};
+const DistillKernel distill_split_kernels[2][5] = {
+    {distill_kernel<float, 0, false>, distill_kernel<float, 1, false>, distill_kernel<float, 2, false>,
+     distill_kernel<float, 4, false>, distill_kernel<float, 8, false>},
+    {distill_kernel<__nv_bfloat16, 0, false>, distill_kernel<__nv_bfloat16, 1, false>, distill_kernel<__nv_bfloat16, 2, false>,
+     distill_kernel<__nv_bfloat16, 4, false>, distill_kernel<__nv_bfloat16, 8, false>}};
+const DistillKernel distill_candidates_kernels[2][3] = {
+    {distill_candidates_kernel<float, FewCandidates<4>>, distill_candidates_kernel<float, FewCandidates<8>>,
+     distill_candidates_kernel<float, ManyCandidates>},
+    {distill_candidates_kernel<__nv_bfloat16, FewCandidates<4>>, distill_candidates_kernel<__nv_bfloat16, FewCandidates<8>>,
+     distill_candidates_kernel<__nv_bfloat16, ManyCandidates>}};
+
 // The device current and the kernels' attributes set.
 template <int BN>
 cudaError_t gemm8_attributes() {
@@ -106,6 +123,11 @@ int prepare(Handle* h) {
     OP_CK(cudaMalloc(&h->op_err, sizeof(unsigned int)));
     OP_CK(cudaMemset(h->op_err, 0, sizeof(unsigned int)));
     OP_CK(cudaDeviceSynchronize());
+    // The streaming kernels live on L1: no more of the SM's memory is shared than they ask for.
+    for (int t = 0; t < 2; ++t)
+      for (int i = 0; i < 5; ++i)
+        for (DistillKernel k : {distill_fused_kernels[t][i], distill_split_kernels[t][i]})
+          OP_CK(cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxL1));
     h->op_ready = true;
   }
   return PRECOND_OK;
@@ -198,20 +220,11 @@ int distill_parts(int64_t rows, int64_t vocab, int dtype) {
     parts *= 2;
   return parts;
 }
-// Whether the candidates have a kernel of their own: from four blocks' work a SM on, the blocks stay for them.
-bool distill_split(int64_t rows, int64_t vocab, int dtype) { return rows * distill_parts(rows, vocab, dtype) >= 4 * PLAN_SMS; }
-typedef void (*DistillKernel)(DistillArgs);
-const DistillKernel distill_fused_kernels[2][5] = {
-    {distill_kernel<float, 0, true>, distill_kernel<float, 1, true>, distill_kernel<float, 2, true>, distill_kernel<float, 4, true>,
-     distill_kernel<float, 8, true>},
-    {distill_kernel<__nv_bfloat16, 0, true>, distill_kernel<__nv_bfloat16, 1, true>, distill_kernel<__nv_bfloat16, 2, true>,
-     distill_kernel<__nv_bfloat16, 4, true>, distill_kernel<__nv_bfloat16, 8, true>}};
-const DistillKernel distill_split_kernels[2][5] = {
-    {distill_kernel<float, 0, false>, distill_kernel<float, 1, false>, distill_kernel<float, 2, false>,
-     distill_kernel<float, 4, false>, distill_kernel<float, 8, false>},
-    {distill_kernel<__nv_bfloat16, 0, false>, distill_kernel<__nv_bfloat16, 1, false>, distill_kernel<__nv_bfloat16, 2, false>,
-     distill_kernel<__nv_bfloat16, 4, false>, distill_kernel<__nv_bfloat16, 8, false>}};
-
+// Whether the candidates have a kernel of their own: with many rows or blocks, one more launch costs less than warps
+// that wait for them (2000 x 131072 bf16, 8000 blocks: 187 us, together 228; 1000 x 32000 fp32, 2000 blocks: 49 and 46).
+bool distill_split(int64_t rows, int64_t vocab, int dtype) {
+  return rows >= 12 * PLAN_SMS || rows * distill_parts(rows, vocab, dtype) >= 24 * PLAN_SMS;
+}
 // ------------------------------------------------------------------------- product
 int encode8(Handle* h, CUtensorMap* map, const void* q, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
   cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
@@ -546,12 +559,11 @@ int precond_distill(precond_t ph, const void* logits, int dtype, int64_t rows, i
                    rows, vocab, top, temperature, (float2*)workspace, nullptr};
   const int parts = distill_parts(rows, vocab, dtype);
   const int64_t vecs = ((vocab + parts - 1) / parts + 63) / 64 * 64 * (int64_t)sz / 16;
-  // Vectors a thread: one block after another on an SM hides nothing, so blocks that only stream have as few threads as
-  // hold their part, 64 at least (8192 x 8000 bf16: 53 us, with 512 threads of 2 vectors 77); a block that also waits
-  // for its candidates as many as it can.
+  // Vectors a thread: one block after another on an SM hides nothing, so a block has as few threads as hold its part, 64
+  // at least (8192 x 8000 bf16: 53 us, with 512 threads of 2 vectors 77).
   int i = 0;
   if (vecs <= 8 * DISTILL_THREADS)
-    for (i = 1; i < 4 && (split ? vecs >= 128 << (i - 1) : vecs > DISTILL_THREADS << (i - 1));) ++i;
+    for (i = 1; i < 4 && vecs >= 128 << (i - 1);) ++i;
   const int nv = i ? 1 << (i - 1) : 0;
   const int threads = nv == 0 ? DISTILL_THREADS : (int)std::max<int64_t>(64, ((vecs + nv - 1) / nv + 31) / 32 * 32);
   if (split && dlogits == logits) {
@@ -567,15 +579,9 @@ int precond_distill(precond_t ph, const void* logits, int dtype, int64_t rows, i
   if (split) {
     // a warp a row, eight to a block where their candidates fit
     const int each = DistillShared::bytes(top, 0), warps = std::max(1, std::min(8, (48 << 10) / each));
-    const int in = top <= 128 ? 0 : top <= 256 ? 1 : 2;          // registers of 4 or 8 a lane, shared memory
-    static const DistillKernel kernels[2][3] = {
-        {distill_candidates_kernel<float, FewCandidates<4>>, distill_candidates_kernel<float, FewCandidates<8>>,
-         distill_candidates_kernel<float, ManyCandidates>},
-        {distill_candidates_kernel<__nv_bfloat16, FewCandidates<4>>, distill_candidates_kernel<__nv_bfloat16, FewCandidates<8>>,
-         distill_candidates_kernel<__nv_bfloat16, ManyCandidates>}};
-    auto k = kernels[bf16][in];
-    OP_CK(launch(k,
-                 dim3((unsigned)((rows + warps - 1) / warps)), dim3(32 * warps), (size_t)each * warps, st, 1, a));
+    const int in = top <= 128 ? 0 : top <= DISTILL_FEW ? 1 : 2;  // registers of 4 or 8 a lane, shared memory
+    auto k = distill_candidates_kernels[bf16][in];
+    OP_CK(launch(k, dim3((unsigned)((rows + warps - 1) / warps)), dim3(32 * warps), (size_t)each * warps, st, 1, a));
     ++h->launches;
   }
   return PRECOND_OK;

@@ -468,6 +468,22 @@ def test_distill_candidate_counts(pc, rows, vocab, top, dtype):
     check_distill(pc, z, ids, t, w, 1.5)
 
 
+@pytest.mark.parametrize("rows,vocab,top", [(2000, 333, 40), (2100, 1001, 5), (1900, 3001, 200), (460, 70001, 30), (1900, 2048, 1024)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_distill_very_many_rows(pc, rows, vocab, top, dtype):
+    """As test_distill_many_rows, with more rows than run at once; every id twice in some."""
+    z, ids, t, w = distill_inputs(rows, vocab, top, dtype)
+    ids[5::9] = -1
+    ids[7::11] = ids[7::11, :1]
+    ids[2::17, top // 2:] = ids[2::17, :top - top // 2]
+    t[3::13] = -math.inf
+    a = check_distill(pc, z, ids, t, w, 1.5)
+    b = check_distill(pc, z, ids, t, w, 1.5, in_place=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    c = check_distill(pc, z, ids, t, w, 1.5, grad=False)
+    assert torch.equal(a[0], c[0])
+
+
 def test_distill_types_and_places(pc):
     z, ids, t, w = distill_inputs(11, 1003, 24, "bf16", ids64=True, tdtype="bf16")
     check_distill(pc, z, ids, t, w, 1.0)
