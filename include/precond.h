@@ -306,7 +306,9 @@ int precond_step_schedule(int p, double l0, double fold, int degree, int max_ste
  *  - Work is enqueued on `stream` and uses no memory but the caller's: calls on
  *    several streams need no ordering among themselves, and every call may be
  *    captured into a CUDA graph, once one call of this group has run on the
- *    handle (it sets kernel attributes).
+ *    handle (it sets kernel attributes).  Kernels of this group are programmatic
+ *    dependents: one may take its place on an SM while its predecessor in the
+ *    stream ends, and touches no memory before that has completed.
  *  - Outputs may not overlap inputs or each other unless the call says so (EINVAL).
  *  - Results do not depend on timing: no sum's order changes between calls.
  *
@@ -374,8 +376,10 @@ int precond_quantize8(precond_t h, const void* x, int dtype, int64_t rows, int64
 /*
  * C = A B^T, or C += A B^T (accumulate, PRECOND_F32 only): A is M x K and B is
  * N x K in 8-bit form, C is M x N in PRECOND_F32 or PRECOND_BF16 (`c_dtype`).
- * Products are exact; sums are fp32, for an fp32 C in stretches of 512 columns
- * that are added to each other in round-to-nearest.
+ * Products are exact; sums are fp32 of the tensor core, which truncates, for an
+ * fp32 C in stretches of 512 or 1024 columns that are added to each other in
+ * round-to-nearest.  Accumulating, the addition to C is the memory's: it is
+ * rounded to nearest, and a subnormal result becomes zero.
  */
 int precond_gemm8(precond_t h, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const uint8_t* scale_a,
                   const void* B, int64_t ldb, const uint8_t* scale_b, void* C, int64_t ldc, int c_dtype,

@@ -14,12 +14,16 @@
 // registers are read twice.
 //
 // The candidates take one warp some microseconds of latency: two dependent loads,
-// a softmax, a table that unites equal ids.  Where the rows fit the GPU at once
-// that warp is part of the row's block, beside those that stream the logits.
-// Many rows leave the candidates to a second kernel with a warp a row, which
-// finds the (m, S) of the rows in a workspace: as a part of each block that warp
-// kept it on the SM longer than the logits did (8192 x 131072: 904 us, without
-// candidates 713).  A call in place gathers the candidates' logits first.
+// a softmax, a table that unites equal ids.  That warp is part of the row's
+// block, beside those that stream the logits.  Many rows leave the candidates to
+// a second kernel with a warp a row, which finds the (m, S) of the rows in a
+// workspace: as a part of each block that warp kept it on the SM longer than the
+// logits did (8192 x 131072: 904 us, without candidates 713).  A call in place
+// gathers the candidates' logits first.
+//
+// Measured: 8192 x 131072 bf16, 128 candidates, 735 us, 81 % of the copy
+// bandwidth; 1000 x 32000 fp32, 64 candidates, 50 us, 71 %; 24 x 50001 without a
+// gradient 4.1 us.
 //
 // With c = log2(e) / tau and m = max(z), q_v = 2^(z_v c - k) / S, S = sum 2^(z_v
 // c - k), k = m c: the exponent is one fma, and the rounding of k cancels.  Where
@@ -675,9 +679,8 @@ __global__ void __launch_bounds__(256) distill_keep_kernel(DistillArgs a) {
   a.kept[i] = id >= 0 && id < a.vocab ? as_float((reinterpret_cast<const T*>(a.z) + row * a.ldz)[id]) : 0.f;
 }
 
-// Many rows: a warp does the loss and the candidates' gradients of a row, after distill_kernel.  Four blocks an SM:
-// with six (40 registers) this kernel takes 60 us, not 47, at 8192 x 128 candidates, and the next call's first kernel,
-// which starts beside it, loses another 100.
+// Many rows: a warp does the loss and the candidates' gradients of a row, after distill_kernel; 47 us at 8192 x 128
+// candidates, with 40 registers (six blocks an SM) 60.
 template <typename T, typename C>
 __global__ void __launch_bounds__(256, 4) distill_candidates_kernel(DistillArgs a) {
   extern __shared__ __align__(16) uint8_t distill_smem[];

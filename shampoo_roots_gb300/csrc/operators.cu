@@ -123,11 +123,6 @@ int prepare(Handle* h) {
     OP_CK(cudaMalloc(&h->op_err, sizeof(unsigned int)));
     OP_CK(cudaMemset(h->op_err, 0, sizeof(unsigned int)));
     OP_CK(cudaDeviceSynchronize());
-    // The streaming kernels live on L1: no more of the SM's memory is shared than they ask for.
-    for (int t = 0; t < 2; ++t)
-      for (int i = 0; i < 5; ++i)
-        for (DistillKernel k : {distill_fused_kernels[t][i], distill_split_kernels[t][i]})
-          OP_CK(cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxL1));
     h->op_ready = true;
   }
   return PRECOND_OK;

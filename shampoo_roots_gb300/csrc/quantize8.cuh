@@ -13,6 +13,10 @@
 // The tile stays in registers as it is stored (32 registers of bf16) and is
 // unpacked where it is used, which leaves room for four blocks on an SM; bf16
 // maxima are taken on packed pairs.
+//
+// Measured (10007 x 6144 bf16): both ways 46.6 us, 79 % of the copy bandwidth,
+// by rows 33.3 us, 82 %; fp32 both ways 72.5 us, 75 %.  What is left is issue
+// slots: 16 conversions, shuffles and maxima for every 16 bytes moved.
 #pragma once
 
 #include "form8.cuh"

@@ -10,7 +10,16 @@
 // threads, 16 consecutive columns a vector, so that the row is read once; the
 // block keeps its columns of w (and of the dw sum) for all of its rows, and
 // loads the next row before it works on the present one.  The threads of a row
-// meet at one barrier a row.
+// meet at one barrier a row; those of a long row, in several blocks of a
+// cluster, at words of their shared memory.
+//
+// Measured (bf16 with residual, as a fraction of the copy bandwidth): norm of
+// 8192 x 6144 55.5 us, 94 %, of 3000 x 16384 58 us, 87 %; gradients of 16384 x
+// 4096 88.3 us, 90 %, of 3000 x 16384 74 us, 78 % (the join of each row).  Rows
+// that do not begin at sectors cost instructions, about as much again: 7000 x
+// 2001 28 us, 52 %, gradients 39 us, 42 %.  dw leaves in fp32 sums of a block's
+// rows, at most 4 an SM, which a second kernel adds in their order (16384 x
+// 4096: 304 sums, 5 MB, 6 us).
 #pragma once
 
 #include <cooperative_groups.h>
