@@ -17,6 +17,7 @@ typedef struct {
 enum { T_F32, T_BF16, T_E4M3, T_E8M0, T_U8, T_I32, T_I64, T_COUNT };
 static PyObject* dtypes[T_COUNT];
 static PyObject *s_shape, *s_stride, *s_data_ptr, *s_dtype, *s_get_device, *s_new_empty, *raw_stream;
+static PyObject *raw_alloc, *raw_delete, *current_device;   /* torch's allocator, NULL where it cannot be had so */
 enum { E_NORM, E_GRAD, E_GRAD_WS, E_QUANTIZE, E_GEMM, E_DISTILL, E_DISTILL_WS, E_COUNT };
 static void* entry[E_COUNT];
 
@@ -175,8 +176,14 @@ static int stream_of(PyObject* stream, PyObject* t, void** out) {
   Py_DECREF(s);
   return PyErr_Occurred() ? -1 : 0;
 }
-/* The workspace argument: None is memory of torch's allocator, a float32 vector like `like` (*own, to be released
- * after the call).  That belongs to the current stream, so another one needs a workspace of the caller's. */
+/* The workspace argument: None is memory of torch's allocator (*own, to be given back with give_back after the call):
+ * a piece of `like`'s device, or a float32 vector like it where the allocator cannot be called itself (a gradient of 45
+ * x 105 takes the host 11.6 us with the vector, 6.88 with the piece).  It belongs to the current stream, so another
+ * one needs a workspace of the caller's. */
+static void give_back(PyObject* own) {
+  if (own && PyLong_Check(own)) Py_XDECREF(PyObject_CallOneArg(raw_delete, own));
+  Py_XDECREF(own);
+}
 static int workspace_of(PyObject* given, PyObject* like, int64_t need, PyObject* stream, void* st, Tensor* o, PyObject** own) {
   *own = NULL;
   o->p = NULL;
@@ -195,6 +202,26 @@ static int workspace_of(PyObject* given, PyObject* like, int64_t need, PyObject*
     void* current;
     if (stream_of(Py_None, like, &current)) return -1;
     if (current != st) return bad(PyExc_ValueError, "give a workspace", "with a stream other than torch's current one");
+  }
+  if (raw_alloc) {
+    PyObject *its = PyObject_CallMethodNoArgs(like, s_get_device), *now = NULL;
+    if (!its) return -1;
+    const long device = PyLong_AsLong(its);
+    if (device >= 0) now = PyObject_CallNoArgs(current_device);
+    const int same = device < 0 ? 0 : now ? PyObject_RichCompareBool(now, its, Py_EQ) : -1;
+    Py_XDECREF(now);
+    Py_DECREF(its);
+    if (same < 0) return -1;
+    if (same) {
+      PyObject *bytes = PyLong_FromLongLong(need), *where = PyLong_FromVoidPtr(st);
+      if (bytes && where) *own = PyObject_CallFunctionObjArgs(raw_alloc, bytes, where, NULL);
+      Py_XDECREF(bytes);
+      Py_XDECREF(where);
+      if (!*own) return -1;
+      o->p = PyLong_AsVoidPtr(*own);
+      o->rows = need;
+      return 0;
+    }
   }
   PyObject* n = PyLong_FromLongLong((need + 3) / 4);
   if (!n) return -1;
@@ -258,8 +285,8 @@ static PyObject* rms_norm_grad(PyObject* self, PyObject* const* a, Py_ssize_t n)
     return NULL;
   const int code = ((fn)entry[E_GRAD])(h, dy.p, x.p, w.p, rs.p, dr.p, dt, wt, dy.rows, dy.cols, dy.ld, x.ld, dr.ld, dx.p, dx.ld,
                                        dw.p, ws.p, ws.rows, st);
-  Py_XDECREF(own);
-  return PyLong_FromLong(code);
+  give_back(own);
+  return PyErr_Occurred() ? NULL : PyLong_FromLong(code);
 }
 
 /* (h, x, q, scale, qt, scale_t, block, x_scale, stream) */
@@ -336,14 +363,18 @@ static PyObject* distill(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     return NULL;
   const int code = ((fn)entry[E_DISTILL])(h, z.p, dt, z.rows, z.cols, z.ld, ids.p, ids.dtype == dtypes[T_I32] ? 32 : 64, ids.ld, t.p,
                                           tt, t.ld, top, w.p, (float)tau, loss.p, dz.p, dz.ld, ws.p, ws.rows, st);
-  Py_XDECREF(own);
-  return PyLong_FromLong(code);
+  give_back(own);
+  return PyErr_Occurred() ? NULL : PyLong_FromLong(code);
 }
 
-/* set_up(dtypes, raw_stream, entries): what the calls need, once. */
+/* set_up(dtypes, raw_stream, entries, (raw_alloc, raw_delete, current_device) or None): what the calls need, once. */
 static PyObject* set_up(PyObject* self, PyObject* args) {
-  PyObject *types, *raw, *addresses;
-  if (!PyArg_ParseTuple(args, "O!OO!", &PyTuple_Type, &types, &raw, &PyTuple_Type, &addresses)) return NULL;
+  PyObject *types, *raw, *addresses, *allocator;
+  if (!PyArg_ParseTuple(args, "O!OO!O", &PyTuple_Type, &types, &raw, &PyTuple_Type, &addresses, &allocator)) return NULL;
+  if (allocator != Py_None && (!PyArg_ParseTuple(allocator, "OOO", &raw_alloc, &raw_delete, &current_device))) return NULL;
+  Py_XINCREF(raw_alloc);
+  Py_XINCREF(raw_delete);
+  Py_XINCREF(current_device);
   if (PyTuple_GET_SIZE(types) != T_COUNT || PyTuple_GET_SIZE(addresses) != E_COUNT) {
     PyErr_SetString(PyExc_ValueError, "wrong number of dtypes or entries");
     return NULL;

@@ -42,8 +42,16 @@ def _load_binding():
              torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else _current_stream,
              tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (
                  L.precond_rms_norm, L.precond_rms_norm_grad, L.precond_rms_norm_grad_workspace, L.precond_quantize8, L.precond_gemm8,
-                 L.precond_distill, L.precond_distill_workspace)))
+                 L.precond_distill, L.precond_distill_workspace)), _allocator())
     return m
+
+
+def _allocator():
+    """(allocate, delete, current device) of torch's caching allocator, what torch.cuda.caching_allocator_alloc calls;
+    None where this torch has them under other names."""
+    names = ("_cuda_cudaCachingAllocator_raw_alloc", "_cuda_cudaCachingAllocator_raw_delete", "_cuda_getDevice")
+    found = tuple(getattr(torch._C, n, None) for n in names)
+    return None if None in found else found
 
 
 def _current_stream(device: int) -> int:
