@@ -149,11 +149,12 @@ cudaError_t launch(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cuda
 // ------------------------------------------------------------------------- norm
 // Threads of a row, rows of a block and blocks of a row.  16 columns a thread, up
 // to 384 threads (a bf16 gradient: 512); then a norm of aligned rows has 32 up
-// to 512 threads (16384 columns: 58 us where a cluster of 4 took 74), and what
-// is still longer a cluster of 2, 4 or 8 blocks.  Longer rows (parts 0) take the
-// kernels that read a row twice.  Blocks of short rows hold several, for warps on each of
-// the SM's four parts (20244 x 1213: 4 rows of 3 warps 59 us, one row 84); up to 256
-// columns, where rows begin at sectors, a warp does.
+// to 512 threads (3000 x 16384 bf16: 58 us, in clusters of 4 61; without a
+// residual 38 and 52), and what is still longer a cluster of 2, 4 or 8 blocks.
+// Longer rows (parts 0) take the kernels that read a row twice.  Blocks of short
+// rows hold several, to have warps on each of the SM's four parts (norm of 20244
+// x 1213 bf16: 4 rows of 3 warps 59 us, one row 84); up to 256 columns, where
+// rows begin at sectors, a warp does.
 struct RowShape { int threads, rows, vectors, parts; };
 RowShape row_shape(int64_t cols, int dtype, bool grad, bool vec) {
   const int64_t one = grad && dtype == PRECOND_BF16 ? 512 : 384, n = (cols + 15) / 16;

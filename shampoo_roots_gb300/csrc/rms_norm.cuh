@@ -134,6 +134,10 @@ __device__ __forceinline__ float cluster_row_sum(float v, unsigned long long* sl
   if (lost) s = __uint_as_float(0x7FFFFFFFu);
   return warp_sum(s);
 }
+// No block leaves while another may still write to it: every one has the last row's words by then, unless a wait ran out.
+__device__ __forceinline__ void cluster_leave() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void zero_red(float* red, int n) {
   for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < n; i += blockDim.x * blockDim.y) red[i] = 0.f;
   __syncthreads();
@@ -267,6 +271,7 @@ __global__ void __launch_bounds__(NV == 2 || (sizeof(T) == 2 && !VEC) ? 512 : 38
   }
   if (a.q && rank == 0)
     for (; row < rblocks * 128; row += step) norm_pad(a, row, rblocks);
+  if (CLUSTER) cluster_leave();
 }
 
 // Rows too long for registers: one block a row, which is read again (from L2) after its norm is known.
@@ -406,6 +411,7 @@ __global__ void __launch_bounds__(sizeof(T) == 4 ? 384 : 512, 1) rms_grad_kernel
     store16<VEC>(reinterpret_cast<T*>(a.dx) + row * a.lddx, c, cols, o, xs);
     cols = next;
   }
+  if (CLUSTER) cluster_leave();
   if (blockDim.y > 1) {                  // the block's rows side by side: in their order, through shared memory
     extern __shared__ __align__(16) uint8_t row_scratch[];
     F16* side = reinterpret_cast<F16*>(row_scratch);
