@@ -403,6 +403,16 @@ __device__ __forceinline__ void distill_loss(const DistillArgs& a, const Distill
   if ((threadIdx.x & 31) == 0) a.loss[row] = teaches ? weight * (a.tau * a.tau) * l : 0.0f;
 }
 
+// A block may be written to by the others of its cluster once it has begun.  It says so first of all, and waits for the
+// others where it writes to them (or, writing nothing, before its next cluster barrier), with its loads in between.
+__device__ __forceinline__ void begun_arrive(int parts) {
+  if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void begun_wait(int parts) {
+  __syncwarp();
+  if (parts > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // The barrier of a row, in two halves: the streaming warps' sums are there and the candidates' logits have been read.
 // Without a cluster it is two named barriers of the block: the streaming warps wait for the candidates' warp at one,
 // it for them at the other, after its work in between.
@@ -601,6 +611,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS + (FUSED ? 32 : 0), 2) distill
   const int64_t row = blockIdx.x / parts;
   const DistillShared sh(distill_smem, a.top, parts * streaming);
   const float c = LOG2E / a.tau;
+  begun_arrive(parts);
   wait_for_previous();
   let_next_start();
   const float weight = a.weight ? a.weight[row] : 1.0f;
@@ -620,6 +631,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS + (FUSED ? 32 : 0), 2) distill
       x.load(z, sl, tid, threads);
       x.sums(z, sl, tid, threads, c, m, s);
       join_warp(m, s, c);
+      begun_wait(parts);
       if (lane < parts) *cluster.map_shared_rank(&sh.sums[part * streaming + warp], lane) = make_float2(m, s);
       if (FUSED || parts > 1) {
         row_arrive(parts, true);
@@ -631,6 +643,8 @@ __global__ void __launch_bounds__(DISTILL_THREADS + (FUSED ? 32 : 0), 2) distill
       shift = Shift(m, c);
       teaches = !FUSED || *sh.most != -INFINITY;
       if (!FUSED && part == 0 && tid == 0) a.stats[row] = make_float2(m, s);
+    } else {
+      begun_wait(parts);
     }
     if (a.dz) {
       x.store(z, dz, sl, tid, threads, teaches, shift, c, teaches ? weight * a.tau / s : 0.f);
@@ -644,6 +658,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS + (FUSED ? 32 : 0), 2) distill
     auto work = [&](auto cand) {
       cand.gather(a, sh, row, z, sl, part == 0);
       if (lane == 0) *sh.most = cand.most;
+      begun_wait(parts);
       row_arrive(parts, false);
       cand.teach(a, sh);
       const bool teaches = cand.most != -INFINITY;
@@ -661,8 +676,9 @@ __global__ void __launch_bounds__(DISTILL_THREADS + (FUSED ? 32 : 0), 2) distill
     if (a.top <= 128) work(FewCandidates<4>());
     else if (a.top <= DISTILL_FEW) work(FewCandidates<8>());
     else work(ManyCandidates());
-  } else if (part == 0 && lane == 0) {
-    a.loss[row] = 0.0f;
+  } else {
+    begun_wait(parts);
+    if (part == 0 && lane == 0) a.loss[row] = 0.0f;
   }
 }
 
