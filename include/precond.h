@@ -367,6 +367,8 @@ int64_t precond_rms_norm_grad_workspace(int64_t rows, int64_t cols);   /* -1: ba
  *             with x_scale: an activation kept in 8 bits is put in blocks of
  *             tokens this way; NULL otherwise).  Powers of two as scales make
  *             that exact but for values below a block's smallest e4m3 number.
+ *             Values count as fp32: those beyond its range, and all under the
+ *             byte 255, are not finite.
  *   block   : PRECOND_BLOCK_ROW or PRECOND_BLOCK_TILE
  */
 int precond_quantize8(precond_t h, const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx,

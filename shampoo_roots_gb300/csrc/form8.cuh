@@ -38,6 +38,7 @@ __device__ __forceinline__ unsigned q8_exponent(unsigned amax_bits) {
 }
 // 2^-(b - 127): b is at most 247 for a finite fp32 block, so this is a normal number.
 __device__ __forceinline__ float q8_inverse(unsigned b) { return __uint_as_float((254u - b) << 23); }
+// The byte 255, e8m0's NaN, gives infinity: no e4m3 value times it is finite.
 __device__ __forceinline__ float q8_value(unsigned b) { return b ? __uint_as_float(b << 23) : __uint_as_float(0x400000u); }
 
 // Four values to e4m3 bytes (nearest, ties to even; magnitudes up to 448; NaN stays NaN).
