@@ -26,10 +26,12 @@
 // gradient 4.1 us.
 //
 // With c = log2(e) / tau and m = max(z), q_v = 2^(z_v c - k) / S, S = sum 2^(z_v
-// c - k), k = m c: the exponent is one fma, and the rounding of k cancels.  Where
-// m c is so large that its rounding would move the exponent (beyond 10^6: a row
-// that is masked with the type's lowest value throughout) it is (z_v - m) c
-// instead; both are (z_v - b) c - k.
+// c - k), k = m c: the exponent is one fma, and the rounding of k cancels, as
+// sums over parts of a row, each with the k of its own maximum, are joined by
+// their difference in k as it was rounded.  (By m c instead, S was off by 4e-4
+// for logits around 10^5.)  Where m c is so large that its rounding would move
+// the exponent (beyond 10^6: a row that is masked with the type's lowest value
+// throughout) it is (z_v - m) c instead; both are (z_v - b) c - k.
 //
 // The candidates' logits are read before anything is written, so that dz may be
 // z itself, and their gradients are written last, those of one id added in the
@@ -80,6 +82,8 @@ struct Shift {
     k = far ? 0.f : m * c;
   }
   __device__ __forceinline__ float operator()(float z, float c) const { return fmaf(z - b, c, -k); }
+  // the exponent of the factor that takes a sum from the shift `o` to this one: -inf from -infinity, where the sum is 0
+  __device__ __forceinline__ float from(const Shift& o, float c) const { return fmaf(o.b - b, c, o.k - k); }
 };
 // (maximum m, sum S of 2^(z c - m c)) of the lanes, joined over the warp: the common maximum first, then one factor
 // a lane.  (A butterfly that joins pairs takes two factors and a shift at each of its five steps.)
@@ -87,7 +91,7 @@ __device__ __forceinline__ void join_warp(float& m, float& s, float c) {
   float M = m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
-  s = warp_sum(m == M ? s : s * ex2(Shift(M, c)(m, c)));   // equal maxima (-inf among them) need no factor
+  s = warp_sum(m == M ? s : s * ex2(Shift(M, c).from(Shift(m, c), c)));   // equal maxima (-inf among them) need no factor
   m = M;
 }
 
@@ -441,7 +445,8 @@ __device__ __forceinline__ void join_sums(const DistillShared& sh, int n, float&
   const Shift at(m, c);
   s = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) s += x[i].x == m ? x[i].y : x[i].y * ex2(at(x[i].x, c));
+  for (int i = 0; i < 4; ++i)
+    if (32 * i < n) s += x[i].x == m ? x[i].y : x[i].y * ex2(at.from(Shift(x[i].x, c), c));
   s = warp_sum(s);
 }
 
@@ -450,7 +455,7 @@ __device__ __forceinline__ void distill_take(float& m, float& s, float v, float 
   const float M = max_nan(m, v);
   const Shift at(M, c);
   if (M != m) {
-    s *= ex2(at(m, c));                 // 0 at the first finite value; NaN stays
+    s *= ex2(at.from(Shift(m, c), c));  // 0 at the first finite value; NaN stays
     m = M;
   }
   if (m != -INFINITY) s += ex2(at(v, c));
@@ -484,7 +489,7 @@ __device__ __forceinline__ void distill_take(float& m, float& s, float (&f)[Logi
   for (int i = 2; i < N; i += 2) M = max3_nan(M, f[i], f[i + 1]);
   const Shift at(M, c);
   if (M != m) {
-    s *= ex2(at(m, c));
+    s *= ex2(at.from(Shift(m, c), c));
     m = M;
   }
   if (m != -INFINITY) s += sum2(distill_sum<N>(0, f, at, c));
