@@ -528,10 +528,10 @@ struct Part {
     one = at >= 0 ? as_float(z[at]) : -INFINITY;
   }
   __device__ __forceinline__ void sums(const T* z, const Slice& sl, int tid, int threads, float c, float& m, float& s) {
-    m = one;
+    m = -INFINITY;
     s = 0.f;
     if constexpr (NV > 0) {
-      m = max_nan(m, V::template largest<NV>(w));
+      m = max_nan(one, V::template largest<NV>(w));
       if (m != -INFINITY) {
         const Shift mine(m, c);
         f2 e2 = f2_of(ex2(mine(one, c)), 0.f);
@@ -544,7 +544,7 @@ struct Part {
         s = sum2(e2);
       }
     } else {
-      if (m != -INFINITY) s = 1.f;
+      distill_take(m, s, one, c);       // +infinity and NaN make the sum NaN
       const uint4* zv = reinterpret_cast<const uint4*>(z + sl.body);
       for (int i0 = tid; i0 < sl.nvec; i0 += U * threads) {
         uint4 x[U];
