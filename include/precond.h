@@ -310,6 +310,8 @@ int precond_step_schedule(int p, double l0, double fold, int degree, int max_ste
  *    dependents: one may take its place on an SM while its predecessor in the
  *    stream ends, and touches no memory before that has completed.
  *  - Outputs may not overlap inputs or each other unless the call says so (EINVAL).
+ *    Column slices of one buffer that share no element do not overlap; other
+ *    matrices do where their spans, from the first element to the last, meet.
  *  - Results do not depend on timing: no sum's order changes between calls.
  *
  * 8-bit form of a rows x cols matrix: `q`, e4m3 bytes, 16-byte aligned, pitch a

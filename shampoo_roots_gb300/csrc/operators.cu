@@ -43,13 +43,20 @@ bool matrix8(const void* q, int64_t ld, const uint8_t* s, int64_t rows, int64_t 
 bool sector_rows(const void* p, int64_t ld, int dtype) {
   return !p || (aligned(p, 32) && ld * (int64_t)size_of(dtype) % 32 == 0);
 }
-struct Range { const char* lo; const char* hi; };
+struct Range { const char* lo; const char* hi; int64_t pitch, width; };      // rows of `width` bytes, `pitch` apart
+constexpr Range NOWHERE = {nullptr, nullptr, 0, 0};
 Range range(const void* p, int64_t rows, int64_t ld, int64_t cols, size_t size) {
   const char* b = reinterpret_cast<const char*>(p);
-  if (!p || rows <= 0 || cols <= 0) return {nullptr, nullptr};
-  return {b, b + ((rows - 1) * ld + cols) * (int64_t)size};
+  if (!p || rows <= 0 || cols <= 0) return NOWHERE;
+  return {b, b + ((rows - 1) * ld + cols) * (int64_t)size, ld * (int64_t)size, cols * (int64_t)size};
 }
-bool overlap(Range a, Range b) { return a.lo && b.lo && a.lo < b.hi && b.lo < a.hi; }
+// Where rows are equally far apart (column slices of one buffer), those of one may lie between the other's.
+bool overlap(const Range& a, const Range& b) {
+  if (!a.lo || !b.lo || a.lo >= b.hi || b.lo >= a.hi) return false;
+  if (a.pitch != b.pitch || a.pitch <= 0) return true;
+  const int64_t d = ((b.lo - a.lo) % a.pitch + a.pitch) % a.pitch;            // b's rows begin d bytes after a's
+  return d < a.width || d + b.width > a.pitch;
+}
 Range scale_range(const uint8_t* s, int64_t rows, int64_t cols) {
   return range(s, 1, 0, (int64_t)q8_groups(cols) * q8_row_blocks(rows) * 512, 1);
 }
@@ -295,7 +302,7 @@ int precond_rms_norm(precond_t ph, const void* x, const void* residual, const vo
   const Range in[3] = {range(x, rows, ldx, cols, sz), range(residual, rows, ldr, cols, sz),
                        range(weight, 1, 0, cols, size_of(weight_dtype))};
   const Range out[5] = {range(total, rows, ldt, cols, sz), range(y, rows, ldy, cols, sz), range(q, rows, ldq, cols, 1),
-                        q ? scale_range(scale, rows, cols) : Range{nullptr, nullptr}, range(rstd, 1, 0, rows, 4)};
+                        q ? scale_range(scale, rows, cols) : NOWHERE, range(rstd, 1, 0, rows, 4)};
   for (int i = 0; i < 5; ++i) {
     for (int j = 0; j < 3; ++j) {
       const bool same = i == 0 && ((j == 0 && total == x && ldt == ldx) || (j == 1 && total == residual && ldt == ldr));
@@ -397,9 +404,9 @@ int precond_quantize8(precond_t ph, const void* x, int dtype, int64_t rows, int6
   if ((q != nullptr) != (scale != nullptr) || (qt != nullptr) != (scale_t != nullptr) || (rows && cols && !q && !qt)) return PRECOND_EINVAL;
   if ((q && !matrix8(q, ldq, scale, rows, cols)) || (qt && !matrix8(qt, ldqt, scale_t, cols, rows))) return PRECOND_EINVAL;
   const Range in[2] = {range(x, rows, ldx, cols, size_of(dtype)),
-                       x_scale ? scale_range(x_scale, rows, cols) : Range{nullptr, nullptr}};
-  const Range out[4] = {range(q, rows, ldq, cols, 1), q ? scale_range(scale, rows, cols) : Range{nullptr, nullptr},
-                        range(qt, cols, ldqt, rows, 1), qt ? scale_range(scale_t, cols, rows) : Range{nullptr, nullptr}};
+                       x_scale ? scale_range(x_scale, rows, cols) : NOWHERE};
+  const Range out[4] = {range(q, rows, ldq, cols, 1), q ? scale_range(scale, rows, cols) : NOWHERE,
+                        range(qt, cols, ldqt, rows, 1), qt ? scale_range(scale_t, cols, rows) : NOWHERE};
   for (int i = 0; i < 4; ++i) {
     for (int j = 0; j < 2; ++j)
       if (overlap(out[i], in[j])) return PRECOND_EINVAL;
@@ -432,8 +439,8 @@ int precond_gemm8(precond_t ph, int64_t M, int64_t N, int64_t K, const void* A, 
   if (accumulate && c_dtype != PRECOND_F32) return PRECOND_EINVAL;
   if (!matrix8(A, lda, scale_a, M, K) || !matrix8(B, ldb, scale_b, N, K) || !matrix(C, M, N, ldc, c_dtype)) return PRECOND_EINVAL;
   const Range in[4] = {range(A, M, lda, K, 1), range(B, N, ldb, K, 1),
-                       M && K ? scale_range(scale_a, M, K) : Range{nullptr, nullptr},
-                       N && K ? scale_range(scale_b, N, K) : Range{nullptr, nullptr}};
+                       M && K ? scale_range(scale_a, M, K) : NOWHERE,
+                       N && K ? scale_range(scale_b, N, K) : NOWHERE};
   const Range out = range(C, M, ldc, N, size_of(c_dtype));
   for (const Range& r : in)
     if (overlap(out, r)) return PRECOND_EINVAL;
