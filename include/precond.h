@@ -407,6 +407,7 @@ int precond_gemm8_status(precond_t h, void* stream);
  *   teacher     : the candidates' logits, rows x top, PRECOND_F32 or PRECOND_BF16; -infinity gives p = 0
  *   weight      : rows floats (the upstream gradient and the row's mask), NULL for 1.  A row of weight 0
  *                 is not read: its loss and gradient are 0 whatever its logits hold.
+ *   temperature : 1e-18 .. 1e18
  *   loss        : rows floats
  *   workspace   : precond_distill_workspace bytes, 16-byte aligned, in use until the call's work has
  *                 completed; may be NULL where that is 0

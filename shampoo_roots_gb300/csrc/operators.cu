@@ -531,8 +531,8 @@ int precond_distill(precond_t ph, const void* logits, int dtype, int64_t rows, i
                     int64_t workspace_bytes, void* stream) {
   Handle* h = as_handle(ph);
   if (!h || !float_type(dtype) || !float_type(teacher_dtype) || !side(rows) || !side(vocab) || vocab < 1) return PRECOND_EINVAL;
-  if ((id_bits != 32 && id_bits != 64) || top < 1 || top > DISTILL_MAX_TOP || !(temperature > 0.f) || temperature > 3e38f)
-    return PRECOND_EINVAL;
+  if ((id_bits != 32 && id_bits != 64) || top < 1 || top > DISTILL_MAX_TOP || !(temperature >= 1e-18f && temperature <= 1e18f))
+    return PRECOND_EINVAL;               // temperature^2 and log2(e) / temperature are fp32 numbers
   const size_t sz = size_of(dtype);
   if (!matrix(logits, rows, vocab, ldz, dtype) || !matrix(teacher, rows, top, ldt, teacher_dtype) ||
       !matrix(loss, 1, rows, rows, PRECOND_F32) || (dlogits && !matrix(dlogits, rows, vocab, lddz, dtype)) ||
