@@ -79,7 +79,7 @@ struct Shift {
   __device__ __forceinline__ Shift(float m, float c) {
     const bool far = !(fabsf(m) * c <= 1e6f);
     b = far ? m : 0.f;
-    k = far ? 0.f : m * c;
+    k = far ? 0.f : __fmul_rn(m, c);    // rounded for good: contracted into an fma, it would differ from use to use
   }
   __device__ __forceinline__ float operator()(float z, float c) const { return fmaf(z - b, c, -k); }
   // the exponent of the factor that takes a sum from the shift `o` to this one: -inf from -infinity, where the sum is 0
