@@ -157,7 +157,8 @@ cudaError_t launch(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cuda
 // Threads of a row, rows of a block and blocks of a row.  16 columns a thread, up
 // to 384 threads (a bf16 gradient: 512); then a norm of aligned rows has 32 up
 // to 512 threads (3000 x 16384 bf16: 58 us, in clusters of 4 61; without a
-// residual 38 and 52), and what is still longer a cluster of 2, 4 or 8 blocks.
+// residual 38 and 52; fp32, which spills in this form, 113 and 122, without a
+// residual 68 and 87), and what is still longer a cluster of 2, 4 or 8 blocks.
 // Longer rows (parts 0) take the kernels that read a row twice.  Blocks of short
 // rows hold several, to have warps on each of the SM's four parts (norm of 20244
 // x 1213 bf16: 4 rows of 3 warps 59 us, one row 84); up to 256 columns, where
@@ -224,7 +225,9 @@ int distill_parts(int64_t rows, int64_t vocab, int dtype) {
   return parts;
 }
 // Whether the candidates have a kernel of their own: with many rows or blocks, one more launch costs less than warps
-// that wait for them (2000 x 131072 bf16, 8000 blocks: 187 us, together 228; 1000 x 32000 fp32, 2000 blocks: 49 and 46).
+// that wait for them.  (2000 x 131072 bf16 with 128 of them, 8000 blocks: 191 us, together 248; 1900 x 32000 fp32 with
+// 64, 86 and 89; 1000 x 32000 fp32, 2000 blocks: 51.8 and 51.3, bf16 32.6 and 27.9; 500 x 32000 fp32 32.0 and 28.3.  Many
+// candidates over a large vocabulary would part earlier: 800 x 131072, 3200 blocks: 87 and 103.)
 bool distill_split(int64_t rows, int64_t vocab, int dtype) {
   return rows >= 12 * PLAN_SMS || rows * distill_parts(rows, vocab, dtype) >= 24 * PLAN_SMS;
 }

@@ -15,11 +15,14 @@
 //
 // Measured (bf16 with residual, as a fraction of the copy bandwidth): norm of
 // 8192 x 6144 55.5 us, 94 %, of 3000 x 16384 58 us, 87 %; gradients of 16384 x
-// 4096 88.3 us, 90 %, of 3000 x 16384 74 us, 78 % (the join of each row).  Rows
-// that do not begin at sectors cost instructions, about as much again: 7000 x
-// 2001 28 us, 52 %, gradients 39 us, 42 %.  dw leaves in fp32 sums of a block's
-// rows, at most 4 an SM, which a second kernel adds in their order (16384 x
-// 4096: 304 sums, 5 MB, 6 us).
+// 4096 88.3 us, 90 %, of 3000 x 16384 74 us, 78 % (the join of each row); in fp32
+// norm of 8192 x 6144 100 us, 97 %, of 3000 x 16384 113 us, 83 %, gradients 188
+// us, 84 %, and 159 us, 73 %.  Rows that do not begin at sectors cost the exchange
+// of their elements through shared memory, and at 126 registers a thread an SM
+// holds too few warps to cover it (issue 56 % of the time): 7000 x 2001 27 us,
+// 53 %, gradients 39 us, 42 %.  dw leaves in fp32 sums of a block's rows, at most
+// 4 an SM, which a second kernel adds in their order (16384 x 4096: 304 sums, 5
+// MB, 6 us).
 #pragma once
 
 #include <cooperative_groups.h>
