@@ -128,7 +128,9 @@ def precond_gemm8_status(h, stream=None, raw: bool = False) -> int:
 
 
 def precond_distill_workspace(rows: int, vocab: int, top: int, dtype: torch.dtype, in_place: bool = False) -> int:
-    """Bytes of workspace of precond_distill."""
+    """Bytes of workspace of precond_distill for logits of float32 or bfloat16."""
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be float32 or bfloat16, got {dtype}")
     L = load()
     L.precond_distill_workspace.restype = ctypes.c_int64
     L.precond_distill_workspace.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int]
@@ -139,6 +141,7 @@ def precond_distill(h, logits, ids, teacher, loss, weight=None, temperature: flo
                     stream=None, raw: bool = False) -> int:
     """loss of every row against the teacher's top logits (``teacher`` at the vocabulary places ``ids``) and,
     with ``dlogits``, its gradient (in place if it is ``logits``).  Without a workspace one comes from torch's
-    allocator where the call needs it (on the current stream; give one together with another ``stream``)."""
+    allocator where the call needs it (on the current stream; give one together with another ``stream``).
+    ``temperature`` is 1e-18 to 1e18."""
     code = _b.distill(h, logits, ids, teacher, loss, weight, temperature, dlogits, workspace, stream)
     return code if raw or code == OK else _check(code, "precond_distill")
