@@ -422,6 +422,93 @@ int precond_distill(precond_t h, const void* logits, int dtype, int64_t rows, in
 /* Bytes; 0 where the call needs none (few rows).  in_place: dlogits is logits.  -1: bad arguments. */
 int64_t precond_distill_workspace(int64_t rows, int64_t vocab, int top, int dtype, int in_place);
 
+/* =========================================================================
+ * Operators of a policy's training step, with the conventions of the group above.
+ *
+ *   precond_layer_norm, precond_layer_norm_grad   the other norm, likewise with a residual and an 8-bit output
+ *   precond_policy                                the clipped policy loss of taken tokens, and dlogits
+ *   precond_grad_norm, precond_clip_grads         all gradients of a step, before precond_step takes them
+ */
+
+/*
+ * h = x + residual (rounded to dtype; h = x without a residual), mean over columns of h,
+ * rstd = 1 / sqrt(mean over columns of (h - mean)^2 + eps), y = (h - mean) rstd weight + bias.
+ *   bias       : cols, in weight_dtype, or NULL for 0
+ *   mean, rstd : rows floats each for precond_layer_norm_grad, or NULL
+ * The other arguments are those of precond_rms_norm.
+ */
+int precond_layer_norm(precond_t h, const void* x, const void* residual, const void* weight, const void* bias, int dtype,
+                       int weight_dtype, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr, float eps, void* total,
+                       int64_t ldt, void* y, int64_t ldy, void* q, int64_t ldq, uint8_t* scale, float* mean, float* rstd,
+                       void* stream);
+
+/*
+ * Gradients of precond_layer_norm (the rounding to 8 bits counts as the identity), with n = (x - mean) rstd, g = dy weight:
+ *   dx = dresidual + rstd (g - mean over columns of g - n mean over columns of (g n)),
+ *   dw = sum over rows of dy n,  db = sum over rows of dy.
+ *   x          : the forward pass's h;  mean, rstd: as it left them
+ *   dresidual  : the gradient that reaches h past the norm, or NULL (zero)
+ *   dx         : in dtype; may be dy, dresidual or x themselves where cols <= 32768
+ *   dw, db     : cols floats each; db may be NULL
+ *   workspace  : precond_layer_norm_grad_workspace(rows, cols) bytes, 16-byte aligned, in use until the call's work
+ *                has completed
+ */
+int precond_layer_norm_grad(precond_t h, const void* dy, const void* x, const void* weight, const float* mean,
+                            const float* rstd, const void* dresidual, int dtype, int weight_dtype, int64_t rows,
+                            int64_t cols, int64_t lddy, int64_t ldx, int64_t lddr, void* dx, int64_t lddx, float* dw,
+                            float* db, void* workspace, int64_t workspace_bytes, void* stream);
+int64_t precond_layer_norm_grad_workspace(int64_t rows, int64_t cols);   /* -1: bad sizes */
+
+/*
+ * Clipped policy loss of every row's taken token and, with `dlogits`, its gradient:
+ *   logp  = log softmax(logits / temperature)[id],  ratio = exp(logp - old_logp),
+ *   loss  = weight (-min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A) + kl (exp(d) - d - 1)),  d = ref_logp - logp,
+ *   dlogits = the gradient of loss with respect to logits; where the min takes the clipped term its part is 0.
+ *   logits    : rows x vocab, PRECOND_F32 or PRECOND_BF16; dlogits likewise, and may be logits itself
+ *   ids       : rows, int32 or int64 (`id_bits` 32 or 64): the taken token; outside 0 .. vocab - 1 there is none
+ *   advantage : rows floats (A), or NULL for the log probabilities alone; then old_logp, ref_logp, loss and dlogits
+ *               are NULL, and logp is not
+ *   old_logp  : rows floats, or NULL for a ratio of 1
+ *   ref_logp  : rows floats, or NULL where kl is 0
+ *   weight    : rows floats (the upstream gradient and the row's mask), NULL for 1.  A row of weight 0, or without a
+ *               taken token, is not read: its loss, logp and gradient are 0 whatever its inputs hold.
+ *   temperature : 1e-18 .. 1e18;  clip_low 0 .. 1, clip_high >= 0 (infinity: no bound above), kl >= 0
+ *   loss, logp  : rows floats; one may be NULL, and loss where dlogits is given
+ * A token that the logits give no probability has logp -infinity (and with kl an infinite loss, whose gradient is not
+ * finite).  Logits that are all -infinity, or one of NaN or +infinity, make the row's results NaN.
+ */
+int precond_policy(precond_t h, const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ldz, const void* ids,
+                   int id_bits, const float* advantage, const float* old_logp, const float* ref_logp, const float* weight,
+                   float temperature, float clip_low, float clip_high, float kl, float* loss, float* logp, void* dlogits,
+                   int64_t lddz, void* stream);
+
+/*
+ * A list of `count` (>= 0) tensors, host side only: tensors[i] is a device pointer to sizes[i] consecutive elements of
+ * dtypes[i] (PRECOND_F32 or PRECOND_BF16); no two may overlap (EINVAL).  The list holds the pointers, not the tensors:
+ * it serves as long as they do, for any handle of their device, and for several threads at once.
+ */
+typedef struct precond_list* precond_list_t;
+int precond_list_create(precond_list_t* out, int count, void* const tensors[], const int dtypes[], const int64_t sizes[]);
+int precond_list_destroy(precond_list_t list);            /* NULL is accepted; captured calls do not need the list */
+int64_t precond_list_workspace(precond_list_t list);      /* bytes for the calls below; -1: NULL */
+
+/*
+ * *norm = sqrt(sum of the squares of all elements of the list), for any finite elements; infinite beyond fp32's
+ * range, and not a number where an element is not.
+ *   workspace : precond_list_workspace bytes, 16-byte aligned, in use until the call's work has completed
+ */
+int precond_grad_norm(precond_t h, precond_list_t list, float* norm, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Scales every element by max_norm / norm, in place and rounded once, where norm > max_norm; otherwise, and where the norm is not
+ * finite, the tensors stay as they are.
+ *   max_norm  : >= 0; infinity clips nothing
+ *   norm      : device float.  given = 0: the list's norm (before scaling) is computed and left there.  given = 1: it
+ *               is read there (the norm of more than this list, of several ranks' lists); then workspace may be NULL
+ */
+int precond_clip_grads(precond_t h, precond_list_t list, float max_norm, float* norm, int given, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* precond_error_string(int code);
 

@@ -269,9 +269,10 @@ class Preconditioner:
             pass
 
 
-_OPERATORS = ("BLOCK_ROW", "BLOCK_TILE", "E4M3", "dequantize8", "empty8", "precond_distill", "precond_distill_workspace", "precond_gemm8",
-              "precond_gemm8_status", "precond_quantize8", "precond_rms_norm", "precond_rms_norm_grad",
-              "precond_rms_norm_grad_workspace", "scale_shape", "scales8")
+_OPERATORS = ("BLOCK_ROW", "BLOCK_TILE", "E4M3", "TensorList", "dequantize8", "empty8", "precond_clip_grads", "precond_distill",
+              "precond_distill_workspace", "precond_gemm8", "precond_gemm8_status", "precond_grad_norm", "precond_layer_norm",
+              "precond_layer_norm_grad", "precond_layer_norm_grad_workspace", "precond_policy", "precond_quantize8", "precond_rms_norm",
+              "precond_rms_norm_grad", "precond_rms_norm_grad_workspace", "scale_shape", "scales8")
 
 
 def __getattr__(name):

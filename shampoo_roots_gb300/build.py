@@ -11,7 +11,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libprecond.so")
 BINDING = os.path.join(HERE, "_binding.so")      # csrc/binding.c: the operators' argument marshalling
-SOURCES = ["precond.cu", "operators.cu"]
+SOURCES = ["precond.cu", "operators.cu", "training.cu"]
 FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC"]
 

@@ -10,7 +10,7 @@
 typedef struct {
   void* p;
   int64_t rows, cols, ld;   /* 2-D: rows, columns, row pitch; else rows = elements, cols = ld = 1 */
-  int dim, contiguous;
+  int dim, contiguous, dense;   /* dense: consecutive elements, in whatever order */
   PyObject* dtype;          /* borrowed: dtypes live as long as torch */
 } Tensor;
 
@@ -18,7 +18,8 @@ enum { T_F32, T_BF16, T_E4M3, T_E8M0, T_U8, T_I32, T_I64, T_COUNT };
 static PyObject* dtypes[T_COUNT];
 static PyObject *s_shape, *s_stride, *s_data_ptr, *s_dtype, *s_get_device, *s_new_empty, *raw_stream;
 static PyObject *raw_alloc, *raw_delete, *current_device;   /* torch's allocator, NULL where it cannot be had so */
-enum { E_NORM, E_GRAD, E_GRAD_WS, E_QUANTIZE, E_GEMM, E_DISTILL, E_DISTILL_WS, E_COUNT };
+enum { E_NORM, E_GRAD, E_GRAD_WS, E_QUANTIZE, E_GEMM, E_DISTILL, E_DISTILL_WS, E_LAYER, E_LAYER_GRAD, E_LAYER_GRAD_WS, E_POLICY,
+       E_LIST, E_LIST_END, E_LIST_WS, E_GRAD_NORM, E_CLIP, E_COUNT };
 static void* entry[E_COUNT];
 
 static int bad(PyObject* type, const char* what, const char* why) {
@@ -26,8 +27,8 @@ static int bad(PyObject* type, const char* what, const char* why) {
   return -1;
 }
 
-/* A tensor's attributes; returns -1 with an exception set. */
-static int get(PyObject* t, const char* what, Tensor* o) {
+/* A tensor's attributes; returns -1 with an exception set.  (`any`: of any strides, as a run of elements.) */
+static int get_as(PyObject* t, const char* what, Tensor* o, int any) {
   PyObject* v = PyObject_GetAttr(t, s_shape);
   if (!v) return -1;
   if (!PyTuple_Check(v)) {
@@ -54,6 +55,21 @@ static int get(PyObject* t, const char* what, Tensor* o) {
     want *= size[i];
   }
   Py_DECREF(v);
+  o->dense = o->contiguous;
+  if (!o->dense) {              /* the dimensions by their strides: each as long as those within it */
+    int used = 0;
+    int64_t inner = 1;
+    for (int found = 1; found;) {
+      found = 0;
+      for (int i = 0; i < o->dim; ++i)
+        if (!(used >> i & 1) && size[i] != 1 && step[i] == inner) {
+          used |= 1 << i;
+          inner *= size[i];
+          found = 1;
+        }
+    }
+    o->dense = inner == n;
+  }
   if (!(v = PyObject_CallMethodNoArgs(t, s_data_ptr))) return -1;
   o->p = PyLong_AsVoidPtr(v);
   Py_DECREF(v);
@@ -61,7 +77,7 @@ static int get(PyObject* t, const char* what, Tensor* o) {
   o->dtype = v;
   Py_DECREF(v);
   if (PyErr_Occurred()) return -1;
-  if (o->dim == 2) {
+  if (o->dim == 2 && !any) {
     o->rows = size[0];
     o->cols = size[1];
     if (step[1] != 1 && size[1] > 1) return bad(PyExc_ValueError, what, "must be 2-D with consecutive columns");
@@ -72,6 +88,7 @@ static int get(PyObject* t, const char* what, Tensor* o) {
   }
   return 0;
 }
+static int get(PyObject* t, const char* what, Tensor* o) { return get_as(t, what, o, 0); }
 
 static int matrix(PyObject* t, const char* what, Tensor* o) {
   if (get(t, what, o)) return -1;
@@ -237,6 +254,26 @@ static int workspace_of(PyObject* given, PyObject* like, int64_t need, PyObject*
   Py_CLEAR(*own);
   return -1;
 }
+/* All tensors among the n arguments are on one device. */
+static int one_device(PyObject* const* a, Py_ssize_t n) {
+  long device = 0;
+  int seen = 0;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    if (a[i] == Py_None || PyFloat_Check(a[i]) || PyLong_Check(a[i])) continue;
+    PyObject* d = PyObject_CallMethodNoArgs(a[i], s_get_device);
+    if (!d) return -1;
+    const long its = PyLong_AsLong(d);
+    Py_DECREF(d);
+    if (its == -1 && PyErr_Occurred()) return -1;
+    if (seen && its != device) {
+      PyErr_SetString(PyExc_ValueError, "the tensors must be on one device");
+      return -1;
+    }
+    device = its;
+    seen = 1;
+  }
+  return 0;
+}
 static int handle(PyObject* h, void** out) {
   *out = h == Py_None ? NULL : PyLong_AsVoidPtr(h);
   return PyErr_Occurred() ? -1 : 0;
@@ -367,6 +404,171 @@ static PyObject* distill(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return PyErr_Occurred() ? NULL : PyLong_FromLong(code);
 }
 
+/* (h, x, weight, eps, bias, residual, total, y, q, scale, mean, rstd, stream) */
+static PyObject* layer_norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  typedef int (*fn)(void*, const void*, const void*, const void*, const void*, int, int, int64_t, int64_t, int64_t, int64_t, float,
+                    void*, int64_t, void*, int64_t, void*, int64_t, uint8_t*, float*, float*, void*);
+  Tensor x, w, b, r, t, y, q, s, m, rs;
+  void *h, *st;
+  if (count(n, 13) || handle(a[0], &h) || matrix(a[1], "x", &x)) return NULL;
+  const int dt = float_type(&x, "x");
+  const double eps = PyFloat_AsDouble(a[3]);
+  if (dt < 0 || PyErr_Occurred() || vector(a[2], "weight", &w, x.cols, 0)) return NULL;
+  const int wt = float_type(&w, "weight");
+  if (wt < 0) return NULL;
+  b.p = NULL;
+  if (a[4] != Py_None) {
+    if (vector(a[4], "bias", &b, x.cols, 0)) return NULL;
+    if (b.dtype != w.dtype) {
+      PyErr_Format(PyExc_TypeError, "bias must be %S, as weight is, got %S", w.dtype, b.dtype);
+      return NULL;
+    }
+  }
+  if (maybe(a[5], "residual", &r, x.rows, x.cols, x.dtype) || maybe(a[6], "total", &t, x.rows, x.cols, x.dtype) ||
+      maybe(a[7], "y", &y, x.rows, x.cols, x.dtype) || maybe8(a[8], a[9], "q", &q, &s, x.rows, x.cols) ||
+      maybe_vector(a[10], "mean", &m, x.rows) || maybe_vector(a[11], "rstd", &rs, x.rows) || one_device(a + 1, 11) ||
+      stream_of(a[12], a[1], &st))
+    return NULL;
+  return PyLong_FromLong(((fn)entry[E_LAYER])(h, x.p, r.p, w.p, b.p, dt, wt, x.rows, x.cols, x.ld, r.ld, (float)eps, t.p, t.ld, y.p,
+                                              y.ld, q.p, q.ld, s.p, m.p, rs.p, st));
+}
+
+/* (h, dy, x, weight, mean, rstd, dx, dw, db, dresidual, workspace, stream) */
+static PyObject* layer_norm_grad(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  typedef int (*fn)(void*, const void*, const void*, const void*, const float*, const float*, const void*, int, int, int64_t, int64_t,
+                    int64_t, int64_t, int64_t, void*, int64_t, float*, float*, void*, int64_t, void*);
+  typedef int64_t (*need_fn)(int64_t, int64_t);
+  PyObject* own;
+  Tensor dy, x, w, m, rs, dx, dw, db, dr, ws;
+  void *h, *st;
+  if (count(n, 12) || handle(a[0], &h) || matrix(a[1], "dy", &dy)) return NULL;
+  const int dt = float_type(&dy, "dy");
+  if (dt < 0 || matrix_like(a[2], "x", &x, dy.rows, dy.cols, dy.dtype) || vector(a[3], "weight", &w, dy.cols, 0)) return NULL;
+  const int wt = float_type(&w, "weight");
+  if (wt < 0 || vector(a[4], "mean", &m, dy.rows, 1) || vector(a[5], "rstd", &rs, dy.rows, 1) ||
+      matrix_like(a[6], "dx", &dx, dy.rows, dy.cols, dy.dtype) || vector(a[7], "dw", &dw, dy.cols, 1) ||
+      maybe_vector(a[8], "db", &db, dy.cols) || maybe(a[9], "dresidual", &dr, dy.rows, dy.cols, dy.dtype) || one_device(a + 1, 10) ||
+      stream_of(a[11], a[1], &st) ||
+      workspace_of(a[10], a[7], a[10] == Py_None ? ((need_fn)entry[E_LAYER_GRAD_WS])(dy.rows, dy.cols) : 0, a[11], st, &ws, &own))
+    return NULL;
+  const int code = ((fn)entry[E_LAYER_GRAD])(h, dy.p, x.p, w.p, m.p, rs.p, dr.p, dt, wt, dy.rows, dy.cols, dy.ld, x.ld, dr.ld, dx.p,
+                                             dx.ld, dw.p, db.p, ws.p, ws.rows, st);
+  give_back(own);
+  return PyErr_Occurred() ? NULL : PyLong_FromLong(code);
+}
+
+/* (h, logits, ids, advantage, old_logp, ref_logp, weight, temperature, clip_low, clip_high, kl, loss, logp, dlogits, stream) */
+static PyObject* policy(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  typedef int (*fn)(void*, const void*, int, int64_t, int64_t, int64_t, const void*, int, const float*, const float*, const float*,
+                    const float*, float, float, float, float, float*, float*, void*, int64_t, void*);
+  Tensor z, ids, adv, old, ref, w, loss, logp, dz;
+  void *h, *st;
+  if (count(n, 15) || handle(a[0], &h) || matrix(a[1], "logits", &z)) return NULL;
+  const int dt = float_type(&z, "logits");
+  if (dt < 0 || vector(a[2], "ids", &ids, z.rows, 0)) return NULL;
+  if (ids.dtype != dtypes[T_I32] && ids.dtype != dtypes[T_I64]) {
+    PyErr_Format(PyExc_TypeError, "ids must be int32 or int64, got %S", ids.dtype);
+    return NULL;
+  }
+  double number[4];
+  for (int i = 0; i < 4; ++i) number[i] = PyFloat_AsDouble(a[7 + i]);
+  if (PyErr_Occurred() || maybe_vector(a[3], "advantage", &adv, z.rows) || maybe_vector(a[4], "old_logp", &old, z.rows) ||
+      maybe_vector(a[5], "ref_logp", &ref, z.rows) || maybe_vector(a[6], "weight", &w, z.rows) ||
+      maybe_vector(a[11], "loss", &loss, z.rows) || maybe_vector(a[12], "logp", &logp, z.rows) ||
+      maybe(a[13], "dlogits", &dz, z.rows, z.cols, z.dtype) || one_device(a + 1, 6) || one_device(a + 11, 3) || stream_of(a[14], a[1], &st))
+    return NULL;
+  return PyLong_FromLong(((fn)entry[E_POLICY])(h, z.p, dt, z.rows, z.cols, z.ld, ids.p, ids.dtype == dtypes[T_I32] ? 32 : 64, adv.p, old.p,
+                                               ref.p, w.p, (float)number[0], (float)number[1], (float)number[2], (float)number[3], loss.p,
+                                               logp.p, dz.p, dz.ld, st));
+}
+
+/* (tensors, a tuple) -> (code, the library's list in a capsule or None, its calls' workspace bytes) */
+#define LIST_NAME "precond_list"
+static void list_end(PyObject* capsule) {
+  typedef int (*fn)(void*);
+  ((fn)entry[E_LIST_END])(PyCapsule_GetPointer(capsule, LIST_NAME));
+}
+static PyObject* tensor_list(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  typedef int (*fn)(void**, int, void* const*, const int*, const int64_t*);
+  typedef int64_t (*need_fn)(void*);
+  if (count(n, 1)) return NULL;
+  if (!PyTuple_Check(a[0])) {
+    PyErr_SetString(PyExc_TypeError, "tensors must be a tuple");
+    return NULL;
+  }
+  const Py_ssize_t many = PyTuple_GET_SIZE(a[0]);
+  if (many > 1 << 24) {
+    PyErr_SetString(PyExc_ValueError, "too many tensors");
+    return NULL;
+  }
+  PyObject *out = NULL, *capsule = NULL;
+  void** p = PyMem_Malloc((many + 1) * sizeof(void*));
+  int* types = PyMem_Malloc((many + 1) * sizeof(int));
+  int64_t* sizes = PyMem_Malloc((many + 1) * sizeof(int64_t));
+  void* list = NULL;
+  if (!p || !types || !sizes) {
+    PyErr_NoMemory();
+    goto done;
+  }
+  for (Py_ssize_t i = 0; i < many; ++i) {
+    Tensor t;
+    if (get_as(PyTuple_GET_ITEM(a[0], i), "a tensor of the list", &t, 1)) goto done;
+    if (!t.dense) {
+      PyErr_Format(PyExc_ValueError, "tensor %zd of the list has gaps between its elements", i);
+      goto done;
+    }
+    if ((types[i] = float_type(&t, "a tensor of the list")) < 0) goto done;
+    p[i] = t.p;
+    sizes[i] = t.rows;
+  }
+  if (many && one_device(&PyTuple_GET_ITEM(a[0], 0), many)) goto done;
+  const int code = ((fn)entry[E_LIST])(&list, (int)many, p, types, sizes);
+  if (code == 0 && !(capsule = PyCapsule_New(list, LIST_NAME, list_end))) goto done;
+  out = capsule ? Py_BuildValue("(iNL)", code, capsule, (long long)((need_fn)entry[E_LIST_WS])(list)) : Py_BuildValue("(iOL)", code, Py_None, 0ll);
+done:
+  PyMem_Free(p);
+  PyMem_Free(types);
+  PyMem_Free(sizes);
+  return out;
+}
+
+/* (h, list, first tensor or None, norm, workspace, stream) and (h, list, first tensor or None, max_norm, norm, given,
+ * workspace, stream) */
+static int list_call(PyObject* list, PyObject* first, PyObject* norm, PyObject* workspace, PyObject* stream, int given, void** l, Tensor* o,
+                     void** st, Tensor* ws, PyObject** own) {
+  typedef int64_t (*need_fn)(void*);
+  *own = NULL;
+  if (!(*l = PyCapsule_GetPointer(list, LIST_NAME)) || get(norm, "norm", o)) return -1;
+  if (o->rows * o->cols != 1 || o->dtype != dtypes[T_F32]) return bad(PyExc_ValueError, "norm", "must be one torch.float32 number");
+  PyObject* both[2] = {norm, first};
+  if (one_device(both, 2) || stream_of(stream, norm, st)) return -1;
+  return workspace_of(workspace, norm, workspace == Py_None && !given ? ((need_fn)entry[E_LIST_WS])(*l) : 0, stream, *st, ws, own);
+}
+static PyObject* grad_norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  typedef int (*fn)(void*, void*, float*, void*, int64_t, void*);
+  PyObject* own;
+  Tensor norm, ws;
+  void *h, *st, *l;
+  if (count(n, 6) || handle(a[0], &h) || list_call(a[1], a[2], a[3], a[4], a[5], 0, &l, &norm, &st, &ws, &own)) return NULL;
+  const int code = ((fn)entry[E_GRAD_NORM])(h, l, norm.p, ws.p, ws.rows, st);
+  give_back(own);
+  return PyErr_Occurred() ? NULL : PyLong_FromLong(code);
+}
+static PyObject* clip_grads(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  typedef int (*fn)(void*, void*, float, float*, int, void*, int64_t, void*);
+  PyObject* own;
+  Tensor norm, ws;
+  void *h, *st, *l;
+  if (count(n, 8) || handle(a[0], &h)) return NULL;
+  const double most = PyFloat_AsDouble(a[3]);
+  if (PyErr_Occurred()) return NULL;
+  const int given = PyObject_IsTrue(a[5]);
+  if (given < 0 || list_call(a[1], a[2], a[4], a[6], a[7], given, &l, &norm, &st, &ws, &own)) return NULL;
+  const int code = ((fn)entry[E_CLIP])(h, l, (float)most, norm.p, given, ws.p, ws.rows, st);
+  give_back(own);
+  return PyErr_Occurred() ? NULL : PyLong_FromLong(code);
+}
+
 /* set_up(dtypes, raw_stream, entries, (raw_alloc, raw_delete, current_device) or None): what the calls need, once. */
 static PyObject* set_up(PyObject* self, PyObject* args) {
   PyObject *types, *raw, *addresses, *allocator;
@@ -397,6 +599,12 @@ static PyMethodDef methods[] = {
     {"quantize8", (PyCFunction)(void (*)(void))quantize8, METH_FASTCALL, NULL},
     {"gemm8", (PyCFunction)(void (*)(void))gemm8, METH_FASTCALL, NULL},
     {"distill", (PyCFunction)(void (*)(void))distill, METH_FASTCALL, NULL},
+    {"layer_norm", (PyCFunction)(void (*)(void))layer_norm, METH_FASTCALL, NULL},
+    {"layer_norm_grad", (PyCFunction)(void (*)(void))layer_norm_grad, METH_FASTCALL, NULL},
+    {"policy", (PyCFunction)(void (*)(void))policy, METH_FASTCALL, NULL},
+    {"tensor_list", (PyCFunction)(void (*)(void))tensor_list, METH_FASTCALL, NULL},
+    {"grad_norm", (PyCFunction)(void (*)(void))grad_norm, METH_FASTCALL, NULL},
+    {"clip_grads", (PyCFunction)(void (*)(void))clip_grads, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods};
 

@@ -432,13 +432,13 @@ __device__ __forceinline__ void row_wait(int parts, bool streams) {
   else asm volatile("bar.sync %0, %1;" ::"r"(streams ? 3 : 2), "r"((int)blockDim.x) : "memory");
 }
 // All warps' sums (up to 128: four a lane), joined in a fixed order; every thread gets them.
-__device__ __forceinline__ void join_sums(const DistillShared& sh, int n, float& m, float& s, float c) {
+__device__ __forceinline__ void join_sums(const float2* sums, int n, float& m, float& s, float c) {
   const int lane = threadIdx.x & 31;
   float2 x[4];
   m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[i] = lane + 32 * i < n ? sh.sums[lane + 32 * i] : make_float2(-INFINITY, 0.f);
+    x[i] = lane + 32 * i < n ? sums[lane + 32 * i] : make_float2(-INFINITY, 0.f);
     m = max_nan(m, x[i].x);
   }
 #pragma unroll
@@ -528,7 +528,9 @@ struct Part {
     }
     one = at >= 0 ? as_float(z[at]) : -INFINITY;
   }
-  __device__ __forceinline__ void sums(const T* z, const Slice& sl, int tid, int threads, float c, float& m, float& s) {
+  // `hide` sees each vector that is read here, NV = 0, before it counts
+  template <typename Hide>
+  __device__ __forceinline__ void sums(const T* z, const Slice& sl, int tid, int threads, float c, float& m, float& s, Hide hide) {
     m = -INFINITY;
     s = 0.f;
     if constexpr (NV > 0) {
@@ -555,6 +557,7 @@ struct Part {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           if (i0 + u * threads < sl.nvec) {
+            hide(i0 + u * threads, x[u]);
             float f[V::N];
             V::unpack(x[u], f);
             distill_take<T>(m, s, f, c);
@@ -635,7 +638,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS + (FUSED ? 32 : 0), 2) distill
     bool teaches = false;
     if (reads) {
       x.load(z, sl, tid, threads);
-      x.sums(z, sl, tid, threads, c, m, s);
+      x.sums(z, sl, tid, threads, c, m, s, [](int, uint4&) {});
       join_warp(m, s, c);
       begun_wait(parts);
       if (lane < parts) *cluster.map_shared_rank(&sh.sums[part * streaming + warp], lane) = make_float2(m, s);
@@ -645,7 +648,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS + (FUSED ? 32 : 0), 2) distill
       } else {
         __syncthreads();
       }
-      join_sums(sh, parts * streaming, m, s, c);
+      join_sums(sh.sums, parts * streaming, m, s, c);
       shift = Shift(m, c);
       teaches = !FUSED || *sh.most != -INFINITY;
       if (!FUSED && part == 0 && tid == 0) a.stats[row] = make_float2(m, s);
@@ -669,7 +672,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS + (FUSED ? 32 : 0), 2) distill
       cand.teach(a, sh);
       const bool teaches = cand.most != -INFINITY;
       row_wait(parts, false);
-      join_sums(sh, parts * streaming, m, s, c);
+      join_sums(sh.sums, parts * streaming, m, s, c);
       const Shift shift(m, c);
       if (part == 0) distill_loss(a, sh, cand, row, weight, c, shift, s, teaches);
       if (a.dz) {

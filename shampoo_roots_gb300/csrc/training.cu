@@ -1,0 +1,389 @@
+// Host side of the operators that train a policy (include/precond.h): layer norm
+// and its gradients, the clipped policy loss, the norm of a list of gradients and
+// their clipping.  Arguments are checked here, before anything is enqueued;
+// kernels go to the caller's stream and use no memory but the caller's.
+
+#include <cmath>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "clip.cuh"
+#include "host.h"
+#include "layer_norm.cuh"
+#include "policy.cuh"
+
+using namespace precond;
+
+namespace {
+
+constexpr int64_t LAYER_IN_PLACE = 32768;           // columns up to which every shape of row is read once
+
+// ------------------------------------------------------------------------- layer norm
+template <typename T, bool VEC>
+struct LayerKernels {
+  typedef void (*Norm)(LayerNormArgs);
+  typedef void (*Grad)(LayerGradArgs);
+  static Norm norm(const RowShape& s) {
+    if (s.parts == 0) return layer_norm_long_kernel<T, VEC>;
+    if (s.parts > 1) return layer_norm_kernel<T, 1, VEC, ROW_CLUSTER>;
+    if (VEC && s.vectors == 2) return layer_norm_kernel<T, 2, true, ROW_BLOCK>;
+    if (VEC && s.threads < 32) return layer_norm_kernel<T, 1, true, ROW_PART>;
+    return layer_norm_kernel<T, 1, VEC, ROW_BLOCK>;
+  }
+  static Grad grad(const RowShape& s) {
+    if (s.parts == 0) return layer_grad_long_kernel<T, VEC>;
+    if (s.parts > 1) return layer_grad_kernel<T, VEC, ROW_CLUSTER>;
+    if (VEC && s.threads < 32) return layer_grad_kernel<T, true, ROW_PART>;
+    return layer_grad_kernel<T, VEC, ROW_BLOCK>;
+  }
+  static size_t scratch(const RowShape& s) { return VEC ? 0 : (size_t)s.threads * s.rows / 32 * Scratch<T>::BYTES; }
+  // the table of w and b, the warps' exchange buffers
+  static size_t norm_bytes(const RowShape& s) { return (s.parts ? (size_t)s.threads * s.vectors * 128 : 0) + scratch(s); }
+  // the table of w, the warps' exchange buffers; then the dw and db sums of the rows side by side
+  static size_t grad_bytes(const RowShape& s) {
+    return std::max((s.parts ? (size_t)s.threads * 64 : 0) + scratch(s), s.rows > 1 ? (size_t)s.threads * s.rows * 128 : 0);
+  }
+  static cudaError_t attributes() {
+    // one of each kernel; the shapes decide how much they ask for
+    const RowShape one[] = {{384, 1, 1, 1}, {512, 1, 2, 1}, {16, 8, 1, 1}, {384, 1, 1, 2}};
+    for (const RowShape& s : one) {
+      cudaError_t e = cudaFuncSetAttribute(norm(s), cudaFuncAttributeMaxDynamicSharedMemorySize, 160 << 10);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(grad(s), cudaFuncAttributeMaxDynamicSharedMemorySize, 160 << 10);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+  }
+};
+int64_t layer_norm_blocks(const RowShape& s, int64_t rows, int dtype, bool vec, int sms, const int* clusters) {
+  return row_blocks_of(s, rows, s.vectors == 2 ? 512 : dtype == PRECOND_F32 ? 384 : vec ? 768 : 512, sms, clusters);
+}
+int64_t layer_grad_blocks(const RowShape& s, int64_t rows, int dtype, int sms, const int* clusters) {
+  return row_blocks_of(s, rows, dtype == PRECOND_F32 ? 384 : 512, sms, clusters);
+}
+template <typename T, bool VEC>
+cudaError_t launch_layer_norm(const LayerNormArgs& a, const RowShape& s, unsigned grid, cudaStream_t st) {
+  typedef LayerKernels<T, VEC> K;
+  return launch(K::norm(s), dim3(grid * std::max(1, s.parts)), dim3(s.threads, s.rows), K::norm_bytes(s), st, std::max(1, s.parts), a);
+}
+template <typename T, bool VEC>
+cudaError_t launch_layer_grad(const LayerGradArgs& a, const RowShape& s, unsigned grid, cudaStream_t st) {
+  typedef LayerKernels<T, VEC> K;
+  return launch(K::grad(s), dim3(grid * std::max(1, s.parts)), dim3(s.threads, s.rows), K::grad_bytes(s), st, std::max(1, s.parts), a);
+}
+
+// ------------------------------------------------------------------------- policy loss
+typedef void (*PolicyKernel)(PolicyArgs);
+const PolicyKernel policy_kernels[2][5] = {
+    {policy_kernel<float, 0>, policy_kernel<float, 1>, policy_kernel<float, 2>, policy_kernel<float, 4>, policy_kernel<float, 8>},
+    {policy_kernel<__nv_bfloat16, 0>, policy_kernel<__nv_bfloat16, 1>, policy_kernel<__nv_bfloat16, 2>, policy_kernel<__nv_bfloat16, 4>,
+     policy_kernel<__nv_bfloat16, 8>}};
+
+// ------------------------------------------------------------------------- lists of tensors
+constexpr int CLIP_FEW = 32, CLIP_SOME = 224, CLIP_MANY = 1400;    // tensors of a launch: 0.7, 4.5 and 28 KB of parameters
+constexpr int CLIP_BLOCKS = 2 * PLAN_SMS;
+
+struct List {
+  std::vector<ClipTensor> tensors;                   // without the empty ones
+  std::vector<Range> ranges;                         // of those, by address
+  int64_t launches() const { return std::max<int64_t>(1, ((int64_t)tensors.size() + CLIP_MANY - 1) / CLIP_MANY); }
+  int64_t bytes() const { return launches() * CLIP_BLOCKS * 8; }
+  bool meets(const Range& r) const {
+    if (!r.lo) return false;
+    auto at = std::lower_bound(ranges.begin(), ranges.end(), r, [](const Range& a, const Range& b) { return a.hi <= b.lo; });
+    return at != ranges.end() && at->lo < r.hi;
+  }
+};
+
+template <int MAX>
+int64_t fill_table(const List& l, size_t from, ClipTable<MAX>& t) {
+  t.count = (int)std::min<size_t>(MAX, l.tensors.size() - from);
+  uint32_t pieces = 0;
+  for (int i = 0; i < t.count; ++i) {
+    t.tensor[i] = l.tensors[from + i];
+    t.first[i] = pieces;
+    pieces += (uint32_t)ClipView(t.tensor[i]).pieces();
+  }
+  t.first[t.count] = pieces;
+  return pieces;
+}
+// The sums of squares of a list, a launch for up to CLIP_MANY tensors; *sums: how many.
+template <int MAX>
+int launch_squares(Handle* h, const List& l, double* partial, int* sums, cudaStream_t st) {
+  ClipTable<MAX> t;
+  *sums = 0;
+  for (size_t from = 0; from < l.tensors.size(); from += MAX) {
+    const int grid = (int)std::min<int64_t>(fill_table(l, from, t), std::min(CLIP_BLOCKS, 2 * h->num_sms));
+    OP_CK(launch(clip_norm_kernel<MAX>, dim3(grid), dim3(CLIP_THREADS), 0, st, 1, t, partial + *sums));
+    ++h->launches;
+    *sums += grid;
+  }
+  return PRECOND_OK;
+}
+template <int MAX>
+int launch_scale(Handle* h, const List& l, const double* partial, int sums, float max_norm, float* norm, cudaStream_t st) {
+  ClipTable<MAX> t;
+  for (size_t from = 0; from < l.tensors.size(); from += MAX) {
+    const int grid = (int)std::min<int64_t>(fill_table(l, from, t), std::min(CLIP_BLOCKS, 2 * h->num_sms));
+    // the first launch leaves the norm, the others (and a caller's norm) find it
+    OP_CK(launch(clip_scale_kernel<MAX>, dim3(grid), dim3(CLIP_THREADS), 0, st, 1, t, partial, from ? 0 : sums, max_norm, norm));
+    ++h->launches;
+  }
+  return PRECOND_OK;
+}
+int squares(Handle* h, const List& l, double* partial, int* sums, cudaStream_t st) {
+  const size_t n = l.tensors.size();
+  return n <= CLIP_FEW ? launch_squares<CLIP_FEW>(h, l, partial, sums, st)
+         : n <= CLIP_SOME ? launch_squares<CLIP_SOME>(h, l, partial, sums, st) : launch_squares<CLIP_MANY>(h, l, partial, sums, st);
+}
+int scale(Handle* h, const List& l, const double* partial, int sums, float max_norm, float* norm, cudaStream_t st) {
+  const size_t n = l.tensors.size();
+  return n <= CLIP_FEW ? launch_scale<CLIP_FEW>(h, l, partial, sums, max_norm, norm, st)
+         : n <= CLIP_SOME ? launch_scale<CLIP_SOME>(h, l, partial, sums, max_norm, norm, st)
+                          : launch_scale<CLIP_MANY>(h, l, partial, sums, max_norm, norm, st);
+}
+int total(Handle* h, const double* partial, int sums, float* norm, cudaStream_t st) {
+  OP_CK(launch(clip_total_kernel<0>, dim3(1), dim3(CLIP_THREADS), 0, st, 1, partial, sums, norm));
+  ++h->launches;
+  return PRECOND_OK;
+}
+const List* as_list(precond_list_t l) { return reinterpret_cast<const List*>(l); }
+
+// What both calls on a list ask of their arguments.
+bool list_arguments(const Handle* h, const List* l, const float* norm, const void* workspace, int64_t workspace_bytes, int64_t need) {
+  if (!h || !l || !norm || !aligned(norm, 4)) return false;
+  if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return false;
+  const Range n = range(norm, 1, 0, 1, 4), w = need > 0 ? range(workspace, 1, 0, need, 1) : NOWHERE;
+  return !l->meets(n) && !l->meets(w) && !overlap(n, w);
+}
+
+}  // namespace
+
+cudaError_t precond::training_attributes() {
+  cudaError_t e = LayerKernels<float, true>::attributes();
+  if (e == cudaSuccess) e = LayerKernels<float, false>::attributes();
+  if (e == cudaSuccess) e = LayerKernels<__nv_bfloat16, true>::attributes();
+  if (e == cudaSuccess) e = LayerKernels<__nv_bfloat16, false>::attributes();
+  return e;
+}
+
+extern "C" {
+
+int precond_layer_norm(precond_t ph, const void* x, const void* residual, const void* weight, const void* bias, int dtype,
+                       int weight_dtype, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr, float eps, void* total, int64_t ldt,
+                       void* y, int64_t ldy, void* q, int64_t ldq, uint8_t* scale, float* mean, float* rstd, void* stream) {
+  Handle* h = as_handle(ph);
+  if (!h || !float_type(dtype) || !float_type(weight_dtype) || !side(rows) || !side(cols) || !(eps > 0.f)) return PRECOND_EINVAL;
+  const size_t sz = size_of(dtype), wz = size_of(weight_dtype);
+  if (!matrix(x, rows, cols, ldx, dtype) || !matrix(weight, 1, cols, cols, weight_dtype) || !aligned(mean, 4) || !aligned(rstd, 4) ||
+      (bias && !aligned(bias, wz)))
+    return PRECOND_EINVAL;
+  if ((residual != nullptr) != (total != nullptr)) return PRECOND_EINVAL;
+  if (residual && (!matrix(residual, rows, cols, ldr, dtype) || !matrix(total, rows, cols, ldt, dtype))) return PRECOND_EINVAL;
+  if (y && !matrix(y, rows, cols, ldy, dtype)) return PRECOND_EINVAL;
+  if ((q != nullptr) != (scale != nullptr) || (q && !matrix8(q, ldq, scale, rows, cols))) return PRECOND_EINVAL;
+  if (rows && cols && !total && !y && !q && !mean && !rstd) return PRECOND_EINVAL;
+  // outputs may not overlap anything, but for `total` over x or residual, element for element
+  const Range in[4] = {range(x, rows, ldx, cols, sz), range(residual, rows, ldr, cols, sz), range(weight, 1, 0, cols, wz),
+                       range(bias, 1, 0, cols, wz)};
+  const Range out[6] = {range(total, rows, ldt, cols, sz), range(y, rows, ldy, cols, sz), range(q, rows, ldq, cols, 1),
+                        q ? scale_range(scale, rows, cols) : NOWHERE, range(mean, 1, 0, rows, 4), range(rstd, 1, 0, rows, 4)};
+  for (int i = 0; i < 6; ++i) {
+    for (int j = 0; j < 4; ++j) {
+      const bool same = i == 0 && ((j == 0 && total == x && ldt == ldx) || (j == 1 && total == residual && ldt == ldr));
+      if (!same && overlap(out[i], in[j])) return PRECOND_EINVAL;
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return PRECOND_EINVAL;
+  }
+  if (h->device < 0) return PRECOND_ENODEV;
+  if (rows == 0 || cols == 0) return PRECOND_OK;
+  int rc = prepare(h);
+  if (rc) return rc;
+  LayerNormArgs a = {x, residual, weight, bias, total, y, (uint8_t*)q, scale, mean, rstd, ldx, ldr, ldt, ldy, ldq, (int)rows, (int)cols,
+                     eps, weight_dtype == PRECOND_BF16};
+  const bool vec = sector_rows(x, ldx, dtype) && sector_rows(residual, ldr, dtype) && sector_rows(total, ldt, dtype) &&
+                   sector_rows(y, ldy, dtype);
+  const RowShape s = row_shape(cols, dtype, false, vec);
+  const unsigned grid = (unsigned)layer_norm_blocks(s, q ? q8_row_blocks(rows) * 128 : rows, dtype, vec, h->num_sms, h->clusters);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == PRECOND_BF16)
+    OP_CK((vec ? launch_layer_norm<__nv_bfloat16, true>(a, s, grid, st) : launch_layer_norm<__nv_bfloat16, false>(a, s, grid, st)));
+  else
+    OP_CK((vec ? launch_layer_norm<float, true>(a, s, grid, st) : launch_layer_norm<float, false>(a, s, grid, st)));
+  ++h->launches;
+  return PRECOND_OK;
+}
+
+int64_t precond_layer_norm_grad_workspace(int64_t rows, int64_t cols) {
+  if (!side(rows) || !side(cols)) return -1;
+  if (rows == 0 || cols == 0) return 0;
+  // of either type; rows in parts of a warp, and clusters that do not fit, only make fewer
+  int64_t blocks = 0;
+  for (const int dtype : {PRECOND_BF16, PRECOND_F32})
+    blocks = std::max(blocks, layer_grad_blocks(row_shape(cols, dtype, true, false), rows, dtype, PLAN_SMS, PLAN_CLUSTERS));
+  return blocks * cols * 8;
+}
+
+int precond_layer_norm_grad(precond_t ph, const void* dy, const void* x, const void* weight, const float* mean, const float* rstd,
+                            const void* dresidual, int dtype, int weight_dtype, int64_t rows, int64_t cols, int64_t lddy, int64_t ldx,
+                            int64_t lddr, void* dx, int64_t lddx, float* dw, float* db, void* workspace, int64_t workspace_bytes,
+                            void* stream) {
+  Handle* h = as_handle(ph);
+  if (!h || !float_type(dtype) || !float_type(weight_dtype) || !side(rows) || !side(cols)) return PRECOND_EINVAL;
+  const size_t sz = size_of(dtype);
+  if (!matrix(dy, rows, cols, lddy, dtype) || !matrix(x, rows, cols, ldx, dtype) || !matrix(dx, rows, cols, lddx, dtype) ||
+      !matrix(weight, 1, cols, cols, weight_dtype) || !matrix(mean, 1, rows, rows, PRECOND_F32) ||
+      !matrix(rstd, 1, rows, rows, PRECOND_F32) || !matrix(dw, 1, cols, cols, PRECOND_F32) || !aligned(db, 4) ||
+      (dresidual && !matrix(dresidual, rows, cols, lddr, dtype)))
+    return PRECOND_EINVAL;
+  const int64_t need = precond_layer_norm_grad_workspace(rows, cols);
+  if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need)) return PRECOND_EINVAL;
+  const Range in[6] = {range(dy, rows, lddy, cols, sz), range(dresidual, rows, lddr, cols, sz), range(x, rows, ldx, cols, sz),
+                       range(weight, 1, 0, cols, size_of(weight_dtype)), range(mean, 1, 0, rows, 4), range(rstd, 1, 0, rows, 4)};
+  const Range out[4] = {range(dx, rows, lddx, cols, sz), range(dw, 1, 0, cols, 4), range(db, 1, 0, cols, 4), range(workspace, 1, 0, need, 1)};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 6; ++j) {
+      // dx may lie over dy, dresidual or x, element for element, where a row is surely read once
+      const bool same = i == 0 && cols <= LAYER_IN_PLACE &&
+                        ((j == 0 && dx == dy && lddx == lddy) || (j == 1 && dx == dresidual && lddx == lddr) ||
+                         (j == 2 && dx == x && lddx == ldx));
+      if (!same && overlap(out[i], in[j])) return PRECOND_EINVAL;
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return PRECOND_EINVAL;
+  }
+  if (h->device < 0) return PRECOND_ENODEV;
+  if (cols == 0) return PRECOND_OK;
+  int rc = prepare(h);
+  if (rc) return rc;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (rows == 0) {
+    OP_CK(cudaMemsetAsync(dw, 0, cols * 4, st));
+    if (db) OP_CK(cudaMemsetAsync(db, 0, cols * 4, st));
+    return PRECOND_OK;
+  }
+  LayerGradArgs a = {dy, x, dresidual, weight, mean, rstd, dx, (float*)workspace, lddy, ldx, lddr, lddx, (int)rows, (int)cols,
+                     weight_dtype == PRECOND_BF16};
+  const bool vec = sector_rows(dy, lddy, dtype) && sector_rows(x, ldx, dtype) && sector_rows(dresidual, lddr, dtype) &&
+                   sector_rows(dx, lddx, dtype);
+  const RowShape s = row_shape(cols, dtype, true, vec);
+  const unsigned grid = (unsigned)layer_grad_blocks(s, rows, dtype, std::min(h->num_sms, PLAN_SMS), h->clusters);
+  if (dtype == PRECOND_BF16)
+    OP_CK((vec ? launch_layer_grad<__nv_bfloat16, true>(a, s, grid, st) : launch_layer_grad<__nv_bfloat16, false>(a, s, grid, st)));
+  else
+    OP_CK((vec ? launch_layer_grad<float, true>(a, s, grid, st) : launch_layer_grad<float, false>(a, s, grid, st)));
+  OP_CK(launch(layer_dw_kernel<0>, dim3((unsigned)((2 * cols + 31) / 32)), dim3(32, 32), 0, st, 1, (const float*)workspace, (int)grid,
+               cols, dw, db));
+  h->launches += 2;
+  return PRECOND_OK;
+}
+
+int precond_policy(precond_t ph, const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ldz, const void* ids, int id_bits,
+                   const float* advantage, const float* old_logp, const float* ref_logp, const float* weight, float temperature,
+                   float clip_low, float clip_high, float kl, float* loss, float* logp, void* dlogits, int64_t lddz, void* stream) {
+  Handle* h = as_handle(ph);
+  if (!h || !float_type(dtype) || !side(rows) || !side(vocab) || vocab < 1 || rows > (int64_t)INT32_MAX / 8) return PRECOND_EINVAL;
+  if ((id_bits != 32 && id_bits != 64) || !(temperature >= 1e-18f && temperature <= 1e18f)) return PRECOND_EINVAL;
+  if (!(clip_low >= 0.f && clip_low <= 1.f) || !(clip_high >= 0.f) || !(kl >= 0.f && kl < INFINITY)) return PRECOND_EINVAL;
+  const size_t sz = size_of(dtype);
+  if (!matrix(logits, rows, vocab, ldz, dtype) || (dlogits && !matrix(dlogits, rows, vocab, lddz, dtype)) ||
+      (rows && (!ids || !aligned(ids, id_bits / 8))))
+    return PRECOND_EINVAL;
+  for (const void* p : {(const void*)advantage, (const void*)old_logp, (const void*)ref_logp, (const void*)weight, (const void*)loss,
+                        (const void*)logp})
+    if (!aligned(p, 4)) return PRECOND_EINVAL;
+  // without an advantage there is no loss, only the log probabilities
+  if (rows && ((advantage ? !loss && !dlogits : loss || dlogits || old_logp || ref_logp || !logp) || (kl != 0.f && !ref_logp && advantage)))
+    return PRECOND_EINVAL;
+  const Range in[6] = {range(logits, rows, ldz, vocab, sz), range(ids, 1, 0, rows, id_bits / 8), range(advantage, 1, 0, rows, 4),
+                       range(old_logp, 1, 0, rows, 4), range(ref_logp, 1, 0, rows, 4), range(weight, 1, 0, rows, 4)};
+  const Range out[3] = {range(dlogits, rows, lddz, vocab, sz), range(loss, 1, 0, rows, 4), range(logp, 1, 0, rows, 4)};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 6; ++j) {
+      const bool same = i == 0 && j == 0 && dlogits == logits && lddz == ldz;
+      if (!same && overlap(out[i], in[j])) return PRECOND_EINVAL;
+    }
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return PRECOND_EINVAL;
+  }
+  if (h->device < 0) return PRECOND_ENODEV;
+  if (rows == 0) return PRECOND_OK;
+  int rc = prepare(h);
+  if (rc) return rc;
+  const PolicyArgs a = {logits, ldz, ids, id_bits == 64, advantage, old_logp, kl != 0.f ? ref_logp : nullptr, weight, loss, logp, dlogits,
+                        lddz, rows, vocab, temperature, clip_low, clip_high, kl};
+  const LogitShape s = logit_shape(rows, vocab, dtype);
+  OP_CK(launch(policy_kernels[dtype == PRECOND_BF16][s.kernel], dim3((unsigned)(rows * s.parts)), dim3(s.threads), 0, (cudaStream_t)stream,
+               s.parts, a));
+  ++h->launches;
+  return PRECOND_OK;
+}
+
+int precond_list_create(precond_list_t* out, int count, void* const tensors[], const int dtypes[], const int64_t sizes[]) {
+  if (!out || count < 0 || (count && (!tensors || !dtypes || !sizes))) return PRECOND_EINVAL;
+  *out = nullptr;
+  try {
+    List l;
+    l.tensors.reserve(count);
+    l.ranges.reserve(count);
+    int64_t pieces = 0;
+    for (int i = 0; i < count; ++i) {
+      if (!float_type(dtypes[i]) || sizes[i] < 0 || sizes[i] > (int64_t)1 << 44) return PRECOND_EINVAL;
+      if (sizes[i] == 0) continue;
+      const size_t sz = size_of(dtypes[i]);
+      if (!tensors[i] || !aligned(tensors[i], sz)) return PRECOND_EINVAL;
+      l.tensors.push_back({tensors[i], dtypes[i] == PRECOND_BF16 ? -sizes[i] : sizes[i]});
+      l.ranges.push_back(range(tensors[i], 1, 0, sizes[i], sz));
+      pieces += ClipView(l.tensors.back()).pieces();
+    }
+    if (pieces > INT32_MAX) return PRECOND_EINVAL;
+    std::sort(l.ranges.begin(), l.ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    for (size_t i = 1; i < l.ranges.size(); ++i)
+      if (l.ranges[i].lo < l.ranges[i - 1].hi) return PRECOND_EINVAL;     // one tensor over another would be scaled twice
+    *out = reinterpret_cast<precond_list_t>(new List(std::move(l)));
+  } catch (const std::bad_alloc&) {
+    return PRECOND_ENOMEM;
+  }
+  return PRECOND_OK;
+}
+
+int precond_list_destroy(precond_list_t l) {
+  delete reinterpret_cast<List*>(l);
+  return PRECOND_OK;
+}
+
+int64_t precond_list_workspace(precond_list_t list) {
+  const List* l = as_list(list);
+  return l ? l->bytes() : -1;
+}
+
+int precond_grad_norm(precond_t ph, precond_list_t list, float* norm, void* workspace, int64_t workspace_bytes, void* stream) {
+  Handle* h = as_handle(ph);
+  const List* l = as_list(list);
+  if (!list_arguments(h, l, norm, workspace, workspace_bytes, l ? l->bytes() : 0)) return PRECOND_EINVAL;
+  if (h->device < 0) return PRECOND_ENODEV;
+  int rc = prepare(h), sums = 0;
+  if (rc) return rc;
+  cudaStream_t st = (cudaStream_t)stream;
+  double* partial = reinterpret_cast<double*>(workspace);
+  if ((rc = squares(h, *l, partial, &sums, st))) return rc;
+  return ::total(h, partial, sums, norm, st);
+}
+
+int precond_clip_grads(precond_t ph, precond_list_t list, float max_norm, float* norm, int given, void* workspace,
+                       int64_t workspace_bytes, void* stream) {
+  Handle* h = as_handle(ph);
+  const List* l = as_list(list);
+  if (!(max_norm >= 0.f) || !list_arguments(h, l, norm, workspace, workspace_bytes, l && !given ? l->bytes() : 0)) return PRECOND_EINVAL;
+  if (h->device < 0) return PRECOND_ENODEV;
+  int rc = prepare(h), sums = 0;
+  if (rc) return rc;
+  cudaStream_t st = (cudaStream_t)stream;
+  double* partial = reinterpret_cast<double*>(workspace);
+  if (!given && (rc = squares(h, *l, partial, &sums, st))) return rc;
+  if (!given && l->tensors.empty()) return ::total(h, partial, 0, norm, st);
+  return scale(h, *l, partial, sums, max_norm, norm, st);
+}
+
+}  // extern "C"

@@ -1,6 +1,7 @@
-"""Binding of the training-step operators of include/precond.h: the RMS norm
-with an 8-bit output and its gradients, the 8-bit form, the product of two 8-bit
-matrices and the distillation loss.
+"""Binding of the training-step operators of include/precond.h: the RMS norm and
+the layer norm with an 8-bit output and their gradients, the 8-bit form, the product
+of two 8-bit matrices, the distillation and the policy loss, and the norm and
+clipping of a list of gradients.
 
 As for the rest of the binding, torch tensors go where the C ABI takes device
 pointers, outputs are the caller's, and the checks of sizes, alignment and
@@ -36,13 +37,17 @@ def _load_binding():
     L = load()
     L.precond_rms_norm_grad_workspace.argtypes = [ctypes.c_int64, ctypes.c_int64]
     L.precond_rms_norm_grad_workspace.restype = ctypes.c_int64
+    L.precond_layer_norm_grad_workspace.argtypes = [ctypes.c_int64, ctypes.c_int64]
+    L.precond_layer_norm_grad_workspace.restype = ctypes.c_int64
     L.precond_gemm8_status.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
     L.precond_gemm8_status.restype = ctypes.c_int
     m.set_up((torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.uint8, torch.int32, torch.int64),
              torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else _current_stream,
              tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (
                  L.precond_rms_norm, L.precond_rms_norm_grad, L.precond_rms_norm_grad_workspace, L.precond_quantize8, L.precond_gemm8,
-                 L.precond_distill, L.precond_distill_workspace)), _allocator())
+                 L.precond_distill, L.precond_distill_workspace, L.precond_layer_norm, L.precond_layer_norm_grad,
+                 L.precond_layer_norm_grad_workspace, L.precond_policy, L.precond_list_create, L.precond_list_destroy,
+                 L.precond_list_workspace, L.precond_grad_norm, L.precond_clip_grads)), _allocator())
     return m
 
 
@@ -145,3 +150,73 @@ def precond_distill(h, logits, ids, teacher, loss, weight=None, temperature: flo
     ``temperature`` is 1e-18 to 1e18."""
     code = _b.distill(h, logits, ids, teacher, loss, weight, temperature, dlogits, workspace, stream)
     return code if raw or code == OK else _check(code, "precond_distill")
+
+
+def precond_layer_norm(h, x, weight, eps: float, bias=None, residual=None, total=None, y=None, q=None, scale=None, mean=None,
+                       rstd=None, stream=None, raw: bool = False) -> int:
+    """total = x + residual; y, and its 8-bit form (q, scale) = (total - mean) * rstd * weight + bias; mean and rstd
+    for the gradients.  Outputs that are None are not written."""
+    code = _b.layer_norm(h, x, weight, eps, bias, residual, total, y, q, scale, mean, rstd, stream)
+    return code if raw or code == OK else _check(code, "precond_layer_norm")
+
+
+def precond_layer_norm_grad_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace of precond_layer_norm_grad."""
+    return load().precond_layer_norm_grad_workspace(rows, cols)
+
+
+def precond_layer_norm_grad(h, dy, x, weight, mean, rstd, dx, dw, db=None, dresidual=None, workspace=None, stream=None,
+                            raw: bool = False) -> int:
+    """dx, dw and db of precond_layer_norm; x is the forward pass's total.  The workspace as in
+    precond_rms_norm_grad."""
+    code = _b.layer_norm_grad(h, dy, x, weight, mean, rstd, dx, dw, db, dresidual, workspace, stream)
+    return code if raw or code == OK else _check(code, "precond_layer_norm_grad")
+
+
+def precond_policy(h, logits, ids, advantage=None, old_logp=None, ref_logp=None, weight=None, temperature: float = 1.0,
+                   clip_low: float = 0.2, clip_high: float = 0.2, kl: float = 0.0, loss=None, logp=None, dlogits=None,
+                   stream=None, raw: bool = False) -> int:
+    """The clipped policy loss of every row's taken token ``ids``, its log probability and, with ``dlogits``, the
+    gradient (in place if it is ``logits``).  Without ``advantage`` the log probabilities alone.  ``old_logp`` None is
+    a ratio of 1; ``kl`` weighs the KL term against ``ref_logp``.  Rows of weight 0 and ids outside the vocabulary are
+    left out: zero loss, logp and gradient.
+
+    A preference loss over pairs of sequences takes two calls: one for logp, whose sums per sequence give each row its
+    coefficient, and one with those as ``-advantage`` for the gradient."""
+    code = _b.policy(h, logits, ids, advantage, old_logp, ref_logp, weight, temperature, clip_low, clip_high, kl, loss, logp,
+                     dlogits, stream)
+    return code if raw or code == OK else _check(code, "precond_policy")
+
+
+class TensorList:
+    """Tensors (float32 or bfloat16, dense, apart from one another) that precond_grad_norm and precond_clip_grads
+    take together.  It keeps them alive; make it once for buffers that stay."""
+
+    def __init__(self, tensors):
+        self.tensors = tuple(tensors)
+        code, self._list, self.workspace = _b.tensor_list(self.tensors)    # workspace: bytes, of a call
+        _check(code, "precond_list_create")
+
+    def __len__(self) -> int:
+        return len(self.tensors)
+
+
+def _listed(grads) -> TensorList:
+    return grads if isinstance(grads, TensorList) else TensorList(grads)
+
+
+def precond_grad_norm(h, grads, norm, workspace=None, stream=None, raw: bool = False) -> int:
+    """norm (one float32 on the device) = the 2-norm of all elements of ``grads``, a TensorList or a sequence of
+    tensors.  The workspace as in precond_rms_norm_grad."""
+    g = _listed(grads)
+    code = _b.grad_norm(h, g._list, g.tensors[0] if g.tensors else None, norm, workspace, stream)
+    return code if raw or code == OK else _check(code, "precond_grad_norm")
+
+
+def precond_clip_grads(h, grads, max_norm: float, norm, given: bool = False, workspace=None, stream=None,
+                       raw: bool = False) -> int:
+    """``grads`` *= max_norm / norm in place where norm > max_norm.  The norm is computed and left in ``norm``, or, with
+    ``given``, read there.  Gradients whose norm is not finite stay as they are."""
+    g = _listed(grads)
+    code = _b.clip_grads(h, g._list, g.tensors[0] if g.tensors else None, max_norm, norm, given, workspace, stream)
+    return code if raw or code == OK else _check(code, "precond_clip_grads")
