@@ -4,25 +4,37 @@
 //
 // Bound by memory: the norm reads every element once; the factor is known only
 // then, so clipping reads them again and writes them.  The second pass goes
-// through each block's tensors from the end, so that what the first one read last
+// through each warp's tensors from the end, so that what the first one read last
 // is still in L2 (129 MB).  Where the norm needs no clipping nothing more is read.
 //
-// The list comes as a kernel parameter (no upload, so that a captured call holds
-// its own copy).  Tensors are cut into pieces of 16 KB; a block takes consecutive
-// pieces, and writes one fp64 sum of its squares, in the workspace; every block of
-// the second kernel adds these in the same order.
+// A short list takes one launch: a cluster of 8 blocks, which read it a second time
+// when they have joined their sums through distributed shared memory.
 //
-// A thread squares up to four sectors (128 B) in fp32 and adds their sum to its
-// fp64 sum.  Where that fp32 sum lies outside 2^-70 .. 2^120, so that squares may
-// have overflowed or been lost, the same registers are squared in fp64.
+// The list comes as a kernel parameter (no upload, so that a captured call holds
+// its own copy).  Tensors are cut into pieces of 4 KB; a warp takes consecutive
+// pieces, four sectors a lane, so that many small tensors are under way at once
+// (by blocks and 16 KB, 97 weights of 333 KB with three vectors each took 25 us).
+// A block writes the sum of its squares, in the workspace; every block of the
+// second kernel adds these in the same order.
+//
+// A lane squares up to four sectors (128 B) in fp32; above that sums are pairs of
+// fp32 numbers, joined by TwoSum (Knuth), so that no length of list costs digits.
+// (fp64 additions, two a clock and SM, took a block's join a microsecond.)  Where
+// the squares of a lane's sectors add up to less than 2^-70 or more than 2^80, so
+// that they may have been lost or the pair's range may not do, they are read again
+// and added up in fp64, beside the pair.
 #pragma once
+
+#include <cooperative_groups.h>
 
 #include "form8.cuh"
 
 namespace precond {
 
-constexpr int CLIP_THREADS = 512, CLIP_PIECE = 512;   // a piece: sectors of 32 bytes
-constexpr int CLIP_U = 4;                             // sectors a thread has under way
+constexpr int CLIP_THREADS = 512, CLIP_WARPS = CLIP_THREADS / 32;
+constexpr int CLIP_U = 4;                             // sectors a lane has under way
+constexpr int CLIP_PIECE = 32 * CLIP_U;               // a piece: sectors of 32 bytes
+constexpr int CLIP_KEPT = (60 << 20) / 32 / CLIP_PIECE; // pieces that L2 is asked to keep between the passes
 
 struct ClipTensor {
   void* p;
@@ -54,32 +66,46 @@ struct ClipView {
   }
 };
 
-__device__ __forceinline__ void clip_load(uint32_t (&w)[8], const char* p) {
-  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p) : "memory");
+// A sector that stays in L2, or that leaves it before others do.
+__device__ __forceinline__ void clip_load(uint32_t (&w)[8], const char* p, bool stays) {
+  if (stays)
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p) : "memory");
+  else
+    asm volatile("ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void clip_store(char* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
 }
 
-// Calls f(tensor, its sectors s0 .. s1 - 1, whether they begin it) for each tensor that a block has pieces of; `back`:
-// from the last one.  A tensor's single elements go with its first piece.
+// Calls f(tensor, first sector of the piece, whether the piece begins it, whether it stays in L2) for each of a warp's
+// pieces; `back`: from the last one.  A block's pieces are consecutive, its warps take every 16th of them.  A tensor's
+// single elements go with its first piece.
 template <int MAX, typename F>
 __device__ __forceinline__ void clip_walk(const ClipTable<MAX>& t, bool back, F f) {
-  const int64_t all = t.first[t.count];
-  const int64_t lo = all * blockIdx.x / gridDim.x, hi = all * (blockIdx.x + 1) / gridDim.x;
-  if (lo >= hi) return;
-  const int64_t at = back ? hi - 1 : lo;
+  const int64_t all = t.first[t.count], lo = all * blockIdx.x / gridDim.x, hi = all * (blockIdx.x + 1) / gridDim.x;
+  // the last of every block's pieces, of all blocks' together what L2 may keep
+  const int64_t keep = hi - (hi - lo) * min(all, (int64_t)CLIP_KEPT) / all;
+  int64_t at = back ? hi - 1 - (threadIdx.x >> 5) : lo + (threadIdx.x >> 5);
+  if (at < lo || at >= hi) return;
   int a = 0, b = t.count - 1;                         // the last tensor that begins at or before this piece
   while (a < b) {
     const int m = (a + b + 1) / 2;
     if ((int64_t)t.first[m] <= at) a = m;
     else b = m - 1;
   }
-  for (; a >= 0 && a < t.count; a += back ? -1 : 1) {
-    const int64_t p0 = max(lo, (int64_t)t.first[a]), p1 = min(hi, (int64_t)t.first[a + 1]);
-    if (back ? (int64_t)t.first[a + 1] <= lo : (int64_t)t.first[a] >= hi) break;
-    if (p0 >= p1) continue;                           // an empty tensor
+  while (true) {
     const ClipView v(t.tensor[a]);
-    const int64_t s0 = (p0 - t.first[a]) * CLIP_PIECE, s1 = min(v.sectors, (p1 - t.first[a]) * CLIP_PIECE);
-    f(v, s0, s1, p0 == (int64_t)t.first[a]);
+    const int64_t p0 = t.first[a], p1 = t.first[a + 1];
+    for (; at >= max(lo, p0) && at < min(hi, p1); at += back ? -CLIP_WARPS : CLIP_WARPS)
+      f(v, (at - p0) * CLIP_PIECE + (threadIdx.x & 31), at == p0, at >= keep);
+    if (at < lo || at >= hi) return;
+    if (back)
+      while ((int64_t)t.first[a] > at) --a;
+    else
+      while ((int64_t)t.first[a + 1] <= at) ++a;
   }
 }
 
@@ -108,74 +134,118 @@ __device__ __noinline__ double clip_square_wide(const uint32_t* w, int n, bool b
   }
   return s;
 }
-// The block's sum in thread 0: lanes and warps in a fixed order.
-__device__ __forceinline__ double clip_block_sum(double v) {
-  __shared__ double red[CLIP_THREADS / 32];
-  v = warp_sum(v);
+// A sum: hi + lo, and what was added in fp64 (mostly nothing).
+struct ClipSum {
+  float hi, lo;
+  double wide;
+  __device__ __forceinline__ void add(float h, float l) {
+    const float s = hi + h, b = s - hi;
+    lo += ((hi - (s - b)) + (h - b)) + l;
+    hi = s;
+  }
+  // over the lanes, the same in each
+  __device__ __forceinline__ void join() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float h = __shfl_xor_sync(0xffffffffu, hi, o), l = __shfl_xor_sync(0xffffffffu, lo, o);
+      add(h, l);
+    }
+    if (__any_sync(0xffffffffu, wide != 0.0)) wide = warp_sum(wide);
+  }
+  __device__ __forceinline__ float root() const;
+};
+constexpr ClipSum CLIP_NOTHING = {0.f, 0.f, 0.0};
+// The block's sum in the first warp: lanes and warps in a fixed order.
+__device__ __forceinline__ ClipSum clip_block_sum(ClipSum v) {
+  __shared__ ClipSum red[CLIP_WARPS];
+  v.join();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  if (threadIdx.x < 32) v = warp_sum((int)threadIdx.x < (int)(blockDim.x >> 5) ? red[threadIdx.x] : 0.0);
+  if (threadIdx.x < 32) {
+    v = threadIdx.x < CLIP_WARPS ? red[threadIdx.x] : CLIP_NOTHING;
+    v.join();
+  }
   return v;
 }
 
+// The sum of the squares of a block's pieces, in thread 0.
 template <int MAX>
-__global__ void __launch_bounds__(CLIP_THREADS, 2) clip_norm_kernel(const __grid_constant__ ClipTable<MAX> t, double* partial) {
-  wait_for_previous();
-  let_next_start();
-  double sum = 0;
-  clip_walk(t, false, [&](const ClipView& v, int64_t s0, int64_t s1, bool begins) {
+__device__ __forceinline__ ClipSum clip_squares(const ClipTable<MAX>& t) {
+  ClipSum sum = CLIP_NOTHING;
+  clip_walk(t, false, [&](const ClipView& v, int64_t s, bool begins, bool stays) {
     const bool bf16 = v.size == 2;
-    for (int64_t s = s0 + threadIdx.x; s < s1; s += CLIP_U * CLIP_THREADS) {
-      uint32_t w[CLIP_U][8];
+    uint32_t w[CLIP_U][8];
 #pragma unroll
-      for (int u = 0; u < CLIP_U; ++u) {
-        if (s + u * CLIP_THREADS < s1) {
-          clip_load(w[u], v.body + (s + u * CLIP_THREADS) * 32);
-        } else {
+    for (int u = 0; u < CLIP_U; ++u) {
+      if (s + u * 32 < v.sectors) {
+        clip_load(w[u], v.body + (s + u * 32) * 32, stays);
+      } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[u][i] = 0;
-        }
-      }
-      f2 e = 0;
-#pragma unroll
-      for (int u = 0; u < CLIP_U; ++u) e = clip_square(w[u], bf16, e);
-      const float q = sum2(e);
-      if (q >= 0x1p-70f && q <= 0x1p120f) {
-        sum += (double)q;
-      } else {                                        // nothing but zeros needs no second look
-        uint32_t any = 0;
-#pragma unroll
-        for (int u = 0; u < CLIP_U; ++u)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) any |= w[u][i];
-        if (any & (bf16 ? 0x7FFF7FFFu : 0x7FFFFFFFu)) {
-          for (int u = 0; u < CLIP_U; ++u)
-            if (s + u * CLIP_THREADS < s1) sum += clip_square_wide(reinterpret_cast<const uint32_t*>(v.body + (s + u * CLIP_THREADS) * 32), 8, bf16);
-        }
+        for (int i = 0; i < 8; ++i) w[u][i] = 0;
       }
     }
-    if (begins && (int)threadIdx.x < v.head + v.tail) {
-      const int64_t bytes = (int)threadIdx.x < v.head ? ((int)threadIdx.x - v.head) * v.size : v.sectors * 32 + ((int)threadIdx.x - v.head) * v.size;
-      const uint32_t w = bf16 ? (uint32_t) * reinterpret_cast<const uint16_t*>(v.body + bytes) : *reinterpret_cast<const uint32_t*>(v.body + bytes);
-      sum += clip_square_wide(&w, 1, bf16);
+    f2 e = 0;
+#pragma unroll
+    for (int u = 0; u < CLIP_U; ++u) e = clip_square(w[u], bf16, e);
+    const float q = sum2(e);
+    if (q >= 0x1p-70f && q <= 0x1p80f) {
+      sum.add(q, 0.f);
+    } else {                                          // nothing but zeros needs no second look
+      uint32_t any = 0;
+#pragma unroll
+      for (int u = 0; u < CLIP_U; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) any |= w[u][i];
+      if (any & (bf16 ? 0x7FFF7FFFu : 0x7FFFFFFFu)) {
+        for (int u = 0; u < CLIP_U; ++u)
+          if (s + u * 32 < v.sectors) sum.wide += clip_square_wide(reinterpret_cast<const uint32_t*>(v.body + (s + u * 32) * 32), 8, bf16);
+      }
+    }
+    const int lane = threadIdx.x & 31;
+    if (begins && lane < v.head + v.tail) {
+      const int64_t bytes = lane < v.head ? (lane - v.head) * v.size : v.sectors * 32 + (lane - v.head) * v.size;
+      const uint32_t x = bf16 ? (uint32_t) * reinterpret_cast<const uint16_t*>(v.body + bytes) : *reinterpret_cast<const uint32_t*>(v.body + bytes);
+      const float f = __uint_as_float(bf16 ? x << 16 : x), q1 = f * f;
+      if (q1 >= 0x1p-70f && q1 <= 0x1p80f) sum.add(q1, 0.f);
+      else sum.wide += (double)f * f;
     }
   });
-  sum = clip_block_sum(sum);
+  return clip_block_sum(sum);
+}
+template <int MAX>
+__global__ void __launch_bounds__(CLIP_THREADS, 2) clip_norm_kernel(const __grid_constant__ ClipTable<MAX> t, ClipSum* partial) {
+  wait_for_previous();
+  let_next_start();
+  const ClipSum sum = clip_squares(t);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
+// The square root.  Of a sum beside which something was added in fp64: of the mantissa and an even part of the exponent.
+__device__ __forceinline__ float ClipSum::root() const {
+  if (wide == 0.0) return sqrtf(hi + lo);
+  const double v = wide + (double)hi + (double)lo;
+  if (!(v > 0.0) || !(v < __longlong_as_double(0x7FF0000000000000ll))) return (float)v;      // infinite, not a number
+  const int e = ((__double2hiint(v) >> 20) - 1023) & ~1;
+  const double up = __hiloint2double((1023 - e / 2) << 20, 0);       // 2^(-e / 2), twice: 2^-e itself may be subnormal
+  const float r = sqrtf((float)(v * up * up));
+  return e > 256 ? INFINITY : e < -298 ? r * 0.f : (float)((double)r * __hiloint2double((1023 + e / 2) << 20, 0));
+}
 // The norm of all sums, in every thread.
-__device__ __forceinline__ float clip_total(const double* partial, int n) {
+__device__ __forceinline__ float clip_total(const ClipSum* partial, int n) {
   __shared__ float norm;
-  double v = 0;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) v += partial[i];
+  ClipSum v = CLIP_NOTHING;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const ClipSum p = partial[i];
+    v.add(p.hi, p.lo);
+    if (p.wide != 0.0) v.wide += p.wide;
+  }
   v = clip_block_sum(v);
-  if (threadIdx.x == 0) norm = (float)sqrt(v);
+  if (threadIdx.x == 0) norm = v.root();
   __syncthreads();
   return norm;
 }
 template <int = 0>
-__global__ void __launch_bounds__(CLIP_THREADS) clip_total_kernel(const double* partial, int n, float* norm) {
+__global__ void __launch_bounds__(CLIP_THREADS) clip_total_kernel(const ClipSum* partial, int n, float* norm) {
   wait_for_previous();
   let_next_start();
   const float v = clip_total(partial, n);
@@ -201,20 +271,17 @@ __device__ __forceinline__ void clip_scale(uint32_t (&w)[8], bool bf16, float c)
   }
 }
 
-// sums: how many of `partial` make the norm, which block 0 then leaves in `norm`; 0: it is there already.
 template <int MAX>
-__global__ void __launch_bounds__(CLIP_THREADS, 2) clip_scale_kernel(const __grid_constant__ ClipTable<MAX> t, const double* partial, int sums,
-                                                                     float max_norm, float* norm) {
-  wait_for_previous();
-  let_next_start();
-  const float total = sums ? clip_total(partial, sums) : *norm;
-  if (sums && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
-  if (!(total > max_norm) || !(total < INFINITY)) return;       // also where the norm is not a number
-  const float c = max_norm / total;
-  clip_walk(t, true, [&](const ClipView& v, int64_t s0, int64_t s1, bool begins) {
+__device__ __forceinline__ void clip_scale_all(const ClipTable<MAX>& t, float c) {
+  clip_walk(t, true, [&](const ClipView& v, int64_t s, bool begins, bool stays) {
     const bool bf16 = v.size == 2;
-    if (begins && (int)threadIdx.x < v.head + v.tail) {
-      const int64_t bytes = (int)threadIdx.x < v.head ? ((int)threadIdx.x - v.head) * v.size : v.sectors * 32 + ((int)threadIdx.x - v.head) * v.size;
+    uint32_t w[CLIP_U][8];
+#pragma unroll
+    for (int u = 0; u < CLIP_U; ++u)
+      if (s + u * 32 < v.sectors) clip_load(w[u], v.body + (s + u * 32) * 32, stays);
+    const int lane = threadIdx.x & 31;
+    if (begins && lane < v.head + v.tail) {
+      const int64_t bytes = lane < v.head ? (lane - v.head) * v.size : v.sectors * 32 + (lane - v.head) * v.size;
       if (bf16) {
         __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(v.body + bytes);
         *p = __float2bfloat16_rn(__bfloat162float(*p) * c);
@@ -222,21 +289,53 @@ __global__ void __launch_bounds__(CLIP_THREADS, 2) clip_scale_kernel(const __gri
         *reinterpret_cast<float*>(v.body + bytes) *= c;
       }
     }
-    const int64_t steps = (s1 - s0 + CLIP_U * CLIP_THREADS - 1) / (CLIP_U * CLIP_THREADS);
-    for (int64_t k = steps - 1; k >= 0; --k) {
-      const int64_t s = s0 + k * (CLIP_U * CLIP_THREADS) + threadIdx.x;
-      uint32_t w[CLIP_U][8];
 #pragma unroll
-      for (int u = 0; u < CLIP_U; ++u)
-        if (s + u * CLIP_THREADS < s1) clip_load(w[u], v.body + (s + u * CLIP_THREADS) * 32);
-#pragma unroll
-      for (int u = 0; u < CLIP_U; ++u)
-        if (s + u * CLIP_THREADS < s1) {
-          clip_scale(w[u], bf16, c);
-          st_sector(v.body + (s + u * CLIP_THREADS) * 32, w[u]);
-        }
-    }
+    for (int u = 0; u < CLIP_U; ++u)
+      if (s + u * 32 < v.sectors) {
+        clip_scale(w[u], bf16, c);
+        clip_store(v.body + (s + u * 32) * 32, w[u]);
+      }
   });
+}
+// Whether a norm is clipped: not where it is infinite or not a number.
+__device__ __forceinline__ bool clips(float norm, float max_norm) { return norm > max_norm && norm < INFINITY; }
+
+// sums: how many of `partial` make the norm, which block 0 then leaves in `norm`; 0: it is there already.
+template <int MAX>
+__global__ void __launch_bounds__(CLIP_THREADS, 2) clip_scale_kernel(const __grid_constant__ ClipTable<MAX> t, const ClipSum* partial, int sums,
+                                                                     float max_norm, float* norm) {
+  wait_for_previous();
+  let_next_start();
+  const float total = sums ? clip_total(partial, sums) : *norm;
+  if (sums && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+  if (clips(total, max_norm)) clip_scale_all(t, max_norm / total);
+}
+
+// A short list: one cluster.  max_norm infinite: the norm alone.
+constexpr int CLIP_CLUSTER = 8;
+template <int MAX>
+__global__ void __launch_bounds__(CLIP_THREADS, 2) clip_short_kernel(const __grid_constant__ ClipTable<MAX> t, float max_norm, float* norm) {
+  namespace cg = cooperative_groups;
+  __shared__ ClipSum sums[CLIP_CLUSTER];
+  cg::cluster_group cluster = cg::this_cluster();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");      // the blocks have begun
+  wait_for_previous();
+  let_next_start();
+  const ClipSum sum = clip_squares(t);
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (threadIdx.x == 0)
+    for (int i = 0; i < CLIP_CLUSTER; ++i) *cluster.map_shared_rank(&sums[blockIdx.x], i) = sum;
+  cluster.sync();
+  ClipSum v = sums[0];
+#pragma unroll
+  for (int i = 1; i < CLIP_CLUSTER; ++i) {
+    v.add(sums[i].hi, sums[i].lo);
+    if (sums[i].wide != 0.0) v.wide += sums[i].wide;
+  }
+  const float total = v.root();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
+  if (clips(total, max_norm)) clip_scale_all(t, max_norm / total);
 }
 
 }  // namespace precond

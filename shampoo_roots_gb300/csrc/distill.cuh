@@ -528,9 +528,7 @@ struct Part {
     }
     one = at >= 0 ? as_float(z[at]) : -INFINITY;
   }
-  // `hide` sees each vector that is read here, NV = 0, before it counts
-  template <typename Hide>
-  __device__ __forceinline__ void sums(const T* z, const Slice& sl, int tid, int threads, float c, float& m, float& s, Hide hide) {
+  __device__ __forceinline__ void sums(const T* z, const Slice& sl, int tid, int threads, float c, float& m, float& s) {
     m = -INFINITY;
     s = 0.f;
     if constexpr (NV > 0) {
@@ -557,7 +555,6 @@ struct Part {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           if (i0 + u * threads < sl.nvec) {
-            hide(i0 + u * threads, x[u]);
             float f[V::N];
             V::unpack(x[u], f);
             distill_take<T>(m, s, f, c);
@@ -638,7 +635,7 @@ __global__ void __launch_bounds__(DISTILL_THREADS + (FUSED ? 32 : 0), 2) distill
     bool teaches = false;
     if (reads) {
       x.load(z, sl, tid, threads);
-      x.sums(z, sl, tid, threads, c, m, s, [](int, uint4&) {});
+      x.sums(z, sl, tid, threads, c, m, s);
       join_warp(m, s, c);
       begun_wait(parts);
       if (lane < parts) *cluster.map_shared_rank(&sh.sums[part * streaming + warp], lane) = make_float2(m, s);

@@ -68,6 +68,15 @@ inline int cuda_error(const char* what, cudaError_t e) {
 int prepare(Handle* h);
 cudaError_t training_attributes();
 
+// The attributes of a launch: programmatic (common.cuh, wait_for_previous), and a cluster of blocks; returns how many.
+inline int launch_attributes(cudaLaunchAttribute (&at)[2], int cluster) {
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  return cluster > 1 ? 2 : 1;
+}
 template <typename... KArgs, typename... Args>
 cudaError_t launch(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, int cluster, Args... args) {
   cudaLaunchConfig_t cfg = {};
@@ -76,13 +85,8 @@ cudaError_t launch(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, cuda
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;     // common.cuh, wait_for_previous
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = cluster;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.numAttrs = launch_attributes(at, cluster);
   cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
 

@@ -22,6 +22,7 @@
 
 #include <type_traits>
 
+#include "ptx.cuh"
 #include "rows.cuh"
 
 namespace precond {
@@ -158,18 +159,20 @@ __device__ __forceinline__ void cluster_exchange(ClusterWords& w, float a, float
   if (lost) got[0] = make_float2(__uint_as_float(0x7FFFFFFFu), __uint_as_float(0x7FFFFFFFu));
 }
 
+// Sum over the warps' values, a warp a lane: the warps that are there come first, the others are zero.
+__device__ __forceinline__ float sum_warps(float v) {
+  if (blockDim.x > 512) v += __shfl_xor_sync(0xffffffffu, v, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ int warp_lane() { return threadIdx.x & (blockDim.x > 512 ? 31 : 15); }
 // mean and squared deviations of a row from its warps' (sum, squared deviations).
 __device__ __forceinline__ float2 row_moments(const float2* mine, const float2* columns, float inv_cols) {
-  const int nw = blockDim.x >> 5;
-  float s = 0.f, dev = 0.f;
-  for (int i = 0; i < nw; ++i) s += mine[i].x;
-  const float mean = s * inv_cols;
-  for (int i = 0; i < nw; ++i) {
-    const float2 v = mine[i], n = columns[i];
-    const float d = fmaf(v.x, n.y, -mean);
-    dev += fmaf(n.x * d, d, v.y);
-  }
-  return make_float2(mean, dev);
+  const float2 v = mine[warp_lane()], n = columns[warp_lane()];
+  const float mean = sum_warps(v.x) * inv_cols;
+  const float d = fmaf(v.x, n.y, -mean);
+  return make_float2(mean, sum_warps(fmaf(n.x * d, d, v.y)));
 }
 __device__ __forceinline__ float2 cluster_moments(const float2 (&got)[4], int cols, float inv_cols) {
   const int lane = threadIdx.x & 31;
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(NV == 2 || (sizeof(T) == 2 && !VEC) ? 512 : 38
   __syncthreads();
   const float inv_mine = mine ? 1.f / (float)mine : 0.f;
   for (unsigned call = 1; row - below < a.rows; row += step, ++call) {
-    F16 v[NV];
+    Raw16<T> h[NV];                      // as stored: unpacked where it is used, which costs less than the registers
     f2 s = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -244,8 +247,8 @@ __global__ void __launch_bounds__(NV == 2 || (sizeof(T) == 2 && !VEC) ? 512 : 38
         add_stream(nx[j], nr[j]);
         store16<VEC>(reinterpret_cast<T*>(a.h) + row * a.ldh, c[j], cols, nx[j], xs);
       }
-      v[j] = unpack(nx[j]);
-      s = total16(v[j], s);
+      h[j] = nx[j];
+      s = total16(unpack(h[j]), s);
     }
     const int next = !PART || row + step < a.rows ? a.cols : 0;
     if (row + step - below < a.rows) {
@@ -261,7 +264,7 @@ __global__ void __launch_bounds__(NV == 2 || (sizeof(T) == 2 && !VEC) ? 512 : 38
     float2 m = make_float2(sum * (PART ? inv_cols : inv_mine), 0.f);
     f2 d2 = 0;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) d2 = deviations(v[j], m.x, cols - c[j], d2);
+    for (int j = 0; j < NV; ++j) d2 = deviations(unpack(h[j]), m.x, cols - c[j], d2);
     m.y = sum2(d2);
     if (PART) {
       part_sums(m.y, none);
@@ -284,10 +287,11 @@ __global__ void __launch_bounds__(NV == 2 || (sizeof(T) == 2 && !VEC) ? 512 : 38
       const f2 rs = f2_of(rstd, rstd), mm = f2_of(-m.x, -m.x);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
+        F16 v = unpack(h[j]);
         const F16 w = table_get(table + j * 8 * bx, bx), b = table_get(table + (j * 8 + 4) * bx, bx);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[j].p[i] = fma2(mul2(add2(v[j].p[i], mm), rs), w.p[i], b.p[i]);
-        norm_write<T, VEC>(a, row, c[j], cols, v[j], q8_scale_at(row, c[j] >> 7, rblocks), xs);
+        for (int i = 0; i < 8; ++i) v.p[i] = fma2(mul2(add2(v.p[i], mm), rs), w.p[i], b.p[i]);
+        norm_write<T, VEC>(a, row, c[j], cols, v, q8_scale_at(row, c[j] >> 7, rblocks), xs);
       }
       if (a.q && (a.cols & 511) && rank == 0 && row < rblocks * 128) norm_pad(a, row, rblocks);
     }
@@ -564,6 +568,280 @@ __global__ void __launch_bounds__(512, 1) layer_grad_long_kernel(LayerGradArgs a
       store16<VEC>(dx, (int)c, a.cols, o, xs);
     }
   }
+}
+
+// ------------------------------------------------------------- rows streamed through shared memory
+// Where a group of threads has several rows, whole 16-byte vectors each, one of
+// its threads copies them into a ring of rows in shared memory (bulk copies that
+// an mbarrier counts), `stages` rows ahead, and the registers hold the present row
+// alone.  A block's groups share the table of w and b; an SM has one block.
+//
+// A stage's row has been read by all of the group's threads when they have met for
+// its sums, and is filled again by then.
+
+// The group's part of the block's shared memory.
+struct RowRing {
+  uint8_t* rows;                       // [stage][input][bytes of a row]
+  unsigned long long* full;            // [stage]
+  float2* words;                       // [row in turn][warp]
+  int stages, inputs, bytes;
+  static __host__ __device__ size_t size(int stages, int inputs, int bytes) {
+    return (size_t)stages * inputs * bytes + (stages + 1) / 2 * 16 + 2 * 32 * sizeof(float2);
+  }
+  __device__ __forceinline__ RowRing(uint8_t* base, int group, int stages_, int inputs_, int bytes_)
+      : stages(stages_), inputs(inputs_), bytes(bytes_) {
+    rows = base + group * size(stages, inputs, bytes);
+    words = reinterpret_cast<float2*>(rows + (size_t)stages * inputs * bytes);
+    full = reinterpret_cast<unsigned long long*>(words + 2 * 32);
+  }
+  __device__ __forceinline__ void start() const {
+    for (int i = 0; i < stages; ++i) mbar_init(smem_u32(full + i), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __device__ __forceinline__ void fill(int stage, const void* const (&from)[3]) const {
+    const uint32_t bar = smem_u32(full + stage);
+    mbar_expect_tx(bar, inputs * bytes);
+    for (int i = 0; i < inputs; ++i)
+      asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                   ::"r"(smem_u32(rows + ((size_t)stage * inputs + i) * bytes)), "l"(from[i]), "r"(bytes), "r"(bar) : "memory");
+  }
+  __device__ __forceinline__ const uint8_t* row(int stage, int input) const { return rows + ((size_t)stage * inputs + input) * bytes; }
+};
+
+// 16 columns from a row in shared memory; what lies past its end is zero.  Lanes begin with different 16-byte pieces, so
+// that no bank is met twice, and put them in order.
+__device__ __forceinline__ void ring_load(Raw16<__nv_bfloat16>& o, const uint8_t* row, int c, int cols) {
+  const int turn = (threadIdx.x >> 2) & 1;
+  uint4 v[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int at = c + 8 * (k ^ turn);
+    v[k] = at < cols ? *reinterpret_cast<const uint4*>(row + at * 2) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o.w[i] = turn ? (&v[1].x)[i] : (&v[0].x)[i];
+    o.w[4 + i] = turn ? (&v[0].x)[i] : (&v[1].x)[i];
+  }
+}
+__device__ __forceinline__ void ring_load(Raw16<float>& o, const uint8_t* row, int c, int cols) {
+  const int turn = (threadIdx.x >> 1) & 3;
+  uint4 v[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int at = c + 4 * (k ^ turn);
+    v[k] = at < cols ? *reinterpret_cast<const uint4*>(row + at * 4) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)            // by the turn's low bit, then by its high bit
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.w[4 * k + i] = turn & 1 ? (&v[k ^ 1].x)[i] : (&v[k].x)[i];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = o.w[4 * k + i], hi = o.w[4 * (k + 2) + i];
+      o.w[4 * k + i] = turn & 2 ? hi : lo;
+      o.w[4 * (k + 2) + i] = turn & 2 ? lo : hi;
+    }
+}
+// Two values of every warp of the group, after which all of its threads are done with the stage's row.
+__device__ __forceinline__ const float2* ring_exchange(const RowRing& ring, float a, float b, int half) {
+  float2* mine = ring.words + half * 32;
+  if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = make_float2(a, b);
+  if (blockDim.x > 32) asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.y), "r"((int)blockDim.x) : "memory");
+  else __syncwarp();
+  return mine;
+}
+
+constexpr int STREAM_THREADS[5] = {0, 768, 640, 0, 512};       // most of a norm's block, by vectors a thread: what the registers allow
+
+// (sum, squared deviations) of a warp's columns, `mine` of them, NV vectors a lane.  Where the warp is full its lanes join
+// in pairs, both values at once: of two halves of n columns, m = (m1 + m2) / 2 and S = S1 + S2 + n (m1 - m2)^2 / 2.
+template <int NV>
+__device__ __forceinline__ float2 warp_moments(const F16 (&v)[NV], const int (&c)[NV], int cols, int mine, float inv_mine) {
+  f2 s = 0, d2 = 0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) s = total16(v[j], s);
+  if (mine == 512 * NV) {
+    float m = sum2(s) * (1.f / (16 * NV));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) d2 = deviations(v[j], m, 16, d2);
+    float dev = sum2(d2);
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, 1 << k), dev2 = __shfl_xor_sync(0xffffffffu, dev, 1 << k), d = m2 - m;
+      dev = fmaf(d * (float)(8 * NV << k), d, dev + dev2);
+      m = 0.5f * (m + m2);
+    }
+    return make_float2(m * (512 * NV), dev);
+  }
+  const float sum = warp_sum(sum2(s)), m = sum * inv_mine;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) d2 = deviations(v[j], m, cols - c[j], d2);
+  return make_float2(sum, warp_sum(sum2(d2)));
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(STREAM_THREADS[NV], 1) layer_norm_stream_kernel(LayerNormArgs a, int stages) {
+  __shared__ float2 columns[32];
+  extern __shared__ __align__(16) uint8_t row_scratch[];
+  const int bx = blockDim.x, tx = threadIdx.x, step = gridDim.x * blockDim.y;
+  float4* table = reinterpret_cast<float4*>(row_scratch) + tx;
+  const RowRing ring(row_scratch + bx * NV * 128, threadIdx.y, stages, a.r ? 2 : 1, a.cols * (int)sizeof(T));
+  int row = blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t rblocks = q8_row_blocks(a.rows);
+  const float inv_cols = 1.0f / (float)a.cols;
+  if (tx == 0) ring.start();
+  for (int i = tx; i < 64; i += bx) ring.words[i] = make_float2(0.f, 0.f);
+  int c[NV], mine = 0;                                                 // mine: columns of this warp
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    c[j] = (j * bx + tx) * 16;
+    mine += warp_columns(a.cols, j * bx + (tx & ~31));
+  }
+  const float inv_mine = mine ? 1.f / (float)mine : 0.f;
+  if (threadIdx.y == 0 && tx < 32) columns[tx] = make_float2(0.f, 0.f);
+  __syncthreads();
+  wait_for_previous();
+  let_next_start();
+  auto fill = [&](int stage, int64_t k) {
+    const void* const from[3] = {reinterpret_cast<const T*>(a.x) + k * a.ldx, reinterpret_cast<const T*>(a.r) + k * a.ldr, nullptr};
+    ring.fill(stage, from);
+  };
+  if (tx == 0)
+    for (int i = 0; i < stages && (int64_t)row + (int64_t)i * step < a.rows; ++i) fill(i, (int64_t)row + (int64_t)i * step);
+  if (threadIdx.y == 0) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      table_set(table + j * 8 * bx, bx, load_w16(a.w, a.w_bf16, c[j], a.cols));
+      table_set(table + (j * 8 + 4) * bx, bx, a.b ? load_w16(a.b, a.w_bf16, c[j], a.cols) : zero16());
+    }
+    if ((tx & 31) == 0) columns[tx >> 5] = make_float2((float)mine, inv_mine);
+  }
+  __syncthreads();
+  int stage = 0, phase = 0, half = 0;
+  for (; row < a.rows; row += step, half ^= 1) {
+    const bool lost = !mbar_wait_own(smem_u32(ring.full + stage), phase, nullptr);
+    F16 v[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      Raw16<T> h;
+      ring_load(h, ring.row(stage, 0), c[j], a.cols);
+      if (a.r) {
+        Raw16<T> r;
+        ring_load(r, ring.row(stage, 1), c[j], a.cols);
+        add_stream(h, r);
+        store16<true>(reinterpret_cast<T*>(a.h) + row * a.ldh, c[j], a.cols, h, nullptr);
+      }
+      v[j] = unpack(h);
+    }
+    const float2 w = warp_moments<NV>(v, c, a.cols, mine, inv_mine);
+    float2 t = row_moments(ring_exchange(ring, w.x, w.y, half), columns, inv_cols);
+    if (tx == 0 && (int64_t)row + (int64_t)stages * step < a.rows) fill(stage, (int64_t)row + (int64_t)stages * step);
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+    if (lost) t = make_float2(__uint_as_float(0x7FFFFFFFu), 0.f);
+    const float rstd = rstd_of(t.y, inv_cols, a.eps);
+    if (tx == 0) {
+      if (a.mean) a.mean[row] = t.x;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    if (!a.q && !a.y) continue;
+    const f2 rs = f2_of(rstd, rstd), mm = f2_of(-t.x, -t.x);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const F16 w = table_get(table + j * 8 * bx, bx), b = table_get(table + (j * 8 + 4) * bx, bx);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j].p[i] = fma2(mul2(add2(v[j].p[i], mm), rs), w.p[i], b.p[i]);
+      norm_write<T, true>(a, row, c[j], a.cols, v[j], q8_scale_at(row, c[j] >> 7, rblocks), nullptr);
+    }
+    if (a.q && (a.cols & 511)) norm_pad(a, row, rblocks);
+  }
+  if (a.q)
+    for (; row < rblocks * 128; row += step) norm_pad(a, row, rblocks);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(512, 1) layer_grad_stream_kernel(LayerGradArgs a, int stages) {
+  extern __shared__ __align__(16) uint8_t row_scratch[];
+  const int bx = blockDim.x, tx = threadIdx.x, step = gridDim.x * blockDim.y;
+  float4* table = reinterpret_cast<float4*>(row_scratch) + tx;
+  const RowRing ring(row_scratch + bx * 64, threadIdx.y, stages, a.dr ? 3 : 2, a.cols * (int)sizeof(T));
+  int row = blockIdx.x * blockDim.y + threadIdx.y;
+  const float inv_cols = 1.0f / (float)a.cols;
+  const int c = tx * 16;
+  if (tx == 0) ring.start();
+  for (int i = tx; i < 64; i += bx) ring.words[i] = make_float2(0.f, 0.f);
+  __syncthreads();
+  wait_for_previous();
+  let_next_start();
+  auto fill = [&](int stage, int64_t k) {
+    const void* const from[3] = {reinterpret_cast<const T*>(a.dy) + k * a.lddy, reinterpret_cast<const T*>(a.x) + k * a.ldx,
+                                 reinterpret_cast<const T*>(a.dr) + k * a.lddr};
+    ring.fill(stage, from);
+  };
+  if (tx == 0)
+    for (int i = 0; i < stages && (int64_t)row + (int64_t)i * step < a.rows; ++i) fill(i, (int64_t)row + (int64_t)i * step);
+  float nmean = 0.f, nrstd = 0.f;
+  if (row < a.rows) {
+    nmean = a.mean[row];
+    nrstd = a.rstd[row];
+  }
+  if (threadIdx.y == 0) table_set(table, bx, load_w16(a.w, a.w_bf16, c, a.cols));
+  __syncthreads();
+  F16 dw = zero16(), db = zero16();
+  int stage = 0, phase = 0, half = 0;
+  for (; row < a.rows; row += step, half ^= 1) {
+    const float mean = nmean;
+    const f2 rs = f2_of(nrstd, nrstd);
+    if (row + step < a.rows) {
+      nmean = a.mean[row + step];
+      nrstd = a.rstd[row + step];
+    }
+    const bool lost = !mbar_wait_own(smem_u32(ring.full + stage), phase, nullptr);
+    Raw16<T> o, res;
+    ring_load(o, ring.row(stage, 0), c, a.cols);
+    F16 g = unpack(o);
+    ring_load(o, ring.row(stage, 1), c, a.cols);
+    F16 n = unpack(o);
+    if (a.dr) ring_load(res, ring.row(stage, 2), c, a.cols);
+    GradSums s = {0, 0};
+    layer_terms(g, n, table_get(table, bx), dw, db, f2_of(-mean, -mean), rs, s);
+    const float2* all = ring_exchange(ring, warp_sum(sum2(s.g)), warp_sum(sum2(s.gn)), half);
+    if (tx == 0 && (int64_t)row + (int64_t)stages * step < a.rows) fill(stage, (int64_t)row + (int64_t)stages * step);
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+    const float2 v = all[warp_lane()];
+    float2 t = make_float2(sum_warps(v.x), sum_warps(v.y));
+    if (lost) t.x = __uint_as_float(0x7FFFFFFFu);
+    layer_out(o, g, n, rs, make_float2(t.x * inv_cols, t.y * inv_cols), a.dr != nullptr, res);
+    store16<true>(reinterpret_cast<T*>(a.dx) + row * a.lddx, c, a.cols, o, nullptr);
+  }
+  if (blockDim.y > 1) {                  // the block's rows side by side: in their order, through shared memory
+    F16* side = reinterpret_cast<F16*>(row_scratch + bx * 64);
+    F16* at = side + (threadIdx.y * bx + tx) * 2;
+    __syncthreads();                     // every row that was copied has been read
+    at[0] = dw;
+    at[1] = db;
+    __syncthreads();
+    if (threadIdx.y > 0) return;
+    for (int y = 1; y < blockDim.y; ++y) {
+      const F16* other = side + (y * bx + tx) * 2;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dw.p[i] = add2(dw.p[i], other[0].p[i]);
+        db.p[i] = add2(db.p[i], other[1].p[i]);
+      }
+    }
+  }
+  float* out = a.partial + (int64_t)blockIdx.x * 2 * a.cols;
+  store_partial(out, c, a.cols, dw);
+  store_partial(out + a.cols, c, a.cols, db);
 }
 
 // dw and db: the blocks' sums, added in their order (32 columns a block; 32 threads a column take every 32nd sum, then

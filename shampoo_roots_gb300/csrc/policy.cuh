@@ -16,7 +16,10 @@
 // policy is sure of it (q_id near 1, where 1 - q_id would be all rounding).
 #pragma once
 
+#include <type_traits>
+
 #include "distill.cuh"
+#include "ptx.cuh"
 
 namespace precond {
 
@@ -45,62 +48,184 @@ __device__ __forceinline__ void hide_element(uint4& w, int e, const float*) {
   w = make_uint4(e == 0 ? NONE : w.x, e == 1 ? NONE : w.y, e == 2 ? NONE : w.z, e == 3 ? NONE : w.w);
 }
 
-template <typename T, int NV>
-__global__ void __launch_bounds__(DISTILL_THREADS, 2) policy_kernel(PolicyArgs a) {
+constexpr int POLICY_THREADS = 512;                  // most of a block
+constexpr int POLICY_PART = 220 << 10;               // bytes of a row that fit into a block's shared memory
+constexpr int POLICY_U = 4;                          // vectors a thread has under way
+
+// f(i, vectors i, i + threads, ...) over a thread's vectors of n, U of them at a time, then one by one; `load(i)`.
+template <int U, typename L, typename F>
+__device__ __forceinline__ void policy_each(int n, int tid, int threads, L load, F f) {
+  int i = tid;
+  for (; i + (U - 1) * threads < n; i += U * threads) {
+    uint4 w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = load(i + u * threads);
+#pragma unroll
+    for (int u = 0; u < U; ++u) f(i + u * threads, w[u]);
+  }
+  for (; i < n; i += threads) f(i, load(i));
+}
+__device__ __forceinline__ float warp_max_fast(float m) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(m));
+  return r;
+}
+__device__ __forceinline__ float largest_of(uint4 w, float m, const __nv_bfloat16*) {
+  uint32_t x = w.x;
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(w.y));
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(w.z));
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(w.w));
+  return max3_nan(m, __uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+}
+__device__ __forceinline__ float largest_of(uint4 w, float m, const float*) {
+  m = max3_nan(m, __uint_as_float(w.x), __uint_as_float(w.y));
+  return max3_nan(m, __uint_as_float(w.z), __uint_as_float(w.w));
+}
+
+// What a row's threads need of its sums and of its loss, from one warp of each block.
+struct PolicyRow {
+  float b, k, g;                                     // the shift, and the factor of 2^(z c - k) in dz
+  float taken;                                       // dz of the taken token
+};
+
+// KEPT: a block's part of the row lies in its shared memory; otherwise the row is read twice.
+template <typename T, bool KEPT>
+__global__ void __launch_bounds__(POLICY_THREADS, 3) policy_kernel(PolicyArgs a) {
   namespace cg = cooperative_groups;
-  __shared__ float2 sums[8 * DISTILL_THREADS / 32];
-  constexpr int N = LogitVec<T>::N;
+  using V = LogitVec<T>;
+  constexpr float NOT_A_NUMBER = __builtin_nanf("");
+  extern __shared__ __align__(16) uint8_t policy_smem[];
+  __shared__ float2 own[POLICY_THREADS / 32], sums[8];   // (maximum, sum) of the block's warps, of the cluster's blocks
+  __shared__ PolicyRow result;
+  __shared__ __align__(8) unsigned long long arrived;
   cg::cluster_group cluster = cg::this_cluster();
   const int parts = (int)cluster.num_blocks(), part = (int)cluster.block_rank();
   const int tid = threadIdx.x, threads = blockDim.x, warps = threads >> 5, warp = tid >> 5, lane = tid & 31;
   const int64_t row = blockIdx.x / parts;
   const float c = LOG2E / a.tau;
   begun_arrive(parts);
+  if (KEPT) {
+    if (tid == 0) {
+      mbar_init(smem_u32(&arrived), 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+  }
   wait_for_previous();
   let_next_start();
   const float weight = a.weight ? a.weight[row] : 1.0f;
-  const int64_t wide = a.ids64 ? reinterpret_cast<const int64_t*>(a.ids)[row] : (int64_t) reinterpret_cast<const int32_t*>(a.ids)[row];
-  const int id = wide >= 0 && wide < a.vocab ? (int)wide : -1;
-  const float advantage = a.advantage ? a.advantage[row] : 0.f, old = a.old ? a.old[row] : 0.f, ref = a.ref ? a.ref[row] : 0.f;
-  const bool reads = weight != 0.0f && id >= 0;          // uniform over the cluster
   const T* z = reinterpret_cast<const T*>(a.z) + row * a.ldz;
   T* dz = reinterpret_cast<T*>(a.dz) + row * a.lddz;
   const Slice sl(z, (int)a.vocab, parts, part);
-  // the vector that holds the taken token, where this block's part has it, and the thread that has that vector
-  const int vec = id >= sl.body && id < sl.tail ? (id - sl.body) / N : -1, element = (id - sl.body) % N;
-
-  Part<T, NV> x;
-  x.at = sl.single(tid);
-  Shift shift(0.f, c);
-  float slope = 0.f, logp = 0.f, loss = 0.f, total = 1.f, rest = 0.f;
-  if (reads) {
-    x.load(z, sl, tid, threads);
-    const float taken = as_float(z[id]);                 // before anything is written: dz may be z
-    if (x.at == id) x.one = -INFINITY;
+  const int single = sl.single(tid), n = sl.nvec;
+  const bool copies = KEPT && n && weight != 0.0f;       // before the taken token is known
+  if (copies && tid == 0) {
+    mbar_expect_tx(smem_u32(&arrived), n * 16);
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(smem_u32(policy_smem)), "l"(z + sl.body), "r"(n * 16), "r"(smem_u32(&arrived)) : "memory");
+  }
+  const int64_t wide = a.ids64 ? reinterpret_cast<const int64_t*>(a.ids)[row] : (int64_t) reinterpret_cast<const int32_t*>(a.ids)[row];
+  const int id = wide >= 0 && wide < a.vocab ? (int)wide : -1;
+  const bool reads = weight != 0.0f && id >= 0;          // uniform over the cluster
+  const bool aligned = (reinterpret_cast<uintptr_t>(dz + sl.body) & 15) == 0;
+  auto put = [&](int i, uint4 w) {
+    if (aligned) {
+      reinterpret_cast<uint4*>(dz + sl.body)[i] = w;
+    } else {
+      float f[V::N];
+      V::unpack(w, f);
 #pragma unroll
-    for (int u = 0; u < NV; ++u)
-      if (tid + u * threads == vec) hide_element(x.w[u], element, z);
-    float m, s;
-    x.sums(z, sl, tid, threads, c, m, s, [&](int i, uint4& w) {
+      for (int e = 0; e < V::N; ++e) set_float(dz + sl.body + i * V::N + e, f[e]);
+    }
+  };
+  auto arrive = [&]() { return mbar_wait_own(smem_u32(&arrived), 0, nullptr) || mbar_wait_own(smem_u32(&arrived), 0, nullptr); };
+  if (!reads) {
+    begun_wait(parts);
+    if (copies) arrive();                                // no block leaves while its copy is under way
+    if (part == 0 && tid == 0) {
+      if (a.loss) a.loss[row] = 0.f;
+      if (a.logp) a.logp[row] = 0.f;
+    }
+    if (a.dz) {
+      for (int i = tid; i < n; i += threads) put(i, make_uint4(0, 0, 0, 0));
+      if (single >= 0) set_float(dz + single, 0.f);
+    }
+    return;
+  }
+  const int vec = id >= sl.body && id < sl.tail ? (id - sl.body) / V::N : -1, element = (id - sl.body) % V::N;
+  bool lost = false;
+  float one = single >= 0 ? as_float(z[single]) : -INFINITY;
+  const float open = single == id ? -INFINITY : one;     // without the taken token
+  float taken = 0.f, advantage = 0.f, old = 0.f, ref = 0.f;
+  if (warp == 0) {                                       // before anything is written: dz may be z
+    taken = as_float(z[id]);
+    if (a.advantage) advantage = a.advantage[row];
+    if (a.old) old = a.old[row];
+    if (a.ref) ref = a.ref[row];
+  }
+  float m, s;
+  if (KEPT) {
+    if (n) lost = !arrive();
+    uint4* kept = reinterpret_cast<uint4*>(policy_smem);
+    if (vec >= 0 && vec % threads == tid) {              // a vector that this thread alone reads
+      uint4 v = kept[vec];
+      hide_element(v, element, z);
+      kept[vec] = v;
+    }
+    auto load = [&](int i) { return kept[i]; };
+    m = open;
+    policy_each<POLICY_U>(n, tid, threads, load, [&](int, uint4 w) { m = largest_of(w, m, z); });
+    m = warp_max_fast(m);                                // one shift for the warp
+    s = 0.f;
+    if (m != -INFINITY) {
+      const Shift mine(m, c);
+      f2 e = f2_of(ex2(mine(open, c)), 0.f);
+      auto add = [&](auto far) {
+        policy_each<POLICY_U>(n, tid, threads, load, [&](int, uint4 w) {
+          float f[V::N];
+          V::unpack(w, f);
+          distill_powers<V::N, decltype(far)::value, false>(f, mine, c);
+#pragma unroll
+          for (int i = 0; i < V::N; i += 2) e = add2(e, f2_of(f[i], f[i + 1]));
+        });
+      };
+      if (mine.b != 0.f) add(std::true_type());
+      else add(std::false_type());
+      s = warp_sum(sum2(e));
+    }
+    if (lost) m = s = NOT_A_NUMBER;
+  } else {
+    const uint4* v = reinterpret_cast<const uint4*>(z + sl.body);
+    m = -INFINITY;
+    s = 0.f;
+    distill_take(m, s, open, c);
+    policy_each<POLICY_U>(n, tid, threads, [&](int i) { return v[i]; }, [&](int i, uint4 w) {
       if (i == vec) hide_element(w, element, z);
+      float f[V::N];
+      V::unpack(w, f);
+      distill_take<T>(m, s, f, c);
     });
     join_warp(m, s, c);
-    begun_wait(parts);
-    if (lane < parts) *cluster.map_shared_rank(&sums[part * warps + warp], lane) = make_float2(m, s);
-    if (parts > 1) {
-      row_arrive(parts, true);
-      row_wait(parts, true);
-    } else {
-      __syncthreads();
-    }
-    join_sums(sums, parts * warps, m, s, c);
+  }
+  if (lane == 0) own[warp] = make_float2(m, s);
+  __syncthreads();
+  begun_wait(parts);
+  if (warp == 0) {
+    join_sums(own, warps, m, s, c);
+    if (lane < parts) *cluster.map_shared_rank(&sums[part], lane) = make_float2(m, s);
+  }
+  if (parts > 1) {
+    row_arrive(parts, true);
+    row_wait(parts, true);
+  }
+  if (warp == 0) {
+    __syncwarp();
+    join_sums(sums, parts, m, s, c);
     const float M = max_nan(m, taken);
-    shift = Shift(M, c);
-    rest = m == M ? s : s * ex2(shift.from(Shift(m, c), c));
-    const float mine = ex2(shift(taken, c));
-    total = rest + mine;
-    logp = taken >= m ? -log1pf(rest / mine) : fmaf(shift(taken, c), LN2, -logf(total));
-    rest /= total;
+    const Shift shift(M, c);
+    const float rest = m == M ? s : s * ex2(shift.from(Shift(m, c), c)), mine = ex2(shift(taken, c)), total = rest + mine;
+    const float logp = taken >= m ? -log1pf(rest / mine) : fmaf(shift(taken, c), LN2, -logf(total));
+    float slope = 0.f, loss = 0.f;
     if (a.advantage) {
       const float ratio = a.old ? expf(logp - old) : logp != logp ? logp : 1.0f;   // what is not a number shows
       const float free = ratio * advantage, held = fminf(fmaxf(ratio, 1.0f - a.low), 1.0f + a.high) * advantage;
@@ -114,17 +239,32 @@ __global__ void __launch_bounds__(DISTILL_THREADS, 2) policy_kernel(PolicyArgs a
       loss *= weight;
       slope *= weight / a.tau;
     }
-  } else {
-    begun_wait(parts);
-  }
-  if (part == 0 && tid == 0) {
-    if (a.loss) a.loss[row] = loss;
-    if (a.logp) a.logp[row] = logp;
+    if (lane == 0) {
+      if (part == 0 && a.loss) a.loss[row] = loss;
+      if (part == 0 && a.logp) a.logp[row] = logp;
+      result = {shift.b, shift.k, -slope / total, slope * (rest / total)};
+    }
   }
   if (!a.dz) return;
-  x.store(z, dz, sl, tid, threads, reads, shift, c, -slope / total);
-  // its own store after the vector's, by the same thread
-  if (reads && (vec >= 0 ? vec % threads == tid : x.at == id)) set_float(dz + id, slope * rest);
+  __syncthreads();
+  const PolicyRow r = result;
+  Shift shift(0.f, c);
+  shift.b = r.b;
+  shift.k = r.k;
+  auto write = [&](auto rare) {
+    auto load = [&](int i) { return KEPT ? reinterpret_cast<const uint4*>(policy_smem)[i] : reinterpret_cast<const uint4*>(z + sl.body)[i]; };
+    policy_each<POLICY_U>(n, tid, threads, load, [&](int i, uint4 w) {
+      float f[V::N];
+      V::unpack(w, f);
+      distill_dense<T>(f, shift, c, r.g, decltype(rare)::value);
+      put(i, V::pack(f));
+    });
+  };
+  if (shift.b != 0.f || fabsf(r.g) > 1e6f) write(std::true_type());
+  else write(std::false_type());
+  if (single >= 0) set_float(dz + single, r.g * ex2(shift(one, c)));
+  // the taken token's, after the vector that it lies in, by the same thread
+  if (vec >= 0 ? vec % threads == tid : single == id) set_float(dz + id, r.taken);
 }
 
 }  // namespace precond

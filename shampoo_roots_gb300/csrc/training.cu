@@ -61,6 +61,12 @@ int64_t layer_norm_blocks(const RowShape& s, int64_t rows, int dtype, bool vec, 
 int64_t layer_grad_blocks(const RowShape& s, int64_t rows, int dtype, int sms, const int* clusters) {
   return row_blocks_of(s, rows, dtype == PRECOND_F32 ? 384 : 512, sms, clusters);
 }
+// Rows of a gradient's block: as many as an SM's registers hold, for each block leaves sums of dw and db (777 x 1000 fp32).
+RowShape layer_grad_shape(int64_t cols, int dtype, bool vec) {
+  RowShape s = row_shape(cols, dtype, true, vec);
+  if (s.parts == 1 && s.threads >= 32) s.rows = std::min(8, std::max(1, (dtype == PRECOND_F32 ? 384 : 512) / s.threads));
+  return s;
+}
 template <typename T, bool VEC>
 cudaError_t launch_layer_norm(const LayerNormArgs& a, const RowShape& s, unsigned grid, cudaStream_t st) {
   typedef LayerKernels<T, VEC> K;
@@ -72,77 +78,147 @@ cudaError_t launch_layer_grad(const LayerGradArgs& a, const RowShape& s, unsigne
   return launch(K::grad(s), dim3(grid * std::max(1, s.parts)), dim3(s.threads, s.rows), K::grad_bytes(s), st, std::max(1, s.parts), a);
 }
 
+// Rows through shared memory: threads of a row, rows of a block, rows of each in the ring (0: not this way).  For rows of
+// more than 256 columns, whole 16-byte vectors, enough of them that a group has its second one.  (Norm of 8192 x 6144
+// bf16 56 us, with the next row in registers 63; of 20000 x 1024 27 and 38; gradients of 16384 x 4096 92 and 97.)
+// Vectors a thread, of a norm: one where that fills the block with threads (8192 x 6144 bf16: 56 us, with two 63; 10000 x
+// 4096 fp32 53 and 60) or rows are short, else two or four, whose groups are more (6000 x 8192 bf16: 66, 60 and 62;
+// 4000 x 12288: 57, 57 and 52).
+constexpr int STREAM_BYTES = 225 << 10;
+struct StreamKernels { void (*norm[3])(LayerNormArgs, int); void (*grad)(LayerGradArgs, int); };    // norm: 1, 2, 4 vectors
+template <typename T>
+StreamKernels stream_kernels() {
+  return {{layer_norm_stream_kernel<T, 1>, layer_norm_stream_kernel<T, 2>, layer_norm_stream_kernel<T, 4>}, layer_grad_stream_kernel<T>};
+}
+struct StreamShape { int threads, rows, vectors, stages; size_t bytes; };
+StreamShape stream_shape(int64_t cols, int dtype, int inputs, bool grad, int64_t rows, int sms) {
+  StreamShape s = {0, 0, 1, 0, 0};
+  const int64_t n = (cols + 15) / 16, row = cols * (int64_t)size_of(dtype);
+  if (n <= 16 || row % 16 || n > (grad ? 512 : 1024)) return s;
+  if (!grad && dtype == PRECOND_F32 && n > 768) s.vectors = 2;
+  if (!grad && dtype == PRECOND_BF16 && n > 200) s.vectors = n > 512 ? 4 : n > 352 && n <= 384 ? 1 : 2;
+  const int most = grad ? 512 : STREAM_THREADS[s.vectors];
+  s.threads = (int)((n + 32 * s.vectors - 1) / (32 * s.vectors) * 32);
+  s.rows = std::max(1, std::min(most / s.threads, s.threads > 32 ? 15 : 16));
+  if (rows <= (int64_t)s.rows * sms) return s;
+  const size_t table = (size_t)s.threads * (grad ? 64 : s.vectors * 128);
+  while (s.stages < 8 && table + s.rows * RowRing::size(s.stages + 1, inputs, (int)row) <= STREAM_BYTES) ++s.stages;
+  if (s.stages < 2) s.stages = 0;
+  s.bytes = table + std::max(s.rows * RowRing::size(s.stages, inputs, (int)row), grad && s.rows > 1 ? (size_t)s.threads * s.rows * 128 : 0);
+  return s;
+}
+
 // ------------------------------------------------------------------------- policy loss
 typedef void (*PolicyKernel)(PolicyArgs);
-const PolicyKernel policy_kernels[2][5] = {
-    {policy_kernel<float, 0>, policy_kernel<float, 1>, policy_kernel<float, 2>, policy_kernel<float, 4>, policy_kernel<float, 8>},
-    {policy_kernel<__nv_bfloat16, 0>, policy_kernel<__nv_bfloat16, 1>, policy_kernel<__nv_bfloat16, 2>, policy_kernel<__nv_bfloat16, 4>,
-     policy_kernel<__nv_bfloat16, 8>}};
+const PolicyKernel policy_kernels[2][2] = {{policy_kernel<float, false>, policy_kernel<float, true>},
+                                           {policy_kernel<__nv_bfloat16, false>, policy_kernel<__nv_bfloat16, true>}};
+// Blocks of a row and threads of a block.  A part takes at most what lets an SM hold three blocks (8192 x 131072 bf16 by
+// parts of 64 KB 673 us, of 32 KB 707, of 128 KB 893; 1900 x 151936 by 74 KB 188, by 37 KB 199); a few rows take more
+// blocks, each with at least 8192 logits.  Threads have 192 bytes each, up to 256 of them (8192 x 8000 bf16, 16 KB: 96
+// threads 45 us, 128 47, 256 62, 512 99; 2999 x 50001: 256 threads 98 us, 512 118); a block alone on its SM 32 bytes.
+struct PolicyShape { int parts, threads, bytes; };   // bytes: of a part in shared memory, or 0: rows read twice
+PolicyShape policy_shape(int64_t rows, int64_t vocab, int dtype) {
+  const int64_t sz = (int64_t)size_of(dtype), third = 76288;
+  int parts = 1;
+  auto bytes = [&]() { return ((vocab + parts - 1) / parts + 63) / 64 * 64 * sz; };
+  while (parts < 8 && (bytes() > third || (rows * parts < 2 * PLAN_SMS && vocab / (parts * 2) >= 8192))) parts *= 2;
+  const int64_t each = bytes();
+  const bool alone = rows * parts <= PLAN_SMS;
+  const int threads = (int)std::min<int64_t>(alone ? 512 : 256, std::max<int64_t>(64, (each / (alone ? 32 : 192) + 31) / 32 * 32));
+  return {parts, threads, each <= POLICY_PART ? (int)each : 0};
+}
 
 // ------------------------------------------------------------------------- lists of tensors
-constexpr int CLIP_FEW = 32, CLIP_SOME = 224, CLIP_MANY = 1400;    // tensors of a launch: 0.7, 4.5 and 28 KB of parameters
+// Tensors of a launch: tables of 0.6, 2.5, 10 and 28 KB of parameters.
+constexpr int CLIP_SIZES[4] = {32, 128, 512, 1400};
 constexpr int CLIP_BLOCKS = 2 * PLAN_SMS;
+constexpr int CLIP_SHORT = 128;                      // pieces of a list that one cluster takes (1 MB: two launches 7.1 us, one 7.2; 128 KB 7.2 and 6.0)
 
+struct ClipKernels { const void *norm, *scale, *one; };
+template <int MAX>
+ClipKernels clip_kernels() {
+  return {(const void*)clip_norm_kernel<MAX>, (const void*)clip_scale_kernel<MAX>, (const void*)clip_short_kernel<MAX>};
+}
+const ClipKernels clip_of[4] = {clip_kernels<32>(), clip_kernels<128>(), clip_kernels<512>(), clip_kernels<1400>()};
+
+// Tensors and the tables of their launches.
 struct List {
   std::vector<ClipTensor> tensors;                   // without the empty ones
   std::vector<Range> ranges;                         // of those, by address
-  int64_t launches() const { return std::max<int64_t>(1, ((int64_t)tensors.size() + CLIP_MANY - 1) / CLIP_MANY); }
-  int64_t bytes() const { return launches() * CLIP_BLOCKS * 8; }
+  int size = 0;                                      // which of CLIP_SIZES
+  std::vector<std::vector<char>> tables;
+  std::vector<int64_t> pieces;                       // of each
+  int64_t bytes() const { return std::max<int64_t>(1, (int64_t)tables.size()) * CLIP_BLOCKS * (int64_t)sizeof(ClipSum); }
   bool meets(const Range& r) const {
     if (!r.lo) return false;
     auto at = std::lower_bound(ranges.begin(), ranges.end(), r, [](const Range& a, const Range& b) { return a.hi <= b.lo; });
     return at != ranges.end() && at->lo < r.hi;
   }
+  template <int MAX>
+  void fill() {
+    for (size_t from = 0; from < tensors.size(); from += MAX) {
+      tables.emplace_back(sizeof(ClipTable<MAX>));
+      ClipTable<MAX>& t = *reinterpret_cast<ClipTable<MAX>*>(tables.back().data());
+      t.count = (int)std::min<size_t>(MAX, tensors.size() - from);
+      uint32_t n = 0;
+      for (int i = 0; i < t.count; ++i) {
+        t.tensor[i] = tensors[from + i];
+        t.first[i] = n;
+        n += (uint32_t)ClipView(t.tensor[i]).pieces();
+      }
+      t.first[t.count] = n;
+      pieces.push_back(n);
+    }
+  }
+  void make_tables() {
+    while (size < 3 && tensors.size() > (size_t)CLIP_SIZES[size]) ++size;
+    if (size == 0) fill<CLIP_SIZES[0]>();
+    else if (size == 1) fill<CLIP_SIZES[1]>();
+    else if (size == 2) fill<CLIP_SIZES[2]>();
+    else fill<CLIP_SIZES[3]>();
+  }
+  bool is_short() const { return tables.size() == 1 && pieces[0] <= CLIP_SHORT; }
 };
 
-template <int MAX>
-int64_t fill_table(const List& l, size_t from, ClipTable<MAX>& t) {
-  t.count = (int)std::min<size_t>(MAX, l.tensors.size() - from);
-  uint32_t pieces = 0;
-  for (int i = 0; i < t.count; ++i) {
-    t.tensor[i] = l.tensors[from + i];
-    t.first[i] = pieces;
-    pieces += (uint32_t)ClipView(t.tensor[i]).pieces();
-  }
-  t.first[t.count] = pieces;
-  return pieces;
+int launch_list(Handle* h, const void* kernel, int grid, int cluster, void** args, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(CLIP_THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  cfg.numAttrs = launch_attributes(at, cluster);
+  cfg.attrs = at;
+  OP_CK(cudaLaunchKernelExC(&cfg, kernel, args));       // the table is copied once, from the list
+  ++h->launches;
+  return PRECOND_OK;
 }
-// The sums of squares of a list, a launch for up to CLIP_MANY tensors; *sums: how many.
-template <int MAX>
-int launch_squares(Handle* h, const List& l, double* partial, int* sums, cudaStream_t st) {
-  ClipTable<MAX> t;
+int clip_grid(const Handle* h, int64_t pieces) { return (int)std::min<int64_t>((pieces + 3) / 4, std::min(CLIP_BLOCKS, 2 * h->num_sms)); }
+// The sums of squares of a list; *sums: how many.
+int squares(Handle* h, const List& l, ClipSum* partial, int* sums, cudaStream_t st) {
   *sums = 0;
-  for (size_t from = 0; from < l.tensors.size(); from += MAX) {
-    const int grid = (int)std::min<int64_t>(fill_table(l, from, t), std::min(CLIP_BLOCKS, 2 * h->num_sms));
-    OP_CK(launch(clip_norm_kernel<MAX>, dim3(grid), dim3(CLIP_THREADS), 0, st, 1, t, partial + *sums));
-    ++h->launches;
+  for (size_t i = 0; i < l.tables.size(); ++i) {
+    ClipSum* at = partial + *sums;
+    void* args[] = {(void*)l.tables[i].data(), &at};
+    const int grid = clip_grid(h, l.pieces[i]), rc = launch_list(h, clip_of[l.size].norm, grid, 1, args, st);
+    if (rc) return rc;
     *sums += grid;
   }
   return PRECOND_OK;
 }
-template <int MAX>
-int launch_scale(Handle* h, const List& l, const double* partial, int sums, float max_norm, float* norm, cudaStream_t st) {
-  ClipTable<MAX> t;
-  for (size_t from = 0; from < l.tensors.size(); from += MAX) {
-    const int grid = (int)std::min<int64_t>(fill_table(l, from, t), std::min(CLIP_BLOCKS, 2 * h->num_sms));
-    // the first launch leaves the norm, the others (and a caller's norm) find it
-    OP_CK(launch(clip_scale_kernel<MAX>, dim3(grid), dim3(CLIP_THREADS), 0, st, 1, t, partial, from ? 0 : sums, max_norm, norm));
-    ++h->launches;
+int scale(Handle* h, const List& l, const ClipSum* partial, int sums, float max_norm, float* norm, cudaStream_t st) {
+  for (size_t i = 0; i < l.tables.size(); ++i) {
+    int mine = i ? 0 : sums;                            // the first launch leaves the norm, the others (and a caller's norm) find it
+    void* args[] = {(void*)l.tables[i].data(), &partial, &mine, &max_norm, &norm};
+    const int rc = launch_list(h, clip_of[l.size].scale, clip_grid(h, l.pieces[i]), 1, args, st);
+    if (rc) return rc;
   }
   return PRECOND_OK;
 }
-int squares(Handle* h, const List& l, double* partial, int* sums, cudaStream_t st) {
-  const size_t n = l.tensors.size();
-  return n <= CLIP_FEW ? launch_squares<CLIP_FEW>(h, l, partial, sums, st)
-         : n <= CLIP_SOME ? launch_squares<CLIP_SOME>(h, l, partial, sums, st) : launch_squares<CLIP_MANY>(h, l, partial, sums, st);
+int short_list(Handle* h, const List& l, float max_norm, float* norm, cudaStream_t st) {
+  void* args[] = {(void*)l.tables[0].data(), &max_norm, &norm};
+  return launch_list(h, clip_of[l.size].one, CLIP_CLUSTER, CLIP_CLUSTER, args, st);
 }
-int scale(Handle* h, const List& l, const double* partial, int sums, float max_norm, float* norm, cudaStream_t st) {
-  const size_t n = l.tensors.size();
-  return n <= CLIP_FEW ? launch_scale<CLIP_FEW>(h, l, partial, sums, max_norm, norm, st)
-         : n <= CLIP_SOME ? launch_scale<CLIP_SOME>(h, l, partial, sums, max_norm, norm, st)
-                          : launch_scale<CLIP_MANY>(h, l, partial, sums, max_norm, norm, st);
-}
-int total(Handle* h, const double* partial, int sums, float* norm, cudaStream_t st) {
+int total(Handle* h, const ClipSum* partial, int sums, float* norm, cudaStream_t st) {
   OP_CK(launch(clip_total_kernel<0>, dim3(1), dim3(CLIP_THREADS), 0, st, 1, partial, sums, norm));
   ++h->launches;
   return PRECOND_OK;
@@ -164,6 +240,12 @@ cudaError_t precond::training_attributes() {
   if (e == cudaSuccess) e = LayerKernels<float, false>::attributes();
   if (e == cudaSuccess) e = LayerKernels<__nv_bfloat16, true>::attributes();
   if (e == cudaSuccess) e = LayerKernels<__nv_bfloat16, false>::attributes();
+  for (const StreamKernels& k : {stream_kernels<float>(), stream_kernels<__nv_bfloat16>()}) {
+    for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = cudaFuncSetAttribute(k.norm[i], cudaFuncAttributeMaxDynamicSharedMemorySize, STREAM_BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k.grad, cudaFuncAttributeMaxDynamicSharedMemorySize, STREAM_BYTES);
+  }
+  for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+    e = cudaFuncSetAttribute(policy_kernels[i][1], cudaFuncAttributeMaxDynamicSharedMemorySize, POLICY_PART);
   return e;
 }
 
@@ -204,6 +286,12 @@ int precond_layer_norm(precond_t ph, const void* x, const void* residual, const 
                      eps, weight_dtype == PRECOND_BF16};
   const bool vec = sector_rows(x, ldx, dtype) && sector_rows(residual, ldr, dtype) && sector_rows(total, ldt, dtype) &&
                    sector_rows(y, ldy, dtype);
+  const StreamShape f = vec ? stream_shape(cols, dtype, residual ? 2 : 1, false, rows, h->num_sms) : StreamShape{};
+  if (f.stages) {
+    OP_CK(launch((dtype == PRECOND_BF16 ? stream_kernels<__nv_bfloat16>() : stream_kernels<float>()).norm[f.vectors / 2], dim3((unsigned)h->num_sms), dim3(f.threads, f.rows), f.bytes, (cudaStream_t)stream, 1, a, f.stages));
+    ++h->launches;
+    return PRECOND_OK;
+  }
   const RowShape s = row_shape(cols, dtype, false, vec);
   const unsigned grid = (unsigned)layer_norm_blocks(s, q ? q8_row_blocks(rows) * 128 : rows, dtype, vec, h->num_sms, h->clusters);
   cudaStream_t st = (cudaStream_t)stream;
@@ -219,9 +307,9 @@ int64_t precond_layer_norm_grad_workspace(int64_t rows, int64_t cols) {
   if (!side(rows) || !side(cols)) return -1;
   if (rows == 0 || cols == 0) return 0;
   // of either type; rows in parts of a warp, and clusters that do not fit, only make fewer
-  int64_t blocks = 0;
+  int64_t blocks = std::min<int64_t>(rows, PLAN_SMS);    // rows through shared memory: a block an SM
   for (const int dtype : {PRECOND_BF16, PRECOND_F32})
-    blocks = std::max(blocks, layer_grad_blocks(row_shape(cols, dtype, true, false), rows, dtype, PLAN_SMS, PLAN_CLUSTERS));
+    blocks = std::max(blocks, layer_grad_blocks(layer_grad_shape(cols, dtype, false), rows, dtype, PLAN_SMS, PLAN_CLUSTERS));
   return blocks * cols * 8;
 }
 
@@ -267,9 +355,15 @@ int precond_layer_norm_grad(precond_t ph, const void* dy, const void* x, const v
                      weight_dtype == PRECOND_BF16};
   const bool vec = sector_rows(dy, lddy, dtype) && sector_rows(x, ldx, dtype) && sector_rows(dresidual, lddr, dtype) &&
                    sector_rows(dx, lddx, dtype);
-  const RowShape s = row_shape(cols, dtype, true, vec);
-  const unsigned grid = (unsigned)layer_grad_blocks(s, rows, dtype, std::min(h->num_sms, PLAN_SMS), h->clusters);
-  if (dtype == PRECOND_BF16)
+  const RowShape s = layer_grad_shape(cols, dtype, vec);
+  const int sms = std::min(h->num_sms, PLAN_SMS);
+  unsigned grid = (unsigned)layer_grad_blocks(s, rows, dtype, sms, h->clusters);
+  const StreamShape f = vec ? stream_shape(cols, dtype, dresidual ? 3 : 2, true, rows, sms) : StreamShape{};
+  if (f.stages) {
+    grid = (unsigned)sms;                // the rows' shapes have at least as many groups
+    OP_CK(launch(dtype == PRECOND_BF16 ? layer_grad_stream_kernel<__nv_bfloat16> : layer_grad_stream_kernel<float>, dim3(grid),
+                 dim3(f.threads, f.rows), f.bytes, st, 1, a, f.stages));
+  } else if (dtype == PRECOND_BF16)
     OP_CK((vec ? launch_layer_grad<__nv_bfloat16, true>(a, s, grid, st) : launch_layer_grad<__nv_bfloat16, false>(a, s, grid, st)));
   else
     OP_CK((vec ? launch_layer_grad<float, true>(a, s, grid, st) : launch_layer_grad<float, false>(a, s, grid, st)));
@@ -313,9 +407,9 @@ int precond_policy(precond_t ph, const void* logits, int dtype, int64_t rows, in
   if (rc) return rc;
   const PolicyArgs a = {logits, ldz, ids, id_bits == 64, advantage, old_logp, kl != 0.f ? ref_logp : nullptr, weight, loss, logp, dlogits,
                         lddz, rows, vocab, temperature, clip_low, clip_high, kl};
-  const LogitShape s = logit_shape(rows, vocab, dtype);
-  OP_CK(launch(policy_kernels[dtype == PRECOND_BF16][s.kernel], dim3((unsigned)(rows * s.parts)), dim3(s.threads), 0, (cudaStream_t)stream,
-               s.parts, a));
+  const PolicyShape s = policy_shape(rows, vocab, dtype);
+  OP_CK(launch(policy_kernels[dtype == PRECOND_BF16][s.bytes > 0], dim3((unsigned)(rows * s.parts)), dim3(s.threads), (size_t)s.bytes,
+               (cudaStream_t)stream, s.parts, a));
   ++h->launches;
   return PRECOND_OK;
 }
@@ -341,6 +435,7 @@ int precond_list_create(precond_list_t* out, int count, void* const tensors[], c
     std::sort(l.ranges.begin(), l.ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
     for (size_t i = 1; i < l.ranges.size(); ++i)
       if (l.ranges[i].lo < l.ranges[i - 1].hi) return PRECOND_EINVAL;     // one tensor over another would be scaled twice
+    l.make_tables();
     *out = reinterpret_cast<precond_list_t>(new List(std::move(l)));
   } catch (const std::bad_alloc&) {
     return PRECOND_ENOMEM;
@@ -366,7 +461,8 @@ int precond_grad_norm(precond_t ph, precond_list_t list, float* norm, void* work
   int rc = prepare(h), sums = 0;
   if (rc) return rc;
   cudaStream_t st = (cudaStream_t)stream;
-  double* partial = reinterpret_cast<double*>(workspace);
+  ClipSum* partial = reinterpret_cast<ClipSum*>(workspace);
+  if (l->is_short()) return short_list(h, *l, INFINITY, norm, st);
   if ((rc = squares(h, *l, partial, &sums, st))) return rc;
   return ::total(h, partial, sums, norm, st);
 }
@@ -380,7 +476,8 @@ int precond_clip_grads(precond_t ph, precond_list_t list, float max_norm, float*
   int rc = prepare(h), sums = 0;
   if (rc) return rc;
   cudaStream_t st = (cudaStream_t)stream;
-  double* partial = reinterpret_cast<double*>(workspace);
+  ClipSum* partial = reinterpret_cast<ClipSum*>(workspace);
+  if (!given && l->is_short()) return short_list(h, *l, max_norm, norm, st);
   if (!given && (rc = squares(h, *l, partial, &sums, st))) return rc;
   if (!given && l->tensors.empty()) return ::total(h, partial, 0, norm, st);
   return scale(h, *l, partial, sums, max_norm, norm, st);

@@ -230,6 +230,27 @@ def test_grad_against_differences(pc):
             assert abs(float((got.cpu().double() * k).sum()) - want) <= 1e-4
 
 
+@pytest.mark.parametrize("rows,cols,dtype,pitch", [(700, 6144, "bf16", 0), (2600, 1000, "bf16", 0), (5000, 264, "bf16", 0), (2450, 512, "f32", 0),
+                                                   (400, 16384, "bf16", 0), (310, 8200, "bf16", 8), (333, 9004, "f32", 4), (1000, 4104, "f32", 8),
+                                                   (2000, 1208, "bf16", 24), (320, 12288, "bf16", 0), (1500, 2052, "f32", 12)])
+def test_norm_many_rows(pc, rows, cols, dtype, pitch):
+    """Enough rows for each group of threads to have several: rows copied through shared memory, more than its ring holds."""
+    check_norm(pc, rows, cols, dtype, pitch=pitch)
+    check_norm(pc, rows, cols, dtype, wtype="bf16", residual=False, pitch=pitch, offset=3.0)
+
+
+@pytest.mark.parametrize("rows,cols,dtype,pitch", [(700, 4096, "bf16", 0), (2600, 1000, "bf16", 0), (2700, 264, "bf16", 0), (2450, 512, "f32", 0),
+                                                   (400, 8192, "bf16", 0), (333, 6148, "f32", 4), (1000, 3004, "f32", 4), (2000, 1208, "bf16", 24),
+                                                   (200, 8192, "f32", 0), (3000, 2056, "bf16", 8)])
+def test_grad_many_rows(pc, rows, cols, dtype, pitch):
+    check_grad(pc, rows, cols, dtype, True, pitch=pitch)
+    c = check_grad(pc, rows, cols, dtype, False, pitch=pitch)
+    d = {k: c[k].cuda() for k in ("x", "dy", "w", "mean", "rstd")}
+    dw = torch.empty(cols, device="cuda")
+    sr.precond_layer_norm_grad(pc.h, d["dy"], d["x"], d["w"], d["mean"], d["rstd"], d["dy"], dw)
+    assert torch.equal(d["dy"], c["dx"]) and (pitch or torch.equal(dw, c["dw"]))
+
+
 def test_empty_and_streams(pc):
     """No rows and no columns; another stream; a captured call replayed on new values."""
     w = torch.ones(64, device="cuda")
