@@ -16,7 +16,7 @@ typedef struct {
 
 enum { T_F32, T_BF16, T_E4M3, T_E8M0, T_U8, T_I32, T_I64, T_COUNT };
 static PyObject* dtypes[T_COUNT];
-static PyObject *s_shape, *s_stride, *s_data_ptr, *s_dtype, *s_get_device, *s_new_empty, *raw_stream;
+static PyObject *s_shape, *s_stride, *s_is_contiguous, *s_data_ptr, *s_dtype, *s_get_device, *s_new_empty, *raw_stream;
 static PyObject *raw_alloc, *raw_delete, *current_device;   /* torch's allocator, NULL where it cannot be had so */
 enum { E_NORM, E_GRAD, E_GRAD_WS, E_QUANTIZE, E_GEMM, E_DISTILL, E_DISTILL_WS, E_LAYER, E_LAYER_GRAD, E_LAYER_GRAD_WS, E_POLICY,
        E_LIST, E_LIST_END, E_LIST_WS, E_GRAD_NORM, E_CLIP, E_COUNT };
@@ -46,20 +46,20 @@ static int get_as(PyObject* t, const char* what, Tensor* o, int any) {
     n *= size[i];
   }
   Py_DECREF(v);
-  if (!(v = PyObject_CallMethodNoArgs(t, s_stride))) return -1;
-  int64_t want = 1;
-  o->contiguous = 1;
-  for (int i = o->dim - 1; i >= 0; --i) {
-    step[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(v, i));
-    if (size[i] != 1 && step[i] != want && n) o->contiguous = 0;
-    want *= size[i];
+  o->contiguous = 0;
+  if (o->dim != 2 || any) {     /* the strides themselves are asked for where they count: of matrices, and of what has gaps */
+    if (!(v = PyObject_CallMethodNoArgs(t, s_is_contiguous))) return -1;
+    o->contiguous = v == Py_True;
+    Py_DECREF(v);
   }
-  Py_DECREF(v);
   o->dense = o->contiguous;
-  if (!o->dense) {              /* the dimensions by their strides: each as long as those within it */
-    int used = 0;
+  if (!o->contiguous && (o->dim == 2 || any)) {
+    if (!(v = PyObject_CallMethodNoArgs(t, s_stride))) return -1;
+    for (int i = 0; i < o->dim; ++i) step[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(v, i));
+    Py_DECREF(v);
+    int used = 0;               /* the dimensions by their strides: each as long as those within it */
     int64_t inner = 1;
-    for (int found = 1; found;) {
+    for (int found = any; found;) {
       found = 0;
       for (int i = 0; i < o->dim; ++i)
         if (!(used >> i & 1) && size[i] != 1 && step[i] == inner) {
@@ -68,7 +68,9 @@ static int get_as(PyObject* t, const char* what, Tensor* o, int any) {
           found = 1;
         }
     }
-    o->dense = inner == n;
+    o->dense = any && inner == n;
+    if (!any)
+      o->contiguous = o->dense = n == 0 || ((size[1] == 1 || step[1] == 1) && (size[0] == 1 || step[0] == size[1]));
   }
   if (!(v = PyObject_CallMethodNoArgs(t, s_data_ptr))) return -1;
   o->p = PyLong_AsVoidPtr(v);
@@ -610,6 +612,7 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1,
 
 PyMODINIT_FUNC PyInit__binding(void) {
   if (!(s_shape = PyUnicode_InternFromString("shape")) || !(s_stride = PyUnicode_InternFromString("stride")) ||
+      !(s_is_contiguous = PyUnicode_InternFromString("is_contiguous")) ||
       !(s_data_ptr = PyUnicode_InternFromString("data_ptr")) || !(s_dtype = PyUnicode_InternFromString("dtype")) ||
       !(s_get_device = PyUnicode_InternFromString("get_device")) || !(s_new_empty = PyUnicode_InternFromString("new_empty")))
     return NULL;
