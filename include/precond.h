@@ -451,13 +451,13 @@ int precond_layer_norm(precond_t h, const void* x, const void* residual, const v
  *   dx         : in dtype; may be dy, dresidual or x themselves where cols <= 32768
  *   dw, db     : cols floats each; db may be NULL
  *   workspace  : precond_layer_norm_grad_workspace(rows, cols) bytes, 16-byte aligned, in use until the call's work
- *                has completed
+ *                has completed; may be NULL where that is 0 (few rows)
  */
 int precond_layer_norm_grad(precond_t h, const void* dy, const void* x, const void* weight, const float* mean,
                             const float* rstd, const void* dresidual, int dtype, int weight_dtype, int64_t rows,
                             int64_t cols, int64_t lddy, int64_t ldx, int64_t lddr, void* dx, int64_t lddx, float* dw,
                             float* db, void* workspace, int64_t workspace_bytes, void* stream);
-int64_t precond_layer_norm_grad_workspace(int64_t rows, int64_t cols);   /* -1: bad sizes */
+int64_t precond_layer_norm_grad_workspace(int64_t rows, int64_t cols);   /* 0 for few rows; -1: bad sizes */
 
 /*
  * Clipped policy loss of every row's taken token and, with `dlogits`, its gradient:

@@ -80,34 +80,47 @@ __device__ __forceinline__ void clip_store(char* p, const uint32_t (&w)[8]) {
                ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
 }
 
-// Calls f(tensor, first sector of the piece, whether the piece begins it, whether it stays in L2) for each of a warp's
-// pieces; `back`: from the last one.  A block's pieces are consecutive, its warps take every 16th of them.  A tensor's
-// single elements go with its first piece.
-template <int MAX, typename F>
-__device__ __forceinline__ void clip_walk(const ClipTable<MAX>& t, bool back, F f) {
-  const int64_t all = t.first[t.count], lo = all * blockIdx.x / gridDim.x, hi = all * (blockIdx.x + 1) / gridDim.x;
-  // the last of every block's pieces, of all blocks' together what L2 may keep
-  const int64_t keep = hi - (hi - lo) * min(all, (int64_t)CLIP_KEPT) / all;
-  int64_t at = back ? hi - 1 - (threadIdx.x >> 5) : lo + (threadIdx.x >> 5);
-  if (at < lo || at >= hi) return;
-  int a = 0, b = t.count - 1;                         // the last tensor that begins at or before this piece
-  while (a < b) {
-    const int m = (a + b + 1) / 2;
-    if ((int64_t)t.first[m] <= at) a = m;
-    else b = m - 1;
+// A warp's pieces of a list: a block's are consecutive, its warps take every 16th of them.  The place in the table is
+// found before the kernel waits for its predecessor.
+struct ClipWalk {
+  int64_t lo, hi, keep, at;                           // the block's pieces; those that L2 may keep; the warp's first
+  int tensor;
+  template <int MAX>
+  __device__ __forceinline__ ClipWalk(const ClipTable<MAX>& t, bool back) {
+    const int64_t all = t.first[t.count];
+    lo = all * blockIdx.x / gridDim.x;
+    hi = all * (blockIdx.x + 1) / gridDim.x;
+    keep = hi - (hi - lo) * min(all, (int64_t)CLIP_KEPT) / all;          // the last of every block's
+    at = back ? hi - 1 - (threadIdx.x >> 5) : lo + (threadIdx.x >> 5);
+    // the last tensor that begins at or before this piece
+    int a = 0, b = t.count - 1;
+    while (a < b) {
+      const int m = (a + b + 1) / 2;
+      if ((int64_t)t.first[m] <= at) a = m;
+      else b = m - 1;
+    }
+    tensor = a;
   }
-  while (true) {
-    const ClipView v(t.tensor[a]);
-    const int64_t p0 = t.first[a], p1 = t.first[a + 1];
-    for (; at >= max(lo, p0) && at < min(hi, p1); at += back ? -CLIP_WARPS : CLIP_WARPS)
-      f(v, (at - p0) * CLIP_PIECE + (threadIdx.x & 31), at == p0, at >= keep);
-    if (at < lo || at >= hi) return;
-    if (back)
-      while ((int64_t)t.first[a] > at) --a;
-    else
-      while ((int64_t)t.first[a + 1] <= at) ++a;
+  // Calls f(tensor, first sector of the piece, whether the piece begins it, whether it stays in L2); `back`: from the last
+  // one.  A tensor's single elements go with its first piece.
+  template <int MAX, typename F>
+  __device__ __forceinline__ void each(const ClipTable<MAX>& t, bool back, F f) const {
+    int64_t i = at;
+    int a = tensor;
+    if (i < lo || i >= hi) return;
+    while (true) {
+      const ClipView v(t.tensor[a]);
+      const int64_t p0 = t.first[a], p1 = t.first[a + 1];
+      for (; i >= max(lo, p0) && i < min(hi, p1); i += back ? -CLIP_WARPS : CLIP_WARPS)
+        f(v, (i - p0) * CLIP_PIECE + (threadIdx.x & 31), i == p0, i >= keep);
+      if (i < lo || i >= hi) return;
+      if (back)
+        while ((int64_t)t.first[a] > i) --a;
+      else
+        while ((int64_t)t.first[a + 1] <= i) ++a;
+    }
   }
-}
+};
 
 // ------------------------------------------------------------- the norm
 __device__ __forceinline__ f2 clip_square(const uint32_t (&w)[8], bool bf16, f2 s) {
@@ -170,9 +183,9 @@ __device__ __forceinline__ ClipSum clip_block_sum(ClipSum v) {
 
 // The sum of the squares of a block's pieces, in thread 0.
 template <int MAX>
-__device__ __forceinline__ ClipSum clip_squares(const ClipTable<MAX>& t) {
+__device__ __forceinline__ ClipSum clip_squares(const ClipTable<MAX>& t, const ClipWalk& walk) {
   ClipSum sum = CLIP_NOTHING;
-  clip_walk(t, false, [&](const ClipView& v, int64_t s, bool begins, bool stays) {
+  walk.each(t, false, [&](const ClipView& v, int64_t s, bool begins, bool stays) {
     const bool bf16 = v.size == 2;
     uint32_t w[CLIP_U][8];
 #pragma unroll
@@ -214,9 +227,10 @@ __device__ __forceinline__ ClipSum clip_squares(const ClipTable<MAX>& t) {
 }
 template <int MAX>
 __global__ void __launch_bounds__(CLIP_THREADS, 2) clip_norm_kernel(const __grid_constant__ ClipTable<MAX> t, ClipSum* partial) {
+  const ClipWalk walk(t, false);
   wait_for_previous();
   let_next_start();
-  const ClipSum sum = clip_squares(t);
+  const ClipSum sum = clip_squares(t, walk);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
@@ -272,8 +286,8 @@ __device__ __forceinline__ void clip_scale(uint32_t (&w)[8], bool bf16, float c)
 }
 
 template <int MAX>
-__device__ __forceinline__ void clip_scale_all(const ClipTable<MAX>& t, float c) {
-  clip_walk(t, true, [&](const ClipView& v, int64_t s, bool begins, bool stays) {
+__device__ __forceinline__ void clip_scale_all(const ClipTable<MAX>& t, const ClipWalk& walk, float c) {
+  walk.each(t, true, [&](const ClipView& v, int64_t s, bool begins, bool stays) {
     const bool bf16 = v.size == 2;
     uint32_t w[CLIP_U][8];
 #pragma unroll
@@ -304,11 +318,12 @@ __device__ __forceinline__ bool clips(float norm, float max_norm) { return norm 
 template <int MAX>
 __global__ void __launch_bounds__(CLIP_THREADS, 2) clip_scale_kernel(const __grid_constant__ ClipTable<MAX> t, const ClipSum* partial, int sums,
                                                                      float max_norm, float* norm) {
+  const ClipWalk walk(t, true);
   wait_for_previous();
   let_next_start();
   const float total = sums ? clip_total(partial, sums) : *norm;
   if (sums && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
-  if (clips(total, max_norm)) clip_scale_all(t, max_norm / total);
+  if (clips(total, max_norm)) clip_scale_all(t, walk, max_norm / total);
 }
 
 // A short list: one cluster.  max_norm infinite: the norm alone.
@@ -319,9 +334,10 @@ __global__ void __launch_bounds__(CLIP_THREADS, 2) clip_short_kernel(const __gri
   __shared__ ClipSum sums[CLIP_CLUSTER];
   cg::cluster_group cluster = cg::this_cluster();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");      // the blocks have begun
+  const ClipWalk walk(t, false);
   wait_for_previous();
   let_next_start();
-  const ClipSum sum = clip_squares(t);
+  const ClipSum sum = clip_squares(t, walk);
   __syncwarp();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (threadIdx.x == 0)
@@ -335,7 +351,7 @@ __global__ void __launch_bounds__(CLIP_THREADS, 2) clip_short_kernel(const __gri
   }
   const float total = v.root();
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
-  if (clips(total, max_norm)) clip_scale_all(t, max_norm / total);
+  if (clips(total, max_norm)) clip_scale_all(t, ClipWalk(t, true), max_norm / total);
 }
 
 }  // namespace precond

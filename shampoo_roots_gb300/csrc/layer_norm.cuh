@@ -38,7 +38,8 @@ struct LayerNormArgs {
 
 struct LayerGradArgs {
   const void* dy; const void* x; const void* dr; const void* w; const float* mean; const float* rstd;
-  void* dx; float* partial;           // partial: [blocks, or clusters][dw, db][cols]
+  void* dx; float* partial;           // partial: [blocks, or clusters][dw, db][columns, padded to 16]
+  float* dw; float* db;               // few rows: the sums themselves, of one block or of one cluster's; else null
   int64_t lddy, ldx, lddr, lddx;
   int rows, cols;
   int w_bf16;
@@ -228,8 +229,8 @@ __global__ void __launch_bounds__(NV == 2 || (sizeof(T) == 2 && !VEC) ? 512 : 38
   if (threadIdx.y == 0) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      table_set(table + j * 8 * bx, bx, load_w16(a.w, a.w_bf16, c[j], a.cols));
-      table_set(table + (j * 8 + 4) * bx, bx, a.b ? load_w16(a.b, a.w_bf16, c[j], a.cols) : zero16());
+      table_set(table + j * 8 * bx, bx, load_w16_wide(a.w, a.w_bf16, c[j], a.cols));
+      table_set(table + (j * 8 + 4) * bx, bx, a.b ? load_w16_wide(a.b, a.w_bf16, c[j], a.cols) : zero16());
     }
     if constexpr (!CLUSTER)
       if (!PART && (tx & 31) == 0) words.columns[tx >> 5] = make_float2((float)mine, mine ? 1.f / (float)mine : 0.f);
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(512, 2) layer_norm_long_kernel(LayerNormArgs a
       load16<VEC>(o, a.r ? h : x, (int)c, a.cols);
       settle<VEC>(o, xs);
       F16 v = unpack(o);
-      const F16 w = load_w16(a.w, a.w_bf16, (int)c, a.cols), b = a.b ? load_w16(a.b, a.w_bf16, (int)c, a.cols) : zero16();
+      const F16 w = load_w16_wide(a.w, a.w_bf16, (int)c, a.cols), b = a.b ? load_w16_wide(a.b, a.w_bf16, (int)c, a.cols) : zero16();
 #pragma unroll
       for (int i = 0; i < 8; ++i) v.p[i] = fma2(mul2(add2(v.p[i], mm), rs), w.p[i], b.p[i]);
       norm_write<T, VEC>(a, row, (int)c, a.cols, v, q8_scale_at(row, (int)(c >> 7), rblocks), xs);
@@ -362,6 +363,52 @@ __global__ void __launch_bounds__(512, 2) layer_norm_long_kernel(LayerNormArgs a
 }
 
 // ------------------------------------------------------------- gradients
+// dw and db of the rows that a block has side by side, added in their order by the threads of the first; through shared
+// memory, 4 columns at a time and thread by thread, so that no bank is met twice.
+__device__ __forceinline__ void join_rows(float4* side, F16& dw, F16& db) {
+  const int bx = blockDim.x, stride = bx * blockDim.y;
+  float4* at = side + threadIdx.x;
+  __syncthreads();                       // what lay there has been read
+  if (threadIdx.y > 0) {
+    table_set(at + threadIdx.y * bx, stride, dw);
+    table_set(at + threadIdx.y * bx + 4 * stride, stride, db);
+  }
+  __syncthreads();
+  if (threadIdx.y == 0)
+    for (int y = 1; y < blockDim.y; ++y) {
+      const F16 w2 = table_get(at + y * bx, stride), b2 = table_get(at + y * bx + 4 * stride, stride);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dw.p[i] = add2(dw.p[i], w2.p[i]);
+        db.p[i] = add2(db.p[i], b2.p[i]);
+      }
+    }
+}
+// The same over the blocks of a cluster: each thread's columns by one of them (`mine`).
+__device__ __forceinline__ void join_blocks(float4* side, F16& dw, F16& db, bool mine) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int bx = blockDim.x, n = (int)cluster.num_blocks();
+  float4* at = side + threadIdx.x;
+  __syncthreads();
+  if (threadIdx.y == 0) {
+    table_set(at, bx, dw);
+    table_set(at + 4 * bx, bx, db);
+  }
+  cluster.sync();
+  if (mine) {
+    dw = db = zero16();
+    for (int k = 0; k < n; ++k) {
+      const float4* other = cluster.map_shared_rank(at, k);
+      const F16 w2 = table_get(other, bx), b2 = table_get(other + 4 * bx, bx);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dw.p[i] = add2(dw.p[i], w2.p[i]);
+        db.p[i] = add2(db.p[i], b2.p[i]);
+      }
+    }
+  }
+  cluster.sync();                        // no block leaves while another may read from it
+}
 struct GradSums { f2 g, gn; };
 // One vector: n = (x - mean) rstd, g = dy w; adds to dw, db and to the row's sums of g and g n.
 __device__ __forceinline__ void layer_terms(F16& g, F16& n, const F16& w, F16& dw, F16& db, f2 minus_mean, f2 rs, GradSums& s) {
@@ -389,13 +436,22 @@ __device__ __forceinline__ void layer_out(Raw16<T>& o, const F16& g, const F16& 
   }
   pack(o, d);
 }
-__device__ __forceinline__ void store_partial(float* out, int c, int cols, const F16& f) {
+__device__ __forceinline__ void store_sums(float* out, int c, int cols, const F16& f) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float2 d = f2_get(f.p[i]);
     if (c + 2 * i < cols) out[c + 2 * i] = d.x;
     if (c + 2 * i + 1 < cols) out[c + 2 * i + 1] = d.y;
   }
+}
+// A block's sums for layer_dw_kernel: whole vectors, 16 bytes at a time.
+__host__ __device__ __forceinline__ int64_t partial_pitch(int64_t cols) { return (cols + 15) / 16 * 16; }
+__device__ __forceinline__ void store_partial(const LayerGradArgs& a, int64_t group, int c, const F16& dw, const F16& db) {
+  if (c >= a.cols) return;
+  const int64_t pitch = partial_pitch(a.cols);
+  float4* out = reinterpret_cast<float4*>(a.partial + group * 2 * pitch + c);
+  table_set(out, 1, dw);
+  table_set(out + pitch / 4, 1, db);
 }
 
 template <typename T, bool VEC, int ROWS>
@@ -435,7 +491,7 @@ __global__ void __launch_bounds__(sizeof(T) == 4 ? 384 : 512, 1) layer_grad_kern
       nrstd = a.rstd[row];
     }
   }
-  if (threadIdx.y == 0) table_set(table, bx, load_w16(a.w, a.w_bf16, c, a.cols));
+  if (threadIdx.y == 0) table_set(table, bx, load_w16_wide(a.w, a.w_bf16, c, a.cols));
   __syncthreads();
   for (unsigned call = 1; row - below < a.rows; row += step, ++call) {
     const f2 rs = f2_of(nrstd, nrstd);
@@ -484,26 +540,20 @@ __global__ void __launch_bounds__(sizeof(T) == 4 ? 384 : 512, 1) layer_grad_kern
     cols = next;
   }
   if (CLUSTER) cluster_leave();
-  if (blockDim.y > 1) {                  // the block's rows side by side: in their order, through shared memory
-    F16* side = reinterpret_cast<F16*>(row_scratch);
-    F16* at = side + (threadIdx.y * bx + tx) * 2;
-    __syncthreads();                     // the table and the exchange buffers lie there too
-    at[0] = dw;
-    at[1] = db;
-    __syncthreads();
-    if (threadIdx.y > 0) return;
-    for (int y = 1; y < blockDim.y; ++y) {
-      const F16* other = side + (y * bx + tx) * 2;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dw.p[i] = add2(dw.p[i], other[0].p[i]);
-        db.p[i] = add2(db.p[i], other[1].p[i]);
-      }
+  float4* side = reinterpret_cast<float4*>(row_scratch);
+  if (blockDim.y > 1) join_rows(side, dw, db);
+  if (!CLUSTER && a.dw) {                // few rows
+    const int n = (int)cg::this_cluster().num_blocks();
+    const bool mine = threadIdx.y == 0 && (tx >> 2) % n == (int)cg::this_cluster().block_rank();   // 64 columns each
+    if (n > 1) join_blocks(side, dw, db, mine);
+    if (mine) {
+      store_sums(a.dw, c, a.cols, dw);
+      if (a.db) store_sums(a.db, c, a.cols, db);
     }
+    return;
   }
-  float* out = a.partial + (int64_t)group * 2 * a.cols;
-  store_partial(out, c, a.cols, dw);
-  store_partial(out + a.cols, c, a.cols, db);
+  if (threadIdx.y > 0) return;
+  store_partial(a, group, c, dw, db);
 }
 
 // Rows too long for registers: the block's dw and db sums live in its rows of `partial` (each thread adds to its own columns).
@@ -514,7 +564,8 @@ __global__ void __launch_bounds__(512, 1) layer_grad_long_kernel(LayerGradArgs a
   wait_for_previous();
   let_next_start();
   void* xs = warp_scratch<T, VEC>();
-  float* out = a.partial + (int64_t)blockIdx.x * 2 * a.cols;
+  const int64_t pitch = partial_pitch(a.cols);
+  const float* out = a.partial + (int64_t)blockIdx.x * 2 * pitch;
   const float inv_cols = 1.0f / (float)a.cols;
   const int64_t stride = 16 * blockDim.x, span = (a.cols + stride - 1) / stride * stride;   // whole warps
   bool first = true;
@@ -529,7 +580,7 @@ __global__ void __launch_bounds__(512, 1) layer_grad_long_kernel(LayerGradArgs a
       F16 f;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        f.p[i] = f2_of(first || c + 2 * i >= a.cols ? 0.f : p[c + 2 * i], first || c + 2 * i + 1 >= a.cols ? 0.f : p[c + 2 * i + 1]);
+        f.p[i] = first || c >= a.cols ? 0 : f2_of(p[c + 2 * i], p[c + 2 * i + 1]);
       return f;
     };
     for (int64_t c = threadIdx.x * 16; c < span; c += stride) {
@@ -539,10 +590,9 @@ __global__ void __launch_bounds__(512, 1) layer_grad_long_kernel(LayerGradArgs a
       F16 g = unpack(o);
       load16<VEC>(o, x, (int)c, a.cols);
       settle<VEC>(o, xs);
-      F16 n = unpack(o), dw = kept(out, (int)c), db = kept(out + a.cols, (int)c);
-      layer_terms(g, n, load_w16(a.w, a.w_bf16, (int)c, a.cols), dw, db, mm, rs, s);
-      store_partial(out, (int)c, a.cols, dw);
-      store_partial(out + a.cols, (int)c, a.cols, db);
+      F16 n = unpack(o), dw = kept(out, (int)c), db = kept(out + pitch, (int)c);
+      layer_terms(g, n, load_w16_wide(a.w, a.w_bf16, (int)c, a.cols), dw, db, mm, rs, s);
+      store_partial(a, blockIdx.x, (int)c, dw, db);
     }
     first = false;
     const float mg = row_sum<false>(sum2(s.g), red, 0) * inv_cols, mgn = row_sum<false>(sum2(s.gn), red, 1) * inv_cols;
@@ -554,7 +604,7 @@ __global__ void __launch_bounds__(512, 1) layer_grad_long_kernel(LayerGradArgs a
       load16<VEC>(o, x, (int)c, a.cols);
       settle<VEC>(o, xs);
       F16 n = unpack(o);
-      const F16 w = load_w16(a.w, a.w_bf16, (int)c, a.cols);
+      const F16 w = load_w16_wide(a.w, a.w_bf16, (int)c, a.cols);
       if (a.dr) {
         load16<VEC>(res, dr, (int)c, a.cols);
         settle<VEC>(res, xs);
@@ -714,8 +764,8 @@ __global__ void __launch_bounds__(STREAM_THREADS[NV], 1) layer_norm_stream_kerne
   if (threadIdx.y == 0) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      table_set(table + j * 8 * bx, bx, load_w16(a.w, a.w_bf16, c[j], a.cols));
-      table_set(table + (j * 8 + 4) * bx, bx, a.b ? load_w16(a.b, a.w_bf16, c[j], a.cols) : zero16());
+      table_set(table + j * 8 * bx, bx, load_w16_wide(a.w, a.w_bf16, c[j], a.cols));
+      table_set(table + (j * 8 + 4) * bx, bx, a.b ? load_w16_wide(a.b, a.w_bf16, c[j], a.cols) : zero16());
     }
     if ((tx & 31) == 0) columns[tx >> 5] = make_float2((float)mine, inv_mine);
   }
@@ -790,7 +840,7 @@ __global__ void __launch_bounds__(512, 1) layer_grad_stream_kernel(LayerGradArgs
     nmean = a.mean[row];
     nrstd = a.rstd[row];
   }
-  if (threadIdx.y == 0) table_set(table, bx, load_w16(a.w, a.w_bf16, c, a.cols));
+  if (threadIdx.y == 0) table_set(table, bx, load_w16_wide(a.w, a.w_bf16, c, a.cols));
   __syncthreads();
   F16 dw = zero16(), db = zero16();
   int stage = 0, phase = 0, half = 0;
@@ -822,49 +872,32 @@ __global__ void __launch_bounds__(512, 1) layer_grad_stream_kernel(LayerGradArgs
     layer_out(o, g, n, rs, make_float2(t.x * inv_cols, t.y * inv_cols), a.dr != nullptr, res);
     store16<true>(reinterpret_cast<T*>(a.dx) + row * a.lddx, c, a.cols, o, nullptr);
   }
-  if (blockDim.y > 1) {                  // the block's rows side by side: in their order, through shared memory
-    F16* side = reinterpret_cast<F16*>(row_scratch + bx * 64);
-    F16* at = side + (threadIdx.y * bx + tx) * 2;
-    __syncthreads();                     // every row that was copied has been read
-    at[0] = dw;
-    at[1] = db;
-    __syncthreads();
+  if (blockDim.y > 1) {                  // every row that was copied has been read
+    join_rows(reinterpret_cast<float4*>(row_scratch + bx * 64), dw, db);
     if (threadIdx.y > 0) return;
-    for (int y = 1; y < blockDim.y; ++y) {
-      const F16* other = side + (y * bx + tx) * 2;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dw.p[i] = add2(dw.p[i], other[0].p[i]);
-        db.p[i] = add2(db.p[i], other[1].p[i]);
-      }
-    }
   }
-  float* out = a.partial + (int64_t)blockIdx.x * 2 * a.cols;
-  store_partial(out, c, a.cols, dw);
-  store_partial(out + a.cols, c, a.cols, db);
+  store_partial(a, blockIdx.x, c, dw, db);
 }
 
-// dw and db: the blocks' sums, added in their order (32 columns a block; 32 threads a column take every 32nd sum, then
-// their results are added in order).
+// dw and db: the blocks' sums, added in their order (32 columns a block; blockDim.y threads a column take every
+// blockDim.y-th sum, then their results are added in order).
 template <int = 0>
 __global__ void __launch_bounds__(1024) layer_dw_kernel(const float* partial, int parts, int64_t cols, float* dw, float* db) {
   __shared__ float s[32][33];
   wait_for_previous();
   let_next_start();
-  const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  const int64_t pitch = partial_pitch(cols), c = (int64_t)blockIdx.x * 32 + threadIdx.x;      // dw's columns, then db's
   float v = 0.f;
-  if (c < 2 * cols) {
+  if (c < 2 * pitch) {
 #pragma unroll 8
-    for (int p = threadIdx.y; p < parts; p += 32) v += partial[(int64_t)p * 2 * cols + c];
+    for (int p = threadIdx.y; p < parts; p += blockDim.y) v += partial[(int64_t)p * 2 * pitch + c];
   }
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
-  v = warp_sum(s[threadIdx.x][threadIdx.y]);
-  const int64_t o = (int64_t)blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0) {
-    if (o < cols) dw[o] = v;
-    else if (db && o < 2 * cols) db[o - cols] = v;
-  }
+  if (threadIdx.y > 0) return;
+  for (int y = 1; y < blockDim.y; ++y) v += s[y][threadIdx.x];
+  if (c < cols) dw[c] = v;
+  else if (db && c >= pitch && c < pitch + cols) db[c - pitch] = v;
 }
 
 }  // namespace precond

@@ -23,6 +23,29 @@ __device__ __forceinline__ F16 load_w16(const void* w, int bf16, int c, int cols
     f.p[i] = f2_of(c + 2 * i < cols ? load_w(w, bf16, c + 2 * i) : 0.f, c + 2 * i + 1 < cols ? load_w(w, bf16, c + 2 * i + 1) : 0.f);
   return f;
 }
+// The same where whole vectors are aligned: 4 or 2 loads in place of 16.
+__device__ __forceinline__ F16 load_w16_wide(const void* w, int bf16, int c, int cols) {
+  if (c + 16 > cols || (reinterpret_cast<uintptr_t>(w) & 15)) return load_w16(w, bf16, c, cols);
+  F16 f;
+  if (bf16) {
+    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(w) + c);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint4 v = p[k];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f.p[4 * k + i] = f2_of(__uint_as_float((&v.x)[i] << 16), __uint_as_float((&v.x)[i] & 0xFFFF0000u));
+    }
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(w) + c);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = p[k];
+      f.p[2 * k] = f2_of(v.x, v.y);
+      f.p[2 * k + 1] = f2_of(v.z, v.w);
+    }
+  }
+  return f;
+}
 __device__ __forceinline__ f2 squares(const F16& v, f2 s) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) s = fma2(v.p[i], v.p[i], s);

@@ -42,7 +42,7 @@ struct LayerKernels {
   static size_t norm_bytes(const RowShape& s) { return (s.parts ? (size_t)s.threads * s.vectors * 128 : 0) + scratch(s); }
   // the table of w, the warps' exchange buffers; then the dw and db sums of the rows side by side
   static size_t grad_bytes(const RowShape& s) {
-    return std::max((s.parts ? (size_t)s.threads * 64 : 0) + scratch(s), s.rows > 1 ? (size_t)s.threads * s.rows * 128 : 0);
+    return std::max((s.parts ? (size_t)s.threads * 64 : 0) + scratch(s), s.parts == 1 ? (size_t)s.threads * s.rows * 128 : 0);
   }
   static cudaError_t attributes() {
     // one of each kernel; the shapes decide how much they ask for
@@ -67,6 +67,12 @@ RowShape layer_grad_shape(int64_t cols, int dtype, bool vec) {
   if (s.parts == 1 && s.threads >= 32) s.rows = std::min(8, std::max(1, (dtype == PRECOND_F32 ? 384 : 512) / s.threads));
   return s;
 }
+// Few rows: a block, or a cluster of them, leaves dw and db itself, without a second kernel or a workspace: its blocks
+// (0: not this way).  (14 x 192 fp32: 5.0 us, with two kernels 7.5; with a second turn, 100 x 1000 bf16, 10.3 and 8.3.)
+int layer_grad_whole(const RowShape& s, int64_t rows) {
+  const int64_t blocks = (rows + s.rows - 1) / s.rows;
+  return s.parts != 1 || blocks > 8 ? 0 : blocks > 4 ? 8 : blocks > 2 ? 4 : (int)blocks;
+}
 template <typename T, bool VEC>
 cudaError_t launch_layer_norm(const LayerNormArgs& a, const RowShape& s, unsigned grid, cudaStream_t st) {
   typedef LayerKernels<T, VEC> K;
@@ -75,7 +81,8 @@ cudaError_t launch_layer_norm(const LayerNormArgs& a, const RowShape& s, unsigne
 template <typename T, bool VEC>
 cudaError_t launch_layer_grad(const LayerGradArgs& a, const RowShape& s, unsigned grid, cudaStream_t st) {
   typedef LayerKernels<T, VEC> K;
-  return launch(K::grad(s), dim3(grid * std::max(1, s.parts)), dim3(s.threads, s.rows), K::grad_bytes(s), st, std::max(1, s.parts), a);
+  const int cluster = a.dw ? (int)grid : std::max(1, s.parts);
+  return launch(K::grad(s), dim3(a.dw ? grid : grid * cluster), dim3(s.threads, s.rows), K::grad_bytes(s), st, cluster, a);
 }
 
 // Rows through shared memory: threads of a row, rows of a block, rows of each in the ring (0: not this way).  For rows of
@@ -307,10 +314,12 @@ int64_t precond_layer_norm_grad_workspace(int64_t rows, int64_t cols) {
   if (!side(rows) || !side(cols)) return -1;
   if (rows == 0 || cols == 0) return 0;
   // of either type; rows in parts of a warp, and clusters that do not fit, only make fewer
+  if (layer_grad_whole(layer_grad_shape(cols, PRECOND_BF16, false), rows) && layer_grad_whole(layer_grad_shape(cols, PRECOND_F32, false), rows))
+    return 0;                                            // aligned rows of the same length never make more blocks
   int64_t blocks = std::min<int64_t>(rows, PLAN_SMS);    // rows through shared memory: a block an SM
   for (const int dtype : {PRECOND_BF16, PRECOND_F32})
     blocks = std::max(blocks, layer_grad_blocks(layer_grad_shape(cols, dtype, false), rows, dtype, PLAN_SMS, PLAN_CLUSTERS));
-  return blocks * cols * 8;
+  return blocks * partial_pitch(cols) * 8;
 }
 
 int precond_layer_norm_grad(precond_t ph, const void* dy, const void* x, const void* weight, const float* mean, const float* rstd,
@@ -351,14 +360,20 @@ int precond_layer_norm_grad(precond_t ph, const void* dy, const void* x, const v
     if (db) OP_CK(cudaMemsetAsync(db, 0, cols * 4, st));
     return PRECOND_OK;
   }
-  LayerGradArgs a = {dy, x, dresidual, weight, mean, rstd, dx, (float*)workspace, lddy, ldx, lddr, lddx, (int)rows, (int)cols,
+  LayerGradArgs a = {dy, x, dresidual, weight, mean, rstd, dx, (float*)workspace, nullptr, nullptr, lddy, ldx, lddr, lddx, (int)rows, (int)cols,
                      weight_dtype == PRECOND_BF16};
   const bool vec = sector_rows(dy, lddy, dtype) && sector_rows(x, ldx, dtype) && sector_rows(dresidual, lddr, dtype) &&
                    sector_rows(dx, lddx, dtype);
   const RowShape s = layer_grad_shape(cols, dtype, vec);
   const int sms = std::min(h->num_sms, PLAN_SMS);
   unsigned grid = (unsigned)layer_grad_blocks(s, rows, dtype, sms, h->clusters);
-  const StreamShape f = vec ? stream_shape(cols, dtype, dresidual ? 3 : 2, true, rows, sms) : StreamShape{};
+  const int whole = need ? 0 : layer_grad_whole(s, rows);
+  if (whole) {
+    grid = (unsigned)whole;
+    a.dw = dw;
+    a.db = db;
+  }
+  const StreamShape f = vec && !whole ? stream_shape(cols, dtype, dresidual ? 3 : 2, true, rows, sms) : StreamShape{};
   if (f.stages) {
     grid = (unsigned)sms;                // the rows' shapes have at least as many groups
     OP_CK(launch(dtype == PRECOND_BF16 ? layer_grad_stream_kernel<__nv_bfloat16> : layer_grad_stream_kernel<float>, dim3(grid),
@@ -367,9 +382,11 @@ int precond_layer_norm_grad(precond_t ph, const void* dy, const void* x, const v
     OP_CK((vec ? launch_layer_grad<__nv_bfloat16, true>(a, s, grid, st) : launch_layer_grad<__nv_bfloat16, false>(a, s, grid, st)));
   else
     OP_CK((vec ? launch_layer_grad<float, true>(a, s, grid, st) : launch_layer_grad<float, false>(a, s, grid, st)));
-  OP_CK(launch(layer_dw_kernel<0>, dim3((unsigned)((2 * cols + 31) / 32)), dim3(32, 32), 0, st, 1, (const float*)workspace, (int)grid,
-               cols, dw, db));
-  h->launches += 2;
+  ++h->launches;
+  if (whole) return PRECOND_OK;
+  OP_CK(launch(layer_dw_kernel<0>, dim3((unsigned)((2 * partial_pitch(cols) + 31) / 32)), dim3(32, grid > 64 ? 32 : 8), 0, st, 1,
+               (const float*)workspace, (int)grid, cols, dw, db));
+  ++h->launches;
   return PRECOND_OK;
 }
 

@@ -251,6 +251,14 @@ def test_grad_many_rows(pc, rows, cols, dtype, pitch):
     assert torch.equal(d["dy"], c["dx"]) and (pitch or torch.equal(dw, c["dw"]))
 
 
+@pytest.mark.parametrize("rows,cols,dtype,pitch", [(r, c, d, 0) for r in (1, 8, 9, 17, 60, 190) for c, d in ((200, "bf16"), (1000, "f32"), (1001, "bf16"))]
+                         + [(24, 64, "f32", 0), (25, 5000, "bf16", 0), (3, 6000, "f32", 0), (384, 128, "bf16", 0), (24, 6100, "f32", 3)])
+def test_grad_few_rows(pc, rows, cols, dtype, pitch):
+    """Rows that one block, or a cluster of 2, 4 or 8, takes alone; and just more than that."""
+    check_grad(pc, rows, cols, dtype, True, pitch=pitch)
+    check_grad(pc, rows, cols, dtype, False, pitch=pitch, wtype="bf16")
+
+
 def test_empty_and_streams(pc):
     """No rows and no columns; another stream; a captured call replayed on new values."""
     w = torch.ones(64, device="cuda")

@@ -48,7 +48,7 @@ def test_norm_accepts(h, good):
 
 
 def grad(kw):
-    a = dict(dy=BASE["a"], x=BASE["b"], w=BASE["c"], mean=BASE["d"], rstd=BASE["e"], dr=BASE["f"], dtype=1, wtype=0, rows=4, cols=256,
+    a = dict(dy=BASE["a"], x=BASE["b"], w=BASE["c"], mean=BASE["d"], rstd=BASE["e"], dr=BASE["f"], dtype=1, wtype=0, rows=400, cols=256,
              lddy=256, ldx=256, lddr=256, dx=BASE["g"], lddx=256, dw=BASE["h"], db=BASE["i"], ws=BASE["j"], bytes=1 << 20)
     a.update(kw)
     return sr.load().precond_layer_norm_grad(
@@ -74,6 +74,7 @@ def test_grad_refuses(h, bad):
 def test_grad_accepts(h, good):
     assert grad({**dict(h_=h), **good}) == sr.ENODEV
     assert sr.precond_layer_norm_grad_workspace(-1, 5) == -1 and sr.precond_layer_norm_grad_workspace(0, 5) == 0
+    assert sr.precond_layer_norm_grad_workspace(4, 256) == 0 and grad(dict(h_=h, rows=4, ws=None, bytes=0)) == sr.ENODEV   # few rows need none
 
 
 def policy(kw):
