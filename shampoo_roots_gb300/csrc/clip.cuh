@@ -4,16 +4,25 @@
 //
 // Bound by memory: the norm reads every element once; the factor is known only
 // then, so clipping reads them again and writes them.  The second pass goes
-// through each warp's tensors from the end, so that what the first one read last
-// is still in L2 (129 MB).  Where the norm needs no clipping nothing more is read.
+// through each block's tensors from the end, so that what the first one read last
+// is still in L2 (129 MB); what it read before that is asked to leave L2 first.
+// Where the norm needs no clipping nothing more is read.
+//
+// Measured: norm of 604 MB 88 us (the copy bandwidth); clipping of 604 MB of bf16
+// 265 us, where three passes over it take 267 and two 179: of 60 MB asked to stay,
+// little does, as what both dies read lies in both halves of L2.  97 weights of 333
+// KB with three vectors each, clipped, 16 us.
 //
 // A short list takes one launch: a cluster of 8 blocks, which read it a second time
-// when they have joined their sums through distributed shared memory.
+// when they have joined their sums through distributed shared memory (one layer of
+// 256 x 128: 4.7 us, with two kernels 6.5).
 //
 // The list comes as a kernel parameter (no upload, so that a captured call holds
-// its own copy).  Tensors are cut into pieces of 4 KB; a warp takes consecutive
-// pieces, four sectors a lane, so that many small tensors are under way at once
-// (by blocks and 16 KB, 97 weights of 333 KB with three vectors each took 25 us).
+// its own copy).  Tensors are cut into pieces of 4 KB, four sectors a lane; a
+// block's pieces are consecutive and its warps take them in turn, so that many
+// small tensors are under way at once and a block reads 64 KB in a row (pieces of
+// 16 KB, a block each: the 97 weights took 25 us; consecutive pieces to each warp:
+// norm of 604 MB 92 us).
 // A block writes the sum of its squares, in the workspace; every block of the
 // second kernel adds these in the same order.
 //
@@ -60,6 +69,10 @@ struct ClipView {
     body = reinterpret_cast<char*>(t.p) + head * size;
     sectors = (n - head) * size / 32;
     tail = (int)(n - head - sectors * (32 / size));
+  }
+  // a lane's single element (there are up to 30), or null
+  __device__ __forceinline__ char* single(int lane) const {
+    return lane >= head + tail ? nullptr : body + (lane < head ? (int64_t)(lane - head) * size : sectors * 32 + (lane - head) * size);
   }
   __host__ __device__ __forceinline__ int64_t pieces() const {
     return sectors ? (sectors + CLIP_PIECE - 1) / CLIP_PIECE : head + tail > 0;
@@ -188,6 +201,9 @@ __device__ __forceinline__ ClipSum clip_squares(const ClipTable<MAX>& t, const C
   walk.each(t, false, [&](const ClipView& v, int64_t s, bool begins, bool stays) {
     const bool bf16 = v.size == 2;
     uint32_t w[CLIP_U][8];
+    const char* single = begins ? v.single(threadIdx.x & 31) : nullptr;
+    float x = 0.f;
+    if (single) x = bf16 ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(single)) : *reinterpret_cast<const float*>(single);
 #pragma unroll
     for (int u = 0; u < CLIP_U; ++u) {
       if (s + u * 32 < v.sectors) {
@@ -214,13 +230,10 @@ __device__ __forceinline__ ClipSum clip_squares(const ClipTable<MAX>& t, const C
           if (s + u * 32 < v.sectors) sum.wide += clip_square_wide(reinterpret_cast<const uint32_t*>(v.body + (s + u * 32) * 32), 8, bf16);
       }
     }
-    const int lane = threadIdx.x & 31;
-    if (begins && lane < v.head + v.tail) {
-      const int64_t bytes = lane < v.head ? (lane - v.head) * v.size : v.sectors * 32 + (lane - v.head) * v.size;
-      const uint32_t x = bf16 ? (uint32_t) * reinterpret_cast<const uint16_t*>(v.body + bytes) : *reinterpret_cast<const uint32_t*>(v.body + bytes);
-      const float f = __uint_as_float(bf16 ? x << 16 : x), q1 = f * f;
+    if (single) {
+      const float q1 = x * x;
       if (q1 >= 0x1p-70f && q1 <= 0x1p80f) sum.add(q1, 0.f);
-      else sum.wide += (double)f * f;
+      else sum.wide += (double)x * x;
     }
   });
   return clip_block_sum(sum);
@@ -286,21 +299,19 @@ __device__ __forceinline__ void clip_scale(uint32_t (&w)[8], bool bf16, float c)
 }
 
 template <int MAX>
-__device__ __forceinline__ void clip_scale_all(const ClipTable<MAX>& t, const ClipWalk& walk, float c) {
-  walk.each(t, true, [&](const ClipView& v, int64_t s, bool begins, bool stays) {
+__device__ __forceinline__ void clip_scale_all(const ClipTable<MAX>& t, const ClipWalk& walk, bool back, float c) {
+  walk.each(t, back, [&](const ClipView& v, int64_t s, bool begins, bool stays) {
     const bool bf16 = v.size == 2;
     uint32_t w[CLIP_U][8];
 #pragma unroll
     for (int u = 0; u < CLIP_U; ++u)
       if (s + u * 32 < v.sectors) clip_load(w[u], v.body + (s + u * 32) * 32, stays);
-    const int lane = threadIdx.x & 31;
-    if (begins && lane < v.head + v.tail) {
-      const int64_t bytes = lane < v.head ? (lane - v.head) * v.size : v.sectors * 32 + (lane - v.head) * v.size;
+    if (char* single = begins ? v.single(threadIdx.x & 31) : nullptr) {
       if (bf16) {
-        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(v.body + bytes);
+        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(single);
         *p = __float2bfloat16_rn(__bfloat162float(*p) * c);
       } else {
-        *reinterpret_cast<float*>(v.body + bytes) *= c;
+        *reinterpret_cast<float*>(single) *= c;
       }
     }
 #pragma unroll
@@ -323,7 +334,7 @@ __global__ void __launch_bounds__(CLIP_THREADS, 2) clip_scale_kernel(const __gri
   let_next_start();
   const float total = sums ? clip_total(partial, sums) : *norm;
   if (sums && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
-  if (clips(total, max_norm)) clip_scale_all(t, walk, max_norm / total);
+  if (clips(total, max_norm)) clip_scale_all(t, walk, true, max_norm / total);
 }
 
 // A short list: one cluster.  max_norm infinite: the norm alone.
@@ -351,7 +362,7 @@ __global__ void __launch_bounds__(CLIP_THREADS, 2) clip_short_kernel(const __gri
   }
   const float total = v.root();
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
-  if (clips(total, max_norm)) clip_scale_all(t, ClipWalk(t, true), max_norm / total);
+  if (clips(total, max_norm)) clip_scale_all(t, walk, false, max_norm / total);
 }
 
 }  // namespace precond

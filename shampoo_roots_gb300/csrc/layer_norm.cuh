@@ -7,7 +7,9 @@
 //   dw = sum_rows dy n,  db = sum_rows dy
 //
 // Rows lie on threads as for the RMS norm (rows.cuh): read once, 16 columns a
-// thread, the next row's loads under way while the present one is worked on.
+// thread.  Where there are many, they come through a ring in shared memory (below);
+// otherwise the next row's loads are under way, in registers, while the present one
+// is worked on.
 //
 // The squares are those of h - mean, never a difference of sums.  So that a row
 // meets once and not twice, each warp takes the mean and the squared deviations
@@ -18,6 +20,14 @@
 // w and b lie in shared memory, where a thread's four columns are one load and a
 // warp's loads meet no bank twice: in registers beside the vectors in flight they
 // would leave room for half the warps.
+//
+// Measured (bf16 with residual): norm of 8192 x 6144 to 8 bits 56 us, 93 % of the
+// copy bandwidth; gradients of 16384 x 4096 85 us, 93 %; in fp32 norm of 8192 x 6144
+// 106 us, gradients of 8000 x 6144 121 us, 96 %.  What bounds them below that is
+// issue slots (56 % busy at 24 warps an SM) and the latency of a row's sums: 21
+// shuffles one after another, which is why lanes join means and deviations in one
+// butterfly.  Rows that do not begin at sectors pass through the exchange of
+// form8.cuh: gradients of 7000 x 2001 40 us, 41 %.
 #pragma once
 
 #include <type_traits>

@@ -7,9 +7,21 @@
 //   dz_v = slope / tau ([v = id] - q_v)
 //
 // Bound by memory: the logits are read once and the gradient is written once.  A
-// row lies in the registers of a cluster's blocks as in the distillation loss
-// (distill.cuh: Part, Shift, the joins), which this shares; but one token needs no
-// warp of its own, and no second kernel.
+// row belongs to a cluster of 1 to 8 blocks.  Each copies its part into shared
+// memory with one bulk copy, three blocks to an SM, so that one's loads run beside
+// another's powers and a third's stores, and goes over it three times: maxima, the
+// sum, the gradient.  (In registers, as the distillation loss keeps its rows, an SM
+// holds two blocks: 817 us where this takes 676, for 8192 x 131072.)  Rows too long
+// for 8 blocks' shared memory, 1.7 MB, are read twice.
+//
+// What a row takes beside its elements, the join of its sums and the loss, is the
+// work of one warp of each block; the others find the shift and the factor in
+// shared memory.  (Done by every thread, that was as many instructions as the
+// elements: 824 us.)
+//
+// Measured: 8192 x 131072 bf16 676 us, 88 % of the copy bandwidth; 2999 x 50001
+// bf16 99 us, 84 %; 1000 x 32000 fp32 45 us, 79 % (four waves of blocks and the
+// first one's latency); scoring 24 x 50001 4.3 us.
 //
 // The taken token is left out of the streamed sum: with R the sum of the others,
 // s = -log(1 + R / e_id) and 1 - q_id = R / (R + e_id) keep their digits where the

@@ -232,7 +232,10 @@ def test_grad_against_differences(pc):
 
 @pytest.mark.parametrize("rows,cols,dtype,pitch", [(700, 6144, "bf16", 0), (2600, 1000, "bf16", 0), (5000, 264, "bf16", 0), (2450, 512, "f32", 0),
                                                    (400, 16384, "bf16", 0), (310, 8200, "bf16", 8), (333, 9004, "f32", 4), (1000, 4104, "f32", 8),
-                                                   (2000, 1208, "bf16", 24), (320, 12288, "bf16", 0), (1500, 2052, "f32", 12)])
+                                                   (2000, 1208, "bf16", 24), (320, 12288, "bf16", 0), (1500, 2052, "f32", 12),
+                                                   (3700, 65, "bf16", 0), (3000, 200, "bf16", 0), (2500, 333, "f32", 0), (2500, 777, "bf16", 2),
+                                                   (700, 6143, "bf16", 0), (900, 4097, "f32", 1), (330, 10001, "bf16", 0), (320, 9001, "f32", 3),
+                                                   (340, 16383, "bf16", 0), (5000, 130, "f32", 5), (1000, 3001, "bf16", 7)])
 def test_norm_many_rows(pc, rows, cols, dtype, pitch):
     """Enough rows for each group of threads to have several: rows copied through shared memory, more than its ring holds."""
     check_norm(pc, rows, cols, dtype, pitch=pitch)
@@ -241,7 +244,9 @@ def test_norm_many_rows(pc, rows, cols, dtype, pitch):
 
 @pytest.mark.parametrize("rows,cols,dtype,pitch", [(700, 4096, "bf16", 0), (2600, 1000, "bf16", 0), (2700, 264, "bf16", 0), (2450, 512, "f32", 0),
                                                    (400, 8192, "bf16", 0), (333, 6148, "f32", 4), (1000, 3004, "f32", 4), (2000, 1208, "bf16", 24),
-                                                   (200, 8192, "f32", 0), (3000, 2056, "bf16", 8)])
+                                                   (200, 8192, "f32", 0), (3000, 2056, "bf16", 8), (3700, 65, "bf16", 0), (3000, 200, "bf16", 0),
+                                                   (2600, 333, "f32", 0), (2500, 777, "bf16", 2), (400, 8191, "bf16", 0), (900, 4097, "f32", 1),
+                                                   (5000, 130, "f32", 5), (1000, 3001, "bf16", 7), (400, 6001, "f32", 2)])
 def test_grad_many_rows(pc, rows, cols, dtype, pitch):
     check_grad(pc, rows, cols, dtype, True, pitch=pitch)
     c = check_grad(pc, rows, cols, dtype, False, pitch=pitch)
