@@ -19,6 +19,9 @@
 // shared memory.  (Done by every thread, that was as many instructions as the
 // elements: 824 us.)
 //
+// Rows of up to 4 KB are a warp's, in registers, and a warp goes from row to row
+// (4013 x 1774 bf16 8.3 us, with a block a row 15.2).
+//
 // Measured: 8192 x 131072 bf16 676 us, 88 % of the copy bandwidth; 2999 x 50001
 // bf16 99 us, 84 %; 1000 x 32000 fp32 45 us, 79 % (four waves of blocks and the
 // first one's latency); scoring 24 x 50001 4.3 us.
@@ -100,7 +103,85 @@ struct PolicyRow {
   float taken;                                       // dz of the taken token
 };
 
-// KEPT: a block's part of the row lies in its shared memory; otherwise the row is read twice.
+__device__ __forceinline__ int policy_id(const PolicyArgs& a, int64_t row) {
+  const int64_t id = a.ids64 ? reinterpret_cast<const int64_t*>(a.ids)[row] : (int64_t) reinterpret_cast<const int32_t*>(a.ids)[row];
+  return id >= 0 && id < a.vocab ? (int)id : -1;
+}
+// From the others' (maximum, sum) and the taken token's logit.
+__device__ __forceinline__ PolicyRow policy_result(const PolicyArgs& a, float c, float weight, float advantage, float old, float ref,
+                                                   float taken, float m, float s, float& loss, float& logp) {
+  const float M = max_nan(m, taken);
+  const Shift shift(M, c);
+  const float rest = m == M ? s : s * ex2(shift.from(Shift(m, c), c)), mine = ex2(shift(taken, c)), total = rest + mine;
+  logp = taken >= m ? -log1pf(rest / mine) : fmaf(shift(taken, c), LN2, -logf(total));
+  loss = 0.f;
+  float slope = 0.f;
+  if (a.advantage) {
+    const float ratio = a.old ? expf(logp - old) : logp != logp ? logp : 1.0f;   // what is not a number shows
+    const float free = ratio * advantage, held = fminf(fmaxf(ratio, 1.0f - a.low), 1.0f + a.high) * advantage;
+    loss = free > held ? -held : -free;
+    slope = free > held ? 0.f : -free;
+    if (a.ref) {
+      const float d = ref - logp, e = expm1f(d);
+      loss = fmaf(a.kl, e - d, loss);
+      slope = fmaf(-a.kl, e, slope);
+    }
+    loss *= weight;
+    slope *= weight / a.tau;
+  }
+  return {shift.b, shift.k, -slope / total, slope * (rest / total)};
+}
+
+// Short rows, up to 32 NV vectors: a warp has each in its registers, and goes on to another.
+template <typename T, int NV>
+__global__ void __launch_bounds__(256, 4) policy_warp_kernel(PolicyArgs a) {
+  const int lane = threadIdx.x & 31;
+  const float c = LOG2E / a.tau;
+  wait_for_previous();
+  let_next_start();
+  for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < a.rows; row += (int64_t)gridDim.x * 8) {
+    const T* z = reinterpret_cast<const T*>(a.z) + row * a.ldz;
+    T* dz = reinterpret_cast<T*>(a.dz) + row * a.lddz;
+    const Slice sl(z, (int)a.vocab, 1, 0);
+    const float weight = a.weight ? a.weight[row] : 1.0f;
+    const int id = policy_id(a, row);
+    Part<T, NV> x;
+    x.at = sl.single(lane);
+    Shift shift(0.f, c);
+    if (weight == 0.0f || id < 0) {
+      if (lane == 0) {
+        if (a.loss) a.loss[row] = 0.f;
+        if (a.logp) a.logp[row] = 0.f;
+      }
+      if (a.dz) x.store(z, dz, sl, lane, 32, false, shift, c, 0.f);
+      continue;
+    }
+    x.load(z, sl, lane, 32);
+    const float taken = as_float(z[id]), advantage = a.advantage ? a.advantage[row] : 0.f, old = a.old ? a.old[row] : 0.f,
+                ref = a.ref ? a.ref[row] : 0.f;
+    const int vec = id >= sl.body && id < sl.tail ? (id - sl.body) / LogitVec<T>::N : -1, element = (id - sl.body) % LogitVec<T>::N;
+    if (x.at == id) x.one = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      if (lane + 32 * u == vec) hide_element(x.w[u], element, z);
+    float m, s, loss, logp;
+    x.sums(z, sl, lane, 32, c, m, s);
+    join_warp(m, s, c);
+    const PolicyRow r = policy_result(a, c, weight, advantage, old, ref, taken, m, s, loss, logp);
+    if (lane == 0) {
+      if (a.loss) a.loss[row] = loss;
+      if (a.logp) a.logp[row] = logp;
+    }
+    if (!a.dz) continue;
+    __syncwarp();                                      // every lane has read the taken token: dz may be z
+    shift.b = r.b;
+    shift.k = r.k;
+    x.store(z, dz, sl, lane, 32, true, shift, c, r.g);
+    if (vec >= 0 ? (vec & 31) == lane : x.at == id) set_float(dz + id, r.taken);
+  }
+}
+
+// Longer rows.  KEPT: a block's part of the row lies in its shared memory; otherwise the row is read twice.
 template <typename T, bool KEPT>
 __global__ void __launch_bounds__(POLICY_THREADS, 3) policy_kernel(PolicyArgs a) {
   namespace cg = cooperative_groups;
@@ -136,8 +217,7 @@ __global__ void __launch_bounds__(POLICY_THREADS, 3) policy_kernel(PolicyArgs a)
     asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  ::"r"(smem_u32(policy_smem)), "l"(z + sl.body), "r"(n * 16), "r"(smem_u32(&arrived)) : "memory");
   }
-  const int64_t wide = a.ids64 ? reinterpret_cast<const int64_t*>(a.ids)[row] : (int64_t) reinterpret_cast<const int32_t*>(a.ids)[row];
-  const int id = wide >= 0 && wide < a.vocab ? (int)wide : -1;
+  const int id = policy_id(a, row);
   const bool reads = weight != 0.0f && id >= 0;          // uniform over the cluster
   const bool aligned = (reinterpret_cast<uintptr_t>(dz + sl.body) & 15) == 0;
   auto put = [&](int i, uint4 w) {
@@ -233,28 +313,12 @@ __global__ void __launch_bounds__(POLICY_THREADS, 3) policy_kernel(PolicyArgs a)
   if (warp == 0) {
     __syncwarp();
     join_sums(sums, parts, m, s, c);
-    const float M = max_nan(m, taken);
-    const Shift shift(M, c);
-    const float rest = m == M ? s : s * ex2(shift.from(Shift(m, c), c)), mine = ex2(shift(taken, c)), total = rest + mine;
-    const float logp = taken >= m ? -log1pf(rest / mine) : fmaf(shift(taken, c), LN2, -logf(total));
-    float slope = 0.f, loss = 0.f;
-    if (a.advantage) {
-      const float ratio = a.old ? expf(logp - old) : logp != logp ? logp : 1.0f;   // what is not a number shows
-      const float free = ratio * advantage, held = fminf(fmaxf(ratio, 1.0f - a.low), 1.0f + a.high) * advantage;
-      loss = free > held ? -held : -free;
-      slope = free > held ? 0.f : -free;
-      if (a.ref) {
-        const float d = ref - logp, e = expm1f(d);
-        loss = fmaf(a.kl, e - d, loss);
-        slope = fmaf(-a.kl, e, slope);
-      }
-      loss *= weight;
-      slope *= weight / a.tau;
-    }
+    float loss, logp;
+    const PolicyRow r = policy_result(a, c, weight, advantage, old, ref, taken, m, s, loss, logp);
     if (lane == 0) {
       if (part == 0 && a.loss) a.loss[row] = loss;
       if (part == 0 && a.logp) a.logp[row] = logp;
-      result = {shift.b, shift.k, -slope / total, slope * (rest / total)};
+      result = r;
     }
   }
   if (!a.dz) return;

@@ -119,6 +119,13 @@ StreamShape stream_shape(int64_t cols, int dtype, int inputs, bool grad, int64_t
 typedef void (*PolicyKernel)(PolicyArgs);
 const PolicyKernel policy_kernels[2][2] = {{policy_kernel<float, false>, policy_kernel<float, true>},
                                            {policy_kernel<__nv_bfloat16, false>, policy_kernel<__nv_bfloat16, true>}};
+// Bytes of a row that a warp takes: 1, 2, 4 or 8 vectors a lane (8192 x 1000 bf16 9.9 us, by blocks 18.3; of rows of 8 KB,
+// with 16 vectors, an SM holds half the warps: 8192 x 4000 33 us, by blocks 31).
+constexpr int64_t POLICY_WARP = 4096;
+const PolicyKernel policy_warp_kernels[2][4] = {
+    {policy_warp_kernel<float, 1>, policy_warp_kernel<float, 2>, policy_warp_kernel<float, 4>, policy_warp_kernel<float, 8>},
+    {policy_warp_kernel<__nv_bfloat16, 1>, policy_warp_kernel<__nv_bfloat16, 2>, policy_warp_kernel<__nv_bfloat16, 4>,
+     policy_warp_kernel<__nv_bfloat16, 8>}};
 // Blocks of a row and threads of a block.  A part takes at most what lets an SM hold three blocks (8192 x 131072 bf16 by
 // parts of 64 KB 673 us, of 32 KB 707, of 128 KB 893; 1900 x 151936 by 74 KB 188, by 37 KB 199); a few rows take more
 // blocks, each with at least 8192 logits.  Threads have 192 bytes each, up to 256 of them (8192 x 8000 bf16, 16 KB: 96
@@ -424,6 +431,14 @@ int precond_policy(precond_t ph, const void* logits, int dtype, int64_t rows, in
   if (rc) return rc;
   const PolicyArgs a = {logits, ldz, ids, id_bits == 64, advantage, old_logp, kl != 0.f ? ref_logp : nullptr, weight, loss, logp, dlogits,
                         lddz, rows, vocab, temperature, clip_low, clip_high, kl};
+  if (vocab * (int64_t)sz <= POLICY_WARP) {
+    int i = 0;
+    while (vocab * (int64_t)sz > (int64_t)512 << i) ++i;
+    OP_CK(launch(policy_warp_kernels[dtype == PRECOND_BF16][i], dim3((unsigned)std::min<int64_t>((rows + 7) / 8, 4 * h->num_sms)), dim3(256), 0,
+                 (cudaStream_t)stream, 1, a));
+    ++h->launches;
+    return PRECOND_OK;
+  }
   const PolicyShape s = policy_shape(rows, vocab, dtype);
   OP_CK(launch(policy_kernels[dtype == PRECOND_BF16][s.bytes > 0], dim3((unsigned)(rows * s.parts)), dim3(s.threads), (size_t)s.bytes,
                (cudaStream_t)stream, s.parts, a));

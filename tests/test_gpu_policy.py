@@ -94,9 +94,10 @@ def test_policy(pc, rows, vocab, dtype):
 
 
 @pytest.mark.parametrize("rows,vocab,dtype,pitch", [(400, 1000, "bf16", 0), (700, 333, "f32", 3), (350, 2047, "bf16", 1), (31, 50257, "bf16", 2),
-                                                    (12, 70001, "f32", 1), (6, 400001, "bf16", 7), (5, 280003, "f32", 5), (320, 9000, "f32", 0)])
+                                                    (12, 70001, "f32", 1), (6, 400001, "bf16", 7), (5, 280003, "f32", 5), (320, 9000, "f32", 0), (5100, 130, "bf16", 0),
+                                                    (5000, 70, "f32", 1), (40, 2048, "bf16", 0), (40, 2049, "bf16", 3), (60, 1024, "f32", 2)])
 def test_policy_layouts(pc, rows, vocab, dtype, pitch):
-    """Rows at every alignment, on 1 to 8 blocks, in registers and read twice."""
+    """Rows at every alignment, on a warp that takes several, on 1 to 8 blocks, and read twice."""
     check(pc, *inputs(rows, vocab, dtype, 1.3), tau=1.3, pitch=pitch)
 
 
