@@ -9,13 +9,13 @@
 // Where the norm needs no clipping nothing more is read.
 //
 // Measured: norm of 604 MB 88 us (the copy bandwidth); clipping of 604 MB of bf16
-// 265 us, where three passes over it take 267 and two 179: of 60 MB asked to stay,
-// little does, as what both dies read lies in both halves of L2.  97 weights of 333
-// KB with three vectors each, clipped, 16 us.
+// 261 us, where three passes over it take 267 and two 179: of the 60 MB that are
+// asked to stay in L2 some 20 are found there.  97 weights of 333 KB with three
+// vectors each, clipped, 15 us.
 //
 // A short list takes one launch: a cluster of 8 blocks, which read it a second time
 // when they have joined their sums through distributed shared memory (one layer of
-// 256 x 128: 4.7 us, with two kernels 6.5).
+// 256 x 128: 4.9 us, with two kernels 6.5).
 //
 // The list comes as a kernel parameter (no upload, so that a captured call holds
 // its own copy).  Tensors are cut into pieces of 4 KB, four sectors a lane; a
@@ -30,8 +30,8 @@
 // fp32 numbers, joined by TwoSum (Knuth), so that no length of list costs digits.
 // (fp64 additions, two a clock and SM, took a block's join a microsecond.)  Where
 // the squares of a lane's sectors add up to less than 2^-70 or more than 2^80, so
-// that they may have been lost or the pair's range may not do, they are read again
-// and added up in fp64, beside the pair.
+// that some may have been lost or the pair's range may not do, the same registers
+// are squared again times a power of two, into a pair of their own (Blue's method).
 #pragma once
 
 #include <cooperative_groups.h>
@@ -152,35 +152,65 @@ __device__ __forceinline__ f2 clip_square(const uint32_t (&w)[8], bool bf16, f2 
   }
   return s;
 }
-__device__ __noinline__ double clip_square_wide(const uint32_t* w, int n, bool bf16) {
-  double s = 0;
-  for (int i = 0; i < n; ++i) {
-    const double lo = __uint_as_float(bf16 ? w[i] << 16 : w[i]), hi = bf16 ? __uint_as_float(w[i] & 0xFFFF0000u) : 0.0;
-    s += lo * lo + hi * hi;
+__device__ __forceinline__ f2 clip_square_scaled(const uint32_t (&w)[8], bool bf16, float by, f2 s) {
+  const f2 k = f2_of(by, by);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    if (bf16) {
+#pragma unroll
+      for (int j = i; j < i + 2; ++j) {
+        const f2 x = mul2(f2_of(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)), k);
+        s = fma2(x, x, s);
+      }
+    } else {
+      const f2 x = mul2(f2_of(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), k);
+      s = fma2(x, x, s);
+    }
   }
   return s;
 }
-// A sum: hi + lo, and what was added in fp64 (mostly nothing).
-struct ClipSum {
+// A sum hi + lo.  An infinite hi, or one that is not a number, stays, whatever lo says.
+struct ClipPair {
   float hi, lo;
-  double wide;
   __device__ __forceinline__ void add(float h, float l) {
     const float s = hi + h, b = s - hi;
     lo += ((hi - (s - b)) + (h - b)) + l;
     hi = s;
   }
+  __device__ __forceinline__ void join(int o) {
+    const float h = __shfl_xor_sync(0xffffffffu, hi, o), l = __shfl_xor_sync(0xffffffffu, lo, o);
+    add(h, l);
+  }
+  __device__ __forceinline__ float value() const { return hi < INFINITY ? hi + lo : hi; }
+};
+// A sum of squares: of ordinary size; of elements times 2^80; of elements times 2^-80.
+constexpr float CLIP_LEAST = 0x1p-70f, CLIP_MOST = 0x1p80f, CLIP_UP = 0x1p80f, CLIP_DOWN = 0x1p-80f;
+struct ClipSum {
+  ClipPair mid, low, high;
+  __device__ __forceinline__ void add(const ClipSum& o) {
+    mid.add(o.mid.hi, o.mid.lo);
+    if (o.low.hi != 0.f) low.add(o.low.hi, o.low.lo);
+    if (o.high.hi != 0.f) high.add(o.high.hi, o.high.lo);
+  }
   // over the lanes, the same in each
   __device__ __forceinline__ void join() {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float h = __shfl_xor_sync(0xffffffffu, hi, o), l = __shfl_xor_sync(0xffffffffu, lo, o);
-      add(h, l);
+    for (int o = 16; o > 0; o >>= 1) mid.join(o);
+    if (__any_sync(0xffffffffu, low.hi != 0.f || high.hi != 0.f)) {
+      for (int o = 16; o > 0; o >>= 1) {
+        low.join(o);
+        high.join(o);
+      }
     }
-    if (__any_sync(0xffffffffu, wide != 0.0)) wide = warp_sum(wide);
   }
-  __device__ __forceinline__ float root() const;
+  // the square root of the whole
+  __device__ __forceinline__ float root() const {
+    const float m = mid.value(), l = low.value(), h = high.value();
+    if (h != 0.f) return sqrtf(fmaf(m * CLIP_DOWN, CLIP_DOWN, h)) * CLIP_UP;           // also where h is not finite
+    return m != 0.f ? sqrtf(fmaf(l * CLIP_DOWN, CLIP_DOWN, m)) : sqrtf(l) * CLIP_DOWN;
+  }
 };
-constexpr ClipSum CLIP_NOTHING = {0.f, 0.f, 0.0};
+constexpr ClipSum CLIP_NOTHING = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
 // The block's sum in the first warp: lanes and warps in a fixed order.
 __device__ __forceinline__ ClipSum clip_block_sum(ClipSum v) {
   __shared__ ClipSum red[CLIP_WARPS];
@@ -213,27 +243,19 @@ __device__ __forceinline__ ClipSum clip_squares(const ClipTable<MAX>& t, const C
         for (int i = 0; i < 8; ++i) w[u][i] = 0;
       }
     }
-    f2 e = 0;
+    f2 e = f2_of(x * x, 0.f);
 #pragma unroll
     for (int u = 0; u < CLIP_U; ++u) e = clip_square(w[u], bf16, e);
     const float q = sum2(e);
-    if (q >= 0x1p-70f && q <= 0x1p80f) {
-      sum.add(q, 0.f);
-    } else {                                          // nothing but zeros needs no second look
-      uint32_t any = 0;
+    if (q >= CLIP_LEAST && q <= CLIP_MOST) {
+      sum.mid.add(q, 0.f);
+    } else {
+      const float by = q < CLIP_LEAST ? CLIP_UP : CLIP_DOWN, y = x * by;
+      e = f2_of(y * y, 0.f);
 #pragma unroll
-      for (int u = 0; u < CLIP_U; ++u)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) any |= w[u][i];
-      if (any & (bf16 ? 0x7FFF7FFFu : 0x7FFFFFFFu)) {
-        for (int u = 0; u < CLIP_U; ++u)
-          if (s + u * 32 < v.sectors) sum.wide += clip_square_wide(reinterpret_cast<const uint32_t*>(v.body + (s + u * 32) * 32), 8, bf16);
-      }
-    }
-    if (single) {
-      const float q1 = x * x;
-      if (q1 >= 0x1p-70f && q1 <= 0x1p80f) sum.add(q1, 0.f);
-      else sum.wide += (double)x * x;
+      for (int u = 0; u < CLIP_U; ++u) e = clip_square_scaled(w[u], bf16, by, e);
+      if (q < CLIP_LEAST) sum.low.add(sum2(e), 0.f);
+      else sum.high.add(sum2(e), 0.f);
     }
   });
   return clip_block_sum(sum);
@@ -247,25 +269,11 @@ __global__ void __launch_bounds__(CLIP_THREADS, 2) clip_norm_kernel(const __grid
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
-// The square root.  Of a sum beside which something was added in fp64: of the mantissa and an even part of the exponent.
-__device__ __forceinline__ float ClipSum::root() const {
-  if (wide == 0.0) return sqrtf(hi + lo);
-  const double v = wide + (double)hi + (double)lo;
-  if (!(v > 0.0) || !(v < __longlong_as_double(0x7FF0000000000000ll))) return (float)v;      // infinite, not a number
-  const int e = ((__double2hiint(v) >> 20) - 1023) & ~1;
-  const double up = __hiloint2double((1023 - e / 2) << 20, 0);       // 2^(-e / 2), twice: 2^-e itself may be subnormal
-  const float r = sqrtf((float)(v * up * up));
-  return e > 256 ? INFINITY : e < -298 ? r * 0.f : (float)((double)r * __hiloint2double((1023 + e / 2) << 20, 0));
-}
 // The norm of all sums, in every thread.
 __device__ __forceinline__ float clip_total(const ClipSum* partial, int n) {
   __shared__ float norm;
   ClipSum v = CLIP_NOTHING;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const ClipSum p = partial[i];
-    v.add(p.hi, p.lo);
-    if (p.wide != 0.0) v.wide += p.wide;
-  }
+  for (int i = threadIdx.x; i < n; i += blockDim.x) v.add(partial[i]);
   v = clip_block_sum(v);
   if (threadIdx.x == 0) norm = v.root();
   __syncthreads();
@@ -356,10 +364,7 @@ __global__ void __launch_bounds__(CLIP_THREADS, 2) clip_short_kernel(const __gri
   cluster.sync();
   ClipSum v = sums[0];
 #pragma unroll
-  for (int i = 1; i < CLIP_CLUSTER; ++i) {
-    v.add(sums[i].hi, sums[i].lo);
-    if (sums[i].wide != 0.0) v.wide += sums[i].wide;
-  }
+  for (int i = 1; i < CLIP_CLUSTER; ++i) v.add(sums[i]);
   const float total = v.root();
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
   if (clips(total, max_norm)) clip_scale_all(t, walk, false, max_norm / total);

@@ -11,7 +11,7 @@
 // memory with one bulk copy, three blocks to an SM, so that one's loads run beside
 // another's powers and a third's stores, and goes over it three times: maxima, the
 // sum, the gradient.  (In registers, as the distillation loss keeps its rows, an SM
-// holds two blocks: 817 us where this takes 676, for 8192 x 131072.)  Rows too long
+// holds two blocks: 817 us where this takes 671, for 8192 x 131072.)  Rows too long
 // for 8 blocks' shared memory, 1.7 MB, are read twice.
 //
 // What a row takes beside its elements, the join of its sums and the loss, is the
@@ -22,8 +22,8 @@
 // Rows of up to 4 KB are a warp's, in registers, and a warp goes from row to row
 // (4013 x 1774 bf16 8.3 us, with a block a row 15.2).
 //
-// Measured: 8192 x 131072 bf16 676 us, 88 % of the copy bandwidth; 2999 x 50001
-// bf16 99 us, 84 %; 1000 x 32000 fp32 45 us, 79 % (four waves of blocks and the
+// Measured: 8192 x 131072 bf16 671 us, 89 % of the copy bandwidth; 2999 x 50001
+// bf16 98 us, 85 %; 1000 x 32000 fp32 45 us, 79 % (four waves of blocks and the
 // first one's latency); scoring 24 x 50001 4.3 us.
 //
 // The taken token is left out of the streamed sum: with R the sum of the others,

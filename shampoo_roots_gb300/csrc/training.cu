@@ -5,7 +5,7 @@
 
 #include <cmath>
 #include <cstring>
-#include <new>
+
 #include <vector>
 
 #include "clip.cuh"
@@ -469,7 +469,7 @@ int precond_list_create(precond_list_t* out, int count, void* const tensors[], c
       if (l.ranges[i].lo < l.ranges[i - 1].hi) return PRECOND_EINVAL;     // one tensor over another would be scaled twice
     l.make_tables();
     *out = reinterpret_cast<precond_list_t>(new List(std::move(l)));
-  } catch (const std::bad_alloc&) {
+  } catch (...) {                                      // of a vector: memory
     return PRECOND_ENOMEM;
   }
   return PRECOND_OK;

@@ -1,7 +1,7 @@
 """The norm of a list of gradients, and their clipping, on the GPU against 64 bits (training_plain.py).
 
-Tolerances: E = 2^-24.  At most 64 squares are added in a row of fp32 (32 pairs), everything above them in fp64; with the
-squares' own rounding the norm, half of it, is within 20 E, and its fp32 value E more.  The factor is within 2 E of that,
+Tolerances: E = 2^-24.  At most 33 squares are added in a row in fp32, everything above them in pairs; with the squares'
+own rounding the norm, half of it, is within 20 E, and its fp32 value E more.  The factor is within 2 E of that,
 and a scaled element is rounded to fp32 and then to its type."""
 import math
 
@@ -134,6 +134,10 @@ def test_extreme_values(pc, dtype):
         t[at] = 1e22
         check(pc, [t])
     check(pc, [random(g, 3000, dtype, 1e30), random(g, 3000, "f32", 1e-30)])
+    # sums of each range beside one another: many small beside one ordinary, many ordinary beside one large
+    check(pc, [random(g, 400000, dtype, 1e-12), random(g, 5, "f32", 3e-11)])
+    check(pc, [random(g, 400000, dtype, 5e11), random(g, 7, "f32", 3e12), random(g, 1, dtype, 1e-3)])
+    check(pc, [random(g, 100, dtype, 1e-12), random(g, 100, "f32", 1.0), random(g, 100, dtype, 1e13)])
 
 
 def test_not_finite(pc):
