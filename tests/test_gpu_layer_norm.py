@@ -61,7 +61,31 @@ def check_norm(pc, rows, cols, dtype, wtype="f32", residual=True, bias=True, pit
     n = (want - (0 if b is None else b.double())).abs()
     tol = (tm * rs)[:, None] * w.double().abs() + n * (tr + 4 * E)[:, None] + 2 * E * want.abs() + 1e-38
     assert bool(((y.cpu().double() - want).abs() <= tol + (E16 * (want.abs() + tol) if dtype == "bf16" else 0)).all())
-    # the 8-bit form: the scale fits the block, and each value is a nearest one
+    check8(q, s, want, tol)
+    # outputs left out change nothing in the others, unless their rows' places chose another kernel (sums in another order)
+    q2, s2 = sr.empty8(rows, cols)
+    t2 = torch.empty_like(total) if residual else None
+    sr.precond_layer_norm(pc.h, dx, w.cuda(), eps, bias=db, residual=dr, total=t2, q=q2, scale=s2)
+    check8(q2, s2, want, tol)
+    if not pitch:
+        assert torch.equal(bytes_of(q), bytes_of(q2)) and torch.equal(bytes_of(s), bytes_of(s2))
+        return
+    # every matrix with the same pitch; nothing is written between the rows
+    y, total = place(torch.zeros_like(x)), place(torch.zeros_like(x)) if residual else None
+    gaps = [(t, t.as_strided((rows - 1, pitch), (cols + pitch, 1), t.storage_offset() + cols)) for t in (y, total) if t is not None]
+    held = [gap.clone() for _, gap in gaps]
+    sr.precond_layer_norm(pc.h, dx, w.cuda(), eps, bias=db, residual=dr, total=total, y=y, mean=mean, rstd=rstd)
+    assert bool(((y.cpu().double() - want).abs() <= tol + (E16 * (want.abs() + tol) if dtype == "bf16" else 0)).all())
+    assert bool(((mean.cpu().double() - m).abs() <= tm + 1e-38).all()) and bool(((rstd.cpu().double() - rs).abs() <= tr * rs).all())
+    if residual:
+        assert torch.equal(total.cpu(), h)
+    for (_, gap), was in zip(gaps, held):
+        assert torch.equal(bytes_of(gap), bytes_of(was))
+
+
+def check8(q, s, want, tol):
+    """The 8-bit form of a matrix known within tol: the scale fits the block, and each value is a nearest one."""
+    rows, cols = want.shape
     sc = sr.scales8(s, rows, cols).cpu().double()
     pad = lambda t: torch.nn.functional.pad(t, (0, P.blocks(cols) * 128 - cols)).view(rows, -1, 128)
     lo, hi = pad((want.abs() - tol).clamp(min=0)).amax(dim=2), pad(want.abs() + tol).amax(dim=2)
@@ -71,11 +95,6 @@ def check_norm(pc, rows, cols, dtype, wtype="f32", residual=True, bias=True, pit
     assert bool(((got - want).abs() <= torch.maximum((want.abs() + tol) * 2.0 ** -4, each * 2.0 ** -10) + tol).all())
     order = P.order_scales(torch.zeros(rows, P.blocks(cols), dtype=torch.int64), rows, cols)
     assert bool((bytes_of(s).view(-1)[order == 127] == 127).all())
-    # outputs left out change nothing in the others
-    q2, s2 = sr.empty8(rows, cols)
-    t2 = torch.empty_like(total) if residual else None
-    sr.precond_layer_norm(pc.h, dx, w.cuda(), eps, bias=db, residual=dr, total=t2, q=q2, scale=s2)
-    assert torch.equal(bytes_of(q), bytes_of(q2)) and torch.equal(bytes_of(s), bytes_of(s2))
 
 
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 2), (1, 64), (1, 1024), (3, 100), (5, 128), (130, 256), (257, 1000), (33, 4096),
@@ -139,14 +158,14 @@ def test_norm_values(pc):
     assert bool(((y.double() - want).abs() <= tol)[keep].all())
 
 
-@pytest.mark.parametrize("cols", [200, 1000, 20000, 70000])
-def test_norm_in_place(pc, cols):
+@pytest.mark.parametrize("rows,cols", [(21, 200), (21, 1000), (21, 20000), (21, 70000), (1500, 2048), (400, 9000)])
+def test_norm_in_place(pc, rows, cols):
     g = P.generator(3)
-    x, r = P.randn(g, 21, cols), P.randn(g, 21, cols)
+    x, r = P.randn(g, rows, cols), P.randn(g, rows, cols)
     w = torch.ones(cols, device="cuda")
     for over in ("x", "residual"):
         dx, dr = x.cuda(), r.cuda()
-        y, y2, t = (torch.empty(21, cols, device="cuda") for _ in range(3))
+        y, y2, t = (torch.empty(rows, cols, device="cuda") for _ in range(3))
         sr.precond_layer_norm(pc.h, dx, w, 1e-6, residual=dr, total=t, y=y)
         sr.precond_layer_norm(pc.h, dx, w, 1e-6, residual=dr, total=dx if over == "x" else dr, y=y2)
         assert torch.equal(t, dx if over == "x" else dr) and torch.equal(y, y2)
@@ -180,6 +199,12 @@ def check_grad(pc, rows, cols, dtype, residual, pitch=0, wtype="f32"):
     dx2, dw2 = torch.empty_like(dx), torch.empty_like(dw)             # without db the others are the same
     sr.precond_layer_norm_grad(pc.h, *args, dx2, dw2, dresidual=d_dr)
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+    if pitch:                                                         # every matrix with the same pitch
+        dx3 = place(torch.zeros_like(x))
+        sr.precond_layer_norm_grad(pc.h, *args, dx3, dw2, db=db, dresidual=d_dr)
+        assert bool(((dx3.cpu().double() - wx).abs() <= tol + (E16 * (wx.abs() + tol) if dtype == "bf16" else 0)).all())
+        assert bool(((dw2.cpu().double() - ww).abs() <= chain * (f(dy).abs() * n).sum(dim=0) + 1e-38).all())
+        assert bool(((db.cpu().double() - wb).abs() <= chain * f(dy).abs().sum(dim=0) + 1e-38).all())
     return dict(x=x, dy=dy, dr=dr, w=w, mean=mean, rstd=rstd, dx=dx, dw=dw, db=db)
 
 
@@ -235,7 +260,9 @@ def test_grad_against_differences(pc):
                                                    (2000, 1208, "bf16", 24), (320, 12288, "bf16", 0), (1500, 2052, "f32", 12),
                                                    (3700, 65, "bf16", 0), (3000, 200, "bf16", 0), (2500, 333, "f32", 0), (2500, 777, "bf16", 2),
                                                    (700, 6143, "bf16", 0), (900, 4097, "f32", 1), (330, 10001, "bf16", 0), (320, 9001, "f32", 3),
-                                                   (340, 16383, "bf16", 0), (5000, 130, "f32", 5), (1000, 3001, "bf16", 7)])
+                                                   (340, 16383, "bf16", 0), (5000, 130, "f32", 5), (1000, 3001, "bf16", 7),
+                                                   (310, 8200, "bf16", 40), (2000, 1004, "f32", 20), (900, 5000, "bf16", 40), (320, 15008, "bf16", 0),
+                                                   (330, 9996, "f32", 60), (170, 13012, "f32", 20)])
 def test_norm_many_rows(pc, rows, cols, dtype, pitch):
     """Enough rows for each group of threads to have several: rows copied through shared memory, more than its ring holds."""
     check_norm(pc, rows, cols, dtype, pitch=pitch)
@@ -246,7 +273,8 @@ def test_norm_many_rows(pc, rows, cols, dtype, pitch):
                                                    (400, 8192, "bf16", 0), (333, 6148, "f32", 4), (1000, 3004, "f32", 4), (2000, 1208, "bf16", 24),
                                                    (200, 8192, "f32", 0), (3000, 2056, "bf16", 8), (3700, 65, "bf16", 0), (3000, 200, "bf16", 0),
                                                    (2600, 333, "f32", 0), (2500, 777, "bf16", 2), (400, 8191, "bf16", 0), (900, 4097, "f32", 1),
-                                                   (5000, 130, "f32", 5), (1000, 3001, "bf16", 7), (400, 6001, "f32", 2)])
+                                                   (5000, 130, "f32", 5), (1000, 3001, "bf16", 7), (400, 6001, "f32", 2),
+                                                   (700, 4104, "bf16", 40), (1500, 3004, "f32", 20), (200, 8184, "bf16", 40), (2000, 1000, "bf16", 40)])
 def test_grad_many_rows(pc, rows, cols, dtype, pitch):
     check_grad(pc, rows, cols, dtype, True, pitch=pitch)
     c = check_grad(pc, rows, cols, dtype, False, pitch=pitch)

@@ -122,16 +122,17 @@ def test_policy_every_place(pc, vocab):
     check(pc, z, ids, adv, logp - 0.05, logp + 0.2, weight, pitch=1)
 
 
-def test_policy_masks(pc):
+@pytest.mark.parametrize("vocab", [701, 3001])
+def test_policy_masks(pc, vocab):
     """Rows of weight 0 and without a taken token are not read, whatever they hold; all rows masked; empty calls."""
-    z, ids, adv, old, ref, weight = inputs(60, 3001, "f32", 1.0)
+    z, ids, adv, old, ref, weight = inputs(60, vocab, "f32", 1.0)
     weight[::4] = 0
-    ids[1], ids[2], ids[3], ids[5] = -1, 3001, -100, 2 ** 40
+    ids[1], ids[2], ids[3], ids[5] = -1, vocab, -100, 2 ** 40
     z[0], z[1], z[2] = math.nan, math.inf, -math.inf
     adv[0], old[0], ref[4] = math.nan, math.inf, math.nan
-    live = ((ids >= 0) & (ids < 3001)) & (weight != 0)
+    live = ((ids >= 0) & (ids < vocab)) & (weight != 0)
     zz = torch.where(live[:, None], z, torch.zeros_like(z))
-    loss, logp, grad = (torch.full(s, math.nan, device="cuda") for s in ((60,), (60,), (60, 3001)))
+    loss, logp, grad = (torch.full(s, math.nan, device="cuda") for s in ((60,), (60,), (60, vocab)))
     sr.precond_policy(pc.h, z.cuda(), ids.cuda(), advantage=adv.cuda(), old_logp=old.cuda(), ref_logp=ref.cuda(), weight=weight.cuda(), kl=0.1,
                       loss=loss, logp=logp, dlogits=grad)
     assert bool(torch.isfinite(loss).all()) and bool(torch.isfinite(grad).all())
@@ -139,23 +140,24 @@ def test_policy_masks(pc):
     assert bool((grad.cpu()[live] != 0).any(dim=1).any())
     keep = live.nonzero()[:, 0]
     check(pc, zz[keep], ids[keep], adv[keep], old[keep], ref[keep], weight[keep])
-    check(pc, zz, ids.clamp(0, 3000), adv.nan_to_num(), old.nan_to_num(posinf=0.0), ref.nan_to_num(), torch.zeros(60))
-    e = torch.empty(0, 3001, device="cuda")
+    check(pc, zz, ids.clamp(0, vocab - 1), adv.nan_to_num(), old.nan_to_num(posinf=0.0), ref.nan_to_num(), torch.zeros(60))
+    e = torch.empty(0, vocab, device="cuda")
     none = torch.empty(0, device="cuda")
     sr.precond_policy(pc.h, e, torch.empty(0, dtype=torch.int64, device="cuda"), advantage=none, loss=none, dlogits=torch.empty_like(e))
 
 
-def test_policy_masked_vocabulary(pc):
+@pytest.mark.parametrize("vocab", [1000, 5000])
+def test_policy_masked_vocabulary(pc, vocab):
     """Forbidden tokens at -infinity or at the type's lowest value; a forbidden token that was taken all the same."""
     for dtype in ("bf16", "f32"):
-        z, ids, adv, old, ref, weight = inputs(24, 5000, dtype, 1.0, seed=9)
+        z, ids, adv, old, ref, weight = inputs(24, vocab, dtype, 1.0, seed=9)
         for low in (-math.inf, torch.finfo(TYPES[dtype]).min):
             m = z.clone()
             m[:, ::2] = low
             ids = ids // 2 * 2 + 1
-            ids[ids >= 5000] = 4999
+            ids[ids >= vocab] = vocab - 1
             logp = torch.log_softmax(m.double(), dim=1).gather(1, ids[:, None])[:, 0].float()
-            loss, lp, grad = (torch.full(s, math.nan, device="cuda") for s in ((24,), (24,), (24, 5000)))
+            loss, lp, grad = (torch.full(s, math.nan, device="cuda") for s in ((24,), (24,), (24, vocab)))
             grad = grad.to(TYPES[dtype])
             sr.precond_policy(pc.h, m.cuda(), ids.cuda(), advantage=adv.cuda(), old_logp=(logp - 0.05).cuda(), loss=loss, logp=lp, dlogits=grad)
             assert bool(((lp.cpu() - logp).abs() <= 1e-4).all()) and bool(torch.isfinite(loss).all())
@@ -168,19 +170,21 @@ def test_policy_masked_vocabulary(pc):
         assert bool((grad == 0).all()) and bool(torch.isfinite(loss).all())
 
 
-def test_policy_sure(pc):
+@pytest.mark.parametrize("vocab", [1000, 5000, 50001, 600001])
+def test_policy_sure(pc, vocab):
     """A policy that is sure of the taken token: log q and 1 - q keep their digits, where 1 - q is far below fp32's step
     at 1 and where q is 1 to the last bit."""
-    z = torch.zeros(6, 1000)
-    ids = torch.tensor([0, 999, 500, 3, 64, 8])
+    z = torch.zeros(6, vocab)
+    ids = torch.tensor([0, vocab - 1, vocab // 2, 3, 64, 8])
     gap = torch.tensor([20.0, 30.0, 50.0, 80.0, 5.0, 200.0])
     z[torch.arange(6), ids] = gap
     adv = torch.ones(6)
-    loss, logp, grad = (torch.full(s, math.nan, device="cuda") for s in ((6,), (6,), (6, 1000)))
+    loss, logp, grad = (torch.full(s, math.nan, device="cuda") for s in ((6,), (6,), (6, vocab)))
     sr.precond_policy(pc.h, z.cuda(), ids.cuda(), advantage=adv.cuda(), loss=loss, logp=logp, dlogits=grad)
-    others = 999 * torch.exp(-gap.double())
+    others = (vocab - 1) * torch.exp(-gap.double())
     want = -torch.log1p(others)
-    tol = 2.0 ** -20 + 4 * E * gap.double()                         # of the powers of 2; the rest is E a step
+    # of the powers of 2; the rest is E a step, of which a thread's sum has vocab / 2048 + 64
+    tol = 2.0 ** -20 + 4 * E * gap.double() + (vocab / 2048 + 64) * E
     assert bool(((logp.cpu().double() - want).abs() <= (tol + 16 * E) * want.abs() + 1e-38).all())
     one = grad.cpu().double()[torch.arange(6), ids]
     rest = -others / (1 + others)
@@ -189,9 +193,29 @@ def test_policy_sure(pc):
     z[0, 1] = math.inf
     sr.precond_policy(pc.h, z.cuda(), ids.cuda(), advantage=adv.cuda(), loss=loss, logp=logp, dlogits=grad)
     assert bool(logp.isnan().all()) and bool(loss.isnan().all()) and bool(grad.isnan().any(dim=1).all())
-    one = torch.full((3, 70), -math.inf, device="cuda")
+    one = torch.full((3, vocab), -math.inf, device="cuda")
     sr.precond_policy(pc.h, one, torch.zeros(3, dtype=torch.int64, device="cuda"), logp=logp[:3])
     assert bool(logp[:3].isnan().all())
+
+
+@pytest.mark.parametrize("vocab,dtype", [(700, "bf16"), (3001, "bf16"), (2003, "f32"), (50001, "f32"), (500003, "f32")])
+def test_policy_gradient_elsewhere(pc, vocab, dtype):
+    """Gradients whose rows begin at other places than the logits': beside vectors, odd pitches, a slice of the logits' own buffer."""
+    z, ids, adv, old, ref, weight = inputs(9, vocab, dtype, 1.0, seed=4)
+    one = check(pc, z, ids, adv, old, ref, weight)
+    kw = dict(advantage=adv.cuda(), old_logp=old.cuda(), ref_logp=ref.cuda(), weight=weight.cuda(), clip_low=LOW, clip_high=HIGH, kl=0.05)
+    for offset, pitch in ((1, 0), (3, 5), (0, 2)):
+        dz = P.pitched(torch.zeros_like(z), vocab + pitch, offset=offset)
+        loss = torch.empty(9, device="cuda")
+        sr.precond_policy(pc.h, z.cuda(), ids.cuda(), loss=loss, dlogits=dz, **kw)
+        assert torch.equal(loss, one[0]) and torch.equal(dz, one[2])
+    both = torch.zeros(9, 2 * vocab + 1, dtype=z.dtype, device="cuda")
+    both[:, :vocab] = z.cuda()
+    sr.precond_policy(pc.h, both[:, :vocab], ids.cuda(), loss=loss, dlogits=both[:, vocab + 1:], **kw)
+    assert bool((both[:, vocab] == 0).all()) and torch.equal(both[:, :vocab], z.cuda())
+    # the rows' vectors begin elsewhere, so that sums are joined in another order
+    tol = 1e-5 * one[2].abs().float() + 2.0 ** -7 * (one[2].abs().float() if dtype == "bf16" else 0) + 1e-9
+    assert bool(((both[:, vocab + 1:].float() - one[2].float()).abs() <= tol).all())
 
 
 def test_policy_bounds(pc):
