@@ -490,12 +490,13 @@ int precond_policy(precond_t h, const void* logits, int dtype, int64_t rows, int
 typedef struct precond_list* precond_list_t;
 int precond_list_create(precond_list_t* out, int count, void* const tensors[], const int dtypes[], const int64_t sizes[]);
 int precond_list_destroy(precond_list_t list);            /* NULL is accepted; captured calls do not need the list */
-int64_t precond_list_workspace(precond_list_t list);      /* bytes for the calls below; -1: NULL */
+int64_t precond_list_workspace(precond_list_t list);      /* bytes for the calls below, 0 for a short list; -1: NULL */
 
 /*
  * *norm = sqrt(sum of the squares of all elements of the list), for any finite elements; infinite beyond fp32's
  * range, and not a number where an element is not.
- *   workspace : precond_list_workspace bytes, 16-byte aligned, in use until the call's work has completed
+ *   workspace : precond_list_workspace bytes, 16-byte aligned, in use until the call's work has completed; may be NULL
+ *               where that is 0
  */
 int precond_grad_norm(precond_t h, precond_list_t list, float* norm, void* workspace, int64_t workspace_bytes, void* stream);
 

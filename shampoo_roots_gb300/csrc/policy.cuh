@@ -20,11 +20,12 @@
 // elements: 824 us.)
 //
 // Rows of up to 4 KB are a warp's, in registers, and a warp goes from row to row
-// (4013 x 1774 bf16 8.3 us, with a block a row 15.2).
+// (4013 x 1774 bf16 8.3 us, with a block a row 15.2).  Few rows, a block or less to
+// an SM, stay in registers too: less to begin with.
 //
 // Measured: 8192 x 131072 bf16 671 us, 89 % of the copy bandwidth; 2999 x 50001
 // bf16 98 us, 85 %; 1000 x 32000 fp32 45 us, 79 % (four waves of blocks and the
-// first one's latency); scoring 24 x 50001 4.3 us.
+// first one's latency); scoring 24 x 50001 3.3 us (the host's call 3.4).
 //
 // The taken token is left out of the streamed sum: with R the sum of the others,
 // s = -log(1 + R / e_id) and 1 - q_id = R / (R + e_id) keep their digits where the
@@ -179,6 +180,70 @@ __global__ void __launch_bounds__(256, 4) policy_warp_kernel(PolicyArgs a) {
     x.store(z, dz, sl, lane, 32, true, shift, c, r.g);
     if (vec >= 0 ? (vec & 31) == lane : x.at == id) set_float(dz + id, r.taken);
   }
+}
+
+// Few rows: a block alone on its SM has its part of a row, up to NV vectors a thread, in registers, which is quicker to
+// begin with than a copy to shared memory; every thread joins the sums and computes the loss, rather than wait for one.
+template <typename T, int NV>
+__global__ void __launch_bounds__(POLICY_THREADS, 1) policy_few_kernel(PolicyArgs a) {
+  namespace cg = cooperative_groups;
+  __shared__ float2 sums[8 * POLICY_THREADS / 32];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int parts = (int)cluster.num_blocks(), part = (int)cluster.block_rank();
+  const int tid = threadIdx.x, threads = blockDim.x, warps = threads >> 5, warp = tid >> 5, lane = tid & 31;
+  const int64_t row = blockIdx.x / parts;
+  const float c = LOG2E / a.tau;
+  begun_arrive(parts);
+  wait_for_previous();
+  let_next_start();
+  const T* z = reinterpret_cast<const T*>(a.z) + row * a.ldz;
+  T* dz = reinterpret_cast<T*>(a.dz) + row * a.lddz;
+  const Slice sl(z, (int)a.vocab, parts, part);
+  const float weight = a.weight ? a.weight[row] : 1.0f;
+  Part<T, NV> x;
+  x.at = sl.single(tid);
+  if (weight != 0.0f) x.load(z, sl, tid, threads);
+  const int id = policy_id(a, row);
+  const float advantage = a.advantage ? a.advantage[row] : 0.f, old = a.old ? a.old[row] : 0.f, ref = a.ref ? a.ref[row] : 0.f;
+  Shift shift(0.f, c);
+  if (weight == 0.0f || id < 0) {                        // uniform over the cluster
+    begun_wait(parts);
+    if (part == 0 && tid == 0) {
+      if (a.loss) a.loss[row] = 0.f;
+      if (a.logp) a.logp[row] = 0.f;
+    }
+    if (a.dz) x.store(z, dz, sl, tid, threads, false, shift, c, 0.f);
+    return;
+  }
+  const float taken = as_float(z[id]);                   // before anything is written: dz may be z
+  const int vec = id >= sl.body && id < sl.tail ? (id - sl.body) / LogitVec<T>::N : -1, element = (id - sl.body) % LogitVec<T>::N;
+  if (x.at == id) x.one = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+    if (tid + u * threads == vec) hide_element(x.w[u], element, z);
+  float m, s, loss, logp;
+  x.sums(z, sl, tid, threads, c, m, s);
+  join_warp(m, s, c);
+  begun_wait(parts);
+  if (lane < parts) *cluster.map_shared_rank(&sums[part * warps + warp], lane) = make_float2(m, s);
+  if (parts > 1) {
+    row_arrive(parts, true);
+    row_wait(parts, true);
+  } else {
+    __syncthreads();
+  }
+  join_sums(sums, parts * warps, m, s, c);
+  const PolicyRow r = policy_result(a, c, weight, advantage, old, ref, taken, m, s, loss, logp);
+  if (part == 0 && tid == 0) {
+    if (a.loss) a.loss[row] = loss;
+    if (a.logp) a.logp[row] = logp;
+  }
+  if (!a.dz) return;
+  shift.b = r.b;
+  shift.k = r.k;
+  x.store(z, dz, sl, tid, threads, true, shift, c, r.g);
+  // the taken token's, after the vector that it lies in, by the same thread
+  if (vec >= 0 ? vec % threads == tid : x.at == id) set_float(dz + id, r.taken);
 }
 
 // Longer rows.  KEPT: a block's part of the row lies in its shared memory; otherwise the row is read twice.

@@ -126,20 +126,32 @@ const PolicyKernel policy_warp_kernels[2][4] = {
     {policy_warp_kernel<float, 1>, policy_warp_kernel<float, 2>, policy_warp_kernel<float, 4>, policy_warp_kernel<float, 8>},
     {policy_warp_kernel<__nv_bfloat16, 1>, policy_warp_kernel<__nv_bfloat16, 2>, policy_warp_kernel<__nv_bfloat16, 4>,
      policy_warp_kernel<__nv_bfloat16, 8>}};
-// Blocks of a row and threads of a block.  A part takes at most what lets an SM hold three blocks (8192 x 131072 bf16 by
-// parts of 64 KB 673 us, of 32 KB 707, of 128 KB 893; 1900 x 151936 by 74 KB 188, by 37 KB 199); a few rows take more
-// blocks, each with at least 8192 logits.  Threads have 192 bytes each, up to 256 of them (8192 x 8000 bf16, 16 KB: 96
-// threads 45 us, 128 47, 256 62, 512 99; 2999 x 50001: 256 threads 98 us, 512 118); a block alone on its SM 32 bytes.
-struct PolicyShape { int parts, threads, bytes; };   // bytes: of a part in shared memory, or 0: rows read twice
+const PolicyKernel policy_few_kernels[2][4] = {
+    {policy_few_kernel<float, 1>, policy_few_kernel<float, 2>, policy_few_kernel<float, 4>, policy_few_kernel<float, 8>},
+    {policy_few_kernel<__nv_bfloat16, 1>, policy_few_kernel<__nv_bfloat16, 2>, policy_few_kernel<__nv_bfloat16, 4>,
+     policy_few_kernel<__nv_bfloat16, 8>}};
+// Blocks of a row, threads of a block, bytes of a part in shared memory.  A part takes at most what lets an SM hold three
+// blocks (8192 x 131072 bf16 by parts of 64 KB 671 us, of 32 KB 707, of 128 KB 893; 1900 x 151936 by 74 KB 188, by 37 KB
+// 199); a few rows take more blocks, each with at least 8192 logits.  Threads have 192 bytes each, up to 256 of them (8192 x
+// 8000 bf16, 16 KB: 96 threads 45 us, 128 47, 256 62, 512 99; 2999 x 50001: 256 threads 98 us, 512 118).  Blocks alone on
+// their SMs keep up to 64 KB in registers (24 x 50001 bf16: 3.9 us on the device, by shared memory 5.4; two to an SM, 200 x
+// 10000 fp32, 7.0 and 6.3).
+struct PolicyShape { PolicyKernel kernel; int parts, threads, bytes; };
 PolicyShape policy_shape(int64_t rows, int64_t vocab, int dtype) {
   const int64_t sz = (int64_t)size_of(dtype), third = 76288;
+  const bool bf16 = dtype == PRECOND_BF16;
   int parts = 1;
   auto bytes = [&]() { return ((vocab + parts - 1) / parts + 63) / 64 * 64 * sz; };
   while (parts < 8 && (bytes() > third || (rows * parts < 2 * PLAN_SMS && vocab / (parts * 2) >= 8192))) parts *= 2;
-  const int64_t each = bytes();
-  const bool alone = rows * parts <= PLAN_SMS;
-  const int threads = (int)std::min<int64_t>(alone ? 512 : 256, std::max<int64_t>(64, (each / (alone ? 32 : 192) + 31) / 32 * 32));
-  return {parts, threads, each <= POLICY_PART ? (int)each : 0};
+  const int64_t each = bytes(), vectors = each / 16;
+  if (rows * parts <= PLAN_SMS && vectors <= 8 * POLICY_THREADS) {
+    int i = 0;
+    while (vectors > POLICY_THREADS << i) ++i;
+    return {policy_few_kernels[bf16][i], parts, (int)std::max<int64_t>(64, ((vectors + (1 << i) - 1) / (1 << i) + 31) / 32 * 32), 0};
+  }
+  const int threads = (int)std::min<int64_t>(256, std::max<int64_t>(64, (each / 192 + 31) / 32 * 32));
+  return each <= POLICY_PART ? PolicyShape{policy_kernels[bf16][1], parts, threads, (int)each}
+                             : PolicyShape{policy_kernels[bf16][0], parts, threads, 0};
 }
 
 // ------------------------------------------------------------------------- lists of tensors
@@ -162,7 +174,7 @@ struct List {
   int size = 0;                                      // which of CLIP_SIZES
   std::vector<std::vector<char>> tables;
   std::vector<int64_t> pieces;                       // of each
-  int64_t bytes() const { return std::max<int64_t>(1, (int64_t)tables.size()) * CLIP_BLOCKS * (int64_t)sizeof(ClipSum); }
+  int64_t bytes() const { return is_short() ? 0 : (int64_t)tables.size() * CLIP_BLOCKS * (int64_t)sizeof(ClipSum); }
   bool meets(const Range& r) const {
     if (!r.lo) return false;
     auto at = std::lower_bound(ranges.begin(), ranges.end(), r, [](const Range& a, const Range& b) { return a.hi <= b.lo; });
@@ -191,7 +203,7 @@ struct List {
     else if (size == 2) fill<CLIP_SIZES[2]>();
     else fill<CLIP_SIZES[3]>();
   }
-  bool is_short() const { return tables.size() == 1 && pieces[0] <= CLIP_SHORT; }
+  bool is_short() const { return tables.empty() || (tables.size() == 1 && pieces[0] <= CLIP_SHORT); }   // needs no workspace
 };
 
 int launch_list(Handle* h, const void* kernel, int grid, int cluster, void** args, cudaStream_t st) {
@@ -229,6 +241,10 @@ int scale(Handle* h, const List& l, const ClipSum* partial, int sums, float max_
   return PRECOND_OK;
 }
 int short_list(Handle* h, const List& l, float max_norm, float* norm, cudaStream_t st) {
+  if (l.tables.empty()) {
+    OP_CK(cudaMemsetAsync(norm, 0, 4, st));
+    return PRECOND_OK;
+  }
   void* args[] = {(void*)l.tables[0].data(), &max_norm, &norm};
   return launch_list(h, clip_of[l.size].one, CLIP_CLUSTER, CLIP_CLUSTER, args, st);
 }
@@ -440,8 +456,7 @@ int precond_policy(precond_t ph, const void* logits, int dtype, int64_t rows, in
     return PRECOND_OK;
   }
   const PolicyShape s = policy_shape(rows, vocab, dtype);
-  OP_CK(launch(policy_kernels[dtype == PRECOND_BF16][s.bytes > 0], dim3((unsigned)(rows * s.parts)), dim3(s.threads), (size_t)s.bytes,
-               (cudaStream_t)stream, s.parts, a));
+  OP_CK(launch(s.kernel, dim3((unsigned)(rows * s.parts)), dim3(s.threads), (size_t)s.bytes, (cudaStream_t)stream, s.parts, a));
   ++h->launches;
   return PRECOND_OK;
 }
@@ -511,7 +526,6 @@ int precond_clip_grads(precond_t ph, precond_list_t list, float max_norm, float*
   ClipSum* partial = reinterpret_cast<ClipSum*>(workspace);
   if (!given && l->is_short()) return short_list(h, *l, max_norm, norm, st);
   if (!given && (rc = squares(h, *l, partial, &sums, st))) return rc;
-  if (!given && l->tensors.empty()) return ::total(h, partial, 0, norm, st);
   return scale(h, *l, partial, sums, max_norm, norm, st);
 }
 

@@ -95,13 +95,16 @@ def test_policy(pc, rows, vocab, dtype):
 
 @pytest.mark.parametrize("rows,vocab,dtype,pitch", [(400, 1000, "bf16", 0), (700, 333, "f32", 3), (350, 2047, "bf16", 1), (31, 50257, "bf16", 2),
                                                     (12, 70001, "f32", 1), (6, 400001, "bf16", 7), (5, 280003, "f32", 5), (320, 9000, "f32", 0), (5100, 130, "bf16", 0),
-                                                    (5000, 70, "f32", 1), (40, 2048, "bf16", 0), (40, 2049, "bf16", 3), (60, 1024, "f32", 2)])
+                                                    (5000, 70, "f32", 1), (40, 2048, "bf16", 0), (40, 2049, "bf16", 3), (60, 1024, "f32", 2),
+                                                    (60, 50001, "bf16", 1), (90, 20003, "f32", 1), (25, 131072, "bf16", 0), (160, 5000, "bf16", 3),
+                                                    (22, 140001, "f32", 1), (40, 300001, "bf16", 1), (320, 2050, "bf16", 0)])
 def test_policy_layouts(pc, rows, vocab, dtype, pitch):
-    """Rows at every alignment, on a warp that takes several, on 1 to 8 blocks, and read twice."""
+    """Rows at every alignment, on a warp that takes several, on 1 to 8 blocks, few and many of them, and read twice."""
     check(pc, *inputs(rows, vocab, dtype, 1.3), tau=1.3, pitch=pitch)
 
 
-@pytest.mark.parametrize("rows,vocab,dtype", [(50, 1000, "bf16"), (9, 50001, "f32"), (3, 131072, "bf16"), (2, 300001, "f32"), (2, 700001, "bf16")])
+@pytest.mark.parametrize("rows,vocab,dtype", [(50, 1000, "bf16"), (9, 50001, "f32"), (3, 131072, "bf16"), (2, 300001, "f32"), (2, 700001, "bf16"), (2, 500003, "f32"),
+                                              (200, 6001, "bf16"), (45, 50001, "bf16"), (3000, 100, "f32")])
 def test_policy_in_place(pc, rows, vocab, dtype):
     a = inputs(rows, vocab, dtype, 1.0)
     one = check(pc, *a)
@@ -122,7 +125,7 @@ def test_policy_every_place(pc, vocab):
     check(pc, z, ids, adv, logp - 0.05, logp + 0.2, weight, pitch=1)
 
 
-@pytest.mark.parametrize("vocab", [701, 3001])
+@pytest.mark.parametrize("vocab", [701, 3001, 40001])
 def test_policy_masks(pc, vocab):
     """Rows of weight 0 and without a taken token are not read, whatever they hold; all rows masked; empty calls."""
     z, ids, adv, old, ref, weight = inputs(60, vocab, "f32", 1.0)
@@ -170,23 +173,24 @@ def test_policy_masked_vocabulary(pc, vocab):
         assert bool((grad == 0).all()) and bool(torch.isfinite(loss).all())
 
 
-@pytest.mark.parametrize("vocab", [1000, 5000, 50001, 600001])
-def test_policy_sure(pc, vocab):
+@pytest.mark.parametrize("vocab,times", [(1000, 1), (5000, 1), (5000, 30), (50001, 1), (50001, 8), (600001, 1)])
+def test_policy_sure(pc, vocab, times):
     """A policy that is sure of the taken token: log q and 1 - q keep their digits, where 1 - q is far below fp32's step
     at 1 and where q is 1 to the last bit."""
-    z = torch.zeros(6, vocab)
-    ids = torch.tensor([0, vocab - 1, vocab // 2, 3, 64, 8])
-    gap = torch.tensor([20.0, 30.0, 50.0, 80.0, 5.0, 200.0])
-    z[torch.arange(6), ids] = gap
-    adv = torch.ones(6)
-    loss, logp, grad = (torch.full(s, math.nan, device="cuda") for s in ((6,), (6,), (6, vocab)))
+    n = 6 * times
+    z = torch.zeros(n, vocab)
+    ids = torch.tensor([0, vocab - 1, vocab // 2, 3, 64, 8]).repeat(times)
+    gap = torch.tensor([20.0, 30.0, 50.0, 80.0, 5.0, 200.0]).repeat(times)
+    z[torch.arange(n), ids] = gap
+    adv = torch.ones(n)
+    loss, logp, grad = (torch.full(s, math.nan, device="cuda") for s in ((n,), (n,), (n, vocab)))
     sr.precond_policy(pc.h, z.cuda(), ids.cuda(), advantage=adv.cuda(), loss=loss, logp=logp, dlogits=grad)
     others = (vocab - 1) * torch.exp(-gap.double())
     want = -torch.log1p(others)
     # of the powers of 2; the rest is E a step, of which a thread's sum has vocab / 2048 + 64
     tol = 2.0 ** -20 + 4 * E * gap.double() + (vocab / 2048 + 64) * E
     assert bool(((logp.cpu().double() - want).abs() <= (tol + 16 * E) * want.abs() + 1e-38).all())
-    one = grad.cpu().double()[torch.arange(6), ids]
+    one = grad.cpu().double()[torch.arange(n), ids]
     rest = -others / (1 + others)
     assert bool(((one - rest).abs() <= (tol + 16 * E) * rest.abs() + 1e-38).all())
     z[:, 1] = math.nan                                              # and what is not a number shows

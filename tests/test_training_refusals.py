@@ -140,14 +140,14 @@ def test_list_refuses_pointers():
 
 @pytest.mark.parametrize("good", [
     ([], [], []), ([BASE["a"], None], [0, 1], [4, 0]), ([BASE["a"], BASE["a"] + 16], [0, 0], [4, 4]), ([BASE["b"], BASE["a"]], [0, 0], [4, 0x4000000]),
-    ([BASE["a"] + 2 * i for i in range(3000)], [1] * 3000, [1] * 3000)])
+    ([BASE["a"] + 2 * i for i in range(3000)], [1] * 3000, [1] * 3000), ([BASE["a"], BASE["b"]], [0, 1], [1 << 20, 5])])
 def test_list_calls(h, good):
     lib = sr.load()
     code, l = make(*good)
     assert code == sr.OK
     lib.precond_list_workspace.restype, lib.precond_list_workspace.argtypes = i64, [P]
     need = lib.precond_list_workspace(l)
-    assert need > 0 and need % 8 == 0
+    assert need % 8 == 0 and (need > 0) == (sum(good[2]) > 1 << 20 or len(good[0]) > 128)
 
     def total(hh=h, norm=BASE["k"], ws=BASE["l"], bytes_=need):
         return lib.precond_grad_norm(P(hh), l, P(norm), P(ws), i64(bytes_), P(0))
@@ -158,11 +158,12 @@ def test_list_calls(h, good):
     assert total() == clip() == clip(most=0.0) == clip(most=float("inf")) == sr.ENODEV
     assert clip(given=1, ws=None, bytes_=0) == sr.ENODEV
     for call in (total, clip):
-        for bad in (dict(hh=None), dict(norm=None), dict(norm=BASE["k"] + 2), dict(ws=None), dict(ws=BASE["l"] + 8), dict(bytes_=need - 1),
-                    dict(norm=BASE["l"] + 8)):
+        for bad in (dict(hh=None), dict(norm=None), dict(norm=BASE["k"] + 2)):
             assert call(**bad) == sr.EINVAL, bad
+        for bad in (dict(ws=None), dict(ws=BASE["l"] + 8), dict(bytes_=need - 1), dict(norm=BASE["l"] + 8)):
+            assert call(**bad) == (sr.EINVAL if need else sr.ENODEV), bad
         if good[0]:
-            assert call(norm=good[0][0]) == sr.EINVAL and call(ws=good[0][0] - 16) == sr.EINVAL
+            assert call(norm=good[0][0]) == sr.EINVAL and call(ws=good[0][0] - 16) == (sr.EINVAL if need else sr.ENODEV)
     for bad in (dict(most=-1.0), dict(most=float("nan"))):
         assert clip(**bad) == sr.EINVAL
     assert lib.precond_list_destroy(l) == sr.OK
@@ -210,4 +211,4 @@ def test_binding_refuses(h):
     with pytest.raises(TypeError):
         sr.precond_clip_grads(h, [x], "1", norm, **ok)
     l = sr.TensorList(t for t in (x, w))
-    assert len(l) == 2 and l.workspace > 0 and l.tensors[0] is x
+    assert len(l) == 2 and l.workspace == 0 and l.tensors[0] is x and sr.TensorList([torch.zeros(1 << 20)]).workspace > 0
