@@ -92,11 +92,12 @@ cudaError_t launch_layer_grad(const LayerGradArgs& a, const RowShape& s, unsigne
 // 4096 fp32 53 and 60) or rows are short, else two or four, whose groups are more (6000 x 8192 bf16: 66, 60 and 62;
 // 4000 x 12288: 57, 57 and 52).
 constexpr int STREAM_BYTES = 225 << 10;
-struct StreamKernels { void (*norm[3])(LayerNormArgs, int); void (*grad)(LayerGradArgs, int); };    // norm: 1, 2, 4 vectors
-template <typename T>
-StreamKernels stream_kernels() {
-  return {{layer_norm_stream_kernel<T, 1>, layer_norm_stream_kernel<T, 2>, layer_norm_stream_kernel<T, 4>}, layer_grad_stream_kernel<T>};
-}
+typedef void (*StreamNorm)(LayerNormArgs, int);
+typedef void (*StreamGrad)(LayerGradArgs, int);
+const StreamNorm stream_norm_kernels[2][3] = {                   // 1, 2, 4 vectors a thread
+    {layer_norm_stream_kernel<float, 1>, layer_norm_stream_kernel<float, 2>, nullptr},
+    {layer_norm_stream_kernel<__nv_bfloat16, 1>, layer_norm_stream_kernel<__nv_bfloat16, 2>, layer_norm_stream_kernel<__nv_bfloat16, 4>}};
+const StreamGrad stream_grad_kernels[2] = {layer_grad_stream_kernel<float>, layer_grad_stream_kernel<__nv_bfloat16>};
 struct StreamShape { int threads, rows, vectors, stages; size_t bytes; };
 StreamShape stream_shape(int64_t cols, int dtype, int inputs, bool grad, int64_t rows, int sms) {
   StreamShape s = {0, 0, 1, 0, 0};
@@ -158,12 +159,15 @@ PolicyShape policy_shape(int64_t rows, int64_t vocab, int dtype) {
 // Tensors of a launch: tables of 0.6, 2.5, 10 and 28 KB of parameters.
 constexpr int CLIP_SIZES[4] = {32, 128, 512, 1400};
 constexpr int CLIP_BLOCKS = 2 * PLAN_SMS;
-constexpr int CLIP_SHORT = 128;                      // pieces of a list that one cluster takes (1 MB: two launches 7.1 us, one 7.2; 128 KB 7.2 and 6.0)
 
+// A short list has at most CLIP_SHORT tensors: the larger tables need no kernel for it.
+constexpr int CLIP_SHORT = 128;                      // pieces of a list that one cluster takes (1 MB: two launches 7.1 us, one 7.2; 128 KB 7.2 and 6.0)
 struct ClipKernels { const void *norm, *scale, *one; };
 template <int MAX>
 ClipKernels clip_kernels() {
-  return {(const void*)clip_norm_kernel<MAX>, (const void*)clip_scale_kernel<MAX>, (const void*)clip_short_kernel<MAX>};
+  ClipKernels k = {(const void*)clip_norm_kernel<MAX>, (const void*)clip_scale_kernel<MAX>, nullptr};
+  if constexpr (MAX <= CLIP_SHORT) k.one = (const void*)clip_short_kernel<MAX>;
+  return k;
 }
 const ClipKernels clip_of[4] = {clip_kernels<32>(), clip_kernels<128>(), clip_kernels<512>(), clip_kernels<1400>()};
 
@@ -270,9 +274,10 @@ cudaError_t precond::training_attributes() {
   if (e == cudaSuccess) e = LayerKernels<float, false>::attributes();
   if (e == cudaSuccess) e = LayerKernels<__nv_bfloat16, true>::attributes();
   if (e == cudaSuccess) e = LayerKernels<__nv_bfloat16, false>::attributes();
-  for (const StreamKernels& k : {stream_kernels<float>(), stream_kernels<__nv_bfloat16>()}) {
-    for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = cudaFuncSetAttribute(k.norm[i], cudaFuncAttributeMaxDynamicSharedMemorySize, STREAM_BYTES);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k.grad, cudaFuncAttributeMaxDynamicSharedMemorySize, STREAM_BYTES);
+  for (int i = 0; i < 2; ++i) {
+    for (const StreamNorm k : stream_norm_kernels[i])
+      if (k && e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, STREAM_BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(stream_grad_kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, STREAM_BYTES);
   }
   for (int i = 0; i < 2 && e == cudaSuccess; ++i)
     e = cudaFuncSetAttribute(policy_kernels[i][1], cudaFuncAttributeMaxDynamicSharedMemorySize, POLICY_PART);
@@ -318,7 +323,7 @@ int precond_layer_norm(precond_t ph, const void* x, const void* residual, const 
                    sector_rows(y, ldy, dtype);
   const StreamShape f = vec ? stream_shape(cols, dtype, residual ? 2 : 1, false, rows, h->num_sms) : StreamShape{};
   if (f.stages) {
-    OP_CK(launch((dtype == PRECOND_BF16 ? stream_kernels<__nv_bfloat16>() : stream_kernels<float>()).norm[f.vectors / 2], dim3((unsigned)h->num_sms), dim3(f.threads, f.rows), f.bytes, (cudaStream_t)stream, 1, a, f.stages));
+    OP_CK(launch(stream_norm_kernels[dtype == PRECOND_BF16][f.vectors / 2], dim3((unsigned)h->num_sms), dim3(f.threads, f.rows), f.bytes, (cudaStream_t)stream, 1, a, f.stages));
     ++h->launches;
     return PRECOND_OK;
   }
@@ -399,8 +404,7 @@ int precond_layer_norm_grad(precond_t ph, const void* dy, const void* x, const v
   const StreamShape f = vec && !whole ? stream_shape(cols, dtype, dresidual ? 3 : 2, true, rows, sms) : StreamShape{};
   if (f.stages) {
     grid = (unsigned)sms;                // the rows' shapes have at least as many groups
-    OP_CK(launch(dtype == PRECOND_BF16 ? layer_grad_stream_kernel<__nv_bfloat16> : layer_grad_stream_kernel<float>, dim3(grid),
-                 dim3(f.threads, f.rows), f.bytes, st, 1, a, f.stages));
+    OP_CK(launch(stream_grad_kernels[dtype == PRECOND_BF16], dim3(grid), dim3(f.threads, f.rows), f.bytes, st, 1, a, f.stages));
   } else if (dtype == PRECOND_BF16)
     OP_CK((vec ? launch_layer_grad<__nv_bfloat16, true>(a, s, grid, st) : launch_layer_grad<__nv_bfloat16, false>(a, s, grid, st)));
   else
