@@ -20,7 +20,9 @@
 // elements: 824 us.)
 //
 // Rows of up to 4 KB are a warp's, in registers, and a warp goes from row to row
-// (4013 x 1774 bf16 8.3 us, with a block a row 15.2).  Few rows, a block or less to
+// (4013 x 1774 bf16 8.3 us, with a block a row 15.2); rows of up to 24 KB are a warp's
+// in shared memory, if there are many (8192 x 4000 bf16 23.4 us, with several warps to a
+// row 31.4).  Few rows, a block or less to
 // an SM, stay in registers too: less to begin with.
 //
 // Measured: 8192 x 131072 bf16 671 us, 89 % of the copy bandwidth; 2999 x 50001
@@ -133,6 +135,60 @@ __device__ __forceinline__ PolicyRow policy_result(const PolicyArgs& a, float c,
   return {shift.b, shift.k, -slope / total, slope * (rest / total)};
 }
 
+// (maximum, sum of 2^(z c - k)) of a warp's share of n vectors and its single elements, from shared memory in two passes:
+// the maximum, which is one shift for the warp, then the sum.
+template <typename T>
+__device__ __forceinline__ void policy_sums(const uint4* kept, int n, int tid, int threads, float open, float c, float& m, float& s) {
+  using V = LogitVec<T>;
+  auto load = [&](int i) { return kept[i]; };
+  m = open;
+  policy_each<POLICY_U>(n, tid, threads, load, [&](int, uint4 w) { m = largest_of(w, m, (const T*)nullptr); });
+  m = warp_max_fast(m);
+  s = 0.f;
+  if (m == -INFINITY) return;
+  const Shift mine(m, c);
+  f2 e = f2_of(ex2(mine(open, c)), 0.f);
+  auto add = [&](auto far) {
+    policy_each<POLICY_U>(n, tid, threads, load, [&](int, uint4 w) {
+      float f[V::N];
+      V::unpack(w, f);
+      distill_powers<V::N, decltype(far)::value, false>(f, mine, c);
+#pragma unroll
+      for (int i = 0; i < V::N; i += 2) e = add2(e, f2_of(f[i], f[i + 1]));
+    });
+  };
+  if (mine.b != 0.f) add(std::true_type());
+  else add(std::false_type());
+  s = warp_sum(sum2(e));
+}
+// Vector i of a row's gradient, at `body`, which may lie at any element.
+template <typename T>
+__device__ __forceinline__ void policy_put(T* body, bool aligned, int i, uint4 w) {
+  if (aligned) {
+    reinterpret_cast<uint4*>(body)[i] = w;
+  } else {
+    float f[LogitVec<T>::N];
+    LogitVec<T>::unpack(w, f);
+#pragma unroll
+    for (int e = 0; e < LogitVec<T>::N; ++e) set_float(body + i * LogitVec<T>::N + e, f[e]);
+  }
+}
+// The gradient of n vectors that `load` gives.
+template <typename T, typename L>
+__device__ __forceinline__ void policy_store(T* body, bool aligned, int n, int tid, int threads, L load, const PolicyRow& r, const Shift& shift,
+                                             float c) {
+  auto write = [&](auto rare) {
+    policy_each<POLICY_U>(n, tid, threads, load, [&](int i, uint4 w) {
+      float f[LogitVec<T>::N];
+      LogitVec<T>::unpack(w, f);
+      distill_dense<T>(f, shift, c, r.g, decltype(rare)::value);
+      policy_put(body, aligned, i, LogitVec<T>::pack(f));
+    });
+  };
+  if (shift.b != 0.f || fabsf(r.g) > 1e6f) write(std::true_type());
+  else write(std::false_type());
+}
+
 // Short rows, up to 32 NV vectors: a warp has each in its registers, and goes on to another.
 template <typename T, int NV>
 __global__ void __launch_bounds__(256, 4) policy_warp_kernel(PolicyArgs a) {
@@ -180,6 +236,77 @@ __global__ void __launch_bounds__(256, 4) policy_warp_kernel(PolicyArgs a) {
     x.store(z, dz, sl, lane, 32, true, shift, c, r.g);
     if (vec >= 0 ? (vec & 31) == lane : x.at == id) set_float(dz + id, r.taken);
   }
+}
+
+// Rows of middle length: a warp has a block to itself and copies its row to shared memory, so that nothing waits for
+// another warp; one row a block, as the next begins when any other ends.  All that the row needs beside its logits is
+// loaded before the copy begins (after it, one load waits for another: 8192 x 4000 bf16 24.6 us, where this takes 23.4).
+template <typename T>
+__global__ void __launch_bounds__(32, 32) policy_row_kernel(PolicyArgs a) {
+  using V = LogitVec<T>;
+  extern __shared__ __align__(16) uint8_t policy_smem[];
+  __shared__ __align__(8) unsigned long long arrived;
+  const int lane = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const float c = LOG2E / a.tau;
+  const uint32_t bar = smem_u32(&arrived);
+  if (lane == 0) {
+    mbar_init(bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
+  wait_for_previous();
+  let_next_start();
+  const float weight = a.weight ? a.weight[row] : 1.0f;
+  const int id = policy_id(a, row);
+  const float advantage = a.advantage ? a.advantage[row] : 0.f, old = a.old ? a.old[row] : 0.f, ref = a.ref ? a.ref[row] : 0.f;
+  const T* z = reinterpret_cast<const T*>(a.z) + row * a.ldz;
+  T* dz = reinterpret_cast<T*>(a.dz) + row * a.lddz;
+  const Slice sl(z, (int)a.vocab, 1, 0);
+  const int single = sl.single(lane), n = sl.nvec;
+  const bool aligned = (reinterpret_cast<uintptr_t>(dz + sl.body) & 15) == 0;
+  if (weight == 0.0f || id < 0) {
+    if (lane == 0) {
+      if (a.loss) a.loss[row] = 0.f;
+      if (a.logp) a.logp[row] = 0.f;
+    }
+    if (a.dz) {
+      for (int i = lane; i < n; i += 32) policy_put(dz + sl.body, aligned, i, make_uint4(0, 0, 0, 0));
+      if (single >= 0) set_float(dz + single, 0.f);
+    }
+    return;
+  }
+  if (n && lane == 0) {
+    mbar_expect_tx(bar, n * 16);
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(smem_u32(policy_smem)), "l"(z + sl.body), "r"(n * 16), "r"(bar) : "memory");
+  }
+  const int vec = id >= sl.body && id < sl.tail ? (id - sl.body) / V::N : -1;
+  const float one = single >= 0 ? as_float(z[single]) : -INFINITY, open = single == id ? -INFINITY : one;
+  const float taken = as_float(z[id]);
+  uint4* kept = reinterpret_cast<uint4*>(policy_smem);
+  const bool lost = n && !mbar_wait_own(bar, 0, nullptr) && !mbar_wait_own(bar, 0, nullptr);
+  if (vec >= 0 && (vec & 31) == lane) {                  // a vector that this lane alone reads
+    uint4 v = kept[vec];
+    hide_element(v, (id - sl.body) % V::N, z);
+    kept[vec] = v;
+  }
+  float m, s, loss, logp;
+  policy_sums<T>(kept, n, lane, 32, open, c, m, s);
+  if (lost) m = s = __builtin_nanf("");
+  const PolicyRow r = policy_result(a, c, weight, advantage, old, ref, taken, m, s, loss, logp);
+  if (lane == 0) {
+    if (a.loss) a.loss[row] = loss;
+    if (a.logp) a.logp[row] = logp;
+  }
+  if (!a.dz) return;
+  Shift shift(0.f, c);
+  shift.b = r.b;
+  shift.k = r.k;
+  __syncwarp();                                          // every lane has read the taken token: dz may be z
+  policy_store<T>(dz + sl.body, aligned, n, lane, 32, [&](int i) { return kept[i]; }, r, shift, c);
+  if (single >= 0) set_float(dz + single, r.g * ex2(shift(one, c)));
+  if (vec >= 0 ? (vec & 31) == lane : single == id) set_float(dz + id, r.taken);
 }
 
 // Few rows: a block alone on its SM has its part of a row, up to NV vectors a thread, in registers, which is quicker to
@@ -285,16 +412,6 @@ __global__ void __launch_bounds__(POLICY_THREADS, 3) policy_kernel(PolicyArgs a)
   const int id = policy_id(a, row);
   const bool reads = weight != 0.0f && id >= 0;          // uniform over the cluster
   const bool aligned = (reinterpret_cast<uintptr_t>(dz + sl.body) & 15) == 0;
-  auto put = [&](int i, uint4 w) {
-    if (aligned) {
-      reinterpret_cast<uint4*>(dz + sl.body)[i] = w;
-    } else {
-      float f[V::N];
-      V::unpack(w, f);
-#pragma unroll
-      for (int e = 0; e < V::N; ++e) set_float(dz + sl.body + i * V::N + e, f[e]);
-    }
-  };
   auto arrive = [&]() { return mbar_wait_own(smem_u32(&arrived), 0, nullptr) || mbar_wait_own(smem_u32(&arrived), 0, nullptr); };
   if (!reads) {
     begun_wait(parts);
@@ -304,7 +421,7 @@ __global__ void __launch_bounds__(POLICY_THREADS, 3) policy_kernel(PolicyArgs a)
       if (a.logp) a.logp[row] = 0.f;
     }
     if (a.dz) {
-      for (int i = tid; i < n; i += threads) put(i, make_uint4(0, 0, 0, 0));
+      for (int i = tid; i < n; i += threads) policy_put(dz + sl.body, aligned, i, make_uint4(0, 0, 0, 0));
       if (single >= 0) set_float(dz + single, 0.f);
     }
     return;
@@ -329,27 +446,7 @@ __global__ void __launch_bounds__(POLICY_THREADS, 3) policy_kernel(PolicyArgs a)
       hide_element(v, element, z);
       kept[vec] = v;
     }
-    auto load = [&](int i) { return kept[i]; };
-    m = open;
-    policy_each<POLICY_U>(n, tid, threads, load, [&](int, uint4 w) { m = largest_of(w, m, z); });
-    m = warp_max_fast(m);                                // one shift for the warp
-    s = 0.f;
-    if (m != -INFINITY) {
-      const Shift mine(m, c);
-      f2 e = f2_of(ex2(mine(open, c)), 0.f);
-      auto add = [&](auto far) {
-        policy_each<POLICY_U>(n, tid, threads, load, [&](int, uint4 w) {
-          float f[V::N];
-          V::unpack(w, f);
-          distill_powers<V::N, decltype(far)::value, false>(f, mine, c);
-#pragma unroll
-          for (int i = 0; i < V::N; i += 2) e = add2(e, f2_of(f[i], f[i + 1]));
-        });
-      };
-      if (mine.b != 0.f) add(std::true_type());
-      else add(std::false_type());
-      s = warp_sum(sum2(e));
-    }
+    policy_sums<T>(kept, n, tid, threads, open, c, m, s);
     if (lost) m = s = NOT_A_NUMBER;
   } else {
     const uint4* v = reinterpret_cast<const uint4*>(z + sl.body);
@@ -392,17 +489,8 @@ __global__ void __launch_bounds__(POLICY_THREADS, 3) policy_kernel(PolicyArgs a)
   Shift shift(0.f, c);
   shift.b = r.b;
   shift.k = r.k;
-  auto write = [&](auto rare) {
-    auto load = [&](int i) { return KEPT ? reinterpret_cast<const uint4*>(policy_smem)[i] : reinterpret_cast<const uint4*>(z + sl.body)[i]; };
-    policy_each<POLICY_U>(n, tid, threads, load, [&](int i, uint4 w) {
-      float f[V::N];
-      V::unpack(w, f);
-      distill_dense<T>(f, shift, c, r.g, decltype(rare)::value);
-      put(i, V::pack(f));
-    });
-  };
-  if (shift.b != 0.f || fabsf(r.g) > 1e6f) write(std::true_type());
-  else write(std::false_type());
+  const uint4* from = KEPT ? reinterpret_cast<const uint4*>(policy_smem) : reinterpret_cast<const uint4*>(z + sl.body);
+  policy_store<T>(dz + sl.body, aligned, n, tid, threads, [&](int i) { return from[i]; }, r, shift, c);
   if (single >= 0) set_float(dz + single, r.g * ex2(shift(one, c)));
   // the taken token's, after the vector that it lies in, by the same thread
   if (vec >= 0 ? vec % threads == tid : single == id) set_float(dz + id, r.taken);

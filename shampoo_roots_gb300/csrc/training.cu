@@ -120,13 +120,22 @@ StreamShape stream_shape(int64_t cols, int dtype, int inputs, bool grad, int64_t
 typedef void (*PolicyKernel)(PolicyArgs);
 const PolicyKernel policy_kernels[2][2] = {{policy_kernel<float, false>, policy_kernel<float, true>},
                                            {policy_kernel<__nv_bfloat16, false>, policy_kernel<__nv_bfloat16, true>}};
-// Bytes of a row that a warp takes: 1, 2, 4 or 8 vectors a lane (8192 x 1000 bf16 9.9 us, by blocks 18.3; of rows of 8 KB,
-// with 16 vectors, an SM holds half the warps: 8192 x 4000 33 us, by blocks 31).
+// Bytes of a row that a warp takes in registers: 1, 2, 4 or 8 vectors a lane (8192 x 1000 bf16 9.9 us, by blocks 18.3; of rows
+// of 8 KB, with 16 vectors, an SM holds half the warps: 8192 x 4000 33 us, by blocks 31).  From 2 KB on shared memory is
+// quicker with a gradient and slower without (8192 x 1500 bf16 15.6 and 12.6 us, scoring 9.0 and 9.2; 30000 x 1500 41 and 35,
+// scoring 26 and 31); the rule does not ask which, so that a token's log probability is the same in both.
 constexpr int64_t POLICY_WARP = 4096;
 const PolicyKernel policy_warp_kernels[2][4] = {
     {policy_warp_kernel<float, 1>, policy_warp_kernel<float, 2>, policy_warp_kernel<float, 4>, policy_warp_kernel<float, 8>},
     {policy_warp_kernel<__nv_bfloat16, 1>, policy_warp_kernel<__nv_bfloat16, 2>, policy_warp_kernel<__nv_bfloat16, 4>,
      policy_warp_kernel<__nv_bfloat16, 8>}};
+// Bytes of a row that a warp takes in shared memory, where there are more rows than SMs: half as many for fewer rows than 4
+// to an SM, whose warps are too few to hide each other's waits (by a block of several warps: 8192 x 2500 bf16 26.2 us, by a
+// warp 16.0; 8192 x 4000 31.4 and 23.4; 8192 x 10000 53.7 and 51.4, scoring 35.5 and 30.4; 8192 x 16000 78.6 and 82.6; 500 x
+// 4000 6.8 and 5.2, 500 x 8000 7.1 and 7.5; four warps to a block, or warps that go from row to row: 8192 x 8000 46 and 49
+// us, by one 42).
+constexpr int64_t POLICY_ROW = 24 << 10;
+const PolicyKernel policy_row_kernels[2] = {policy_row_kernel<float>, policy_row_kernel<__nv_bfloat16>};
 const PolicyKernel policy_few_kernels[2][4] = {
     {policy_few_kernel<float, 1>, policy_few_kernel<float, 2>, policy_few_kernel<float, 4>, policy_few_kernel<float, 8>},
     {policy_few_kernel<__nv_bfloat16, 1>, policy_few_kernel<__nv_bfloat16, 2>, policy_few_kernel<__nv_bfloat16, 4>,
@@ -150,7 +159,7 @@ PolicyShape policy_shape(int64_t rows, int64_t vocab, int dtype) {
     while (vectors > POLICY_THREADS << i) ++i;
     return {policy_few_kernels[bf16][i], parts, (int)std::max<int64_t>(64, ((vectors + (1 << i) - 1) / (1 << i) + 31) / 32 * 32), 0};
   }
-  const int threads = (int)std::min<int64_t>(256, std::max<int64_t>(64, (each / 192 + 31) / 32 * 32));
+  const int threads = (int)std::min<int64_t>(256, (each / 192 + 31) / 32 * 32);
   return each <= POLICY_PART ? PolicyShape{policy_kernels[bf16][1], parts, threads, (int)each}
                              : PolicyShape{policy_kernels[bf16][0], parts, threads, 0};
 }
@@ -451,11 +460,17 @@ int precond_policy(precond_t ph, const void* logits, int dtype, int64_t rows, in
   if (rc) return rc;
   const PolicyArgs a = {logits, ldz, ids, id_bits == 64, advantage, old_logp, kl != 0.f ? ref_logp : nullptr, weight, loss, logp, dlogits,
                         lddz, rows, vocab, temperature, clip_low, clip_high, kl};
-  if (vocab * (int64_t)sz <= POLICY_WARP) {
+  const int64_t bytes = vocab * (int64_t)sz;
+  if (bytes <= POLICY_WARP) {
     int i = 0;
-    while (vocab * (int64_t)sz > (int64_t)512 << i) ++i;
+    while (bytes > (int64_t)512 << i) ++i;
     OP_CK(launch(policy_warp_kernels[dtype == PRECOND_BF16][i], dim3((unsigned)std::min<int64_t>((rows + 7) / 8, 4 * h->num_sms)), dim3(256), 0,
                  (cudaStream_t)stream, 1, a));
+    ++h->launches;
+    return PRECOND_OK;
+  }
+  if (rows > PLAN_SMS && bytes <= (rows > 4 * PLAN_SMS ? POLICY_ROW : POLICY_ROW / 2)) {
+    OP_CK(launch(policy_row_kernels[dtype == PRECOND_BF16], dim3((unsigned)rows), dim3(32), (size_t)bytes, (cudaStream_t)stream, 1, a));
     ++h->launches;
     return PRECOND_OK;
   }

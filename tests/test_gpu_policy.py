@@ -113,6 +113,62 @@ def test_policy_in_place(pc, rows, vocab, dtype):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("rows,vocab,dtype,pitch", [(153, 2049, "bf16", 0), (153, 1025, "f32", 1), (160, 2500, "bf16", 3), (200, 6144, "bf16", 0),
+                                                    (200, 6145, "bf16", 0), (608, 6001, "bf16", 5), (609, 6145, "bf16", 1), (609, 12288, "bf16", 0),
+                                                    (609, 12289, "bf16", 0), (700, 4099, "f32", 2), (650, 6143, "f32", 1), (1201, 2001, "f32", 0),
+                                                    (5003, 2055, "bf16", 1)])
+def test_policy_middle_rows(pc, rows, vocab, dtype, pitch):
+    """Rows of a warp in shared memory, at both ends of their lengths and numbers and at every alignment; in place as well."""
+    a = inputs(rows, vocab, dtype, 0.9)
+    one = check(pc, *a, tau=0.9, pitch=pitch)
+    two = check(pc, *a, tau=0.9, pitch=pitch, in_place=True)
+    for x, y in zip(one, two):
+        assert torch.equal(x, y)
+    z, ids, adv, old, ref, weight = a
+    weight[::3], ids[1::7], ids[2::7] = 0, -1, vocab
+    check(pc, z, ids, adv, old, ref, weight, tau=0.9, pitch=pitch)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_policy_middle_masks(pc, dtype):
+    """Rows of a warp in shared memory: forbidden tokens, rows that are not read, what is not a number, a sure policy, the
+    taken token at every place, and gradients beside the logits' vectors."""
+    rows, vocab = 640, 2601
+    z, _, adv, _, ref, weight = inputs(rows, vocab, "f32", 1.0, seed=3)
+    z = z.to(TYPES[dtype])
+    ids = (torch.arange(rows) * 61) % vocab
+    ids[:40], ids[40:80] = torch.arange(40), vocab - 1 - torch.arange(40)
+    z[:, 5::9] = -math.inf
+    ids = torch.where(ids % 9 == 5, ids - 1, ids)
+    z[100:110, :] = z[100:110, :].clamp(max=0.0)
+    z[torch.arange(100, 110), ids[100:110]] = 90.0
+    logp = torch.log_softmax(z.double(), dim=1).gather(1, ids[:, None])[:, 0].float()
+    got = [torch.full(s, math.nan, device="cuda") for s in ((rows,), (rows,), (rows, vocab))]
+    got[2] = got[2].to(TYPES[dtype])
+    kw = dict(advantage=adv.cuda(), old_logp=(logp - 0.05).cuda(), clip_low=LOW, clip_high=HIGH)
+    zz, at = z.clone(), ids.clone()
+    zz[7], zz[8, 3], zz[9, 3], zz[10] = math.nan, math.nan, math.inf, math.nan
+    weight[7], at[10] = 0.0, -1
+    sr.precond_policy(pc.h, zz.cuda(), at.cuda(), loss=got[0], logp=got[1], dlogits=got[2], weight=weight.cuda(), **kw)
+    wl, ws, wg = T.policy(z, ids, adv, logp - 0.05, None, weight, 1.0, LOW, HIGH, 0.0)
+    loss, lp, grad = (t.cpu().double() for t in got)
+    assert bool(lp[8:10].isnan().all()) and bool(grad[8:10].isnan().any(dim=1).all())
+    for r in (7, 10):
+        assert loss[r] == 0 and lp[r] == 0 and bool((grad[r] == 0).all())
+    keep = torch.tensor([r for r in range(rows) if r not in (7, 8, 9, 10)])
+    # log q by 4 E (|x| + 8) + 2^-21 + 66 E relative to 1, |x| < 128; the factors by that and E for each of their roundings
+    by = 4 * E * 136 + 2.0 ** -21 + 66 * E
+    assert bool(((lp - ws)[keep].abs() <= by + E * ws[keep].abs()).all())
+    size = (weight.double() * math.exp(0.05) * adv.double().abs())[keep, None]
+    tol = 8 * by * (size * (ids[keep, None] == torch.arange(vocab)) + wg[keep].abs()) + 1e-38
+    assert bool(((grad - wg)[keep].abs() <= tol + (E16 * (wg[keep].abs() + tol) if dtype == "bf16" else 0)).all())
+    assert bool((grad[keep][:, 5::9] == 0).all())
+    one = got[2].clone()
+    both = torch.zeros(rows, vocab + 3, dtype=z.dtype, device="cuda")
+    sr.precond_policy(pc.h, zz.cuda(), at.cuda(), loss=got[0], dlogits=both[:, 3:], weight=weight.cuda(), **kw)
+    assert torch.equal(both[:, 3:][keep.cuda()], one[keep.cuda()]) and bool((both[:, :3] == 0).all())
+
+
 @pytest.mark.parametrize("vocab", [9, 700, 50001, 600001])
 def test_policy_every_place(pc, vocab):
     """The taken token first, last, and beside every border of vectors, threads and blocks' parts."""
