@@ -123,6 +123,22 @@ inline int64_t row_blocks_of(const RowShape& s, int64_t rows, int sm_threads, in
   const int64_t most = resident * (s.parts > 1 ? clusters[s.parts] : sms);
   return std::max<int64_t>(1, std::min((rows + s.rows - 1) / s.rows, most));
 }
+// ------------------------------------------------------------------------- gradients of the layer norm
+// Rows of a gradient's block: as many as an SM's registers hold, for each block leaves sums of dw and db (777 x 1000 fp32).
+inline RowShape layer_grad_shape(int64_t cols, int dtype, bool vec) {
+  RowShape s = row_shape(cols, dtype, true, vec);
+  if (s.parts == 1 && s.threads >= 32) s.rows = std::min(8, std::max(1, (dtype == PRECOND_F32 ? 384 : 512) / s.threads));
+  return s;
+}
+inline int64_t layer_grad_blocks(const RowShape& s, int64_t rows, int dtype, int sms, const int* clusters) {
+  return row_blocks_of(s, rows, dtype == PRECOND_F32 ? 384 : 512, sms, clusters);
+}
+// Few rows: a block, or a cluster of them, leaves dw and db itself, without a second kernel or a workspace: its blocks
+// (0: not this way).  (14 x 192 fp32: 5.0 us, with two kernels 7.5; with a second turn, 100 x 1000 bf16, 10.3 and 8.3.)
+inline int layer_grad_whole(const RowShape& s, int64_t rows) {
+  const int64_t blocks = (rows + s.rows - 1) / s.rows;
+  return s.parts != 1 || blocks > 8 ? 0 : blocks > 4 ? 8 : blocks > 2 ? 4 : (int)blocks;
+}
 // ------------------------------------------------------------------------- logits on blocks
 // Blocks of a row: as many as hold it in registers, and more where rows are few, each with at least 8192 logits.
 inline int distill_parts(int64_t rows, int64_t vocab, int dtype) {

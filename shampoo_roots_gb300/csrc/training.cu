@@ -58,21 +58,6 @@ struct LayerKernels {
 int64_t layer_norm_blocks(const RowShape& s, int64_t rows, int dtype, bool vec, int sms, const int* clusters) {
   return row_blocks_of(s, rows, s.vectors == 2 ? 512 : dtype == PRECOND_F32 ? 384 : vec ? 768 : 512, sms, clusters);
 }
-int64_t layer_grad_blocks(const RowShape& s, int64_t rows, int dtype, int sms, const int* clusters) {
-  return row_blocks_of(s, rows, dtype == PRECOND_F32 ? 384 : 512, sms, clusters);
-}
-// Rows of a gradient's block: as many as an SM's registers hold, for each block leaves sums of dw and db (777 x 1000 fp32).
-RowShape layer_grad_shape(int64_t cols, int dtype, bool vec) {
-  RowShape s = row_shape(cols, dtype, true, vec);
-  if (s.parts == 1 && s.threads >= 32) s.rows = std::min(8, std::max(1, (dtype == PRECOND_F32 ? 384 : 512) / s.threads));
-  return s;
-}
-// Few rows: a block, or a cluster of them, leaves dw and db itself, without a second kernel or a workspace: its blocks
-// (0: not this way).  (14 x 192 fp32: 5.0 us, with two kernels 7.5; with a second turn, 100 x 1000 bf16, 10.3 and 8.3.)
-int layer_grad_whole(const RowShape& s, int64_t rows) {
-  const int64_t blocks = (rows + s.rows - 1) / s.rows;
-  return s.parts != 1 || blocks > 8 ? 0 : blocks > 4 ? 8 : blocks > 2 ? 4 : (int)blocks;
-}
 template <typename T, bool VEC>
 cudaError_t launch_layer_norm(const LayerNormArgs& a, const RowShape& s, unsigned grid, cudaStream_t st) {
   typedef LayerKernels<T, VEC> K;
@@ -350,12 +335,17 @@ int precond_layer_norm(precond_t ph, const void* x, const void* residual, const 
 int64_t precond_layer_norm_grad_workspace(int64_t rows, int64_t cols) {
   if (!side(rows) || !side(cols)) return -1;
   if (rows == 0 || cols == 0) return 0;
-  // of either type; rows in parts of a warp, and clusters that do not fit, only make fewer
-  if (layer_grad_whole(layer_grad_shape(cols, PRECOND_BF16, false), rows) && layer_grad_whole(layer_grad_shape(cols, PRECOND_F32, false), rows))
-    return 0;                                            // aligned rows of the same length never make more blocks
+  // Rows of either type, at sectors or not: the most blocks of any form (up to 256 columns those at sectors have smaller
+  // blocks, and more of them).  Fewer clusters that fit only make fewer.
+  bool whole = true;
   int64_t blocks = std::min<int64_t>(rows, PLAN_SMS);    // rows through shared memory: a block an SM
   for (const int dtype : {PRECOND_BF16, PRECOND_F32})
-    blocks = std::max(blocks, layer_grad_blocks(layer_grad_shape(cols, dtype, false), rows, dtype, PLAN_SMS, PLAN_CLUSTERS));
+    for (const bool vec : {false, true}) {
+      const RowShape s = layer_grad_shape(cols, dtype, vec);
+      whole = whole && layer_grad_whole(s, rows);
+      blocks = std::max(blocks, layer_grad_blocks(s, rows, dtype, PLAN_SMS, PLAN_CLUSTERS));
+    }
+  if (whole) return 0;
   return blocks * partial_pitch(cols) * 8;
 }
 
