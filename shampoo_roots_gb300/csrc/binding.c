@@ -477,8 +477,10 @@ static PyObject* policy(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (PyErr_Occurred() || maybe_vector(a[3], "advantage", &adv, z.rows) || maybe_vector(a[4], "old_logp", &old, z.rows) ||
       maybe_vector(a[5], "ref_logp", &ref, z.rows) || maybe_vector(a[6], "weight", &w, z.rows) ||
       maybe_vector(a[11], "loss", &loss, z.rows) || maybe_vector(a[12], "logp", &logp, z.rows) ||
-      maybe(a[13], "dlogits", &dz, z.rows, z.cols, z.dtype) || one_device(a + 1, 6) || one_device(a + 11, 3) || stream_of(a[14], a[1], &st))
+      maybe(a[13], "dlogits", &dz, z.rows, z.cols, z.dtype))
     return NULL;
+  PyObject* tensors[9] = {a[1], a[2], a[3], a[4], a[5], a[6], a[11], a[12], a[13]};
+  if (one_device(tensors, 9) || stream_of(a[14], a[1], &st)) return NULL;
   return PyLong_FromLong(((fn)entry[E_POLICY])(h, z.p, dt, z.rows, z.cols, z.ld, ids.p, ids.dtype == dtypes[T_I32] ? 32 : 64, adv.p, old.p,
                                                ref.p, w.p, (float)number[0], (float)number[1], (float)number[2], (float)number[3], loss.p,
                                                logp.p, dz.p, dz.ld, st));
@@ -542,8 +544,8 @@ static int list_call(PyObject* list, PyObject* first, PyObject* norm, PyObject* 
   *own = NULL;
   if (!(*l = PyCapsule_GetPointer(list, LIST_NAME)) || get(norm, "norm", o)) return -1;
   if (o->rows * o->cols != 1 || o->dtype != dtypes[T_F32]) return bad(PyExc_ValueError, "norm", "must be one torch.float32 number");
-  PyObject* both[2] = {norm, first};
-  if (one_device(both, 2) || stream_of(stream, norm, st)) return -1;
+  PyObject* tensors[3] = {norm, first, workspace};
+  if (one_device(tensors, 3) || stream_of(stream, norm, st)) return -1;
   return workspace_of(workspace, norm, workspace == Py_None && !given ? ((need_fn)entry[E_LIST_WS])(*l) : 0, stream, *st, ws, own);
 }
 static PyObject* grad_norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
