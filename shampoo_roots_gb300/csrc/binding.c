@@ -261,7 +261,7 @@ static int one_device(PyObject* const* a, Py_ssize_t n) {
   long device = 0;
   int seen = 0;
   for (Py_ssize_t i = 0; i < n; ++i) {
-    if (a[i] == Py_None || PyFloat_Check(a[i]) || PyLong_Check(a[i])) continue;
+    if (a[i] == Py_None) continue;
     PyObject* d = PyObject_CallMethodNoArgs(a[i], s_get_device);
     if (!d) return -1;
     const long its = PyLong_AsLong(d);
@@ -428,9 +428,10 @@ static PyObject* layer_norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   }
   if (maybe(a[5], "residual", &r, x.rows, x.cols, x.dtype) || maybe(a[6], "total", &t, x.rows, x.cols, x.dtype) ||
       maybe(a[7], "y", &y, x.rows, x.cols, x.dtype) || maybe8(a[8], a[9], "q", &q, &s, x.rows, x.cols) ||
-      maybe_vector(a[10], "mean", &m, x.rows) || maybe_vector(a[11], "rstd", &rs, x.rows) || one_device(a + 1, 11) ||
-      stream_of(a[12], a[1], &st))
+      maybe_vector(a[10], "mean", &m, x.rows) || maybe_vector(a[11], "rstd", &rs, x.rows))
     return NULL;
+  PyObject* tensors[10] = {a[1], a[2], a[4], a[5], a[6], a[7], a[8], a[9], a[10], a[11]};
+  if (one_device(tensors, 10) || stream_of(a[12], a[1], &st)) return NULL;
   return PyLong_FromLong(((fn)entry[E_LAYER])(h, x.p, r.p, w.p, b.p, dt, wt, x.rows, x.cols, x.ld, r.ld, (float)eps, t.p, t.ld, y.p,
                                               y.ld, q.p, q.ld, s.p, m.p, rs.p, st));
 }
