@@ -126,7 +126,7 @@ __device__ __forceinline__ PolicyRow policy_result(const PolicyArgs& a, float c,
     slope = free > held ? 0.f : -free;
     if (a.ref) {
       const float d = ref - logp, e = expm1f(d);
-      loss = fmaf(a.kl, e - d, loss);
+      loss = fmaf(a.kl, e < INFINITY ? e - d : e, loss);             // d may be infinite with e
       slope = fmaf(-a.kl, e, slope);
     }
     loss *= weight;
