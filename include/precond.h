@@ -474,7 +474,7 @@ int64_t precond_layer_norm_grad_workspace(int64_t rows, int64_t cols);   /* 0 fo
  *               taken token, is not read: its loss, logp and gradient are 0 whatever its inputs hold.
  *   temperature : 1e-18 .. 1e18;  clip_low 0 .. 1, clip_high >= 0 (infinity: no bound above), kl >= 0
  *   loss, logp  : rows floats; one may be NULL, and loss where dlogits is given
- * A token that the logits give no probability has logp -infinity (and with kl an infinite loss, whose gradient is not
+ * A token whose logit is -infinity has logp -infinity (and with kl an infinite loss, whose gradient is not
  * finite).  Logits that are all -infinity, or one of NaN or +infinity, make the row's results NaN.
  */
 int precond_policy(precond_t h, const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ldz, const void* ids,

@@ -116,7 +116,12 @@ __device__ __forceinline__ PolicyRow policy_result(const PolicyArgs& a, float c,
   const float M = max_nan(m, taken);
   const Shift shift(M, c);
   const float rest = m == M ? s : s * ex2(shift.from(Shift(m, c), c)), mine = ex2(shift(taken, c)), total = rest + mine;
-  logp = taken >= m ? -log1pf(rest / mine) : fmaf(shift(taken, c), LN2, -logf(total));
+  // x, log2 of the taken power, may pass fp32's range where the log probability, 0.69 times as large, does not (a token masked with
+  // the type's lowest value); halves, as the difference may pass it too
+  const float x = shift(taken, c);
+  logp = taken >= m       ? -log1pf(rest / mine)
+         : x > -INFINITY ? fmaf(x, LN2, -logf(total))
+                          : 2.f * ((0.5f * taken - 0.5f * M) / a.tau) - logf(total);
   loss = 0.f;
   float slope = 0.f;
   if (a.advantage) {
