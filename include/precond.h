@@ -501,8 +501,9 @@ int64_t precond_list_workspace(precond_list_t list);      /* bytes for the calls
 int precond_grad_norm(precond_t h, precond_list_t list, float* norm, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
- * Scales every element by max_norm / norm, in place and rounded once, where norm > max_norm; otherwise, and where the norm is not
- * finite, the tensors stay as they are.
+ * Scales every element by max_norm / norm, in place, where norm > max_norm; otherwise, and where the norm is not finite,
+ * the tensors stay as they are.  The factor and the product are rounded to fp32, the product then to the tensor's type;
+ * a factor below fp32's normal numbers costs no digits.
  *   max_norm  : >= 0; infinity clips nothing
  *   norm      : device float.  given = 0: the list's norm (before scaling) is computed and left there.  given = 1: it
  *               is read there (the norm of more than this list, of several ranks' lists); then workspace may be NULL

@@ -288,18 +288,33 @@ __global__ void __launch_bounds__(CLIP_THREADS) clip_total_kernel(const ClipSum*
 }
 
 // ------------------------------------------------------------- scaling
-__device__ __forceinline__ void clip_scale(uint32_t (&w)[8], bool bf16, float c) {
-  const f2 cc = f2_of(c, c);
+// max_norm / norm; below fp32's normal numbers in two steps, so that large elements keep their digits: 2^-126, which is exact
+// for what does not end below the normal numbers, and 2^126 max_norm / norm (no overflow: max_norm < 4 then).
+struct ClipFactor {
+  float first, c;
+  __device__ __forceinline__ ClipFactor(float max_norm, float norm) : first(1.f), c(max_norm / norm) {
+    if (c < 0x1p-126f) {
+      first = 0x1p-126f;
+      c = max_norm * 0x1p126f / norm;
+    }
+  }
+  __device__ __forceinline__ float operator()(float x) const { return x * first * c; }
+  __device__ __forceinline__ f2 operator()(f2 x) const {
+    if (first != 1.f) x = mul2(x, f2_of(first, first));
+    return mul2(x, f2_of(c, c));
+  }
+};
+__device__ __forceinline__ void clip_scale(uint32_t (&w)[8], bool bf16, const ClipFactor& factor) {
   if (bf16) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float2 x = f2_get(mul2(f2_of(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), cc));
+      const float2 x = f2_get(factor(f2_of(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u))));
       w[i] = bf16x2_bits(x.x, x.y);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      const float2 x = f2_get(mul2(f2_of(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), cc));
+      const float2 x = f2_get(factor(f2_of(__uint_as_float(w[i]), __uint_as_float(w[i + 1]))));
       w[i] = __float_as_uint(x.x);
       w[i + 1] = __float_as_uint(x.y);
     }
@@ -307,7 +322,7 @@ __device__ __forceinline__ void clip_scale(uint32_t (&w)[8], bool bf16, float c)
 }
 
 template <int MAX>
-__device__ __forceinline__ void clip_scale_all(const ClipTable<MAX>& t, const ClipWalk& walk, bool back, float c) {
+__device__ __forceinline__ void clip_scale_all(const ClipTable<MAX>& t, const ClipWalk& walk, bool back, const ClipFactor& factor) {
   walk.each(t, back, [&](const ClipView& v, int64_t s, bool begins, bool stays) {
     const bool bf16 = v.size == 2;
     uint32_t w[CLIP_U][8];
@@ -317,15 +332,16 @@ __device__ __forceinline__ void clip_scale_all(const ClipTable<MAX>& t, const Cl
     if (char* single = begins ? v.single(threadIdx.x & 31) : nullptr) {
       if (bf16) {
         __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(single);
-        *p = __float2bfloat16_rn(__bfloat162float(*p) * c);
+        *p = __float2bfloat16_rn(factor(__bfloat162float(*p)));
       } else {
-        *reinterpret_cast<float*>(single) *= c;
+        float* p = reinterpret_cast<float*>(single);
+        *p = factor(*p);
       }
     }
 #pragma unroll
     for (int u = 0; u < CLIP_U; ++u)
       if (s + u * 32 < v.sectors) {
-        clip_scale(w[u], bf16, c);
+        clip_scale(w[u], bf16, factor);
         clip_store(v.body + (s + u * 32) * 32, w[u]);
       }
   });
@@ -342,7 +358,7 @@ __global__ void __launch_bounds__(CLIP_THREADS, 2) clip_scale_kernel(const __gri
   let_next_start();
   const float total = sums ? clip_total(partial, sums) : *norm;
   if (sums && blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
-  if (clips(total, max_norm)) clip_scale_all(t, walk, true, max_norm / total);
+  if (clips(total, max_norm)) clip_scale_all(t, walk, true, ClipFactor(max_norm, total));
 }
 
 // A short list: one cluster.  max_norm infinite: the norm alone.
@@ -367,7 +383,7 @@ __global__ void __launch_bounds__(CLIP_THREADS, 2) clip_short_kernel(const __gri
   for (int i = 1; i < CLIP_CLUSTER; ++i) v.add(sums[i]);
   const float total = v.root();
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = total;
-  if (clips(total, max_norm)) clip_scale_all(t, walk, false, max_norm / total);
+  if (clips(total, max_norm)) clip_scale_all(t, walk, false, ClipFactor(max_norm, total));
 }
 
 }  // namespace precond
