@@ -73,9 +73,12 @@ cudaError_t launch_layer_grad(const LayerGradArgs& a, const RowShape& s, unsigne
 // Rows through shared memory: threads of a row, rows of a block, rows of each in the ring (0: not this way).  For rows of
 // more than 256 columns, whole 16-byte vectors, enough of them that a group has its second one.  (Norm of 8192 x 6144
 // bf16 56 us, with the next row in registers 63; of 20000 x 1024 27 and 38; gradients of 16384 x 4096 92 and 97.)
-// Vectors a thread, of a norm: one where that fills the block with threads (8192 x 6144 bf16: 56 us, with two 63; 10000 x
-// 4096 fp32 53 and 60) or rows are short, else two or four, whose groups are more (6000 x 8192 bf16: 66, 60 and 62;
-// 4000 x 12288: 57, 57 and 52).
+// Vectors a thread, of a norm: one where rows are short, and, with a residual, where whole warps of them fill the block's 768
+// threads (bf16 to 8 bits, one and two: 8192 x 6144 56 and 63 us, 8192 x 4096 39 and 43, 4000 x 12288 58 and 61; y kept 72 and
+// 70, 48 and 49, 68 and 70; without a residual, which leaves room for more stages, 52 and 49, 36 and 34, 53 and 55; a last warp
+// half empty, 8548 x 5888, 65 and 60).  Else two, or four for wide rows, whose groups are more (one, two and four: 6000 x 8192
+// 65, 59 and 57, 4000 x 12288 without a residual 53, 55 and 50).  fp32: one up to 768 threads (10000 x 4096 without a residual,
+// y kept, one and two 53 and 60, to 8 bits 46 and 43).
 constexpr int STREAM_BYTES = 225 << 10;
 typedef void (*StreamNorm)(LayerNormArgs, int);
 typedef void (*StreamGrad)(LayerGradArgs, int);
@@ -89,7 +92,8 @@ StreamShape stream_shape(int64_t cols, int dtype, int inputs, bool grad, int64_t
   const int64_t n = (cols + 15) / 16, row = cols * (int64_t)size_of(dtype);
   if (n <= 16 || row % 16 || n > (grad ? 512 : 1024)) return s;
   if (!grad && dtype == PRECOND_F32 && n > 768) s.vectors = 2;
-  if (!grad && dtype == PRECOND_BF16 && n > 200) s.vectors = n > 512 ? 4 : n > 352 && n <= 384 ? 1 : 2;
+  const bool fills = inputs == 2 && n % 32 == 0 && STREAM_THREADS[1] % n == 0;
+  if (!grad && dtype == PRECOND_BF16 && n > 200 && !fills) s.vectors = n > 512 ? 4 : 2;
   const int most = grad ? 512 : STREAM_THREADS[s.vectors];
   s.threads = (int)((n + 32 * s.vectors - 1) / (32 * s.vectors) * 32);
   s.rows = std::max(1, std::min(most / s.threads, s.threads > 32 ? 15 : 16));
