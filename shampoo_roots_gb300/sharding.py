@@ -126,7 +126,19 @@ class OwnerSharding:
 
     def step(self, grads: Sequence[torch.Tensor],
              compute: Callable[[List[int], List[torch.Tensor]], Sequence[torch.Tensor]]) -> List[torch.Tensor]:
-        """Reduce to owners, ``compute(owned indices, averaged grads) -> updates``, gather to all ranks."""
+        """Reduce to owners, ``compute(owned indices, averaged grads) -> updates``, gather to all ranks.
+
+        ``compute`` runs only on ranks that own something, so no collective may be in it.  Clipping by the norm over
+        all ranks' matrices goes between the halves of this method, called one after another on every rank::
+
+            mine = plan.reduce_gradients(grads)
+            precond_grad_norm(h, mine, norm)                  # 0 where nothing is owned
+            norm.square_()
+            dist.all_reduce(norm)
+            norm.sqrt_()
+            precond_clip_grads(h, mine, max_norm, norm, given=True)
+            updates = plan.gather_updates(compute(plan.mine, mine) if mine else [], device=grads[0].device)
+        """
         g = self.reduce_gradients(grads)
         u = list(compute(self.mine, g)) if self.mine else []
         return self.gather_updates(u, device=grads[0].device)
