@@ -8,7 +8,6 @@
 #include <algorithm>
 #include <cstdio>
 
-#include "distill.cuh"
 #include "form8.cuh"
 #include "handle.h"
 
@@ -138,29 +137,6 @@ inline int64_t layer_grad_blocks(const RowShape& s, int64_t rows, int dtype, int
 inline int layer_grad_whole(const RowShape& s, int64_t rows) {
   const int64_t blocks = (rows + s.rows - 1) / s.rows;
   return s.parts != 1 || blocks > 8 ? 0 : blocks > 4 ? 8 : blocks > 2 ? 4 : (int)blocks;
-}
-// ------------------------------------------------------------------------- logits on blocks
-// Blocks of a row: as many as hold it in registers, and more where rows are few, each with at least 8192 logits.
-inline int distill_parts(int64_t rows, int64_t vocab, int dtype) {
-  const int64_t sz = (int64_t)size_of(dtype), capacity = 8 * DISTILL_THREADS * 16 / sz;
-  int parts = 1;
-  while (parts < 8 && (((vocab + parts - 1) / parts + 63) / 64 * 64 > capacity ||
-                       (rows * parts < 2 * PLAN_SMS && vocab / (parts * 2) >= 8192)))
-    parts *= 2;
-  return parts;
-}
-// Vectors a thread: one block after another on an SM hides nothing, so a block has as few threads as hold its part, 64
-// at least (distillation of 8192 x 8000 bf16: 53 us, with 512 threads of 2 vectors 77).  `kernel` 0: rows read twice,
-// else 1 << (kernel - 1) vectors.
-struct LogitShape { int parts, threads, kernel; };
-inline LogitShape logit_shape(int64_t rows, int64_t vocab, int dtype) {
-  const int parts = distill_parts(rows, vocab, dtype);
-  const int64_t vecs = ((vocab + parts - 1) / parts + 63) / 64 * 64 * (int64_t)size_of(dtype) / 16;
-  int i = 0;
-  if (vecs <= 8 * DISTILL_THREADS)
-    for (i = 1; i < 4 && vecs >= 128 << (i - 1);) ++i;
-  const int nv = i ? 1 << (i - 1) : 0;
-  return {parts, nv == 0 ? DISTILL_THREADS : (int)std::max<int64_t>(64, ((vecs + nv - 1) / nv + 31) / 32 * 32), i};
 }
 
 }  // namespace precond

@@ -76,6 +76,28 @@ cudaError_t launch_grad(const RmsGradArgs& a, const RowShape& s, unsigned grid, 
 }
 
 // ------------------------------------------------------------------------- distillation
+// Blocks of a row: as many as hold it in registers, and more where rows are few, each with at least 8192 logits.
+int distill_parts(int64_t rows, int64_t vocab, int dtype) {
+  const int64_t sz = (int64_t)size_of(dtype), capacity = 8 * DISTILL_THREADS * 16 / sz;
+  int parts = 1;
+  while (parts < 8 && (((vocab + parts - 1) / parts + 63) / 64 * 64 > capacity ||
+                       (rows * parts < 2 * PLAN_SMS && vocab / (parts * 2) >= 8192)))
+    parts *= 2;
+  return parts;
+}
+// Vectors a thread: one block after another on an SM hides nothing, so a block has as few threads as hold its part, 64
+// at least (distillation of 8192 x 8000 bf16: 53 us, with 512 threads of 2 vectors 77).  `kernel` 0: rows read twice,
+// else 1 << (kernel - 1) vectors.
+struct LogitShape { int parts, threads, kernel; };
+LogitShape logit_shape(int64_t rows, int64_t vocab, int dtype) {
+  const int parts = distill_parts(rows, vocab, dtype);
+  const int64_t vecs = ((vocab + parts - 1) / parts + 63) / 64 * 64 * (int64_t)size_of(dtype) / 16;
+  int i = 0;
+  if (vecs <= 8 * DISTILL_THREADS)
+    for (i = 1; i < 4 && vecs >= 128 << (i - 1);) ++i;
+  const int nv = i ? 1 << (i - 1) : 0;
+  return {parts, nv == 0 ? DISTILL_THREADS : (int)std::max<int64_t>(64, ((vecs + nv - 1) / nv + 31) / 32 * 32), i};
+}
 // Whether the candidates have a kernel of their own: with many rows or blocks, one more launch costs less than warps
 // that wait for them.  (2000 x 131072 bf16 with 128 of them, 8000 blocks: 191 us, together 248; 1900 x 32000 fp32 with
 // 64, 86 and 89; 1000 x 32000 fp32, 2000 blocks: 51.8 and 51.3, bf16 32.6 and 27.9; 500 x 32000 fp32 32.0 and 28.3.  Many
