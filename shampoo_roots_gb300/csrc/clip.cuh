@@ -9,13 +9,13 @@
 // Where the norm needs no clipping nothing more is read.
 //
 // Measured: norm of 604 MB 88 us (the copy bandwidth); clipping of 604 MB of bf16
-// 261 us, where three passes over it take 267 and two 179: of the 60 MB that are
+// 261 to 283 us, where three passes over it take 267 and two 179: of the 60 MB that are
 // asked to stay in L2 some 20 are found there.  97 weights of 333 KB with three
 // vectors each, clipped, 15 us.
 //
 // A short list takes one launch: a cluster of 8 blocks, which read it a second time
 // when they have joined their sums through distributed shared memory (one layer of
-// 256 x 128: 4.9 us, with two kernels 6.5).
+// 256 x 128, clipped: 4.0 us, with two kernels 6.7).
 //
 // The list comes as a kernel parameter (no upload, so that a captured call holds
 // its own copy).  Tensors are cut into pieces of 4 KB, four sectors a lane; a

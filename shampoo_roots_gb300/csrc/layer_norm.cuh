@@ -24,7 +24,7 @@
 // Measured (bf16 with residual): norm of 8192 x 6144 to 8 bits 56 us, 93 % of the
 // copy bandwidth; gradients of 16384 x 4096 85 us, 93 %; in fp32 norm of 8192 x 6144
 // 106 us, gradients of 8000 x 6144 121 us, 96 %.  What bounds them below that is
-// issue slots (56 % busy at 24 warps an SM) and the latency of a row's sums: 21
+// issue slots (64 % busy at 24 warps an SM) and the latency of a row's sums: 18
 // shuffles one after another, which is why lanes join means and deviations in one
 // butterfly.  Rows that do not begin at sectors pass through the exchange of
 // form8.cuh: gradients of 7000 x 2001 40 us, 41 %.

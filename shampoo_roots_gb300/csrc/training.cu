@@ -133,8 +133,8 @@ const PolicyKernel policy_few_kernels[2][4] = {
 // blocks (8192 x 131072 bf16 by parts of 64 KB 671 us, of 32 KB 707, of 128 KB 893; 1900 x 151936 by 74 KB 188, by 37 KB
 // 199); a few rows take more blocks, each with at least 8192 logits.  Threads have 192 bytes each, up to 256 of them (8192 x
 // 8000 bf16, 16 KB: 96 threads 45 us, 128 47, 256 62, 512 99; 2999 x 50001: 256 threads 98 us, 512 118).  Blocks alone on
-// their SMs keep up to 64 KB in registers (24 x 50001 bf16: 3.9 us on the device, by shared memory 5.4; two to an SM, 200 x
-// 10000 fp32, 7.0 and 6.3).
+// their SMs keep up to 64 KB in registers (24 x 50001 bf16 scored: 3.2 us on the device, by shared memory 4.2); where there
+// are more blocks than SMs it goes either way (300 x 10000 fp32 7.4 and 8.8 us, 100 x 30000 11.5 and 9.7).
 struct PolicyShape { PolicyKernel kernel; int parts, threads, bytes; };
 PolicyShape policy_shape(int64_t rows, int64_t vocab, int dtype) {
   const int64_t sz = (int64_t)size_of(dtype), third = 76288;
@@ -159,7 +159,7 @@ constexpr int CLIP_SIZES[4] = {32, 128, 512, 1400};
 constexpr int CLIP_BLOCKS = 2 * PLAN_SMS;
 
 // A short list has at most CLIP_SHORT tensors: the larger tables need no kernel for it.
-constexpr int CLIP_SHORT = 128;                      // pieces of a list that one cluster takes (1 MB: two launches 7.1 us, one 7.2; 128 KB 7.2 and 6.0)
+constexpr int CLIP_SHORT = 128;                      // pieces of a list that one cluster takes (512 KB: two launches 6.7 us, one 5.2; 128 KB 6.7 and 3.8)
 struct ClipKernels { const void *norm, *scale, *one; };
 template <int MAX>
 ClipKernels clip_kernels() {
